@@ -50,7 +50,7 @@ def listed():
         # An odd vocabulary (rows not 16-byte aligned), padded examples, labels mixed in.
         dict(name="distill_odd_vocab", op="distill", dtype="bf16", B=16, T=128, V=50257, K=32, tau=2.0, alpha=0.3,
              grad=True),
-        # The loss of a held-out batch, no gradient.
+        # The loss of a held-out batch, per example and per token, no gradient.
         dict(name="distill_eval", op="distill", dtype="bf16", B=32, T=128, V=32768, K=50, tau=1.0, alpha=0.0,
              grad=False),
         # A large vocabulary at a training batch.
@@ -258,8 +258,9 @@ def _distill_plain(case, st):
         row = row + alpha * (lse1 - torch.gather(z, 2, y)).squeeze(-1)
         if case["grad"]:
             grad = grad.add_(q1, alpha=alpha).scatter_add_(2, y, torch.full_like(y, -alpha, dtype=torch.float32))
-    loss = (row * w).sum(dim=-1)
-    return (loss, grad.mul_(w.unsqueeze(-1)).to(st["logits"].dtype)) if case["grad"] else loss
+    row = row * w
+    loss = row.sum(dim=-1)
+    return (loss, grad.mul_(w.unsqueeze(-1)).to(st["logits"].dtype)) if case["grad"] else (loss, row)
 
 
 def run(state):
@@ -381,7 +382,7 @@ def _exact_attention(case, st):
 
 def _exact_distill(case, st):
     B, T, V, tau, alpha = case["B"], case["T"], case["V"], case["tau"], case["alpha"]
-    loss = torch.zeros(B, dtype=torch.float64, device="cuda")
+    rows = torch.zeros(B, T, dtype=torch.float64, device="cuda")
     grad = torch.zeros(B, T, V, dtype=torch.float64, device="cuda") if case["grad"] else None
     for b in range(B):
         z = st["logits"][b].double()
@@ -399,10 +400,10 @@ def _exact_distill(case, st):
             row = row - alpha * one[torch.arange(T, device="cuda"), y]
             d = d + alpha * torch.exp(one)
             d[torch.arange(T, device="cuda"), y] -= alpha
-        loss[b] = (w * row).sum()
+        rows[b] = w * row
         if case["grad"]:
             grad[b] = w[:, None] * d
-    return (loss, grad) if case["grad"] else loss
+    return (rows.sum(dim=1), grad if case["grad"] else rows)
 
 
 def exact(case, seed):
