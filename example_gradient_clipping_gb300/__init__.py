@@ -1,8 +1,8 @@
 """Python binding of libdpclip, DP-SGD per-example gradient clipping on GB300.
 
 Argument marshalling only: every function calls the C entry point of the same
-name (declared in include/dpclip.h) with raw device pointers and the current CUDA
-stream.  Tensors may be torch tensors (their data_ptr() is passed) or integer
+name (declared in include/dpclip.h or include/dpclip_seq.h) with raw device pointers and
+the current CUDA stream.  Tensors may be torch tensors (their data_ptr() is passed) or integer
 device addresses.  There is no fallback: importing this package fails if the
 compiled library is missing, and every non-DP_OK status raises DPError.
 """
@@ -284,3 +284,7 @@ def dp_check_status(stream=None) -> int:
 
 from .step import ClipPipeline, ClipStep, VirtualStep  # noqa: E402,F401
 from .engine import PrivacyEngine  # noqa: E402,F401
+from .sequence import (DP_ROTARY_BASE, DP_ROTARY_LINEAR, DP_ROTARY_PARTS, DP_ROTARY_PLAIN, AttnDesc,  # noqa: E402,F401
+                       DistillDesc, RotaryDesc, RotaryTableDesc, Strides, attention, attention_backward,
+                       attention_forward, distill_loss, distill_loss_and_grad, dp_attention, dp_attention_grad,
+                       dp_attention_grad_workspace, dp_distill, dp_rotary, dp_rotary_table, rotary, rotary_table)

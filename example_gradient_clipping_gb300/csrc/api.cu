@@ -401,6 +401,7 @@ void count_launch(unsigned n) { g_launches.fetch_add(n, std::memory_order_relaxe
 // For entry points defined in other translation units.
 dp_status geom_from_desc(const dp_layer_desc* d, Geom* g) { return make_geom(d, g); }
 dp_status set_error(dp_status st, const char* msg) { return fail(st, "%s", msg); }
+unsigned* device_status() { return status_ptr(); }
 }  // namespace dph
 
 extern "C" {
@@ -848,6 +849,7 @@ dp_status dp_check_status(cudaStream_t stream) {
   }
   if (v & dpk::kStatusTimeout) return fail(DP_ERR_TIMEOUT, "a bounded device wait gave up");
   if (v & dpk::kStatusNonfinite) return fail(DP_ERR_NONFINITE, "a per-example norm was not finite");
+  if (v & dpk::kStatusIndex) return fail(DP_ERR_INVALID_ARG, "a position or index in device memory was out of range");
   return ok();
 }
 

@@ -11,6 +11,7 @@ namespace dpk {
 // Device status bits (ORed into the status word; dp_check_status maps them).
 constexpr unsigned kStatusNonfinite = 1u;
 constexpr unsigned kStatusTimeout = 2u;
+constexpr unsigned kStatusIndex = 4u;   // an index or position in device memory out of range
 
 // Geometry of one layer's per-example contraction, resolved on the host.
 // Linear: row t of example i is A[i, t, :] / G[i, t, :].
@@ -243,6 +244,8 @@ cudaError_t launch_plain(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t
 // Descriptor validation and the thread-local error message, shared by entry points.
 dp_status geom_from_desc(const dp_layer_desc* d, Geom* g);
 dp_status set_error(dp_status st, const char* msg);
+// The current device's status word (nullptr: it cannot be resolved).
+unsigned* device_status();
 cudaError_t launch_t1_norm(const Geom& g, int dtype, const void* A, const void* G, float* out,
                            cudaStream_t s);
 // One-row (T = 1) linear clipped sum, FFMA, example splits reduced in a fixed order.

@@ -1,0 +1,371 @@
+// Attention and its gradient on the FFMA pipes: fp32 inputs (whose 1e-5 rules out the tensor
+// cores' formats) and bf16 shapes the tensor-core kernels do not take.
+//
+//   S = scale Q K^T,  P = softmax over the keys a query sees,  O = P V,  lse = log sum exp S
+//   delta = rowsum(dO * O),  dS = P * (dO V^T - delta),
+//   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO
+//
+// 64 x 64 score tiles, 256 threads, 4 x 4 scores a thread; operands in shared memory as fp32
+// rows of DP + 4 floats (DP = D rounded up to 32, 64 or 128 with zeros).  Forward: one pass
+// over the keys with the running maximum and sum of each row in registers.  Gradient: the
+// scores are formed again from lse, so nothing of size T x S is stored; one kernel per own
+// side (a key tile's dK and dV over every query that sees it, heads sharing the key head in
+// turn; a query tile's dQ over its keys), which costs two of the seven products twice and
+// needs no atomics: every sum has one order.
+#include <algorithm>
+
+#include "seq.cuh"
+
+namespace dpk {
+namespace attnsimt {
+
+constexpr int BT = 64, PS = BT + 4, kThreads = 256;
+
+// Keys [lo, hi) that some query of [t0, t1) sees (t1 <= Lq).
+__device__ __forceinline__ void key_range(const AttnParams& P, int t0, int t1, int lq, int lk, int* lo, int* hi) {
+  const int e = lk - lq;
+  *lo = P.window ? max(0, t0 + e - P.window + 1) : 0;
+  *hi = P.causal ? min(lk, t1 + e) : lk;
+}
+// Queries [lo, hi) that see some key of [j0, j1) (j1 <= Lk).
+__device__ __forceinline__ void query_range(const AttnParams& P, int j0, int j1, int lq, int lk, int* lo, int* hi) {
+  const int e = lk - lq;
+  *lo = P.causal ? max(0, j0 - e) : 0;
+  *hi = P.window ? min(lq, j1 - 1 - e + P.window) : lq;
+}
+__device__ __forceinline__ bool sees(const AttnParams& P, int t, int j, int lq, int lk) {
+  const int last = t + lk - lq;
+  return t < lq && j < lk && (!P.causal || j <= last) && (!P.window || j > last - P.window);
+}
+
+// Rows [row0, row0 + BT) of a [.., D] tensor as fp32 rows of DP + 4; zero from row `end` and
+// column D on (rows past the valid length are not read).
+template <class E, int DP>
+__device__ __forceinline__ void load_tile(float* dst, const E* src, long long stride, int row0, int end, int D) {
+  for (int i = threadIdx.x; i < BT * DP; i += kThreads) {
+    const int r = i / DP, c = i % DP;
+    dst[r * (DP + 4) + c] = row0 + r < end && c < D ? to_f(src[(row0 + r) * stride + c]) : 0.f;
+  }
+}
+
+// s[a][c] = A row (4 ty + a) . B row (tx + 16 c)
+template <int DP>
+__device__ __forceinline__ void tile_dot(const float* A, const float* B, int ty, int tx, float (&s)[4][4]) {
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s[a][c] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < DP; d += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) x[a] = *reinterpret_cast<const float4*>(A + (4 * ty + a) * (DP + 4) + d);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * (DP + 4) + d);
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        s[a][c] = fmaf(x[a].x, y[c].x, s[a][c]);
+        s[a][c] = fmaf(x[a].y, y[c].y, s[a][c]);
+        s[a][c] = fmaf(x[a].z, y[c].z, s[a][c]);
+        s[a][c] = fmaf(x[a].w, y[c].w, s[a][c]);
+      }
+  }
+}
+
+// Columns of a thread's accumulator: VW consecutive ones from tx VW + 16 VW c.
+template <int DP> struct Cols {
+  static constexpr int VW = DP >= 64 ? 4 : 2, NC = DP / (16 * VW);
+};
+
+// acc[a][..] += sum_j W[4 ty + a][j] X[j][cols], j < BT
+template <int DP>
+__device__ __forceinline__ void tile_acc(const float* W, const float* X, int ty, int tx, float (&acc)[4][DP / 16]) {
+  using C = Cols<DP>;
+#pragma unroll 2
+  for (int j = 0; j < BT; j += 4) {
+    float4 w[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) w[a] = *reinterpret_cast<const float4*>(W + (4 * ty + a) * PS + j);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float x[DP / 16];
+#pragma unroll
+      for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+        for (int v = 0; v < C::VW; v += 2) {
+          const float2 q = *reinterpret_cast<const float2*>(X + (j + u) * (DP + 4) + (tx + 16 * c) * C::VW + v);
+          x[c * C::VW + v] = q.x;
+          x[c * C::VW + v + 1] = q.y;
+        }
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const float p = u == 0 ? w[a].x : u == 1 ? w[a].y : u == 2 ? w[a].z : w[a].w;
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) acc[a][c] = fmaf(p, x[c], acc[a][c]);
+      }
+    }
+  }
+}
+
+// A thread's accumulator rows, times f[a], to rows row0 + 4 ty + a < end of dst.
+template <class E, int DP>
+__device__ __forceinline__ void store_acc(const float (&acc)[4][DP / 16], const float (&f)[4], E* dst,
+                                          long long stride, int row0, int end, int D, int ty, int tx) {
+  using C = Cols<DP>;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const int r = row0 + 4 * ty + a;
+    if (r >= end) continue;
+#pragma unroll
+    for (int c = 0; c < DP / 16; ++c) {
+      const int col = (tx + 16 * (c / C::VW)) * C::VW + c % C::VW;
+      if (col < D) dst[r * stride + col] = from_f(acc[a][c] * f[a], E());
+    }
+  }
+}
+
+__device__ __forceinline__ float half_warp_max(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float half_warp_sum(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int DP> constexpr int fwd_smem() { return (3 * BT * (DP + 4) + BT * PS) * 4; }
+template <int DP> constexpr int grad_smem() { return (4 * BT * (DP + 4) + 2 * BT * PS + 2 * BT) * 4; }
+
+template <class E, int DP>
+__global__ void __launch_bounds__(kThreads) attn_fwd_kernel(AttnParams P) {
+  pdl_trigger();
+  pdl_wait();
+  extern __shared__ float sm[];
+  float *sq = sm, *sk = sq + BT * (DP + 4), *sv = sk + BT * (DP + 4), *sp = sv + BT * (DP + 4);
+  const int tiles = (P.T + BT - 1) / BT;
+  const int tile = tiles - 1 - blockIdx.x % tiles, h = blockIdx.x / tiles % P.Hq, b = blockIdx.x / tiles / P.Hq;
+  const int t0 = tile * BT, hk = h / (P.Hq / P.Hk);
+  const int lq = attn_lq(P, b), lk = attn_lk(P, b);
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const E* K = static_cast<const E*>(P.K) + b * P.k.b + hk * P.k.h;
+  const E* V = static_cast<const E*>(P.V) + b * P.v.b + hk * P.v.h;
+  float acc[4][DP / 16], m[4], l[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    m[a] = -INFINITY;
+    l[a] = 0.f;
+#pragma unroll
+    for (int c = 0; c < DP / 16; ++c) acc[a][c] = 0.f;
+  }
+  if (t0 < lq) {
+    load_tile<E, DP>(sq, static_cast<const E*>(P.Q) + b * P.q.b + h * P.q.h, P.q.t, t0, lq, P.D);
+    int lo, hi;
+    key_range(P, t0, min(t0 + BT, lq), lq, lk, &lo, &hi);
+    for (int j0 = lo / BT * BT; j0 < hi; j0 += BT) {
+      __syncthreads();
+      load_tile<E, DP>(sk, K, P.k.t, j0, lk, P.D);
+      load_tile<E, DP>(sv, V, P.v.t, j0, lk, P.D);
+      __syncthreads();
+      float s[4][4];
+      tile_dot<DP>(sq, sk, ty, tx, s);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const int t = t0 + 4 * ty + a;
+        float mx = m[a];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          s[a][c] = sees(P, t, j0 + tx + 16 * c, lq, lk) ? s[a][c] * P.scale : -INFINITY;
+          mx = fmaxf(mx, s[a][c]);
+        }
+        mx = half_warp_max(mx);
+        const float base = mx == -INFINITY ? 0.f : mx;   // a row that has seen no key yet
+        const float f = expf(m[a] - base);
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float p = expf(s[a][c] - base);
+          sp[(4 * ty + a) * PS + tx + 16 * c] = p;
+          sum += p;
+        }
+        m[a] = mx;
+        l[a] = l[a] * f + half_warp_sum(sum);
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) acc[a][c] *= f;
+      }
+      __syncwarp();   // a row's 16 threads are one half warp
+      tile_acc<DP>(sp, sv, ty, tx, acc);
+    }
+  }
+  float f[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const int t = t0 + 4 * ty + a;
+    f[a] = l[a] > 0.f ? 1.f / l[a] : (l[a] == 0.f ? 0.f : l[a]);   // no key: 0; NaN stays NaN
+    if (P.lse && tx == 0 && t < P.T)
+      P.lse[((size_t)b * P.Hq + h) * P.T + t] = l[a] == 0.f ? -INFINITY : m[a] + logf(l[a]);
+  }
+  store_acc<E, DP>(acc, f, static_cast<E*>(P.O) + b * P.o.b + h * P.o.h, P.o.t, t0, P.T, P.D, ty, tx);
+}
+
+// kKeys: own tile = keys (dK, dV), the other side = queries; else own = queries (dQ).
+template <class E, int DP, bool kKeys>
+__global__ void __launch_bounds__(kThreads) attn_grad_kernel(AttnParams P) {
+  pdl_trigger();
+  pdl_wait();
+  extern __shared__ float sm[];
+  constexpr int TILE = BT * (DP + 4);
+  float *a1 = sm, *a2 = a1 + TILE, *b1 = a2 + TILE, *b2 = b1 + TILE, *sp = b2 + TILE, *sd = sp + BT * PS;
+  float *slse = sd + BT * PS, *sdel = slse + BT;
+  const int nown = kKeys ? P.S : P.T, hown = kKeys ? P.Hk : P.Hq, group = P.Hq / P.Hk;
+  const int tiles = (nown + BT - 1) / BT;
+  const int tile = kKeys ? blockIdx.x % tiles : tiles - 1 - blockIdx.x % tiles;
+  const int ho = blockIdx.x / tiles % hown, b = blockIdx.x / tiles / hown;
+  const int own0 = tile * BT;
+  const int lq = attn_lq(P, b), lk = attn_lk(P, b);
+  const int lown = kKeys ? lk : lq, loth = kKeys ? lq : lk;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int hk = kKeys ? ho : ho / group;
+  const E* K = static_cast<const E*>(P.K) + b * P.k.b + hk * P.k.h;
+  const E* V = static_cast<const E*>(P.V) + b * P.v.b + hk * P.v.h;
+  float acc1[4][DP / 16], acc2[4][DP / 16];   // dV (keys only); dK or dQ
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int c = 0; c < DP / 16; ++c) acc1[a][c] = acc2[a][c] = 0.f;
+  if (own0 < lown) {
+    int lo, hi;
+    if (kKeys) query_range(P, own0, min(own0 + BT, lk), lq, lk, &lo, &hi);
+    else key_range(P, own0, min(own0 + BT, lq), lq, lk, &lo, &hi);
+    if (kKeys) {
+      load_tile<E, DP>(a1, K, P.k.t, own0, lk, P.D);
+      load_tile<E, DP>(a2, V, P.v.t, own0, lk, P.D);
+    }
+    for (int g = 0; g < (kKeys ? group : 1); ++g) {
+      const int hq = kKeys ? ho * group + g : ho;
+      const E* Q = static_cast<const E*>(P.Q) + b * P.q.b + hq * P.q.h;
+      const E* dO = static_cast<const E*>(P.dO) + b * P.d_o.b + hq * P.d_o.h;
+      const size_t stat = ((size_t)b * P.Hq + hq) * P.T;
+      if (!kKeys) {
+        load_tile<E, DP>(a1, Q, P.q.t, own0, lq, P.D);
+        load_tile<E, DP>(a2, dO, P.d_o.t, own0, lq, P.D);
+      }
+      for (int o0 = lo / BT * BT; o0 < hi; o0 += BT) {
+        __syncthreads();
+        load_tile<E, DP>(b1, kKeys ? Q : K, kKeys ? P.q.t : P.k.t, o0, loth, P.D);
+        load_tile<E, DP>(b2, kKeys ? dO : V, kKeys ? P.d_o.t : P.v.t, o0, loth, P.D);
+        if (threadIdx.x < BT) {
+          const int t = (kKeys ? o0 : own0) + threadIdx.x;
+          slse[threadIdx.x] = t < lq ? P.lse[stat + t] : 0.f;
+          sdel[threadIdx.x] = t < lq ? P.delta[stat + t] : 0.f;
+        }
+        __syncthreads();
+        float s[4][4], d[4][4];
+        tile_dot<DP>(a1, b1, ty, tx, s);
+        tile_dot<DP>(a2, b2, ty, tx, d);
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int own = 4 * ty + a, oth = tx + 16 * c, q = kKeys ? oth : own;
+            const bool see = kKeys ? sees(P, o0 + oth, own0 + own, lq, lk) : sees(P, own0 + own, o0 + oth, lq, lk);
+            const float p = see ? expf(s[a][c] * P.scale - slse[q]) : 0.f;
+            if (kKeys) sp[own * PS + oth] = p;
+            sd[own * PS + oth] = see ? p * (d[a][c] - sdel[q]) : 0.f;
+          }
+        __syncwarp();
+        if (kKeys) tile_acc<DP>(sp, b2, ty, tx, acc1);
+        tile_acc<DP>(sd, b1, ty, tx, acc2);
+      }
+    }
+  }
+  const float one[4] = {1.f, 1.f, 1.f, 1.f}, sc[4] = {P.scale, P.scale, P.scale, P.scale};
+  if (kKeys) {
+    store_acc<E, DP>(acc1, one, static_cast<E*>(P.dV) + b * P.dv.b + ho * P.dv.h, P.dv.t, own0, P.S, P.D, ty, tx);
+    store_acc<E, DP>(acc2, sc, static_cast<E*>(P.dK) + b * P.dk.b + ho * P.dk.h, P.dk.t, own0, P.S, P.D, ty, tx);
+  } else {
+    store_acc<E, DP>(acc2, sc, static_cast<E*>(P.dQ) + b * P.dq.b + ho * P.dq.h, P.dq.t, own0, P.T, P.D, ty, tx);
+  }
+}
+
+// One warp per query row of one head: delta = dO . O (0 past Lq).
+template <class E>
+__global__ void __launch_bounds__(256) attn_delta_kernel(AttnParams P, float* __restrict__ delta) {
+  pdl_trigger();
+  pdl_wait();
+  const size_t n = (size_t)P.B * P.T * P.Hq;
+  const size_t i = (size_t)blockIdx.x * 8 + threadIdx.x / 32;
+  if (i >= n) return;
+  const int h = (int)(i % P.Hq);
+  const size_t bt = i / P.Hq;
+  const int b = (int)(bt / P.T), t = (int)(bt - (size_t)b * P.T);
+  float s = 0.f;
+  if (t < attn_lq(P, b)) {
+    const E* o = static_cast<const E*>(P.O) + b * P.o.b + t * P.o.t + h * P.o.h;
+    const E* g = static_cast<const E*>(P.dO) + b * P.d_o.b + t * P.d_o.t + h * P.d_o.h;
+    for (int c = threadIdx.x % 32; c < P.D; c += 32) s = fmaf(to_f(o[c]), to_f(g[c]), s);
+    s = warp_sum(s);
+  }
+  if (threadIdx.x % 32 == 0) delta[((size_t)b * P.Hq + h) * P.T + t] = s;
+}
+
+template <class E, int DP>
+cudaError_t fwd(const AttnParams& P, cudaStream_t s) {
+  constexpr int smem = fwd_smem<DP>();
+  static const cudaError_t set =
+      cudaFuncSetAttribute(attn_fwd_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (set != cudaSuccess) return set;
+  const unsigned grid = (unsigned)((size_t)P.B * P.Hq * ((P.T + BT - 1) / BT));
+  return dph::launch_pdl(attn_fwd_kernel<E, DP>, grid, kThreads, smem, s, P);
+}
+
+template <class E, int DP, bool kKeys>
+cudaError_t grad_one(const AttnParams& P, cudaStream_t s) {
+  constexpr int smem = grad_smem<DP>();
+  static const cudaError_t set =
+      cudaFuncSetAttribute(attn_grad_kernel<E, DP, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (set != cudaSuccess) return set;
+  const unsigned grid =
+      (unsigned)((size_t)P.B * (kKeys ? P.Hk : P.Hq) * (((kKeys ? P.S : P.T) + BT - 1) / BT));
+  return dph::launch_pdl(attn_grad_kernel<E, DP, kKeys>, grid, kThreads, smem, s, P);
+}
+
+template <class E, int DP>
+cudaError_t grad(const AttnParams& P, cudaStream_t s) {
+  const cudaError_t e = grad_one<E, DP, true>(P, s);
+  return e != cudaSuccess ? e : grad_one<E, DP, false>(P, s);
+}
+
+}  // namespace attnsimt
+}  // namespace dpk
+
+namespace dph {
+using namespace dpk;
+
+template <class E>
+static cudaError_t fwd_d(const AttnParams& P, cudaStream_t s) {
+  return P.D <= 32 ? attnsimt::fwd<E, 32>(P, s) : P.D <= 64 ? attnsimt::fwd<E, 64>(P, s) : attnsimt::fwd<E, 128>(P, s);
+}
+template <class E>
+static cudaError_t grad_d(const AttnParams& P, cudaStream_t s) {
+  return P.D <= 32   ? attnsimt::grad<E, 32>(P, s)
+         : P.D <= 64 ? attnsimt::grad<E, 64>(P, s)
+                     : attnsimt::grad<E, 128>(P, s);
+}
+
+cudaError_t launch_attn_simt_fwd(const AttnParams& P, int dtype, cudaStream_t s) {
+  return dtype == DP_BF16 ? fwd_d<__nv_bfloat16>(P, s) : fwd_d<float>(P, s);
+}
+cudaError_t launch_attn_simt_grad(const AttnParams& P, int dtype, cudaStream_t s) {
+  return dtype == DP_BF16 ? grad_d<__nv_bfloat16>(P, s) : grad_d<float>(P, s);
+}
+cudaError_t launch_attn_delta(const AttnParams& P, int dtype, float* delta, cudaStream_t s) {
+  const unsigned grid = (unsigned)(((size_t)P.B * P.T * P.Hq + 7) / 8);
+  if (dtype == DP_BF16) return launch_pdl(attnsimt::attn_delta_kernel<__nv_bfloat16>, grid, 256, 0, s, P, delta);
+  return launch_pdl(attnsimt::attn_delta_kernel<float>, grid, 256, 0, s, P, delta);
+}
+
+}  // namespace dph

@@ -1,0 +1,75 @@
+// Sequence operators (rotary positions, attention, distillation): parameters and launchers.
+#pragma once
+#include "common.cuh"
+#include "dpclip_seq.h"
+
+namespace dpk {
+
+// Four or eight consecutive values of E as floats, through one aligned access.
+template <class E, int N> struct alignas(sizeof(E) * N) Vec { E e[N]; };
+
+__device__ __forceinline__ float from_f(float v, float) { return v; }
+__device__ __forceinline__ __nv_bfloat16 from_f(float v, __nv_bfloat16) { return __float2bfloat16_rn(v); }
+
+// An element of a device array of 32- or 64-bit integers.
+__device__ __forceinline__ long long ld_index(const void* p, int i64, size_t i) {
+  return i64 ? static_cast<const long long*>(p)[i] : (long long)static_cast<const int*>(p)[i];
+}
+
+struct RotaryParams {
+  const void *Q, *K;
+  void *Qo, *Ko;
+  const float* table;      // [P, R]
+  const void* positions;   // [B, T] or null
+  unsigned* status;
+  int B, T, Hq, Hk, D, R, P;
+  int interleaved, inverse, pos_i64;
+  dp_strides q, k, qo, ko;
+};
+
+struct AttnParams {
+  const void *Q, *K, *V;
+  void* O;
+  float* lse;              // [B, Hq, T] (may be null in the forward pass)
+  const int *q_lens, *k_lens;
+  // gradient only
+  const void* dO;
+  const float* delta;      // [B, Hq, T]
+  void *dQ, *dK, *dV;
+  unsigned* status;
+  int B, T, S, Hq, Hk, D, causal, window;
+  float scale;
+  dp_strides q, k, v, o, d_o, dq, dk, dv;
+};
+
+// Example i's valid queries and keys.
+__device__ __forceinline__ int attn_lq(const AttnParams& P, int i) {
+  return P.q_lens ? max(0, min(P.T, P.q_lens[i])) : P.T;
+}
+__device__ __forceinline__ int attn_lk(const AttnParams& P, int i) {
+  return P.k_lens ? max(0, min(P.S, P.k_lens[i])) : P.S;
+}
+
+struct DistillParams {
+  const void *logits, *idx, *teacher, *labels;
+  const float *weights, *upstream;
+  float *row_loss, *loss;
+  void* grad;
+  unsigned* status;
+  int B, T, V, K, index_i64, label_i64, teacher_dtype;
+  long long ld, ldg;
+  float tau, alpha;
+};
+
+}  // namespace dpk
+
+namespace dph {
+cudaError_t launch_rotary_table(const dp_rotary_table_desc& d, float* table, cudaStream_t s);
+cudaError_t launch_rotary(const dpk::RotaryParams& P, int dtype, cudaStream_t s);
+// FFMA attention: both types, any strides, D <= 128.
+cudaError_t launch_attn_simt_fwd(const dpk::AttnParams& P, int dtype, cudaStream_t s);
+cudaError_t launch_attn_simt_grad(const dpk::AttnParams& P, int dtype, cudaStream_t s);
+// delta[b, h, t] = dO . O of each query row.
+cudaError_t launch_attn_delta(const dpk::AttnParams& P, int dtype, float* delta, cudaStream_t s);
+cudaError_t launch_distill(const dpk::DistillParams& P, int dtype, cudaStream_t s);
+}  // namespace dph

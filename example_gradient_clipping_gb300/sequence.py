@@ -1,0 +1,406 @@
+"""The sequence operators: rotary positions, attention and the distillation loss, with their gradients.
+
+They run between the linear layers whose per-example gradients PrivacyEngine clips:
+
+    table = dp.rotary_table(R=64, P=4096)                        # once
+    q, k = dp.rotary(q, k, table)                                # q [B, T, Hq, D], k [B, T, Hk, D]
+    o = dp.attention(q, k, v, causal=True, q_lens=lens, k_lens=lens)
+    loss, rows = dp.distill_loss(logits, indices, teacher, labels=y, weights=w, temperature=2.0, alpha=0.1)
+    loss.sum().backward(); engine.privatise(seed)
+
+rotary, attention and distill_loss take part in autograd; attention_forward,
+attention_backward and distill_loss_and_grad are the same computations without it.  The dp_*
+functions marshal the arguments of the C entry points of include/dpclip_seq.h, which states
+the formulas.  Work goes to the current stream of the tensors' device; results are allocated
+by torch, so the usual rules for using a tensor on another stream apply.  An argument that
+does not fit raises ValueError (or DPError, from the C side) before anything is launched.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from . import DP_BF16, DP_FP32, _check, _lib, _ptr, _stream
+
+DP_ROTARY_PLAIN, DP_ROTARY_LINEAR, DP_ROTARY_BASE, DP_ROTARY_PARTS = 0, 1, 2, 3
+_SCALINGS = {"plain": DP_ROTARY_PLAIN, "linear": DP_ROTARY_LINEAR, "base": DP_ROTARY_BASE, "parts": DP_ROTARY_PARTS}
+
+
+class Strides(ctypes.Structure):
+    """dp_strides: element strides of a [B, T, H, D] tensor."""
+    _fields_ = [("b", ctypes.c_longlong), ("t", ctypes.c_longlong), ("h", ctypes.c_longlong)]
+
+
+class RotaryTableDesc(ctypes.Structure):
+    _fields_ = [("P", ctypes.c_int), ("R", ctypes.c_int), ("scaling", ctypes.c_int), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("context", ctypes.c_double), ("slow", ctypes.c_double),
+                ("fast", ctypes.c_double)]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "B", "T", "Hq", "Hk", "D", "R", "P", "interleaved", "inverse",
+                                            "pos_i64")] + \
+               [(n, Strides) for n in ("q", "k", "q_out", "k_out")]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "B", "T", "S", "Hq", "Hk", "D", "causal", "window")] + \
+               [("scale", ctypes.c_float)] + \
+               [(n, Strides) for n in ("q", "k", "v", "o", "d_o", "dq", "dk", "dv")]
+
+
+class DistillDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "teacher_dtype", "B", "T", "V", "K", "index_i64", "label_i64")] + \
+               [("ld", ctypes.c_longlong), ("ld_grad", ctypes.c_longlong), ("tau", ctypes.c_float),
+                ("alpha", ctypes.c_float)]
+
+
+def _declare():
+    v, sz = ctypes.c_void_p, ctypes.c_size_t
+    P = ctypes.POINTER
+    sig = {
+        "dp_rotary_table": (ctypes.c_int, [P(RotaryTableDesc), v, v]),
+        "dp_rotary": (ctypes.c_int, [P(RotaryDesc)] + [v] * 7),
+        "dp_attention": (ctypes.c_int, [P(AttnDesc)] + [v] * 8),
+        "dp_attention_grad_workspace": (sz, [P(AttnDesc)]),
+        "dp_attention_grad": (ctypes.c_int, [P(AttnDesc)] + [v] * 12 + [sz, v]),
+        "dp_distill": (ctypes.c_int, [P(DistillDesc)] + [v] * 10),
+    }
+    for name, (res, args) in sig.items():
+        f = getattr(_lib, name)
+        f.restype, f.argtypes = res, args
+
+
+_declare()
+
+
+# ---- the C entry points ---------------------------------------------------------------
+def dp_rotary_table(desc: RotaryTableDesc, table, stream=None) -> None:
+    _check(_lib.dp_rotary_table(desc, _ptr(table), _stream(stream)))
+
+
+def dp_rotary(desc: RotaryDesc, Q, K, table, positions, Q_out, K_out, stream=None) -> None:
+    _check(_lib.dp_rotary(desc, _ptr(Q), _ptr(K), _ptr(table), _ptr(positions), _ptr(Q_out), _ptr(K_out),
+                          _stream(stream)))
+
+
+def dp_attention(desc: AttnDesc, Q, K, V, O, lse=None, q_lens=None, k_lens=None, stream=None) -> None:
+    _check(_lib.dp_attention(desc, _ptr(Q), _ptr(K), _ptr(V), _ptr(q_lens), _ptr(k_lens), _ptr(O), _ptr(lse),
+                             _stream(stream)))
+
+
+def dp_attention_grad_workspace(desc: AttnDesc) -> int:
+    return int(_lib.dp_attention_grad_workspace(desc))
+
+
+def dp_attention_grad(desc: AttnDesc, Q, K, V, O, lse, dO, dQ, dK, dV, workspace, q_lens=None, k_lens=None,
+                      ws_bytes: Optional[int] = None, stream=None) -> None:
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(_lib.dp_attention_grad(desc, _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse), _ptr(dO), _ptr(q_lens),
+                                  _ptr(k_lens), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(workspace), ws_bytes,
+                                  _stream(stream)))
+
+
+def dp_distill(desc: DistillDesc, logits, indices, teacher, labels=None, weights=None, upstream=None, row_loss=None,
+               loss=None, dlogits=None, stream=None) -> None:
+    _check(_lib.dp_distill(desc, _ptr(logits), _ptr(indices), _ptr(teacher), _ptr(labels), _ptr(weights),
+                           _ptr(upstream), _ptr(row_loss), _ptr(loss), _ptr(dlogits), _stream(stream)))
+
+
+# ---- argument checks ------------------------------------------------------------------
+_DTYPES = {torch.bfloat16: DP_BF16, torch.float32: DP_FP32}
+
+
+def _need(ok: bool, msg: str) -> None:
+    if not ok:
+        raise ValueError(msg)
+
+
+def _heads(x, name: str) -> None:
+    _need(x.dim() == 4 and x.is_cuda, f"{name}: a CUDA tensor [B, T, H, D], got {tuple(x.shape)} on {x.device}")
+    _need(x.dtype in _DTYPES, f"{name}: bf16 or fp32, got {x.dtype}")
+    _need(x.stride(3) == 1 or x.shape[3] == 1, f"{name}: the innermost stride must be 1, got {x.stride()}")
+
+
+def _like(x, ref, name: str) -> None:
+    _need(x.dtype == ref.dtype and x.device == ref.device, f"{name}: {x.dtype} on {x.device}, expected {ref.dtype} on "
+                                                           f"{ref.device}")
+
+
+def _vector(x, ref, shape, dtypes, name: str) -> None:
+    """A contiguous device array of `shape`, or None."""
+    if x is None:
+        return
+    _need(tuple(x.shape) == tuple(shape) and x.device == ref.device and x.is_contiguous() and x.dtype in dtypes,
+          f"{name}: a contiguous {' or '.join(str(d) for d in dtypes)} tensor {list(shape)} on {ref.device}, got "
+          f"{x.dtype} {list(x.shape)} on {x.device}")
+
+
+def _strides(x) -> Tuple[int, int, int]:
+    return x.stride()[:3]
+
+
+_INTS = (torch.int32, torch.int64)
+
+
+class _on:
+    """The tensors' device made current for the call (the C side uses the current device)."""
+
+    def __init__(self, x):
+        self.idx = x.device.index
+        self.prev = -1
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if cur != self.idx:
+            self.prev = cur
+            torch.cuda.set_device(self.idx)
+
+    def __exit__(self, *_):
+        if self.prev >= 0:
+            torch.cuda.set_device(self.prev)
+
+
+# Descriptors are plain values of shapes, strides and options: kept, so that a repeated call
+# does not build its structure again.
+_descs: dict = {}
+
+
+def _desc(key, make):
+    d = _descs.get(key)
+    if d is None:
+        if len(_descs) >= 512:
+            _descs.clear()
+        d = _descs[key] = make()
+    return d
+
+
+# ---- rotary ---------------------------------------------------------------------------
+def rotary_table(R: int, P: int, theta: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                 context: float = 4096.0, slow: float = 1.0, fast: float = 32.0, device="cuda", stream=None):
+    """Table fp32 [P, R] of the cosines and sines of R rotated entries at positions 0 .. P - 1.
+    scaling: "plain", "linear" (positions / factor), "base" (theta stretched by factor) or
+    "parts" (slow pairs interpolated, fast ones kept, by their turns over `context`)."""
+    _need(scaling in _SCALINGS, f"scaling {scaling!r}: one of {sorted(_SCALINGS)}")
+    _need(P > 0 and R > 0, f"P={P} and R={R} must be > 0")
+    table = torch.empty(P, R, dtype=torch.float32, device=device)
+    with _on(table):
+        dp_rotary_table(RotaryTableDesc(P, R, _SCALINGS[scaling], theta, factor, context, slow, fast), table, stream)
+    return table
+
+
+def _rotary(q, k, table, positions, interleaved, inverse, stream):
+    _heads(q, "q")
+    B, T, Hq, D = q.shape
+    if k is not None:
+        _heads(k, "k")
+        _like(k, q, "k")
+        _need(k.shape[0] == B and k.shape[1] == T and k.shape[3] == D, f"k {tuple(k.shape)} does not fit q {tuple(q.shape)}")
+    _need(table.dim() == 2 and table.dtype == torch.float32 and table.is_contiguous() and table.device == q.device,
+          "table: the contiguous fp32 [P, R] tensor of rotary_table, on q's device")
+    _vector(positions, q, (B, T), _INTS, "positions")
+    qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    ko = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k is not None else None
+    if q.numel() == 0 and (k is None or k.numel() == 0):
+        return qo, ko
+    Hk = k.shape[2] if k is not None else 0
+    p64 = positions is not None and positions.dtype == torch.int64
+    sq, sk = q.stride(), k.stride() if k is not None else (0, 0, 0, 1)
+    key = (RotaryDesc, q.dtype, B, T, Hq, Hk, D, table.shape, interleaved, inverse, p64, sq, sk)
+    d = _desc(key, lambda: RotaryDesc(_DTYPES[q.dtype], B, T, Hq, Hk, D, table.shape[1], table.shape[0],
+                                      int(bool(interleaved)), int(bool(inverse)), int(p64), Strides(*sq[:3]),
+                                      Strides(*sk[:3]), Strides(*_strides(qo)),
+                                      Strides(*(_strides(ko) if ko is not None else (0, 0, 0)))))
+    with _on(q):
+        dp_rotary(d, q, k, table, positions, qo, ko, stream)
+    return qo, ko
+
+
+def _rows_contiguous(g):
+    """A gradient as autograd hands it over (it may be expanded) with an innermost stride of 1."""
+    return g if g.stride(-1) == 1 or g.shape[-1] == 1 else g.contiguous()
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, table, positions, interleaved, inverse):
+        ctx.save_for_backward(table, positions)
+        ctx.opts = (interleaved, inverse)
+        return _rotary(q, k, table, positions, interleaved, inverse, None)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        table, positions = ctx.saved_tensors
+        interleaved, inverse = ctx.opts
+        dk = _rows_contiguous(dk) if dk is not None else None
+        gq, gk = _rotary(_rows_contiguous(dq), dk, table, positions, interleaved, not inverse, None)
+        return gq, gk, None, None, None, None
+
+
+def rotary(q, k, table, positions=None, interleaved: bool = False, inverse: bool = False, stream=None):
+    """(q', k') with the first table.shape[1] entries of every head turned by their position's
+    angles; k may be None.  positions: int32 or int64 [B, T], None for 0 .. T - 1.  inverse
+    turns back (and is the gradient)."""
+    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+        _need(stream is None, "a differentiable call runs on the current stream")
+        return _Rotary.apply(q, k, table, positions, interleaved, inverse)
+    return _rotary(q, k, table, positions, interleaved, inverse, stream)
+
+
+# ---- attention ------------------------------------------------------------------------
+def _attn_check(q, k, v, q_lens, k_lens):
+    for x, n in ((q, "q"), (k, "k"), (v, "v")):
+        _heads(x, n)
+    _like(k, q, "k")
+    _like(v, q, "v")
+    B, T, Hq, D = q.shape
+    _need(k.shape == v.shape and k.shape[0] == B and k.shape[3] == D, f"k {tuple(k.shape)} and v {tuple(v.shape)} do not "
+                                                                      f"fit q {tuple(q.shape)}")
+    _vector(q_lens, q, (B,), (torch.int32,), "q_lens")
+    _vector(k_lens, q, (B,), (torch.int32,), "k_lens")
+
+
+def _attn_desc(q, k, causal, window, scale, strides):
+    key = (AttnDesc, q.dtype, q.shape, k.shape, causal, window, scale, strides)
+
+    def make():
+        B, T, Hq, D = q.shape
+        d = AttnDesc(_DTYPES[q.dtype], B, T, k.shape[1], Hq, k.shape[2], D, int(bool(causal)), int(window),
+                     float(scale or 0.0))
+        for name, st in zip(("q", "k", "v", "o", "d_o", "dq", "dk", "dv"), strides):
+            setattr(d, name, Strides(*st[:3]))
+        return d
+    return _desc(key, make)
+
+
+def attention_forward(q, k, v, causal: bool = False, window: int = 0, scale: Optional[float] = None, q_lens=None,
+                      k_lens=None, stream=None):
+    """(o, lse): attention of q [B, T, Hq, D] over k, v [B, S, Hk, D] and each query's log-sum-exp
+    fp32 [B, Hq, T].  q_lens, k_lens: int32 [B], how many leading rows of each example are
+    there; causal aligns the last query with the last key; window > 0 keeps the latest
+    `window` keys.  scale defaults to 1/sqrt(D).  A query that sees no key gives 0 and -inf."""
+    _attn_check(q, k, v, q_lens, k_lens)
+    B, T, Hq, D = q.shape
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(B, Hq, T, dtype=torch.float32, device=q.device)
+    if q.numel() == 0 or k.numel() == 0:
+        return o.zero_(), lse.fill_(-float("inf"))
+    d = _attn_desc(q, k, causal, window, scale, (q.stride(), k.stride(), v.stride(), o.stride()))
+    with _on(q):
+        dp_attention(d, q, k, v, o, lse, q_lens, k_lens, stream)
+    return o, lse
+
+
+def attention_backward(q, k, v, o, lse, do, causal: bool = False, window: int = 0, scale: Optional[float] = None,
+                       q_lens=None, k_lens=None, stream=None):
+    """(dq, dk, dv) for the gradient `do` of attention_forward's o, the probabilities formed
+    again from lse; the other arguments as in the forward call."""
+    _attn_check(q, k, v, q_lens, k_lens)
+    for x, n in ((o, "o"), (do, "do")):
+        _heads(x, n)
+        _like(x, q, n)
+        _need(x.shape == q.shape, f"{n} {tuple(x.shape)} is not shaped like q {tuple(q.shape)}")
+    _vector(lse, q, (q.shape[0], q.shape[2], q.shape[1]), (torch.float32,), "lse")
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    dv = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    if q.numel() == 0 or k.numel() == 0:
+        return dq.zero_(), dk.zero_(), dv.zero_()
+    d = _attn_desc(q, k, causal, window, scale, (q.stride(), k.stride(), v.stride(), o.stride(), do.stride(),
+                                                 dq.stride(), dk.stride(), dv.stride()))
+    ws = torch.empty(dp_attention_grad_workspace(d), dtype=torch.uint8, device=q.device)
+    with _on(q):
+        dp_attention_grad(d, q, k, v, o, lse, do, dq, dk, dv, ws, q_lens, k_lens, stream=stream)
+    return dq, dk, dv
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, causal, window, scale, q_lens, k_lens):
+        o, lse = attention_forward(q, k, v, causal, window, scale, q_lens, k_lens)
+        ctx.save_for_backward(q, k, v, o, lse, q_lens, k_lens)
+        ctx.opts = (causal, window, scale)
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, o, lse, q_lens, k_lens = ctx.saved_tensors
+        return attention_backward(q, k, v, o, lse, _rows_contiguous(do), *ctx.opts, q_lens, k_lens) + (None,) * 5
+
+
+def attention(q, k, v, causal: bool = False, window: int = 0, scale: Optional[float] = None, q_lens=None, k_lens=None):
+    """attention_forward's o, with its gradient."""
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        return _Attention.apply(q, k, v, causal, window, scale, q_lens, k_lens)
+    return attention_forward(q, k, v, causal, window, scale, q_lens, k_lens)[0]
+
+
+# ---- distillation ---------------------------------------------------------------------
+def _distill(logits, indices, teacher, labels, weights, upstream, temperature, alpha, want_loss, want_grad, stream):
+    _need(logits.dim() == 3 and logits.is_cuda and logits.dtype in _DTYPES,
+          f"logits: a bf16 or fp32 CUDA tensor [B, T, V], got {logits.dtype} {tuple(logits.shape)} on {logits.device}")
+    B, T, V = logits.shape
+    sb, sr, sv = logits.stride()
+    ld = sr if T > 1 else sb if B > 1 else V
+    _need((sv == 1 or V == 1) and (B <= 1 or T <= 1 or sb == T * sr), f"logits: rows at one stride and an innermost "
+                                                                      f"stride of 1, got strides {logits.stride()}")
+    _need(indices.dim() == 3 and teacher.dtype in _DTYPES, "indices and teacher: [B, T, K], teacher bf16 or fp32")
+    K = indices.shape[2]
+    _vector(indices, logits, (B, T, K), _INTS, "indices")
+    _vector(teacher, logits, (B, T, K), tuple(_DTYPES), "teacher")
+    _vector(labels, logits, (B, T), _INTS, "labels")
+    _vector(weights, logits, (B, T), (torch.float32,), "weights")
+    _vector(upstream, logits, (B,), (torch.float32,), "upstream")
+    dev = logits.device
+    loss = torch.empty(B, dtype=torch.float32, device=dev) if want_loss else None
+    rows = torch.empty(B, T, dtype=torch.float32, device=dev) if want_loss else None
+    grad = torch.empty(B, T, V, dtype=logits.dtype, device=dev) if want_grad else None
+    if logits.numel() == 0:
+        _need(V > 0, "logits: the vocabulary is empty")
+        return (loss.zero_() if want_loss else None), rows, grad
+    i64, l64 = indices.dtype == torch.int64, labels is not None and labels.dtype == torch.int64
+    key = (DistillDesc, logits.dtype, teacher.dtype, B, T, V, K, i64, l64, ld, temperature, alpha)
+    d = _desc(key, lambda: DistillDesc(_DTYPES[logits.dtype], _DTYPES[teacher.dtype], B, T, V, K, int(i64), int(l64), ld,
+                                       V, float(temperature), float(alpha)))
+    with _on(logits):
+        dp_distill(d, logits, indices, teacher, labels, weights, upstream, rows, loss, grad, stream)
+    return loss, rows, grad
+
+
+class _Distill(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, indices, teacher, labels, weights, temperature, alpha):
+        loss, rows, _ = _distill(logits, indices, teacher, labels, weights, None, temperature, alpha, True, False, None)
+        ctx.save_for_backward(logits, indices, teacher, labels, weights)
+        ctx.opts = (temperature, alpha)
+        ctx.mark_non_differentiable(rows)
+        return loss, rows
+
+    @staticmethod
+    def backward(ctx, up, _):
+        logits, indices, teacher, labels, weights = ctx.saved_tensors
+        grad = _distill(logits, indices, teacher, labels, weights, up.float().contiguous(), *ctx.opts, False, True, None)[2]
+        return grad, None, None, None, None, None, None
+
+
+def distill_loss(logits, indices, teacher, labels=None, weights=None, temperature: float = 1.0, alpha: float = 0.0,
+                 stream=None):
+    """(loss, rows): each example's distillation loss fp32 [B] and its weighted tokens' losses
+    fp32 [B, T].  logits [B, T, V] of the student; indices (int32 or int64, -1: no entry) and
+    teacher [B, T, K] the teacher's top logits; labels [B, T] (negative: none); weights fp32
+    [B, T].  loss carries the gradient with respect to the logits."""
+    if torch.is_grad_enabled() and logits.requires_grad:
+        _need(stream is None, "a differentiable call runs on the current stream")
+        return _Distill.apply(logits, indices, teacher, labels, weights, temperature, alpha)
+    return _distill(logits, indices, teacher, labels, weights, None, temperature, alpha, True, False, stream)[:2]
+
+
+def distill_loss_and_grad(logits, indices, teacher, labels=None, weights=None, upstream=None, temperature: float = 1.0,
+                          alpha: float = 0.0, stream=None):
+    """(loss, dlogits) in one pass over the logits: distill_loss and the gradient of
+    sum_i upstream_i loss_i (upstream fp32 [B], None: 1), the G of the layer that made them."""
+    loss, _, grad = _distill(logits, indices, teacher, labels, weights, upstream, temperature, alpha, True, True, stream)
+    return loss, grad
