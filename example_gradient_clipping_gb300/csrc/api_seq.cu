@@ -113,7 +113,9 @@ dp_status dp_attention(const dp_attn_desc* d, const void* Q, const void* K, cons
   if (!Q || !K || !V || !O) return bad(DP_ERR_INVALID_ARG, "Q, K, V and O must be non-NULL");
   if (!P.status) return bad(DP_ERR_CUDA, "cannot resolve the device status word");
   P.Q = Q; P.K = K; P.V = V; P.O = O; P.lse = lse; P.q_lens = q_lens; P.k_lens = k_lens;
-  return launched(dph::launch_attn_simt_fwd(P, d->dtype, stream), "dp_attention");
+  const cudaError_t e = dph::attn_tc_fwd_supported(P, d->dtype) ? dph::launch_attn_tc_fwd(P, stream)
+                                                                 : dph::launch_attn_simt_fwd(P, d->dtype, stream);
+  return launched(e, "dp_attention");
 }
 
 size_t dp_attention_grad_workspace(const dp_attn_desc* d) {
@@ -140,7 +142,9 @@ dp_status dp_attention_grad(const dp_attn_desc* d, const void* Q, const void* K,
   float* delta = static_cast<float*>(workspace);
   P.delta = delta;
   cudaError_t e = dph::launch_attn_delta(P, d->dtype, delta, stream);
-  if (e == cudaSuccess) e = dph::launch_attn_simt_grad(P, d->dtype, stream);
+  if (e == cudaSuccess)
+    e = dph::attn_tc_grad_supported(P, d->dtype) ? dph::launch_attn_tc_grad(P, stream)
+                                                 : dph::launch_attn_simt_grad(P, d->dtype, stream);
   return launched(e, "dp_attention_grad");
 }
 

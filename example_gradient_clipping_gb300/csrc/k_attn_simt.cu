@@ -21,18 +21,6 @@ namespace attnsimt {
 
 constexpr int BT = 64, PS = BT + 4, kThreads = 256;
 
-// Keys [lo, hi) that some query of [t0, t1) sees (t1 <= Lq).
-__device__ __forceinline__ void key_range(const AttnParams& P, int t0, int t1, int lq, int lk, int* lo, int* hi) {
-  const int e = lk - lq;
-  *lo = P.window ? max(0, t0 + e - P.window + 1) : 0;
-  *hi = P.causal ? min(lk, t1 + e) : lk;
-}
-// Queries [lo, hi) that see some key of [j0, j1) (j1 <= Lk).
-__device__ __forceinline__ void query_range(const AttnParams& P, int j0, int j1, int lq, int lk, int* lo, int* hi) {
-  const int e = lk - lq;
-  *lo = P.causal ? max(0, j0 - e) : 0;
-  *hi = P.window ? min(lq, j1 - 1 - e + P.window) : lq;
-}
 __device__ __forceinline__ bool sees(const AttnParams& P, int t, int j, int lq, int lk) {
   const int last = t + lk - lq;
   return t < lq && j < lk && (!P.causal || j <= last) && (!P.window || j > last - P.window);

@@ -1,0 +1,404 @@
+// Attention's forward pass on the tensor cores (bf16, D <= 128).
+//
+//   S = scale Q K^T,  P = exp2(S log2e - m),  O = P V / l,  one pass over the keys with each
+//   row's running reference m and sum l; lse = m ln2 + log l.
+//
+// A CTA holds NT query tiles of 128 rows of one head (NT = 2: the tensor cores work on one
+// tile's products while the other tile's softmax runs).
+//   warp 0     TMA: Q once, then K and V tiles of 128 keys through a ring of slots
+//   warp 1     MMA issuer: S = Q K^T (both from shared memory), O += P V with P read from
+//              tensor memory, where it overlays the S it was made from
+//   warps 4..  softmax, a warpgroup per query tile, a thread per row: S from TMEM, mask,
+//              reference, exp2, P as bf16 back to TMEM; at the end O / l and lse
+// The reference m follows the row's maximum lazily: only when the maximum has grown past it
+// by 8 (P up to 256, exact in the fp32 sums and no worse rounded in bf16) are O and l
+// rescaled, so after the first tiles nearly no tile touches O.
+// Rows of V past the keys' length may hold anything: the issuing warp zeroes them in shared
+// memory before the product (0 * NaN); K's only reach scores that the mask replaces.
+#include <algorithm>
+
+#include "seq.cuh"
+#include "tc.cuh"
+#include "tc_ptx.cuh"
+
+namespace dpk {
+namespace attntc {
+
+constexpr int BT = 128;            // rows of a query tile, keys of a key tile
+constexpr int SUB = BT * 128;      // 128 rows x 64 columns of bf16 (128-byte swizzle)
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Zero rows [r0, 128) of a tile of DP columns (whole 128-byte rows of each 64-column part, so
+// the swizzle does not matter), by one warp, for the async proxy.
+template <int DP>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int lane) {
+  for (int i = r0 * 8 + lane; i < BT * 8; i += 32)
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c) *reinterpret_cast<uint4*>(tile + c * SUB + i * 16) = make_uint4(0, 0, 0, 0);
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+}
+
+template <int DP>
+__device__ __forceinline__ void load_tile(const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int row, int h, int b) {
+#pragma unroll
+  for (int c = 0; c < DP / 64; ++c) ptx::tma_load_4d(map, bar, dst + c * SUB, 64 * c, row, h, b);
+}
+
+// D[128, 128] = A rows . B rows over DP columns (both K-major)
+template <int DP>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
+  const uint64_t da = ptx::sdesc_sw128(a, 16, 1024), db = ptx::sdesc_sw128(b, 16, 1024);
+  constexpr uint32_t idesc = ptx::idesc_bf16_f32(BT, BT, 0, 0);
+#pragma unroll
+  for (int kk = 0; kk < DP / 16; ++kk) {
+    const uint32_t o = (kk / 4) * SUB + (kk % 4) * 32;
+    ptx::umma_bf16(d, ptx::sdesc_add(da, o), ptx::sdesc_add(db, o), idesc, kk != 0);
+  }
+}
+
+template <int DP, int NT> struct Fwd {
+  static constexpr int TILE = DP / 64 * SUB;
+  // key/value slots: what fits beside the query tiles (NT = 1: of half an SM)
+  static constexpr int SLOTS = NT == 2 ? (DP == 128 ? 4 : 6) : (DP == 128 ? 2 : 4);
+  static constexpr int THREADS = 128 + 128 * NT;
+  static constexpr int SMEM = (NT + SLOTS) * TILE + 1024 + 256;
+  static constexpr uint32_t TCOLS = NT == 2 ? 512 : 256;
+  // registers: the first warpgroup's give-away must cover what the softmax warpgroups take
+  // (of the launch's 168 x 384 or 128 x 256)
+  static constexpr int REGS_LOW = 56, REGS_HIGH = NT == 2 ? 224 : 200;
+  static_assert(128 * REGS_LOW + 128 * NT * REGS_HIGH <= THREADS * (NT == 2 ? 168 : 128), "register split");
+};
+
+template <int DP, int NT>
+__global__ void __launch_bounds__(Fwd<DP, NT>::THREADS, NT == 2 ? 1 : 2)
+attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                   const __grid_constant__ CUtensorMap mapV, AttnParams P) {
+  using C = Fwd<DP, NT>;
+  constexpr int TILE = C::TILE, SLOTS = C::SLOTS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = smem + NT * TILE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + SLOTS * TILE);
+  uint64_t* empty = full + SLOTS;
+  uint64_t* q_full = empty + SLOTS;
+  uint64_t* s_full = q_full + 1;      // NT
+  uint64_t* p_ready = s_full + NT;    // NT
+  uint64_t* o_full = p_ready + NT;    // NT
+  uint64_t* drain = o_full + NT;      // after an abort only
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // causal: the longest tiles first, over all heads; else a head's tiles next to one another
+  const int tiles = (P.T + NT * BT - 1) / (NT * BT), heads = P.B * P.Hq;
+  const int idx = (int)blockIdx.x;
+  const int tile = P.causal ? tiles - 1 - idx / heads : idx % tiles;
+  const int bh = P.causal ? idx % heads : idx / tiles;
+  const int b = bh / P.Hq, h = bh - b * P.Hq, hk = h / (P.Hq / P.Hk);
+  const int t0 = tile * NT * BT;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < SLOTS; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    ptx::mbar_init(q_full, 1);
+    ptx::mbar_init(drain, 1);
+    for (int x = 0; x < NT; ++x) {
+      ptx::mbar_init(&s_full[x], 1);
+      ptx::mbar_init(&p_ready[x], 4);
+      ptx::mbar_init(&o_full[x], 1);
+    }
+    *abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tensormap(&mapQ);
+    ptx::prefetch_tensormap(&mapK);
+    ptx::prefetch_tensormap(&mapV);
+  }
+  if (warp == 1) ptx::tmem_alloc(tmem_slot, C::TCOLS);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tS = tmem, tO = tmem + NT * BT;   // S (and P) of tile x at tS + 128 x, O at tO + DP x
+  pdl_trigger();
+  pdl_wait();
+
+  const int lq = attn_lq(P, b), lk = attn_lk(P, b), e = lk - lq;
+  // key tiles [j0, j0 + n[x]) of each query tile
+  int j0 = 0, n[NT], nmax = 0;
+#pragma unroll
+  for (int x = 0; x < NT; ++x) {
+    const int ta = t0 + x * BT;
+    int lo = 0, hi = 0;
+    if (ta < lq) key_range(P, ta, min(ta + BT, lq), lq, lk, &lo, &hi);
+    if (x == 0) j0 = lo / BT;
+    n[x] = max(0, (hi + BT - 1) / BT - j0);
+    nmax = max(nmax, n[x]);
+  }
+
+  if (warp >= 4) {
+    ptx::regs_inc<C::REGS_HIGH>();
+    const int x = (warp - 4) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane, ta = t0 + x * BT, t = ta + row;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t mS = tS + x * BT + lanes, mO = tO + x * DP + lanes;
+    const int nx = NT == 1 || x == 0 ? n[0] : n[NT - 1];
+    const float sc2 = P.scale * kLog2e;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < nx; ++j) {
+      const bool w = ptx::mbar_wait(&s_full[x], j & 1, abort, P.status);
+      if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+      ptx::tc_fence_after();
+      float s[BT];
+#pragma unroll
+      for (int c = 0; c < BT / 32; ++c) ptx::tmem_ld32(mS + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
+      ptx::tmem_wait_ld();
+      const int k0 = (j0 + j) * BT;
+      // some entry of the tile is hidden: past the keys, after the query, before its window
+      if (k0 + BT > lk || (P.causal && k0 + BT - 1 > ta + e) || (P.window && k0 <= ta + BT - 1 + e - P.window)) {
+        const int hi = (P.causal ? min(lk - 1, t + e) : lk - 1) - k0;
+        const int lo = (P.window ? t + e - P.window + 1 : 0) - k0;
+#pragma unroll
+        for (int c = 0; c < BT; ++c)
+          if (c > hi || c < lo) s[c] = -INFINITY;
+      }
+      float mx = s[0];
+#pragma unroll
+      for (int c = 1; c < BT; ++c) mx = fmaxf(mx, s[c]);
+      mx *= sc2;
+      const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
+      if (__any_sync(0xffffffffu, grow)) {
+        const float f = grow ? ex2(m - mx) : 1.f;
+        if (grow) m = mx;
+        l *= f;
+        if (j > 0) {
+#pragma unroll 1
+          for (int c = 0; c < DP; c += 32) {
+            float o[32];
+            ptx::tmem_ld32(mO + c, o);
+            ptx::tmem_wait_ld();
+            uint32_t u[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
+            ptx::tmem_st32(mO + c, u);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < BT; c += 64) {
+        uint32_t u[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float p0 = ex2(fmaf(s[c + 2 * i], sc2, -base)), p1 = ex2(fmaf(s[c + 2 * i + 1], sc2, -base));
+          sum[(2 * i) & 3] += p0;
+          sum[(2 * i + 1) & 3] += p1;
+          u[i] = pack_bf16(p0, p1);
+        }
+        ptx::tmem_st32(mS + c / 2, u);
+      }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&p_ready[x]);
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
+    if (nx > 0 && ok) {
+      const bool w = ptx::mbar_wait(&o_full[x], 0, abort, P.status);
+      ok = __all_sync(0xffffffffu, w);
+      ptx::tc_fence_after();
+    }
+    if (ok) {
+      const bool none = t >= lq || nx == 0 || l == 0.f;   // a query that sees no key
+      const float inv = none ? 0.f : 1.f / l;
+      if (P.lse && t < P.T) P.lse[((size_t)b * P.Hq + h) * P.T + t] = none ? -INFINITY : m * kLn2 + logf(l);
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(P.O) + b * P.o.b + t * P.o.t + h * P.o.h;
+#pragma unroll 1
+      for (int c = 0; c < DP; c += 32) {
+        float o[32];
+        if (nx > 0) {
+          ptx::tmem_ld32(mO + c, o);
+          ptx::tmem_wait_ld();
+        }
+        if (t < P.T) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (c + 8 * q < P.D) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (!none)
+                v = make_uint4(pack_bf16(o[8 * q] * inv, o[8 * q + 1] * inv),
+                               pack_bf16(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                               pack_bf16(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
+                               pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+              *reinterpret_cast<uint4*>(out + c + 8 * q) = v;
+            }
+          }
+        }
+      }
+    }
+  } else {
+    ptx::regs_dec<C::REGS_LOW>();
+    if (warp == 0) {
+      int last = -1;
+      if (nmax > 0 && ptx::elect_one()) {
+        ptx::mbar_arrive_expect_tx(q_full, NT * TILE);
+        for (int x = 0; x < NT; ++x) load_tile<DP>(&mapQ, q_full, smem + x * TILE, t0 + x * BT, h, b);
+      }
+      __syncwarp();
+      for (int i = 0; i < 2 * nmax; ++i) {   // K 0, V 0, K 1, V 1, ...
+        const int s = i % SLOTS;
+        const bool w = ptx::mbar_wait(&empty[s], ((i / SLOTS) & 1) ^ 1, abort, P.status);
+        if (!__all_sync(0xffffffffu, w)) break;
+        if (ptx::elect_one()) {
+          ptx::mbar_arrive_expect_tx(&full[s], TILE);
+          load_tile<DP>(i & 1 ? &mapV : &mapK, &full[s], ring + s * TILE, (j0 + i / 2) * BT, hk, b);
+        }
+        __syncwarp();
+        last = i;
+      }
+      if (*abort && lane == 0) {   // let the copies in flight land before the CTA exits
+        if (nmax > 0) ptx::mbar_wait_drain(q_full, 0);
+        for (int i = max(0, last - SLOTS + 1); i <= last; ++i) ptx::mbar_wait_drain(&full[i % SLOTS], (i / SLOTS) & 1);
+      }
+    } else if (warp == 1) {
+      constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(BT, DP, 0, 1);
+      const uint32_t sq = ptx::smem_u32(smem), sr = ptx::smem_u32(ring);
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int parity) {
+        const bool w = ptx::mbar_wait(bar, parity & 1, abort, P.status);
+        ok = __all_sync(0xffffffffu, w);
+        return ok;
+      };
+      if (nmax > 0 && wait(q_full, 0) && wait(&full[0], 0)) {
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+  #pragma unroll
+          for (int x = 0; x < NT; ++x)
+            if (n[x] > 0) {
+              mma_rows<DP>(tS + x * BT, sq + x * TILE, sr);
+              ptx::umma_commit(&s_full[x]);
+            }
+          ptx::umma_commit(&empty[0]);
+        }
+        __syncwarp();
+        for (int j = 0; j < nmax && ok; ++j) {
+          const int iv = 2 * j + 1, ik = 2 * j + 2, sv = iv % SLOTS, sk = ik % SLOTS;
+          if (!wait(&full[sv], iv / SLOTS)) break;
+          const int rest = lk - (j0 + j) * BT;   // keys of this tile that are there
+          if (rest < BT && lk < P.S) zero_rows<DP>(ring + sv * TILE, rest, lane);
+          const bool more = j + 1 < nmax;
+          if (more && !wait(&full[sk], ik / SLOTS)) break;
+  #pragma unroll
+          for (int x = 0; x < NT; ++x) {
+            if (j >= n[x]) continue;
+            if (!wait(&p_ready[x], j)) break;
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) {
+              const uint64_t db = ptx::sdesc_sw128(sr + sv * TILE, SUB, 1024);
+  #pragma unroll
+              for (int kk = 0; kk < BT / 16; ++kk)
+                ptx::umma_bf16_ta(tO + x * DP, tS + x * BT + kk * 8, ptx::sdesc_add(db, kk * 2048), idesc_pv,
+                                  (j | kk) != 0);
+              if (j + 1 < n[x]) {   // in order after the product that reads P from these columns
+                mma_rows<DP>(tS + x * BT, sq + x * TILE, sr + sk * TILE);
+                ptx::umma_commit(&s_full[x]);
+              } else {
+                ptx::umma_commit(&o_full[x]);
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (ptx::elect_one()) {
+            ptx::umma_commit(&empty[sv]);
+            if (more) ptx::umma_commit(&empty[sk]);
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (*abort && threadIdx.x == 32) {   // MMAs in flight
+    ptx::umma_commit(drain);
+    ptx::mbar_wait_drain(drain, 0);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::TCOLS);
+  }
+}
+
+}  // namespace attntc
+}  // namespace dpk
+
+namespace dph {
+using namespace dpk;
+
+// A [B, n, H, D] bf16 tensor that TMA can address: 16-byte base and strides (those of an
+// extent of 1 do not count).
+static bool tma_ok(const void* p, const dp_strides& s, int B, int n, int H) {
+  auto fits = [](long long st, int extent) { return extent == 1 || (st > 0 && st % 8 == 0 && st < (1ll << 38)); };
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && fits(s.b, B) && fits(s.t, n) && fits(s.h, H);
+}
+static bool vec_ok(const void* p, const dp_strides& s, int B, int n, int H) {
+  auto fits = [](long long st, int extent) { return extent == 1 || st % 8 == 0; };
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && fits(s.b, B) && fits(s.t, n) && fits(s.h, H);
+}
+
+static bool map_heads(CUtensorMap* map, const void* p, const dp_strides& s, int B, int n, int H, int D) {
+  auto bytes = [](long long st, int extent) { return extent == 1 ? (uint64_t)1 << 20 : (uint64_t)st * 2; };
+  const uint64_t dims[4] = {(uint64_t)D, (uint64_t)n, (uint64_t)H, (uint64_t)B};
+  const uint64_t st[3] = {bytes(s.t, n), bytes(s.h, H), bytes(s.b, B)};
+  const uint32_t box[4] = {64, attntc::BT, 1, 1};
+  return encode_tmap_bf16(map, p, 4, dims, st, box);
+}
+
+bool attn_tc_fwd_supported(const AttnParams& P, int dtype) {
+  return dtype == DP_BF16 && P.D % 8 == 0 && tma_ok(P.Q, P.q, P.B, P.T, P.Hq) && tma_ok(P.K, P.k, P.B, P.S, P.Hk) &&
+         tma_ok(P.V, P.v, P.B, P.S, P.Hk) && vec_ok(P.O, P.o, P.B, P.T, P.Hq);
+}
+
+template <int DP, int NT>
+static cudaError_t run_fwd(const AttnParams& P, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                           cudaStream_t s) {
+  using C = attntc::Fwd<DP, NT>;
+  static const cudaError_t set = cudaFuncSetAttribute(attntc::attn_tc_fwd_kernel<DP, NT>,
+                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (set != cudaSuccess) return set;
+  const unsigned grid = (unsigned)((size_t)P.B * P.Hq * ((P.T + NT * attntc::BT - 1) / (NT * attntc::BT)));
+  return launch_pdl(attntc::attn_tc_fwd_kernel<DP, NT>, grid, C::THREADS, C::SMEM, s, mq, mk, mv, P);
+}
+
+cudaError_t launch_attn_tc_fwd(const AttnParams& P, cudaStream_t s) {
+  CUtensorMap mq, mk, mv;
+  if (!map_heads(&mq, P.Q, P.q, P.B, P.T, P.Hq, P.D) || !map_heads(&mk, P.K, P.k, P.B, P.S, P.Hk, P.D) ||
+      !map_heads(&mv, P.V, P.v, P.B, P.S, P.Hk, P.D))
+    return cudaErrorInvalidValue;
+  // one tile per CTA where there is only one, or where pairs of tiles would leave SMs idle
+  const bool pair = P.T > attntc::BT && (size_t)P.B * P.Hq * ((P.T + 2 * attntc::BT - 1) / (2 * attntc::BT)) >= 152;
+  if (P.D <= 64) return pair ? run_fwd<64, 2>(P, mq, mk, mv, s) : run_fwd<64, 1>(P, mq, mk, mv, s);
+  return pair ? run_fwd<128, 2>(P, mq, mk, mv, s) : run_fwd<128, 1>(P, mq, mk, mv, s);
+}
+
+bool attn_tc_grad_supported(const AttnParams&, int) { return false; }
+cudaError_t launch_attn_tc_grad(const AttnParams&, cudaStream_t) { return cudaErrorNotSupported; }
+
+}  // namespace dph

@@ -42,6 +42,19 @@ struct AttnParams {
   dp_strides q, k, v, o, d_o, dq, dk, dv;
 };
 
+// Keys [lo, hi) that some query of [t0, t1) sees (t1 <= Lq).
+__device__ __forceinline__ void key_range(const AttnParams& P, int t0, int t1, int lq, int lk, int* lo, int* hi) {
+  const int e = lk - lq;
+  *lo = P.window ? max(0, t0 + e - P.window + 1) : 0;
+  *hi = P.causal ? min(lk, t1 + e) : lk;
+}
+// Queries [lo, hi) that see some key of [j0, j1) (j1 <= Lk).
+__device__ __forceinline__ void query_range(const AttnParams& P, int j0, int j1, int lq, int lk, int* lo, int* hi) {
+  const int e = lk - lq;
+  *lo = P.causal ? max(0, j0 - e) : 0;
+  *hi = P.window ? min(lq, j1 - 1 - e + P.window) : lq;
+}
+
 // Example i's valid queries and keys.
 __device__ __forceinline__ int attn_lq(const AttnParams& P, int i) {
   return P.q_lens ? max(0, min(P.T, P.q_lens[i])) : P.T;
@@ -69,6 +82,11 @@ cudaError_t launch_rotary(const dpk::RotaryParams& P, int dtype, cudaStream_t s)
 // FFMA attention: both types, any strides, D <= 128.
 cudaError_t launch_attn_simt_fwd(const dpk::AttnParams& P, int dtype, cudaStream_t s);
 cudaError_t launch_attn_simt_grad(const dpk::AttnParams& P, int dtype, cudaStream_t s);
+// Tensor-core attention: bf16, D a multiple of 8, operands TMA can address.
+bool attn_tc_fwd_supported(const dpk::AttnParams& P, int dtype);
+bool attn_tc_grad_supported(const dpk::AttnParams& P, int dtype);
+cudaError_t launch_attn_tc_fwd(const dpk::AttnParams& P, cudaStream_t s);
+cudaError_t launch_attn_tc_grad(const dpk::AttnParams& P, cudaStream_t s);
 // delta[b, h, t] = dO . O of each query row.
 cudaError_t launch_attn_delta(const dpk::AttnParams& P, int dtype, float* delta, cudaStream_t s);
 cudaError_t launch_distill(const dpk::DistillParams& P, int dtype, cudaStream_t s);

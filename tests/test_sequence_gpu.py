@@ -1,7 +1,7 @@
 """The sequence operators on the GPU against their definitions in 64 bits (seq_reference).
 
 Attention is held to componentwise error bounds that seq_reference derives beside its values:
-fp32 sums and statistics, and for bf16 the rounding (2^-9) of the probabilities and their
+fp32 sums and statistics, and for bf16 the rounding (2^-8) of the probabilities and their
 gradients in the second products, of the stored o and of the results.  The other operators'
 tolerances are derived where they stand.
 """
@@ -38,7 +38,7 @@ def _within(got, want):
 
 
 def _r(dtype):
-    return 2.0 ** -9 if dtype == "bf16" else 0.0
+    return 2.0 ** -8 if dtype == "bf16" else 0.0   # 8 significant bits
 
 
 # ---------------------------------------------------------------------------------------- rotary
