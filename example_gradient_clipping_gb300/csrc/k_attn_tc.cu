@@ -17,55 +17,10 @@
 // memory before the product (0 * NaN); K's only reach scores that the mask replaces.
 #include <algorithm>
 
-#include "seq.cuh"
-#include "tc.cuh"
-#include "tc_ptx.cuh"
+#include "attn_tc.cuh"
 
 namespace dpk {
 namespace attntc {
-
-constexpr int BT = 128;            // rows of a query tile, keys of a key tile
-constexpr int SUB = BT * 128;      // 128 rows x 64 columns of bf16 (128-byte swizzle)
-constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Zero rows [r0, 128) of a tile of DP columns (whole 128-byte rows of each 64-column part, so
-// the swizzle does not matter), by one warp, for the async proxy.
-template <int DP>
-__device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int lane) {
-  for (int i = r0 * 8 + lane; i < BT * 8; i += 32)
-#pragma unroll
-    for (int c = 0; c < DP / 64; ++c) *reinterpret_cast<uint4*>(tile + c * SUB + i * 16) = make_uint4(0, 0, 0, 0);
-  ptx::fence_proxy_async_smem();
-  __syncwarp();
-}
-
-template <int DP>
-__device__ __forceinline__ void load_tile(const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int row, int h, int b) {
-#pragma unroll
-  for (int c = 0; c < DP / 64; ++c) ptx::tma_load_4d(map, bar, dst + c * SUB, 64 * c, row, h, b);
-}
-
-// D[128, 128] = A rows . B rows over DP columns (both K-major)
-template <int DP>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
-  const uint64_t da = ptx::sdesc_sw128(a, 16, 1024), db = ptx::sdesc_sw128(b, 16, 1024);
-  constexpr uint32_t idesc = ptx::idesc_bf16_f32(BT, BT, 0, 0);
-#pragma unroll
-  for (int kk = 0; kk < DP / 16; ++kk) {
-    const uint32_t o = (kk / 4) * SUB + (kk % 4) * 32;
-    ptx::umma_bf16(d, ptx::sdesc_add(da, o), ptx::sdesc_add(db, o), idesc, kk != 0);
-  }
-}
 
 template <int DP, int NT> struct Fwd {
   static constexpr int TILE = DP / 64 * SUB;
@@ -352,25 +307,6 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
 namespace dph {
 using namespace dpk;
 
-// A [B, n, H, D] bf16 tensor that TMA can address: 16-byte base and strides (those of an
-// extent of 1 do not count).
-static bool tma_ok(const void* p, const dp_strides& s, int B, int n, int H) {
-  auto fits = [](long long st, int extent) { return extent == 1 || (st > 0 && st % 8 == 0 && st < (1ll << 38)); };
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && fits(s.b, B) && fits(s.t, n) && fits(s.h, H);
-}
-static bool vec_ok(const void* p, const dp_strides& s, int B, int n, int H) {
-  auto fits = [](long long st, int extent) { return extent == 1 || st % 8 == 0; };
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && fits(s.b, B) && fits(s.t, n) && fits(s.h, H);
-}
-
-static bool map_heads(CUtensorMap* map, const void* p, const dp_strides& s, int B, int n, int H, int D) {
-  auto bytes = [](long long st, int extent) { return extent == 1 ? (uint64_t)1 << 20 : (uint64_t)st * 2; };
-  const uint64_t dims[4] = {(uint64_t)D, (uint64_t)n, (uint64_t)H, (uint64_t)B};
-  const uint64_t st[3] = {bytes(s.t, n), bytes(s.h, H), bytes(s.b, B)};
-  const uint32_t box[4] = {64, attntc::BT, 1, 1};
-  return encode_tmap_bf16(map, p, 4, dims, st, box);
-}
-
 bool attn_tc_fwd_supported(const AttnParams& P, int dtype) {
   return dtype == DP_BF16 && P.D % 8 == 0 && tma_ok(P.Q, P.q, P.B, P.T, P.Hq) && tma_ok(P.K, P.k, P.B, P.S, P.Hk) &&
          tma_ok(P.V, P.v, P.B, P.S, P.Hk) && vec_ok(P.O, P.o, P.B, P.T, P.Hq);
@@ -397,8 +333,5 @@ cudaError_t launch_attn_tc_fwd(const AttnParams& P, cudaStream_t s) {
   if (P.D <= 64) return pair ? run_fwd<64, 2>(P, mq, mk, mv, s) : run_fwd<64, 1>(P, mq, mk, mv, s);
   return pair ? run_fwd<128, 2>(P, mq, mk, mv, s) : run_fwd<128, 1>(P, mq, mk, mv, s);
 }
-
-bool attn_tc_grad_supported(const AttnParams&, int) { return false; }
-cudaError_t launch_attn_tc_grad(const AttnParams&, cudaStream_t) { return cudaErrorNotSupported; }
 
 }  // namespace dph

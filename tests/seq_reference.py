@@ -49,7 +49,8 @@ def visible(T, S, lq, lk, causal, window):
     return see
 
 
-U = 2.0 ** -24   # unit roundoff of fp32
+U = 2.0 ** -24     # unit roundoff of fp32
+ETA = 2.0 ** -126  # what is below it may be flushed to 0 (also by bf16, whose range is fp32's)
 
 
 def attention(q, k, v, causal=False, window=0, scale=None, q_lens=None, k_lens=None, do=None, r=0.0):
@@ -65,6 +66,7 @@ def attention(q, k, v, causal=False, window=0, scale=None, q_lens=None, k_lens=N
       delta          sum |do| (error of o) + (D + 4) U sum |do||o|      (o as it was stored)
       dS             P (|dP - delta| (E + 4 U) + (D + 4) U sum |do||v| + error of delta) + r |dS|
       dq, dk, dv     the same sums over the errors of dS and P, + n U and r of the result.
+    Every probability, gradient of one and result may also lose ETA to underflow.
     Where a query sees one key its P is 1 and its dS cancels to 0: no bound relative to the
     result could hold there."""
     B, T, Hq, D = q.shape
@@ -96,7 +98,7 @@ def attention(q, k, v, causal=False, window=0, scale=None, q_lens=None, k_lens=N
             y = torch.logsumexp(s, 1)
             p = torch.exp(s - y[:, None])
             O = p @ V
-            eO = (p @ V.abs()) * (E + r + n * U) + (r + U) * O.abs()
+            eO = (p @ V.abs()) * (E + r + n * U) + (r + U) * O.abs() + ETA * (see.double() @ V.abs() + 1)
             val["o"][b, rows, h], err["o"][b, rows, h] = O, eO
             val["lse"][b, h, rows], err["lse"][b, h, rows] = y, E[:, 0] + 4 * U * y.abs()
             if do is None:
@@ -106,15 +108,16 @@ def attention(q, k, v, causal=False, window=0, scale=None, q_lens=None, k_lens=N
             edel = (G.abs() * eO).sum(1, keepdim=True) + c * (G.abs() * O.abs()).sum(1, keepdim=True)
             dS = p * x
             eS = p * (x.abs() * (E + 4 * U) + c * (G.abs() @ V.abs().T) + edel) + r * dS.abs()
-            eP = p * (E + r + nt * U)
+            eS = eS + ETA * (x.abs() + 1) * see
+            eP = p * (E + r + nt * U) + ETA * see
             val["dq"][b, rows, h] = dS @ K * scale
-            err["dq"][b, rows, h] = (eS + n * U * dS.abs()) @ K.abs() * scale + (r + 2 * U) * (dS @ K * scale).abs()
+            err["dq"][b, rows, h] = (eS + n * U * dS.abs()) @ K.abs() * scale + (r + 2 * U) * (dS @ K * scale).abs() + ETA
             val["dk"][b, keys, g] += dS.T @ Q * scale
             err["dk"][b, keys, g] += (eS + nt * U * dS.abs()).T @ Q.abs() * scale
             val["dv"][b, keys, g] += p.T @ G
             err["dv"][b, keys, g] += eP.T @ G.abs()
     for m in ("dk", "dv"):
-        err[m] += (r + 2 * U) * val[m].abs()
+        err[m] += (r + 2 * U) * val[m].abs() + ETA
     return tuple((val[m], err[m]) for m in (("o", "lse") if do is None else ("o", "lse", "dq", "dk", "dv")))
 
 
