@@ -93,7 +93,7 @@ dp_status dp_rotary(const dp_rotary_desc* d, const void* Q, const void* K, const
   if (!strides_ok(d->q) || !writable(d->q_out, d->B, d->T, d->Hq, d->D) ||
       (d->Hk && (!strides_ok(d->k) || !writable(d->k_out, d->B, d->T, d->Hk, d->D))))
     return bad(DP_ERR_INVALID_ARG, "strides must be >= 0, and rows of Q_out and K_out must not overlap");
-  if (d->Hq > kMaxLen || d->Hk > kMaxLen || (double)d->B * d->T * ((double)d->Hq + d->Hk) * d->D / 256.0 > kMaxBlocks)
+  if (d->Hq > kMaxLen || d->Hk > kMaxLen || (double)d->B * d->T > kMaxBlocks || ((double)d->Hq + d->Hk) * d->D > 1 << 24)
     return bad(DP_ERR_UNSUPPORTED, "too many elements for one launch");
   dpk::RotaryParams P = {};
   P.Q = Q; P.K = K; P.Qo = Q_out; P.Ko = K_out;
