@@ -37,85 +37,88 @@ __global__ void __launch_bounds__(256) rotary_table_kernel(dp_rotary_table_desc 
 }
 
 // A unit is VEC pairs (half layout: two chunks of VEC entries), VEC/2 pairs (interleaved: one
-// chunk) or VEC copied entries of one token, for HG heads: the angles are loaded once for HG
-// heads' independent loads of 16 bytes.
-// Consecutive threads take consecutive chunks, then consecutive heads, so a warp's accesses
-// fill whole sectors.
+// chunk) or VEC copied entries of one token, for HG heads of Q or of K: the angles are loaded
+// once for HG heads' independent loads of 16 bytes.  Consecutive threads take consecutive
+// chunks, then consecutive heads, so a warp's accesses fill whole sectors.
 template <class E, int VEC, int HG, bool kInter>
-__global__ void __launch_bounds__(256) rotary_kernel(RotaryParams P, int units, int groups, int per_block) {
+__global__ void __launch_bounds__(256, 4) rotary_kernel(RotaryParams P, int items, int gq, int gk, int per_block) {
   pdl_trigger();
   pdl_wait();
-  using V = Vec<E, VEC>;
+  using V = Pack<E, VEC>;
   constexpr int NC = kInter ? (VEC > 1 ? VEC / 2 : 1) : VEC;   // pairs of a unit
-  const int half = P.R / 2, rot = kInter ? (VEC > 1 ? P.R / VEC : half) : half / VEC, H = P.Hq + P.Hk;
-  const int u = blockIdx.y * 256 + threadIdx.x % (units < 256 ? units : 256);
-  const long long tok = (long long)blockIdx.x * per_block + (units < 256 ? threadIdx.x / units : 0);
-  if (u >= units || (units < 256 && (int)threadIdx.x >= units * per_block) || tok >= (long long)P.B * P.T) return;
-  const int items = units / groups, it = u % items, g0 = u / items;
-  const int b = (int)(tok / P.T), t = (int)(tok - (long long)b * P.T);
-  // this token's part of each tensor
-  const E* q = static_cast<const E*>(P.Q) + b * P.q.b + t * P.q.t;
-  const E* k = static_cast<const E*>(P.K) + b * P.k.b + t * P.k.t;
-  E* qo = static_cast<E*>(P.Qo) + b * P.qo.b + t * P.qo.t;
-  E* ko = static_cast<E*>(P.Ko) + b * P.ko.b + t * P.ko.t;
-  auto src = [&](int h) { return h < P.Hq ? q + h * P.q.h : k + (h - P.Hq) * P.k.h; };
-  auto dst = [&](int h) { return h < P.Hq ? qo + h * P.qo.h : ko + (h - P.Hq) * P.ko.h; };
-  if (it >= rot) {   // past the rotated part
-    const int c = P.R + (it - rot) * VEC;
-    V x[HG];
-#pragma unroll
-    for (int i = 0; i < HG; ++i)
-      if (g0 + i * groups < H) x[i] = *reinterpret_cast<const V*>(src(g0 + i * groups) + c);
-#pragma unroll
-    for (int i = 0; i < HG; ++i)
-      if (g0 + i * groups < H) *reinterpret_cast<V*>(dst(g0 + i * groups) + c) = x[i];
-    return;
+  constexpr bool kTwo = !kInter || VEC == 1;                   // a pair's entries in two chunks
+  const int units = items * (gq + gk), half = P.R / 2, rot = half / NC;
+  int u = blockIdx.y * 256 + threadIdx.x, sub = 0;
+  if (units < 256) {
+    sub = threadIdx.x / units;
+    u = threadIdx.x - sub * units;
+    if (sub >= per_block) return;
   }
-  constexpr bool kTwo = !kInter || VEC == 1;   // the pair's entries in two chunks
-  const int j = it * NC;                       // first pair
-  const int ca = kInter ? 2 * j : j, cb = kInter ? 2 * j + 1 : j + half;
-  const long long pos = P.positions ? ld_index(P.positions, P.pos_i64, tok) : t;
-  Vec<float, NC> c, s;
+  const long long tok = (long long)blockIdx.x * per_block + sub;
+  if (u >= units || tok >= (long long)P.B * P.T) return;
+  const int grp = u / items, it = u - grp * items;
+  const int b = (int)((unsigned)tok / (unsigned)P.T), t = (int)(tok - (long long)b * P.T);
+  const bool isq = grp < gq;
+  const int g0 = isq ? grp : grp - gq, groups = isq ? gq : gk, heads = isq ? P.Hq : P.Hk;   // heads g0 + i groups
+  const dp_strides &si = isq ? P.q : P.k, &so = isq ? P.qo : P.ko;
+  // first chunk of the unit: entry j of a head; the second one (kTwo) `off` entries further
+  const int ca = it < rot ? (kInter ? 2 * it * NC : it * NC) : P.R + (it - rot) * VEC;
+  const int off = kInter ? 1 : half;
+  const E* x = static_cast<const E*>(isq ? P.Q : P.K) + b * si.b + t * si.t + g0 * si.h + ca;
+  E* y = static_cast<E*>(isq ? P.Qo : P.Ko) + b * so.b + t * so.t + g0 * so.h + ca;
+  const long long sx = groups * si.h, sy = groups * so.h;
+  const bool turned = it < rot;
+  const long long pos = !turned ? 0 : P.positions ? ld_index(P.positions, P.pos_i64, tok) : t;
   V xa[HG], xb[HG];
 #pragma unroll
   for (int i = 0; i < HG; ++i)
-    if (g0 + i * groups < H) {
-      xa[i] = *reinterpret_cast<const V*>(src(g0 + i * groups) + ca);
-      if (kTwo) xb[i] = *reinterpret_cast<const V*>(src(g0 + i * groups) + cb);
+    if (g0 + i * groups < heads) {
+      xa[i] = *reinterpret_cast<const V*>(x + i * sx);
+      if (kTwo && turned) xb[i] = *reinterpret_cast<const V*>(x + i * sx + off);
     }
+  if (!turned) {   // past the rotated part
+#pragma unroll
+    for (int i = 0; i < HG; ++i)
+      if (g0 + i * groups < heads) *reinterpret_cast<V*>(y + i * sy) = xa[i];
+    return;
+  }
+  Pack<float, NC> c, s;
   if (pos < 0 || pos >= P.P) {
     if (it == 0) atomicOr(P.status, kStatusIndex);
 #pragma unroll
-    for (int n = 0; n < NC; ++n) c.e[n] = s.e[n] = __int_as_float(0x7fc00000);
+    for (int n = 0; n < NC; ++n) c.w[n] = s.w[n] = __int_as_float(0x7fc00000);
   } else {
-    c = *reinterpret_cast<const Vec<float, NC>*>(P.table + (size_t)pos * P.R + j);
-    s = *reinterpret_cast<const Vec<float, NC>*>(P.table + (size_t)pos * P.R + half + j);
+    c = *reinterpret_cast<const Pack<float, NC>*>(P.table + (size_t)pos * P.R + it * NC);
+    s = *reinterpret_cast<const Pack<float, NC>*>(P.table + (size_t)pos * P.R + half + it * NC);
   }
   if (P.inverse) {
 #pragma unroll
-    for (int n = 0; n < NC; ++n) s.e[n] = -s.e[n];
+    for (int n = 0; n < NC; ++n) s.w[n] = -s.w[n];
   }
 #pragma unroll
   for (int i = 0; i < HG; ++i)
-    if (g0 + i * groups < H) {
-      V ya, yb;
+    if (g0 + i * groups < heads) {
+      float ya[VEC], yb[VEC];
+      V o;
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        const float p = kTwo ? xa[i].get(n % VEC) : xa[i].get(2 * n % VEC);
+        const float r = kTwo ? xb[i].get(n % VEC) : xa[i].get((2 * n + 1) % VEC);
+        // written out, so that every variant rounds alike
+        const float yp = fmaf(p, c.w[n], -__fmul_rn(r, s.w[n])), yr = fmaf(r, c.w[n], __fmul_rn(p, s.w[n]));
+        if (kTwo) {
+          ya[n % VEC] = yp;
+          yb[n % VEC] = yr;
+        } else {
+          ya[2 * n % VEC] = yp;
+          ya[(2 * n + 1) % VEC] = yr;
+        }
+      }
+      o.set(ya);
+      *reinterpret_cast<V*>(y + i * sy) = o;
       if (kTwo) {
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-          const float a = to_f(xa[i].e[n]), d = to_f(xb[i].e[n]);
-          ya.e[n] = from_f(a * c.e[n] - d * s.e[n], E());
-          yb.e[n] = from_f(d * c.e[n] + a * s.e[n], E());
-        }
-        *reinterpret_cast<V*>(dst(g0 + i * groups) + ca) = ya;
-        *reinterpret_cast<V*>(dst(g0 + i * groups) + cb) = yb;
-      } else {
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-          const float a = to_f(xa[i].e[2 * n % VEC]), d = to_f(xa[i].e[(2 * n + 1) % VEC]);
-          ya.e[2 * n % VEC] = from_f(a * c.e[n] - d * s.e[n], E());
-          ya.e[(2 * n + 1) % VEC] = from_f(d * c.e[n] + a * s.e[n], E());
-        }
-        *reinterpret_cast<V*>(dst(g0 + i * groups) + ca) = ya;
+        o.set(yb);
+        *reinterpret_cast<V*>(y + i * sy + off) = o;
       }
     }
 }
@@ -133,23 +136,22 @@ cudaError_t launch_rotary_table(const dp_rotary_table_desc& d, float* table, cud
 
 template <class E, int VEC, int HG>
 static cudaError_t run_rotary(const RotaryParams& P, cudaStream_t s) {
-  const int half = P.R / 2, H = P.Hq + P.Hk;
-  const int rot = P.interleaved ? (VEC > 1 ? P.R / VEC : half) : half / VEC, items = rot + (P.D - P.R) / VEC;
-  const int groups = (H + HG - 1) / HG;
-  const long long units = (long long)items * groups, tokens = (long long)P.B * P.T;
+  const int half = P.R / 2, items = half / (P.interleaved && VEC > 1 ? VEC / 2 : VEC) + (P.D - P.R) / VEC;
+  const int gq = (P.Hq + HG - 1) / HG, gk = (P.Hk + HG - 1) / HG;
+  const long long units = (long long)items * (gq + gk), tokens = (long long)P.B * P.T;
   if (units > (1 << 24)) return cudaErrorInvalidConfiguration;
   const int per_block = units < 256 ? 256 / (int)units : 1;
   const dim3 grid((unsigned)((tokens + per_block - 1) / per_block), (unsigned)((units + 255) / 256));
-  if (P.interleaved) return launch_pdl(rotary_kernel<E, VEC, HG, true>, grid, 256, 0, s, P, (int)units, groups, per_block);
-  return launch_pdl(rotary_kernel<E, VEC, HG, false>, grid, 256, 0, s, P, (int)units, groups, per_block);
+  if (P.interleaved) return launch_pdl(rotary_kernel<E, VEC, HG, true>, grid, 256, 0, s, P, items, gq, gk, per_block);
+  return launch_pdl(rotary_kernel<E, VEC, HG, false>, grid, 256, 0, s, P, items, gq, gk, per_block);
 }
 
 template <class E, int VEC>
 static cudaError_t run_rotary_heads(const RotaryParams& P, cudaStream_t s) {
-  // four heads a thread once that still leaves every SM its 2048 threads; a smaller call is
-  // latency, and wants its chain of loads short
-  const double threads = (double)P.B * P.T * (P.Hq + P.Hk) * (P.D / VEC);
-  return threads >= 4.0 * 152 * 2048 ? run_rotary<E, VEC, 4>(P, s) : run_rotary<E, VEC, 1>(P, s);
+  // four heads a thread once that still leaves every SM its threads four times; a smaller call
+  // is latency, and wants one head a thread
+  const double threads = (double)P.B * P.T * (P.Hq + P.Hk) * (P.D / VEC) / 4;
+  return threads >= 4.0 * 152 * 1024 ? run_rotary<E, VEC, 4>(P, s) : run_rotary<E, VEC, 1>(P, s);
 }
 
 // The widest vector (up to 16 bytes) that fits every address, the two parts of a head and

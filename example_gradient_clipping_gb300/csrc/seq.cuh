@@ -5,8 +5,34 @@
 
 namespace dpk {
 
-// Four or eight consecutive values of E as floats, through one aligned access.
-template <class E, int N> struct alignas(sizeof(E) * N) Vec { E e[N]; };
+// N consecutive values of E as one aligned access, kept packed in registers.
+template <class E, int N> struct Pack;
+template <int N> struct alignas(4 * N) Pack<float, N> {
+  float w[N];
+  __device__ __forceinline__ float get(int n) const { return w[n]; }
+  __device__ __forceinline__ void set(const float (&v)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) w[n] = v[n];
+  }
+};
+template <int N> struct alignas(2 * N) Pack<__nv_bfloat16, N> {
+  uint32_t w[N / 2];
+  __device__ __forceinline__ float get(int n) const {
+    return __uint_as_float(n & 1 ? w[n / 2] & 0xffff0000u : w[n / 2] << 16);
+  }
+  __device__ __forceinline__ void set(const float (&v)[N]) {
+#pragma unroll
+    for (int n = 0; n < N / 2; ++n) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * n], v[2 * n + 1]);
+      w[n] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+};
+template <> struct Pack<__nv_bfloat16, 1> {
+  __nv_bfloat16 w;
+  __device__ __forceinline__ float get(int) const { return __bfloat162float(w); }
+  __device__ __forceinline__ void set(const float (&v)[1]) { w = __float2bfloat16_rn(v[0]); }
+};
 
 __device__ __forceinline__ float from_f(float v, float) { return v; }
 __device__ __forceinline__ __nv_bfloat16 from_f(float v, __nv_bfloat16) { return __float2bfloat16_rn(v); }

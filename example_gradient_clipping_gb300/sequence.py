@@ -18,7 +18,7 @@ does not fit raises ValueError (or DPError, from the C side) before anything is 
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from typing import Optional
 
 import torch
 
@@ -112,70 +112,75 @@ def dp_distill(desc: DistillDesc, logits, indices, teacher, labels=None, weights
 
 # ---- argument checks ------------------------------------------------------------------
 _DTYPES = {torch.bfloat16: DP_BF16, torch.float32: DP_FP32}
-
-
-def _need(ok: bool, msg: str) -> None:
-    if not ok:
-        raise ValueError(msg)
+_INTS = (torch.int32, torch.int64)
 
 
 def _heads(x, name: str) -> None:
-    _need(x.dim() == 4 and x.is_cuda, f"{name}: a CUDA tensor [B, T, H, D], got {tuple(x.shape)} on {x.device}")
-    _need(x.dtype in _DTYPES, f"{name}: bf16 or fp32, got {x.dtype}")
-    _need(x.stride(3) == 1 or x.shape[3] == 1, f"{name}: the innermost stride must be 1, got {x.stride()}")
+    if x.dim() != 4 or not x.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor [B, T, H, D], got {tuple(x.shape)} on {x.device}")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"{name}: bf16 or fp32, got {x.dtype}")
+    if x.stride(3) != 1 and x.shape[3] > 1:
+        raise ValueError(f"{name}: the innermost stride must be 1, got {x.stride()}")
 
 
 def _like(x, ref, name: str) -> None:
-    _need(x.dtype == ref.dtype and x.device == ref.device, f"{name}: {x.dtype} on {x.device}, expected {ref.dtype} on "
-                                                           f"{ref.device}")
+    if x.dtype != ref.dtype or x.device != ref.device:
+        raise ValueError(f"{name}: {x.dtype} on {x.device}, expected {ref.dtype} on {ref.device}")
 
 
 def _vector(x, ref, shape, dtypes, name: str) -> None:
     """A contiguous device array of `shape`, or None."""
-    if x is None:
-        return
-    _need(tuple(x.shape) == tuple(shape) and x.device == ref.device and x.is_contiguous() and x.dtype in dtypes,
-          f"{name}: a contiguous {' or '.join(str(d) for d in dtypes)} tensor {list(shape)} on {ref.device}, got "
-          f"{x.dtype} {list(x.shape)} on {x.device}")
+    if x is not None and (tuple(x.shape) != tuple(shape) or x.device != ref.device or not x.is_contiguous() or
+                          x.dtype not in dtypes):
+        raise ValueError(f"{name}: a contiguous {' or '.join(str(d) for d in dtypes)} tensor {list(shape)} on "
+                         f"{ref.device}, got {x.dtype} {list(x.shape)} on {x.device}")
 
 
-def _strides(x) -> Tuple[int, int, int]:
-    return x.stride()[:3]
+def _sig(x):
+    """What the checks and the descriptor look at of a tensor (never its address or values)."""
+    return None if x is None else (x.shape, x.stride(), x.dtype, x.get_device())
 
 
-_INTS = (torch.int32, torch.int64)
-
-
-class _on:
-    """The tensors' device made current for the call (the C side uses the current device)."""
-
-    def __init__(self, x):
-        self.idx = x.device.index
-        self.prev = -1
-
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if cur != self.idx:
-            self.prev = cur
-            torch.cuda.set_device(self.idx)
-
-    def __exit__(self, *_):
-        if self.prev >= 0:
-            torch.cuda.set_device(self.prev)
-
-
-# Descriptors are plain values of shapes, strides and options: kept, so that a repeated call
-# does not build its structure again.
+# Descriptors by the signatures of a call's tensors and its options: a call like one that was
+# checked before is neither checked nor described again.
 _descs: dict = {}
 
 
 def _desc(key, make):
     d = _descs.get(key)
     if d is None:
-        if len(_descs) >= 512:
+        if len(_descs) >= 1024:
             _descs.clear()
         d = _descs[key] = make()
     return d
+
+
+def _raw_stream(x, stream):
+    """Raw handle of `stream`, or of the current stream of x's device."""
+    return torch._C._cuda_getCurrentRawStream(x.get_device()) if stream is None else _stream(stream)
+
+
+class _on:
+    """The tensors' device made current for the call (the C side uses the current device)."""
+
+    def __init__(self, x):
+        self.idx, self.prev = x.get_device(), torch.cuda.current_device()
+
+    def __enter__(self):
+        torch.cuda.set_device(self.idx)
+
+    def __exit__(self, *_):
+        torch.cuda.set_device(self.prev)
+
+
+def _call(f, x, *args):
+    """f(*args) of the C side with x's device current."""
+    if x.get_device() == torch._C._cuda_getDevice():
+        _check(f(*args))
+    else:
+        with _on(x):
+            _check(f(*args))
 
 
 # ---- rotary ---------------------------------------------------------------------------
@@ -184,38 +189,43 @@ def rotary_table(R: int, P: int, theta: float = 10000.0, scaling: str = "plain",
     """Table fp32 [P, R] of the cosines and sines of R rotated entries at positions 0 .. P - 1.
     scaling: "plain", "linear" (positions / factor), "base" (theta stretched by factor) or
     "parts" (slow pairs interpolated, fast ones kept, by their turns over `context`)."""
-    _need(scaling in _SCALINGS, f"scaling {scaling!r}: one of {sorted(_SCALINGS)}")
-    _need(P > 0 and R > 0, f"P={P} and R={R} must be > 0")
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling {scaling!r}: one of {sorted(_SCALINGS)}")
+    if P <= 0 or R <= 0:
+        raise ValueError(f"P={P} and R={R} must be > 0")
     table = torch.empty(P, R, dtype=torch.float32, device=device)
-    with _on(table):
-        dp_rotary_table(RotaryTableDesc(P, R, _SCALINGS[scaling], theta, factor, context, slow, fast), table, stream)
+    _call(_lib.dp_rotary_table, table, RotaryTableDesc(P, R, _SCALINGS[scaling], theta, factor, context, slow, fast),
+          table.data_ptr(), _raw_stream(table, stream))
     return table
 
 
-def _rotary(q, k, table, positions, interleaved, inverse, stream):
+def _rotary_desc(q, k, table, positions, interleaved, inverse):
     _heads(q, "q")
     B, T, Hq, D = q.shape
     if k is not None:
         _heads(k, "k")
         _like(k, q, "k")
-        _need(k.shape[0] == B and k.shape[1] == T and k.shape[3] == D, f"k {tuple(k.shape)} does not fit q {tuple(q.shape)}")
-    _need(table.dim() == 2 and table.dtype == torch.float32 and table.is_contiguous() and table.device == q.device,
-          "table: the contiguous fp32 [P, R] tensor of rotary_table, on q's device")
+        if k.shape[0] != B or k.shape[1] != T or k.shape[3] != D:
+            raise ValueError(f"k {tuple(k.shape)} does not fit q {tuple(q.shape)}")
+    if table.dim() != 2 or table.dtype != torch.float32 or not table.is_contiguous() or table.device != q.device:
+        raise ValueError("table: the contiguous fp32 [P, R] tensor of rotary_table, on q's device")
     _vector(positions, q, (B, T), _INTS, "positions")
+    Hk = k.shape[2] if k is not None else 0
+    return RotaryDesc(_DTYPES[q.dtype], B, T, Hq, Hk, D, table.shape[1], table.shape[0], int(bool(interleaved)),
+                      int(bool(inverse)), int(positions is not None and positions.dtype == torch.int64),
+                      Strides(*q.stride()[:3]), Strides(*(k.stride()[:3] if k is not None else (0, 0, 0))),
+                      Strides(T * Hq * D, Hq * D, D), Strides(T * Hk * D, Hk * D, D))
+
+
+def _rotary(q, k, table, positions, interleaved, inverse, stream):
+    d = _desc((_sig(q), _sig(k), _sig(table), _sig(positions), interleaved, inverse),
+              lambda: _rotary_desc(q, k, table, positions, interleaved, inverse))
     qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     ko = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k is not None else None
-    if q.numel() == 0 and (k is None or k.numel() == 0):
+    if qo.numel() == 0 and (ko is None or ko.numel() == 0):
         return qo, ko
-    Hk = k.shape[2] if k is not None else 0
-    p64 = positions is not None and positions.dtype == torch.int64
-    sq, sk = q.stride(), k.stride() if k is not None else (0, 0, 0, 1)
-    key = (RotaryDesc, q.dtype, B, T, Hq, Hk, D, table.shape, interleaved, inverse, p64, sq, sk)
-    d = _desc(key, lambda: RotaryDesc(_DTYPES[q.dtype], B, T, Hq, Hk, D, table.shape[1], table.shape[0],
-                                      int(bool(interleaved)), int(bool(inverse)), int(p64), Strides(*sq[:3]),
-                                      Strides(*sk[:3]), Strides(*_strides(qo)),
-                                      Strides(*(_strides(ko) if ko is not None else (0, 0, 0)))))
-    with _on(q):
-        dp_rotary(d, q, k, table, positions, qo, ko, stream)
+    _call(_lib.dp_rotary, q, d, q.data_ptr(), _ptr(k), table.data_ptr(), _ptr(positions), qo.data_ptr(), _ptr(ko),
+          _raw_stream(q, stream))
     return qo, ko
 
 
@@ -245,35 +255,39 @@ def rotary(q, k, table, positions=None, interleaved: bool = False, inverse: bool
     angles; k may be None.  positions: int32 or int64 [B, T], None for 0 .. T - 1.  inverse
     turns back (and is the gradient)."""
     if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
-        _need(stream is None, "a differentiable call runs on the current stream")
+        if stream is not None:
+            raise ValueError("a differentiable call runs on the current stream")
         return _Rotary.apply(q, k, table, positions, interleaved, inverse)
     return _rotary(q, k, table, positions, interleaved, inverse, stream)
 
 
 # ---- attention ------------------------------------------------------------------------
-def _attn_check(q, k, v, q_lens, k_lens):
+def _attn_desc(q, k, v, q_lens, k_lens, causal, window, scale, more=None):
+    """Descriptor of a forward call, or with more = (o, lse, do) of a gradient call."""
     for x, n in ((q, "q"), (k, "k"), (v, "v")):
         _heads(x, n)
     _like(k, q, "k")
     _like(v, q, "v")
     B, T, Hq, D = q.shape
-    _need(k.shape == v.shape and k.shape[0] == B and k.shape[3] == D, f"k {tuple(k.shape)} and v {tuple(v.shape)} do not "
-                                                                      f"fit q {tuple(q.shape)}")
+    S, Hk = k.shape[1], k.shape[2]
+    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != D:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not fit q {tuple(q.shape)}")
     _vector(q_lens, q, (B,), (torch.int32,), "q_lens")
     _vector(k_lens, q, (B,), (torch.int32,), "k_lens")
-
-
-def _attn_desc(q, k, causal, window, scale, strides):
-    key = (AttnDesc, q.dtype, q.shape, k.shape, causal, window, scale, strides)
-
-    def make():
-        B, T, Hq, D = q.shape
-        d = AttnDesc(_DTYPES[q.dtype], B, T, k.shape[1], Hq, k.shape[2], D, int(bool(causal)), int(window),
-                     float(scale or 0.0))
-        for name, st in zip(("q", "k", "v", "o", "d_o", "dq", "dk", "dv"), strides):
-            setattr(d, name, Strides(*st[:3]))
-        return d
-    return _desc(key, make)
+    d = AttnDesc(_DTYPES[q.dtype], B, T, S, Hq, Hk, D, int(bool(causal)), int(window), float(scale or 0.0))
+    own, kv = Strides(T * Hq * D, Hq * D, D), Strides(S * Hk * D, Hk * D, D)   # of the results
+    d.q, d.k, d.v, d.o = Strides(*q.stride()[:3]), Strides(*k.stride()[:3]), Strides(*v.stride()[:3]), own
+    if more is not None:
+        o, lse, do = more
+        for x, n in ((o, "o"), (do, "do")):
+            _heads(x, n)
+            _like(x, q, n)
+            if x.shape != q.shape:
+                raise ValueError(f"{n} {tuple(x.shape)} is not shaped like q {tuple(q.shape)}")
+        _vector(lse, q, (B, Hq, T), (torch.float32,), "lse")
+        d.o, d.d_o, d.dq, d.dk, d.dv = Strides(*o.stride()[:3]), Strides(*do.stride()[:3]), own, kv, kv
+        d.ws_bytes = dp_attention_grad_workspace(d)
+    return d
 
 
 def attention_forward(q, k, v, causal: bool = False, window: int = 0, scale: Optional[float] = None, q_lens=None,
@@ -282,15 +296,15 @@ def attention_forward(q, k, v, causal: bool = False, window: int = 0, scale: Opt
     fp32 [B, Hq, T].  q_lens, k_lens: int32 [B], how many leading rows of each example are
     there; causal aligns the last query with the last key; window > 0 keeps the latest
     `window` keys.  scale defaults to 1/sqrt(D).  A query that sees no key gives 0 and -inf."""
-    _attn_check(q, k, v, q_lens, k_lens)
-    B, T, Hq, D = q.shape
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(B, Hq, T, dtype=torch.float32, device=q.device)
-    if q.numel() == 0 or k.numel() == 0:
+    d = _desc((_sig(q), _sig(k), _sig(v), _sig(q_lens), _sig(k_lens), causal, window, scale),
+              lambda: _attn_desc(q, k, v, q_lens, k_lens, causal, window, scale))
+    dev = q.device
+    o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    lse = torch.empty((d.B, d.Hq, d.T), dtype=torch.float32, device=dev)
+    if o.numel() == 0 or k.numel() == 0:
         return o.zero_(), lse.fill_(-float("inf"))
-    d = _attn_desc(q, k, causal, window, scale, (q.stride(), k.stride(), v.stride(), o.stride()))
-    with _on(q):
-        dp_attention(d, q, k, v, o, lse, q_lens, k_lens, stream)
+    _call(_lib.dp_attention, q, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(q_lens), _ptr(k_lens), o.data_ptr(),
+          lse.data_ptr(), _raw_stream(q, stream))
     return o, lse
 
 
@@ -298,22 +312,18 @@ def attention_backward(q, k, v, o, lse, do, causal: bool = False, window: int = 
                        q_lens=None, k_lens=None, stream=None):
     """(dq, dk, dv) for the gradient `do` of attention_forward's o, the probabilities formed
     again from lse; the other arguments as in the forward call."""
-    _attn_check(q, k, v, q_lens, k_lens)
-    for x, n in ((o, "o"), (do, "do")):
-        _heads(x, n)
-        _like(x, q, n)
-        _need(x.shape == q.shape, f"{n} {tuple(x.shape)} is not shaped like q {tuple(q.shape)}")
-    _vector(lse, q, (q.shape[0], q.shape[2], q.shape[1]), (torch.float32,), "lse")
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    dv = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    if q.numel() == 0 or k.numel() == 0:
+    d = _desc((_sig(q), _sig(k), _sig(v), _sig(q_lens), _sig(k_lens), causal, window, scale, _sig(o), _sig(lse), _sig(do)),
+              lambda: _attn_desc(q, k, v, q_lens, k_lens, causal, window, scale, (o, lse, do)))
+    dev = q.device
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    dv = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    if dq.numel() == 0 or dk.numel() == 0:
         return dq.zero_(), dk.zero_(), dv.zero_()
-    d = _attn_desc(q, k, causal, window, scale, (q.stride(), k.stride(), v.stride(), o.stride(), do.stride(),
-                                                 dq.stride(), dk.stride(), dv.stride()))
-    ws = torch.empty(dp_attention_grad_workspace(d), dtype=torch.uint8, device=q.device)
-    with _on(q):
-        dp_attention_grad(d, q, k, v, o, lse, do, dq, dk, dv, ws, q_lens, k_lens, stream=stream)
+    ws = torch.empty(d.ws_bytes, dtype=torch.uint8, device=dev)
+    _call(_lib.dp_attention_grad, q, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+          do.data_ptr(), _ptr(q_lens), _ptr(k_lens), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), d.ws_bytes,
+          _raw_stream(q, stream))
     return dq, dk, dv
 
 
@@ -339,34 +349,41 @@ def attention(q, k, v, causal: bool = False, window: int = 0, scale: Optional[fl
 
 
 # ---- distillation ---------------------------------------------------------------------
-def _distill(logits, indices, teacher, labels, weights, upstream, temperature, alpha, want_loss, want_grad, stream):
-    _need(logits.dim() == 3 and logits.is_cuda and logits.dtype in _DTYPES,
-          f"logits: a bf16 or fp32 CUDA tensor [B, T, V], got {logits.dtype} {tuple(logits.shape)} on {logits.device}")
+def _distill_desc(logits, indices, teacher, labels, weights, upstream, temperature, alpha):
+    if logits.dim() != 3 or not logits.is_cuda or logits.dtype not in _DTYPES or logits.shape[2] == 0:
+        raise ValueError(f"logits: a bf16 or fp32 CUDA tensor [B, T, V], got {logits.dtype} {tuple(logits.shape)} on "
+                         f"{logits.device}")
     B, T, V = logits.shape
     sb, sr, sv = logits.stride()
-    ld = sr if T > 1 else sb if B > 1 else V
-    _need((sv == 1 or V == 1) and (B <= 1 or T <= 1 or sb == T * sr), f"logits: rows at one stride and an innermost "
-                                                                      f"stride of 1, got strides {logits.stride()}")
-    _need(indices.dim() == 3 and teacher.dtype in _DTYPES, "indices and teacher: [B, T, K], teacher bf16 or fp32")
+    if (sv != 1 and V > 1) or (B > 1 and T > 1 and sb != T * sr):
+        raise ValueError(f"logits: rows at one stride and an innermost stride of 1, got strides {logits.stride()}")
+    if indices.dim() != 3 or teacher.dtype not in _DTYPES:
+        raise ValueError("indices and teacher: [B, T, K], teacher bf16 or fp32")
     K = indices.shape[2]
     _vector(indices, logits, (B, T, K), _INTS, "indices")
     _vector(teacher, logits, (B, T, K), tuple(_DTYPES), "teacher")
     _vector(labels, logits, (B, T), _INTS, "labels")
     _vector(weights, logits, (B, T), (torch.float32,), "weights")
     _vector(upstream, logits, (B,), (torch.float32,), "upstream")
+    return DistillDesc(_DTYPES[logits.dtype], _DTYPES[teacher.dtype], B, T, V, K, int(indices.dtype == torch.int64),
+                       int(labels is not None and labels.dtype == torch.int64), sr if T > 1 else sb if B > 1 else V, V,
+                       float(temperature), float(alpha))
+
+
+def _distill(logits, indices, teacher, labels, weights, upstream, temperature, alpha, want_loss, want_grad, stream):
+    d = _desc((_sig(logits), _sig(indices), _sig(teacher), _sig(labels), _sig(weights), _sig(upstream), temperature,
+               alpha), lambda: _distill_desc(logits, indices, teacher, labels, weights, upstream, temperature, alpha))
     dev = logits.device
-    loss = torch.empty(B, dtype=torch.float32, device=dev) if want_loss else None
-    rows = torch.empty(B, T, dtype=torch.float32, device=dev) if want_loss else None
-    grad = torch.empty(B, T, V, dtype=logits.dtype, device=dev) if want_grad else None
+    loss = rows = grad = None
+    if want_loss:
+        loss = torch.empty(d.B, dtype=torch.float32, device=dev)
+        rows = torch.empty((d.B, d.T), dtype=torch.float32, device=dev)
+    if want_grad:
+        grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
     if logits.numel() == 0:
-        _need(V > 0, "logits: the vocabulary is empty")
         return (loss.zero_() if want_loss else None), rows, grad
-    i64, l64 = indices.dtype == torch.int64, labels is not None and labels.dtype == torch.int64
-    key = (DistillDesc, logits.dtype, teacher.dtype, B, T, V, K, i64, l64, ld, temperature, alpha)
-    d = _desc(key, lambda: DistillDesc(_DTYPES[logits.dtype], _DTYPES[teacher.dtype], B, T, V, K, int(i64), int(l64), ld,
-                                       V, float(temperature), float(alpha)))
-    with _on(logits):
-        dp_distill(d, logits, indices, teacher, labels, weights, upstream, rows, loss, grad, stream)
+    _call(_lib.dp_distill, logits, d, logits.data_ptr(), indices.data_ptr(), teacher.data_ptr(), _ptr(labels),
+          _ptr(weights), _ptr(upstream), _ptr(rows), _ptr(loss), _ptr(grad), _raw_stream(logits, stream))
     return loss, rows, grad
 
 
@@ -393,7 +410,8 @@ def distill_loss(logits, indices, teacher, labels=None, weights=None, temperatur
     teacher [B, T, K] the teacher's top logits; labels [B, T] (negative: none); weights fp32
     [B, T].  loss carries the gradient with respect to the logits."""
     if torch.is_grad_enabled() and logits.requires_grad:
-        _need(stream is None, "a differentiable call runs on the current stream")
+        if stream is not None:
+            raise ValueError("a differentiable call runs on the current stream")
         return _Distill.apply(logits, indices, teacher, labels, weights, temperature, alpha)
     return _distill(logits, indices, teacher, labels, weights, None, temperature, alpha, True, False, stream)[:2]
 
