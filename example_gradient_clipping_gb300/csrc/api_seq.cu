@@ -156,6 +156,7 @@ dp_status dp_distill(const dp_distill_desc* d, const void* logits, const void* i
     if (t != DP_BF16 && t != DP_FP32) return bad(DP_ERR_INVALID_ARG, "dtype %d is not DP_BF16 or DP_FP32", t);
   if (d->B <= 0 || d->T <= 0 || d->V <= 0 || d->K < 0)
     return bad(DP_ERR_INVALID_ARG, "B=%d, T=%d and V=%d must be > 0, K=%d >= 0", d->B, d->T, d->V, d->K);
+  if (d->V > kMaxLen) return bad(DP_ERR_UNSUPPORTED, "V=%d is above 2^30", d->V);
   if (d->K > 1024) return bad(DP_ERR_UNSUPPORTED, "K=%d teacher entries are above 1024", d->K);
   if (d->ld < d->V || (dlogits && d->ld_grad < d->V))
     return bad(DP_ERR_INVALID_ARG, "ld=%lld and ld_grad=%lld must be >= V=%d", d->ld, d->ld_grad, d->V);

@@ -5,17 +5,18 @@
 // with lse_tau = log sum exp(z / tau), lse_1 = log sum exp z, and
 //   dz = g w [ (1 - alpha) tau (q - p) + alpha (softmax(z) - e_y) ].
 //
-// distill_cluster_kernel: a cluster of 1 to 8 CTAs per row, each with its slice of the row in
-// registers (up to eight or sixteen 16-byte vectors a thread, all loads in flight at once),
-// so the row is read once and its gradient written once.  Each CTA forms the maximum and the
-// sums of its slice; the slices' are exchanged through distributed shared memory after the
-// row's one cluster barrier.  Rows off the 16-byte grid (an odd V) are read as the aligned
-// vectors that cover them, the two that reach past the row entry by entry.
-// distill_row_kernel: any length, a block per row that reads it three times (rows longer than
-// a cluster's registers hold).  The softmax statistics are fp32: the maximum first, then the sums
-// relative to it.  The few entries that the teacher or the label touches are written after
-// the row, each by a thread that adds up every teacher entry of the same index, so a
-// repeated index needs no atomics and the result does not depend on any order.
+// Persistent CTAs, a row at a time: one pass with each thread's running maximum and sums, and
+// for the gradient a second pass over the row, which is still in L2 (the rows in work are
+// about a tenth of it), so HBM sees the row once and its gradient once.
+//   producer warp   the row's aligned vectors in 16 KB chunks through a ring (bulk copies)
+//   teacher warp    one row ahead: the teacher's distribution, the label, and the ends of rows
+//                   off the 16-byte grid (an odd V)
+//   consumers       256 threads, four 16-byte vectors of a chunk each
+// The few entries that the teacher or the label touches are written after the row, each by a
+// thread that adds up every teacher entry of the same index, so a repeated index needs no
+// atomics and the result does not depend on any order.
+// (A row spread over a cluster's registers, read once, waited 3-4 us a row for the exchange of
+// its sums and ran at half the speed.)
 #include <algorithm>
 
 #include "seq.cuh"
@@ -24,152 +25,20 @@
 namespace dpk {
 namespace distill {
 
-constexpr int kMaxK = 1024;
-
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
-// Sum (or maximum) of v over the block, in every thread; `red` holds 33 floats.
-template <bool kMax>
-__device__ __forceinline__ float block_reduce(float v, float* red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
+__device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = kMax ? fmaxf(v, u) : v + u;
-  }
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    v = lane < nw ? red[lane] : (kMax ? -INFINITY : 0.f);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float u = __shfl_xor_sync(0xffffffffu, v, o);
-      v = kMax ? fmaxf(v, u) : v + u;
-    }
-    if (lane == 0) red[32] = v;
-  }
-  __syncthreads();
-  const float r = red[32];
-  __syncthreads();
-  return r;
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
 
 __device__ __forceinline__ float ld_teacher(const DistillParams& P, size_t i) {
   return P.teacher_dtype == DP_BF16 ? to_f(static_cast<const __nv_bfloat16*>(P.teacher)[i])
                                     : static_cast<const float*>(P.teacher)[i];
-}
-
-// The teacher's distribution of a row into shared memory (index -1: no entry); returns the
-// number of valid entries and sets *bad if an index is past the vocabulary.
-__device__ __forceinline__ int load_teacher(const DistillParams& P, size_t row, int* sk, float* sp, float* red,
-                                            bool* bad) {
-  float m = -INFINITY, n = 0.f, oob = 0.f;
-  for (int j = threadIdx.x; j < P.K; j += blockDim.x) {
-    const long long k = ld_index(P.idx, P.index_i64, row * P.K + j);
-    const bool have = k >= 0 && k < P.V;
-    if (k >= P.V) oob = 1.f;
-    const float t = have ? ld_teacher(P, row * P.K + j) / P.tau : -INFINITY;
-    sk[j] = have ? (int)k : -1;
-    sp[j] = t;
-    if (have) n += 1.f;
-    m = fmaxf(m, t);
-  }
-  m = block_reduce<true>(m, red);
-  const float valid = block_reduce<false>(n, red);
-  *bad = block_reduce<true>(oob, red) > 0.f;
-  float s = 0.f;
-  for (int j = threadIdx.x; j < P.K; j += blockDim.x) {
-    const float e = sk[j] >= 0 ? expf(sp[j] - m) : 0.f;
-    sp[j] = e;
-    s += e;
-  }
-  s = block_reduce<false>(s, red);
-  const float inv = valid > 0.f ? 1.f / s : 0.f;
-  for (int j = threadIdx.x; j < P.K; j += blockDim.x) sp[j] *= inv;
-  __syncthreads();
-  return (int)valid;
-}
-
-template <class E>
-__global__ void __launch_bounds__(512) distill_row_kernel(DistillParams P) {
-  pdl_trigger();
-  pdl_wait();
-  __shared__ float red[33];
-  __shared__ int sk[kMaxK];
-  __shared__ float sp[kMaxK];
-  const size_t row = blockIdx.x;
-  const int b = (int)(row / P.T);
-  const E* z = static_cast<const E*>(P.logits) + row * (size_t)P.ld;
-  E* g = P.grad ? static_cast<E*>(P.grad) + row * (size_t)P.ldg : nullptr;
-  const float w = P.weights ? P.weights[row] : 1.f;
-  if (w == 0.f) {   // not read
-    if (g)
-      for (int v = threadIdx.x; v < P.V; v += blockDim.x) g[v] = from_f(0.f, E());
-    if (P.row_loss && threadIdx.x == 0) P.row_loss[row] = 0.f;
-    return;
-  }
-  bool bad;
-  const int valid = load_teacher(P, row, sk, sp, red, &bad);
-  long long y = P.labels ? ld_index(P.labels, P.label_i64, row) : -1;
-  if (y >= P.V) { bad = true; y = -1; }
-  if (bad && threadIdx.x == 0) atomicOr(P.status, kStatusIndex);
-  const float ct = valid ? 1.f - P.alpha : 0.f, cl = y >= 0 ? P.alpha : 0.f;   // the row's two terms
-  const float it = 1.f / P.tau;
-
-  float m = -INFINITY;
-  for (int v = threadIdx.x; v < P.V; v += blockDim.x) m = fmaxf(m, to_f(z[v]));
-  m = block_reduce<true>(m, red);
-  float st = 0.f, s1 = 0.f;
-  for (int v = threadIdx.x; v < P.V; v += blockDim.x) {
-    const float d = to_f(z[v]) - m;
-    st += expf(d * it);
-    s1 += expf(d);
-  }
-  st = block_reduce<false>(st, red);
-  s1 = block_reduce<false>(s1, red);
-  if (P.row_loss) {
-    float kl = 0.f;
-    for (int j = threadIdx.x; j < P.K; j += blockDim.x)
-      if (sp[j] > 0.f) kl += sp[j] * (logf(sp[j]) - (to_f(z[sk[j]]) - m) * it);
-    kl = block_reduce<false>(kl, red);
-    if (threadIdx.x == 0) {
-      float l = ct != 0.f ? ct * P.tau * P.tau * (kl + logf(st)) : 0.f;
-      if (cl != 0.f) l += cl * (logf(s1) - (to_f(z[y]) - m));
-      P.row_loss[row] = bad ? __int_as_float(0x7fc00000) : w * l;
-    }
-  }
-  if (!g) return;
-  const float gw = w * (P.upstream ? P.upstream[b] : 1.f);
-  const float at = ct * P.tau / st, a1 = cl / s1;
-  for (int v = threadIdx.x; v < P.V; v += blockDim.x) {
-    const float d = to_f(z[v]) - m;
-    g[v] = from_f(gw * (at * expf(d * it) + a1 * expf(d)), E());
-  }
-  __syncthreads();
-  for (int j = threadIdx.x; j <= P.K; j += blockDim.x) {   // K teacher entries and the label
-    const int v = j < P.K ? sk[j] : (int)y;
-    if (v < 0) continue;
-    float p = 0.f;
-    for (int u = 0; u < P.K; ++u)
-      if (sk[u] == v) p += sp[u];
-    const float d = to_f(z[v]) - m;
-    float x = at * expf(d * it) + a1 * expf(d) - ct * P.tau * p;
-    if (v == (int)y) x -= cl;
-    g[v] = from_f(gw * x, E());
-  }
-}
-
-constexpr int kMaxCluster = 8;
-
-// Sum (or maximum) over a warp.
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
 }
 
 // A 16-byte vector of a row as its four words: entry n of it as a float, and set from one.
@@ -211,208 +80,307 @@ template <class E> struct Words {
   }
 };
 
-struct alignas(16) SliceStats { float m, st, s1, pad; };   // read as one 16-byte vector
 
-template <class E, int NV>
-__global__ void __launch_bounds__(512, NV <= 8 ? 2 : 1) distill_cluster_kernel(DistillParams P, int cluster) {
-  pdl_trigger();
-  pdl_wait();
+constexpr int kNT = 256, kNW = kNT / 32, kThreads = kNT + 64;
+constexpr int kNV = 4, kChunk = kNT * kNV, kChunkBytes = kChunk * 16;   // vectors and bytes of a chunk
+constexpr int kStages = 4, kMaxK = 1024, kMinBlocks = 3;
+// behind the ring: reductions [2][8] of (max, sums), row ends [2][2], barriers, flags; teacher
+constexpr int kFixed = 2 * kNW * 16 + 2 * 2 * 16 + (2 * kStages + 4) * 8 + 32;
+constexpr int stream_smem(int K) { return kStages * kChunkBytes + kFixed + 2 * (12 * ((K + 3) / 4 * 4) + 16); }
+
+// The consumers' barrier, true in all of them if `p` is in any.
+__device__ __forceinline__ bool bar_any(bool p) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %1, 0;\n\t"
+      "barrier.cta.red.or.pred b, 1, %2, a;\n\t"
+      "selp.s32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"((int)p), "n"(kNT)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   ptx::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+               : "memory");
+}
+
+// kBoth: the label's softmax (temperature 1) beside the teacher's.
+template <class E, bool kBoth>
+__global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(DistillParams P) {
   using V = Words<E>;
   constexpr int W = V::W;
-  __shared__ float red[3][17];
-  __shared__ SliceStats mine;
-  __shared__ int sk[kMaxK];
-  __shared__ float sp[kMaxK], sz[kMaxK + 1];
-  __shared__ int s_valid, s_bad;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  const int rank = cluster > 1 ? (int)ptx::cluster_rank() : 0;
-  const size_t row = blockIdx.x / cluster;
-  const int b = (int)(row / P.T);
-  const E* z = static_cast<const E*>(P.logits) + row * (size_t)P.ld;
-  E* g = P.grad ? static_cast<E*>(P.grad) + row * (size_t)P.ldg : nullptr;
-  // vector v covers entries [W v - shift, W v - shift + W); this CTA's are [v0, v1)
-  const int shift = (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(E));
-  const bool gvec = (reinterpret_cast<uintptr_t>(g) & 15) == (reinterpret_cast<uintptr_t>(z) & 15);
-  const int nvec = (P.V + shift + W - 1) / W, per = (nvec + cluster - 1) / cluster;
-  const int v0 = min(nvec, rank * per), v1 = min(nvec, v0 + per);
-  const float w = P.weights ? P.weights[row] : 1.f;
-  auto whole = [&](int v) { return W * v - shift >= 0 && W * v - shift + W <= P.V; };
-  auto store = [&](int v, const V& x) {
-    const int e0 = W * v - shift;
-    if (gvec && whole(v)) *reinterpret_cast<uint4*>(g + e0) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
-    else x.store_edge(g, e0, P.V);
-  };
-  if (w == 0.f) {   // not read (the whole cluster agrees)
-    const V zero = {{0u, 0u, 0u, 0u}};
-    if (g)
-      for (int v = v0 + tid; v < v1; v += blockDim.x) store(v, zero);
-    if (P.row_loss && rank == 0 && tid == 0) P.row_loss[row] = 0.f;
-    return;
-  }
-  V x[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = v0 + tid + i * (int)blockDim.x, e0 = W * v - shift;
-    if (v < v1 && whole(v)) x[i].load(z + e0);
-    else x[i].fill();
-  }
-#pragma unroll 1
-  for (int side = 0; side < 2; ++side) {   // the row's first and last vector, where they reach past it
-    const int v = side ? nvec - 1 : 0;
-    if (v >= v0 && v < v1 && !whole(v) && (v - v0) % (int)blockDim.x == tid) {
-      V t;
-      t.load_edge(z, W * v - shift, P.V);
-      const int at = (v - v0) / (int)blockDim.x;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) x[i].w[n] = at == i ? t.w[n] : x[i].w[n];
+  extern __shared__ __align__(128) uint8_t smem[];
+  float4* red = reinterpret_cast<float4*>(smem + kStages * kChunkBytes);   // [2][warp] (max, sums)
+  V* edge = reinterpret_cast<V*>(red + 2 * kNW);                           // [2][first, last vector]
+  uint64_t* full = reinterpret_cast<uint64_t*>(edge + 4);
+  uint64_t *empty = full + kStages, *tfull = empty + kStages, *tempty = tfull + 2;
+  volatile int* abort = reinterpret_cast<volatile int*>(tempty + 2);
+  struct Meta { int valid, bad, y; float zy; };
+  const int kpad = (P.K + 3) / 4 * 4;
+  uint8_t* teacher = smem + kStages * kChunkBytes + kFixed;                // [2]{Meta, sk, sp, sz}
+  const int tbytes = 16 + 12 * kpad;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], kNW);
     }
-  }
-  // the teacher's distribution and the label, by the last warp, while the row arrives
-  long long y = P.labels ? ld_index(P.labels, P.label_i64, row) : -1;
-  if (warp == nw - 1) {
-    float tm = -INFINITY, sum = 0.f;
-    int n = 0, oob = y >= P.V;
-    for (int j = lane; j < P.K; j += 32) {
-      const long long k = ld_index(P.idx, P.index_i64, row * P.K + j);
-      const bool have = k >= 0 && k < P.V;
-      oob |= k >= P.V;
-      n += have;
-      const float t = have ? ld_teacher(P, row * P.K + j) / P.tau : -INFINITY;
-      sk[j] = have ? (int)k : -1;
-      sp[j] = t;
-      sz[j] = have ? to_f(z[k]) : 0.f;
-      tm = fmaxf(tm, t);
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(&tfull[s], 1);
+      ptx::mbar_init(&tempty[s], kNW);
     }
-    tm = warp_max(tm);
-    n = __reduce_add_sync(0xffffffffu, n);
-    oob = __any_sync(0xffffffffu, oob);
-    for (int j = lane; j < P.K; j += 32) {
-      const float e = sk[j] >= 0 ? expf(sp[j] - tm) : 0.f;
-      sp[j] = e;
-      sum += e;
-    }
-    sum = warp_sum(sum);
-    const float inv = n > 0 ? 1.f / sum : 0.f;
-    for (int j = lane; j < P.K; j += 32) sp[j] *= inv;
-    if (lane == 0) {
-      s_valid = n;
-      s_bad = oob;
-      if (y >= 0 && y < P.V) sz[P.K] = to_f(z[y]);
-    }
-  }
-  if (y >= P.V) y = -1;
-  // this slice's maximum, then its sums relative to it
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int n = 0; n < W; ++n) m = fmaxf(m, x[i].get(n));
-  m = warp_max(m);
-  if (lane == 0) red[0][warp] = m;
-  __syncthreads();
-  m = warp_max(lane < nw ? red[0][lane] : -INFINITY);
-  // the words stay packed between the passes (kept unpacked they would not fit the registers)
-  auto opaque = [&]() {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int n = 0; n < 4; ++n) asm volatile("" : "+r"(x[i].w[n]));
-  };
-  opaque();
-  const float kL2 = 1.44269504088896341f, ct2 = kL2 / P.tau;   // exp(d / tau) = exp2(d ct2)
-  const float base = m == -INFINITY ? 0.f : m;                 // a slice the student rules out
-  const bool both = P.alpha > 0.f && P.labels;                 // uniform: the label's softmax too
-  float st = 0.f, s1 = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int n = 0; n < W; ++n) {
-      const float d = x[i].get(n) - base;
-      st += exp2_approx(d * ct2);
-      if (both) s1 += exp2_approx(d * kL2);
-    }
-  opaque();
-  st = warp_sum(st);
-  s1 = warp_sum(s1);
-  if (lane == 0) {
-    red[1][warp] = st;
-    red[2][warp] = s1;
+    *abort = 0;
+    ptx::fence_mbar_init();
   }
   __syncthreads();
-  st = warp_sum(lane < nw ? red[1][lane] : 0.f);
-  s1 = warp_sum(lane < nw ? red[2][lane] : 0.f);
-  if (cluster > 1) {   // every CTA combines the slices in rank order
-    if (tid == 0) mine = {m, st, s1, 0.f};
-    ptx::cluster_sync();
-    const uint32_t at = ptx::smem_u32(&mine);
-    float4 o[kMaxCluster];
-    m = -INFINITY;
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)
-      if (r < cluster) {
-        o[r] = ptx::ld_cluster_v4(ptx::map_rank(at, r));
-        m = fmaxf(m, o[r].x);
-      }
-    st = s1 = 0.f;
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)
-      if (r < cluster && o[r].x > -INFINITY) {
-        st += o[r].y * exp2_approx((o[r].x - m) * ct2);
-        s1 += o[r].z * exp2_approx((o[r].x - m) * kL2);
-      }
-  }
-  const int valid = s_valid, bad = s_bad;
-  const float ct = valid ? 1.f - P.alpha : 0.f, cl = y >= 0 ? P.alpha : 0.f;   // the row's two terms
-  if (rank == 0 && warp == nw - 1) {
-    if (bad && lane == 0) atomicOr(P.status, kStatusIndex);
-    if (P.row_loss) {
-      float kl = 0.f;
-      for (int j = lane; j < P.K; j += 32)
-        if (sp[j] > 0.f) kl += sp[j] * (logf(sp[j]) - (sz[j] - m) / P.tau);
-      kl = warp_sum(kl);
-      if (lane == 0) {
-        float l = ct != 0.f ? ct * P.tau * P.tau * (kl + logf(st)) : 0.f;
-        if (cl != 0.f) l += cl * (logf(s1) - (sz[P.K] - m));
-        P.row_loss[row] = bad ? __int_as_float(0x7fc00000) : w * l;
-      }
-    }
-  }
-  if (g) {
-    const float gw = w * (P.upstream ? P.upstream[b] : 1.f);
-    const float at = gw * ct * P.tau / st, a1 = cl != 0.f ? gw * cl / s1 : 0.f;
-    auto entry = [&](float zv) {   // of the student's part of the gradient
-      const float d = zv - m, q = at * exp2_approx(d * ct2);
-      return both ? fmaf(a1, exp2_approx(d * kL2), q) : q;
-    };
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = v0 + tid + i * (int)blockDim.x;
-      if (v < v1) {
-        V o;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          if (sizeof(E) == 4) o.w[n] = __float_as_uint(entry(x[i].get(n)));
-          else o.set_pair(n, entry(x[i].get(2 * n % W)), entry(x[i].get((2 * n + 1) % W)));
+  pdl_trigger();
+  pdl_wait();
+
+  const unsigned rows = (unsigned)(P.B * P.T), first = blockIdx.x, step = gridDim.x;   // < 2^31
+  const E* logits = static_cast<const E*>(P.logits);
+  const int passes = P.grad ? 2 : 1;
+  // vector v of a row covers its entries [W v - shift, W v - shift + W), v < nvec
+  auto shift_of = [&](const E* z) { return (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(E)); };
+  auto vectors = [&](int shift) { return (int)(((long long)P.V + shift + W - 1) / W); };
+
+  if (warp == kNW) {   // ---- producer
+    int i = 0;         // chunks so far
+    bool ok = true;
+    for (unsigned row = first; row < rows && ok; row += step) {
+      if (P.weights && P.weights[row] == 0.f) continue;   // not read
+      const E* z = logits + row * (size_t)P.ld;
+      const int shift = shift_of(z), nvec = vectors(shift);
+      // whole vectors [a, b); the others are the teacher warp's
+      const int a = shift > 0 ? 1 : 0, b = (int)(((long long)P.V + shift) / W);
+      for (int pass = 0; pass < passes && ok; ++pass)
+        for (int v = 0; v < nvec; v += kChunk, ++i) {
+          const int s = i % kStages;
+          const bool w = ptx::mbar_wait(&empty[s], ((i / kStages) & 1) ^ 1, abort, P.status);
+          if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+          const int v0 = max(v, a), v1 = min(v + kChunk, b);
+          if (lane == 0) {
+            if (v1 > v0) {
+              const uint32_t bytes = (uint32_t)(v1 - v0) * 16;
+              ptx::mbar_arrive_expect_tx(&full[s], bytes);
+              bulk_load(smem + s * kChunkBytes + (v0 - v) * 16, z + ((long long)W * v0 - shift), bytes, &full[s]);
+            } else {
+              ptx::mbar_arrive(&full[s]);
+            }
+          }
+          __syncwarp();
         }
-        store(v, o);
-      }
     }
-    __syncthreads();
-    for (int j = tid; j <= P.K; j += blockDim.x) {   // the teacher's entries and the label
-      const int v = j < P.K ? sk[j] : (int)y;
-      const int at_v = (v + shift) / W;
-      if (v < 0 || at_v < v0 || at_v >= v1) continue;
-      float p = 0.f;
-      for (int u = 0; u < P.K; ++u)
-        if (sk[u] == v) p += sp[u];
-      float q = entry(sz[j]) - gw * ct * P.tau * p;
-      if (v == (int)y) q -= gw * cl;
-      g[v] = from_f(q, E());
+    if (*abort && lane == 0)   // let the copies in flight land before the CTA exits
+      for (int n = max(0, i - kStages); n < i; ++n) ptx::mbar_wait_drain(&full[n % kStages], (n / kStages) & 1);
+  } else if (warp == kNW + 1) {   // ---- teacher
+    int k = 0;
+    for (unsigned row = first; row < rows; row += step) {
+      if (P.weights && P.weights[row] == 0.f) continue;
+      const int s = k & 1;
+      const bool w = ptx::mbar_wait(&tempty[s], ((k >> 1) & 1) ^ 1, abort, P.status);
+      if (!__all_sync(0xffffffffu, w)) break;
+      ++k;
+      Meta* meta = reinterpret_cast<Meta*>(teacher + s * tbytes);
+      int* sk = reinterpret_cast<int*>(meta + 1);
+      float *sp = reinterpret_cast<float*>(sk + kpad), *sz = sp + kpad;
+      const E* z = logits + row * (size_t)P.ld;
+      const int shift = shift_of(z), nvec = vectors(shift);
+      long long y = P.labels ? ld_index(P.labels, P.label_i64, row) : -1;
+      if (lane < 2) edge[2 * s + lane].load_edge(z, lane == 0 ? -shift : W * (nvec - 1) - shift, P.V);
+      float tm = -INFINITY, sum = 0.f;
+      int n = 0, oob = y >= P.V;
+      for (int j = lane; j < kpad; j += 32) {
+        const long long kk = j < P.K ? ld_index(P.idx, P.index_i64, (size_t)row * P.K + j) : -1;
+        const bool have = kk >= 0 && kk < P.V;
+        oob |= kk >= P.V;
+        n += have;
+        const float t = have ? ld_teacher(P, (size_t)row * P.K + j) / P.tau : -INFINITY;
+        sk[j] = have ? (int)kk : -1;
+        sp[j] = t;
+        sz[j] = have ? to_f(z[kk]) : 0.f;
+        tm = fmaxf(tm, t);
+      }
+      tm = warp_max(tm);
+      n = __reduce_add_sync(0xffffffffu, n);
+      oob = __any_sync(0xffffffffu, oob);
+      for (int j = lane; j < kpad; j += 32) {
+        const float e = sk[j] >= 0 ? expf(sp[j] - tm) : 0.f;
+        sp[j] = e;
+        sum += e;
+      }
+      sum = warp_sum(sum);
+      const float inv = n > 0 ? 1.f / sum : 0.f;
+      for (int j = lane; j < kpad; j += 32) sp[j] *= inv;
+      if (lane == 0) {
+        if (y < 0 || y >= P.V) y = -1;
+        *meta = {n, oob, (int)y, y >= 0 ? to_f(z[y]) : 0.f};
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&tfull[s]);
+    }
+  } else {   // ---- consumers
+    const float kL2 = 1.44269504088896341f, ct2 = kL2 / P.tau;   // exp(d / tau) = exp2(d ct2)
+    int k = 0, i = 0;
+    bool ok = true;
+    for (unsigned row = first; row < rows; row += step) {
+      const E* z = logits + row * (size_t)P.ld;
+      E* g = P.grad ? static_cast<E*>(P.grad) + row * (size_t)P.ldg : nullptr;
+      const int shift = shift_of(z), nvec = vectors(shift);
+      const bool gvec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+      const int a = shift > 0 ? 1 : 0, b = (int)(((long long)P.V + shift) / W);   // whole vectors
+      auto store = [&](int v, const V& x) {
+        const int e0 = W * v - shift;
+        if (gvec && v >= a && v < b) *reinterpret_cast<uint4*>(g + e0) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+        else x.store_edge(g, e0, P.V);
+      };
+      const float w = P.weights ? P.weights[row] : 1.f;
+      if (w == 0.f) {   // not read
+        const V zero = {{0u, 0u, 0u, 0u}};
+        if (g)
+          for (int v = tid; v < nvec; v += kNT) store(v, zero);
+        if (P.row_loss && tid == 0) P.row_loss[row] = 0.f;
+        continue;
+      }
+      const int ts = k & 1;
+      auto wait = [&](uint64_t* bar, int parity) {
+        const bool r = ptx::mbar_wait(bar, parity & 1, abort, P.status);
+        ok = __all_sync(0xffffffffu, r);
+        return ok;
+      };
+      // this thread's vectors of the next chunk, starting at vector v, into x; the ring slot freed
+      auto take = [&](int v, V (&x)[kNV]) {
+        const int s = i % kStages;
+        if (!wait(&full[s], i / kStages)) return false;
+        ++i;
+#pragma unroll
+        for (int n = 0; n < kNV; ++n) {
+          const int vn = v + n * kNT + tid;
+          if (vn >= a && vn < b)
+            x[n].load(reinterpret_cast<const E*>(smem + s * kChunkBytes + (n * kNT + tid) * 16));
+          else if (vn < nvec) x[n] = edge[2 * ts + (vn == 0 ? 0 : 1)];
+          else x[n].fill();
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&empty[s]);
+        return true;
+      };
+      wait(&tfull[ts], k >> 1);
+      // first pass: the thread's running maximum and the sums relative to it
+      float m = -INFINITY, st = 0.f, s1 = 0.f;
+      for (int v = 0; v < nvec && ok; v += kChunk) {
+        V x[kNV];
+        if (!take(v, x)) break;
+        float top = m;
+#pragma unroll
+        for (int n = 0; n < kNV; ++n)
+#pragma unroll
+          for (int c = 0; c < W; ++c) top = fmaxf(top, x[n].get(c));
+        if (top > m) {   // rare after the first chunks
+          st *= exp2_approx((m - top) * ct2);
+          if (kBoth) s1 *= exp2_approx((m - top) * kL2);
+          m = top;
+        }
+        const float base = m == -INFINITY ? 0.f : m;   // entries the student rules out
+        float u[2] = {0.f, 0.f}, u1[2] = {0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < kNV; ++n)
+#pragma unroll
+          for (int c = 0; c < W; ++c) {
+            const float d = x[n].get(c) - base;
+            u[c & 1] += exp2_approx(d * ct2);
+            if (kBoth) u1[c & 1] += exp2_approx(d * kL2);
+          }
+        st += u[0] + u[1];
+        if (kBoth) s1 += u1[0] + u1[1];
+      }
+      // the warp's, then the row's (every warp adds the warps' in one order)
+      auto combine = [&](float mx, float a1, float a2, float& rt, float& r1) {
+        const float top = warp_max(mx);
+        const float f = mx == -INFINITY ? 0.f : 1.f;   // (its sums are 0, or NaN)
+        rt = warp_sum(f == 0.f ? a1 : a1 * exp2_approx((mx - top) * ct2));
+        r1 = kBoth ? warp_sum(f == 0.f ? a2 : a2 * exp2_approx((mx - top) * kL2)) : 0.f;
+        return top;
+      };
+      float rt, r1;
+      m = combine(m, st, s1, rt, r1);
+      if (lane == 0) red[(k & 1) * kNW + warp] = make_float4(m, rt, r1, 0.f);
+      if (bar_any(!ok)) break;
+      const float4 o = lane < kNW ? red[(k & 1) * kNW + lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      m = combine(o.x, o.y, o.z, st, s1);
+
+      const Meta* meta = reinterpret_cast<const Meta*>(teacher + ts * tbytes);
+      const int* sk = reinterpret_cast<const int*>(meta + 1);
+      const float *sp = reinterpret_cast<const float*>(sk + kpad), *sz = sp + kpad;
+      const float ct = meta->valid ? 1.f - P.alpha : 0.f, cl = meta->y >= 0 ? P.alpha : 0.f;   // the two terms
+      const float gw = w * (P.upstream ? P.upstream[row / P.T] : 1.f);
+      const float at = gw * ct * P.tau / st, a1 = kBoth && cl != 0.f ? gw * cl / s1 : 0.f;
+      auto entry = [&](float zv) {   // of the student's part of the gradient
+        const float d = zv - m, q = at * exp2_approx(d * ct2);
+        return kBoth ? fmaf(a1, exp2_approx(d * kL2), q) : q;
+      };
+      if (g) {   // second pass
+        for (int v = 0; v < nvec && ok; v += kChunk) {
+          V x[kNV];
+          if (!take(v, x)) break;
+#pragma unroll
+          for (int n = 0; n < kNV; ++n) {
+            const int vn = v + n * kNT + tid;
+            if (vn < nvec) {
+              V r;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                constexpr int F = W / 4;   // entries of a word
+                const float q0 = entry(x[n].get(F * c));
+                if (F == 1) r.w[c] = __float_as_uint(q0);
+                else r.set_pair(c, q0, entry(x[n].get(F * c + F - 1)));
+              }
+              store(vn, r);
+            }
+          }
+        }
+      }
+      if (warp == kNW - 1) {
+        if (meta->bad && lane == 0) atomicOr(P.status, kStatusIndex);
+        if (P.row_loss) {
+          float kl = 0.f;
+          for (int j = lane; j < P.K; j += 32)
+            if (sp[j] > 0.f) kl += sp[j] * (logf(sp[j]) - (sz[j] - m) / P.tau);
+          kl = warp_sum(kl);
+          if (lane == 0) {
+            float l = ct != 0.f ? ct * P.tau * P.tau * (kl + logf(st)) : 0.f;
+            if (kBoth && cl != 0.f) l += cl * (logf(s1) - (meta->zy - m));
+            P.row_loss[row] = meta->bad ? __int_as_float(0x7fc00000) : w * l;
+          }
+        }
+      }
+      if (g) {
+        if (bar_any(!ok)) break;   // the row's entries are stored
+        for (int j = tid; j <= P.K; j += kNT) {   // the teacher's entries and the label
+          const int v = j < P.K ? sk[j] : meta->y;
+          if (v < 0) continue;
+          float p = 0.f;
+          for (int u = 0; u < kpad; u += 4) {
+            const int4 q = *reinterpret_cast<const int4*>(sk + u);
+            if (q.x == v) p += sp[u];
+            if (q.y == v) p += sp[u + 1];
+            if (q.z == v) p += sp[u + 2];
+            if (q.w == v) p += sp[u + 3];
+          }
+          float q = entry(j < P.K ? sz[j] : meta->zy) - gw * ct * P.tau * p;
+          if (kBoth && v == meta->y) q -= gw * cl;
+          g[v] = from_f(q, E());
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&tempty[ts]);
+      ++k;
     }
   }
-  if (cluster > 1) ptx::cluster_sync();   // no CTA leaves while another may read its slice's sums
 }
 
 // loss_i = the sum of example i's rows, in a fixed order.
@@ -420,11 +388,13 @@ __global__ void __launch_bounds__(256) distill_loss_kernel(const float* __restri
                                                            float* __restrict__ loss) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float red[33];
+  __shared__ float red[8];
   float s = 0.f;
-  for (int t = threadIdx.x; t < T; t += blockDim.x) s += rows[(size_t)blockIdx.x * T + t];
-  s = block_reduce<false>(s, red);
-  if (threadIdx.x == 0) loss[blockIdx.x] = s;
+  for (int t = threadIdx.x; t < T; t += 256) s += rows[(size_t)blockIdx.x * T + t];
+  s = warp_sum(s);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) loss[blockIdx.x] = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
 }
 
 }  // namespace distill
@@ -433,43 +403,23 @@ __global__ void __launch_bounds__(256) distill_loss_kernel(const float* __restri
 namespace dph {
 using namespace dpk;
 
-template <class E, int NV>
-static cudaError_t run_cluster(const DistillParams& P, int cluster, int per, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((size_t)P.B * P.T * cluster));
-  cfg.blockDim = dim3((unsigned)std::min(512, std::max(64, (per + 31) / 32 * 32)));
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, distill::distill_cluster_kernel<E, NV>, P, cluster);
-  count_launch();
-  return e;
-}
-
-// The smallest cluster whose registers hold a row (eight vectors a thread: two CTAs per SM,
-// so one loads while the other computes; sixteen for the longest rows), else the row kernel.
-template <class E>
+template <class E, bool kBoth>
 static cudaError_t run_distill(const DistillParams& P, cudaStream_t s) {
-  const size_t rows = (size_t)P.B * P.T;
-  const long long nvec = ((long long)P.V * sizeof(E) + 15) / 16 + 1;   // one more off the grid
-  for (int nv : {8, 16})
-    for (int c = 1; c <= distill::kMaxCluster; c *= 2) {
-      const long long per = (nvec + c - 1) / c;
-      if (per > 512LL * nv || rows * c > 0x7fffffffu) continue;
-      return nv == 8 ? run_cluster<E, 8>(P, c, (int)per, s) : run_cluster<E, 16>(P, c, (int)per, s);
-    }
-  return launch_pdl(distill::distill_row_kernel<E>, (unsigned)rows, 512, 0, s, P);
+  static const cudaError_t set =
+      cudaFuncSetAttribute(distill::distill_stream_kernel<E, kBoth>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           distill::stream_smem(distill::kMaxK));
+  if (set != cudaSuccess) return set;
+  // three CTAs per SM, two where many teacher entries take their shared memory
+  const int smem = distill::stream_smem(P.K), per_sm = std::min(distill::kMinBlocks, 232448 / (smem + 1024));
+  const unsigned grid = (unsigned)std::min<size_t>((size_t)P.B * P.T, (size_t)152 * per_sm);
+  return launch_pdl(distill::distill_stream_kernel<E, kBoth>, grid, distill::kThreads, smem, s, P);
 }
 
 cudaError_t launch_distill(const DistillParams& P, int dtype, cudaStream_t s) {
-  if ((size_t)P.B * P.T > 0x7fffffffu) return cudaErrorInvalidConfiguration;
-  cudaError_t e = dtype == DP_BF16 ? run_distill<__nv_bfloat16>(P, s) : run_distill<float>(P, s);
+  const bool both = P.alpha > 0.f && P.labels;   // the label's softmax beside the teacher's
+  cudaError_t e = dtype == DP_BF16
+                      ? both ? run_distill<__nv_bfloat16, true>(P, s) : run_distill<__nv_bfloat16, false>(P, s)
+                      : both ? run_distill<float, true>(P, s) : run_distill<float, false>(P, s);
   if (e == cudaSuccess && P.loss)
     e = launch_pdl(distill::distill_loss_kernel, (unsigned)P.B, 256, 0, s, (const float*)P.row_loss, P.T, P.loss);
   return e;
