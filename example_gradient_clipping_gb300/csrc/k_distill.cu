@@ -6,8 +6,8 @@
 //   dz = g w [ (1 - alpha) tau (q - p) + alpha (softmax(z) - e_y) ].
 //
 // Persistent CTAs, a row at a time: one pass with each thread's running maximum and sums, and
-// for the gradient a second pass over the row, which is still in L2 (the rows in work are
-// about a tenth of it), so HBM sees the row once and its gradient once.
+// for the gradient a second pass over the row, backwards: its last chunks are still in shared
+// memory, the others mostly in L2.
 //   producer warp   the row's aligned vectors in 16 KB chunks through a ring (bulk copies)
 //   teacher warp    one row ahead: the teacher's distribution, the label, and the ends of rows
 //                   off the 16-byte grid (an odd V)
@@ -83,7 +83,32 @@ template <class E> struct Words {
 
 constexpr int kNT = 256, kNW = kNT / 32, kThreads = kNT + 64;
 constexpr int kNV = 4, kChunk = kNT * kNV, kChunkBytes = kChunk * 16;   // vectors and bytes of a chunk
-constexpr int kStages = 4, kMaxK = 1024, kMinBlocks = 3;
+constexpr int kStages = 6, kMaxK = 1024, kMinBlocks = 2;
+
+// The slots of the ring in the order in which a row's chunks take them.  The gradient's pass
+// runs over the chunks backwards and so over the slots: the row's last kStages chunks are
+// still in theirs, the others follow into the slots as these fall free, and the next row goes
+// on in the same direction.
+struct Ring {
+  int pos = 0, dir = 1;
+  uint32_t phases = 0;   // of each slot's barrier
+  __device__ __forceinline__ int next() {
+    const int s = pos;
+    skip(1);
+    return s;
+  }
+  __device__ __forceinline__ void skip(int n) { pos = (pos + dir * n + kStages) % kStages; }   // n <= kStages
+  __device__ __forceinline__ void turn() {
+    dir = -dir;
+    skip(1);
+  }
+  // The parity of slot s's next phase.
+  __device__ __forceinline__ uint32_t flip(int s) {
+    const uint32_t p = phases >> s & 1;
+    phases ^= 1u << s;
+    return p;
+  }
+};
 // behind the ring: reductions [2][8] of (max, sums), row ends [2][2], barriers, flags; teacher
 constexpr int kFixed = 2 * kNW * 16 + 2 * 2 * 16 + (2 * kStages + 4) * 8 + 32;
 constexpr int stream_smem(int K) { return kStages * kChunkBytes + kFixed + 2 * (12 * ((K + 3) / 4 * 4) + 16); }
@@ -143,40 +168,48 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
 
   const unsigned rows = (unsigned)(P.B * P.T), first = blockIdx.x, step = gridDim.x;   // < 2^31
   const E* logits = static_cast<const E*>(P.logits);
-  const int passes = P.grad ? 2 : 1;
   // vector v of a row covers its entries [W v - shift, W v - shift + W), v < nvec
   auto shift_of = [&](const E* z) { return (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(E)); };
-  auto vectors = [&](int shift) { return (int)(((long long)P.V + shift + W - 1) / W); };
+  auto vectors = [&](int shift) { return (P.V + shift + W - 1) / W; };
+  auto whole_end = [&](int shift) { return (P.V + shift) / W; };   // vectors from here on reach past the row
 
   if (warp == kNW) {   // ---- producer
-    int i = 0;         // chunks so far
+    Ring ring;
+    uint32_t used = 0;   // slots that hold a load not known to have landed (for a drain)
     bool ok = true;
+    // chunk c of the row at z into the next slot, once that is free
+    auto load = [&](const E* z, int shift, int c) {
+      const int s = ring.next();
+      const bool w = ptx::mbar_wait(&empty[s], ring.flip(s) ^ 1, abort, P.status);
+      ok = __all_sync(0xffffffffu, w);
+      if (!ok) return;
+      // whole vectors only; the others are the teacher warp's
+      const int v = c * kChunk, v0 = max(v, shift > 0 ? 1 : 0), v1 = min(v + kChunk, whole_end(shift));
+      if (lane == 0) {
+        if (v1 > v0) {
+          const uint32_t bytes = (uint32_t)(v1 - v0) * 16;
+          ptx::mbar_arrive_expect_tx(&full[s], bytes);
+          bulk_load(smem + s * kChunkBytes + (v0 - v) * 16, z + ((long long)W * v0 - shift), bytes, &full[s]);
+        } else {
+          ptx::mbar_arrive(&full[s]);
+        }
+      }
+      used |= 1u << s;
+      __syncwarp();
+    };
     for (unsigned row = first; row < rows && ok; row += step) {
       if (P.weights && P.weights[row] == 0.f) continue;   // not read
       const E* z = logits + row * (size_t)P.ld;
-      const int shift = shift_of(z), nvec = vectors(shift);
-      // whole vectors [a, b); the others are the teacher warp's
-      const int a = shift > 0 ? 1 : 0, b = (int)(((long long)P.V + shift) / W);
-      for (int pass = 0; pass < passes && ok; ++pass)
-        for (int v = 0; v < nvec; v += kChunk, ++i) {
-          const int s = i % kStages;
-          const bool w = ptx::mbar_wait(&empty[s], ((i / kStages) & 1) ^ 1, abort, P.status);
-          if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-          const int v0 = max(v, a), v1 = min(v + kChunk, b);
-          if (lane == 0) {
-            if (v1 > v0) {
-              const uint32_t bytes = (uint32_t)(v1 - v0) * 16;
-              ptx::mbar_arrive_expect_tx(&full[s], bytes);
-              bulk_load(smem + s * kChunkBytes + (v0 - v) * 16, z + ((long long)W * v0 - shift), bytes, &full[s]);
-            } else {
-              ptx::mbar_arrive(&full[s]);
-            }
-          }
-          __syncwarp();
-        }
+      const int shift = shift_of(z), nc = (vectors(shift) + kChunk - 1) / kChunk;
+      for (int c = 0; c < nc && ok; ++c) load(z, shift, c);
+      if (!P.grad) continue;
+      ring.turn();
+      ring.skip(min(nc, kStages));   // the last chunks are still there
+      for (int c = nc - 1 - kStages; c >= 0 && ok; --c) load(z, shift, c);
     }
     if (*abort && lane == 0)   // let the copies in flight land before the CTA exits
-      for (int n = max(0, i - kStages); n < i; ++n) ptx::mbar_wait_drain(&full[n % kStages], (n / kStages) & 1);
+      for (int s = 0; s < kStages; ++s)
+        if (used >> s & 1) ptx::mbar_wait_drain(&full[s], (ring.phases >> s & 1) ^ 1);
   } else if (warp == kNW + 1) {   // ---- teacher
     int k = 0;
     for (unsigned row = first; row < rows; row += step) {
@@ -225,14 +258,16 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
     }
   } else {   // ---- consumers
     const float kL2 = 1.44269504088896341f, ct2 = kL2 / P.tau;   // exp(d / tau) = exp2(d ct2)
-    int k = 0, i = 0;
+    Ring ring;
+    int k = 0;
     bool ok = true;
     for (unsigned row = first; row < rows; row += step) {
       const E* z = logits + row * (size_t)P.ld;
       E* g = P.grad ? static_cast<E*>(P.grad) + row * (size_t)P.ldg : nullptr;
       const int shift = shift_of(z), nvec = vectors(shift);
       const bool gvec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
-      const int a = shift > 0 ? 1 : 0, b = (int)(((long long)P.V + shift) / W);   // whole vectors
+      const int a = shift > 0 ? 1 : 0, b = whole_end(shift);   // whole vectors
+      const int nc = (nvec + kChunk - 1) / kChunk;
       auto store = [&](int v, const V& x) {
         const int e0 = W * v - shift;
         if (gvec && v >= a && v < b) *reinterpret_cast<uint4*>(g + e0) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
@@ -252,11 +287,11 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
         ok = __all_sync(0xffffffffu, r);
         return ok;
       };
-      // this thread's vectors of the next chunk, starting at vector v, into x; the ring slot freed
-      auto take = [&](int v, V (&x)[kNV]) {
-        const int s = i % kStages;
-        if (!wait(&full[s], i / kStages)) return false;
-        ++i;
+      // this thread's vectors of chunk c, in the ring's next slot; `held`: it was there before,
+      // `keep`: it will be taken again
+      auto take = [&](int c, bool held, bool keep, V (&x)[kNV]) {
+        const int s = ring.next(), v = c * kChunk;
+        if (!held && !wait(&full[s], ring.flip(s))) return false;
 #pragma unroll
         for (int n = 0; n < kNV; ++n) {
           const int vn = v + n * kNT + tid;
@@ -266,15 +301,15 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
           else x[n].fill();
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&empty[s]);
+        if (lane == 0 && !keep) ptx::mbar_arrive(&empty[s]);
         return true;
       };
       wait(&tfull[ts], k >> 1);
       // first pass: the thread's running maximum and the sums relative to it
       float m = -INFINITY, st = 0.f, s1 = 0.f;
-      for (int v = 0; v < nvec && ok; v += kChunk) {
+      for (int c = 0; c < nc; ++c) {
         V x[kNV];
-        if (!take(v, x)) break;
+        if (!take(c, false, g && c >= nc - kStages, x)) break;
         float top = m;
 #pragma unroll
         for (int n = 0; n < kNV; ++n)
@@ -324,20 +359,21 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
         return kBoth ? fmaf(a1, exp2_approx(d * kL2), q) : q;
       };
       if (g) {   // second pass
-        for (int v = 0; v < nvec && ok; v += kChunk) {
+        ring.turn();
+        for (int c = nc - 1; c >= 0; --c) {
           V x[kNV];
-          if (!take(v, x)) break;
+          if (!take(c, c >= nc - kStages, false, x)) break;
 #pragma unroll
           for (int n = 0; n < kNV; ++n) {
-            const int vn = v + n * kNT + tid;
+            const int vn = c * kChunk + n * kNT + tid;
             if (vn < nvec) {
               V r;
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
+              for (int i = 0; i < 4; ++i) {
                 constexpr int F = W / 4;   // entries of a word
-                const float q0 = entry(x[n].get(F * c));
-                if (F == 1) r.w[c] = __float_as_uint(q0);
-                else r.set_pair(c, q0, entry(x[n].get(F * c + F - 1)));
+                const float q0 = entry(x[n].get(F * i));
+                if (F == 1) r.w[i] = __float_as_uint(q0);
+                else r.set_pair(i, q0, entry(x[n].get(F * i + F - 1)));
               }
               store(vn, r);
             }
@@ -409,7 +445,7 @@ static cudaError_t run_distill(const DistillParams& P, cudaStream_t s) {
       cudaFuncSetAttribute(distill::distill_stream_kernel<E, kBoth>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            distill::stream_smem(distill::kMaxK));
   if (set != cudaSuccess) return set;
-  // three CTAs per SM, two where many teacher entries take their shared memory
+  // two CTAs per SM, one where many teacher entries take their shared memory
   const int smem = distill::stream_smem(P.K), per_sm = std::min(distill::kMinBlocks, 232448 / (smem + 1024));
   const unsigned grid = (unsigned)std::min<size_t>((size_t)P.B * P.T, (size_t)152 * per_sm);
   return launch_pdl(distill::distill_stream_kernel<E, kBoth>, grid, distill::kThreads, smem, s, P);
