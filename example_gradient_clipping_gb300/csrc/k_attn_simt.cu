@@ -279,25 +279,42 @@ __global__ void __launch_bounds__(kThreads) attn_grad_kernel(AttnParams P) {
   }
 }
 
-// One warp per query row of one head: delta = dO . O (0 past Lq).
-template <class E>
-__global__ void __launch_bounds__(256) attn_delta_kernel(AttnParams P, float* __restrict__ delta) {
+// delta = dO . O of each query row of one head (0 past Lq): `lanes` lanes a row (a power of two),
+// vectors of VEC values, four rows a lane in flight.  Reads O and dO once: HBM.
+template <class E, int VEC>
+__global__ void __launch_bounds__(256) attn_delta_kernel(AttnParams P, float* __restrict__ delta, int lanes) {
   pdl_trigger();
   pdl_wait();
+  using V = Pack<E, VEC>;
+  constexpr int R = 4;
   const size_t n = (size_t)P.B * P.T * P.Hq;
-  const size_t i = (size_t)blockIdx.x * 8 + threadIdx.x / 32;
-  if (i >= n) return;
-  const int h = (int)(i % P.Hq);
-  const size_t bt = i / P.Hq;
-  const int b = (int)(bt / P.T), t = (int)(bt - (size_t)b * P.T);
-  float s = 0.f;
-  if (t < attn_lq(P, b)) {
+  const int per_block = 256 / lanes, nv = P.D / VEC, l = threadIdx.x & (lanes - 1);
+  const size_t i0 = (size_t)blockIdx.x * per_block * R + threadIdx.x / lanes;
+  float s[R];
+  size_t at[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const size_t i = i0 + (size_t)r * per_block;   // row (b, t, h), h innermost
+    s[r] = 0.f;
+    at[r] = n;
+    if (i >= n) continue;
+    const size_t bt = i / P.Hq;
+    const int h = (int)(i - bt * P.Hq), b = (int)(bt / P.T), t = (int)(bt - (size_t)b * P.T);
+    at[r] = ((size_t)b * P.Hq + h) * P.T + t;
+    if (t >= attn_lq(P, b)) continue;
     const E* o = static_cast<const E*>(P.O) + b * P.o.b + t * P.o.t + h * P.o.h;
     const E* g = static_cast<const E*>(P.dO) + b * P.d_o.b + t * P.d_o.t + h * P.d_o.h;
-    for (int c = threadIdx.x % 32; c < P.D; c += 32) s = fmaf(to_f(o[c]), to_f(g[c]), s);
-    s = warp_sum(s);
+    for (int v = l; v < nv; v += lanes) {
+      const V x = *reinterpret_cast<const V*>(o + v * VEC), y = *reinterpret_cast<const V*>(g + v * VEC);
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) s[r] = fmaf(x.get(c), y.get(c), s[r]);
+    }
   }
-  if (threadIdx.x % 32 == 0) delta[((size_t)b * P.Hq + h) * P.T + t] = s;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    for (int o = lanes / 2; o > 0; o >>= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+    if (l == 0 && at[r] < n) delta[at[r]] = s[r];
+  }
 }
 
 template <class E, int DP>
@@ -350,10 +367,27 @@ cudaError_t launch_attn_simt_fwd(const AttnParams& P, int dtype, cudaStream_t s)
 cudaError_t launch_attn_simt_grad(const AttnParams& P, int dtype, cudaStream_t s) {
   return dtype == DP_BF16 ? grad_d<__nv_bfloat16>(P, s) : grad_d<float>(P, s);
 }
+template <class E, int VEC>
+static cudaError_t run_delta(const AttnParams& P, float* delta, cudaStream_t s) {
+  int lanes = 1;
+  while (lanes < 32 && lanes * VEC < P.D) lanes *= 2;
+  const size_t rows = (size_t)P.B * P.T * P.Hq, per_block = 256 / lanes * 4;
+  return launch_pdl(attnsimt::attn_delta_kernel<E, VEC>, (unsigned)((rows + per_block - 1) / per_block), 256, 0, s, P,
+                    delta, lanes);
+}
+
+template <class E>
+static cudaError_t delta_vec(const AttnParams& P, float* delta, cudaStream_t s) {
+  constexpr int W = 16 / sizeof(E);
+  auto ok = [&](const void* p, const dp_strides& st) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (P.B == 1 || st.b % W == 0) && (P.T == 1 || st.t % W == 0) &&
+           (P.Hq == 1 || st.h % W == 0);
+  };
+  return P.D % W == 0 && ok(P.O, P.o) && ok(P.dO, P.d_o) ? run_delta<E, W>(P, delta, s) : run_delta<E, 1>(P, delta, s);
+}
+
 cudaError_t launch_attn_delta(const AttnParams& P, int dtype, float* delta, cudaStream_t s) {
-  const unsigned grid = (unsigned)(((size_t)P.B * P.T * P.Hq + 7) / 8);
-  if (dtype == DP_BF16) return launch_pdl(attnsimt::attn_delta_kernel<__nv_bfloat16>, grid, 256, 0, s, P, delta);
-  return launch_pdl(attnsimt::attn_delta_kernel<float>, grid, 256, 0, s, P, delta);
+  return dtype == DP_BF16 ? delta_vec<__nv_bfloat16>(P, delta, s) : delta_vec<float>(P, delta, s);
 }
 
 }  // namespace dph
