@@ -21,13 +21,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Zero rows [r0, 128) of a tile of DP columns (whole 128-byte rows of each 64-column part, so
+// Zero rows [r0, R) of a tile of DP columns (whole 128-byte rows of each 64-column part, so
 // the swizzle does not matter), by one warp, for the async proxy.
-template <int DP>
+template <int DP, int R = BT>
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int lane) {
-  for (int i = r0 * 8 + lane; i < BT * 8; i += 32)
+  for (int i = r0 * 8 + lane; i < R * 8; i += 32)
 #pragma unroll
-    for (int c = 0; c < DP / 64; ++c) *reinterpret_cast<uint4*>(tile + c * SUB + i * 16) = make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < DP / 64; ++c) *reinterpret_cast<uint4*>(tile + c * R * 128 + i * 16) = make_uint4(0, 0, 0, 0);
   ptx::fence_proxy_async_smem();
   __syncwarp();
 }
@@ -65,11 +65,12 @@ inline bool vec_ok(const void* p, const dp_strides& s, int B, int n, int H) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && fits(s.b, B) && fits(s.t, n) && fits(s.h, H);
 }
 
-inline bool map_heads(CUtensorMap* map, const void* p, const dp_strides& s, int B, int n, int H, int D) {
+inline bool map_heads(CUtensorMap* map, const void* p, const dp_strides& s, int B, int n, int H, int D,
+                      int rows = dpk::attntc::BT) {
   auto bytes = [](long long st, int extent) { return extent == 1 ? (uint64_t)1 << 20 : (uint64_t)st * 2; };
   const uint64_t dims[4] = {(uint64_t)D, (uint64_t)n, (uint64_t)H, (uint64_t)B};
   const uint64_t st[3] = {bytes(s.t, n), bytes(s.h, H), bytes(s.b, B)};
-  const uint32_t box[4] = {64, dpk::attntc::BT, 1, 1};
+  const uint32_t box[4] = {64, (uint32_t)rows, 1, 1};
   return encode_tmap_bf16(map, p, 4, dims, st, box);
 }
 

@@ -86,9 +86,9 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tS = tmem, tO = tmem + NT * BT;   // S (and P) of tile x at tS + 128 x, O at tO + DP x
   pdl_trigger();
   pdl_wait();
+  const uint32_t tS = tmem, tO = tmem + NT * BT;   // S (and P) of tile x at tS + 128 x, O at tO + DP x
 
   const int lq = attn_lq(P, b), lk = attn_lk(P, b), e = lk - lq;
   // key tiles [j0, j0 + n[x]) of each query tile

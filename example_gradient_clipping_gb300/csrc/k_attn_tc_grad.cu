@@ -12,14 +12,20 @@
 // one order.  With X1, X2 = K, V (Q, dO) the own tiles and Y1, Y2 = Q, dO (K, V) the other
 // side's, both kernels are
 //   S = X1 Y1^T,  dP = X2 Y2^T,  [acc1 += P Y2,]  acc2 += dS Y1.
-// Per tile: Y1 and Y2 serve both as K-major and as MN-major operands from one copy in shared
-// memory; dS goes back to tensor memory over the dP it was made from; P (kKeys) to shared
-// memory, because S, dP, dV and dK already fill the 512 columns at D = 128.
+// P and dS go back to tensor memory over the S and dP they were made from and are read there as
+// the A operand, so shared memory carries only the tiles, and Y1 and Y2 serve both as K-major
+// and as MN-major operands from one copy.
+// The other side's tiles have 64 NW rows, a warpgroup of softmax threads for each 64 of them:
+//   D > 64   NW = 2, one CTA per SM (S, dP, dV and dK fill its 512 columns): an MMA of N <= 128
+//            takes as long as one of N = 128, so S and dP want all of it
+//   D <= 64  NW = 1, two CTAs per SM, half of the tensor memory each: they fill each other's gaps
+// (measured at D = 128: 64-row tiles taken in turn by two warpgroups, 105 clk per MMA of N = 64,
+// 2500 clk a tile; P through shared memory, two stages of both tiles: 4250 clk per 128 rows, a
+// quarter of them waiting for the copies.)
 //   warps 0, 3  TMA: own tiles and Y1; Y2 (one warp moves ~48 B/clk, a tile pair needs more)
-//   warp 1      MMA issuer; S of the next tile is issued as soon as this tile's is in
-//               registers, so it runs under the exponentials
+//   warp 1      MMA issuer
 //   warp 2      kKeys: lse and delta of the next tiles' queries into shared memory
-//   warps 4-11  two warpgroups, a thread per own row and 64 of the other side's 128 columns
+//   warps 4..   the warpgroups, a thread per own row
 // Rows of Y1 and Y2 past their length may hold anything: the issuing warp zeroes them.
 #include <algorithm>
 
@@ -29,33 +35,47 @@ namespace dpk {
 namespace attntc {
 
 template <int DP, bool kKeys> struct Grad {
-  static constexpr int TILE = DP / 64 * SUB;
-  static constexpr int STAGES = DP == 128 ? 2 : 3;
-  static constexpr int PBUF = kKeys ? 2 * SUB : 0;
-  static constexpr int AUX = kKeys ? STAGES * 2 * BT * 4 : 0;
-  static constexpr int BARS = 4 * STAGES + STAGES + 9;
-  static constexpr int SMEM = (2 + 2 * STAGES) * TILE + PBUF + AUX + BARS * 8 + 16;
-  static constexpr int THREADS = 384;
-  static constexpr int REGS_LOW = 56, REGS_HIGH = 224;
-  static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= THREADS * 168, "register split");
-  static_assert(SMEM <= 232448, "shared memory");
+  static constexpr int NW = DP == 128 ? 2 : 1, BO = 64 * NW, SUBO = BO * 128;
+  static constexpr int ST1 = DP == 128 ? 3 : 4, ST2 = DP == 128 ? 2 : 4, STA = 2;   // stages of Y1, Y2, aux
+  static constexpr int ND = kKeys ? 1 : 2;                                          // dP buffers
+  static constexpr int TILE = DP / 64 * SUB, OTILE = DP / 64 * SUBO;
+  static constexpr int AUX = kKeys ? STA * 2 * BO * 4 : 0;
+  static constexpr int BARS = 2 * ST1 + 2 * ST2 + STA + 2 * ND + 5;
+  static constexpr int SMEM = 2 * TILE + (ST1 + ST2) * OTILE + AUX + BARS * 8 + 16;
+  static constexpr int THREADS = 128 + 128 * NW, BLOCKS = NW == 2 ? 1 : 2;
+  static constexpr uint32_t TCOLS = NW == 2 ? 512 : 256;
+  static_assert((1 + ND) * BO + (kKeys ? 2 : 1) * DP <= (int)TCOLS, "tensor memory");
+  // registers of the launch: 168 x 384, 128 x 256
+  static constexpr int REGS_LOW = 56, REGS_HIGH = NW == 2 ? 224 : 200;
+  static_assert(128 * REGS_LOW + 128 * NW * REGS_HIGH <= THREADS * (NW == 2 ? 168 : 128), "register split");
+  static_assert(BLOCKS * (SMEM + 1024) <= 233472, "shared memory");
 };
 
+// Rows [row0, row0 + 64 n) of a head as n boxes of 64 rows per 64 columns.
+template <int DP>
+__device__ __forceinline__ void load_rows(const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int n, int row, int h,
+                                          int b) {
+#pragma unroll
+  for (int c = 0; c < DP / 64; ++c)
+    for (int i = 0; i < n; ++i)
+      ptx::tma_load_4d(map, bar, dst + (c * n + i) * 64 * 128, 64 * c, row + 64 * i, h, b);
+}
+
 template <int DP, bool kKeys>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(Grad<DP, kKeys>::THREADS, Grad<DP, kKeys>::BLOCKS)
 attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_constant__ CUtensorMap mapX2,
                     const __grid_constant__ CUtensorMap mapY1, const __grid_constant__ CUtensorMap mapY2,
                     AttnParams P) {
   using C = Grad<DP, kKeys>;
-  constexpr int TILE = C::TILE, ST = C::STAGES;
+  constexpr int TILE = C::TILE, OTILE = C::OTILE, ST1 = C::ST1, ST2 = C::ST2, STA = C::STA, NW = C::NW, BO = C::BO,
+                SUBO = C::SUBO, ND = C::ND;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *sx1 = smem, *sx2 = sx1 + TILE, *sy1 = sx2 + TILE, *sy2 = sy1 + ST * TILE, *sp = sy2 + ST * TILE;
-  float* aux = reinterpret_cast<float*>(sp + C::PBUF);   // [stage][lse log2e, delta][128]
-  uint64_t* full1 = reinterpret_cast<uint64_t*>(sp + C::PBUF + C::AUX);
-  uint64_t *empty1 = full1 + ST, *full2 = empty1 + ST, *empty2 = full2 + ST, *aux_full = empty2 + ST;
-  uint64_t *own_full = aux_full + ST, *s_full = own_full + 1, *s_read = s_full + 1, *p_ready = s_read + 1,
-           *p_free = p_ready + 1, *dp_full = p_free + 1, *ds_ready = dp_full + 1, *acc_full = ds_ready + 1,
-           *drain = acc_full + 1;
+  uint8_t *sx1 = smem, *sx2 = sx1 + TILE, *sy1 = sx2 + TILE, *sy2 = sy1 + ST1 * OTILE;
+  float* aux = reinterpret_cast<float*>(sy2 + ST2 * OTILE);   // [stage][lse log2e, delta][BO]
+  uint64_t* full1 = reinterpret_cast<uint64_t*>(sy2 + ST2 * OTILE + C::AUX);
+  uint64_t *empty1 = full1 + ST1, *full2 = empty1 + ST1, *empty2 = full2 + ST2, *aux_full = empty2 + ST2;
+  uint64_t *dp_full = aux_full + STA, *ds_ready = dp_full + ND, *s_full = ds_ready + ND, *s_done = s_full + 1;
+  uint64_t *own_full = s_done + 1, *acc_full = own_full + 1, *drain = acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -69,20 +89,22 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
   const int own0 = tile * BT;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < ST; ++s) {
+    for (int s = 0; s < ST1; ++s) {
       ptx::mbar_init(&full1[s], 1);
       ptx::mbar_init(&empty1[s], 1);
+    }
+    for (int s = 0; s < ST2; ++s) {
       ptx::mbar_init(&full2[s], 1);
       ptx::mbar_init(&empty2[s], 1);
-      ptx::mbar_init(&aux_full[s], 1);
     }
-    ptx::mbar_init(own_full, 1);
+    for (int s = 0; s < STA; ++s) ptx::mbar_init(&aux_full[s], 1);
+    for (int s = 0; s < ND; ++s) {
+      ptx::mbar_init(&dp_full[s], 1);
+      ptx::mbar_init(&ds_ready[s], 4 * NW);
+    }
     ptx::mbar_init(s_full, 1);
-    ptx::mbar_init(s_read, 8);
-    ptx::mbar_init(p_ready, 8);
-    ptx::mbar_init(p_free, 1);
-    ptx::mbar_init(dp_full, 1);
-    ptx::mbar_init(ds_ready, 8);
+    ptx::mbar_init(s_done, 4 * NW);
+    ptx::mbar_init(own_full, 1);
     ptx::mbar_init(acc_full, 1);
     ptx::mbar_init(drain, 1);
     *abort = 0;
@@ -92,14 +114,15 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
     ptx::prefetch_tensormap(&mapY1);
     ptx::prefetch_tensormap(&mapY2);
   }
-  if (warp == 1) ptx::tmem_alloc(tmem_slot, 512);
+  if (warp == 1) ptx::tmem_alloc(tmem_slot, C::TCOLS);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tS = tmem, tdP = tmem + BT, tA1 = tmem + 2 * BT, tA2 = tA1 + (kKeys ? DP : 0);
   pdl_trigger();
   pdl_wait();
+  // S (then P) and dP (then dS), ND buffers of it; warpgroup w's are the 64 columns from 64 w
+  const uint32_t tS = tmem, tdP = tmem + BO, tA1 = tmem + (1 + ND) * BO, tA2 = tA1 + (kKeys ? DP : 0);
 
   const int lq = attn_lq(P, b), lk = attn_lk(P, b), e = lk - lq;
   const int lown = kKeys ? lk : lq, loth = kKeys ? lq : lk, noth = kKeys ? P.T : P.S;
@@ -108,7 +131,7 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
     if (kKeys) query_range(P, own0, min(own0 + BT, lk), lq, lk, &lo, &hi);
     else key_range(P, own0, min(own0 + BT, lq), lq, lk, &lo, &hi);
   }
-  const int j0 = lo / BT, nt = hi > lo ? (hi + BT - 1) / BT - j0 : 0;   // the other side's tiles
+  const int j0 = lo / BO, nt = hi > lo ? (hi + BO - 1) / BO - j0 : 0;   // the other side's tiles
   const int N = nt * (kKeys ? group : 1);
 
   if (warp >= 4) {
@@ -129,21 +152,24 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
       return ok;
     };
     for (int it = 0; it < N; ++it) {
-      const int s = it % ST, o0 = (j0 + (kKeys ? it % nt : it)) * BT;
+      const int s = it % STA, o0 = (j0 + (kKeys ? it % nt : it)) * BO + wg * 64;   // first of these columns
+      const uint32_t mS = tS + lanes + wg * 64, mdP = tdP + (it % ND) * BO + lanes + wg * 64;
       if (!wait(s_full, it)) break;
       ptx::tc_fence_after();
       float p[64];
-      ptx::tmem_ld32(tS + lanes + wg * 64, *reinterpret_cast<float(*)[32]>(p));
-      ptx::tmem_ld32(tS + lanes + wg * 64 + 32, *reinterpret_cast<float(*)[32]>(p + 32));
+      ptx::tmem_ld32(mS, *reinterpret_cast<float(*)[32]>(p));
+      ptx::tmem_ld32(mS + 32, *reinterpret_cast<float(*)[32]>(p + 32));
       ptx::tmem_wait_ld();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(s_read);
+      if (!kKeys) {   // S is in registers
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(s_done);
+      }
       const float4 *l4 = nullptr, *d4 = nullptr;
       if (kKeys) {
-        if (!wait(&aux_full[s], it / ST)) break;
-        l4 = reinterpret_cast<const float4*>(aux + s * 2 * BT + wg * 64);
-        d4 = l4 + BT / 4;
+        if (!wait(&aux_full[s], it / STA)) break;
+        l4 = reinterpret_cast<const float4*>(aux + s * 2 * BO + wg * 64);
+        d4 = l4 + BO / 4;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
           const float4 l = l4[c];
@@ -158,9 +184,10 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
       }
       // columns [clo, chi] of this row are seen; `masked`: some entry of the tile is not
       const int t1 = kKeys ? o0 : own0, k1 = kKeys ? own0 : o0;   // first query, first key of the tile
-      const bool masked = o0 + BT > loth || (P.causal && k1 + BT - 1 > t1 + e) ||
-                          (P.window && k1 <= t1 + BT - 1 + e - P.window);
-      int clo = 0, chi = BT;
+      const int tn = kKeys ? 64 : BT, kn = kKeys ? BT : 64;
+      const bool masked = o0 + 64 > loth || (P.causal && k1 + kn - 1 > t1 + e) ||
+                          (P.window && k1 <= t1 + tn - 1 + e - P.window);
+      int clo = 0, chi = 64;
       if (masked) {
         if (kKeys) {
           clo = (P.causal ? own - e : 0) - o0;
@@ -169,29 +196,25 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
           clo = (P.window ? own + e - P.window + 1 : 0) - o0;
           chi = (P.causal ? min(lk - 1, own + e) : lk - 1) - o0;
         }
-        clo -= wg * 64;
-        chi -= wg * 64;
 #pragma unroll
         for (int c = 0; c < 64; ++c)
           if (c < clo || c > chi) p[c] = 0.f;
       }
       if (kKeys) {
-        if (it > 0 && !wait(p_free, it - 1)) break;
-        uint8_t* dst = sp + wg * SUB + row * 128;
+        uint32_t u[32];
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<uint4*>(dst + ((q ^ (row & 7)) << 4)) =
-              make_uint4(pack_bf16(p[8 * q], p[8 * q + 1]), pack_bf16(p[8 * q + 2], p[8 * q + 3]),
-                         pack_bf16(p[8 * q + 4], p[8 * q + 5]), pack_bf16(p[8 * q + 6], p[8 * q + 7]));
-        ptx::fence_proxy_async_smem();
+        for (int i = 0; i < 32; ++i) u[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
+        ptx::tmem_st32(mS, u);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(p_ready);
+        if (lane == 0) ptx::mbar_arrive(s_done);
       }
-      if (!wait(dp_full, it)) break;
+      if (!wait(&dp_full[it % ND], it / ND)) break;
       ptx::tc_fence_after();
       float d[64];
-      ptx::tmem_ld32(tdP + lanes + wg * 64, *reinterpret_cast<float(*)[32]>(d));
-      ptx::tmem_ld32(tdP + lanes + wg * 64 + 32, *reinterpret_cast<float(*)[32]>(d + 32));
+      ptx::tmem_ld32(mdP, *reinterpret_cast<float(*)[32]>(d));
+      ptx::tmem_ld32(mdP + 32, *reinterpret_cast<float(*)[32]>(d + 32));
       ptx::tmem_wait_ld();
       if (kKeys) {
 #pragma unroll
@@ -214,11 +237,11 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
       uint32_t u[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) u[i] = pack_bf16(d[2 * i], d[2 * i + 1]);
-      ptx::tmem_st32(tdP + lanes + wg * 64, u);   // over this warpgroup's own half of dP
+      ptx::tmem_st32(mdP, u);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ds_ready);
+      if (lane == 0) ptx::mbar_arrive(&ds_ready[it % ND]);
     }
     if (ok && N > 0) {
       wait(acc_full, 0);
@@ -233,7 +256,7 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
                              own * st.t + ho * st.h;
         const float f = which == 0 ? 1.f : P.scale;
 #pragma unroll 1
-        for (int c = wg * (DP / 2); c < (wg + 1) * (DP / 2); c += 32) {
+        for (int c = wg * (DP / NW); c < (wg + 1) * (DP / NW); c += 32) {
           float o[32];
           if (N > 0) {
             ptx::tmem_ld32((which == 0 ? tA1 : tA2) + lanes + c, o);
@@ -261,51 +284,57 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
       const CUtensorMap* map = warp == 0 ? &mapY1 : &mapY2;
       uint64_t *full = warp == 0 ? full1 : full2, *empty = warp == 0 ? empty1 : empty2;
       uint8_t* ring = warp == 0 ? sy1 : sy2;
+      const int st = warp == 0 ? ST1 : ST2;
       if (warp == 0 && N > 0 && ptx::elect_one()) {
         ptx::mbar_arrive_expect_tx(own_full, 2 * TILE);
-        load_tile<DP>(&mapX1, own_full, sx1, own0, ho, b);
-        load_tile<DP>(&mapX2, own_full, sx2, own0, ho, b);
+        load_rows<DP>(&mapX1, own_full, sx1, 2, own0, ho, b);
+        load_rows<DP>(&mapX2, own_full, sx2, 2, own0, ho, b);
       }
       __syncwarp();
       int last = -1;
       for (int it = 0; it < N; ++it) {
-        const int s = it % ST;
-        const bool w = ptx::mbar_wait(&empty[s], ((it / ST) & 1) ^ 1, abort, P.status);
+        const int s = it % st;
+        const bool w = ptx::mbar_wait(&empty[s], ((it / st) & 1) ^ 1, abort, P.status);
         if (!__all_sync(0xffffffffu, w)) break;
-        const int g = kKeys ? it / nt : 0, o0 = (j0 + it - g * nt) * BT;
+        const int g = kKeys ? it / nt : 0, o0 = (j0 + it - g * nt) * BO;
         if (ptx::elect_one()) {
-          ptx::mbar_arrive_expect_tx(&full[s], TILE);
-          load_tile<DP>(map, &full[s], ring + s * TILE, o0, kKeys ? ho * group + g : ho / group, b);
+          ptx::mbar_arrive_expect_tx(&full[s], OTILE);
+          load_rows<DP>(map, &full[s], ring + s * OTILE, NW, o0, kKeys ? ho * group + g : ho / group, b);
         }
         __syncwarp();
         last = it;
       }
       if (*abort && lane == 0) {   // let the copies in flight land before the CTA exits
         if (warp == 0 && N > 0) ptx::mbar_wait_drain(own_full, 0);
-        for (int i = max(0, last - ST + 1); i <= last; ++i) ptx::mbar_wait_drain(&full[i % ST], (i / ST) & 1);
+        for (int i = max(0, last - st + 1); i <= last; ++i) ptx::mbar_wait_drain(&full[i % st], (i / st) & 1);
       }
     } else if (warp == 2) {
+      constexpr int R = BO / 32;   // queries a lane
       for (int it = 0; kKeys && it < N; ++it) {
-        const int s = it % ST, g = it / nt, t = (j0 + it - g * nt) * BT + 4 * lane;
-        const bool w = ptx::mbar_wait(&empty1[s], ((it / ST) & 1) ^ 1, abort, P.status);
-        if (!__all_sync(0xffffffffu, w)) break;
+        const int s = it % STA, g = it / nt, t = (j0 + it - g * nt) * BO + R * lane;
         const size_t i = ((size_t)b * P.Hq + ho * group + g) * P.T + t;
-        float l[4], d[4];
+        float l[R], d[R];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < R; ++c) {
           l[c] = t + c < lq ? P.lse[i + c] * kLog2e : 0.f;
           d[c] = t + c < lq ? P.delta[i + c] : 0.f;
         }
-        float* dst = aux + s * 2 * BT + 4 * lane;
-        *reinterpret_cast<float4*>(dst) = make_float4(l[0], l[1], l[2], l[3]);
-        *reinterpret_cast<float4*>(dst + BT) = make_float4(d[0], d[1], d[2], d[3]);
+        // tile it - STA is done with once dK has taken it
+        const int old = it - STA;
+        const bool w = old < 0 || ptx::mbar_wait(&empty1[old % ST1], (old / ST1) & 1, abort, P.status);
+        if (!__all_sync(0xffffffffu, w)) break;
+        float* dst = aux + s * 2 * BO + R * lane;
+#pragma unroll
+        for (int c = 0; c < R; ++c) {
+          dst[c] = l[c];
+          dst[BO + c] = d[c];
+        }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&aux_full[s]);
       }
     } else {
-      constexpr uint32_t idesc = ptx::idesc_bf16_f32(BT, DP, 0, 1);
-      const uint32_t x1 = ptx::smem_u32(sx1), x2 = ptx::smem_u32(sx2), y1 = ptx::smem_u32(sy1),
-                     y2 = ptx::smem_u32(sy2), pb = ptx::smem_u32(sp);
+      constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(BT, BO, 0, 0), idesc_a = ptx::idesc_bf16_f32(BT, DP, 0, 1);
+      const uint32_t x1 = ptx::smem_u32(sx1), x2 = ptx::smem_u32(sx2), y1 = ptx::smem_u32(sy1), y2 = ptx::smem_u32(sy2);
       bool ok = true;
       auto wait = [&](uint64_t* bar, int parity) {
         const bool w = ptx::mbar_wait(bar, parity & 1, abort, P.status);
@@ -313,64 +342,69 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
         return ok;
       };
       // tile `it` of Y1 (Y2) has arrived: zero what lies past its length
-      auto arrive = [&](uint64_t* full, uint8_t* ring, int it) {
-        const int s = it % ST;
-        if (!wait(&full[s], it / ST)) return false;
-        const int rest = loth - (j0 + (kKeys ? it % nt : it)) * BT;
-        if (rest < BT && loth < noth) zero_rows<DP>(ring + s * TILE, rest, lane);
+      auto arrive = [&](uint64_t* full, uint8_t* ring, int it, int st) {
+        const int s = it % st;
+        if (!wait(&full[s], it / st)) return false;
+        const int rest = loth - (j0 + (kKeys ? it % nt : it)) * BO;
+        if (rest < BO && loth < noth) zero_rows<DP, BO>(ring + s * OTILE, rest, lane);
         ptx::tc_fence_after();
         return true;
       };
-      auto rows = [&](uint32_t d, uint32_t x, uint32_t y, uint64_t* done) {
+      // D[128, BO] = X Y^T over DP columns (both K-major), then one or two commits
+      auto rows = [&](uint32_t d, uint32_t x, uint32_t y, uint64_t* done, uint64_t* freed) {
         if (ptx::elect_one()) {
-          mma_rows<DP>(d, x, y);
+          const uint64_t da = ptx::sdesc_sw128(x, 16, 1024), db = ptx::sdesc_sw128(y, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < DP / 16; ++kk)
+            ptx::umma_bf16(d, ptx::sdesc_add(da, (kk / 4) * SUB + (kk % 4) * 32),
+                           ptx::sdesc_add(db, (kk / 4) * SUBO + (kk % 4) * 32), idesc_s, kk != 0);
           ptx::umma_commit(done);
+          if (freed) ptx::umma_commit(freed);
         }
         __syncwarp();
       };
-      if (N > 0 && wait(own_full, 0) && arrive(full1, sy1, 0)) {
-        rows(tS, x1, y1, s_full);
-        if (arrive(full2, sy2, 0)) rows(tdP, x2, y2, dp_full);
-        for (int it = 0; it < N && ok; ++it) {
-          const int s = it % ST, sn = (it + 1) % ST;
-          const bool more = it + 1 < N;
-          if (more) {
-            if (!arrive(full1, sy1, it + 1) || !wait(s_read, it)) break;
-            ptx::tc_fence_after();
-            rows(tS, x1, y1 + sn * TILE, s_full);
-          }
-          if (kKeys) {
-            if (!wait(p_ready, it)) break;
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-              const uint64_t da = ptx::sdesc_sw128(pb, 16, 1024), db = ptx::sdesc_sw128(y2 + s * TILE, SUB, 1024);
+      // acc[128, DP] += W Y over the tile's rows, W from tensor memory (64 rows in 32 columns, from 64 w)
+      auto accumulate = [&](uint32_t acc, uint32_t w, uint32_t y, bool first, uint64_t* freed) {
+        if (ptx::elect_one()) {
+          const uint64_t db = ptx::sdesc_sw128(y, SUBO, 1024);
 #pragma unroll
-              for (int kk = 0; kk < BT / 16; ++kk)
-                ptx::umma_bf16(tA1, ptx::sdesc_add(da, (kk / 4) * SUB + (kk % 4) * 32), ptx::sdesc_add(db, kk * 2048),
-                               idesc, (it | kk) != 0);
-              ptx::umma_commit(p_free);
-              ptx::umma_commit(&empty2[s]);
-            }
-            __syncwarp();
-          }
-          if (!wait(ds_ready, it)) break;
-          ptx::tc_fence_after();
-          if (ptx::elect_one()) {
-            const uint64_t db = ptx::sdesc_sw128(y1 + s * TILE, SUB, 1024);
-#pragma unroll
-            for (int kk = 0; kk < BT / 16; ++kk)
-              ptx::umma_bf16_ta(tA2, tdP + (kk / 4) * 64 + (kk % 4) * 8, ptx::sdesc_add(db, kk * 2048), idesc,
-                                (it | kk) != 0);
-            ptx::umma_commit(&empty1[s]);
-            if (!kKeys) ptx::umma_commit(&empty2[s]);
-            if (!more) ptx::umma_commit(acc_full);
-          }
-          __syncwarp();
-          if (more) {   // in order after the product that reads dS from these columns
-            if (!arrive(full2, sy2, it + 1)) break;
-            rows(tdP, x2, y2 + sn * TILE, dp_full);
-          }
+          for (int kk = 0; kk < BO / 16; ++kk)
+            ptx::umma_bf16_ta(acc, w + (kk / 4) * 64 + (kk % 4) * 8, ptx::sdesc_add(db, kk * 2048), idesc_a,
+                              !first || kk != 0);
+          ptx::umma_commit(freed);
         }
+        __syncwarp();
+      };
+      // dP's tile of Y2 is done with once it is formed, unless dV takes it too
+      auto dp_rows = [&](int it) {
+        const int s = it % ST2;
+        if (arrive(full2, sy2, it, ST2))
+          rows(tdP + (it % ND) * BO, x2, y2 + s * OTILE, &dp_full[it % ND], kKeys ? nullptr : &empty2[s]);
+        return ok;
+      };
+      auto s_rows = [&](int it) {
+        if (arrive(full1, sy1, it, ST1)) rows(tS, x1, y1 + (it % ST1) * OTILE, s_full, nullptr);
+        return ok;
+      };
+      if (N > 0 && wait(own_full, 0)) {
+        if (s_rows(0)) dp_rows(0);
+        for (int it = 0; it < N && ok; ++it) {
+          const bool more = it + 1 < N;
+          // products run in order: the next S after the one that reads P from its columns, the
+          // next dP of a buffer after the one that reads dS
+          if (!wait(s_done, it)) break;
+          ptx::tc_fence_after();
+          if (kKeys) accumulate(tA1, tS, y2 + (it % ST2) * OTILE, it == 0, &empty2[it % ST2]);
+          if (more && !s_rows(it + 1)) break;
+          if (ND == 2 && more && !dp_rows(it + 1)) break;
+          // (a barrier per buffer: with two, the warpgroups may be a tile past the one waited for)
+          if (!wait(&ds_ready[it % ND], it / ND)) break;
+          ptx::tc_fence_after();
+          accumulate(tA2, tdP + (it % ND) * BO, y1 + (it % ST1) * OTILE, it == 0, &empty1[it % ST1]);
+          if (ND == 1 && more && !dp_rows(it + 1)) break;
+        }
+        if (ptx::elect_one()) ptx::umma_commit(acc_full);
+        __syncwarp();
       }
     }
   }
@@ -384,7 +418,7 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    ptx::tmem_dealloc(tmem, C::TCOLS);
   }
 }
 
@@ -413,8 +447,8 @@ static cudaError_t run_grad(const AttnParams& P, const CUtensorMap (&x)[2], cons
 
 cudaError_t launch_attn_tc_grad(const AttnParams& P, cudaStream_t s) {
   CUtensorMap q[2], k[2];   // Q and dO, K and V
-  if (!map_heads(&q[0], P.Q, P.q, P.B, P.T, P.Hq, P.D) || !map_heads(&q[1], P.dO, P.d_o, P.B, P.T, P.Hq, P.D) ||
-      !map_heads(&k[0], P.K, P.k, P.B, P.S, P.Hk, P.D) || !map_heads(&k[1], P.V, P.v, P.B, P.S, P.Hk, P.D))
+  if (!map_heads(&q[0], P.Q, P.q, P.B, P.T, P.Hq, P.D, 64) || !map_heads(&q[1], P.dO, P.d_o, P.B, P.T, P.Hq, P.D, 64) ||
+      !map_heads(&k[0], P.K, P.k, P.B, P.S, P.Hk, P.D, 64) || !map_heads(&k[1], P.V, P.v, P.B, P.S, P.Hk, P.D, 64))
     return cudaErrorInvalidValue;
   const cudaError_t e = P.D <= 64 ? run_grad<64, true>(P, k, q, s) : run_grad<128, true>(P, k, q, s);
   if (e != cudaSuccess) return e;

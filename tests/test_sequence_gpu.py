@@ -345,6 +345,28 @@ def test_attention_stream_graph_and_empty(lib):
     assert lib.attention_forward(q[:0], k[:0], v[:0])[0].shape == (0, 200, 2, 64)
 
 
+@pytest.mark.parametrize("D,T,H", [(64, 197, 24), (64, 500, 16), (128, 400, 16)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_attention_passes_back_to_back(lib, D, T, H, causal):
+    """Many passes with nothing between them (a kernel's first CTAs start under the last of the
+    one before): no wait gives up, and the last pass has the first one's bits."""
+    import torch
+    q, k, v, do, _, _ = _attn_inputs(16, T, T, H, H, D, None, "bf16")
+
+    def one():
+        o, lse = lib.attention_forward(q, k, v, causal=causal)
+        return (o, lse) + lib.attention_backward(q, k, v, o, lse, do, causal=causal)
+
+    want = one()
+    torch.cuda.synchronize()
+    assert lib.dp_check_status() == lib.DP_OK
+    for _ in range(60):
+        got = one()
+    torch.cuda.synchronize()
+    assert lib.dp_check_status() == lib.DP_OK
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_attention_offsets_past_32_bits(lib, D):
     import torch
