@@ -130,9 +130,15 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         for (int c = 0; c < BT; ++c)
           if (c > hi || c < lo) s[c] = -INFINITY;
       }
-      float mx = s[0];
+      float top[8];   // eight chains
 #pragma unroll
-      for (int c = 1; c < BT; ++c) mx = fmaxf(mx, s[c]);
+      for (int c = 0; c < 8; ++c) top[c] = fmaxf(s[c], s[c + 8]);
+#pragma unroll
+      for (int c = 16; c < BT; c += 16)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top[i] = fmaxf(fmaxf(top[i], s[c + i]), s[c + 8 + i]);
+      float mx = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])),
+                       fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7])));
       mx *= sc2;
       const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
       if (__any_sync(0xffffffffu, grow)) {
@@ -153,15 +159,16 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         }
       }
       const float base = m == -INFINITY ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t scale2 = pair(sc2, sc2), base2 = pair(-base, -base);
+      uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};   // pairs of zeros
 #pragma unroll
       for (int c = 0; c < BT; c += 64) {
         uint32_t u[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float p0 = ex2(fmaf(s[c + 2 * i], sc2, -base)), p1 = ex2(fmaf(s[c + 2 * i + 1], sc2, -base));
-          sum[(2 * i) & 3] += p0;
-          sum[(2 * i + 1) & 3] += p1;
+          const float2 d = unpair(fma2(pair(s[c + 2 * i], s[c + 2 * i + 1]), scale2, base2));
+          const float p0 = ex2(d.x), p1 = ex2(d.y);
+          sum[i & 3] = add2(sum[i & 3], pair(p0, p1));
           u[i] = pack_bf16(p0, p1);
         }
         ptx::tmem_st32(mS + c / 2, u);
@@ -170,7 +177,8 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&p_ready[x]);
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      const float2 total = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+      l += total.x + total.y;
     }
     if (nx > 0 && ok) {
       const bool w = ptx::mbar_wait(&o_full[x], 0, abort, P.status);

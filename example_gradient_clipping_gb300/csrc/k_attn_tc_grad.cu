@@ -71,7 +71,7 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
                 SUBO = C::SUBO, ND = C::ND;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sx1 = smem, *sx2 = sx1 + TILE, *sy1 = sx2 + TILE, *sy2 = sy1 + ST1 * OTILE;
-  float* aux = reinterpret_cast<float*>(sy2 + ST2 * OTILE);   // [stage][lse log2e, delta][BO]
+  float* aux = reinterpret_cast<float*>(sy2 + ST2 * OTILE);   // [stage][-lse log2e, -delta][BO]
   uint64_t* full1 = reinterpret_cast<uint64_t*>(sy2 + ST2 * OTILE + C::AUX);
   uint64_t *empty1 = full1 + ST1, *full2 = empty1 + ST1, *empty2 = full2 + ST2, *aux_full = empty2 + ST2;
   uint64_t *dp_full = aux_full + STA, *ds_ready = dp_full + ND, *s_full = ds_ready + ND, *s_done = s_full + 1;
@@ -145,6 +145,7 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
       lse2 = P.lse[i] * kLog2e;
       delta = P.delta[i];
     }
+    const uint64_t scale2 = pair(sc2, sc2), lse_2 = pair(-lse2, -lse2), delta_2 = pair(-delta, -delta);
     bool ok = true;
     auto wait = [&](uint64_t* bar, int parity) {
       const bool w = ptx::mbar_wait(bar, parity & 1, abort, P.status);
@@ -172,15 +173,21 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
         d4 = l4 + BO / 4;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const float4 l = l4[c];
-          p[4 * c] = ex2(fmaf(p[4 * c], sc2, -l.x));
-          p[4 * c + 1] = ex2(fmaf(p[4 * c + 1], sc2, -l.y));
-          p[4 * c + 2] = ex2(fmaf(p[4 * c + 2], sc2, -l.z));
-          p[4 * c + 3] = ex2(fmaf(p[4 * c + 3], sc2, -l.w));
+          const float4 l = l4[c];   // -lse log2e
+          const float2 x = unpair(fma2(pair(p[4 * c], p[4 * c + 1]), scale2, pair(l.x, l.y)));
+          const float2 y = unpair(fma2(pair(p[4 * c + 2], p[4 * c + 3]), scale2, pair(l.z, l.w)));
+          p[4 * c] = ex2(x.x);
+          p[4 * c + 1] = ex2(x.y);
+          p[4 * c + 2] = ex2(y.x);
+          p[4 * c + 3] = ex2(y.y);
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < 64; ++c) p[c] = ex2(fmaf(p[c], sc2, -lse2));
+        for (int c = 0; c < 32; ++c) {
+          const float2 x = unpair(fma2(pair(p[2 * c], p[2 * c + 1]), scale2, lse_2));
+          p[2 * c] = ex2(x.x);
+          p[2 * c + 1] = ex2(x.y);
+        }
       }
       // columns [clo, chi] of this row are seen; `masked`: some entry of the tile is not
       const int t1 = kKeys ? o0 : own0, k1 = kKeys ? own0 : o0;   // first query, first key of the tile
@@ -216,18 +223,20 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
       ptx::tmem_ld32(mdP, *reinterpret_cast<float(*)[32]>(d));
       ptx::tmem_ld32(mdP + 32, *reinterpret_cast<float(*)[32]>(d + 32));
       ptx::tmem_wait_ld();
-      if (kKeys) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+      for (int c = 0; c < 16; ++c) {
+        uint64_t m0 = delta_2, m1 = delta_2;   // -delta
+        if (kKeys) {
           const float4 x = d4[c];
-          d[4 * c] = p[4 * c] * (d[4 * c] - x.x);
-          d[4 * c + 1] = p[4 * c + 1] * (d[4 * c + 1] - x.y);
-          d[4 * c + 2] = p[4 * c + 2] * (d[4 * c + 2] - x.z);
-          d[4 * c + 3] = p[4 * c + 3] * (d[4 * c + 3] - x.w);
+          m0 = pair(x.x, x.y);
+          m1 = pair(x.z, x.w);
         }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 64; ++c) d[c] = p[c] * (d[c] - delta);
+        const float2 x = unpair(mul2(pair(p[4 * c], p[4 * c + 1]), add2(pair(d[4 * c], d[4 * c + 1]), m0)));
+        const float2 y = unpair(mul2(pair(p[4 * c + 2], p[4 * c + 3]), add2(pair(d[4 * c + 2], d[4 * c + 3]), m1)));
+        d[4 * c] = x.x;
+        d[4 * c + 1] = x.y;
+        d[4 * c + 2] = y.x;
+        d[4 * c + 3] = y.y;
       }
       if (masked) {   // a hidden entry adds nothing, whatever its dP
 #pragma unroll
@@ -316,8 +325,8 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
         float l[R], d[R];
 #pragma unroll
         for (int c = 0; c < R; ++c) {
-          l[c] = t + c < lq ? P.lse[i + c] * kLog2e : 0.f;
-          d[c] = t + c < lq ? P.delta[i + c] : 0.f;
+          l[c] = t + c < lq ? -P.lse[i + c] * kLog2e : 0.f;
+          d[c] = t + c < lq ? -P.delta[i + c] : 0.f;
         }
         // tile it - STA is done with once dK has taken it
         const int old = it - STA;
