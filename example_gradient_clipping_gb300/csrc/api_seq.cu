@@ -40,7 +40,7 @@ dp_status attn_params(const dp_attn_desc* d, bool grad, dpk::AttnParams* P) {
   if (!std::isfinite(d->scale) || d->scale < 0.f) return bad(DP_ERR_INVALID_ARG, "scale must be finite and >= 0");
   if (d->D > 128) return bad(DP_ERR_UNSUPPORTED, "head width D=%d is above 128", d->D);
   if (d->T > kMaxLen || d->S > kMaxLen) return bad(DP_ERR_UNSUPPORTED, "T=%d or S=%d is above 2^30", d->T, d->S);
-  if ((double)d->B * d->Hq * (std::max(d->T, d->S) / 8.0 + 1.0) > kMaxBlocks)
+  if ((double)d->B * d->Hq * ((double)d->T + d->S + 2.0) > kMaxBlocks)
     return bad(DP_ERR_UNSUPPORTED, "B x Hq x length is too large for one launch");
   if (!strides_ok(d->q) || !strides_ok(d->k) || !strides_ok(d->v))
     return bad(DP_ERR_INVALID_ARG, "strides of Q, K and V must be >= 0");
@@ -59,6 +59,9 @@ dp_status attn_params(const dp_attn_desc* d, bool grad, dpk::AttnParams* P) {
   P->status = dph::device_status();
   return DP_OK;
 }
+
+// Floats of delta, rounded up so that what follows is 16-byte aligned.
+size_t delta_floats(const dpk::AttnParams& P) { return ((size_t)P.B * P.Hq * P.T + 3) / 4 * 4; }
 
 }  // namespace
 
@@ -121,7 +124,7 @@ dp_status dp_attention(const dp_attn_desc* d, const void* Q, const void* K, cons
 size_t dp_attention_grad_workspace(const dp_attn_desc* d) {
   dpk::AttnParams P;
   if (attn_params(d, true, &P) != DP_OK) return 0;
-  return (size_t)P.B * P.Hq * P.T * sizeof(float);   // delta
+  return (delta_floats(P) + (d->dtype == DP_BF16 ? dph::attn_tc_grad_floats(P) : 0)) * sizeof(float);
 }
 
 dp_status dp_attention_grad(const dp_attn_desc* d, const void* Q, const void* K, const void* V, const void* O,
@@ -143,7 +146,7 @@ dp_status dp_attention_grad(const dp_attn_desc* d, const void* Q, const void* K,
   P.delta = delta;
   cudaError_t e = dph::launch_attn_delta(P, d->dtype, delta, stream);
   if (e == cudaSuccess)
-    e = dph::attn_tc_grad_supported(P, d->dtype) ? dph::launch_attn_tc_grad(P, stream)
+    e = dph::attn_tc_grad_supported(P, d->dtype) ? dph::launch_attn_tc_grad(P, delta + delta_floats(P), stream)
                                                  : dph::launch_attn_simt_grad(P, d->dtype, stream);
   return launched(e, "dp_attention_grad");
 }

@@ -3,7 +3,7 @@
 //   S = scale Q K^T,  P = exp2(S log2e - lse log2e),  dP = dO V^T,  dS = P * (dP - delta),
 //   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
 //
-// One kernel for either own side, a CTA per own tile of 128 rows:
+// One body for either own side, a CTA per own tile of 128 rows (or per split of its sums):
 //   kKeys   own = 128 keys: over every query tile that sees them, and the query heads that
 //           share the key head in turn, dV and dK accumulate in tensor memory
 //   !kKeys  own = 128 queries: over their key tiles, dQ accumulates
@@ -28,6 +28,7 @@
 //   warps 4..   the warpgroups, a thread per own row
 // Rows of Y1 and Y2 past their length may hold anything: the issuing warp zeroes them.
 #include <algorithm>
+#include <cmath>
 
 #include "attn_tc.cuh"
 
@@ -51,6 +52,12 @@ template <int DP, bool kKeys> struct Grad {
   static_assert(BLOCKS * (SMEM + 1024) <= 233472, "shared memory");
 };
 
+// CTAs of either own side, and the splits of each (parts in fp32 where there are several).
+struct GradSplit {
+  int keys, queries, key_ctas, query_ctas;
+  float *dk, *dv, *dq;
+};
+
 // Rows [row0, row0 + 64 n) of a head as n boxes of 64 rows per 64 columns.
 template <int DP>
 __device__ __forceinline__ void load_rows(const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int n, int row, int h,
@@ -61,11 +68,10 @@ __device__ __forceinline__ void load_rows(const CUtensorMap* map, uint64_t* bar,
       ptx::tma_load_4d(map, bar, dst + (c * n + i) * 64 * 128, 64 * c, row + 64 * i, h, b);
 }
 
+// CTA `idx` of one own side.
 template <int DP, bool kKeys>
-__global__ void __launch_bounds__(Grad<DP, kKeys>::THREADS, Grad<DP, kKeys>::BLOCKS)
-attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_constant__ CUtensorMap mapX2,
-                    const __grid_constant__ CUtensorMap mapY1, const __grid_constant__ CUtensorMap mapY2,
-                    AttnParams P) {
+__device__ __forceinline__ void grad_body(const CUtensorMap& mapX1, const CUtensorMap& mapX2, const CUtensorMap& mapY1,
+                                          const CUtensorMap& mapY2, const AttnParams& P, const GradSplit& sp, int idx) {
   using C = Grad<DP, kKeys>;
   constexpr int TILE = C::TILE, OTILE = C::OTILE, ST1 = C::ST1, ST2 = C::ST2, STA = C::STA, NW = C::NW, BO = C::BO,
                 SUBO = C::SUBO, ND = C::ND;
@@ -82,8 +88,9 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nown = kKeys ? P.S : P.T, hown = kKeys ? P.Hk : P.Hq, group = P.Hq / P.Hk;
   // causal: the longest tiles first, over all heads; else a head's tiles next to one another
-  const int tiles = (nown + BT - 1) / BT, heads = P.B * hown, idx = (int)blockIdx.x;
-  const int rank = P.causal ? idx / heads : idx % tiles, bh = P.causal ? idx % heads : idx / tiles;
+  const int tiles = (nown + BT - 1) / BT, splits = kKeys ? sp.keys : sp.queries, heads = P.B * hown * splits;
+  const int rank = P.causal ? idx / heads : idx % tiles, bhs = P.causal ? idx % heads : idx / tiles;
+  const int split = bhs % splits, bh = bhs / splits;
   const int tile = P.causal && !kKeys ? tiles - 1 - rank : rank;
   const int b = bh / hown, ho = bh - b * hown;
   const int own0 = tile * BT;
@@ -132,7 +139,11 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
     else key_range(P, own0, min(own0 + BT, lq), lq, lk, &lo, &hi);
   }
   const int j0 = lo / BO, nt = hi > lo ? (hi + BO - 1) / BO - j0 : 0;   // the other side's tiles
-  const int N = nt * (kKeys ? group : 1);
+  // this split's part of them, over the heads in turn: [i0, i0 + N)
+  const int all = nt * (kKeys ? group : 1);
+  const int i0 = (int)((long long)all * split / splits), N = (int)((long long)all * (split + 1) / splits) - i0;
+  auto head_of = [&](int it) { return kKeys ? (i0 + it) / nt : 0; };
+  auto row_of = [&](int it) { return (j0 + (kKeys ? (i0 + it) % nt : i0 + it)) * BO; };   // first of tile `it`
 
   if (warp >= 4) {
     ptx::regs_inc<C::REGS_HIGH>();
@@ -153,7 +164,7 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
       return ok;
     };
     for (int it = 0; it < N; ++it) {
-      const int s = it % STA, o0 = (j0 + (kKeys ? it % nt : it)) * BO + wg * 64;   // first of these columns
+      const int s = it % STA, o0 = row_of(it) + wg * 64;   // first of these columns
       const uint32_t mS = tS + lanes + wg * 64, mdP = tdP + (it % ND) * BO + lanes + wg * 64;
       if (!wait(s_full, it)) break;
       ptx::tc_fence_after();
@@ -264,6 +275,10 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(which == 0 ? P.dV : kKeys ? P.dK : P.dQ) + b * st.b +
                              own * st.t + ho * st.h;
         const float f = which == 0 ? 1.f : P.scale;
+        // a split's part, unscaled: [split][b][head][row][DP]
+        float4* part = reinterpret_cast<float4*>(
+            (which == 0 ? sp.dv : kKeys ? sp.dk : sp.dq) +
+            ((((size_t)split * P.B + b) * hown + ho) * nown + own) * DP);
 #pragma unroll 1
         for (int c = wg * (DP / NW); c < (wg + 1) * (DP / NW); c += 32) {
           float o[32];
@@ -272,15 +287,23 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
             ptx::tmem_wait_ld();
           }
           if (own < nown) {
+            if (splits > 1) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (c + 8 * q < P.D) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (live)
-                  v = make_uint4(pack_bf16(o[8 * q] * f, o[8 * q + 1] * f), pack_bf16(o[8 * q + 2] * f, o[8 * q + 3] * f),
-                                 pack_bf16(o[8 * q + 4] * f, o[8 * q + 5] * f),
-                                 pack_bf16(o[8 * q + 6] * f, o[8 * q + 7] * f));
-                *reinterpret_cast<uint4*>(out + c + 8 * q) = v;
+              for (int q = 0; q < 8; ++q)
+                part[c / 4 + q] = live ? make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3])
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (c + 8 * q < P.D) {
+                  uint4 v = make_uint4(0, 0, 0, 0);
+                  if (live)
+                    v = make_uint4(pack_bf16(o[8 * q] * f, o[8 * q + 1] * f),
+                                   pack_bf16(o[8 * q + 2] * f, o[8 * q + 3] * f),
+                                   pack_bf16(o[8 * q + 4] * f, o[8 * q + 5] * f),
+                                   pack_bf16(o[8 * q + 6] * f, o[8 * q + 7] * f));
+                  *reinterpret_cast<uint4*>(out + c + 8 * q) = v;
+                }
               }
             }
           }
@@ -305,7 +328,7 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
         const int s = it % st;
         const bool w = ptx::mbar_wait(&empty[s], ((it / st) & 1) ^ 1, abort, P.status);
         if (!__all_sync(0xffffffffu, w)) break;
-        const int g = kKeys ? it / nt : 0, o0 = (j0 + it - g * nt) * BO;
+        const int g = head_of(it), o0 = row_of(it);
         if (ptx::elect_one()) {
           ptx::mbar_arrive_expect_tx(&full[s], OTILE);
           load_rows<DP>(map, &full[s], ring + s * OTILE, NW, o0, kKeys ? ho * group + g : ho / group, b);
@@ -320,7 +343,7 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
     } else if (warp == 2) {
       constexpr int R = BO / 32;   // queries a lane
       for (int it = 0; kKeys && it < N; ++it) {
-        const int s = it % STA, g = it / nt, t = (j0 + it - g * nt) * BO + R * lane;
+        const int s = it % STA, g = head_of(it), t = row_of(it) + R * lane;
         const size_t i = ((size_t)b * P.Hq + ho * group + g) * P.T + t;
         float l[R], d[R];
 #pragma unroll
@@ -354,7 +377,7 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
       auto arrive = [&](uint64_t* full, uint8_t* ring, int it, int st) {
         const int s = it % st;
         if (!wait(&full[s], it / st)) return false;
-        const int rest = loth - (j0 + (kKeys ? it % nt : it)) * BO;
+        const int rest = loth - row_of(it);
         if (rest < BO && loth < noth) zero_rows<DP, BO>(ring + s * OTILE, rest, lane);
         ptx::tc_fence_after();
         return true;
@@ -431,6 +454,50 @@ attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapX1, const __grid_cons
   }
 }
 
+// Both own sides in one grid, keys first (their CTAs are the longest): the queries' CTAs fill the
+// SMs that the last keys' leave.
+template <int DP>
+__global__ void __launch_bounds__(Grad<DP, true>::THREADS, Grad<DP, true>::BLOCKS)
+attn_tc_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapG,
+                    const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV, AttnParams P,
+                    GradSplit sp) {
+  const int idx = (int)blockIdx.x;
+  if (idx < sp.key_ctas) grad_body<DP, true>(mapK, mapV, mapQ, mapG, P, sp, idx);
+  else grad_body<DP, false>(mapQ, mapG, mapK, mapV, P, sp, idx - sp.key_ctas);
+}
+
+// The splits' parts added in order, scaled and rounded: eight entries a thread; dK, dV, dQ in turn.
+__global__ void __launch_bounds__(256) attn_tc_join_kernel(AttnParams P, GradSplit sp, int DP) {
+  pdl_trigger();
+  pdl_wait();
+  const int vecs = P.D / 8;
+  const size_t nk = sp.keys > 1 ? (size_t)P.B * P.Hk * P.S * vecs : 0;
+  const size_t nq = sp.queries > 1 ? (size_t)P.B * P.Hq * P.T * vecs : 0;
+  size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= 2 * nk + nq) return;
+  const int which = i < nk ? 0 : i < 2 * nk ? 1 : 2;
+  i -= which * nk;
+  const int H = which == 2 ? P.Hq : P.Hk, n = which == 2 ? P.T : P.S, splits = which == 2 ? sp.queries : sp.keys;
+  const float* part = which == 0 ? sp.dk : which == 1 ? sp.dv : sp.dq;
+  const dp_strides& st = which == 0 ? P.dk : which == 1 ? P.dv : P.dq;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which == 0 ? P.dK : which == 1 ? P.dV : P.dQ);
+  const int v = (int)(i % vecs);
+  const size_t row = i / vecs;   // (b, head, row)
+  const int t = (int)(row % n), h = (int)(row / n % H), b = (int)(row / n / H);
+  const size_t step = (size_t)P.B * H * n * DP;
+  float a[8] = {};
+  for (int s = 0; s < splits; ++s) {
+    const float4* q = reinterpret_cast<const float4*>(part + s * step + row * DP + 8 * v);
+    const float4 x = q[0], y = q[1];
+    a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
+    a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
+  }
+  const float f = which == 1 ? 1.f : P.scale;
+  *reinterpret_cast<uint4*>(dst + b * st.b + t * st.t + h * st.h + 8 * v) =
+      make_uint4(pack_bf16(a[0] * f, a[1] * f), pack_bf16(a[2] * f, a[3] * f), pack_bf16(a[4] * f, a[5] * f),
+                 pack_bf16(a[6] * f, a[7] * f));
+}
+
 }  // namespace attntc
 }  // namespace dpk
 
@@ -443,25 +510,63 @@ bool attn_tc_grad_supported(const AttnParams& P, int dtype) {
          vec_ok(P.dQ, P.dq, P.B, P.T, P.Hq) && vec_ok(P.dK, P.dk, P.B, P.S, P.Hk) && vec_ok(P.dV, P.dv, P.B, P.S, P.Hk);
 }
 
-template <int DP, bool kKeys>
-static cudaError_t run_grad(const AttnParams& P, const CUtensorMap (&x)[2], const CUtensorMap (&y)[2], cudaStream_t s) {
-  using C = attntc::Grad<DP, kKeys>;
-  static const cudaError_t set = cudaFuncSetAttribute(attntc::attn_tc_grad_kernel<DP, kKeys>,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (set != cudaSuccess) return set;
-  const int nown = kKeys ? P.S : P.T, hown = kKeys ? P.Hk : P.Hq;
-  const unsigned grid = (unsigned)((size_t)P.B * hown * ((nown + attntc::BT - 1) / attntc::BT));
-  return launch_pdl(attntc::attn_tc_grad_kernel<DP, kKeys>, grid, C::THREADS, C::SMEM, s, x[0], x[1], y[0], y[1], P);
+// Splits of the own sides' sums: where the longest CTA would outlast an even share of all the work
+// (few heads, or many query heads on one key head), its tiles are dealt to several CTAs whose fp32
+// parts go to the workspace and are added in order.  No CTA gets fewer than four tiles.
+static attntc::GradSplit grad_split(const AttnParams& P) {
+  const int BO = P.D <= 64 ? 64 : 128;
+  const double tk = (P.S + attntc::BT - 1) / attntc::BT, tq = (P.T + attntc::BT - 1) / attntc::BT;   // own tiles
+  const double nk = (double)(P.Hq / P.Hk) * ((P.T + BO - 1) / BO), nq = (P.S + BO - 1) / BO;         // their work
+  const double share = (1.4 * P.B * P.Hk * tk * nk + P.B * P.Hq * tq * nq) / (152.0 * (P.D <= 64 ? 2 : 1));
+  auto splits = [&](double n, double cost) {
+    return (int)std::max(1.0, std::min(std::ceil(n * cost / std::max(share, 1.0)), std::floor(n / 4)));
+  };
+  attntc::GradSplit sp = {};
+  sp.keys = splits(nk, 1.4);
+  sp.queries = splits(nq, 1.0);
+  sp.key_ctas = (int)(P.B * P.Hk * tk) * sp.keys;
+  sp.query_ctas = (int)(P.B * P.Hq * tq) * sp.queries;
+  return sp;
 }
 
-cudaError_t launch_attn_tc_grad(const AttnParams& P, cudaStream_t s) {
+static size_t key_part_floats(const AttnParams& P, const attntc::GradSplit& sp) {
+  return sp.keys > 1 ? (size_t)sp.keys * P.B * P.Hk * P.S * (P.D <= 64 ? 64 : 128) : 0;
+}
+static size_t query_part_floats(const AttnParams& P, const attntc::GradSplit& sp) {
+  return sp.queries > 1 ? (size_t)sp.queries * P.B * P.Hq * P.T * (P.D <= 64 ? 64 : 128) : 0;
+}
+
+size_t attn_tc_grad_floats(const AttnParams& P) {
+  const attntc::GradSplit sp = grad_split(P);
+  return 2 * key_part_floats(P, sp) + query_part_floats(P, sp);
+}
+
+template <int DP>
+static cudaError_t run_grad(const AttnParams& P, const attntc::GradSplit& sp, const CUtensorMap (&q)[2],
+                            const CUtensorMap (&k)[2], cudaStream_t s) {
+  using C = attntc::Grad<DP, true>;
+  static_assert(C::SMEM >= attntc::Grad<DP, false>::SMEM, "one launch serves both sides");
+  static const cudaError_t set = cudaFuncSetAttribute(attntc::attn_tc_grad_kernel<DP>,
+                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (set != cudaSuccess) return set;
+  return launch_pdl(attntc::attn_tc_grad_kernel<DP>, (unsigned)(sp.key_ctas + sp.query_ctas), C::THREADS, C::SMEM, s, q[0],
+                    q[1], k[0], k[1], P, sp);
+}
+
+cudaError_t launch_attn_tc_grad(const AttnParams& P, float* ws, cudaStream_t s) {
   CUtensorMap q[2], k[2];   // Q and dO, K and V
   if (!map_heads(&q[0], P.Q, P.q, P.B, P.T, P.Hq, P.D, 64) || !map_heads(&q[1], P.dO, P.d_o, P.B, P.T, P.Hq, P.D, 64) ||
       !map_heads(&k[0], P.K, P.k, P.B, P.S, P.Hk, P.D, 64) || !map_heads(&k[1], P.V, P.v, P.B, P.S, P.Hk, P.D, 64))
     return cudaErrorInvalidValue;
-  const cudaError_t e = P.D <= 64 ? run_grad<64, true>(P, k, q, s) : run_grad<128, true>(P, k, q, s);
-  if (e != cudaSuccess) return e;
-  return P.D <= 64 ? run_grad<64, false>(P, q, k, s) : run_grad<128, false>(P, q, k, s);
+  attntc::GradSplit sp = grad_split(P);
+  sp.dk = ws;
+  sp.dv = sp.dk + key_part_floats(P, sp);
+  sp.dq = sp.dv + key_part_floats(P, sp);
+  const cudaError_t e = P.D <= 64 ? run_grad<64>(P, sp, q, k, s) : run_grad<128>(P, sp, q, k, s);
+  if (e != cudaSuccess || (sp.keys == 1 && sp.queries == 1)) return e;
+  const size_t n = ((sp.keys > 1 ? 2 * (size_t)P.B * P.Hk * P.S : 0) + (sp.queries > 1 ? (size_t)P.B * P.Hq * P.T : 0)) *
+                   (P.D / 8);
+  return launch_pdl(attntc::attn_tc_join_kernel, (unsigned)((n + 255) / 256), 256, 0, s, P, sp, P.D <= 64 ? 64 : 128);
 }
 
 }  // namespace dph

@@ -112,7 +112,9 @@ cudaError_t launch_attn_simt_grad(const dpk::AttnParams& P, int dtype, cudaStrea
 bool attn_tc_fwd_supported(const dpk::AttnParams& P, int dtype);
 bool attn_tc_grad_supported(const dpk::AttnParams& P, int dtype);
 cudaError_t launch_attn_tc_fwd(const dpk::AttnParams& P, cudaStream_t s);
-cudaError_t launch_attn_tc_grad(const dpk::AttnParams& P, cudaStream_t s);
+// ws: attn_tc_grad_floats(P) floats, 16-byte aligned.
+size_t attn_tc_grad_floats(const dpk::AttnParams& P);
+cudaError_t launch_attn_tc_grad(const dpk::AttnParams& P, float* ws, cudaStream_t s);
 // delta[b, h, t] = dO . O of each query row.
 cudaError_t launch_attn_delta(const dpk::AttnParams& P, int dtype, float* delta, cudaStream_t s);
 cudaError_t launch_distill(const dpk::DistillParams& P, int dtype, cudaStream_t s);

@@ -168,6 +168,12 @@ ATTENTION = [  # B, T, S, Hq, Hk, D, causal, window, lengths
     (1, 65, 70, 2, 2, 33, True, 0, None),
     (2, 70, 65, 2, 1, 1, False, 0, None),
     (2, 260, 260, 2, 2, 120, False, 0, None),
+    # few heads: the gradient's sums are split over CTAs and joined
+    (1, 1500, 1500, 4, 1, 128, True, 0, None),
+    (1, 900, 1300, 1, 1, 64, False, 0, None),
+    (1, 130, 2000, 2, 1, 128, False, 0, None),
+    (1, 1700, 300, 3, 1, 72, True, 200, None),
+    (3, 1100, 1100, 2, 1, 64, True, 0, "ragged"),
 ]
 
 
