@@ -27,39 +27,69 @@ __device__ __forceinline__ bool sees(const AttnParams& P, int t, int j, int lq, 
 }
 
 // Rows [row0, row0 + BT) of a [.., D] tensor as fp32 rows of DP + 4; zero from row `end` and
-// column D on (rows past the valid length are not read).
-template <class E, int DP>
+// column D on (rows past the valid length are not read).  kAsync (fp32, 16-byte rows): asynchronous
+// copies, one group, landed after wait_copies; else done on return.
+template <class E, int DP, bool kAsync>
 __device__ __forceinline__ void load_tile(float* dst, const E* src, long long stride, int row0, int end, int D) {
-  for (int i = threadIdx.x; i < BT * DP; i += kThreads) {
-    const int r = i / DP, c = i % DP;
-    dst[r * (DP + 4) + c] = row0 + r < end && c < D ? to_f(src[(row0 + r) * stride + c]) : 0.f;
+  if constexpr (kAsync) {
+    for (int i = threadIdx.x; i < BT * DP / 4; i += kThreads) {
+      const int r = i / (DP / 4), c = i % (DP / 4) * 4;
+      const bool in = row0 + r < end && c < D;
+      const float* p = in ? src + (row0 + r) * stride + c : src;   // not read when nothing is copied
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       static_cast<uint32_t>(__cvta_generic_to_shared(dst + r * (DP + 4) + c))),
+                   "l"(p), "r"(in ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  } else {
+    for (int i = threadIdx.x; i < BT * DP; i += kThreads) {
+      const int r = i / DP, c = i % DP;
+      dst[r * (DP + 4) + c] = row0 + r < end && c < D ? to_f(src[(row0 + r) * stride + c]) : 0.f;
+    }
   }
 }
+// All but the latest kLeft groups of copies have landed, for the whole block.
+template <int kLeft>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+  __syncthreads();
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 
 // s[a][c] = A row (4 ty + a) . B row (tx + 16 c)
 template <int DP>
 __device__ __forceinline__ void tile_dot(const float* A, const float* B, int ty, int tx, float (&s)[4][4]) {
+  uint64_t acc[4][4];   // sums over even and odd d, two products an instruction
 #pragma unroll
   for (int a = 0; a < 4; ++a)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) s[a][c] = 0.f;
+    for (int c = 0; c < 4; ++c) acc[a][c] = 0ull;
 #pragma unroll 4
   for (int d = 0; d < DP; d += 4) {
-    float4 x[4], y[4];
+    ulonglong2 x[4], y[4];
 #pragma unroll
-    for (int a = 0; a < 4; ++a) x[a] = *reinterpret_cast<const float4*>(A + (4 * ty + a) * (DP + 4) + d);
+    for (int a = 0; a < 4; ++a) x[a] = *reinterpret_cast<const ulonglong2*>(A + (4 * ty + a) * (DP + 4) + d);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * (DP + 4) + d);
+    for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const ulonglong2*>(B + (tx + 16 * c) * (DP + 4) + d);
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        s[a][c] = fmaf(x[a].x, y[c].x, s[a][c]);
-        s[a][c] = fmaf(x[a].y, y[c].y, s[a][c]);
-        s[a][c] = fmaf(x[a].z, y[c].z, s[a][c]);
-        s[a][c] = fmaf(x[a].w, y[c].w, s[a][c]);
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[a][c]) : "l"(x[a].x), "l"(y[c].x));
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[a][c]) : "l"(x[a].y), "l"(y[c].y));
       }
   }
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      s[a][c] = __uint_as_float((uint32_t)acc[a][c]) + __uint_as_float((uint32_t)(acc[a][c] >> 32));
 }
 
 // Columns of a thread's accumulator: VW consecutive ones from tx VW + 16 VW c.
@@ -128,20 +158,24 @@ __device__ __forceinline__ float half_warp_sum(float v) {
 template <int DP> constexpr int fwd_smem() { return (3 * BT * (DP + 4) + BT * PS) * 4; }
 template <int DP> constexpr int grad_smem() { return (4 * BT * (DP + 4) + 2 * BT * PS + 2 * BT) * 4; }
 
-template <class E, int DP>
-__global__ void __launch_bounds__(kThreads) attn_fwd_kernel(AttnParams P) {
+// One buffer each for K and V: a tile's V is copied under its scores, the next K under P V.
+template <class E, int DP, bool kAsync>
+__global__ void __launch_bounds__(kThreads, DP <= 64 ? 3 : 2) attn_fwd_kernel(AttnParams P) {
   pdl_trigger();
   pdl_wait();
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   float *sq = sm, *sk = sq + BT * (DP + 4), *sv = sk + BT * (DP + 4), *sp = sv + BT * (DP + 4);
-  const int tiles = (P.T + BT - 1) / BT;
-  const int tile = tiles - 1 - blockIdx.x % tiles, h = blockIdx.x / tiles % P.Hq, b = blockIdx.x / tiles / P.Hq;
+  // causal: the longest tiles first, over all heads
+  const int tiles = (P.T + BT - 1) / BT, heads = P.B * P.Hq, idx = (int)blockIdx.x;
+  const int tile = tiles - 1 - (P.causal ? idx / heads : idx % tiles), bh = P.causal ? idx % heads : idx / tiles;
+  const int h = bh % P.Hq, b = bh / P.Hq;
   const int t0 = tile * BT, hk = h / (P.Hq / P.Hk);
   const int lq = attn_lq(P, b), lk = attn_lk(P, b);
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   const E* K = static_cast<const E*>(P.K) + b * P.k.b + hk * P.k.h;
   const E* V = static_cast<const E*>(P.V) + b * P.v.b + hk * P.v.h;
-  float acc[4][DP / 16], m[4], l[4];
+  const float sc2 = P.scale * kLog2e;
+  float acc[4][DP / 16], m[4], l[4];   // m in units of log2
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
     m[a] = -INFINITY;
@@ -149,15 +183,15 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_kernel(AttnParams P) {
 #pragma unroll
     for (int c = 0; c < DP / 16; ++c) acc[a][c] = 0.f;
   }
-  if (t0 < lq) {
-    load_tile<E, DP>(sq, static_cast<const E*>(P.Q) + b * P.q.b + h * P.q.h, P.q.t, t0, lq, P.D);
-    int lo, hi;
-    key_range(P, t0, min(t0 + BT, lq), lq, lk, &lo, &hi);
-    for (int j0 = lo / BT * BT; j0 < hi; j0 += BT) {
-      __syncthreads();
-      load_tile<E, DP>(sk, K, P.k.t, j0, lk, P.D);
-      load_tile<E, DP>(sv, V, P.v.t, j0, lk, P.D);
-      __syncthreads();
+  int lo = 0, hi = 0;
+  if (t0 < lq) key_range(P, t0, min(t0 + BT, lq), lq, lk, &lo, &hi);
+  lo = lo / BT * BT;
+  if (lo < hi) {
+    load_tile<E, DP, kAsync>(sq, static_cast<const E*>(P.Q) + b * P.q.b + h * P.q.h, P.q.t, t0, lq, P.D);
+    load_tile<E, DP, kAsync>(sk, K, P.k.t, lo, lk, P.D);
+    for (int j0 = lo; j0 < hi; j0 += BT) {
+      load_tile<E, DP, kAsync>(sv, V, P.v.t, j0, lk, P.D);
+      wait_copies<1>();   // Q and K
       float s[4][4];
       tile_dot<DP>(sq, sk, ty, tx, s);
 #pragma unroll
@@ -166,16 +200,16 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_kernel(AttnParams P) {
         float mx = m[a];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          s[a][c] = sees(P, t, j0 + tx + 16 * c, lq, lk) ? s[a][c] * P.scale : -INFINITY;
+          s[a][c] = sees(P, t, j0 + tx + 16 * c, lq, lk) ? s[a][c] * sc2 : -INFINITY;
           mx = fmaxf(mx, s[a][c]);
         }
         mx = half_warp_max(mx);
         const float base = mx == -INFINITY ? 0.f : mx;   // a row that has seen no key yet
-        const float f = expf(m[a] - base);
+        const float f = ex2(m[a] - base);
         float sum = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float p = expf(s[a][c] - base);
+          const float p = ex2(s[a][c] - base);
           sp[(4 * ty + a) * PS + tx + 16 * c] = p;
           sum += p;
         }
@@ -184,8 +218,10 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_kernel(AttnParams P) {
 #pragma unroll
         for (int c = 0; c < DP / 16; ++c) acc[a][c] *= f;
       }
-      __syncwarp();   // a row's 16 threads are one half warp
+      wait_copies<0>();   // V; K is free
+      if (j0 + BT < hi) load_tile<E, DP, kAsync>(sk, K, P.k.t, j0 + BT, lk, P.D);
       tile_acc<DP>(sp, sv, ty, tx, acc);
+      __syncthreads();    // V is free
     }
   }
   float f[4];
@@ -194,24 +230,28 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_kernel(AttnParams P) {
     const int t = t0 + 4 * ty + a;
     f[a] = l[a] > 0.f ? 1.f / l[a] : (l[a] == 0.f ? 0.f : l[a]);   // no key: 0; NaN stays NaN
     if (P.lse && tx == 0 && t < P.T)
-      P.lse[((size_t)b * P.Hq + h) * P.T + t] = l[a] == 0.f ? -INFINITY : m[a] + logf(l[a]);
+      P.lse[((size_t)b * P.Hq + h) * P.T + t] = l[a] == 0.f ? -INFINITY : m[a] * kLn2 + logf(l[a]);
   }
   store_acc<E, DP>(acc, f, static_cast<E*>(P.O) + b * P.o.b + h * P.o.h, P.o.t, t0, P.T, P.D, ty, tx);
 }
 
-// kKeys: own tile = keys (dK, dV), the other side = queries; else own = queries (dQ).
-template <class E, int DP, bool kKeys>
-__global__ void __launch_bounds__(kThreads) attn_grad_kernel(AttnParams P) {
+// kKeys: own tile = keys (dK, dV), the other side = queries; else own = queries (dQ).  One buffer for
+// each of the other side's tiles: the next b1 is copied under the product with b2, the next b2
+// under the one with b1.
+template <class E, int DP, bool kKeys, bool kAsync>
+__global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) attn_grad_kernel(AttnParams P) {
   pdl_trigger();
   pdl_wait();
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   constexpr int TILE = BT * (DP + 4);
   float *a1 = sm, *a2 = a1 + TILE, *b1 = a2 + TILE, *b2 = b1 + TILE, *sp = b2 + TILE, *sd = sp + BT * PS;
   float *slse = sd + BT * PS, *sdel = slse + BT;
   const int nown = kKeys ? P.S : P.T, hown = kKeys ? P.Hk : P.Hq, group = P.Hq / P.Hk;
-  const int tiles = (nown + BT - 1) / BT;
-  const int tile = kKeys ? blockIdx.x % tiles : tiles - 1 - blockIdx.x % tiles;
-  const int ho = blockIdx.x / tiles % hown, b = blockIdx.x / tiles / hown;
+  // causal: the longest tiles first, over all heads
+  const int tiles = (nown + BT - 1) / BT, heads = P.B * hown, idx = (int)blockIdx.x;
+  const int rank = P.causal ? idx / heads : idx % tiles, bh = P.causal ? idx % heads : idx / tiles;
+  const int tile = kKeys ? rank : tiles - 1 - rank;
+  const int ho = bh % hown, b = bh / hown;
   const int own0 = tile * BT;
   const int lq = attn_lq(P, b), lk = attn_lk(P, b);
   const int lown = kKeys ? lk : lq, loth = kKeys ? lq : lk;
@@ -219,56 +259,66 @@ __global__ void __launch_bounds__(kThreads) attn_grad_kernel(AttnParams P) {
   const int hk = kKeys ? ho : ho / group;
   const E* K = static_cast<const E*>(P.K) + b * P.k.b + hk * P.k.h;
   const E* V = static_cast<const E*>(P.V) + b * P.v.b + hk * P.v.h;
+  const E *Q = static_cast<const E*>(P.Q) + b * P.q.b, *dO = static_cast<const E*>(P.dO) + b * P.d_o.b;
+  const float sc2 = P.scale * kLog2e;
   float acc1[4][DP / 16], acc2[4][DP / 16];   // dV (keys only); dK or dQ
 #pragma unroll
   for (int a = 0; a < 4; ++a)
 #pragma unroll
     for (int c = 0; c < DP / 16; ++c) acc1[a][c] = acc2[a][c] = 0.f;
+  int lo = 0, hi = 0;
   if (own0 < lown) {
-    int lo, hi;
     if (kKeys) query_range(P, own0, min(own0 + BT, lk), lq, lk, &lo, &hi);
     else key_range(P, own0, min(own0 + BT, lq), lq, lk, &lo, &hi);
-    if (kKeys) {
-      load_tile<E, DP>(a1, K, P.k.t, own0, lk, P.D);
-      load_tile<E, DP>(a2, V, P.v.t, own0, lk, P.D);
+  }
+  lo = lo / BT * BT;
+  const int nt = hi > lo ? (hi - lo + BT - 1) / BT : 0, N = nt * (kKeys ? group : 1);
+  // tile `it`: of query head ho * group + it / nt (keys), rows lo + BT (it % nt)
+  auto head = [&](int it) { return kKeys ? ho * group + it / nt : ho; };
+  auto load1 = [&](int it) {
+    const int o0 = lo + it % nt * BT;
+    load_tile<E, DP, kAsync>(b1, kKeys ? Q + head(it) * P.q.h : K, kKeys ? P.q.t : P.k.t, o0, loth, P.D);
+  };
+  auto load2 = [&](int it) {
+    const int o0 = lo + it % nt * BT;
+    load_tile<E, DP, kAsync>(b2, kKeys ? dO + head(it) * P.d_o.h : V, kKeys ? P.d_o.t : P.v.t, o0, loth, P.D);
+  };
+  if (N > 0) {
+    load_tile<E, DP, kAsync>(a1, kKeys ? K : Q + ho * P.q.h, kKeys ? P.k.t : P.q.t, own0, lown, P.D);
+    load_tile<E, DP, kAsync>(a2, kKeys ? V : dO + ho * P.d_o.h, kKeys ? P.v.t : P.d_o.t, own0, lown, P.D);
+    load2(0);
+    load1(0);
+  }
+  for (int it = 0; it < N; ++it) {
+    const int o0 = lo + it % nt * BT;
+    if (threadIdx.x < BT) {
+      const int t = (kKeys ? o0 : own0) + threadIdx.x;
+      const size_t stat = ((size_t)b * P.Hq + head(it)) * P.T;
+      slse[threadIdx.x] = t < lq ? P.lse[stat + t] * kLog2e : 0.f;
+      sdel[threadIdx.x] = t < lq ? P.delta[stat + t] : 0.f;
     }
-    for (int g = 0; g < (kKeys ? group : 1); ++g) {
-      const int hq = kKeys ? ho * group + g : ho;
-      const E* Q = static_cast<const E*>(P.Q) + b * P.q.b + hq * P.q.h;
-      const E* dO = static_cast<const E*>(P.dO) + b * P.d_o.b + hq * P.d_o.h;
-      const size_t stat = ((size_t)b * P.Hq + hq) * P.T;
-      if (!kKeys) {
-        load_tile<E, DP>(a1, Q, P.q.t, own0, lq, P.D);
-        load_tile<E, DP>(a2, dO, P.d_o.t, own0, lq, P.D);
-      }
-      for (int o0 = lo / BT * BT; o0 < hi; o0 += BT) {
-        __syncthreads();
-        load_tile<E, DP>(b1, kKeys ? Q : K, kKeys ? P.q.t : P.k.t, o0, loth, P.D);
-        load_tile<E, DP>(b2, kKeys ? dO : V, kKeys ? P.d_o.t : P.v.t, o0, loth, P.D);
-        if (threadIdx.x < BT) {
-          const int t = (kKeys ? o0 : own0) + threadIdx.x;
-          slse[threadIdx.x] = t < lq ? P.lse[stat + t] : 0.f;
-          sdel[threadIdx.x] = t < lq ? P.delta[stat + t] : 0.f;
-        }
-        __syncthreads();
-        float s[4][4], d[4][4];
-        tile_dot<DP>(a1, b1, ty, tx, s);
-        tile_dot<DP>(a2, b2, ty, tx, d);
+    wait_copies<1>();   // b2 (and the own tiles)
+    float s[4][4], d[4][4];
+    tile_dot<DP>(a2, b2, ty, tx, d);
+    wait_copies<0>();   // b1
+    tile_dot<DP>(a1, b1, ty, tx, s);
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < 4; ++a)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int own = 4 * ty + a, oth = tx + 16 * c, q = kKeys ? oth : own;
-            const bool see = kKeys ? sees(P, o0 + oth, own0 + own, lq, lk) : sees(P, own0 + own, o0 + oth, lq, lk);
-            const float p = see ? expf(s[a][c] * P.scale - slse[q]) : 0.f;
-            if (kKeys) sp[own * PS + oth] = p;
-            sd[own * PS + oth] = see ? p * (d[a][c] - sdel[q]) : 0.f;
-          }
-        __syncwarp();
-        if (kKeys) tile_acc<DP>(sp, b2, ty, tx, acc1);
-        tile_acc<DP>(sd, b1, ty, tx, acc2);
+      for (int c = 0; c < 4; ++c) {
+        const int own = 4 * ty + a, oth = tx + 16 * c, q = kKeys ? oth : own;
+        const bool see = kKeys ? sees(P, o0 + oth, own0 + own, lq, lk) : sees(P, own0 + own, o0 + oth, lq, lk);
+        const float p = see ? ex2(s[a][c] * sc2 - slse[q]) : 0.f;
+        if (kKeys) sp[own * PS + oth] = p;
+        sd[own * PS + oth] = see ? p * (d[a][c] - sdel[q]) : 0.f;
       }
-    }
+    __syncwarp();   // a row's 16 threads are one half warp
+    if (kKeys) tile_acc<DP>(sp, b2, ty, tx, acc1);
+    __syncthreads();    // b2 is free
+    if (it + 1 < N) load2(it + 1);
+    tile_acc<DP>(sd, b1, ty, tx, acc2);
+    __syncthreads();    // b1, lse and delta are free
+    if (it + 1 < N) load1(it + 1);
   }
   const float one[4] = {1.f, 1.f, 1.f, 1.f}, sc[4] = {P.scale, P.scale, P.scale, P.scale};
   if (kKeys) {
@@ -317,31 +367,41 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(AttnParams P, float* __
   }
 }
 
-template <class E, int DP>
+// Rows of whole 16-byte pieces: D and every stride multiples of four, bases on the grid.
+inline bool async_ok(const AttnParams& P, bool grad) {
+  auto ok = [&](const void* p, const dp_strides& st, int n, int H) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (P.B == 1 || st.b % 4 == 0) && (n == 1 || st.t % 4 == 0) &&
+           (H == 1 || st.h % 4 == 0);
+  };
+  return P.D % 4 == 0 && ok(P.Q, P.q, P.T, P.Hq) && ok(P.K, P.k, P.S, P.Hk) && ok(P.V, P.v, P.S, P.Hk) &&
+         (!grad || ok(P.dO, P.d_o, P.T, P.Hq));
+}
+
+template <class E, int DP, bool kAsync>
 cudaError_t fwd(const AttnParams& P, cudaStream_t s) {
   constexpr int smem = fwd_smem<DP>();
   static const cudaError_t set =
-      cudaFuncSetAttribute(attn_fwd_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncSetAttribute(attn_fwd_kernel<E, DP, kAsync>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (set != cudaSuccess) return set;
   const unsigned grid = (unsigned)((size_t)P.B * P.Hq * ((P.T + BT - 1) / BT));
-  return dph::launch_pdl(attn_fwd_kernel<E, DP>, grid, kThreads, smem, s, P);
+  return dph::launch_pdl(attn_fwd_kernel<E, DP, kAsync>, grid, kThreads, smem, s, P);
 }
 
-template <class E, int DP, bool kKeys>
+template <class E, int DP, bool kKeys, bool kAsync>
 cudaError_t grad_one(const AttnParams& P, cudaStream_t s) {
   constexpr int smem = grad_smem<DP>();
   static const cudaError_t set =
-      cudaFuncSetAttribute(attn_grad_kernel<E, DP, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncSetAttribute(attn_grad_kernel<E, DP, kKeys, kAsync>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (set != cudaSuccess) return set;
   const unsigned grid =
       (unsigned)((size_t)P.B * (kKeys ? P.Hk : P.Hq) * (((kKeys ? P.S : P.T) + BT - 1) / BT));
-  return dph::launch_pdl(attn_grad_kernel<E, DP, kKeys>, grid, kThreads, smem, s, P);
+  return dph::launch_pdl(attn_grad_kernel<E, DP, kKeys, kAsync>, grid, kThreads, smem, s, P);
 }
 
-template <class E, int DP>
+template <class E, int DP, bool kAsync>
 cudaError_t grad(const AttnParams& P, cudaStream_t s) {
-  const cudaError_t e = grad_one<E, DP, true>(P, s);
-  return e != cudaSuccess ? e : grad_one<E, DP, false>(P, s);
+  const cudaError_t e = grad_one<E, DP, true, kAsync>(P, s);
+  return e != cudaSuccess ? e : grad_one<E, DP, false, kAsync>(P, s);
 }
 
 }  // namespace attnsimt
@@ -350,22 +410,26 @@ cudaError_t grad(const AttnParams& P, cudaStream_t s) {
 namespace dph {
 using namespace dpk;
 
-template <class E>
+template <class E, bool kAsync>
 static cudaError_t fwd_d(const AttnParams& P, cudaStream_t s) {
-  return P.D <= 32 ? attnsimt::fwd<E, 32>(P, s) : P.D <= 64 ? attnsimt::fwd<E, 64>(P, s) : attnsimt::fwd<E, 128>(P, s);
+  return P.D <= 32   ? attnsimt::fwd<E, 32, kAsync>(P, s)
+         : P.D <= 64 ? attnsimt::fwd<E, 64, kAsync>(P, s)
+                     : attnsimt::fwd<E, 128, kAsync>(P, s);
 }
-template <class E>
+template <class E, bool kAsync>
 static cudaError_t grad_d(const AttnParams& P, cudaStream_t s) {
-  return P.D <= 32   ? attnsimt::grad<E, 32>(P, s)
-         : P.D <= 64 ? attnsimt::grad<E, 64>(P, s)
-                     : attnsimt::grad<E, 128>(P, s);
+  return P.D <= 32   ? attnsimt::grad<E, 32, kAsync>(P, s)
+         : P.D <= 64 ? attnsimt::grad<E, 64, kAsync>(P, s)
+                     : attnsimt::grad<E, 128, kAsync>(P, s);
 }
 
 cudaError_t launch_attn_simt_fwd(const AttnParams& P, int dtype, cudaStream_t s) {
-  return dtype == DP_BF16 ? fwd_d<__nv_bfloat16>(P, s) : fwd_d<float>(P, s);
+  if (dtype == DP_BF16) return fwd_d<__nv_bfloat16, false>(P, s);
+  return attnsimt::async_ok(P, false) ? fwd_d<float, true>(P, s) : fwd_d<float, false>(P, s);
 }
 cudaError_t launch_attn_simt_grad(const AttnParams& P, int dtype, cudaStream_t s) {
-  return dtype == DP_BF16 ? grad_d<__nv_bfloat16>(P, s) : grad_d<float>(P, s);
+  if (dtype == DP_BF16) return grad_d<__nv_bfloat16, false>(P, s);
+  return attnsimt::async_ok(P, true) ? grad_d<float, true>(P, s) : grad_d<float, false>(P, s);
 }
 template <class E, int VEC>
 static cudaError_t run_delta(const AttnParams& P, float* delta, cudaStream_t s) {
