@@ -239,16 +239,13 @@ __global__ void __launch_bounds__(kThreads, DP <= 64 ? 3 : 2) attn_fwd_kernel(At
 // each of the other side's tiles: the next b1 is copied under the product with b2, the next b2
 // under the one with b1.
 template <class E, int DP, bool kKeys, bool kAsync>
-__global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) attn_grad_kernel(AttnParams P) {
-  pdl_trigger();
-  pdl_wait();
-  extern __shared__ __align__(16) float sm[];
+__device__ __forceinline__ void grad_body(const AttnParams& P, int idx, float* sm) {
   constexpr int TILE = BT * (DP + 4);
   float *a1 = sm, *a2 = a1 + TILE, *b1 = a2 + TILE, *b2 = b1 + TILE, *sp = b2 + TILE, *sd = sp + BT * PS;
   float *slse = sd + BT * PS, *sdel = slse + BT;
   const int nown = kKeys ? P.S : P.T, hown = kKeys ? P.Hk : P.Hq, group = P.Hq / P.Hk;
   // causal: the longest tiles first, over all heads
-  const int tiles = (nown + BT - 1) / BT, heads = P.B * hown, idx = (int)blockIdx.x;
+  const int tiles = (nown + BT - 1) / BT, heads = P.B * hown;
   const int rank = P.causal ? idx / heads : idx % tiles, bh = P.causal ? idx % heads : idx / tiles;
   const int tile = kKeys ? rank : tiles - 1 - rank;
   const int ho = bh % hown, b = bh / hown;
@@ -329,6 +326,17 @@ __global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) attn_grad_kernel(A
   }
 }
 
+// Both own sides in one grid, keys first: the queries' CTAs fill the SMs that the last keys' leave.
+template <class E, int DP, bool kAsync>
+__global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) attn_grad_kernel(AttnParams P, int key_ctas) {
+  pdl_trigger();
+  pdl_wait();
+  extern __shared__ __align__(16) float sm[];
+  const int idx = (int)blockIdx.x;
+  if (idx < key_ctas) grad_body<E, DP, true, kAsync>(P, idx, sm);
+  else grad_body<E, DP, false, kAsync>(P, idx - key_ctas, sm);
+}
+
 // delta = dO . O of each query row of one head (0 past Lq): `lanes` lanes a row (a power of two),
 // vectors of VEC values, four rows a lane in flight.  Reads O and dO once: HBM.
 template <class E, int VEC>
@@ -337,20 +345,20 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(AttnParams P, float* __
   pdl_wait();
   using V = Pack<E, VEC>;
   constexpr int R = 4;
-  const size_t n = (size_t)P.B * P.T * P.Hq;
+  const unsigned n = (unsigned)P.B * P.T * P.Hq;   // < 2^31
   const int per_block = 256 / lanes, nv = P.D / VEC, l = threadIdx.x & (lanes - 1);
-  const size_t i0 = (size_t)blockIdx.x * per_block * R + threadIdx.x / lanes;
+  const unsigned i0 = blockIdx.x * per_block * R + threadIdx.x / lanes;
   float s[R];
-  size_t at[R];
+  unsigned at[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const size_t i = i0 + (size_t)r * per_block;   // row (b, t, h), h innermost
+    const unsigned i = i0 + r * per_block;   // row (b, t, h), h innermost
     s[r] = 0.f;
     at[r] = n;
     if (i >= n) continue;
-    const size_t bt = i / P.Hq;
-    const int h = (int)(i - bt * P.Hq), b = (int)(bt / P.T), t = (int)(bt - (size_t)b * P.T);
-    at[r] = ((size_t)b * P.Hq + h) * P.T + t;
+    const unsigned bt = i / (unsigned)P.Hq;
+    const int h = (int)(i - bt * P.Hq), b = (int)(bt / (unsigned)P.T), t = (int)(bt - (unsigned)b * P.T);
+    at[r] = ((unsigned)b * P.Hq + h) * P.T + t;
     if (t >= attn_lq(P, b)) continue;
     const E* o = static_cast<const E*>(P.O) + b * P.o.b + t * P.o.t + h * P.o.h;
     const E* g = static_cast<const E*>(P.dO) + b * P.d_o.b + t * P.d_o.t + h * P.d_o.h;
@@ -387,21 +395,15 @@ cudaError_t fwd(const AttnParams& P, cudaStream_t s) {
   return dph::launch_pdl(attn_fwd_kernel<E, DP, kAsync>, grid, kThreads, smem, s, P);
 }
 
-template <class E, int DP, bool kKeys, bool kAsync>
-cudaError_t grad_one(const AttnParams& P, cudaStream_t s) {
-  constexpr int smem = grad_smem<DP>();
-  static const cudaError_t set =
-      cudaFuncSetAttribute(attn_grad_kernel<E, DP, kKeys, kAsync>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (set != cudaSuccess) return set;
-  const unsigned grid =
-      (unsigned)((size_t)P.B * (kKeys ? P.Hk : P.Hq) * (((kKeys ? P.S : P.T) + BT - 1) / BT));
-  return dph::launch_pdl(attn_grad_kernel<E, DP, kKeys, kAsync>, grid, kThreads, smem, s, P);
-}
-
 template <class E, int DP, bool kAsync>
 cudaError_t grad(const AttnParams& P, cudaStream_t s) {
-  const cudaError_t e = grad_one<E, DP, true, kAsync>(P, s);
-  return e != cudaSuccess ? e : grad_one<E, DP, false, kAsync>(P, s);
+  constexpr int smem = grad_smem<DP>();
+  static const cudaError_t set =
+      cudaFuncSetAttribute(attn_grad_kernel<E, DP, kAsync>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (set != cudaSuccess) return set;
+  const int key_ctas = P.B * P.Hk * ((P.S + BT - 1) / BT), query_ctas = P.B * P.Hq * ((P.T + BT - 1) / BT);
+  return dph::launch_pdl(attn_grad_kernel<E, DP, kAsync>, (unsigned)(key_ctas + query_ctas), kThreads, smem, s, P,
+                         key_ctas);
 }
 
 }  // namespace attnsimt
