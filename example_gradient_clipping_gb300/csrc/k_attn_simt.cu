@@ -55,13 +55,6 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
   __syncthreads();
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
-
 // s[a][c] = A row (4 ty + a) . B row (tx + 16 c)
 template <int DP>
 __device__ __forceinline__ void tile_dot(const float* A, const float* B, int ty, int tx, float (&s)[4][4]) {

@@ -25,11 +25,6 @@
 namespace dpk {
 namespace distill {
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -49,10 +44,17 @@ template <class E> struct Words {
     if (sizeof(E) == 4) return __uint_as_float(w[n]);
     return __uint_as_float(n & 1 ? w[n / 2] & 0xffff0000u : w[n / 2] << 16);
   }
-  // entries 2i and 2i + 1 (bf16), or entry i
-  __device__ __forceinline__ void set_pair(int i, float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  // entries 2i and 2i + 1
+  __device__ __forceinline__ uint64_t get2(int i) const { return pair(get(2 * i), get(2 * i + 1)); }
+  __device__ __forceinline__ void set2(int i, uint64_t v) {
+    const float2 f = unpair(v);
+    if constexpr (sizeof(E) == 4) {
+      w[2 * i] = __float_as_uint(f.x);
+      w[2 * i + 1] = __float_as_uint(f.y);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
   }
   __device__ __forceinline__ void load(const E* p) {
     const uint4 v = *reinterpret_cast<const uint4*>(p);
@@ -80,6 +82,9 @@ template <class E> struct Words {
   }
 };
 
+
+// Exponents are formed as z ct2 - c with c rounded: exact enough while |c| stays below this.
+constexpr float kFar = 1e6f;
 
 constexpr int kNT = 256, kNW = kNT / 32, kThreads = kNT + 64;
 constexpr int kNV = 4, kChunk = kNT * kNV, kChunkBytes = kChunk * 16;   // vectors and bytes of a chunk
@@ -133,11 +138,14 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// kBoth: the label's softmax (temperature 1) beside the teacher's.
-template <class E, bool kBoth>
+// kMode: 0 the teacher's softmax alone; 1 the label's (temperature 1) beside it; 2 + n the same
+// where tau = 2^n: exp(d) is then exp(d / tau) squared n times, which saves half of the
+// exponentials, the kernel's bound with two temperatures (2048 x 50257 at tau = 2: 100 -> 74 us).
+template <class E, int kMode>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(DistillParams P) {
   using V = Words<E>;
   constexpr int W = V::W;
+  constexpr bool kBoth = kMode > 0;
   extern __shared__ __align__(128) uint8_t smem[];
   float4* red = reinterpret_cast<float4*>(smem + kStages * kChunkBytes);   // [2][warp] (max, sums)
   V* edge = reinterpret_cast<V*>(red + 2 * kNW);                           // [2][first, last vector]
@@ -169,6 +177,8 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
   const unsigned rows = (unsigned)(P.B * P.T), first = blockIdx.x, step = gridDim.x;   // < 2^31
   const E* logits = static_cast<const E*>(P.logits);
   // vector v of a row covers its entries [W v - shift, W v - shift + W), v < nvec
+  // a row's weight, asked for a row ahead
+  auto weight = [&](unsigned row) { return P.weights && row < rows ? P.weights[row] : 1.f; };
   auto shift_of = [&](const E* z) { return (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(E)); };
   auto vectors = [&](int shift) { return (P.V + shift + W - 1) / W; };
   auto whole_end = [&](int shift) { return (P.V + shift) / W; };   // vectors from here on reach past the row
@@ -197,8 +207,11 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
       used |= 1u << s;
       __syncwarp();
     };
+    float next_w = weight(first);
     for (unsigned row = first; row < rows && ok; row += step) {
-      if (P.weights && P.weights[row] == 0.f) continue;   // not read
+      const float w = next_w;
+      next_w = weight(row + step);
+      if (w == 0.f) continue;   // not read
       const E* z = logits + row * (size_t)P.ld;
       const int shift = shift_of(z), nc = (vectors(shift) + kChunk - 1) / kChunk;
       for (int c = 0; c < nc && ok; ++c) load(z, shift, c);
@@ -211,23 +224,68 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
       for (int s = 0; s < kStages; ++s)
         if (used >> s & 1) ptx::mbar_wait_drain(&full[s], (ring.phases >> s & 1) ^ 1);
   } else if (warp == kNW + 1) {   // ---- teacher
+    // a row's entries are asked for a row ahead (128 at most; more are loaded when their row comes)
+    constexpr int A = 4;
+    long long ak[A], ay = -1;
+    float at[A], aw = 1.f;
+    auto ask = [&](unsigned row) {
+      aw = weight(row);
+      if (row >= rows) return;
+      if (P.labels) ay = ld_index(P.labels, P.label_i64, row);
+#pragma unroll
+      for (int i = 0; i < A; ++i) {
+        const int j = lane + 32 * i;
+        ak[i] = j < P.K ? ld_index(P.idx, P.index_i64, (size_t)row * P.K + j) : -1;
+        at[i] = j < P.K ? ld_teacher(P, (size_t)row * P.K + j) : 0.f;
+      }
+    };
+    ask(first);
     int k = 0;
     for (unsigned row = first; row < rows; row += step) {
-      if (P.weights && P.weights[row] == 0.f) continue;
+      if (aw == 0.f) {
+        ask(row + step);
+        continue;
+      }
       const int s = k & 1;
+      const E* z = logits + row * (size_t)P.ld;
+      const int shift = shift_of(z), nvec = vectors(shift);
+      long long y = ay;
+      const bool labelled = y >= 0 && y < P.V;
+      const float zy = lane == 0 && labelled ? to_f(z[y]) : 0.f;
+      int n = 0, oob = y >= P.V;
+      int rk[A];
+      float rt[A], rz[A];
+#pragma unroll
+      for (int i = 0; i < A; ++i) {
+        const bool have = ak[i] >= 0 && ak[i] < P.V;
+        oob |= ak[i] >= P.V;
+        n += have;
+        rk[i] = have ? (int)ak[i] : -1;
+        rt[i] = have ? at[i] / P.tau : -INFINITY;
+        rz[i] = have ? to_f(z[ak[i]]) : 0.f;
+      }
+      V end;
+      if (lane < 2) end.load_edge(z, lane == 0 ? -shift : W * (nvec - 1) - shift, P.V);
+      ask(row + step);
       const bool w = ptx::mbar_wait(&tempty[s], ((k >> 1) & 1) ^ 1, abort, P.status);
       if (!__all_sync(0xffffffffu, w)) break;
       ++k;
       Meta* meta = reinterpret_cast<Meta*>(teacher + s * tbytes);
       int* sk = reinterpret_cast<int*>(meta + 1);
       float *sp = reinterpret_cast<float*>(sk + kpad), *sz = sp + kpad;
-      const E* z = logits + row * (size_t)P.ld;
-      const int shift = shift_of(z), nvec = vectors(shift);
-      long long y = P.labels ? ld_index(P.labels, P.label_i64, row) : -1;
-      if (lane < 2) edge[2 * s + lane].load_edge(z, lane == 0 ? -shift : W * (nvec - 1) - shift, P.V);
+      if (lane < 2) edge[2 * s + lane] = end;
       float tm = -INFINITY, sum = 0.f;
-      int n = 0, oob = y >= P.V;
-      for (int j = lane; j < kpad; j += 32) {
+#pragma unroll
+      for (int i = 0; i < A; ++i) {
+        const int j = lane + 32 * i;
+        if (j < kpad) {
+          sk[j] = rk[i];
+          sp[j] = rt[i];
+          sz[j] = rz[i];
+        }
+        tm = fmaxf(tm, rt[i]);
+      }
+      for (int j = lane + 32 * A; j < kpad; j += 32) {
         const long long kk = j < P.K ? ld_index(P.idx, P.index_i64, (size_t)row * P.K + j) : -1;
         const bool have = kk >= 0 && kk < P.V;
         oob |= kk >= P.V;
@@ -249,18 +307,43 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
       sum = warp_sum(sum);
       const float inv = n > 0 ? 1.f / sum : 0.f;
       for (int j = lane; j < kpad; j += 32) sp[j] *= inv;
-      if (lane == 0) {
-        if (y < 0 || y >= P.V) y = -1;
-        *meta = {n, oob, (int)y, y >= 0 ? to_f(z[y]) : 0.f};
-      }
+      if (lane == 0) *meta = {n, oob, labelled ? (int)y : -1, zy};
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&tfull[s]);
     }
   } else {   // ---- consumers
-    const float kL2 = 1.44269504088896341f, ct2 = kL2 / P.tau;   // exp(d / tau) = exp2(d ct2)
+    // exp(z / tau - top / tau) = 2^(z ct2 - c) with c = top ct2 as rounded: every term and the
+    // log-sum-exp c ln2 + log sum use the same c, so its rounding cancels.  For temperature 1
+    // (kBoth): 2^(z log2e - c1), which is the other's power where tau is one of two.
+    const float ct2 = kLog2e / P.tau;
+    const uint64_t ct2p = pair(ct2, ct2), onep = pair(kLog2e, kLog2e);
+    auto ref = [&](float top) { return fmaxf(top * ct2, -kFar); };   // (masks below it add nothing)
+    auto ref1 = [&](float top, float c) {
+      return kMode >= 2 ? c * (float)(1 << (kMode >= 2 ? kMode - 2 : 0)) : fmaxf(top * kLog2e, -kFar);
+    };
+    auto power = [&](float f) {   // of a factor of the sums for tau: that of the sums for 1
+#pragma unroll
+      for (int n = 0; n < (kMode >= 2 ? kMode - 2 : 0); ++n) f *= f;
+      return f;
+    };
+    auto exps = [&](uint64_t z, uint64_t c) {   // c: the negated reference
+      const float2 d = unpair(fma2(z, ct2p, c));
+      return pair(ex2(d.x), ex2(d.y));
+    };
+    auto exps1 = [&](uint64_t z, uint64_t e, uint64_t c1) {
+      if constexpr (kMode < 2) {
+        const float2 d = unpair(fma2(z, onep, c1));
+        return pair(ex2(d.x), ex2(d.y));
+      } else {
+        if constexpr (kMode >= 3) e = mul2(e, e);
+        if constexpr (kMode >= 4) e = mul2(e, e);
+        return e;
+      }
+    };
     Ring ring;
     int k = 0;
     bool ok = true;
+    float next_w = weight(first);
     for (unsigned row = first; row < rows; row += step) {
       const E* z = logits + row * (size_t)P.ld;
       E* g = P.grad ? static_cast<E*>(P.grad) + row * (size_t)P.ldg : nullptr;
@@ -273,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
         if (gvec && v >= a && v < b) *reinterpret_cast<uint4*>(g + e0) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
         else x.store_edge(g, e0, P.V);
       };
-      const float w = P.weights ? P.weights[row] : 1.f;
+      const float w = next_w;
+      next_w = weight(row + step);
       if (w == 0.f) {   // not read
         const V zero = {{0u, 0u, 0u, 0u}};
         if (g)
@@ -306,90 +390,132 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
       };
       wait(&tfull[ts], k >> 1);
       // first pass: the thread's running maximum and the sums relative to it
-      float m = -INFINITY, st = 0.f, s1 = 0.f;
-      for (int c = 0; c < nc; ++c) {
+      float m = -INFINITY, c = 0.f, c1 = 0.f, st = 0.f, s1 = 0.f;
+      for (int j = 0; j < nc; ++j) {
         V x[kNV];
-        if (!take(c, false, g && c >= nc - kStages, x)) break;
+        if (!take(j, false, g && j >= nc - kStages, x)) break;
         float top = m;
+        if constexpr (sizeof(E) == 2) {   // maxima of packed pairs
+          __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&x[0].w[0]);
 #pragma unroll
-        for (int n = 0; n < kNV; ++n)
+          for (int n = 0; n < kNV; ++n)
 #pragma unroll
-          for (int c = 0; c < W; ++c) top = fmaxf(top, x[n].get(c));
-        if (top > m) {   // rare after the first chunks
-          st *= exp2_approx((m - top) * ct2);
-          if (kBoth) s1 *= exp2_approx((m - top) * kL2);
-          m = top;
+            for (int i = 0; i < 4; ++i) h = __hmax2(h, *reinterpret_cast<const __nv_bfloat162*>(&x[n].w[i]));
+          top = fmaxf(top, fmaxf(__low2float(h), __high2float(h)));
+        } else {
+#pragma unroll
+          for (int n = 0; n < kNV; ++n)
+#pragma unroll
+            for (int i = 0; i < W; ++i) top = fmaxf(top, x[n].get(i));
         }
-        const float base = m == -INFINITY ? 0.f : m;   // entries the student rules out
-        float u[2] = {0.f, 0.f}, u1[2] = {0.f, 0.f};
+        if (top > m) {   // rare after the first chunks
+          const float cn = ref(top), c1n = ref1(top, cn);
+          if (m > -INFINITY) {   // (else the sums are 0, and the new reference may be any finite value)
+            const float f = ex2(c - cn);
+            st *= f;
+            if (kBoth) s1 *= kMode >= 2 ? power(f) : ex2(c1 - c1n);
+          }
+          m = top;
+          c = cn;
+          c1 = c1n;
+        }
+        const uint64_t cp = pair(-c, -c), c1p = pair(-c1, -c1);
+        uint64_t u[2] = {0ull, 0ull}, u1[2] = {0ull, 0ull};
 #pragma unroll
         for (int n = 0; n < kNV; ++n)
 #pragma unroll
-          for (int c = 0; c < W; ++c) {
-            const float d = x[n].get(c) - base;
-            u[c & 1] += exp2_approx(d * ct2);
-            if (kBoth) u1[c & 1] += exp2_approx(d * kL2);
+          for (int i = 0; i < W / 2; ++i) {
+            const uint64_t z2 = x[n].get2(i), e = exps(z2, cp);
+            u[i & 1] = add2(u[i & 1], e);
+            if (kBoth) u1[i & 1] = add2(u1[i & 1], exps1(z2, e, c1p));
           }
-        st += u[0] + u[1];
-        if (kBoth) s1 += u1[0] + u1[1];
+        const float2 a = unpair(add2(u[0], u[1]));
+        st += a.x + a.y;
+        if (kBoth) {
+          const float2 a1 = unpair(add2(u1[0], u1[1]));
+          s1 += a1.x + a1.y;
+        }
       }
       // the warp's, then the row's (every warp adds the warps' in one order)
-      auto combine = [&](float mx, float a1, float a2, float& rt, float& r1) {
-        const float top = warp_max(mx);
-        const float f = mx == -INFINITY ? 0.f : 1.f;   // (its sums are 0, or NaN)
-        rt = warp_sum(f == 0.f ? a1 : a1 * exp2_approx((mx - top) * ct2));
-        r1 = kBoth ? warp_sum(f == 0.f ? a2 : a2 * exp2_approx((mx - top) * kL2)) : 0.f;
-        return top;
+      auto combine = [&](float mx, float a, float a1) {
+        m = warp_max(mx);
+        const float cm = ref(mx), c1m = ref1(mx, cm);   // of these sums
+        c = ref(m);
+        c1 = ref1(m, c);
+        const float f = mx == -INFINITY ? 1.f : ex2(cm - c), f1 = kMode >= 2 ? power(f) : ex2(c1m - c1);
+        st = warp_sum(a * f);   // (without a maximum the sums are 0, or NaN)
+        if (kBoth) s1 = warp_sum(mx == -INFINITY ? a1 : a1 * f1);
       };
-      float rt, r1;
-      m = combine(m, st, s1, rt, r1);
-      if (lane == 0) red[(k & 1) * kNW + warp] = make_float4(m, rt, r1, 0.f);
+      combine(m, st, s1);
+      if (lane == 0) red[(k & 1) * kNW + warp] = make_float4(m, st, s1, 0.f);
       if (bar_any(!ok)) break;
       const float4 o = lane < kNW ? red[(k & 1) * kNW + lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      m = combine(o.x, o.y, o.z, st, s1);
-
+      combine(o.x, o.y, o.z);
+      // A row whose maximum is far from 0 (nothing but masks of the type's lowest value): its sums
+      // once more, over the differences to its maximum.
+      const bool far = !(fabsf(m * ct2) < kFar && fabsf(m * kLog2e) < kFar);
+      if (far) {
+        st = s1 = 0.f;
+        for (int v = tid; v < P.V; v += kNT) {
+          const float d = to_f(z[v]) - m;
+          st += ex2(d * ct2);
+          if (kBoth) s1 += ex2(d * kLog2e);
+        }
+        st = warp_sum(st);
+        s1 = warp_sum(s1);
+        bar_any(false);   // everyone has read red
+        if (lane == 0) red[(k & 1) * kNW + warp] = make_float4(0.f, st, s1, 0.f);
+        bar_any(false);
+        const float4 p = lane < kNW ? red[(k & 1) * kNW + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        st = warp_sum(p.y);
+        s1 = warp_sum(p.z);
+      }
+      auto rel = [&](float zv) { return far ? (zv - m) * ct2 : fmaf(zv, ct2, -c); };        // log2 of a term
+      auto rel1 = [&](float zv) { return far ? (zv - m) * kLog2e : fmaf(zv, kLog2e, -c1); };
       const Meta* meta = reinterpret_cast<const Meta*>(teacher + ts * tbytes);
       const int* sk = reinterpret_cast<const int*>(meta + 1);
       const float *sp = reinterpret_cast<const float*>(sk + kpad), *sz = sp + kpad;
       const float ct = meta->valid ? 1.f - P.alpha : 0.f, cl = meta->y >= 0 ? P.alpha : 0.f;   // the two terms
       const float gw = w * (P.upstream ? P.upstream[row / P.T] : 1.f);
       const float at = gw * ct * P.tau / st, a1 = kBoth && cl != 0.f ? gw * cl / s1 : 0.f;
-      auto entry = [&](float zv) {   // of the student's part of the gradient
-        const float d = zv - m, q = at * exp2_approx(d * ct2);
-        return kBoth ? fmaf(a1, exp2_approx(d * kL2), q) : q;
+      const uint64_t cp = pair(-c, -c), c1p = pair(-c1, -c1), atp = pair(at, at), a1p = pair(a1, a1);
+      auto entries = [&](uint64_t z2) {   // of the student's part of the gradient
+        const uint64_t e = exps(z2, cp), q = mul2(atp, e);
+        return kBoth ? fma2(a1p, exps1(z2, e, c1p), q) : q;
       };
-      if (g) {   // second pass
+      auto entry = [&](float zv) {   // the same for one, in any row
+        const float q = at * ex2(rel(zv));
+        return kBoth ? fmaf(a1, kMode >= 2 ? power(ex2(rel(zv))) : ex2(rel1(zv)), q) : q;
+      };
+      auto second_pass = [&](auto form) {   // form: a vector's entries from its logits
         ring.turn();
-        for (int c = nc - 1; c >= 0; --c) {
+        for (int j = nc - 1; j >= 0; --j) {
           V x[kNV];
-          if (!take(c, c >= nc - kStages, false, x)) break;
+          if (!take(j, j >= nc - kStages, false, x)) break;
 #pragma unroll
           for (int n = 0; n < kNV; ++n) {
-            const int vn = c * kChunk + n * kNT + tid;
+            const int vn = j * kChunk + n * kNT + tid;
             if (vn < nvec) {
               V r;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                constexpr int F = W / 4;   // entries of a word
-                const float q0 = entry(x[n].get(F * i));
-                if (F == 1) r.w[i] = __float_as_uint(q0);
-                else r.set_pair(i, q0, entry(x[n].get(F * i + F - 1)));
-              }
+              for (int i = 0; i < W / 2; ++i) r.set2(i, form(x[n].get2(i)));
               store(vn, r);
             }
           }
         }
-      }
+      };
+      if (g && !far) second_pass(entries);
+      else if (g) second_pass([&](uint64_t z2) { return pair(entry(unpair(z2).x), entry(unpair(z2).y)); });
       if (warp == kNW - 1) {
         if (meta->bad && lane == 0) atomicOr(P.status, kStatusIndex);
         if (P.row_loss) {
           float kl = 0.f;
           for (int j = lane; j < P.K; j += 32)
-            if (sp[j] > 0.f) kl += sp[j] * (logf(sp[j]) - (sz[j] - m) / P.tau);
+            if (sp[j] > 0.f) kl += sp[j] * (logf(sp[j]) - rel(sz[j]) * kLn2);
           kl = warp_sum(kl);
           if (lane == 0) {
             float l = ct != 0.f ? ct * P.tau * P.tau * (kl + logf(st)) : 0.f;
-            if (kBoth && cl != 0.f) l += cl * (logf(s1) - (meta->zy - m));
+            if (kBoth && cl != 0.f) l += cl * (logf(s1) - rel1(meta->zy) * kLn2);
             P.row_loss[row] = meta->bad ? __int_as_float(0x7fc00000) : w * l;
           }
         }
@@ -439,23 +565,29 @@ __global__ void __launch_bounds__(256) distill_loss_kernel(const float* __restri
 namespace dph {
 using namespace dpk;
 
-template <class E, bool kBoth>
+template <class E, int kMode>
 static cudaError_t run_distill(const DistillParams& P, cudaStream_t s) {
   static const cudaError_t set =
-      cudaFuncSetAttribute(distill::distill_stream_kernel<E, kBoth>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      cudaFuncSetAttribute(distill::distill_stream_kernel<E, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            distill::stream_smem(distill::kMaxK));
   if (set != cudaSuccess) return set;
   // two CTAs per SM, one where many teacher entries take their shared memory
   const int smem = distill::stream_smem(P.K), per_sm = std::min(distill::kMinBlocks, 232448 / (smem + 1024));
   const unsigned grid = (unsigned)std::min<size_t>((size_t)P.B * P.T, (size_t)152 * per_sm);
-  return launch_pdl(distill::distill_stream_kernel<E, kBoth>, grid, distill::kThreads, smem, s, P);
+  return launch_pdl(distill::distill_stream_kernel<E, kMode>, grid, distill::kThreads, smem, s, P);
+}
+
+template <class E>
+static cudaError_t distill_mode(const DistillParams& P, cudaStream_t s) {
+  if (!(P.alpha > 0.f) || !P.labels) return run_distill<E, 0>(P, s);
+  return P.tau == 1.f   ? run_distill<E, 2>(P, s)
+         : P.tau == 2.f ? run_distill<E, 3>(P, s)
+         : P.tau == 4.f ? run_distill<E, 4>(P, s)
+                        : run_distill<E, 1>(P, s);
 }
 
 cudaError_t launch_distill(const DistillParams& P, int dtype, cudaStream_t s) {
-  const bool both = P.alpha > 0.f && P.labels;   // the label's softmax beside the teacher's
-  cudaError_t e = dtype == DP_BF16
-                      ? both ? run_distill<__nv_bfloat16, true>(P, s) : run_distill<__nv_bfloat16, false>(P, s)
-                      : both ? run_distill<float, true>(P, s) : run_distill<float, false>(P, s);
+  cudaError_t e = dtype == DP_BF16 ? distill_mode<__nv_bfloat16>(P, s) : distill_mode<float>(P, s);
   if (e == cudaSuccess && P.loss)
     e = launch_pdl(distill::distill_loss_kernel, (unsigned)P.B, 256, 0, s, (const float*)P.row_loss, P.T, P.loss);
   return e;

@@ -416,13 +416,14 @@ def _distill_inputs(dtype, B, T, V, K, seed=0):
 L_TOL, G_TOL = 1e-5, {"fp32": 1e-5, "bf16": 2 ** -8}
 
 
-def _distill_close(got, want, dtype):
+def _distill_close(got, want, dtype, terms=0.0):
+    """terms: the size of the gradient's terms where they may cancel to nothing (q - p with q = p)."""
     import torch
     loss, grad = got
     wl, _, wg = want
     assert ((loss.double() - wl).abs() <= L_TOL * (1 + wl.abs())).all()
     if grad is not None:
-        big = wg.abs().amax(-1, keepdim=True)
+        big = wg.abs().amax(-1, keepdim=True).clamp(min=terms)
         assert torch.isfinite(grad).all()
         assert ((grad.double() - wg).abs() <= G_TOL[dtype] * wg.abs() + 1e-6 * big + 1e-38).all()
 
@@ -475,6 +476,29 @@ def test_distill_missing_masked_and_repeated(lib, dtype, V):
     again = lib.distill_loss_and_grad(z, idx, t, labels=y, weights=w, temperature=2.0, alpha=0.25)
     assert all(torch.equal(a, b) for a, b in zip(got, again))
     assert lib.dp_check_status() == lib.DP_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("tau", [0.5, 1.0, 2.0, 3.0])
+def test_distill_rows_of_masks(lib, dtype, tau):
+    """Nothing but the type's lowest value (a uniform softmax), all but one entry, and -inf
+    instead of it; over a few chunks of a row, so that some threads see masks alone."""
+    import torch
+    V = 20011
+    z, idx, t, y = _distill_inputs(dtype, 2, 3, V, 4)
+    low = torch.finfo(z.dtype).min
+    z[0, 0], z[0, 1], z[0, 2], z[1, 0] = low, low, -float("inf"), low
+    z[0, 1, idx[0, 1, 0]] = z[0, 2, idx[0, 2, 0]] = 3.0
+    z[1, 0, ::2] = -float("inf")
+    t[0, 1, 1:] = t[0, 2, 1:] = -float("inf")
+    idx[1, 0] = torch.tensor([1, 3, 5, 7], device="cuda")
+    y[0, 1], y[0, 2], y[1, 0] = idx[0, 1, 0], idx[0, 2, 0], 9
+    kw = dict(labels=y, temperature=tau, alpha=0.25)
+    want = ref.distill(z, idx, t, y, None, None, tau, 0.25)
+    # a softmax of one entry: q and p are both 1
+    _distill_close(lib.distill_loss_and_grad(z, idx, t, **kw), want, dtype, terms=tau)
+    want = ref.distill(z, idx, t, None, None, None, tau, 0.0)
+    _distill_close(lib.distill_loss_and_grad(z, idx, t, temperature=tau), want, dtype, terms=tau)
 
 
 def test_distill_index_out_of_vocabulary(lib):
