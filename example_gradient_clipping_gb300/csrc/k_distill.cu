@@ -9,8 +9,8 @@
 // for the gradient a second pass over the row, backwards: its last chunks are still in shared
 // memory, the others mostly in L2.
 //   producer warp   the row's aligned vectors in 16 KB chunks through a ring (bulk copies)
-//   teacher warp    one row ahead: the teacher's distribution, the label, and the ends of rows
-//                   off the 16-byte grid (an odd V)
+//   teacher warps   up to three rows ahead: the teacher's distribution, the label, and the ends
+//                   of rows off the 16-byte grid (an odd V)
 //   consumers       256 threads, four 16-byte vectors of a chunk each
 // The few entries that the teacher or the label touches are written after the row, each by a
 // thread that adds up every teacher entry of the same index, so a repeated index needs no
@@ -86,7 +86,7 @@ template <class E> struct Words {
 // Exponents are formed as z ct2 - c with c rounded: exact enough while |c| stays below this.
 constexpr float kFar = 1e6f;
 
-constexpr int kNT = 256, kNW = kNT / 32, kThreads = kNT + 64;
+constexpr int kNT = 256, kNW = kNT / 32, kTeachers = 3, kThreads = kNT + 32 + 32 * kTeachers;
 constexpr int kNV = 4, kChunk = kNT * kNV, kChunkBytes = kChunk * 16;   // vectors and bytes of a chunk
 constexpr int kStages = 6, kMaxK = 1024, kMinBlocks = 2;
 
@@ -114,9 +114,9 @@ struct Ring {
     return p;
   }
 };
-// behind the ring: reductions [2][8] of (max, sums), row ends [2][2], barriers, flags; teacher
-constexpr int kFixed = 2 * kNW * 16 + 2 * 2 * 16 + (2 * kStages + 4) * 8 + 32;
-constexpr int stream_smem(int K) { return kStages * kChunkBytes + kFixed + 2 * (12 * ((K + 3) / 4 * 4) + 16); }
+// behind the ring: reductions [2][8] of (max, sums), row ends [3][2], barriers, flags; teachers
+constexpr int kFixed = 2 * kNW * 16 + kTeachers * 2 * 16 + (kStages + kTeachers) * 16 + 16;
+constexpr int stream_smem(int K) { return kStages * kChunkBytes + kFixed + kTeachers * (12 * ((K + 3) / 4 * 4) + 16); }
 
 // The consumers' barrier, true in all of them if `p` is in any.
 __device__ __forceinline__ bool bar_any(bool p) {
@@ -148,13 +148,13 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
   constexpr bool kBoth = kMode > 0;
   extern __shared__ __align__(128) uint8_t smem[];
   float4* red = reinterpret_cast<float4*>(smem + kStages * kChunkBytes);   // [2][warp] (max, sums)
-  V* edge = reinterpret_cast<V*>(red + 2 * kNW);                           // [2][first, last vector]
-  uint64_t* full = reinterpret_cast<uint64_t*>(edge + 4);
-  uint64_t *empty = full + kStages, *tfull = empty + kStages, *tempty = tfull + 2;
-  volatile int* abort = reinterpret_cast<volatile int*>(tempty + 2);
+  V* edge = reinterpret_cast<V*>(red + 2 * kNW);                           // [teacher][first, last vector]
+  uint64_t* full = reinterpret_cast<uint64_t*>(edge + 2 * kTeachers);
+  uint64_t *empty = full + kStages, *tfull = empty + kStages, *tempty = tfull + kTeachers;
+  volatile int* abort = reinterpret_cast<volatile int*>(tempty + kTeachers);
   struct Meta { int valid, bad, y; float zy; };
   const int kpad = (P.K + 3) / 4 * 4;
-  uint8_t* teacher = smem + kStages * kChunkBytes + kFixed;                // [2]{Meta, sk, sp, sz}
+  uint8_t* teacher = smem + kStages * kChunkBytes + kFixed;                // [teacher]{Meta, sk, sp, sz}
   const int tbytes = 16 + 12 * kpad;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
       ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], kNW);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kTeachers; ++s) {
       ptx::mbar_init(&tfull[s], 1);
       ptx::mbar_init(&tempty[s], kNW);
     }
@@ -177,8 +177,30 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
   const unsigned rows = (unsigned)(P.B * P.T), first = blockIdx.x, step = gridDim.x;   // < 2^31
   const E* logits = static_cast<const E*>(P.logits);
   // vector v of a row covers its entries [W v - shift, W v - shift + W), v < nvec
-  // a row's weight, asked for a row ahead
-  auto weight = [&](unsigned row) { return P.weights && row < rows ? P.weights[row] : 1.f; };
+  // This CTA's rows are first, first + step, ...; bit i of batch(n): the (n + i)-th has a weight
+  // other than 0 (or `zero`: one of 0).  Every warp looks at 32 of them at a time.
+  constexpr unsigned kEnd = ~0u;
+  const unsigned mine = first < rows ? (rows - first + step - 1) / step : 0;
+  auto batch = [&](unsigned n, bool zero) {
+    const unsigned i = n + lane;
+    const bool in = i < mine, off = in && P.weights && P.weights[first + i * step] == 0.f;
+    return __ballot_sync(0xffffffffu, in && off == zero);
+  };
+  struct Next { unsigned n = 0; uint32_t bits = 0; bool begun = false; };
+  auto next = [&](Next& it, bool zero) -> unsigned {   // the next such row, or kEnd
+    if (!it.begun) {
+      it.begun = true;
+      it.bits = batch(0, zero);
+    }
+    while (it.bits == 0) {
+      it.n += 32;
+      if (it.n >= mine) return kEnd;
+      it.bits = batch(it.n, zero);
+    }
+    const int i = __ffs((int)it.bits) - 1;
+    it.bits &= it.bits - 1;
+    return first + (it.n + i) * step;
+  };
   auto shift_of = [&](const E* z) { return (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(E)); };
   auto vectors = [&](int shift) { return (P.V + shift + W - 1) / W; };
   auto whole_end = [&](int shift) { return (P.V + shift) / W; };   // vectors from here on reach past the row
@@ -207,11 +229,8 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
       used |= 1u << s;
       __syncwarp();
     };
-    float next_w = weight(first);
-    for (unsigned row = first; row < rows && ok; row += step) {
-      const float w = next_w;
-      next_w = weight(row + step);
-      if (w == 0.f) continue;   // not read
+    Next it;
+    for (unsigned row = next(it, false); row != kEnd && ok; row = next(it, false)) {
       const E* z = logits + row * (size_t)P.ld;
       const int shift = shift_of(z), nc = (vectors(shift) + kChunk - 1) / kChunk;
       for (int c = 0; c < nc && ok; ++c) load(z, shift, c);
@@ -223,53 +242,39 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
     if (*abort && lane == 0)   // let the copies in flight land before the CTA exits
       for (int s = 0; s < kStages; ++s)
         if (used >> s & 1) ptx::mbar_wait_drain(&full[s], (ring.phases >> s & 1) ^ 1);
-  } else if (warp == kNW + 1) {   // ---- teacher
-    // a row's entries are asked for a row ahead (128 at most; more are loaded when their row comes)
-    constexpr int A = 4;
-    long long ak[A], ay = -1;
-    float at[A], aw = 1.f;
-    auto ask = [&](unsigned row) {
-      aw = weight(row);
-      if (row >= rows) return;
-      if (P.labels) ay = ld_index(P.labels, P.label_i64, row);
-#pragma unroll
-      for (int i = 0; i < A; ++i) {
-        const int j = lane + 32 * i;
-        ak[i] = j < P.K ? ld_index(P.idx, P.index_i64, (size_t)row * P.K + j) : -1;
-        at[i] = j < P.K ? ld_teacher(P, (size_t)row * P.K + j) : 0.f;
-      }
-    };
-    ask(first);
+  } else if (warp > kNW) {   // ---- teachers
+    // Each takes every kTeachers-th row, a buffer of its own: a row's chain of loads (its indices, the
+    // logits there) takes some 10^4 clk while the rows themselves stream in, two or three of them.
+    const int s = warp - kNW - 1;
+    constexpr int A = 4;   // the first 128 entries in registers while the buffer is in use
+    Next it;
     int k = 0;
-    for (unsigned row = first; row < rows; row += step) {
-      if (aw == 0.f) {
-        ask(row + step);
-        continue;
-      }
-      const int s = k & 1;
+    for (unsigned row = next(it, false); row != kEnd; row = next(it, false), ++k) {
+      if (k % kTeachers != s) continue;
       const E* z = logits + row * (size_t)P.ld;
       const int shift = shift_of(z), nvec = vectors(shift);
-      long long y = ay;
-      const bool labelled = y >= 0 && y < P.V;
-      const float zy = lane == 0 && labelled ? to_f(z[y]) : 0.f;
-      int n = 0, oob = y >= P.V;
-      int rk[A];
+      const long long y = P.labels ? ld_index(P.labels, P.label_i64, row) : -1;
+      int n = 0, oob = y >= P.V, rk[A];
       float rt[A], rz[A];
 #pragma unroll
       for (int i = 0; i < A; ++i) {
-        const bool have = ak[i] >= 0 && ak[i] < P.V;
-        oob |= ak[i] >= P.V;
-        n += have;
-        rk[i] = have ? (int)ak[i] : -1;
-        rt[i] = have ? at[i] / P.tau : -INFINITY;
-        rz[i] = have ? to_f(z[ak[i]]) : 0.f;
+        const int j = lane + 32 * i;
+        const long long kk = j < P.K ? ld_index(P.idx, P.index_i64, (size_t)row * P.K + j) : -1;
+        rt[i] = j < P.K ? ld_teacher(P, (size_t)row * P.K + j) / P.tau : 0.f;
+        oob |= kk >= P.V;
+        rk[i] = kk >= 0 && kk < P.V ? (int)kk : -1;
+      }
+      const float zy = lane == 0 && y >= 0 && y < P.V ? to_f(z[y]) : 0.f;
+#pragma unroll
+      for (int i = 0; i < A; ++i) {
+        rz[i] = rk[i] >= 0 ? to_f(z[rk[i]]) : 0.f;
+        if (rk[i] < 0) rt[i] = -INFINITY;
+        n += rk[i] >= 0;
       }
       V end;
       if (lane < 2) end.load_edge(z, lane == 0 ? -shift : W * (nvec - 1) - shift, P.V);
-      ask(row + step);
-      const bool w = ptx::mbar_wait(&tempty[s], ((k >> 1) & 1) ^ 1, abort, P.status);
+      const bool w = ptx::mbar_wait(&tempty[s], ((k / kTeachers) & 1) ^ 1, abort, P.status);
       if (!__all_sync(0xffffffffu, w)) break;
-      ++k;
       Meta* meta = reinterpret_cast<Meta*>(teacher + s * tbytes);
       int* sk = reinterpret_cast<int*>(meta + 1);
       float *sp = reinterpret_cast<float*>(sk + kpad), *sz = sp + kpad;
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
       sum = warp_sum(sum);
       const float inv = n > 0 ? 1.f / sum : 0.f;
       for (int j = lane; j < kpad; j += 32) sp[j] *= inv;
-      if (lane == 0) *meta = {n, oob, labelled ? (int)y : -1, zy};
+      if (lane == 0) *meta = {n, oob, y >= 0 && y < P.V ? (int)y : -1, zy};
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&tfull[s]);
     }
@@ -343,29 +348,21 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
     Ring ring;
     int k = 0;
     bool ok = true;
-    float next_w = weight(first);
-    for (unsigned row = first; row < rows; row += step) {
+    Next it;
+    for (unsigned row = next(it, false); row != kEnd; row = next(it, false)) {
       const E* z = logits + row * (size_t)P.ld;
       E* g = P.grad ? static_cast<E*>(P.grad) + row * (size_t)P.ldg : nullptr;
+      const float w = P.weights ? P.weights[row] : 1.f, up = P.upstream ? P.upstream[row / P.T] : 1.f;
       const int shift = shift_of(z), nvec = vectors(shift);
-      const bool gvec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
       const int a = shift > 0 ? 1 : 0, b = whole_end(shift);   // whole vectors
       const int nc = (nvec + kChunk - 1) / kChunk;
+      const bool gvec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
       auto store = [&](int v, const V& x) {
         const int e0 = W * v - shift;
         if (gvec && v >= a && v < b) *reinterpret_cast<uint4*>(g + e0) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
         else x.store_edge(g, e0, P.V);
       };
-      const float w = next_w;
-      next_w = weight(row + step);
-      if (w == 0.f) {   // not read
-        const V zero = {{0u, 0u, 0u, 0u}};
-        if (g)
-          for (int v = tid; v < nvec; v += kNT) store(v, zero);
-        if (P.row_loss && tid == 0) P.row_loss[row] = 0.f;
-        continue;
-      }
-      const int ts = k & 1;
+      const int ts = k % kTeachers;
       auto wait = [&](uint64_t* bar, int parity) {
         const bool r = ptx::mbar_wait(bar, parity & 1, abort, P.status);
         ok = __all_sync(0xffffffffu, r);
@@ -388,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
         if (lane == 0 && !keep) ptx::mbar_arrive(&empty[s]);
         return true;
       };
-      wait(&tfull[ts], k >> 1);
+      wait(&tfull[ts], k / kTeachers);
       // first pass: the thread's running maximum and the sums relative to it
       float m = -INFINITY, c = 0.f, c1 = 0.f, st = 0.f, s1 = 0.f;
       for (int j = 0; j < nc; ++j) {
@@ -476,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
       const int* sk = reinterpret_cast<const int*>(meta + 1);
       const float *sp = reinterpret_cast<const float*>(sk + kpad), *sz = sp + kpad;
       const float ct = meta->valid ? 1.f - P.alpha : 0.f, cl = meta->y >= 0 ? P.alpha : 0.f;   // the two terms
-      const float gw = w * (P.upstream ? P.upstream[row / P.T] : 1.f);
+      const float gw = w * up;
       const float at = gw * ct * P.tau / st, a1 = kBoth && cl != 0.f ? gw * cl / s1 : 0.f;
       const uint64_t cp = pair(-c, -c), c1p = pair(-c1, -c1), atp = pair(at, at), a1p = pair(a1, a1);
       auto entries = [&](uint64_t z2) {   // of the student's part of the gradient
@@ -541,6 +538,20 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&tempty[ts]);
       ++k;
+    }
+    // rows of weight 0: not read
+    Next zero;
+    for (unsigned row = P.weights ? next(zero, true) : kEnd; row != kEnd; row = next(zero, true)) {
+      if (P.row_loss && tid == 0) P.row_loss[row] = 0.f;
+      if (!P.grad) continue;
+      E* g = static_cast<E*>(P.grad) + row * (size_t)P.ldg;
+      const int shift = shift_of(g), nvec = vectors(shift);
+      const int a = shift > 0 ? 1 : 0, b = whole_end(shift);
+      const V none = {{0u, 0u, 0u, 0u}};
+      for (int v = tid; v < nvec; v += kNT) {
+        if (v >= a && v < b) *reinterpret_cast<uint4*>(g + (W * v - shift)) = make_uint4(0u, 0u, 0u, 0u);
+        else none.store_edge(g, W * v - shift, P.V);
+      }
     }
   }
 }
