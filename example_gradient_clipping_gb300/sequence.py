@@ -137,50 +137,38 @@ def _vector(x, ref, shape, dtypes, name: str) -> None:
                          f"{ref.device}, got {x.dtype} {list(x.shape)} on {x.device}")
 
 
-def _sig(x):
-    """What the checks and the descriptor look at of a tensor (never its address or values)."""
-    return None if x is None else (x.shape, x.stride(), x.dtype, x.get_device())
-
-
-# Descriptors by the signatures of a call's tensors and its options: a call like one that was
-# checked before is neither checked nor described again.
+# Descriptors by what the checks and the descriptor look at of a call's tensors (shapes, strides,
+# types and devices, never addresses or values) and by its options: a call like one that was
+# checked before is neither checked nor described again.  The calls are a few microseconds of
+# kernel at their smallest, so what is done per call is kept short.
 _descs: dict = {}
+_get, _empty, _f32 = _descs.get, torch.empty, torch.float32
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
-def _desc(key, make):
-    d = _descs.get(key)
-    if d is None:
-        if len(_descs) >= 1024:
-            _descs.clear()
-        d = _descs[key] = make()
+def _keep(key, d):
+    if len(_descs) >= 1024:
+        _descs.clear()
+    _descs[key] = d
     return d
 
 
-def _raw_stream(x, stream):
-    """Raw handle of `stream`, or of the current stream of x's device."""
-    return torch._C._cuda_getCurrentRawStream(x.get_device()) if stream is None else _stream(stream)
+def _opt(x):
+    """The key's part for an optional contiguous array."""
+    return None if x is None else (x.shape, x.stride(), x.dtype, x.get_device())
 
 
-class _on:
-    """The tensors' device made current for the call (the C side uses the current device)."""
-
-    def __init__(self, x):
-        self.idx, self.prev = x.get_device(), torch.cuda.current_device()
-
-    def __enter__(self):
-        torch.cuda.set_device(self.idx)
-
-    def __exit__(self, *_):
-        torch.cuda.set_device(self.prev)
-
-
-def _call(f, x, *args):
-    """f(*args) of the C side with x's device current."""
-    if x.get_device() == torch._C._cuda_getDevice():
-        _check(f(*args))
+def _call(f, device, stream, *args):
+    """f(*args, stream) of the C side with `device` current (the C side uses that); stream None:
+    the device's current stream."""
+    stream = _current_stream(device) if stream is None else _stream(stream)
+    if device == _current_device():
+        status = f(*args, stream)
     else:
-        with _on(x):
-            _check(f(*args))
+        with torch.cuda.device(device):
+            status = f(*args, stream)
+    if status:
+        _check(status)
 
 
 # ---- rotary ---------------------------------------------------------------------------
@@ -194,8 +182,8 @@ def rotary_table(R: int, P: int, theta: float = 10000.0, scaling: str = "plain",
     if P <= 0 or R <= 0:
         raise ValueError(f"P={P} and R={R} must be > 0")
     table = torch.empty(P, R, dtype=torch.float32, device=device)
-    _call(_lib.dp_rotary_table, table, RotaryTableDesc(P, R, _SCALINGS[scaling], theta, factor, context, slow, fast),
-          table.data_ptr(), _raw_stream(table, stream))
+    _call(_lib.dp_rotary_table, table.get_device(), stream,
+          RotaryTableDesc(P, R, _SCALINGS[scaling], theta, factor, context, slow, fast), table.data_ptr())
     return table
 
 
@@ -218,14 +206,17 @@ def _rotary_desc(q, k, table, positions, interleaved, inverse):
 
 
 def _rotary(q, k, table, positions, interleaved, inverse, stream):
-    d = _desc((_sig(q), _sig(k), _sig(table), _sig(positions), interleaved, inverse),
-              lambda: _rotary_desc(q, k, table, positions, interleaved, inverse))
-    qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ko = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k is not None else None
-    if qo.numel() == 0 and (ko is None or ko.numel() == 0):
-        return qo, ko
-    _call(_lib.dp_rotary, q, d, q.data_ptr(), _ptr(k), table.data_ptr(), _ptr(positions), qo.data_ptr(), _ptr(ko),
-          _raw_stream(q, stream))
+    shape, dtype, dev = q.shape, q.dtype, q.get_device()
+    key = (shape, q.stride(), dtype, dev, table.shape, table.stride(), table.dtype, table.get_device(), interleaved,
+           inverse, None if k is None else (k.shape, k.stride(), k.dtype, k.get_device()),
+           None if positions is None else (positions.shape, positions.stride(), positions.dtype, positions.get_device()))
+    d = _get(key) or _keep(key, _rotary_desc(q, k, table, positions, interleaved, inverse))
+    device = q.device
+    qo = _empty(shape, dtype=dtype, device=device)
+    ko = _empty(k.shape, dtype=dtype, device=device) if k is not None else None
+    if d.B * d.T * (d.Hq + d.Hk) * d.D:
+        _call(_lib.dp_rotary, dev, stream, d, q.data_ptr(), None if k is None else k.data_ptr(), table.data_ptr(),
+              None if positions is None else positions.data_ptr(), qo.data_ptr(), None if k is None else ko.data_ptr())
     return qo, ko
 
 
@@ -296,15 +287,19 @@ def attention_forward(q, k, v, causal: bool = False, window: int = 0, scale: Opt
     fp32 [B, Hq, T].  q_lens, k_lens: int32 [B], how many leading rows of each example are
     there; causal aligns the last query with the last key; window > 0 keeps the latest
     `window` keys.  scale defaults to 1/sqrt(D).  A query that sees no key gives 0 and -inf."""
-    d = _desc((_sig(q), _sig(k), _sig(v), _sig(q_lens), _sig(k_lens), causal, window, scale),
-              lambda: _attn_desc(q, k, v, q_lens, k_lens, causal, window, scale))
-    dev = q.device
-    o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    lse = torch.empty((d.B, d.Hq, d.T), dtype=torch.float32, device=dev)
-    if o.numel() == 0 or k.numel() == 0:
+    shape, dtype, dev = q.shape, q.dtype, q.get_device()
+    key = (shape, q.stride(), dtype, dev, k.shape, k.stride(), k.dtype, k.get_device(), v.shape, v.stride(), v.dtype,
+           v.get_device(), causal, window, scale, None if q_lens is None else _opt(q_lens),
+           None if k_lens is None else _opt(k_lens))
+    d = _get(key) or _keep(key, _attn_desc(q, k, v, q_lens, k_lens, causal, window, scale))
+    device = q.device
+    o = _empty(shape, dtype=dtype, device=device)
+    lse = _empty((d.B, d.Hq, d.T), dtype=_f32, device=device)
+    if not d.B * d.T * d.Hq * d.D * d.S * d.Hk:
         return o.zero_(), lse.fill_(-float("inf"))
-    _call(_lib.dp_attention, q, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(q_lens), _ptr(k_lens), o.data_ptr(),
-          lse.data_ptr(), _raw_stream(q, stream))
+    _call(_lib.dp_attention, dev, stream, d, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          None if q_lens is None else q_lens.data_ptr(), None if k_lens is None else k_lens.data_ptr(), o.data_ptr(),
+          lse.data_ptr())
     return o, lse
 
 
@@ -312,18 +307,22 @@ def attention_backward(q, k, v, o, lse, do, causal: bool = False, window: int = 
                        q_lens=None, k_lens=None, stream=None):
     """(dq, dk, dv) for the gradient `do` of attention_forward's o, the probabilities formed
     again from lse; the other arguments as in the forward call."""
-    d = _desc((_sig(q), _sig(k), _sig(v), _sig(q_lens), _sig(k_lens), causal, window, scale, _sig(o), _sig(lse), _sig(do)),
-              lambda: _attn_desc(q, k, v, q_lens, k_lens, causal, window, scale, (o, lse, do)))
-    dev = q.device
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    dv = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    if dq.numel() == 0 or dk.numel() == 0:
+    shape, dtype, dev = q.shape, q.dtype, q.get_device()
+    key = (shape, q.stride(), dtype, dev, k.shape, k.stride(), k.dtype, k.get_device(), v.shape, v.stride(), v.dtype,
+           v.get_device(), causal, window, scale, None if q_lens is None else _opt(q_lens),
+           None if k_lens is None else _opt(k_lens), o.shape, o.stride(), o.dtype, o.get_device(), lse.shape,
+           lse.stride(), lse.dtype, lse.get_device(), do.shape, do.stride(), do.dtype, do.get_device())
+    d = _get(key) or _keep(key, _attn_desc(q, k, v, q_lens, k_lens, causal, window, scale, (o, lse, do)))
+    device = q.device
+    dq = _empty(shape, dtype=dtype, device=device)
+    dk = _empty(k.shape, dtype=dtype, device=device)
+    dv = _empty(k.shape, dtype=dtype, device=device)
+    if not d.B * d.T * d.Hq * d.D * d.S * d.Hk:
         return dq.zero_(), dk.zero_(), dv.zero_()
-    ws = torch.empty(d.ws_bytes, dtype=torch.uint8, device=dev)
-    _call(_lib.dp_attention_grad, q, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-          do.data_ptr(), _ptr(q_lens), _ptr(k_lens), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), d.ws_bytes,
-          _raw_stream(q, stream))
+    ws = _empty(d.ws_bytes, dtype=torch.uint8, device=device)
+    _call(_lib.dp_attention_grad, dev, stream, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+          do.data_ptr(), None if q_lens is None else q_lens.data_ptr(), None if k_lens is None else k_lens.data_ptr(),
+          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), d.ws_bytes)
     return dq, dk, dv
 
 
@@ -371,19 +370,24 @@ def _distill_desc(logits, indices, teacher, labels, weights, upstream, temperatu
 
 
 def _distill(logits, indices, teacher, labels, weights, upstream, temperature, alpha, want_loss, want_grad, stream):
-    d = _desc((_sig(logits), _sig(indices), _sig(teacher), _sig(labels), _sig(weights), _sig(upstream), temperature,
-               alpha), lambda: _distill_desc(logits, indices, teacher, labels, weights, upstream, temperature, alpha))
-    dev = logits.device
+    shape, dtype, dev = logits.shape, logits.dtype, logits.get_device()
+    key = (shape, logits.stride(), dtype, dev, indices.shape, indices.stride(), indices.dtype, indices.get_device(),
+           teacher.shape, teacher.stride(), teacher.dtype, teacher.get_device(), temperature, alpha, _opt(labels),
+           _opt(weights), _opt(upstream))
+    d = _get(key) or _keep(key, _distill_desc(logits, indices, teacher, labels, weights, upstream, temperature, alpha))
+    device = logits.device
     loss = rows = grad = None
     if want_loss:
-        loss = torch.empty(d.B, dtype=torch.float32, device=dev)
-        rows = torch.empty((d.B, d.T), dtype=torch.float32, device=dev)
+        loss = _empty(d.B, dtype=_f32, device=device)
+        rows = _empty((d.B, d.T), dtype=_f32, device=device)
     if want_grad:
-        grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-    if logits.numel() == 0:
+        grad = _empty(shape, dtype=dtype, device=device)
+    if not d.B * d.T:
         return (loss.zero_() if want_loss else None), rows, grad
-    _call(_lib.dp_distill, logits, d, logits.data_ptr(), indices.data_ptr(), teacher.data_ptr(), _ptr(labels),
-          _ptr(weights), _ptr(upstream), _ptr(rows), _ptr(loss), _ptr(grad), _raw_stream(logits, stream))
+    _call(_lib.dp_distill, dev, stream, d, logits.data_ptr(), indices.data_ptr(), teacher.data_ptr(),
+          None if labels is None else labels.data_ptr(), None if weights is None else weights.data_ptr(),
+          None if upstream is None else upstream.data_ptr(), None if rows is None else rows.data_ptr(),
+          None if loss is None else loss.data_ptr(), None if grad is None else grad.data_ptr())
     return loss, rows, grad
 
 
