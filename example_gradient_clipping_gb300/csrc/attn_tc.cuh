@@ -32,6 +32,38 @@ __device__ __forceinline__ void load_tile(const CUtensorMap* map, uint64_t* bar,
   for (int c = 0; c < DP / 64; ++c) ptx::tma_load_4d(map, bar, dst + c * SUB, 64 * c, row, h, b);
 }
 
+// 64 columns of an accumulator's 32 lanes of this warp, times f, to rows row0 .. row0 + 31 < n of a
+// bf16 tensor (out: column 0 of its row 0; columns at or past `cols` are not stored); 0 where
+// `live` is false (per lane).  Through 4 KB of shared memory of the warp's own, so that a store
+// covers four whole rows: straight from the lanes it would touch 32 rows, 16 bytes each, and the
+// store unit, taking a row a cycle, was measured at 2000-3400 clk for a tile.
+__device__ __forceinline__ void store_rows(uint32_t acc, bool any, float f, bool live, uint8_t* stage, int lane,
+                                           __nv_bfloat16* out, long long stride, int row0, int n, int cols) {
+  float o[64];
+  if (any) {
+    ptx::tmem_ld32(acc, *reinterpret_cast<float(*)[32]>(o));
+    ptx::tmem_ld32(acc + 32, *reinterpret_cast<float(*)[32]>(o + 32));
+    ptx::tmem_wait_ld();
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (any && live)
+      v = make_uint4(pack_bf16(o[8 * q] * f, o[8 * q + 1] * f), pack_bf16(o[8 * q + 2] * f, o[8 * q + 3] * f),
+                     pack_bf16(o[8 * q + 4] * f, o[8 * q + 5] * f), pack_bf16(o[8 * q + 6] * f, o[8 * q + 7] * f));
+    *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = v;
+  }
+  __syncwarp();
+  const int q = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((q ^ (r & 7)) << 4));
+    if (row0 + r < n && 8 * q < cols) *reinterpret_cast<uint4*>(out + (row0 + r) * stride + 8 * q) = v;
+  }
+  __syncwarp();
+}
+
 // D[128, 128] = A rows . B rows over DP columns (both K-major)
 template <int DP>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {

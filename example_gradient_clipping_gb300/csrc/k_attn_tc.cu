@@ -183,8 +183,8 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
       const float2 total = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
       l += total.x + total.y;
     }
-    if (nx > 0 && ok) {
-      const bool w = ptx::mbar_wait(&o_full[x], 0, abort, P.status);
+    if (nmax > 0 && ok) {   // the products are done; without any, the query tile has at least landed
+      const bool w = ptx::mbar_wait(nx > 0 ? &o_full[x] : q_full, 0, abort, P.status);
       ok = __all_sync(0xffffffffu, w);
       ptx::tc_fence_after();
     }
@@ -192,29 +192,12 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
       const bool none = t >= lq || nx == 0 || l == 0.f;   // a query that sees no key
       const float inv = none ? 0.f : 1.f / l;
       if (P.lse && t < P.T) P.lse[((size_t)b * P.Hq + h) * P.T + t] = none ? -INFINITY : m * kLn2 + logf(l);
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(P.O) + b * P.o.b + t * P.o.t + h * P.o.h;
-#pragma unroll 1
-      for (int c = 0; c < DP; c += 32) {
-        float o[32];
-        if (nx > 0) {
-          ptx::tmem_ld32(mO + c, o);
-          ptx::tmem_wait_ld();
-        }
-        if (t < P.T) {
+      // the query tile in shared memory is done with: the warp's part of it is the staging space
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(P.O) + b * P.o.b + h * P.o.h;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (c + 8 * q < P.D) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (!none)
-                v = make_uint4(pack_bf16(o[8 * q] * inv, o[8 * q + 1] * inv),
-                               pack_bf16(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
-                               pack_bf16(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
-                               pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
-              *reinterpret_cast<uint4*>(out + c + 8 * q) = v;
-            }
-          }
-        }
-      }
+      for (int c = 0; c < DP; c += 64)
+        store_rows(mO + c, nx > 0, inv, !none, smem + x * TILE + quarter * 4096, lane, out + c, P.o.t, ta + quarter * 32,
+                   P.T, P.D - c);
     }
   } else {
     ptx::regs_dec<C::REGS_LOW>();

@@ -272,40 +272,31 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& mapX1, const CUtens
 #pragma unroll
       for (int which = kKeys ? 0 : 1; which < 2; ++which) {   // dV; dK or dQ
         const dp_strides& st = which == 0 ? P.dv : kKeys ? P.dk : P.dq;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(which == 0 ? P.dV : kKeys ? P.dK : P.dQ) + b * st.b +
-                             own * st.t + ho * st.h;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(which == 0 ? P.dV : kKeys ? P.dK : P.dQ) + b * st.b + ho * st.h;
         const float f = which == 0 ? 1.f : P.scale;
+        const int c0 = wg * 64;   // a warpgroup's columns: all 64, or its half of 128
+        if (splits == 1) {
+          // the own tiles in shared memory are done with: the warp's part of one is the staging space
+          store_rows((which == 0 ? tA1 : tA2) + lanes + c0, N > 0, f, live, sx1 + (warp - 4) * 4096, lane, out + c0, st.t,
+                     own0 + quarter * 32, nown, P.D - c0);
+          continue;
+        }
         // a split's part, unscaled: [split][b][head][row][DP]
         float4* part = reinterpret_cast<float4*>(
             (which == 0 ? sp.dv : kKeys ? sp.dk : sp.dq) +
             ((((size_t)split * P.B + b) * hown + ho) * nown + own) * DP);
 #pragma unroll 1
-        for (int c = wg * (DP / NW); c < (wg + 1) * (DP / NW); c += 32) {
+        for (int c = c0; c < c0 + 64; c += 32) {
           float o[32];
           if (N > 0) {
             ptx::tmem_ld32((which == 0 ? tA1 : tA2) + lanes + c, o);
             ptx::tmem_wait_ld();
           }
           if (own < nown) {
-            if (splits > 1) {
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                part[c / 4 + q] = live ? make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3])
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-            } else {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if (c + 8 * q < P.D) {
-                  uint4 v = make_uint4(0, 0, 0, 0);
-                  if (live)
-                    v = make_uint4(pack_bf16(o[8 * q] * f, o[8 * q + 1] * f),
-                                   pack_bf16(o[8 * q + 2] * f, o[8 * q + 3] * f),
-                                   pack_bf16(o[8 * q + 4] * f, o[8 * q + 5] * f),
-                                   pack_bf16(o[8 * q + 6] * f, o[8 * q + 7] * f));
-                  *reinterpret_cast<uint4*>(out + c + 8 * q) = v;
-                }
-              }
-            }
+            for (int q = 0; q < 8; ++q)
+              part[c / 4 + q] = live ? make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3])
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
           }
         }
       }
@@ -554,6 +545,7 @@ static cudaError_t run_grad(const AttnParams& P, const attntc::GradSplit& sp, co
 }
 
 cudaError_t launch_attn_tc_grad(const AttnParams& P, float* ws, cudaStream_t s) {
+  if (attn_tc_short_supported(P)) return launch_attn_tc_short_grad(P, s);
   CUtensorMap q[2], k[2];   // Q and dO, K and V
   if (!map_heads(&q[0], P.Q, P.q, P.B, P.T, P.Hq, P.D, 64) || !map_heads(&q[1], P.dO, P.d_o, P.B, P.T, P.Hq, P.D, 64) ||
       !map_heads(&k[0], P.K, P.k, P.B, P.S, P.Hk, P.D, 64) || !map_heads(&k[1], P.V, P.v, P.B, P.S, P.Hk, P.D, 64))

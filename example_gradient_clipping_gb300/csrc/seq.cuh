@@ -147,6 +147,9 @@ cudaError_t launch_attn_simt_grad(const dpk::AttnParams& P, int dtype, cudaStrea
 bool attn_tc_fwd_supported(const dpk::AttnParams& P, int dtype);
 bool attn_tc_grad_supported(const dpk::AttnParams& P, int dtype);
 cudaError_t launch_attn_tc_fwd(const dpk::AttnParams& P, cudaStream_t s);
+// Short sequences (what attn_tc_grad_supported takes, and T, S <= 256, D <= 64, Hq = Hk).
+bool attn_tc_short_supported(const dpk::AttnParams& P);
+cudaError_t launch_attn_tc_short_grad(const dpk::AttnParams& P, cudaStream_t s);
 // ws: attn_tc_grad_floats(P) floats, 16-byte aligned.
 size_t attn_tc_grad_floats(const dpk::AttnParams& P);
 cudaError_t launch_attn_tc_grad(const dpk::AttnParams& P, float* ws, cudaStream_t s);

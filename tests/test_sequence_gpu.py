@@ -168,6 +168,16 @@ ATTENTION = [  # B, T, S, Hq, Hk, D, causal, window, lengths
     (1, 65, 70, 2, 2, 33, True, 0, None),
     (2, 70, 65, 2, 1, 1, False, 0, None),
     (2, 260, 260, 2, 2, 120, False, 0, None),
+    # enough heads for two query tiles a CTA, one of them without a key or without a query
+    (80, 257, 129, 1, 1, 128, True, 0, None),
+    (80, 300, 300, 1, 1, 128, True, 0, "ragged"),
+    # short sequences with a key head for every query head: a kernel of their own
+    (5, 200, 256, 2, 2, 64, True, 0, "ragged"),
+    (4, 256, 130, 3, 3, 48, True, 60, "ragged"),
+    (5, 256, 256, 2, 2, 64, False, 0, "ragged"),
+    (2, 256, 256, 2, 2, 64, True, 0, None),
+    (2, 140, 120, 2, 2, 56, True, 0, None),
+    (2, 120, 140, 2, 2, 64, True, 1, None),
     # few heads: the gradient's sums are split over CTAs and joined
     (1, 1500, 1500, 4, 1, 128, True, 0, None),
     (1, 900, 1300, 1, 1, 64, False, 0, None),
@@ -184,8 +194,8 @@ def _attn_inputs(B, T, S, Hq, Hk, D, lengths, dtype, seed=0):
                    for n, h in ((T, Hq), (S, Hk), (S, Hk), (T, Hq)))
     lq = lk = None
     if lengths:
-        lq = torch.tensor([T, 0, 1, T // 2 + 1, T - 1][:B], dtype=torch.int32, device="cuda")
-        lk = torch.tensor([S - 1, S, 0, S // 3 + 1, 1][:B], dtype=torch.int32, device="cuda")
+        lq = torch.tensor(([T, 0, 1, T // 2 + 1, T - 1] * B)[:B], dtype=torch.int32, device="cuda")
+        lk = torch.tensor(([S - 1, S, 0, S // 3 + 1, 1] * B)[:B], dtype=torch.int32, device="cuda")
     return q, k, v, do, lq, lk
 
 
@@ -213,10 +223,10 @@ def test_attention(lib, case, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("junk", [float("nan"), float("inf"), -float("inf"), 3.38e38])
-@pytest.mark.parametrize("D", [64, 128])
-def test_attention_padded_rows_may_hold_anything(lib, dtype, junk, D):
+@pytest.mark.parametrize("D,T,S,Hk", [(64, 150, 270, 1), (128, 150, 270, 1), (64, 150, 220, 2)])
+def test_attention_padded_rows_may_hold_anything(lib, dtype, junk, D, T, S, Hk):
     import torch
-    B, T, S, Hq, Hk = 5, 150, 270, 2, 1
+    B, Hq = 5, 2
     q, k, v, do, lq, lk = _attn_inputs(B, T, S, Hq, Hk, D, "ragged", dtype)
     kw = dict(causal=True, q_lens=lq, k_lens=lk)
     clean_o, clean_l = lib.attention_forward(q, k, v, **kw)
