@@ -144,10 +144,11 @@ dp_status dp_attention_grad(const dp_attn_desc* d, const void* Q, const void* K,
   P.q_lens = q_lens; P.k_lens = k_lens; P.dQ = dQ; P.dK = dK; P.dV = dV;
   float* delta = static_cast<float*>(workspace);
   P.delta = delta;
+  const bool tc = dph::attn_tc_grad_supported(P, d->dtype);
+  if (tc && dph::attn_tc_short_supported(P)) return launched(dph::launch_attn_tc_short_grad(P, stream), "dp_attention_grad");
   cudaError_t e = dph::launch_attn_delta(P, d->dtype, delta, stream);
   if (e == cudaSuccess)
-    e = dph::attn_tc_grad_supported(P, d->dtype) ? dph::launch_attn_tc_grad(P, delta + delta_floats(P), stream)
-                                                 : dph::launch_attn_simt_grad(P, d->dtype, stream);
+    e = tc ? dph::launch_attn_tc_grad(P, delta + delta_floats(P), stream) : dph::launch_attn_simt_grad(P, d->dtype, stream);
   return launched(e, "dp_attention_grad");
 }
 

@@ -545,7 +545,6 @@ static cudaError_t run_grad(const AttnParams& P, const attntc::GradSplit& sp, co
 }
 
 cudaError_t launch_attn_tc_grad(const AttnParams& P, float* ws, cudaStream_t s) {
-  if (attn_tc_short_supported(P)) return launch_attn_tc_short_grad(P, s);
   CUtensorMap q[2], k[2];   // Q and dO, K and V
   if (!map_heads(&q[0], P.Q, P.q, P.B, P.T, P.Hq, P.D, 64) || !map_heads(&q[1], P.dO, P.d_o, P.B, P.T, P.Hq, P.D, 64) ||
       !map_heads(&k[0], P.K, P.k, P.B, P.S, P.Hk, P.D, 64) || !map_heads(&k[1], P.V, P.v, P.B, P.S, P.Hk, P.D, 64))

@@ -4,7 +4,7 @@
 //   S = scale Q K^T,  P = exp2(S log2e - lse log2e),  dP = dO V^T,  dS = P * (dP - delta),
 //   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
 //
-// Up to two tiles of 128 keys by two of 128 queries: Q, K, V and dO are read once into shared memory
+// Up to two tiles of 128 keys by two of 128 queries: Q, K, V, dO and O are read once into shared memory
 // and all three gradients accumulate in tensor memory (S and dP 128 columns each, dV and dK 64,
 // dQ 64 for each of two query tiles: all 512), so a pair of tiles costs five products where the
 // kernel for any length forms seven, and those in full 128-wide instructions: at D = 64 that
@@ -12,9 +12,9 @@
 // Rows are keys: S^T = K Q^T and dP^T = V dO^T; P^T and dS^T go back to tensor memory over the
 // scores they came from as the A operands of dV and dK; dS^T also to shared memory, where its
 // 128-byte rows of queries are dQ's A operand with M contiguous.
-//   warp 0     TMA, everything at once, a barrier per tile
+//   warps 0, 2, 3  TMA, everything at once, a barrier per tile; warp 2: lse into shared memory too
 //   warp 1     MMA issuer: [P ready] dV, next S, [dS ready] dK, dQ, next dP
-//   warp 2     lse and delta of the head's queries into shared memory
+//              (delta = dO . O is formed by the softmax threads while the tiles land)
 //   warps 4-11 two warpgroups, a thread per key and 64 of the tile's 128 queries
 // dV and dK of a key tile are stored by the warpgroups once they have the next tile's P ready.
 #include <algorithm>
@@ -26,9 +26,9 @@ namespace attntc {
 namespace shortseq {
 
 constexpr int DP = 64, TILE = SUB, DSB = 2 * SUB, THREADS = 384;
-constexpr int BARS = 8 + 9;
+constexpr int BARS = 10 + 9;
 constexpr int STAGE = 8 * 4096;   // of each softmax warp, for its stores
-constexpr int SMEM = 8 * TILE + DSB + STAGE + 2 * 256 * 4 + BARS * 8 + 16;
+constexpr int SMEM = 10 * TILE + DSB + STAGE + 2 * 256 * 4 + BARS * 8 + 16;
 constexpr int REGS_LOW = 56, REGS_HIGH = 224;
 static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= THREADS * 168, "register split");
 static_assert(SMEM + 1024 <= 233472, "shared memory");
@@ -50,13 +50,13 @@ struct Pairs {
 __global__ void __launch_bounds__(THREADS, 1)
 attn_tc_short_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapG,
                           const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-                          AttnParams P) {
+                          const __grid_constant__ CUtensorMap mapO, AttnParams P) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *sq = smem, *sg = sq + 2 * TILE, *sk = sg + 2 * TILE, *sv = sk + 2 * TILE, *sds = sv + 2 * TILE,
+  uint8_t *sq = smem, *sg = sq + 2 * TILE, *sk = sg + 2 * TILE, *sv = sk + 2 * TILE, *so = sv + 2 * TILE, *sds = so + 2 * TILE,
           *stage = sds + DSB;
   float* aux = reinterpret_cast<float*>(stage + STAGE);   // -lse log2e, then -delta, of 256 queries
-  uint64_t* landed = reinterpret_cast<uint64_t*>(aux + 512);   // Q0 Q1 G0 G1 K0 K1 V0 V1
-  uint64_t *aux_full = landed + 8, *s_full = aux_full + 1, *s_done = s_full + 1, *dp_full = s_done + 1,
+  uint64_t* landed = reinterpret_cast<uint64_t*>(aux + 512);   // Q0 Q1 G0 G1 K0 K1 V0 V1 O0 O1
+  uint64_t *aux_full = landed + 10, *s_full = aux_full + 1, *s_done = s_full + 1, *dp_full = s_done + 1,
            *ds_ready = dp_full + 1, *ds_free = ds_ready + 1, *acc_full = ds_free + 1, *dq_full = acc_full + 1,
            *drain = dq_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -65,7 +65,7 @@ attn_tc_short_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid
   const int b = (int)blockIdx.x / P.Hq, h = (int)blockIdx.x - b * P.Hq;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 8; ++i) ptx::mbar_init(&landed[i], 1);
+    for (int i = 0; i < 10; ++i) ptx::mbar_init(&landed[i], 1);
     ptx::mbar_init(aux_full, 1);
     ptx::mbar_init(s_full, 1);
     ptx::mbar_init(s_done, 8);
@@ -81,6 +81,7 @@ attn_tc_short_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid
     ptx::prefetch_tensormap(&mapG);
     ptx::prefetch_tensormap(&mapK);
     ptx::prefetch_tensormap(&mapV);
+    ptx::prefetch_tensormap(&mapO);
   }
   if (warp == 1) ptx::tmem_alloc(tmem_slot, 512);
   ptx::tc_fence_before();
@@ -115,6 +116,23 @@ attn_tc_short_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid
       if (wg == 0) store(tdV, P.dV, P.dv, kt * BT, lk, P.S, 1.f, any);
       else store(tdK, P.dK, P.dk, kt * BT, lk, P.S, P.scale, any);
     };
+    // delta of the query tile with this warpgroup's number, a thread per query
+    if (lk > 0 && wg < nq && wait(&landed[2 + wg], 0) && wait(&landed[8 + wg], 0)) {
+      float x = 0.f;
+      const int at = wg * TILE + row * 128;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int o = at + ((q ^ (row & 7)) << 4);
+        const Pack<__nv_bfloat16, 8> g8 = *reinterpret_cast<const Pack<__nv_bfloat16, 8>*>(sg + o);
+        const Pack<__nv_bfloat16, 8> o8 = *reinterpret_cast<const Pack<__nv_bfloat16, 8>*>(so + o);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x = fmaf(g8.get(c), o8.get(c), x);
+      }
+      aux[256 + wg * BT + row] = wg * BT + row < lq ? -x : 0.f;   // (a row past the length may hold anything)
+    } else {
+      aux[256 + wg * BT + row] = 0.f;
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
     int i = 0, pending = -1, accs = 0;   // tiles so far; key tile whose dV and dK wait in tensor memory; how many did
     uint32_t queries = 0;                // query tiles that some key tile met
     for (int kt = 0; kt < 2 && ok; ++kt) {
@@ -225,50 +243,50 @@ attn_tc_short_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid
     }
   } else {
     ptx::regs_dec<REGS_LOW>();
-    if (warp == 0) {
+    if (warp != 1) {
+      // three issuing warps (one moves ~48 B/clk): K and Q; O; V and dO
+      const CUtensorMap *m0 = warp == 0 ? &mapK : warp == 2 ? &mapO : &mapV, *m1 = warp == 0 ? &mapQ : &mapG;
+      uint8_t *d0 = warp == 0 ? sk : warp == 2 ? so : sv, *d1 = warp == 0 ? sq : sg;
+      const int b0 = warp == 0 ? 4 : warp == 2 ? 8 : 6, b1 = warp == 0 ? 0 : 2, n0 = warp == 2 ? lq : lk;
+      const bool two = warp != 2;
       if (lq > 0 && lk > 0 && ptx::elect_one()) {
         auto load = [&](const CUtensorMap* map, int bar, uint8_t* dst, int row) {
           ptx::mbar_arrive_expect_tx(&landed[bar], TILE);
           ptx::tma_load_4d(map, &landed[bar], dst, 0, row, h, b);
         };
         for (int t = 0; t < 2; ++t) {
-          if (t * BT < lk) load(&mapK, 4 + t, sk + t * TILE, t * BT);
-          if (t * BT < lq) load(&mapQ, t, sq + t * TILE, t * BT);
-          if (t * BT < lk) load(&mapV, 6 + t, sv + t * TILE, t * BT);
-          if (t * BT < lq) load(&mapG, 2 + t, sg + t * TILE, t * BT);
+          if (t * BT < n0) load(m0, b0 + t, d0 + t * TILE, t * BT);
+          if (two && t * BT < lq) load(m1, b1 + t, d1 + t * TILE, t * BT);
         }
       }
       __syncwarp();
+      if (warp == 2) {
+        const size_t at = ((size_t)b * P.Hq + h) * P.T;
+        float l[8];   // all loads in flight at once
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l[i] = lane + 32 * i < lq ? P.lse[at + lane + 32 * i] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) aux[lane + 32 * i] = -l[i] * kLog2e;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(aux_full);
+      }
       // every copy lands before the CTA exits, also those of tiles that no pair takes
       if (lq > 0 && lk > 0 && lane == 0)
         for (int t = 0; t < 2; ++t) {
-          if (t * BT < lq) {
-            ptx::mbar_wait_drain(&landed[t], 0);
-            ptx::mbar_wait_drain(&landed[2 + t], 0);
-          }
-          if (t * BT < lk) {
-            ptx::mbar_wait_drain(&landed[4 + t], 0);
-            ptx::mbar_wait_drain(&landed[6 + t], 0);
-          }
+          if (t * BT < n0) ptx::mbar_wait_drain(&landed[b0 + t], 0);
+          if (two && t * BT < lq) ptx::mbar_wait_drain(&landed[b1 + t], 0);
         }
       __syncwarp();
-    } else if (warp == 2) {
-      const size_t at = ((size_t)b * P.Hq + h) * P.T;
-      float l[8], d[8];   // all loads in flight at once
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int t = lane + 32 * i;
-        l[i] = t < lq ? P.lse[at + t] : 0.f;
-        d[i] = t < lq ? P.delta[at + t] : 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        aux[lane + 32 * i] = -l[i] * kLog2e;
-        aux[256 + lane + 32 * i] = -d[i];
-      }
+      // the head that follows on an SM, into L2: its copies then come without HBM's latency, which
+      // nothing else here hides (one CTA per SM)
+      const int nb = ((int)blockIdx.x + 152) / P.Hq, nh = ((int)blockIdx.x + 152) - nb * P.Hq;
+      if (nb < P.B && ptx::elect_one())
+        for (int t = 0; t < 2; ++t) {
+          if (t * BT < (warp == 2 ? P.T : P.S)) ptx::tma_prefetch_4d(m0, 0, t * BT, nh, nb);
+          if (two && t * BT < P.T) ptx::tma_prefetch_4d(m1, 0, t * BT, nh, nb);
+        }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(aux_full);
-    } else if (warp == 1) {
+    } else {
       constexpr uint32_t idesc = ptx::idesc_bf16_f32(BT, DP, 0, 1), idesc_q = ptx::idesc_bf16_f32(BT, DP, 1, 1);
       const uint32_t q = ptx::smem_u32(sq), g = ptx::smem_u32(sg), k = ptx::smem_u32(sk), v = ptx::smem_u32(sv),
                      ds = ptx::smem_u32(sds);
@@ -393,7 +411,7 @@ namespace dph {
 using namespace dpk;
 
 bool attn_tc_short_supported(const AttnParams& P) {
-  return P.D <= 64 && P.T <= 256 && P.S <= 256 && P.Hq == P.Hk;
+  return P.D <= 64 && P.T <= 256 && P.S <= 256 && P.Hq == P.Hk && tma_ok(P.O, P.o, P.B, P.T, P.Hq);
 }
 
 cudaError_t launch_attn_tc_short_grad(const AttnParams& P, cudaStream_t s) {
@@ -401,11 +419,12 @@ cudaError_t launch_attn_tc_short_grad(const AttnParams& P, cudaStream_t s) {
   static const cudaError_t set =
       cudaFuncSetAttribute(ns::attn_tc_short_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ns::SMEM);
   if (set != cudaSuccess) return set;
-  CUtensorMap q, g, k, v;
+  CUtensorMap q, g, k, v, o;
   if (!map_heads(&q, P.Q, P.q, P.B, P.T, P.Hq, P.D) || !map_heads(&g, P.dO, P.d_o, P.B, P.T, P.Hq, P.D) ||
-      !map_heads(&k, P.K, P.k, P.B, P.S, P.Hk, P.D) || !map_heads(&v, P.V, P.v, P.B, P.S, P.Hk, P.D))
+      !map_heads(&k, P.K, P.k, P.B, P.S, P.Hk, P.D) || !map_heads(&v, P.V, P.v, P.B, P.S, P.Hk, P.D) ||
+      !map_heads(&o, P.O, P.o, P.B, P.T, P.Hq, P.D))
     return cudaErrorInvalidValue;
-  return launch_pdl(ns::attn_tc_short_grad_kernel, (unsigned)(P.B * P.Hq), ns::THREADS, ns::SMEM, s, q, g, k, v, P);
+  return launch_pdl(ns::attn_tc_short_grad_kernel, (unsigned)(P.B * P.Hq), ns::THREADS, ns::SMEM, s, q, g, k, v, o, P);
 }
 
 }  // namespace dph

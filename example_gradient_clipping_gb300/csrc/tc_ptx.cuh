@@ -110,6 +110,13 @@ __device__ __forceinline__ void tma_load_4d(const CUtensorMap* map, uint64_t* ba
       : "memory");
 }
 
+// The same box into L2 only.
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(x), "r"(y),
+               "r"(z), "r"(w)
+               : "memory");
+}
+
 // TMA im2col load from an NHWC tensor: the pixels of one column (walking W, then H,
 // then N from the start pixel (w, h, n) inside the map's bounding box), each shifted by
 // the filter tap (ow, oh), channels c .. c + channelsPerPixel; zero outside the tensor.
