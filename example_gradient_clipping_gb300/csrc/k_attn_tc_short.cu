@@ -17,6 +17,9 @@
 //              (delta = dO . O is formed by the softmax threads while the tiles land)
 //   warps 4-11 two warpgroups, a thread per key and 64 of the tile's 128 queries
 // dV and dK of a key tile are stored by the warpgroups once they have the next tile's P ready.
+// ViT layer (B = 64, T = 197, H = 12): 87 us (the kernel for any length with its delta pass 119), 14 us a
+// CTA: 5 until its tiles have landed (126 KB per SM at once is HBM's rate), 2 a pair of tiles, 2.5 for
+// the last stores; 768 CTAs are 5.05 waves of 152.
 #include <algorithm>
 
 #include "attn_tc.cuh"

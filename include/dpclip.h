@@ -307,8 +307,9 @@ dp_status dp_clipped_sum_kept_noised(const dp_layer_desc* desc, const float* gra
                                      float* dW, float* db, int accumulate, const dp_noise_desc* noise,
                                      void* workspace, size_t ws_bytes, cudaStream_t stream);
 
-/* Synchronizes `stream`, returns the device status word (DP_OK, DP_ERR_NONFINITE or
- * DP_ERR_TIMEOUT) raised since the last check, and clears it. */
+/* Synchronizes `stream`, returns the device status word (DP_OK, DP_ERR_NONFINITE,
+ * DP_ERR_TIMEOUT, or DP_ERR_INVALID_ARG for a position or index in device memory out of its
+ * range, dpclip_seq.h) raised since the last check, and clears it. */
 dp_status dp_check_status(cudaStream_t stream);
 
 /* Diagnostic of the device-side failure path.  Launches (asynchronously, on `stream`)
