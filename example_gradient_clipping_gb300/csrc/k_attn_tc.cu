@@ -7,7 +7,7 @@
 // products while another tile's softmax runs: the CTA's own other tile (NT = 2, D > 64: both share
 // the K and V tiles' copies), or that of the SM's second CTA (NT = 1: half an SM each; D <= 64,
 // where the shorter products leave more of a CTA's beginning and end to hide: ViT layer 48 -> 41 us,
-// T = 1024 causal 45 -> 41 us; at D = 128 and T = 4096 118 against 120 us the other way).
+// T = 1024 causal 45 -> 41 us when it was taken).
 //   warp 0     TMA: Q once, then K and V tiles of 128 keys through a ring of slots
 //   warp 1     MMA issuer: S = Q K^T (both from shared memory), O += P V with P read from
 //              tensor memory, where it overlays the S it was made from
@@ -16,9 +16,9 @@
 // The reference m follows the row's maximum lazily: only when the maximum has grown past it
 // by 8 (P up to 256, exact in the fp32 sums and no worse rounded in bf16) are O and l
 // rescaled, so after the first tiles nearly no tile touches O.
-// Bound by the chain scores - softmax - product of each tile, the tensor pipe 58% busy: causal T = 8192,
-// 32 query heads over 8, D = 128 397 us, 1.38 PFLOP/s (0.73 of the measured bf16 rate); T = 4096, 16
-// over 4 115 us (1.19 PFLOP/s); ViT layer (B = 64, T = 197, H = 12, D = 64) 39.5 us.
+// Bound by the chain scores - softmax - product of each tile: causal T = 8192, 32 query heads over 8,
+// D = 128 392 us, 1.40 PFLOP/s (0.74 of cuBLAS's measured bf16 rate); T = 4096, B = 2, 16 over 4 112 us
+// (1.23 PFLOP/s); ViT layer (B = 64, T = 197, H = 12, D = 64) 38 us.
 // Rows of V past the keys' length may hold anything: the issuing warp zeroes them in shared
 // memory before the product (0 * NaN); K's only reach scores that the mask replaces.
 #include <algorithm>
@@ -31,7 +31,8 @@ namespace attntc {
 template <int DP, int NT> struct Fwd {
   static constexpr int TILE = DP / 64 * SUB;
   // key/value slots: what fits beside the query tiles (NT = 1: of half an SM)
-  static constexpr int SLOTS = NT == 2 ? (DP == 128 ? 4 : 6) : (DP == 128 ? 2 : 4);
+  static_assert(NT == 1 || DP == 128, "two tiles a CTA: D > 64");
+  static constexpr int SLOTS = NT == 2 ? 4 : DP == 128 ? 2 : 4;
   static constexpr int THREADS = 128 + 128 * NT;
   static constexpr int SMEM = (NT + SLOTS) * TILE + 1024 + 256;
   static constexpr uint32_t TCOLS = NT == 2 ? 512 : 256;
@@ -131,10 +132,15 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
       // some entry of the tile is hidden: past the keys, after the query, before its window
       if (k0 + BT > lk || (P.causal && k0 + BT - 1 > ta + e) || (P.window && k0 <= ta + BT - 1 + e - P.window)) {
         const int hi = (P.causal ? min(lk - 1, t + e) : lk - 1) - k0;
-        const int lo = (P.window ? t + e - P.window + 1 : 0) - k0;
 #pragma unroll
         for (int c = 0; c < BT; ++c)
-          if (c > hi || c < lo) s[c] = -INFINITY;
+          if (c > hi) s[c] = -INFINITY;
+        if (P.window) {
+          const int lo = t + e - P.window + 1 - k0;
+#pragma unroll
+          for (int c = 0; c < BT; ++c)
+            if (c < lo) s[c] = -INFINITY;
+        }
       }
       float top[8];   // eight chains
 #pragma unroll
@@ -326,8 +332,13 @@ cudaError_t launch_attn_tc_fwd(const AttnParams& P, cudaStream_t s) {
       !map_heads(&mv, P.V, P.v, P.B, P.S, P.Hk, P.D))
     return cudaErrorInvalidValue;
   if (P.D <= 64) return run_fwd<64, 1>(P, mq, mk, mv, s);
-  // two tiles a CTA where their pairs still fill the SMs
-  const bool pair = P.T > attntc::BT && (size_t)P.B * P.Hq * ((P.T + 2 * attntc::BT - 1) / (2 * attntc::BT)) >= 152;
+  // Two tiles a CTA where there are pairs for two fifths of the SMs; a causal pair's tiles end at
+  // different keys, which only long sequences hide, and under a window hardly share any (us, two tiles
+  // a CTA against one.  Not causal: 1 x 2048 with 16 heads 30.1 and 32.5, 1 x 512 with 8 10.7 and 10.4,
+  // 8 x 1024 with 16 74 and 78; causal: the same 31.3 and 31.7, 11.5 and 10.2, 54.9 and 53.5, 1 x 4096
+  // with 16 56.0 and 58.2; windows: 256 of 1 x 4096 27.2 and 23.4, 512 of 1 x 8192 126 and 105)
+  const size_t pairs = (size_t)P.B * P.Hq * ((P.T + 2 * attntc::BT - 1) / (2 * attntc::BT));
+  const bool pair = P.T > attntc::BT && pairs >= 64 && !P.window && (P.T >= 2048 || !P.causal);
   return pair ? run_fwd<128, 2>(P, mq, mk, mv, s) : run_fwd<128, 1>(P, mq, mk, mv, s);
 }
 

@@ -22,9 +22,9 @@
 // (measured at D = 128: 64-row tiles taken in turn by two warpgroups, 105 clk per MMA of N = 64,
 // 2500 clk a tile; P through shared memory, two stages of both tiles: 4250 clk per 128 rows, a
 // quarter of them waiting for the copies.)
-// Causal T = 4096, B = 2, 16 query heads over 4, D = 128: 363 us, the tensor pipe 57% busy, 0.94 PFLOP/s
-// counting the five products a gradient needs (1.32 of the seven formed); T = 8192, 32 over 8 1.32 ms
-// (1.04 and 1.46).  What is left is the chain S - P - dS of a single S buffer and each CTA's first
+// Causal T = 4096, B = 2, 16 query heads over 4, D = 128, with the delta pass before it: 370 us, 0.93
+// PFLOP/s counting the five products a gradient needs (1.30 of the seven formed); T = 8192, 32 over 8
+// 1.32-1.34 ms (1.04 and 1.46).  What is left is the chain S - P - dS of a single S buffer and each CTA's first
 // copies and last stores (B = 8, T = 1024, H = 16: 0.44 PFLOP/s).
 //   warps 0, 3  TMA: own tiles and Y1; Y2 (one warp moves ~48 B/clk, a tile pair needs more)
 //   warp 1      MMA issuer
@@ -507,7 +507,9 @@ bool attn_tc_grad_supported(const AttnParams& P, int dtype) {
 
 // Splits of the own sides' sums: where the longest CTA would outlast an even share of all the work
 // (few heads, or many query heads on one key head), its tiles are dealt to several CTAs whose fp32
-// parts go to the workspace and are added in order.  No CTA gets fewer than four tiles.
+// parts go to the workspace and are added in order.  No CTA gets fewer than four tiles.  (Gradient in
+// us, split against whole: 1 x 2048 with 8 query heads on one, D = 128 77 and 213; 1 x 4096 with 4 on
+// one, D = 64 114 and 330; causal 8 on 2 at 4096 131 and 220; 4 heads of 1024 at D = 64 24 and 27.)
 static attntc::GradSplit grad_split(const AttnParams& P) {
   const int BO = P.D <= 64 ? 64 : 128;
   const double tk = (P.S + attntc::BT - 1) / attntc::BT, tq = (P.T + attntc::BT - 1) / attntc::BT;   // own tiles

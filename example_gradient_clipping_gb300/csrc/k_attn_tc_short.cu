@@ -17,9 +17,11 @@
 //              (delta = dO . O is formed by the softmax threads while the tiles land)
 //   warps 4-11 two warpgroups, a thread per key and 64 of the tile's 128 queries
 // dV and dK of a key tile are stored by the warpgroups once they have the next tile's P ready.
-// ViT layer (B = 64, T = 197, H = 12): 87 us (the kernel for any length with its delta pass 119), 14 us a
-// CTA: 5 until its tiles have landed (126 KB per SM at once is HBM's rate), 2 a pair of tiles, 2.5 for
-// the last stores; 768 CTAs are 5.05 waves of 152.
+// Bound by each CTA's chain of steps, one CTA per SM.  ViT layer (B = 64, T = 197, H = 12) 80 us (the
+// kernel for any length with its delta pass 119): 768 CTAs in 5.05 waves of 152, a fifth of a CTA's time
+// until its tiles have landed (126 KB per SM at once), then some 4000 clk a pair of tiles.  Fewer heads:
+// 4 x 33 with 12 heads 6.5 us against 9.8, 8 x 197 13.8 against 22.8; a single example of 256 12.9
+// against 12.1 (12 CTAs), which no rule of its own is made for.
 #include <algorithm>
 
 #include "attn_tc.cuh"
@@ -166,14 +168,16 @@ attn_tc_short_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid
           p[4 * c + 2] = ex2(y.x);
           p[4 * c + 3] = ex2(y.y);
         }
-        // queries [clo, chi] of these 64 see this key; `masked`: some pair of the tile is hidden
+        // queries [clo, chi] of these 64 see this key; `masked`: a causal or window edge crosses the
+        // tile.  Queries past the length have P = 0 already (-lse = -inf), keys past it are zeroed as
+        // packed words: selects for every edge tile cost 600 clk a tile (ViT layer 87 us, now 80).
         const int k1 = kt * BT;
-        const bool masked = o0 + 64 > lq || k1 + BT > lk || (P.causal && k1 + BT - 1 > o0 + e) ||
-                            (P.window && k1 <= o0 + 63 + e - P.window);
+        const bool masked = (P.causal && k1 + BT - 1 > o0 + e) || (P.window && k1 <= o0 + 63 + e - P.window);
+        const bool tail = k1 + BT > lk, dead = own >= lk;
         int clo = 0, chi = 64;
         if (masked) {
           clo = (P.causal ? own - e : 0) - o0;
-          chi = own < lk ? (P.window ? min(lq - 1, own - e + P.window - 1) : lq - 1) - o0 : -1;
+          chi = (P.window ? min(lq - 1, own - e + P.window - 1) : lq - 1) - o0;
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             if (c < clo || c > chi) p[c] = 0.f;
@@ -182,6 +186,10 @@ attn_tc_short_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid
           uint32_t u[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) u[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
+          if (tail) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) u[c] = dead ? 0u : u[c];
+          }
           ptx::tmem_st32(tS + lanes + wg * 64, u);
           ptx::tmem_wait_st();
         }
@@ -220,6 +228,10 @@ attn_tc_short_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid
         uint32_t u[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) u[c] = pack_bf16(d[2 * c], d[2 * c + 1]);
+        if (tail) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) u[c] = dead ? 0u : u[c];
+        }
         ptx::tmem_st32(tdP + lanes + wg * 64, u);
         if (i > 0 && !wait(ds_free, i - 1)) break;   // dQ has read the tile before
         uint8_t* dst = sds + wg * SUB + row * 128;
@@ -269,7 +281,7 @@ attn_tc_short_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid
 #pragma unroll
         for (int i = 0; i < 8; ++i) l[i] = lane + 32 * i < lq ? P.lse[at + lane + 32 * i] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) aux[lane + 32 * i] = -l[i] * kLog2e;
+        for (int i = 0; i < 8; ++i) aux[lane + 32 * i] = lane + 32 * i < lq ? -l[i] * kLog2e : -INFINITY;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(aux_full);
       }

@@ -16,10 +16,10 @@
 // thread that adds up every teacher entry of the same index, so a repeated index needs no
 // atomics and the result does not depend on any order.
 // Bound by HBM, with long vocabularies also by the second pass's misses in L2: bf16, 8192 rows of
-// 131072 (0.71 of them of weight 1) loss and gradient 690-700 us, 5.1 TB/s or 0.76 of a copy's rate;
+// 131072 (0.64 of them of weight 1) loss and gradient 690-700 us, 5.1 TB/s or 0.76 of a copy's rate;
 // 4096 x 32768 loss alone 45 us (3.8 TB/s); 2048 x 50257 with labels at tau = 2 80 us (4.2 TB/s).
 // (A row spread over a cluster's registers, read once, waited 3-4 us a row for the exchange of
-// its sums and ran at half the speed; three passes from global memory took 3512 us instead of 690.)
+// its sums and ran at half the speed.)
 #include <algorithm>
 
 #include "seq.cuh"
@@ -91,8 +91,9 @@ constexpr float kFar = 1e6f;
 
 constexpr int kNT = 256, kNW = kNT / 32, kTeachers = 3, kThreads = kNT + 32 + 32 * kTeachers;
 constexpr int kNV = 4, kChunk = kNT * kNV, kChunkBytes = kChunk * 16;   // vectors and bytes of a chunk
-// Six slots and two CTAs per SM: 690 us on the long case, 80 on the odd one; four slots and three
-// CTAs 739 and 93 (the rows in work outgrow L2), twelve slots and one CTA 729 and 120.
+// Slots and CTAs per SM, us on 8192 x 131072, 2048 x 50257 at tau = 2 and 4096 x 32768 loss alone:
+// six and two 697, 80, 49; four and three 745, 93, 49 (the rows in work outgrow L2); eleven and one
+// 681, 100, 67.
 constexpr int kStages = 6, kMaxK = 1024, kMinBlocks = 2;
 
 // The slots of the ring in the order in which a row's chunks take them.  The gradient's pass
@@ -145,7 +146,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 // kMode: 0 the teacher's softmax alone; 1 the label's (temperature 1) beside it; 2 + n the same
 // where tau = 2^n: exp(d) is then exp(d / tau) squared n times, which saves half of the
-// exponentials, the kernel's bound with two temperatures (2048 x 50257 at tau = 2: 100 -> 92 us).
+// exponentials, the kernel's bound with two temperatures (2048 x 50257 at tau = 2: 89 -> 80 us).
 template <class E, int kMode>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(DistillParams P) {
   using V = Words<E>;

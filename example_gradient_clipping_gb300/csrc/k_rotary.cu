@@ -43,8 +43,8 @@ __global__ void __launch_bounds__(256) rotary_table_kernel(dp_rotary_table_desc 
 // chunk) or VEC copied entries of one token, for HG heads of Q or of K: the angles are loaded
 // once for HG heads' independent loads of 16 bytes.  Consecutive threads take consecutive
 // chunks, then consecutive heads, so a warp's accesses fill whole sectors.
-// Measured on the long case: two heads a thread 135-158 us, four 114 (at four blocks per SM; 130 at
-// three), eight 125; one pair a thread 838; threads that loop over all heads of a token 156-220.
+// Measured on the long case: four heads a thread 115 us (132 with registers for three blocks per SM),
+// one 183, two 161, eight 181.
 template <class E, int VEC, int HG, bool kInter>
 __global__ void __launch_bounds__(256, 4) rotary_kernel(RotaryParams P, int items, int gq, int gk, int per_block) {
   pdl_trigger();
@@ -153,10 +153,11 @@ static cudaError_t run_rotary(const RotaryParams& P, cudaStream_t s) {
 
 template <class E, int VEC>
 static cudaError_t run_rotary_heads(const RotaryParams& P, cudaStream_t s) {
-  // four heads a thread once that still leaves every SM its threads four times (the long case: 114
-  // us against 302 with one); a smaller call is latency, and wants one head a thread
+  // four heads a thread once that leaves every SM 1280 threads; a smaller call is latency, and
+  // wants one (us, one head against four; D = 64, 12 + 12 heads, bf16: 8 x 197 tokens 2.9 and 4.1,
+  // 16 x 197 at 0.78 of the limit 4.3 and 4.5, 32 x 197 at 1.6 7.1 and 5.5, 64 x 197 13.0 and 9.0)
   const double threads = (double)P.B * P.T * (P.Hq + P.Hk) * (P.D / VEC) / 4;
-  return threads >= 4.0 * 152 * 1024 ? run_rotary<E, VEC, 4>(P, s) : run_rotary<E, VEC, 1>(P, s);
+  return threads >= 1280.0 * 152 ? run_rotary<E, VEC, 4>(P, s) : run_rotary<E, VEC, 1>(P, s);
 }
 
 // The widest vector (up to 16 bytes) that fits every address, the two parts of a head and
