@@ -11,16 +11,18 @@ They run between the linear layers whose per-example gradients PrivacyEngine cli
 rotary, attention and distill_loss take part in autograd; attention_forward,
 attention_backward and distill_loss_and_grad are the same computations without it.  The dp_*
 functions marshal the arguments of the C entry points of include/dpclip_seq.h, which states
-the formulas.  Work goes to the current stream of the tensors' device; results are allocated
-by torch, so the usual rules for using a tensor on another stream apply.  An argument that
-does not fit raises ValueError (or DPError, from the C side) before anything is launched.
+the formulas.  Work goes to the current stream of the tensors' device, or to `stream` as if it
+were the current one: results and workspaces are allocated by torch for that stream, and the
+usual rules for using a tensor on another stream apply.  An argument that does not fit raises ValueError (or DPError, from the C side) before anything is launched.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import DP_BF16, DP_FP32, _check, _lib, _ptr, _stream
 
@@ -158,10 +160,23 @@ def _opt(x):
     return None if x is None else (x.shape, x.stride(), x.dtype, x.get_device())
 
 
-def _call(f, device, stream, *args):
-    """f(*args, stream) of the C side with `device` current (the C side uses that); stream None:
-    the device's current stream."""
-    stream = _current_stream(device) if stream is None else _stream(stream)
+def _on(stream, device):
+    """`stream` (a torch stream or a handle) as the current one: what the call allocates then
+    belongs to it, and a workspace that is dropped on return is not handed to another stream's
+    work while the call still uses it."""
+    if device.type != "cuda":
+        return contextlib.nullcontext()   # refused by the checks
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    if stream.device.index != index:
+        raise ValueError(f"stream: on {stream.device}, the tensors on cuda:{index}")
+    return torch.cuda.stream(stream)
+
+
+def _call(f, device, *args):
+    """f(*args, stream) of the C side on the current stream of `device`, with that current."""
+    stream = _current_stream(device)
     if device == _current_device():
         status = f(*args, stream)
     else:
@@ -181,8 +196,11 @@ def rotary_table(R: int, P: int, theta: float = 10000.0, scaling: str = "plain",
         raise ValueError(f"scaling {scaling!r}: one of {sorted(_SCALINGS)}")
     if P <= 0 or R <= 0:
         raise ValueError(f"P={P} and R={R} must be > 0")
+    if stream is not None:
+        with _on(stream, torch.device(device)):
+            return rotary_table(R, P, theta, scaling, factor, context, slow, fast, device)
     table = torch.empty(P, R, dtype=torch.float32, device=device)
-    _call(_lib.dp_rotary_table, table.get_device(), stream,
+    _call(_lib.dp_rotary_table, table.get_device(),
           RotaryTableDesc(P, R, _SCALINGS[scaling], theta, factor, context, slow, fast), table.data_ptr())
     return table
 
@@ -205,7 +223,7 @@ def _rotary_desc(q, k, table, positions, interleaved, inverse):
                       Strides(T * Hq * D, Hq * D, D), Strides(T * Hk * D, Hk * D, D))
 
 
-def _rotary(q, k, table, positions, interleaved, inverse, stream):
+def _rotary(q, k, table, positions, interleaved, inverse):
     shape, dtype, dev = q.shape, q.dtype, q.get_device()
     key = (shape, q.stride(), dtype, dev, table.shape, table.stride(), table.dtype, table.get_device(), interleaved,
            inverse, None if k is None else (k.shape, k.stride(), k.dtype, k.get_device()),
@@ -215,7 +233,7 @@ def _rotary(q, k, table, positions, interleaved, inverse, stream):
     qo = _empty(shape, dtype=dtype, device=device)
     ko = _empty(k.shape, dtype=dtype, device=device) if k is not None else None
     if d.B * d.T * (d.Hq + d.Hk) * d.D:
-        _call(_lib.dp_rotary, dev, stream, d, q.data_ptr(), None if k is None else k.data_ptr(), table.data_ptr(),
+        _call(_lib.dp_rotary, dev, d, q.data_ptr(), None if k is None else k.data_ptr(), table.data_ptr(),
               None if positions is None else positions.data_ptr(), qo.data_ptr(), None if k is None else ko.data_ptr())
     return qo, ko
 
@@ -230,14 +248,15 @@ class _Rotary(torch.autograd.Function):
     def forward(ctx, q, k, table, positions, interleaved, inverse):
         ctx.save_for_backward(table, positions)
         ctx.opts = (interleaved, inverse)
-        return _rotary(q, k, table, positions, interleaved, inverse, None)
+        return _rotary(q, k, table, positions, interleaved, inverse)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         table, positions = ctx.saved_tensors
         interleaved, inverse = ctx.opts
         dk = _rows_contiguous(dk) if dk is not None else None
-        gq, gk = _rotary(_rows_contiguous(dq), dk, table, positions, interleaved, not inverse, None)
+        gq, gk = _rotary(_rows_contiguous(dq), dk, table, positions, interleaved, not inverse)
         return gq, gk, None, None, None, None
 
 
@@ -249,7 +268,10 @@ def rotary(q, k, table, positions=None, interleaved: bool = False, inverse: bool
         if stream is not None:
             raise ValueError("a differentiable call runs on the current stream")
         return _Rotary.apply(q, k, table, positions, interleaved, inverse)
-    return _rotary(q, k, table, positions, interleaved, inverse, stream)
+    if stream is not None:
+        with _on(stream, q.device):
+            return _rotary(q, k, table, positions, interleaved, inverse)
+    return _rotary(q, k, table, positions, interleaved, inverse)
 
 
 # ---- attention ------------------------------------------------------------------------
@@ -287,6 +309,9 @@ def attention_forward(q, k, v, causal: bool = False, window: int = 0, scale: Opt
     fp32 [B, Hq, T].  q_lens, k_lens: int32 [B], how many leading rows of each example are
     there; causal aligns the last query with the last key; window > 0 keeps the latest
     `window` keys.  scale defaults to 1/sqrt(D).  A query that sees no key gives 0 and -inf."""
+    if stream is not None:
+        with _on(stream, q.device):
+            return attention_forward(q, k, v, causal, window, scale, q_lens, k_lens)
     shape, dtype, dev = q.shape, q.dtype, q.get_device()
     key = (shape, q.stride(), dtype, dev, k.shape, k.stride(), k.dtype, k.get_device(), v.shape, v.stride(), v.dtype,
            v.get_device(), causal, window, scale, None if q_lens is None else _opt(q_lens),
@@ -297,7 +322,7 @@ def attention_forward(q, k, v, causal: bool = False, window: int = 0, scale: Opt
     lse = _empty((d.B, d.Hq, d.T), dtype=_f32, device=device)
     if not d.B * d.T * d.Hq * d.D * d.S * d.Hk:
         return o.zero_(), lse.fill_(-float("inf"))
-    _call(_lib.dp_attention, dev, stream, d, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _call(_lib.dp_attention, dev, d, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           None if q_lens is None else q_lens.data_ptr(), None if k_lens is None else k_lens.data_ptr(), o.data_ptr(),
           lse.data_ptr())
     return o, lse
@@ -307,6 +332,9 @@ def attention_backward(q, k, v, o, lse, do, causal: bool = False, window: int = 
                        q_lens=None, k_lens=None, stream=None):
     """(dq, dk, dv) for the gradient `do` of attention_forward's o, the probabilities formed
     again from lse; the other arguments as in the forward call."""
+    if stream is not None:
+        with _on(stream, q.device):
+            return attention_backward(q, k, v, o, lse, do, causal, window, scale, q_lens, k_lens)
     shape, dtype, dev = q.shape, q.dtype, q.get_device()
     key = (shape, q.stride(), dtype, dev, k.shape, k.stride(), k.dtype, k.get_device(), v.shape, v.stride(), v.dtype,
            v.get_device(), causal, window, scale, None if q_lens is None else _opt(q_lens),
@@ -320,7 +348,7 @@ def attention_backward(q, k, v, o, lse, do, causal: bool = False, window: int = 
     if not d.B * d.T * d.Hq * d.D * d.S * d.Hk:
         return dq.zero_(), dk.zero_(), dv.zero_()
     ws = _empty(d.ws_bytes, dtype=torch.uint8, device=device)
-    _call(_lib.dp_attention_grad, dev, stream, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+    _call(_lib.dp_attention_grad, dev, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
           do.data_ptr(), None if q_lens is None else q_lens.data_ptr(), None if k_lens is None else k_lens.data_ptr(),
           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), d.ws_bytes)
     return dq, dk, dv
@@ -335,6 +363,7 @@ class _Attention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, q_lens, k_lens = ctx.saved_tensors
         return attention_backward(q, k, v, o, lse, _rows_contiguous(do), *ctx.opts, q_lens, k_lens) + (None,) * 5
@@ -369,7 +398,10 @@ def _distill_desc(logits, indices, teacher, labels, weights, upstream, temperatu
                        float(temperature), float(alpha))
 
 
-def _distill(logits, indices, teacher, labels, weights, upstream, temperature, alpha, want_loss, want_grad, stream):
+def _distill(logits, indices, teacher, labels, weights, upstream, temperature, alpha, want_loss, want_grad, stream=None):
+    if stream is not None:
+        with _on(stream, logits.device):
+            return _distill(logits, indices, teacher, labels, weights, upstream, temperature, alpha, want_loss, want_grad)
     shape, dtype, dev = logits.shape, logits.dtype, logits.get_device()
     key = (shape, logits.stride(), dtype, dev, indices.shape, indices.stride(), indices.dtype, indices.get_device(),
            teacher.shape, teacher.stride(), teacher.dtype, teacher.get_device(), temperature, alpha, _opt(labels),
@@ -384,7 +416,7 @@ def _distill(logits, indices, teacher, labels, weights, upstream, temperature, a
         grad = _empty(shape, dtype=dtype, device=device)
     if not d.B * d.T:
         return (loss.zero_() if want_loss else None), rows, grad
-    _call(_lib.dp_distill, dev, stream, d, logits.data_ptr(), indices.data_ptr(), teacher.data_ptr(),
+    _call(_lib.dp_distill, dev, d, logits.data_ptr(), indices.data_ptr(), teacher.data_ptr(),
           None if labels is None else labels.data_ptr(), None if weights is None else weights.data_ptr(),
           None if upstream is None else upstream.data_ptr(), None if rows is None else rows.data_ptr(),
           None if loss is None else loss.data_ptr(), None if grad is None else grad.data_ptr())
@@ -394,16 +426,17 @@ def _distill(logits, indices, teacher, labels, weights, upstream, temperature, a
 class _Distill(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, indices, teacher, labels, weights, temperature, alpha):
-        loss, rows, _ = _distill(logits, indices, teacher, labels, weights, None, temperature, alpha, True, False, None)
+        loss, rows, _ = _distill(logits, indices, teacher, labels, weights, None, temperature, alpha, True, False)
         ctx.save_for_backward(logits, indices, teacher, labels, weights)
         ctx.opts = (temperature, alpha)
         ctx.mark_non_differentiable(rows)
         return loss, rows
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, up, _):
         logits, indices, teacher, labels, weights = ctx.saved_tensors
-        grad = _distill(logits, indices, teacher, labels, weights, up.float().contiguous(), *ctx.opts, False, True, None)[2]
+        grad = _distill(logits, indices, teacher, labels, weights, up.float().contiguous(), *ctx.opts, False, True)[2]
         return grad, None, None, None, None, None, None
 
 

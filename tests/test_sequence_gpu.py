@@ -554,6 +554,49 @@ def test_distill_gradient_against_differences(lib):
     assert abs((f[0] - f[1]) / 2e-2 - (grad.double() * d.double()).sum().item()) <= 3e-3 * grad.double().norm().item()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_another_stream_owns_what_a_call_allocates(lib, D):
+    """stream=: while the side stream's work still waits, the caller's stream reuses freed memory.
+    The gradient's workspace must not be among it: the late kernels would write over new tensors."""
+    import torch
+    q, k, v, do, _, _ = _attn_inputs(2, 300, 300, 2, 2, D, None, "bf16")
+    z, idx, t, y = _distill_inputs("bf16", 2, 5, 1001, 8)
+    table = lib.rotary_table(D, 300)
+    want = (lib.attention_forward(q, k, v, causal=True) + lib.rotary(q, k, table) +
+            lib.distill_loss_and_grad(z, idx, t, labels=y, alpha=0.5))
+    want += lib.attention_backward(q, k, v, *want[:2], do, causal=True)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for s in (side, side.cuda_stream):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)   # some 10 ms ahead of the calls
+        got = (lib.attention_forward(q, k, v, causal=True, stream=s) + lib.rotary(q, k, table, stream=s) +
+               lib.distill_loss_and_grad(z, idx, t, labels=y, alpha=0.5, stream=s))
+        got += lib.attention_backward(q, k, v, *got[:2], do, causal=True, stream=s)
+        new = [torch.full((n,), 7.0, device="cuda") for n in (600, 1200, 2400, 5000, 20000, 1 << 20) for _ in range(8)]
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(x.eq(7).all() for x in new)
+    own = lib.rotary_table(D, 300, stream=side)
+    side.synchronize()
+    assert torch.equal(own, table)
+
+
+def test_no_second_derivative(lib):
+    """The gradients are not differentiable themselves: asking for it is an error, not a zero."""
+    import torch
+    q, k, v, _, _, _ = _attn_inputs(1, 8, 8, 1, 1, 64, None, "fp32")
+    z, idx, t, _ = _distill_inputs("fp32", 1, 3, 17, 4)
+    leaves = [x.requires_grad_() for x in (q, k, v, z)]
+    table = lib.rotary_table(64, 8)
+    for out, x in ((lib.attention(*leaves[:3]), q), (lib.rotary(q, k, table)[0], q), (lib.distill_loss(z, idx, t)[0], z)):
+        (g,) = torch.autograd.grad(out.square().sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(g.sum(), x)
+
+
 def test_operators_refuse_on_the_host(lib):
     """What the binding refuses: nothing is launched."""
     import torch
