@@ -396,6 +396,41 @@ std::atomic<unsigned long long> g_launches{0};
 }  // namespace
 
 namespace dph {
+// Open-addressed and never emptied: a slot is a stream and device with the mark in bit 0.  Should
+// more streams than slots ever be used, every launch behind an operator's is ordinary from then on.
+// So is every one on the per-thread default stream, whose handle stands for many streams.
+constexpr int kMarkSlots = 512;
+static std::atomic<unsigned long long> g_marks[kMarkSlots];
+static std::atomic<bool> g_marked{false}, g_marks_full{false};
+
+static std::atomic<unsigned long long>* mark_slot(cudaStream_t s, bool insert) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const unsigned long long key = (unsigned long long)reinterpret_cast<uintptr_t>(s) << 8 | 0x80 | (dev & 63) << 1;
+  unsigned i = (unsigned)((key * 0x9e3779b97f4a7c15ull) >> 55);   // 9 bits
+  for (int n = 0; n < kMarkSlots; ++n, i = (i + 1) % kMarkSlots) {
+    unsigned long long v = g_marks[i].load(std::memory_order_acquire);
+    if (v == 0 && insert && g_marks[i].compare_exchange_strong(v, key)) return &g_marks[i];
+    if ((v & ~1ull) == key) return &g_marks[i];
+    if (v == 0) return nullptr;
+  }
+  return nullptr;
+}
+
+void mark_operator(cudaStream_t s) {
+  std::atomic<unsigned long long>* m = mark_slot(s, true);
+  if (m) m->fetch_or(1);
+  else g_marks_full.store(true);
+  g_marked.store(true, std::memory_order_release);
+}
+
+bool take_operator(cudaStream_t s) {
+  if (!g_marked.load(std::memory_order_acquire)) return false;
+  if (g_marks_full.load() || s == cudaStreamPerThread) return true;
+  std::atomic<unsigned long long>* m = mark_slot(s, false);
+  return m && (m->fetch_and(~1ull) & 1);
+}
+
 void count_launch(unsigned n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 
 // For entry points defined in other translation units.

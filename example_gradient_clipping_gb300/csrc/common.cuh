@@ -65,8 +65,10 @@ __device__ __forceinline__ float ld_a(const E* __restrict__ A, const Geom& g, in
 // its CTAs are running (pdl_trigger), and waits for the previous kernel in the stream to
 // complete, with its memory visible, before its first global-memory access (pdl_wait) --
 // except the tensor-core kernels of linear layers, whose loads of the caller's A and G
-// (which no library kernel writes) may precede the wait.  Kernels that do not use these
-// (another library's) keep ordinary stream order.
+// may precede the wait.  Of the library's kernels only the sequence operators' write what can
+// be an A or G; the first other kernel behind them on a stream starts in ordinary stream order
+// (take_operator), and every kernel behind that one starts after them too.  Kernels
+// that do not use these (another library's) keep ordinary stream order.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -210,6 +212,12 @@ using dpk::Geom;
 // Counts kernels the library launched (reported by dp_launch_count).
 void count_launch(unsigned n = 1);
 
+// Streams on which a sequence operator was launched and no other library kernel since: set by
+// an operator's launch, and taken (read and cleared) by the next other launch, which must then
+// be an ordinary one.
+void mark_operator(cudaStream_t s);
+bool take_operator(cudaStream_t s);
+
 // Launch with programmatic stream serialization (see pdl_wait); counts the launch.
 // `pdl` false gives ordinary stream order (the kernel's pdl_wait is then a no-op): the
 // conv layout and im2col kernels, where overlapping launches measured slower.
@@ -230,10 +238,20 @@ cudaError_t launch_k(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block, 
   count_launch();
   return e;
 }
+// A sequence operator's kernel: none of them reads anything before its pdl_wait.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_operator(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                            Args&&... args) {
+  mark_operator(s);
+  return launch_k(true, kernel, grid, block, smem, s, static_cast<Args&&>(args)...);
+}
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        Args&&... args) {
-  return launch_k(true, kernel, grid, block, smem, s, static_cast<Args&&>(args)...);
+  const bool after = take_operator(s);
+  const cudaError_t e = launch_k(!after, kernel, grid, block, smem, s, static_cast<Args&&>(args)...);
+  if (after && e != cudaSuccess) mark_operator(s);   // nothing was put behind the operator
+  return e;
 }
 template <typename... KArgs, typename... Args>
 cudaError_t launch_plain(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,

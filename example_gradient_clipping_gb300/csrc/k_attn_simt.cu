@@ -389,7 +389,7 @@ cudaError_t fwd(const AttnParams& P, cudaStream_t s) {
       cudaFuncSetAttribute(attn_fwd_kernel<E, DP, kAsync>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (set != cudaSuccess) return set;
   const unsigned grid = (unsigned)((size_t)P.B * P.Hq * ((P.T + BT - 1) / BT));
-  return dph::launch_pdl(attn_fwd_kernel<E, DP, kAsync>, grid, kThreads, smem, s, P);
+  return dph::launch_operator(attn_fwd_kernel<E, DP, kAsync>, grid, kThreads, smem, s, P);
 }
 
 template <class E, int DP, bool kAsync>
@@ -399,7 +399,7 @@ cudaError_t grad(const AttnParams& P, cudaStream_t s) {
       cudaFuncSetAttribute(attn_grad_kernel<E, DP, kAsync>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (set != cudaSuccess) return set;
   const int key_ctas = P.B * P.Hk * ((P.S + BT - 1) / BT), query_ctas = P.B * P.Hq * ((P.T + BT - 1) / BT);
-  return dph::launch_pdl(attn_grad_kernel<E, DP, kAsync>, (unsigned)(key_ctas + query_ctas), kThreads, smem, s, P,
+  return dph::launch_operator(attn_grad_kernel<E, DP, kAsync>, (unsigned)(key_ctas + query_ctas), kThreads, smem, s, P,
                          key_ctas);
 }
 
@@ -435,7 +435,7 @@ static cudaError_t run_delta(const AttnParams& P, float* delta, cudaStream_t s) 
   int lanes = 1;
   while (lanes < 32 && lanes * VEC < P.D) lanes *= 2;
   const size_t rows = (size_t)P.B * P.T * P.Hq, per_block = 256 / lanes * 4;
-  return launch_pdl(attnsimt::attn_delta_kernel<E, VEC>, (unsigned)((rows + per_block - 1) / per_block), 256, 0, s, P,
+  return launch_operator(attnsimt::attn_delta_kernel<E, VEC>, (unsigned)((rows + per_block - 1) / per_block), 256, 0, s, P,
                     delta, lanes);
 }
 

@@ -323,7 +323,7 @@ static cudaError_t run_fwd(const AttnParams& P, const CUtensorMap& mq, const CUt
                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (set != cudaSuccess) return set;
   const unsigned grid = (unsigned)((size_t)P.B * P.Hq * ((P.T + NT * attntc::BT - 1) / (NT * attntc::BT)));
-  return launch_pdl(attntc::attn_tc_fwd_kernel<DP, NT>, grid, C::THREADS, C::SMEM, s, mq, mk, mv, P);
+  return launch_operator(attntc::attn_tc_fwd_kernel<DP, NT>, grid, C::THREADS, C::SMEM, s, mq, mk, mv, P);
 }
 
 cudaError_t launch_attn_tc_fwd(const AttnParams& P, cudaStream_t s) {

@@ -546,7 +546,7 @@ static cudaError_t run_grad(const AttnParams& P, const attntc::GradSplit& sp, co
   static const cudaError_t set = cudaFuncSetAttribute(attntc::attn_tc_grad_kernel<DP>,
                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (set != cudaSuccess) return set;
-  return launch_pdl(attntc::attn_tc_grad_kernel<DP>, (unsigned)(sp.key_ctas + sp.query_ctas), C::THREADS, C::SMEM, s, q[0],
+  return launch_operator(attntc::attn_tc_grad_kernel<DP>, (unsigned)(sp.key_ctas + sp.query_ctas), C::THREADS, C::SMEM, s, q[0],
                     q[1], k[0], k[1], P, sp);
 }
 
@@ -563,7 +563,7 @@ cudaError_t launch_attn_tc_grad(const AttnParams& P, float* ws, cudaStream_t s) 
   if (e != cudaSuccess || (sp.keys == 1 && sp.queries == 1)) return e;
   const size_t n = ((sp.keys > 1 ? 2 * (size_t)P.B * P.Hk * P.S : 0) + (sp.queries > 1 ? (size_t)P.B * P.Hq * P.T : 0)) *
                    (P.D / 8);
-  return launch_pdl(attntc::attn_tc_join_kernel, (unsigned)((n + 255) / 256), 256, 0, s, P, sp, P.D <= 64 ? 64 : 128);
+  return launch_operator(attntc::attn_tc_join_kernel, (unsigned)((n + 255) / 256), 256, 0, s, P, sp, P.D <= 64 ? 64 : 128);
 }
 
 }  // namespace dph

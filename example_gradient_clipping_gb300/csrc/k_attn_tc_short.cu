@@ -439,7 +439,7 @@ cudaError_t launch_attn_tc_short_grad(const AttnParams& P, cudaStream_t s) {
       !map_heads(&k, P.K, P.k, P.B, P.S, P.Hk, P.D) || !map_heads(&v, P.V, P.v, P.B, P.S, P.Hk, P.D) ||
       !map_heads(&o, P.O, P.o, P.B, P.T, P.Hq, P.D))
     return cudaErrorInvalidValue;
-  return launch_pdl(ns::attn_tc_short_grad_kernel, (unsigned)(P.B * P.Hq), ns::THREADS, ns::SMEM, s, q, g, k, v, o, P);
+  return launch_operator(ns::attn_tc_short_grad_kernel, (unsigned)(P.B * P.Hq), ns::THREADS, ns::SMEM, s, q, g, k, v, o, P);
 }
 
 }  // namespace dph

@@ -591,7 +591,7 @@ static cudaError_t run_distill(const DistillParams& P, cudaStream_t s) {
   // two CTAs per SM, one where many teacher entries take their shared memory
   const int smem = distill::stream_smem(P.K), per_sm = std::min(distill::kMinBlocks, 232448 / (smem + 1024));
   const unsigned grid = (unsigned)std::min<size_t>((size_t)P.B * P.T, (size_t)152 * per_sm);
-  return launch_pdl(distill::distill_stream_kernel<E, kMode>, grid, distill::kThreads, smem, s, P);
+  return launch_operator(distill::distill_stream_kernel<E, kMode>, grid, distill::kThreads, smem, s, P);
 }
 
 template <class E>
@@ -606,7 +606,7 @@ static cudaError_t distill_mode(const DistillParams& P, cudaStream_t s) {
 cudaError_t launch_distill(const DistillParams& P, int dtype, cudaStream_t s) {
   cudaError_t e = dtype == DP_BF16 ? distill_mode<__nv_bfloat16>(P, s) : distill_mode<float>(P, s);
   if (e == cudaSuccess && P.loss)
-    e = launch_pdl(distill::distill_loss_kernel, (unsigned)P.B, 256, 0, s, (const float*)P.row_loss, P.T, P.loss);
+    e = launch_operator(distill::distill_loss_kernel, (unsigned)P.B, 256, 0, s, (const float*)P.row_loss, P.T, P.loss);
   return e;
 }
 

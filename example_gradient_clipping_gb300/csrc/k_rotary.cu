@@ -136,7 +136,7 @@ using namespace dpk;
 cudaError_t launch_rotary_table(const dp_rotary_table_desc& d, float* table, cudaStream_t s) {
   const size_t n = (size_t)d.P * (d.R / 2);
   const unsigned grid = (unsigned)std::min<size_t>((n + 255) / 256, 152 * 8);
-  return launch_pdl(rotary_table_kernel, grid, 256, 0, s, d, table);
+  return launch_operator(rotary_table_kernel, grid, 256, 0, s, d, table);
 }
 
 template <class E, int VEC, int HG>
@@ -147,8 +147,8 @@ static cudaError_t run_rotary(const RotaryParams& P, cudaStream_t s) {
   if (units > (1 << 24)) return cudaErrorInvalidConfiguration;
   const int per_block = units < 256 ? 256 / (int)units : 1;
   const dim3 grid((unsigned)((tokens + per_block - 1) / per_block), (unsigned)((units + 255) / 256));
-  if (P.interleaved) return launch_pdl(rotary_kernel<E, VEC, HG, true>, grid, 256, 0, s, P, items, gq, gk, per_block);
-  return launch_pdl(rotary_kernel<E, VEC, HG, false>, grid, 256, 0, s, P, items, gq, gk, per_block);
+  if (P.interleaved) return launch_operator(rotary_kernel<E, VEC, HG, true>, grid, 256, 0, s, P, items, gq, gk, per_block);
+  return launch_operator(rotary_kernel<E, VEC, HG, false>, grid, 256, 0, s, P, items, gq, gk, per_block);
 }
 
 template <class E, int VEC>

@@ -152,7 +152,7 @@ tc_ghost_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_trigger();   // the next kernel in the stream may start launching
-  // With P.early, A and G (the caller's inputs, which no library kernel writes) are loaded
+  // With P.early, A and G (the caller's inputs, complete before the library's last launch) are loaded
   // and multiplied before the previous kernel in the stream has completed; the epilogue
   // warps pass pdl_wait before they write.  Otherwise every warp waits here.
   if (!P.early) pdl_wait();
@@ -552,8 +552,9 @@ static cudaError_t run_ghost(const Geom& g, const CUtensorMap& ma, const CUtenso
   cfg.dynamicSmemBytes = tcghost::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
+  const bool after = take_operator(s);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].val.programmaticStreamSerializationAllowed = after ? 0 : 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = P.ksplit;
@@ -562,6 +563,7 @@ static cudaError_t run_ghost(const Geom& g, const CUtensorMap& ma, const CUtenso
   cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, tcghost::tc_ghost_kernel, ma, mg, ma1, mg1, P);
   count_launch();
+  if (after && e != cudaSuccess) mark_operator(s);
   return e;
 }
 

@@ -671,7 +671,7 @@ tc_sumx_kernel(const __grid_constant__ CUtensorMap mapG64, const __grid_constant
   ptx::tc_fence_after();
   const uint32_t tmem = c->tmem;
   pdl_trigger();   // the next kernel in the stream may start launching
-  // With P.early, A and G (the caller's inputs, which no library kernel writes) are loaded
+  // With P.early, A and G (the caller's inputs, complete before the library's last launch) are loaded
   // and multiplied before the previous kernel in the stream has completed: the factors,
   // the outputs and the workspace are touched after pdl_wait, which every warp passes
   // before its first such access.  Otherwise every warp waits here.
@@ -855,8 +855,9 @@ cudaError_t launch_tc_sumx(const Geom& g, const void* A, const void* G, const fl
   cfg.dynamicSmemBytes = tcsumx::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
+  const bool after = take_operator(s);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].val.programmaticStreamSerializationAllowed = after ? 0 : 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = 1;
@@ -867,6 +868,7 @@ cudaError_t launch_tc_sumx(const Geom& g, const void* A, const void* G, const fl
                       ? cudaLaunchKernelEx(&cfg, tcsumx::tc_sumx_kernel<false, true>, mg64, ma64, mg16, ma16, P)
                       : cudaLaunchKernelEx(&cfg, tcsumx::tc_sumx_kernel<false, false>, mg64, ma64, mg16, ma16, P);
   count_launch();
+  if (after && e != cudaSuccess) mark_operator(s);
   if (e == cudaSuccess && bias_nt > 1) {   // the column tiles' partial biases, in order
     e = launch_reduce_splits(P.bias_part, bias_nt, (size_t)g.p, db, accumulate, s, nz, nz ? nz->off_b : 0);
     if (nz && nz->on) nz->applied_b = 1;

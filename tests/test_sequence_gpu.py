@@ -584,6 +584,57 @@ def test_another_stream_owns_what_a_call_allocates(lib, D):
     assert torch.equal(own, table)
 
 
+@pytest.mark.parametrize("mode", ["GHOST", "INSTANTIATE"])
+def test_clipped_path_right_behind_an_operator(lib, mode):
+    """What an operator has just written is the A or G of the next call: the kernels that may load
+    their inputs early must not load these, nor may the ones behind them.  Every operator's output
+    lies where zeros lay before, and the norms must be those of a run that waits in between.  (312
+    rows: a few CTAs write a second one while the others' SMs are free for the next kernel.)"""
+    import torch
+    B, T, V, d, H, D = 3, 104, 65536, 64, 8, 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    z = torch.randn(B, T, V, generator=g, device="cuda").bfloat16()
+    idx = torch.randint(0, V, (B, T, 16), generator=g, device="cuda", dtype=torch.int32)
+    top = torch.randn(B, T, 16, generator=g, device="cuda").bfloat16()
+    q, k, v = (torch.randn(B, T, H, D, generator=g, device="cuda").bfloat16() for _ in range(3))
+    A = torch.randn(B, T, d, generator=g, device="cuda").bfloat16()
+    small = torch.randn(B, T, 64, generator=g, device="cuda").bfloat16()
+    mode = getattr(lib, "DP_NORM_" + mode)
+    head = lib.layer_desc(lib.DP_LINEAR, lib.DP_BF16, B=B, p=V, T=T, d=d)
+    other = lib.layer_desc(lib.DP_LINEAR, lib.DP_BF16, B=B, p=64, T=T, d=H * D)
+    ws = [torch.empty(lib.dp_workspace_size(x, mode), dtype=torch.uint8, device="cuda") for x in (head, other)]
+    sq = torch.empty(3, B, device="cuda")
+
+    def zeros_then(f, *shapes):
+        old = [torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in shapes]
+        torch.cuda.synchronize()
+        del old   # the operator's outputs take this memory
+        torch.cuda._sleep(2_000_000)   # about 1 ms: everything is queued before any of it runs
+        return f()
+
+    def run(wait, between):
+        sq.zero_()
+        o = zeros_then(lambda: lib.attention_forward(q, k, v)[0], q.shape)
+        if wait:
+            torch.cuda.synchronize()
+        lib.dp_layer_sqnorms(other, o, small, sq[0], ws[1], mode=mode)
+        torch.cuda.synchronize()
+        dz = zeros_then(lambda: lib.distill_loss_and_grad(z, idx, top)[1], z.shape)
+        if wait:
+            torch.cuda.synchronize()
+        if between:
+            lib.dp_layer_sqnorms(other, o, small, sq[1], ws[1], mode=mode)   # lets the next one start
+        lib.dp_layer_sqnorms(head, A, dz, sq[2], ws[0], mode=mode)
+        torch.cuda.synchronize()
+        return sq.clone()
+
+    for between in (False, True):
+        want = run(True, between)
+        assert (want[[0, 1, 2] if between else [0, 2]] > 0).all()
+        for _ in range(5):
+            assert torch.equal(run(False, between), want)
+
+
 def test_no_second_derivative(lib):
     """The gradients are not differentiable themselves: asking for it is an error, not a zero."""
     import torch
