@@ -238,7 +238,11 @@ cudaError_t launch_k(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block, 
   count_launch();
   return e;
 }
-// A sequence operator's kernel: none of them reads anything before its pdl_wait.
+// A sequence operator's kernel: none of them reads anything before its pdl_wait.  They call
+// pdl_trigger late, once a CTA's main loop is done: the next kernel's CTAs, started while most SMs
+// are still taken, crowd onto the few that are not and then run one after another there (gradient
+// split over CTAs, 1 x 2048, 8 query heads on one: 56.6 -> 51.7 us; fp32 forward, 2 x 1024, 8 heads:
+// 122 -> 97; 4 x 33 tokens, 12 heads: 4.9 -> 4.7).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_operator(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                             Args&&... args) {

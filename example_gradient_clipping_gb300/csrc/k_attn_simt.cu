@@ -12,10 +12,13 @@
 // side (a key tile's dK and dV over every query that sees it, heads sharing the key head in
 // turn; a query tile's dQ over its keys), which costs two of the seven products twice and
 // needs no atomics: every sum has one order.
-// Bound by FFMA and shared-memory issue at low occupancy (104 KB and 128 registers a thread leave two
-// CTAs per SM for the gradient, which uses half of the issue slots): fp32 B = 16, T = 250, H = 12,
-// D = 64, causal, lengths 250 to 0: forward and gradient together 165 us; full lengths 65 and 196 us,
-// without the asynchronous copies 80 and 289.
+// Bound by FFMA and shared-memory issue, two CTAs of 128 registers a thread per SM: fp32 B = 16,
+// T = 250, H = 12, D = 64, causal, lengths 250 to 0: forward and gradient together 137 us; with full
+// lengths forward 60 us, gradient 183; 2 x 1024, 8 heads, not causal 132 and 415 (25.9 TFLOP/s of the
+// gradient's five products, 36 of the seven formed).
+// Forward and gradient at full lengths step by step: 80 and 289 us with plain loads, 65 and 196 with
+// asynchronous ones, 64 and 189 with packed products of P and dS, 61 and 183 with the scores' loop
+// unrolled in full.  The forward pass with three CTAs of 80 registers: 61 us, and 150 for 132 above.
 #include <algorithm>
 
 #include "seq.cuh"
@@ -67,7 +70,7 @@ __device__ __forceinline__ void tile_dot(const float* A, const float* B, int ty,
   for (int a = 0; a < 4; ++a)
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[a][c] = 0ull;
-#pragma unroll 4
+#pragma unroll
   for (int d = 0; d < DP; d += 4) {
     ulonglong2 x[4], y[4];
 #pragma unroll
@@ -98,27 +101,30 @@ template <int DP> struct Cols {
 template <int DP>
 __device__ __forceinline__ void tile_acc(const float* W, const float* X, int ty, int tx, float (&acc)[4][DP / 16]) {
   using C = Cols<DP>;
-#pragma unroll 2
+#pragma unroll 4
   for (int j = 0; j < BT; j += 4) {
     float4 w[4];
 #pragma unroll
     for (int a = 0; a < 4; ++a) w[a] = *reinterpret_cast<const float4*>(W + (4 * ty + a) * PS + j);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      float x[DP / 16];
+      uint64_t x[DP / 32];   // pairs of columns, two products an instruction
 #pragma unroll
       for (int c = 0; c < C::NC; ++c)
 #pragma unroll
-        for (int v = 0; v < C::VW; v += 2) {
-          const float2 q = *reinterpret_cast<const float2*>(X + (j + u) * (DP + 4) + (tx + 16 * c) * C::VW + v);
-          x[c * C::VW + v] = q.x;
-          x[c * C::VW + v + 1] = q.y;
-        }
+        for (int v = 0; v < C::VW; v += 2)
+          x[(c * C::VW + v) / 2] =
+              *reinterpret_cast<const uint64_t*>(X + (j + u) * (DP + 4) + (tx + 16 * c) * C::VW + v);
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
         const float p = u == 0 ? w[a].x : u == 1 ? w[a].y : u == 2 ? w[a].z : w[a].w;
+        const uint64_t p2 = pair(p, p);
 #pragma unroll
-        for (int c = 0; c < DP / 16; ++c) acc[a][c] = fmaf(p, x[c], acc[a][c]);
+        for (int c = 0; c < DP / 32; ++c) {
+          const float2 y = unpair(fma2(p2, x[c], pair(acc[a][2 * c], acc[a][2 * c + 1])));
+          acc[a][2 * c] = y.x;
+          acc[a][2 * c + 1] = y.y;
+        }
       }
     }
   }
@@ -157,8 +163,7 @@ template <int DP> constexpr int grad_smem() { return (4 * BT * (DP + 4) + 2 * BT
 
 // One buffer each for K and V: a tile's V is copied under its scores, the next K under P V.
 template <class E, int DP, bool kAsync>
-__global__ void __launch_bounds__(kThreads, DP <= 64 ? 3 : 2) attn_fwd_kernel(AttnParams P) {
-  pdl_trigger();
+__global__ void __launch_bounds__(kThreads, 2) attn_fwd_kernel(AttnParams P) {
   pdl_wait();
   extern __shared__ __align__(16) float sm[];
   float *sq = sm, *sk = sq + BT * (DP + 4), *sv = sk + BT * (DP + 4), *sp = sv + BT * (DP + 4);
@@ -221,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 64 ? 3 : 2) attn_fwd_kernel(At
       __syncthreads();    // V is free
     }
   }
+  pdl_trigger();
   float f[4];
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
@@ -314,6 +320,7 @@ __device__ __forceinline__ void grad_body(const AttnParams& P, int idx, float* s
     __syncthreads();    // b1, lse and delta are free
     if (it + 1 < N) load1(it + 1);
   }
+  pdl_trigger();
   const float one[4] = {1.f, 1.f, 1.f, 1.f}, sc[4] = {P.scale, P.scale, P.scale, P.scale};
   if (kKeys) {
     store_acc<E, DP>(acc1, one, static_cast<E*>(P.dV) + b * P.dv.b + ho * P.dv.h, P.dv.t, own0, P.S, P.D, ty, tx);
@@ -326,7 +333,6 @@ __device__ __forceinline__ void grad_body(const AttnParams& P, int idx, float* s
 // Both own sides in one grid, keys first: the queries' CTAs fill the SMs that the last keys' leave.
 template <class E, int DP, bool kAsync>
 __global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) attn_grad_kernel(AttnParams P, int key_ctas) {
-  pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(16) float sm[];
   const int idx = (int)blockIdx.x;
@@ -338,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) attn_grad_kernel(A
 // vectors of VEC values, four rows a lane in flight.  Reads O and dO once: HBM.
 template <class E, int VEC>
 __global__ void __launch_bounds__(256) attn_delta_kernel(AttnParams P, float* __restrict__ delta, int lanes) {
-  pdl_trigger();
   pdl_wait();
   using V = Pack<E, VEC>;
   constexpr int R = 4;
@@ -365,6 +370,7 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(AttnParams P, float* __
       for (int c = 0; c < VEC; ++c) s[r] = fmaf(x.get(c), y.get(c), s[r]);
     }
   }
+  pdl_trigger();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     for (int o = lanes / 2; o > 0; o >>= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);

@@ -17,8 +17,8 @@
 // by 8 (P up to 256, exact in the fp32 sums and no worse rounded in bf16) are O and l
 // rescaled, so after the first tiles nearly no tile touches O.
 // Bound by the chain scores - softmax - product of each tile: causal T = 8192, 32 query heads over 8,
-// D = 128 392 us, 1.40 PFLOP/s (0.74 of cuBLAS's measured bf16 rate); T = 4096, B = 2, 16 over 4 112 us
-// (1.23 PFLOP/s); ViT layer (B = 64, T = 197, H = 12, D = 64) 38 us.
+// D = 128 390 us, 1.41 PFLOP/s (0.74 of cuBLAS's measured bf16 rate); T = 4096, B = 2, 16 over 4 111 us
+// (1.23 PFLOP/s); ViT layer (B = 64, T = 197, H = 12, D = 64) 37 us.
 // Rows of V past the keys' length may hold anything: the issuing warp zeroes them in shared
 // memory before the product (0 * NaN); K's only reach scores that the mask replaces.
 #include <algorithm>
@@ -93,7 +93,6 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_trigger();
   pdl_wait();
   const uint32_t tS = tmem, tO = tmem + NT * BT;   // S (and P) of tile x at tS + 128 x, O at tO + DP x
 
@@ -291,6 +290,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     }
   }
 
+  pdl_trigger();
   ptx::tc_fence_before();
   __syncthreads();
   if (*abort && threadIdx.x == 32) {   // MMAs in flight

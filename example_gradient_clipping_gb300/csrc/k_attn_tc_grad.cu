@@ -130,7 +130,6 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& mapX1, const CUtens
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_trigger();
   pdl_wait();
   // S (then P) and dP (then dS), ND buffers of it; warpgroup w's are the 64 columns from 64 w
   const uint32_t tS = tmem, tdP = tmem + BO, tA1 = tmem + (1 + ND) * BO, tA2 = tA1 + (kKeys ? DP : 0);
@@ -436,6 +435,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& mapX1, const CUtens
     }
   }
 
+  pdl_trigger();
   ptx::tc_fence_before();
   __syncthreads();
   if (*abort && threadIdx.x == 32) {   // MMAs in flight

@@ -94,7 +94,6 @@ attn_tc_short_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS = tmem, tdP = tmem + 128, tdV = tmem + 256, tdK = tmem + 320, tdQ = tmem + 384;
-  pdl_trigger();
   pdl_wait();
 
   const Pairs pairs(P, b);
@@ -405,6 +404,7 @@ attn_tc_short_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid
     }
   }
 
+  pdl_trigger();
   ptx::tc_fence_before();
   __syncthreads();
   if (*abort && threadIdx.x == 32) {   // MMAs in flight

@@ -17,7 +17,7 @@
 // atomics and the result does not depend on any order.
 // Bound by HBM, with long vocabularies also by the second pass's misses in L2: bf16, 8192 rows of
 // 131072 (0.64 of them of weight 1) loss and gradient 690-700 us, 5.1 TB/s or 0.76 of a copy's rate;
-// 4096 x 32768 loss alone 45 us (3.8 TB/s); 2048 x 50257 with labels at tau = 2 80 us (4.2 TB/s).
+// 4096 x 32768 loss alone 44 us (3.9 TB/s); 2048 x 50257 with labels at tau = 2 80 us (4.2 TB/s).
 // (A row spread over a cluster's registers, read once, waited 3-4 us a row for the exchange of
 // its sums and ran at half the speed.)
 #include <algorithm>
@@ -177,7 +177,6 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
     ptx::fence_mbar_init();
   }
   __syncthreads();
-  pdl_trigger();
   pdl_wait();
 
   const unsigned rows = (unsigned)(P.B * P.T), first = blockIdx.x, step = gridDim.x;   // < 2^31
@@ -560,16 +559,17 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
       }
     }
   }
+  pdl_trigger();
 }
 
 // loss_i = the sum of example i's rows, in a fixed order.
 __global__ void __launch_bounds__(256) distill_loss_kernel(const float* __restrict__ rows, int T,
                                                            float* __restrict__ loss) {
-  pdl_trigger();
   pdl_wait();
   __shared__ float red[8];
   float s = 0.f;
   for (int t = threadIdx.x; t < T; t += 256) s += rows[(size_t)blockIdx.x * T + t];
+  pdl_trigger();
   s = warp_sum(s);
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = s;
   __syncthreads();

@@ -4,9 +4,9 @@
 //
 // The table is built once in fp64 (an fp32 product position * frequency is off by 4e-3 at
 // position 131072) and stays in L2; the kernel is one read and one write of the heads, bound by
-// HBM: bf16 B = 4, T = 8191, 32 + 8 heads of 128 (half of each turned, gradient direction) 114 us,
-// 5.97 TB/s or 0.90 of a copy's rate; fp32 B = 64, T = 197, 12 + 12 heads of 64 read from a packed
-// projection 24.9 us, 6.2 TB/s.
+// HBM: bf16 B = 4, T = 8191, 32 + 8 heads of 128 (half of each turned, gradient direction) 113 us,
+// 6.0 TB/s or 0.90 of a copy's rate; fp32 B = 64, T = 197, 12 + 12 heads of 64 read from a packed
+// projection 24.3 us, 6.4 TB/s.
 #include <algorithm>
 
 #include "seq.cuh"
@@ -47,7 +47,6 @@ __global__ void __launch_bounds__(256) rotary_table_kernel(dp_rotary_table_desc 
 // one 183, two 161, eight 181.
 template <class E, int VEC, int HG, bool kInter>
 __global__ void __launch_bounds__(256, 4) rotary_kernel(RotaryParams P, int items, int gq, int gk, int per_block) {
-  pdl_trigger();
   pdl_wait();
   using V = Pack<E, VEC>;
   constexpr int NC = kInter ? (VEC > 1 ? VEC / 2 : 1) : VEC;   // pairs of a unit
@@ -81,6 +80,7 @@ __global__ void __launch_bounds__(256, 4) rotary_kernel(RotaryParams P, int item
       xa[i] = *reinterpret_cast<const V*>(x + i * sx);
       if (kTwo && turned) xb[i] = *reinterpret_cast<const V*>(x + i * sx + off);
     }
+  pdl_trigger();
   if (!turned) {   // past the rotated part
 #pragma unroll
     for (int i = 0; i < HG; ++i)
