@@ -20,9 +20,19 @@ dp_status launched(cudaError_t e, const char* where) {
 }
 
 bool strides_ok(const dp_strides& s) { return s.b >= 0 && s.t >= 0 && s.h >= 0; }
-// A written tensor's rows must not fall on one another (an extent of 1 has any stride).
+// A written tensor's rows must not fall on one another: with the extents above 1 in the order of
+// their strides, each stride clears everything that the ones before it span.
 bool writable(const dp_strides& s, int B, int T, int H, int D) {
-  return strides_ok(s) && (B == 1 || s.b >= D) && (T == 1 || s.t >= D) && (H == 1 || s.h >= D);
+  struct { long long stride; int n; } d[3] = {{s.b, B}, {s.t, T}, {s.h, H}};
+  if (!strides_ok(s)) return false;
+  std::sort(d, d + 3, [](const auto& x, const auto& y) { return x.stride < y.stride; });
+  __int128 span = D;
+  for (const auto& x : d) {
+    if (x.n == 1) continue;   // any stride
+    if (x.stride < span) return false;
+    span += (__int128)x.stride * (x.n - 1);
+  }
+  return true;
 }
 constexpr int kMaxLen = 1 << 30;   // lengths whose sums stay within 32 bits
 constexpr double kMaxBlocks = 2147483647.0;

@@ -13,8 +13,10 @@
  *
  * Heads: tensors are [B, T, H, D] with the strides of the descriptor (in elements; the
  * innermost stride is 1), so heads can be read from one packed projection.  Every stride
- * must be >= 0 and the tensors that a call writes must not overlap one another or its
- * inputs (dp_rotary may write in place).  Integers in device memory (positions, lengths,
+ * must be >= 0, and the tensors that a call writes must not overlap one another or its
+ * inputs (dp_rotary may write in place).  Rows of a written tensor must not overlap either: of
+ * its extents above 1, each stride is at least D plus all that the smaller strides reach, or the
+ * call is refused.  Integers in device memory (positions, lengths,
  * indices) are 32 bits unless a descriptor says 64.
  */
 #ifndef DPCLIP_SEQ_H
