@@ -148,3 +148,14 @@ def test_distill_refuses(fake, kw, status, text):
     _refused(fake, lambda: call(d, loss=PTR), INVALID, "row_loss")
     call(d, row_loss=PTR, loss=PTR, dlogits=PTR)
     assert len(fake.launches()) == 2
+
+
+@pytest.mark.parametrize("device", ["cpu", "meta"])
+@pytest.mark.parametrize("stream", [None, STREAM])
+def test_rotary_table_on_the_host_is_refused(fake, device, stream):
+    """The table is written by a kernel: memory that is not the GPU's must not get that far."""
+    import torch
+    for d in (device, torch.device(device)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            fake.dp.rotary_table(8, 4, device=d, stream=stream)
+    assert fake.launches() == []
