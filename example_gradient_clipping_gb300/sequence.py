@@ -196,10 +196,11 @@ def rotary_table(R: int, P: int, theta: float = 10000.0, scaling: str = "plain",
         raise ValueError(f"scaling {scaling!r}: one of {sorted(_SCALINGS)}")
     if P <= 0 or R <= 0:
         raise ValueError(f"P={P} and R={R} must be > 0")
-    if torch.device(device).type != "cuda":
+    device = torch.get_default_device() if device is None else torch.device(device)
+    if device.type != "cuda":
         raise ValueError(f"device: a CUDA device, got {device}")
     if stream is not None:
-        with _on(stream, torch.device(device)):
+        with _on(stream, device):
             return rotary_table(R, P, theta, scaling, factor, context, slow, fast, device)
     table = torch.empty(P, R, dtype=torch.float32, device=device)
     _call(_lib.dp_rotary_table, table.get_device(),

@@ -155,7 +155,7 @@ def test_distill_refuses(fake, kw, status, text):
 def test_rotary_table_on_the_host_is_refused(fake, device, stream):
     """The table is written by a kernel: memory that is not the GPU's must not get that far."""
     import torch
-    for d in (device, torch.device(device)):
+    for d in (device, torch.device(device)) + ((None,) if device == "cpu" else ()):   # None: torch's default device
         with pytest.raises(ValueError, match="CUDA device"):
             fake.dp.rotary_table(8, 4, device=d, stream=stream)
     assert fake.launches() == []
