@@ -396,39 +396,56 @@ std::atomic<unsigned long long> g_launches{0};
 }  // namespace
 
 namespace dph {
-// Open-addressed and never emptied: a slot is a stream and device with the mark in bit 0.  Should
-// more streams than slots ever be used, every launch behind an operator's is ordinary from then on.
-// So is every one on the per-thread default stream, whose handle stands for many streams.
-constexpr int kMarkSlots = 512;
-static std::atomic<unsigned long long> g_marks[kMarkSlots];
-static std::atomic<bool> g_marked{false}, g_marks_full{false};
+// Open-addressed and never emptied: a slot is a stream and device.  Should more streams than slots
+// ever be used, every launch behind an operator's is ordinary from then on.  So is every one on the
+// per-thread default stream, whose handle stands for many streams.
+struct StreamSlot {
+  std::atomic<unsigned long long> key, operators, covered;
+};
+constexpr int kStreamSlots = 512;
+static StreamSlot g_streams[kStreamSlots];
+static std::atomic<bool> g_operators{false}, g_streams_full{false};
 
-static std::atomic<unsigned long long>* mark_slot(cudaStream_t s, bool insert) {
+static StreamSlot* stream_slot(cudaStream_t s, bool insert) {
   int dev = 0;
   cudaGetDevice(&dev);
-  const unsigned long long key = (unsigned long long)reinterpret_cast<uintptr_t>(s) << 8 | 0x80 | (dev & 63) << 1;
+  if (s == cudaStreamLegacy) s = nullptr;   // one stream with two handles
+  const unsigned long long key = (unsigned long long)reinterpret_cast<uintptr_t>(s) << 8 | 0x80 | (dev & 127);
   unsigned i = (unsigned)((key * 0x9e3779b97f4a7c15ull) >> 55);   // 9 bits
-  for (int n = 0; n < kMarkSlots; ++n, i = (i + 1) % kMarkSlots) {
-    unsigned long long v = g_marks[i].load(std::memory_order_acquire);
-    if (v == 0 && insert && g_marks[i].compare_exchange_strong(v, key)) return &g_marks[i];
-    if ((v & ~1ull) == key) return &g_marks[i];
+  for (int n = 0; n < kStreamSlots; ++n, i = (i + 1) % kStreamSlots) {
+    unsigned long long v = g_streams[i].key.load(std::memory_order_acquire);
+    if (v == 0 && insert && g_streams[i].key.compare_exchange_strong(v, key)) return &g_streams[i];
+    if (v == key) return &g_streams[i];
     if (v == 0) return nullptr;
   }
   return nullptr;
 }
 
 void mark_operator(cudaStream_t s) {
-  std::atomic<unsigned long long>* m = mark_slot(s, true);
-  if (m) m->fetch_or(1);
-  else g_marks_full.store(true);
-  g_marked.store(true, std::memory_order_release);
+  StreamSlot* m = stream_slot(s, true);
+  if (m) m->operators.fetch_add(1, std::memory_order_release);
+  else g_streams_full.store(true);
+  g_operators.store(true, std::memory_order_release);
 }
 
-bool take_operator(cudaStream_t s) {
-  if (!g_marked.load(std::memory_order_acquire)) return false;
-  if (g_marks_full.load() || s == cudaStreamPerThread) return true;
-  std::atomic<unsigned long long>* m = mark_slot(s, false);
-  return m && (m->fetch_and(~1ull) & 1);
+StreamOrder behind_operators(cudaStream_t s) {
+  StreamOrder o;
+  if (!g_operators.load(std::memory_order_acquire)) return o;
+  o.full = g_streams_full.load() || s == cudaStreamPerThread;
+  if (o.full) return o;
+  StreamSlot* m = stream_slot(s, false);
+  if (!m) return o;
+  o.upto = m->operators.load(std::memory_order_acquire);
+  o.full = o.upto > m->covered.load(std::memory_order_acquire);
+  if (o.full) o.covered = &m->covered;
+  return o;
+}
+
+void cover_operators(const StreamOrder& o) {
+  if (!o.covered) return;
+  unsigned long long c = o.covered->load(std::memory_order_relaxed);
+  while (c < o.upto && !o.covered->compare_exchange_weak(c, o.upto, std::memory_order_release)) {
+  }
 }
 
 void count_launch(unsigned n) { g_launches.fetch_add(n, std::memory_order_relaxed); }

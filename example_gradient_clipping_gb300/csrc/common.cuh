@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "dpclip.h"
 
 namespace dpk {
@@ -67,7 +69,7 @@ __device__ __forceinline__ float ld_a(const E* __restrict__ A, const Geom& g, in
 // except the tensor-core kernels of linear layers, whose loads of the caller's A and G
 // may precede the wait.  Of the library's kernels only the sequence operators' write what can
 // be an A or G; the first other kernel behind them on a stream starts in ordinary stream order
-// (take_operator), and every kernel behind that one starts after them too.  Kernels
+// (StreamOrder), and every kernel behind that one starts after them too.  Kernels
 // that do not use these (another library's) keep ordinary stream order.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -212,11 +214,18 @@ using dpk::Geom;
 // Counts kernels the library launched (reported by dp_launch_count).
 void count_launch(unsigned n = 1);
 
-// Streams on which a sequence operator was launched and no other library kernel since: set by
-// an operator's launch, and taken (read and cleared) by the next other launch, which must then
-// be an ordinary one.
-void mark_operator(cudaStream_t s);
-bool take_operator(cudaStream_t s);
+// Whether a launch on a stream must be an ordinary one because sequence operators stand there that
+// no ordinary launch has come behind yet.  Operators are counted per stream once they are launched, and
+// count as covered only when the launch behind them has succeeded, up to the count that it saw before
+// it: so host threads that share a stream cannot lose one between another's look and its launch.
+struct StreamOrder {
+  bool full = false;
+  std::atomic<unsigned long long>* covered = nullptr;
+  unsigned long long upto = 0;
+};
+StreamOrder behind_operators(cudaStream_t s);
+void cover_operators(const StreamOrder& o);   // after the launch
+void mark_operator(cudaStream_t s);           // after an operator's launch
 
 // Launch with programmatic stream serialization (see pdl_wait); counts the launch.
 // `pdl` false gives ordinary stream order (the kernel's pdl_wait is then a no-op): the
@@ -246,15 +255,16 @@ cudaError_t launch_k(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block, 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_operator(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                             Args&&... args) {
-  mark_operator(s);
-  return launch_k(true, kernel, grid, block, smem, s, static_cast<Args&&>(args)...);
+  const cudaError_t e = launch_k(true, kernel, grid, block, smem, s, static_cast<Args&&>(args)...);
+  if (e == cudaSuccess) mark_operator(s);
+  return e;
 }
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        Args&&... args) {
-  const bool after = take_operator(s);
-  const cudaError_t e = launch_k(!after, kernel, grid, block, smem, s, static_cast<Args&&>(args)...);
-  if (after && e != cudaSuccess) mark_operator(s);   // nothing was put behind the operator
+  const StreamOrder order = behind_operators(s);
+  const cudaError_t e = launch_k(!order.full, kernel, grid, block, smem, s, static_cast<Args&&>(args)...);
+  if (e == cudaSuccess) cover_operators(order);
   return e;
 }
 template <typename... KArgs, typename... Args>

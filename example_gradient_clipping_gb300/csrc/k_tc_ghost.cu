@@ -552,9 +552,9 @@ static cudaError_t run_ghost(const Geom& g, const CUtensorMap& ma, const CUtenso
   cfg.dynamicSmemBytes = tcghost::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  const bool after = take_operator(s);
+  const StreamOrder order = behind_operators(s);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = after ? 0 : 1;
+  attr[0].val.programmaticStreamSerializationAllowed = order.full ? 0 : 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = P.ksplit;
@@ -563,7 +563,7 @@ static cudaError_t run_ghost(const Geom& g, const CUtensorMap& ma, const CUtenso
   cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, tcghost::tc_ghost_kernel, ma, mg, ma1, mg1, P);
   count_launch();
-  if (after && e != cudaSuccess) mark_operator(s);
+  if (e == cudaSuccess) cover_operators(order);
   return e;
 }
 

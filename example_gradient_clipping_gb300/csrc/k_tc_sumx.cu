@@ -855,9 +855,9 @@ cudaError_t launch_tc_sumx(const Geom& g, const void* A, const void* G, const fl
   cfg.dynamicSmemBytes = tcsumx::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  const bool after = take_operator(s);
+  const StreamOrder order = behind_operators(s);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = after ? 0 : 1;
+  attr[0].val.programmaticStreamSerializationAllowed = order.full ? 0 : 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = 1;
@@ -868,7 +868,7 @@ cudaError_t launch_tc_sumx(const Geom& g, const void* A, const void* G, const fl
                       ? cudaLaunchKernelEx(&cfg, tcsumx::tc_sumx_kernel<false, true>, mg64, ma64, mg16, ma16, P)
                       : cudaLaunchKernelEx(&cfg, tcsumx::tc_sumx_kernel<false, false>, mg64, ma64, mg16, ma16, P);
   count_launch();
-  if (after && e != cudaSuccess) mark_operator(s);
+  if (e == cudaSuccess) cover_operators(order);
   if (e == cudaSuccess && bias_nt > 1) {   // the column tiles' partial biases, in order
     e = launch_reduce_splits(P.bias_part, bias_nt, (size_t)g.p, db, accumulate, s, nz, nz ? nz->off_b : 0);
     if (nz && nz->on) nz->applied_b = 1;

@@ -30,6 +30,7 @@ std::map<std::pair<const void*, int>, int> allowed;   // dynamic shared memory b
 std::vector<Launch> launches;
 std::map<unsigned long long, unsigned long long> capturing;   // stream -> capture
 thread_local int device = 0;
+thread_local cudaError_t last_error = cudaSuccess;
 int attribute_failures = 0, attribute_calls = 0, launch_failures = 0;
 void (*hook)() = nullptr;
 unsigned words[64][4];
@@ -52,7 +53,11 @@ cudaError_t cudaGetDevice(int* d) {
   *d = device;
   return cudaSuccess;
 }
-cudaError_t cudaGetLastError() { return cudaSuccess; }
+cudaError_t cudaGetLastError() {
+  const cudaError_t e = last_error;
+  last_error = cudaSuccess;
+  return e;
+}
 const char* cudaGetErrorString(cudaError_t e) { return e == cudaErrorInvalidValue ? "invalid argument" : "error"; }
 cudaError_t cudaGetSymbolAddress(void** p, const void*) {
   *p = words[device];
@@ -72,7 +77,7 @@ cudaError_t cudaFuncSetAttribute(const void* fn, cudaFuncAttribute a, int v) {
   ++attribute_calls;
   if (attribute_failures > 0) {
     --attribute_failures;
-    return cudaErrorInvalidValue;
+    return last_error = cudaErrorInvalidValue;
   }
   if (a == cudaFuncAttributeMaxDynamicSharedMemorySize) allowed[{fn, device}] = v;
   return cudaSuccess;
@@ -107,6 +112,7 @@ cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* fn, voi
     l.status = cudaErrorInvalidValue;
   }
   launches.push_back(l);
+  if (l.status) last_error = (cudaError_t)l.status;
   return (cudaError_t)l.status;
 }
 
