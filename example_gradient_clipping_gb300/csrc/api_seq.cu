@@ -16,6 +16,7 @@ dp_status bad(dp_status st, const char* fmt, Args... args) {
 dp_status bad(dp_status st, const char* msg) { return dph::set_error(st, msg); }
 
 dp_status launched(cudaError_t e, const char* where) {
+  if (e != cudaSuccess) cudaGetLastError();   // reported here, and not by the next call that looks
   return e == cudaSuccess ? DP_OK : bad(DP_ERR_CUDA, "%s launch: %s", where, cudaGetErrorString(e));
 }
 
