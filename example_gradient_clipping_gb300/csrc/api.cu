@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <mutex>
 #include <string>
 
 #include "common.cuh"
@@ -401,7 +402,10 @@ namespace dph {
 // per-thread default stream, whose handle stands for many streams.
 struct StreamSlot {
   std::atomic<unsigned long long> key, operators, covered;
+  unsigned long long capture;   // under g_capture_mutex: the last capture with a launch here, and its node
+  cudaGraphNode_t node;
 };
+static std::mutex g_capture_mutex;
 constexpr int kStreamSlots = 512;
 static StreamSlot g_streams[kStreamSlots];
 static std::atomic<bool> g_operators{false}, g_streams_full{false};
@@ -428,23 +432,55 @@ void mark_operator(cudaStream_t s) {
   g_operators.store(true, std::memory_order_release);
 }
 
+// The capture that `s` is part of (0: none) and the node it depends on (null: none, or several).
+static unsigned long long capture_of(cudaStream_t s, cudaGraphNode_t* node) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  const cudaGraphNode_t* nodes = nullptr;
+  size_t n = 0;
+  *node = nullptr;
+  if (cudaStreamGetCaptureInfo(s, &status, &id, nullptr, &nodes, nullptr, &n) != cudaSuccess) {
+    cudaGetLastError();   // the launch reports it
+    return 0;
+  }
+  if (status == cudaStreamCaptureStatusNone) return 0;
+  if (n == 1) *node = nodes[0];
+  return id;
+}
+
 StreamOrder behind_operators(cudaStream_t s) {
   StreamOrder o;
   if (!g_operators.load(std::memory_order_acquire)) return o;
   o.full = g_streams_full.load() || s == cudaStreamPerThread;
   if (o.full) return o;
-  StreamSlot* m = stream_slot(s, false);
-  if (!m) return o;
-  o.upto = m->operators.load(std::memory_order_acquire);
-  o.full = o.upto > m->covered.load(std::memory_order_acquire);
-  if (o.full) o.covered = &m->covered;
+  cudaGraphNode_t node;
+  o.capture = capture_of(s, &node);
+  StreamSlot* m = stream_slot(s, o.capture != 0);
+  if (o.capture) {
+    o.slot = m;
+    std::lock_guard<std::mutex> lock(g_capture_mutex);
+    o.full = !m || !node || m->capture != o.capture || m->node != node;
+  } else if (m) {
+    o.upto = m->operators.load(std::memory_order_acquire);
+    o.full = o.upto > m->covered.load(std::memory_order_acquire);
+    if (o.full) o.slot = m;
+  }
   return o;
 }
 
-void cover_operators(const StreamOrder& o) {
-  if (!o.covered) return;
-  unsigned long long c = o.covered->load(std::memory_order_relaxed);
-  while (c < o.upto && !o.covered->compare_exchange_weak(c, o.upto, std::memory_order_release)) {
+void cover_operators(const StreamOrder& o, cudaStream_t s) {
+  if (!o.slot) return;
+  if (o.capture) {
+    cudaGraphNode_t node;
+    const unsigned long long id = capture_of(s, &node);
+    std::lock_guard<std::mutex> lock(g_capture_mutex);
+    o.slot->capture = node ? id : 0;
+    o.slot->node = node;
+    return;
+  }
+  std::atomic<unsigned long long>& covered = o.slot->covered;
+  unsigned long long c = covered.load(std::memory_order_relaxed);
+  while (c < o.upto && !covered.compare_exchange_weak(c, o.upto, std::memory_order_release)) {
   }
 }
 

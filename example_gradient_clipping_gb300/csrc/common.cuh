@@ -218,14 +218,20 @@ void count_launch(unsigned n = 1);
 // no ordinary launch has come behind yet.  Operators are counted per stream once they are launched, and
 // count as covered only when the launch behind them has succeeded, up to the count that it saw before
 // it: so host threads that share a stream cannot lose one between another's look and its launch.
+// In a stream capture nothing is put on the stream, so nothing is covered; and every kernel that the
+// stream depends on there, also one joined from another stream by an event, would become one that the
+// launch may start under.  So a captured launch is an ordinary one unless the stream depends on the
+// library's last (operators apart) captured launch on it alone.
+struct StreamSlot;
 struct StreamOrder {
   bool full = false;
-  std::atomic<unsigned long long>* covered = nullptr;
-  unsigned long long upto = 0;
+  StreamSlot* slot = nullptr;        // to be told of the launch
+  unsigned long long upto = 0;       // operators that it covers
+  unsigned long long capture = 0;    // the capture it is part of
 };
 StreamOrder behind_operators(cudaStream_t s);
-void cover_operators(const StreamOrder& o);   // after the launch
-void mark_operator(cudaStream_t s);           // after an operator's launch
+void cover_operators(const StreamOrder& o, cudaStream_t s);   // after the launch
+void mark_operator(cudaStream_t s);                           // after an operator's launch
 
 // Launch with programmatic stream serialization (see pdl_wait); counts the launch.
 // `pdl` false gives ordinary stream order (the kernel's pdl_wait is then a no-op): the
@@ -264,15 +270,17 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
                        Args&&... args) {
   const StreamOrder order = behind_operators(s);
   const cudaError_t e = launch_k(!order.full, kernel, grid, block, smem, s, static_cast<Args&&>(args)...);
-  if (e == cudaSuccess) cover_operators(order);
+  if (e == cudaSuccess) cover_operators(order, s);
   return e;
 }
 template <typename... KArgs, typename... Args>
 cudaError_t launch_plain(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                          Args&&... args) {
-  return launch_k(false, kernel, grid, block, smem, s, static_cast<Args&&>(args)...);
+  const StreamOrder order = behind_operators(s);
+  const cudaError_t e = launch_k(false, kernel, grid, block, smem, s, static_cast<Args&&>(args)...);
+  if (e == cudaSuccess) cover_operators(order, s);
+  return e;
 }
-// Counts kernels the library launched (reported by dp_launch_count).
 // Descriptor validation and the thread-local error message, shared by entry points.
 dp_status geom_from_desc(const dp_layer_desc* d, Geom* g);
 dp_status set_error(dp_status st, const char* msg);

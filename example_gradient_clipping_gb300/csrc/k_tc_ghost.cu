@@ -563,7 +563,7 @@ static cudaError_t run_ghost(const Geom& g, const CUtensorMap& ma, const CUtenso
   cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, tcghost::tc_ghost_kernel, ma, mg, ma1, mg1, P);
   count_launch();
-  if (e == cudaSuccess) cover_operators(order);
+  if (e == cudaSuccess) cover_operators(order, s);
   return e;
 }
 

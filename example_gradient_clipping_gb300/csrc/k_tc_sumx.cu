@@ -868,7 +868,7 @@ cudaError_t launch_tc_sumx(const Geom& g, const void* A, const void* G, const fl
                       ? cudaLaunchKernelEx(&cfg, tcsumx::tc_sumx_kernel<false, true>, mg64, ma64, mg16, ma16, P)
                       : cudaLaunchKernelEx(&cfg, tcsumx::tc_sumx_kernel<false, false>, mg64, ma64, mg16, ma16, P);
   count_launch();
-  if (e == cudaSuccess) cover_operators(order);
+  if (e == cudaSuccess) cover_operators(order, s);
   if (e == cudaSuccess && bias_nt > 1) {   // the column tiles' partial biases, in order
     e = launch_reduce_splits(P.bias_part, bias_nt, (size_t)g.p, db, accumulate, s, nz, nz ? nz->off_b : 0);
     if (nz && nz->on) nz->applied_b = 1;

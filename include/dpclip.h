@@ -30,7 +30,8 @@
  *    complete before the previous such kernel in the stream starts: never written by
  *    a kernel that itself triggers programmatic launch right before the call.  The
  *    library's sequence operators (dpclip_seq.h) may write them: the next other call on
- *    the same stream waits for the operators in full.  Nothing else here writes A or G.
+ *    the same stream waits for the operators in full, in a stream capture also for those
+ *    joined from other streams.  Nothing else here writes A or G.
  *  - Layouts (row-major, contiguous, PyTorch conventions):
  *      linear: A [B, T, d], G [B, T, p]; weight gradient [p, d]
  *      conv2d: A [B, Cin, H, W] (NCHW), G [B, p, Hout, Wout]; weight gradient

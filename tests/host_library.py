@@ -40,7 +40,7 @@ class Host:
                 g = getattr(self.so, name)
                 g.restype, g.argtypes = f.restype, f.argtypes
         self.so.fake_kernel.restype = ctypes.c_char_p
-        self.so.fake_capture.argtypes = [ctypes.c_ulonglong] * 2
+        self.so.fake_capture.argtypes = self.so.fake_join.argtypes = [ctypes.c_ulonglong] * 2
         self.hook_type = ctypes.CFUNCTYPE(None)
 
     @contextlib.contextmanager

@@ -2,7 +2,8 @@
 // objects are linked with this file in place of the runtime.  Nothing is ever launched.  A launch is
 // written to a log (kernel, device, stream, whether it may start under the launch before it) and refused
 // as the runtime refuses it when it wants more dynamic shared memory than the kernel was allowed on
-// the current device.  `fake_hook` is called inside every launch, so that a test can make
+// the current device.  On a stream that a test has set to capture, a launch becomes the one node that the
+// stream depends on.  `fake_hook` is called inside every launch, so that a test can make
 // another call there, as another host thread would.
 #include <cuda_runtime.h>
 
@@ -28,7 +29,12 @@ std::map<const void*, std::string>& names() {
 }
 std::map<std::pair<const void*, int>, int> allowed;   // dynamic shared memory by kernel and device
 std::vector<Launch> launches;
-std::map<unsigned long long, unsigned long long> capturing;   // stream -> capture
+struct Capture {
+  unsigned long long id;
+  std::vector<cudaGraphNode_t> nodes;   // that the stream depends on
+};
+std::map<unsigned long long, Capture> capturing;   // by stream
+uintptr_t nodes_made = 0;
 thread_local int device = 0;
 thread_local cudaError_t last_error = cudaSuccess;
 int attribute_failures = 0, attribute_calls = 0, launch_failures = 0;
@@ -83,11 +89,15 @@ cudaError_t cudaFuncSetAttribute(const void* fn, cudaFuncAttribute a, int v) {
   return cudaSuccess;
 }
 cudaError_t cudaStreamGetCaptureInfo(cudaStream_t s, cudaStreamCaptureStatus* status, unsigned long long* id,
-                                     cudaGraph_t*, const cudaGraphNode_t**, const cudaGraphEdgeData**, size_t*) {
+                                     cudaGraph_t*, const cudaGraphNode_t** nodes, const cudaGraphEdgeData**,
+                                     size_t* n) {
   std::lock_guard<std::recursive_mutex> lock(mu);
   const auto it = capturing.find((unsigned long long)(uintptr_t)s);
   *status = it == capturing.end() ? cudaStreamCaptureStatusNone : cudaStreamCaptureStatusActive;
-  if (id && it != capturing.end()) *id = it->second;
+  if (it == capturing.end()) return cudaSuccess;
+  if (id) *id = it->second.id;
+  if (nodes) *nodes = it->second.nodes.data();
+  if (n) *n = it->second.nodes.size();
   return cudaSuccess;
 }
 cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* fn, void**) {
@@ -112,6 +122,8 @@ cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* fn, voi
     l.status = cudaErrorInvalidValue;
   }
   launches.push_back(l);
+  const auto cap = capturing.find(l.stream);
+  if (cap != capturing.end() && !l.status) cap->second.nodes = {(cudaGraphNode_t)(16 * ++nodes_made)};
   if (l.status) last_error = (cudaError_t)l.status;
   return (cudaError_t)l.status;
 }
@@ -129,8 +141,18 @@ cudaError_t cudaGetDriverEntryPointByVersion(const char*, void** p, unsigned, un
 void fake_device(int d) { device = d; }
 void fake_hook(void (*h)()) { hook = h; }   // called once, inside the next launch and before it
 void fake_capture(unsigned long long stream, unsigned long long id) {   // id 0: the capture ends
-  if (id) capturing[stream] = id;
+  if (id) capturing[stream] = {id, {}};
   else capturing.erase(stream);
+}
+// `stream` waits for an event that was recorded on `other`, or (other == stream) another library's kernel
+void fake_join(unsigned long long stream, unsigned long long other) {
+  if (stream == other) {
+    capturing[stream].nodes = {(cudaGraphNode_t)(16 * ++nodes_made)};
+    return;
+  }
+  Capture& c = capturing[stream];
+  c.id = capturing[other].id;
+  for (cudaGraphNode_t n : capturing[other].nodes) c.nodes.push_back(n);
 }
 void fake_fail_attributes(int n) { attribute_failures = n; }
 void fake_fail_launches(int n) { launch_failures = n; }

@@ -156,6 +156,65 @@ def test_a_launch_that_failed_covers_nothing(fake):
     assert _early(fake) == [True]
 
 
+_captures = iter(range(1, 1 << 20))
+
+
+def test_a_captured_launch_covers_no_operator_on_the_stream(fake):
+    """Nothing is put on the stream: what is launched after the capture still waits."""
+    s = next(_streams)
+    _operator(fake, s)
+    fake.so.fake_capture(s, next(_captures))
+    _noise(fake, s)
+    fake.so.fake_capture(s, 0)
+    fake.launches()
+    _noise(fake, s)
+    _noise(fake, s)
+    assert _early(fake) == [False, True]
+
+
+@pytest.mark.parametrize("call", CALLS, ids=["ghost", "instantiate", "ghost-split", "sum", "noise"])
+def test_captured_behind_an_operator(fake, call):
+    s = next(_streams)
+    for _ in range(2):   # a stream is captured again
+        fake.so.fake_capture(s, next(_captures))
+        _noise(fake, s)
+        fake.launches()
+        _noise(fake, s)
+        assert _early(fake) == [True]
+        _operator(fake, s)
+        call(fake, s)
+        first, *rest = _early(fake)
+        assert not first and all(rest)
+        call(fake, s)
+        assert all(_early(fake))
+        fake.so.fake_capture(s, 0)
+
+
+def test_captured_behind_an_operator_of_another_stream(fake):
+    """An event's wait makes the operator one of the kernels that the launch would start under."""
+    a, b = next(_streams), next(_streams)
+    fake.so.fake_capture(a, next(_captures))
+    _operator(fake, a)
+    fake.so.fake_join(b, a)
+    _norm(fake, b)
+    assert _early(fake)[0] is False
+    _norm(fake, b)
+    assert all(_early(fake))
+    _operator(fake, a)
+    fake.so.fake_join(b, a)      # now behind its own last launch and the operator
+    _norm(fake, b)
+    assert _early(fake)[0] is False
+    _norm(fake, b)
+    assert all(_early(fake))
+    _operator(fake, a)
+    fake.so.fake_join(a, a)      # another library's kernel behind the operator
+    fake.so.fake_join(b, a)
+    _norm(fake, b)
+    assert _early(fake)[0] is False
+    for x in (a, b):
+        fake.so.fake_capture(x, 0)
+
+
 def test_the_per_thread_stream_and_more_streams_than_slots():
     """A process of its own: from then on every launch waits."""
     code = """
