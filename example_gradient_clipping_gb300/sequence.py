@@ -142,7 +142,9 @@ def _vector(x, ref, shape, dtypes, name: str) -> None:
 # Descriptors by what the checks and the descriptor look at of a call's tensors (shapes, strides,
 # types and devices, never addresses or values) and by its options: a call like one that was
 # checked before is neither checked nor described again.  The calls are a few microseconds of
-# kernel at their smallest, so what is done per call is kept short.
+# kernel at their smallest, so what is done per call is kept short.  Options are plain numbers
+# before they are part of a key: one held in a tensor would be found by its identity, with the
+# value that it had at an earlier call.
 _descs: dict = {}
 _get, _empty, _f32 = _descs.get, torch.empty, torch.float32
 _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
@@ -220,8 +222,8 @@ def _rotary_desc(q, k, table, positions, interleaved, inverse):
         raise ValueError("table: the contiguous fp32 [P, R] tensor of rotary_table, on q's device")
     _vector(positions, q, (B, T), _INTS, "positions")
     Hk = k.shape[2] if k is not None else 0
-    return RotaryDesc(_DTYPES[q.dtype], B, T, Hq, Hk, D, table.shape[1], table.shape[0], int(bool(interleaved)),
-                      int(bool(inverse)), int(positions is not None and positions.dtype == torch.int64),
+    return RotaryDesc(_DTYPES[q.dtype], B, T, Hq, Hk, D, table.shape[1], table.shape[0], int(interleaved),
+                      int(inverse), int(positions is not None and positions.dtype == torch.int64),
                       Strides(*q.stride()[:3]), Strides(*(k.stride()[:3] if k is not None else (0, 0, 0))),
                       Strides(T * Hq * D, Hq * D, D), Strides(T * Hk * D, Hk * D, D))
 
@@ -267,6 +269,7 @@ def rotary(q, k, table, positions=None, interleaved: bool = False, inverse: bool
     """(q', k') with the first table.shape[1] entries of every head turned by their position's
     angles; k may be None.  positions: int32 or int64 [B, T], None for 0 .. T - 1.  inverse
     turns back (and is the gradient)."""
+    interleaved, inverse = bool(interleaved), bool(inverse)
     if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
         if stream is not None:
             raise ValueError("a differentiable call runs on the current stream")
@@ -290,7 +293,7 @@ def _attn_desc(q, k, v, q_lens, k_lens, causal, window, scale, more=None):
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not fit q {tuple(q.shape)}")
     _vector(q_lens, q, (B,), (torch.int32,), "q_lens")
     _vector(k_lens, q, (B,), (torch.int32,), "k_lens")
-    d = AttnDesc(_DTYPES[q.dtype], B, T, S, Hq, Hk, D, int(bool(causal)), int(window), float(scale or 0.0))
+    d = AttnDesc(_DTYPES[q.dtype], B, T, S, Hq, Hk, D, int(causal), window, scale or 0.0)
     own, kv = Strides(T * Hq * D, Hq * D, D), Strides(S * Hk * D, Hk * D, D)   # of the results
     d.q, d.k, d.v, d.o = Strides(*q.stride()[:3]), Strides(*k.stride()[:3]), Strides(*v.stride()[:3]), own
     if more is not None:
@@ -306,6 +309,10 @@ def _attn_desc(q, k, v, q_lens, k_lens, causal, window, scale, more=None):
     return d
 
 
+def _options(causal, window, scale):
+    return bool(causal), int(window), None if scale is None else float(scale)
+
+
 def attention_forward(q, k, v, causal: bool = False, window: int = 0, scale: Optional[float] = None, q_lens=None,
                       k_lens=None, stream=None):
     """(o, lse): attention of q [B, T, Hq, D] over k, v [B, S, Hk, D] and each query's log-sum-exp
@@ -315,6 +322,7 @@ def attention_forward(q, k, v, causal: bool = False, window: int = 0, scale: Opt
     if stream is not None:
         with _on(stream, q.device):
             return attention_forward(q, k, v, causal, window, scale, q_lens, k_lens)
+    causal, window, scale = _options(causal, window, scale)
     shape, dtype, dev = q.shape, q.dtype, q.get_device()
     key = (shape, q.stride(), dtype, dev, k.shape, k.stride(), k.dtype, k.get_device(), v.shape, v.stride(), v.dtype,
            v.get_device(), causal, window, scale, None if q_lens is None else _opt(q_lens),
@@ -338,6 +346,7 @@ def attention_backward(q, k, v, o, lse, do, causal: bool = False, window: int = 
     if stream is not None:
         with _on(stream, q.device):
             return attention_backward(q, k, v, o, lse, do, causal, window, scale, q_lens, k_lens)
+    causal, window, scale = _options(causal, window, scale)
     shape, dtype, dev = q.shape, q.dtype, q.get_device()
     key = (shape, q.stride(), dtype, dev, k.shape, k.stride(), k.dtype, k.get_device(), v.shape, v.stride(), v.dtype,
            v.get_device(), causal, window, scale, None if q_lens is None else _opt(q_lens),
@@ -375,7 +384,7 @@ class _Attention(torch.autograd.Function):
 def attention(q, k, v, causal: bool = False, window: int = 0, scale: Optional[float] = None, q_lens=None, k_lens=None):
     """attention_forward's o, with its gradient."""
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
-        return _Attention.apply(q, k, v, causal, window, scale, q_lens, k_lens)
+        return _Attention.apply(q, k, v, *_options(causal, window, scale), q_lens, k_lens)
     return attention_forward(q, k, v, causal, window, scale, q_lens, k_lens)[0]
 
 
@@ -398,13 +407,14 @@ def _distill_desc(logits, indices, teacher, labels, weights, upstream, temperatu
     _vector(upstream, logits, (B,), (torch.float32,), "upstream")
     return DistillDesc(_DTYPES[logits.dtype], _DTYPES[teacher.dtype], B, T, V, K, int(indices.dtype == torch.int64),
                        int(labels is not None and labels.dtype == torch.int64), sr if T > 1 else sb if B > 1 else V, V,
-                       float(temperature), float(alpha))
+                       temperature, alpha)
 
 
 def _distill(logits, indices, teacher, labels, weights, upstream, temperature, alpha, want_loss, want_grad, stream=None):
     if stream is not None:
         with _on(stream, logits.device):
             return _distill(logits, indices, teacher, labels, weights, upstream, temperature, alpha, want_loss, want_grad)
+    temperature, alpha = float(temperature), float(alpha)
     shape, dtype, dev = logits.shape, logits.dtype, logits.get_device()
     key = (shape, logits.stride(), dtype, dev, indices.shape, indices.stride(), indices.dtype, indices.get_device(),
            teacher.shape, teacher.stride(), teacher.dtype, teacher.get_device(), temperature, alpha, _opt(labels),
@@ -452,7 +462,7 @@ def distill_loss(logits, indices, teacher, labels=None, weights=None, temperatur
     if torch.is_grad_enabled() and logits.requires_grad:
         if stream is not None:
             raise ValueError("a differentiable call runs on the current stream")
-        return _Distill.apply(logits, indices, teacher, labels, weights, temperature, alpha)
+        return _Distill.apply(logits, indices, teacher, labels, weights, float(temperature), float(alpha))
     return _distill(logits, indices, teacher, labels, weights, None, temperature, alpha, True, False, stream)[:2]
 
 
