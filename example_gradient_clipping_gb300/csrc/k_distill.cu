@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
         if (P.row_loss) {
           float kl = 0.f;
           for (int j = lane; j < P.K; j += 32)
-            if (sp[j] > 0.f) kl += sp[j] * (logf(sp[j]) - rel(sz[j]) * kLn2);
+            if (sp[j] != 0.f) kl += sp[j] * (logf(sp[j]) - rel(sz[j]) * kLn2);   // (NaN counts)
           kl = warp_sum(kl);
           if (lane == 0) {
             float l = ct != 0.f ? ct * P.tau * P.tau * (kl + logf(st)) : 0.f;

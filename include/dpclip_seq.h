@@ -119,7 +119,8 @@ dp_status dp_attention_grad(const dp_attn_desc* desc, const void* Q, const void*
  *   dz = g_i w [ (1 - alpha) tau (q - sum_j p_j e_{k_j}) + alpha (softmax(z) - e_y) ],
  * g_i the upstream gradient of loss_i.  A row without a teacher entry has no teacher term, a
  * label < 0 no label term; a row of weight 0 is not read and its gradient is 0.  An entry
- * that occurs twice counts twice.  p_j = 0 adds nothing, whatever q.  An index or label
+ * that occurs twice counts twice.  p_j = 0 adds nothing, whatever q.  A teacher's NaN or +inf, or
+ * nothing but -inf, makes its row's loss NaN.  An index or label
  * >= V sets the device status DP_ERR_INVALID_ARG, and its row's loss is NaN. */
 typedef struct {
   int dtype;               /* dp_dtype of logits and dlogits */

@@ -76,3 +76,40 @@ def test_the_gradient_goes_by_the_forward_calls_options(lib):
     inverse.fill_(True)
     y1.backward(do)
     assert torch.equal(x.grad, lib.rotary(do, None, table, inverse=True)[0])
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("V", [50, 40001])
+@pytest.mark.parametrize("tau,alpha", [(1.0, 0.0), (2.0, 0.25), (3.0, 0.25)])
+def test_distill_with_a_teacher_that_is_not_finite(lib, dtype, V, tau, alpha):
+    """A softmax over NaN, +inf or nothing but -inf is NaN, and so is the row's loss and its gradient at the
+    teacher's entries; one -inf among others is a probability of 0.  Other rows keep their bits."""
+    import math
+
+    import torch
+    z, idx, top, y = _rows(2, 4, V, 5)
+    idx = torch.arange(5, device="cuda").expand(2, 4, 5).contiguous() * 9
+    z, top = z.to(getattr(torch, dtype)), top.to(getattr(torch, dtype))
+    idx[1, 3, 4] = -1
+    kw = dict(labels=y, temperature=tau, alpha=alpha)
+    clean, clean_rows = lib.distill_loss(z, idx, top, **kw)
+    clean_grad = lib.distill_loss_and_grad(z, idx, top, **kw)[1]
+    bad = top.clone()
+    bad[0, 1, 2], bad[0, 3, 0], bad[1, 3, :4] = math.nan, math.inf, -math.inf
+    bad[1, 3, 4] = math.nan            # not an entry
+    bad[1, 1, 1] = -math.inf
+    off = torch.zeros(2, 4, dtype=torch.bool, device="cuda")
+    off[0, 1] = off[0, 3] = off[1, 3] = True
+    loss, rows = lib.distill_loss(z, idx, bad, **kw)
+    both, grad = lib.distill_loss_and_grad(z, idx, bad, **kw)
+    assert torch.equal(torch.isnan(rows), off)
+    assert torch.isnan(loss).all() and torch.isnan(both).all()
+    for t in range(4):
+        for b in range(2):
+            if off[b, t]:
+                hit = torch.zeros(V, dtype=torch.bool, device="cuda")
+                hit[idx[b, t][idx[b, t] >= 0]] = True
+                assert torch.equal(torch.isnan(grad[b, t]), hit)
+            elif (b, t) != (1, 1):
+                assert torch.equal(rows[b, t], clean_rows[b, t]) and torch.equal(grad[b, t], clean_grad[b, t])
+    assert torch.isfinite(grad[1, 1]).all() and torch.isfinite(clean).all()
