@@ -13,7 +13,9 @@ attention_backward and distill_loss_and_grad are the same computations without i
 functions marshal the arguments of the C entry points of include/dpclip_seq.h, which states
 the formulas.  Work goes to the current stream of the tensors' device, or to `stream` as if it
 were the current one: results and workspaces are allocated by torch for that stream, and the
-usual rules for using a tensor on another stream apply.  An argument that does not fit raises ValueError (or DPError, from the C side) before anything is launched.
+usual rules for using a tensor on another stream apply.  An argument that does not fit raises ValueError (or
+DPError, from the C side) before anything is launched.  Second and forward-mode derivatives are not there
+and raise an error.  The kernels are launched past torch's dispatcher, so torch.jit.trace does not record them.
 """
 from __future__ import annotations
 
@@ -22,6 +24,7 @@ import ctypes
 from typing import Optional
 
 import torch
+import torch.autograd.forward_ad as _forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import DP_BF16, DP_FP32, _check, _lib, _ptr, _stream
@@ -162,6 +165,12 @@ def _opt(x):
     return None if x is None else (x.shape, x.stride(), x.dtype, x.get_device())
 
 
+def _no_tangents(*xs):
+    """Forward-mode tangents would be dropped without a word: the kernels see addresses."""
+    if any(x is not None and _forward_ad.unpack_dual(x).tangent is not None for x in xs):
+        raise NotImplementedError("the sequence operators have no forward-mode derivatives")
+
+
 def _on(stream, device):
     """`stream` (a torch stream or a handle) as the current one: what the call allocates then
     belongs to it, and a workspace that is dropped on return is not handed to another stream's
@@ -229,6 +238,8 @@ def _rotary_desc(q, k, table, positions, interleaved, inverse):
 
 
 def _rotary(q, k, table, positions, interleaved, inverse):
+    if _forward_ad._current_level >= 0:
+        _no_tangents(q, k, table)
     shape, dtype, dev = q.shape, q.dtype, q.get_device()
     key = (shape, q.stride(), dtype, dev, table.shape, table.stride(), table.dtype, table.get_device(), interleaved,
            inverse, None if k is None else (k.shape, k.stride(), k.dtype, k.get_device()),
@@ -322,6 +333,8 @@ def attention_forward(q, k, v, causal: bool = False, window: int = 0, scale: Opt
     if stream is not None:
         with _on(stream, q.device):
             return attention_forward(q, k, v, causal, window, scale, q_lens, k_lens)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(q, k, v)
     causal, window, scale = _options(causal, window, scale)
     shape, dtype, dev = q.shape, q.dtype, q.get_device()
     key = (shape, q.stride(), dtype, dev, k.shape, k.stride(), k.dtype, k.get_device(), v.shape, v.stride(), v.dtype,
@@ -346,6 +359,8 @@ def attention_backward(q, k, v, o, lse, do, causal: bool = False, window: int = 
     if stream is not None:
         with _on(stream, q.device):
             return attention_backward(q, k, v, o, lse, do, causal, window, scale, q_lens, k_lens)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(q, k, v, o, lse, do)
     causal, window, scale = _options(causal, window, scale)
     shape, dtype, dev = q.shape, q.dtype, q.get_device()
     key = (shape, q.stride(), dtype, dev, k.shape, k.stride(), k.dtype, k.get_device(), v.shape, v.stride(), v.dtype,
@@ -414,6 +429,8 @@ def _distill(logits, indices, teacher, labels, weights, upstream, temperature, a
     if stream is not None:
         with _on(stream, logits.device):
             return _distill(logits, indices, teacher, labels, weights, upstream, temperature, alpha, want_loss, want_grad)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(logits, teacher, weights, upstream)
     temperature, alpha = float(temperature), float(alpha)
     shape, dtype, dev = logits.shape, logits.dtype, logits.get_device()
     key = (shape, logits.stride(), dtype, dev, indices.shape, indices.stride(), indices.dtype, indices.get_device(),

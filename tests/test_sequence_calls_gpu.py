@@ -113,3 +113,34 @@ def test_distill_with_a_teacher_that_is_not_finite(lib, dtype, V, tau, alpha):
             elif (b, t) != (1, 1):
                 assert torch.equal(rows[b, t], clean_rows[b, t]) and torch.equal(grad[b, t], clean_grad[b, t])
     assert torch.isfinite(grad[1, 1]).all() and torch.isfinite(clean).all()
+
+
+def test_forward_mode_is_an_error(lib):
+    """The operators have no forward-mode derivative: a tangent must not vanish without a word, with or
+    without grad mode.  Inside a dual level without tangents they work as ever."""
+    import torch
+    import torch.autograd.forward_ad as fw
+    z, idx, top, y = _rows()
+    w = torch.ones(2, 3, device="cuda")
+    q, k, v, do = (_heads(2, 40, 2, 64, dtype="float32", seed=i) for i in range(4))
+    table = lib.rotary_table(64, 40)
+    calls = [
+        (lambda a, b, c: lib.attention(a, b, c), (q, k, v)),
+        (lambda a, b, c: lib.attention_forward(a, b, c)[0], (q, k, v)),
+        (lambda a, b, c: lib.rotary(a, b, c)[0], (q, k, table)),
+        (lambda a, b, c: lib.distill_loss(a, idx, b, labels=y, weights=c, alpha=0.5)[0], (z, top, w)),
+        (lambda a, b, c: lib.distill_loss_and_grad(a, idx, b, weights=w, upstream=c)[0], (z, top, torch.ones(2, device="cuda"))),
+    ]
+    o, lse = lib.attention_forward(q, k, v)
+    calls.append((lambda a, b, c: lib.attention_backward(q, a, v, b, lse, c)[0], (k, o, do)))
+    for f, xs in calls:
+        want = f(*xs)
+        with fw.dual_level():
+            assert torch.equal(f(*xs), want)
+            for i in range(3):
+                dual = list(xs)
+                dual[i] = fw.make_dual(xs[i], torch.ones_like(xs[i]))
+                for mode in (torch.enable_grad, torch.no_grad):
+                    with mode(), pytest.raises(NotImplementedError, match="forward"):
+                        f(*dual)
+        assert torch.equal(f(*xs), want)
