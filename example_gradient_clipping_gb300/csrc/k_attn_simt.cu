@@ -391,8 +391,7 @@ inline bool async_ok(const AttnParams& P, bool grad) {
 template <class E, int DP, bool kAsync>
 cudaError_t fwd(const AttnParams& P, cudaStream_t s) {
   constexpr int smem = fwd_smem<DP>();
-  static const cudaError_t set =
-      cudaFuncSetAttribute(attn_fwd_kernel<E, DP, kAsync>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t set = dph::allow_smem<attn_fwd_kernel<E, DP, kAsync>>(smem);
   if (set != cudaSuccess) return set;
   const unsigned grid = (unsigned)((size_t)P.B * P.Hq * ((P.T + BT - 1) / BT));
   return dph::launch_operator(attn_fwd_kernel<E, DP, kAsync>, grid, kThreads, smem, s, P);
@@ -401,8 +400,7 @@ cudaError_t fwd(const AttnParams& P, cudaStream_t s) {
 template <class E, int DP, bool kAsync>
 cudaError_t grad(const AttnParams& P, cudaStream_t s) {
   constexpr int smem = grad_smem<DP>();
-  static const cudaError_t set =
-      cudaFuncSetAttribute(attn_grad_kernel<E, DP, kAsync>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t set = dph::allow_smem<attn_grad_kernel<E, DP, kAsync>>(smem);
   if (set != cudaSuccess) return set;
   const int key_ctas = P.B * P.Hk * ((P.S + BT - 1) / BT), query_ctas = P.B * P.Hq * ((P.T + BT - 1) / BT);
   return dph::launch_operator(attn_grad_kernel<E, DP, kAsync>, (unsigned)(key_ctas + query_ctas), kThreads, smem, s, P,

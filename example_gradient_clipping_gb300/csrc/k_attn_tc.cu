@@ -319,8 +319,7 @@ template <int DP, int NT>
 static cudaError_t run_fwd(const AttnParams& P, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                            cudaStream_t s) {
   using C = attntc::Fwd<DP, NT>;
-  static const cudaError_t set = cudaFuncSetAttribute(attntc::attn_tc_fwd_kernel<DP, NT>,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  const cudaError_t set = allow_smem<attntc::attn_tc_fwd_kernel<DP, NT>>(C::SMEM);
   if (set != cudaSuccess) return set;
   const unsigned grid = (unsigned)((size_t)P.B * P.Hq * ((P.T + NT * attntc::BT - 1) / (NT * attntc::BT)));
   return launch_operator(attntc::attn_tc_fwd_kernel<DP, NT>, grid, C::THREADS, C::SMEM, s, mq, mk, mv, P);

@@ -543,8 +543,7 @@ static cudaError_t run_grad(const AttnParams& P, const attntc::GradSplit& sp, co
                             const CUtensorMap (&k)[2], cudaStream_t s) {
   using C = attntc::Grad<DP, true>;
   static_assert(C::SMEM >= attntc::Grad<DP, false>::SMEM, "one launch serves both sides");
-  static const cudaError_t set = cudaFuncSetAttribute(attntc::attn_tc_grad_kernel<DP>,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  const cudaError_t set = allow_smem<attntc::attn_tc_grad_kernel<DP>>(C::SMEM);
   if (set != cudaSuccess) return set;
   return launch_operator(attntc::attn_tc_grad_kernel<DP>, (unsigned)(sp.key_ctas + sp.query_ctas), C::THREADS, C::SMEM, s, q[0],
                     q[1], k[0], k[1], P, sp);

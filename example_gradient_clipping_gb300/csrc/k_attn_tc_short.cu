@@ -431,8 +431,7 @@ bool attn_tc_short_supported(const AttnParams& P) {
 
 cudaError_t launch_attn_tc_short_grad(const AttnParams& P, cudaStream_t s) {
   namespace ns = attntc::shortseq;
-  static const cudaError_t set =
-      cudaFuncSetAttribute(ns::attn_tc_short_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ns::SMEM);
+  const cudaError_t set = allow_smem<ns::attn_tc_short_grad_kernel>(ns::SMEM);
   if (set != cudaSuccess) return set;
   CUtensorMap q, g, k, v, o;
   if (!map_heads(&q, P.Q, P.q, P.B, P.T, P.Hq, P.D) || !map_heads(&g, P.dO, P.d_o, P.B, P.T, P.Hq, P.D) ||

@@ -586,9 +586,7 @@ using namespace dpk;
 
 template <class E, int kMode>
 static cudaError_t run_distill(const DistillParams& P, cudaStream_t s) {
-  static const cudaError_t set =
-      cudaFuncSetAttribute(distill::distill_stream_kernel<E, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           distill::stream_smem(distill::kMaxK));
+  const cudaError_t set = allow_smem<distill::distill_stream_kernel<E, kMode>>(distill::stream_smem(distill::kMaxK));
   if (set != cudaSuccess) return set;
   // two CTAs per SM, one where many teacher entries take their shared memory
   const int smem = distill::stream_smem(P.K), per_sm = std::min(distill::kMinBlocks, 232448 / (smem + 1024));

@@ -138,6 +138,21 @@ struct DistillParams {
 }  // namespace dpk
 
 namespace dph {
+// Lets `Kernel` have `bytes` of dynamic shared memory on the current device, once for each device (the
+// attribute is the device's); a failure is not remembered.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool kept = dev >= 0 && dev < 64;
+  if (kept && set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (kept && e == cudaSuccess) set[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 cudaError_t launch_rotary_table(const dp_rotary_table_desc& d, float* table, cudaStream_t s);
 cudaError_t launch_rotary(const dpk::RotaryParams& P, int dtype, cudaStream_t s);
 // FFMA attention: both types, any strides, D <= 128.
