@@ -305,6 +305,8 @@ def _attn_desc(q, k, v, q_lens, k_lens, causal, window, scale, more=None):
     _vector(q_lens, q, (B,), (torch.int32,), "q_lens")
     _vector(k_lens, q, (B,), (torch.int32,), "k_lens")
     d = AttnDesc(_DTYPES[q.dtype], B, T, S, Hq, Hk, D, int(causal), window, scale or 0.0)
+    if scale is not None and d.scale == 0:   # which the C side reads as the default
+        raise ValueError(f"scale {scale}: 0 in fp32; None is 1/sqrt(D)")
     own, kv = Strides(T * Hq * D, Hq * D, D), Strides(S * Hk * D, Hk * D, D)   # of the results
     d.q, d.k, d.v, d.o = Strides(*q.stride()[:3]), Strides(*k.stride()[:3]), Strides(*v.stride()[:3]), own
     if more is not None:
@@ -329,7 +331,7 @@ def attention_forward(q, k, v, causal: bool = False, window: int = 0, scale: Opt
     """(o, lse): attention of q [B, T, Hq, D] over k, v [B, S, Hk, D] and each query's log-sum-exp
     fp32 [B, Hq, T].  q_lens, k_lens: int32 [B], how many leading rows of each example are
     there; causal aligns the last query with the last key; window > 0 keeps the latest
-    `window` keys.  scale defaults to 1/sqrt(D).  A query that sees no key gives 0 and -inf."""
+    `window` keys.  scale: > 0, None for 1/sqrt(D).  A query that sees no key gives 0 and -inf."""
     if stream is not None:
         with _on(stream, q.device):
             return attention_forward(q, k, v, causal, window, scale, q_lens, k_lens)

@@ -144,3 +144,21 @@ def test_forward_mode_is_an_error(lib):
                     with mode(), pytest.raises(NotImplementedError, match="forward"):
                         f(*dual)
         assert torch.equal(f(*xs), want)
+
+
+def test_a_scale_of_zero_is_refused(lib):
+    """The C entry points read 0 as 1/sqrt(D); a scale of 0 (or one that fp32 does not hold) asks for
+    something else, and None is there for the default."""
+    import torch
+    q, k, v, do = (_heads(2, 40, 2, 64, dtype="float32", seed=i) for i in range(4))
+    o, lse = lib.attention_forward(q, k, v, scale=None)
+    assert torch.equal(o, lib.attention_forward(q, k, v, scale=0.125)[0])
+    n = lib.dp_launch_count()
+    x = q.clone().requires_grad_()
+    for zero in (0.0, 0, -0.0, 1e-60, torch.tensor(0.0)):
+        for f in (lambda: lib.attention_forward(q, k, v, scale=zero), lambda: lib.attention(q, k, v, scale=zero),
+                  lambda: lib.attention(x, k, v, scale=zero),
+                  lambda: lib.attention_backward(q, k, v, o, lse, do, scale=zero)):
+            with pytest.raises(ValueError, match="scale"):
+                f()
+    assert lib.dp_launch_count() == n
