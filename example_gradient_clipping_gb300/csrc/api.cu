@@ -935,9 +935,21 @@ dp_status dp_check_status(cudaStream_t stream) {
     e = cudaMemcpy(st, &zero, sizeof(zero), cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return cuda_fail(e, "dp_check_status clear");
   }
-  if (v & dpk::kStatusTimeout) return fail(DP_ERR_TIMEOUT, "a bounded device wait gave up");
-  if (v & dpk::kStatusNonfinite) return fail(DP_ERR_NONFINITE, "a per-example norm was not finite");
-  if (v & dpk::kStatusIndex) return fail(DP_ERR_INVALID_ARG, "a position or index in device memory was out of range");
+  // the cause before its effect: what gave up left rows unwritten, a bad index leaves NaN, and the
+  // norms of either are not finite
+  static const struct { unsigned bit; dp_status status; const char* text; } kinds[] = {
+      {dpk::kStatusTimeout, DP_ERR_TIMEOUT, "a bounded device wait gave up"},
+      {dpk::kStatusIndex, DP_ERR_INVALID_ARG, "a position or index in device memory was out of range"},
+      {dpk::kStatusNonfinite, DP_ERR_NONFINITE, "a per-example norm was not finite"}};
+  dp_status first = DP_OK;
+  char text[256] = "";
+  for (const auto& k : kinds) {
+    if (!(v & k.bit)) continue;
+    if (first == DP_OK) first = k.status;
+    const size_t n = strlen(text);
+    snprintf(text + n, sizeof(text) - n, "%s%s", n ? "; " : "", k.text);
+  }
+  if (first != DP_OK) return fail(first, "%s", text);
   return ok();
 }
 

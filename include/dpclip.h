@@ -311,7 +311,8 @@ dp_status dp_clipped_sum_kept_noised(const dp_layer_desc* desc, const float* gra
 
 /* Synchronizes `stream`, returns the device status word (DP_OK, DP_ERR_NONFINITE,
  * DP_ERR_TIMEOUT, or DP_ERR_INVALID_ARG for a position or index in device memory out of its
- * range, dpclip_seq.h) raised since the last check, and clears it. */
+ * range, dpclip_seq.h) raised since the last check, and clears it.  Of several conditions the
+ * cause is returned (a wait that gave up, then an index, then a norm); the message names all. */
 dp_status dp_check_status(cudaStream_t stream);
 
 /* Diagnostic of the device-side failure path.  Launches (asynchronously, on `stream`)

@@ -162,3 +162,21 @@ def test_a_scale_of_zero_is_refused(lib):
             with pytest.raises(ValueError, match="scale"):
                 f()
     assert lib.dp_launch_count() == n
+
+
+def test_a_bad_position_is_reported_behind_the_norms_it_spoils(lib):
+    import torch
+    q = _heads(2, 8, 2, 64)
+    table = lib.rotary_table(64, 16)
+    pos = torch.arange(8, dtype=torch.int32, device="cuda").expand(2, 8).contiguous()
+    pos[1, 3] = 16
+    y = lib.rotary(q, None, table, positions=pos)[0]
+    o = lib.attention_forward(y, y, q)[0]
+    layer = lib.layer_desc(lib.DP_LINEAR, lib.DP_BF16, B=2, p=64, T=8, d=128)
+    ws = torch.empty(lib.dp_workspace_size(layer), dtype=torch.uint8, device="cuda")
+    sq, factors = torch.empty(1, 2, device="cuda"), torch.empty(1, 2, device="cuda")
+    lib.dp_layer_sqnorms(layer, o, _heads(2, 8, 64, seed=1), sq[0], ws)
+    lib.dp_clip_factors(sq, 2, 1, False, 1.0, factors)
+    assert lib.dp_check_status() == lib.DP_ERR_INVALID_ARG
+    assert torch.isfinite(sq[0, 0]) and torch.isnan(sq[0, 1])
+    assert lib.dp_check_status() == lib.DP_OK
