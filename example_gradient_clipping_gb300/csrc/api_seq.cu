@@ -63,7 +63,9 @@ dp_status attn_params(const dp_attn_desc* d, bool grad, dpk::AttnParams* P) {
   *P = {};
   P->B = d->B; P->T = d->T; P->S = d->S; P->Hq = d->Hq; P->Hk = d->Hk; P->D = d->D;
   P->causal = d->causal ? 1 : 0;
-  P->window = d->window >= d->T + d->S ? 0 : d->window;   // hides nothing
+  // No query sees past the last key: a window of S or more hides nothing (and T + window, of smaller
+  // ones, stays within 32 bits).
+  P->window = d->window >= d->S ? 0 : d->window;
   P->scale = d->scale > 0.f ? d->scale : (float)(1.0 / std::sqrt((double)d->D));
   P->q = d->q; P->k = d->k; P->v = d->v; P->o = d->o;
   P->d_o = d->d_o; P->dq = d->dq; P->dk = d->dk; P->dv = d->dv;

@@ -180,3 +180,23 @@ def test_a_bad_position_is_reported_behind_the_norms_it_spoils(lib):
     assert lib.dp_check_status() == lib.DP_ERR_INVALID_ARG
     assert torch.isfinite(sq[0, 0]) and torch.isnan(sq[0, 1])
     assert lib.dp_check_status() == lib.DP_OK
+
+
+def test_a_window_wider_than_the_keys_hides_nothing(lib):
+    """Up to the longest sequence and the widest window that are taken (their sum passes 32 bits): the
+    gradient of the few last queries, which alone see a key, as with no window."""
+    import torch
+    T, S = 1 << 30, 200
+    q, do = (torch.zeros(1, T, 1, 1, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q[:, -S:], do[:, -S:] = _heads(1, S, 1, 1), _heads(1, S, 1, 1, seed=1)
+    k, v = _heads(1, S, 1, 1, seed=2), _heads(1, S, 1, 1, seed=3)
+    o, lse = lib.attention_forward(q, k, v, causal=True)
+    want = lib.attention_backward(q, k, v, o, lse, do, causal=True)
+    assert want[1].any() and want[2].any()
+    for window in (S, T // 2, T + S // 2, T + S - 1, T + S, 2 ** 31 - 1):
+        got = lib.attention_backward(q, k, v, o, lse, do, causal=True, window=window)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), window
+        del got
+    last = lib.attention_forward(q[:, -S:].contiguous(), k, v, causal=True)
+    assert torch.equal(last[0], o[:, -S:]) and torch.equal(last[1], lse[..., -S:])
+    assert torch.isneginf(lse[..., :-S]).all()
