@@ -118,6 +118,7 @@ def dp_distill(desc: DistillDesc, logits, indices, teacher, labels=None, weights
 # ---- argument checks ------------------------------------------------------------------
 _DTYPES = {torch.bfloat16: DP_BF16, torch.float32: DP_FP32}
 _INTS = (torch.int32, torch.int64)
+_MOST = 2 ** 31 - 1   # of a size: the descriptors' fields are C ints, which ctypes would fill modulo 2^32
 
 
 def _heads(x, name: str) -> None:
@@ -125,6 +126,8 @@ def _heads(x, name: str) -> None:
         raise ValueError(f"{name}: a CUDA tensor [B, T, H, D], got {tuple(x.shape)} on {x.device}")
     if x.dtype not in _DTYPES:
         raise ValueError(f"{name}: bf16 or fp32, got {x.dtype}")
+    if max(x.shape) > _MOST:
+        raise ValueError(f"{name}: sizes up to {_MOST}, got {tuple(x.shape)}")
     if x.stride(3) != 1 and x.shape[3] > 1:
         raise ValueError(f"{name}: the innermost stride must be 1, got {x.stride()}")
 
@@ -205,8 +208,8 @@ def rotary_table(R: int, P: int, theta: float = 10000.0, scaling: str = "plain",
     "parts" (slow pairs interpolated, fast ones kept, by their turns over `context`)."""
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling {scaling!r}: one of {sorted(_SCALINGS)}")
-    if P <= 0 or R <= 0:
-        raise ValueError(f"P={P} and R={R} must be > 0")
+    if not (0 < P <= _MOST and 0 < R <= _MOST):
+        raise ValueError(f"P={P} and R={R} must be > 0 and up to {_MOST}")
     device = torch.get_default_device() if device is None else torch.device(device)
     if device.type != "cuda":
         raise ValueError(f"device: a CUDA device, got {device}")
@@ -227,7 +230,7 @@ def _rotary_desc(q, k, table, positions, interleaved, inverse):
         _like(k, q, "k")
         if k.shape[0] != B or k.shape[1] != T or k.shape[3] != D:
             raise ValueError(f"k {tuple(k.shape)} does not fit q {tuple(q.shape)}")
-    if table.dim() != 2 or table.dtype != torch.float32 or not table.is_contiguous() or table.device != q.device:
+    if table.dim() != 2 or max(table.shape) > _MOST or table.dtype != torch.float32 or not table.is_contiguous() or table.device != q.device:
         raise ValueError("table: the contiguous fp32 [P, R] tensor of rotary_table, on q's device")
     _vector(positions, q, (B, T), _INTS, "positions")
     Hk = k.shape[2] if k is not None else 0
@@ -323,7 +326,8 @@ def _attn_desc(q, k, v, q_lens, k_lens, causal, window, scale, more=None):
 
 
 def _options(causal, window, scale):
-    return bool(causal), int(window), None if scale is None else float(scale)
+    # a window past a C int's range hides nothing, as the largest in it (below it: refused, as -1)
+    return bool(causal), max(-1, min(int(window), _MOST)), None if scale is None else float(scale)
 
 
 def attention_forward(q, k, v, causal: bool = False, window: int = 0, scale: Optional[float] = None, q_lens=None,
@@ -410,6 +414,8 @@ def _distill_desc(logits, indices, teacher, labels, weights, upstream, temperatu
     if logits.dim() != 3 or not logits.is_cuda or logits.dtype not in _DTYPES or logits.shape[2] == 0:
         raise ValueError(f"logits: a bf16 or fp32 CUDA tensor [B, T, V], got {logits.dtype} {tuple(logits.shape)} on "
                          f"{logits.device}")
+    if max(logits.shape) > _MOST:
+        raise ValueError(f"logits: sizes up to {_MOST}, got {tuple(logits.shape)}")
     B, T, V = logits.shape
     sb, sr, sv = logits.stride()
     if (sv != 1 and V > 1) or (B > 1 and T > 1 and sb != T * sr):
@@ -422,7 +428,7 @@ def _distill_desc(logits, indices, teacher, labels, weights, upstream, temperatu
     _vector(labels, logits, (B, T), _INTS, "labels")
     _vector(weights, logits, (B, T), (torch.float32,), "weights")
     _vector(upstream, logits, (B,), (torch.float32,), "upstream")
-    return DistillDesc(_DTYPES[logits.dtype], _DTYPES[teacher.dtype], B, T, V, K, int(indices.dtype == torch.int64),
+    return DistillDesc(_DTYPES[logits.dtype], _DTYPES[teacher.dtype], B, T, V, min(K, _MOST), int(indices.dtype == torch.int64),
                        int(labels is not None and labels.dtype == torch.int64), sr if T > 1 else sb if B > 1 else V, V,
                        temperature, alpha)
 

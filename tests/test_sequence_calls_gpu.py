@@ -200,3 +200,34 @@ def test_a_window_wider_than_the_keys_hides_nothing(lib):
     last = lib.attention_forward(q[:, -S:].contiguous(), k, v, causal=True)
     assert torch.equal(last[0], o[:, -S:]) and torch.equal(last[1], lse[..., -S:])
     assert torch.isneginf(lse[..., :-S]).all()
+
+
+def test_sizes_and_windows_past_32_bits(lib):
+    """The descriptors hold 32-bit sizes: what does not fit is refused and not taken modulo 2^32, and a
+    window that does not fit hides nothing."""
+    import torch
+    n, far = lib.dp_launch_count(), (1 << 32) + 8
+    x = torch.zeros(1, 1, 1, 8, device="cuda")
+    table = torch.zeros(1, 8, device="cuda")
+    for shape in ((far, 1, 1, 8), (1, far, 1, 8), (1, 1, far, 8)):
+        big = x.expand(shape)
+        for f in (lambda: lib.rotary(big, None, table), lambda: lib.attention_forward(big, big, big),
+                  lambda: lib.attention_forward(x, *(x.expand(1, far, 1, 8),) * 2)):
+            with pytest.raises(ValueError, match="2147483647"):
+                f()
+    for f in (lambda: lib.rotary(x, None, torch.zeros(1, 8, device="cuda").expand(far, 8)),
+              lambda: lib.rotary_table(2, far), lambda: lib.rotary_table(far, 2)):
+        with pytest.raises(ValueError):
+            f()
+    z = torch.zeros(1, 1, 8, device="cuda").expand(far, 1, 8)
+    empty = torch.zeros(far, 1, 0, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="2147483647"):
+        lib.distill_loss(z, empty, empty.float())
+    assert lib.dp_launch_count() == n
+    q, k, v = (_heads(2, 40, 2, 64, seed=i) for i in range(3))
+    want = lib.attention_forward(q, k, v, causal=True)
+    for window in (1 << 31, far, 1 << 63, 1 << 70):
+        assert all(torch.equal(a, b) for a, b in zip(lib.attention_forward(q, k, v, causal=True, window=window), want))
+    for window in (-1, -far + 16, -(1 << 70)):
+        with pytest.raises(lib.DPError, match="window"):
+            lib.attention_forward(q, k, v, causal=True, window=window)
