@@ -253,11 +253,14 @@ cudaError_t launch_k(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block, 
   count_launch();
   return e;
 }
-// A sequence operator's kernel: none of them reads anything before its pdl_wait.  They call
+// A sequence operator's kernel: none of them reads anything before its pdl_wait.  The long ones call
 // pdl_trigger late, once a CTA's main loop is done: the next kernel's CTAs, started while most SMs
-// are still taken, crowd onto the few that are not and then run one after another there (gradient
-// split over CTAs, 1 x 2048, 8 query heads on one: 56.6 -> 51.7 us; fp32 forward, 2 x 1024, 8 heads:
-// 122 -> 97; 4 x 33 tokens, 12 heads: 4.9 -> 4.7).
+// are still taken, crowd onto the few that are not and then run one after another there (early and
+// late, us: causal gradient split over CTAs, 1 x 2048, 8 query heads on one, 60.7 and 52.3 at D = 128,
+// 65.4 and 57.9 at 64; causal fp32 forward, 2 x 1024, 8 heads of 64, 123 and 97.  Without causal's uneven
+// tiles there is little in it: the same gradient 77.5 and 77.2, at D = 64 65.0 and 68.6, the same fp32
+// forward 132 both; 4 x 33 tokens, 12 heads, 4.8 both).  rotary_table_kernel and attn_tc_join_kernel, short
+// and even, call it first.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_operator(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                             Args&&... args) {

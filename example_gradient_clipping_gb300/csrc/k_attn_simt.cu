@@ -1,5 +1,6 @@
-// Attention and its gradient on the FFMA pipes: fp32 inputs (whose 1e-5 rules out the tensor
-// cores' formats) and bf16 shapes the tensor-core kernels do not take.
+// Attention and its gradient on the FFMA pipes: fp32 inputs (whose 1e-5 a single product in the tensor
+// cores' formats does not hold; operands split into several parts, which would, are not built) and
+// bf16 shapes the tensor-core kernels do not take.
 //
 //   S = scale Q K^T,  P = softmax over the keys a query sees,  O = P V,  lse = log sum exp S
 //   delta = rowsum(dO * O),  dS = P * (dO V^T - delta),
@@ -8,11 +9,12 @@
 // 64 x 64 score tiles, 256 threads, 4 x 4 scores a thread; operands in shared memory as fp32
 // rows of DP + 4 floats (DP = D rounded up to 32, 64 or 128 with zeros).  Forward: one pass
 // over the keys with the running maximum and sum of each row in registers.  Gradient: the
-// scores are formed again from lse, so nothing of size T x S is stored; one kernel per own
-// side (a key tile's dK and dV over every query that sees it, heads sharing the key head in
-// turn; a query tile's dQ over its keys), which costs two of the seven products twice and
-// needs no atomics: every sum has one order.
-// Bound by FFMA and shared-memory issue, two CTAs of 128 registers a thread per SM: fp32 B = 16,
+// scores are formed again from lse, so nothing of size T x S is stored; a CTA per tile of either own
+// side, both in one grid (a key tile's dK and dV over every query that sees it, heads sharing the
+// key head in turn; a query tile's dQ over its keys), which costs two of the seven products twice
+// and needs no atomics: every sum has one order.
+// Bound by FFMA and shared-memory issue, two CTAs of 128 registers a thread per SM (at D > 64 their shared
+// memory leaves one): fp32 B = 16,
 // T = 250, H = 12, D = 64, causal, lengths 250 to 0: forward and gradient together 137 us; with full
 // lengths forward 60 us, gradient 183; 2 x 1024, 8 heads, not causal 132 and 415 (25.9 TFLOP/s of the
 // gradient's five products, 36 of the seven formed).

@@ -15,8 +15,9 @@
 // The few entries that the teacher or the label touches are written after the row, each by a
 // thread that adds up every teacher entry of the same index, so a repeated index needs no
 // atomics and the result does not depend on any order.
-// Long vocabularies are bound by HBM and the second pass's misses in L2, shorter ones by the
-// instructions of a row and the waits between them (43-46% of the issue slots): bf16, 8192 rows of
+// Long vocabularies are bound by HBM and the second pass's misses in L2.  On shorter ones no unit is full
+// (43-46% of the issue slots, 46-47% of DRAM): the consumers wait at every row, for its teacher before the
+// first chunk and for one another after the last: bf16, 8192 rows of
 // 131072 (0.64 of them of weight 1) loss and gradient 690-700 us, 5.1 TB/s or 0.76 of a copy's rate;
 // 4096 x 32768 loss alone 44 us (3.9 TB/s); 2048 x 50257 with labels at tau = 2 80 us (4.2 TB/s).
 // (A quarter of the first pass's exponentials as polynomials on the FMA pipe: 45 -> 51 us on the loss
@@ -148,7 +149,8 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 // kMode: 0 the teacher's softmax alone; 1 the label's (temperature 1) beside it; 2 + n the same
 // where tau = 2^n: exp(d) is then exp(d / tau) squared n times, which saves half of the
-// exponentials with two temperatures (2048 x 50257 at tau = 2: 89 -> 80 us).
+// exponentials with two temperatures (2048 x 50257 at tau = 2: 89 -> 80 us).  Each squaring doubles the
+// exponential's relative error, about 2^-22.
 template <class E, int kMode>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(DistillParams P) {
   using V = Words<E>;

@@ -282,7 +282,8 @@ class _Rotary(torch.autograd.Function):
 def rotary(q, k, table, positions=None, interleaved: bool = False, inverse: bool = False, stream=None):
     """(q', k') with the first table.shape[1] entries of every head turned by their position's
     angles; k may be None.  positions: int32 or int64 [B, T], None for 0 .. T - 1.  inverse
-    turns back (and is the gradient)."""
+    turns the other way, the transposed rotation: the gradient, and what turns back unless the
+    table has a magnitude ("parts", whose square then remains)."""
     interleaved, inverse = bool(interleaved), bool(inverse)
     if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
         if stream is not None:

@@ -6,8 +6,10 @@
  * gradients the library clips, and the loss whose gradient is the last layer's G.  The
  * conventions of dpclip.h hold: device pointers, caller-owned buffers, no allocation,
  * asynchronous on `stream`, arguments validated on the host before anything is launched, a
- * message in dp_last_error().  Every result is deterministic (the same inputs give the same
- * bits), and an example's outputs depend on that example alone.  Inputs are DP_BF16 or
+ * message in dp_last_error().  Every result is deterministic (the same call on the same inputs
+ * gives the same bits), and no example's values enter another's outputs.  (The bits of an
+ * example's attention gradient may differ between batch sizes: how many partial sums a key or
+ * query tile is split into, each added in order, follows from the whole call's shape.)  Inputs are DP_BF16 or
  * DP_FP32; sums, maxima and softmax statistics are fp32; an output of type bf16 is rounded
  * once, from fp32.
  *
@@ -84,7 +86,9 @@ dp_status dp_rotary(const dp_rotary_desc* desc, const void* Q, const void* K, co
  *   S_tj = scale q_t . k_j,  lse_t = log sum_j exp S_tj,  P_tj = exp(S_tj - lse_t),
  *   O_t = sum_j P_tj v_j
  * over the keys it sees.  A query that sees none: O = 0, lse = -inf and no gradient.
- * Rows past Lq_i and Lk_i may hold anything (NaN included); their outputs are 0.
+ * Rows past Lq_i and Lk_i may hold anything (NaN included); their outputs are 0.  Within the
+ * lengths a NaN or infinity in a row of K or V may also reach queries of its head that do not
+ * see it (0 times it is NaN), and one in Q or dO the gradients of keys that its query does not see.
  * Gradient, the probabilities recomputed from lse:
  *   delta_t = dO_t . O_t,   dS_tj = P_tj (dO_t . v_j - delta_t),
  *   dQ_t = scale sum_j dS_tj k_j,  dK_j = scale sum_t dS_tj q_t,  dV_j = sum_t P_tj dO_t,
