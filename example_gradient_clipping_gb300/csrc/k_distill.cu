@@ -390,6 +390,10 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(Di
           else if (vn < nvec) x[n] = edge[2 * ts + (vn == 0 ? 0 : 1)];
           else x[n].fill();
         }
+        // The next copy into the slot writes through another proxy than these reads: the arrival alone does
+        // not order it behind them.  (Without the fence reads that stood behind stores in the queue got the
+        // next chunk's values, on fp32 rows in nearly every call of a few thousand.)
+        if (!keep) ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && !keep) ptx::mbar_arrive(&empty[s]);
         return true;

@@ -231,3 +231,45 @@ def test_sizes_and_windows_past_32_bits(lib):
     for window in (-1, -far + 16, -(1 << 70)):
         with pytest.raises(lib.DPError, match="window"):
             lib.attention_forward(q, k, v, causal=True, window=window)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("B,T,V,K,tau,alpha", [
+    (149, 11, 17884, 93, 2.0, 0.3), (43, 173, 24963, 119, 1.0, 0.0), (1033, 5, 7156, 49, 4.0, 1.0),
+    (79, 50, 102670, 122, 1.0, 0.0), (538, 12, 12602, 59, 3.0, 0.5), (40, 128, 40000, 8, 1.0, 0.0),
+])
+def test_distill_many_rows_a_cta(lib, dtype, B, T, V, K, tau, alpha):
+    """Each CTA streams row after row through the same slots: a chunk must not be copied over before every
+    thread has read the one before it.  All entries against 64 bits, and the same bits in every call."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(V)
+    z = (torch.randn(B, T, V, generator=g, device="cuda") * 2).to(getattr(torch, dtype))
+    first = torch.randint(0, V, (B, T, 1), generator=g, device="cuda")
+    idx = (first + torch.randint(1, V // K, (B, T, 1), generator=g, device="cuda") * torch.arange(K, device="cuda")) % V
+    top = torch.randn(B, T, K, generator=g, device="cuda") * 2 + 5
+    y = torch.randint(0, V, (B, T), generator=g, device="cuda")
+    w = (torch.rand(B, T, generator=g, device="cuda") + 0.5) * (torch.rand(B, T, generator=g, device="cuda") < 0.8)
+    kw = dict(labels=y, weights=w, temperature=tau, alpha=alpha)
+    loss, grad = lib.distill_loss_and_grad(z, idx, top, **kw)
+    alone, rows = lib.distill_loss(z, idx, top, **kw)
+    assert torch.equal(loss, alone)
+    # fp32 statistics and entries: within a few 1e-7 of an entry and of the row's largest; bf16: rounded once
+    tol = 1e-5 if dtype == "float32" else 2 ** -8
+    for b in range(0, B, 8):
+        at = slice(b, b + 8)
+        x = z[at].double()
+        logq, p = torch.log_softmax(x / tau, -1), torch.softmax(top[at].double() / tau, -1)
+        row = (1 - alpha) * tau ** 2 * (p * (torch.log(p) - torch.gather(logq, 2, idx[at]))).sum(-1)
+        d = ((1 - alpha) * tau * torch.exp(logq)).scatter_add_(2, idx[at], p * (-(1 - alpha) * tau))
+        if alpha:
+            logp, hit = torch.log_softmax(x, -1), y[at].unsqueeze(-1)
+            row = row - alpha * torch.gather(logp, 2, hit).squeeze(-1)
+            d = (d + alpha * torch.exp(logp)).scatter_add_(2, hit, torch.full_like(logp[..., :1], -alpha))
+        row, d = row * w[at], d * w[at].unsqueeze(-1)
+        assert ((rows[at].double() - row).abs() <= 1e-5 * (1 + row.abs())).all()
+        off = (grad[at].double() - d).abs()
+        assert (off <= tol * d.abs() + 1e-6 * d.abs().amax(-1, keepdim=True) + 1e-38).all()
+    for _ in range(10):
+        again = lib.distill_loss_and_grad(z, idx, top, **kw)
+        assert torch.equal(again[0], loss) and torch.equal(again[1], grad)
+    assert lib.dp_check_status() == lib.DP_OK
