@@ -330,6 +330,7 @@ __device__ __forceinline__ void epilogue_norm(const Params& P, uint8_t* smem, Ct
         } else {
           add_bf16x8(*reinterpret_cast<const uint4*>(gt), bt);
         }
+        ptx::fence_proxy_async_smem();   // the reads are done before the next copy into the stage
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&c->empty[s]);
       }
@@ -440,6 +441,7 @@ __device__ __forceinline__ void epilogue(const Params& P, uint8_t* smem, Ctl* c,
         } else {
           add_bf16x8(*reinterpret_cast<const uint4*>(gt), btmp);
         }
+        ptx::fence_proxy_async_smem();   // the reads are done before the next copy into the stage
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&c->bfree[s]);
       }
