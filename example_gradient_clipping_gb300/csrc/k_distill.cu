@@ -16,13 +16,13 @@
 // thread that adds up every teacher entry of the same index, so a repeated index needs no
 // atomics and the result does not depend on any order.
 // Long vocabularies are bound by HBM and the second pass's misses in L2.  On shorter ones no unit is full
-// (43-46% of the issue slots, 46-47% of DRAM): the consumers wait at every row, for its teacher before the
-// first chunk and for one another after the last: bf16, 8192 rows of
-// 131072 (0.64 of them of weight 1) loss and gradient 690-700 us, 5.1 TB/s or 0.76 of a copy's rate;
-// 4096 x 32768 loss alone 44 us (3.9 TB/s); 2048 x 50257 with labels at tau = 2 80 us (4.2 TB/s).
-// (A quarter of the first pass's exponentials as polynomials on the FMA pipe: 45 -> 51 us on the loss
-// alone, so their unit is not what bounds it.  A row spread over a cluster's registers, read once, waited 3-4 us a row for the exchange of
-// its sums and ran at half the speed.)
+// (42-45% of the issue slots, 46-47% of DRAM): the consumers wait at every row, for its teacher before the
+// first chunk and for one another after the last.  bf16, 8192 rows of 131072 (0.64 of them of weight 1) loss
+// and gradient 696 us, 5.1 TB/s or 0.76 of a copy's rate; 4096 x 32768 loss alone 47 us (3.6 TB/s);
+// 2048 x 50257 with labels at tau = 2 78 us (4.3 TB/s).
+// (A quarter of the first pass's exponentials as polynomials on the FMA pipe, before the ring's proxy
+// fence: 45 -> 51 us on the loss alone, so their unit is not what bounds it.  A row spread over a cluster's
+// registers, read once, waited 3-4 us a row for the exchange of its sums and ran at half the speed.)
 #include <algorithm>
 
 #include "seq.cuh"
@@ -95,8 +95,8 @@ constexpr float kFar = 1e6f;
 constexpr int kNT = 256, kNW = kNT / 32, kTeachers = 3, kThreads = kNT + 32 + 32 * kTeachers;
 constexpr int kNV = 4, kChunk = kNT * kNV, kChunkBytes = kChunk * 16;   // vectors and bytes of a chunk
 // Slots and CTAs per SM, us on 8192 x 131072, 2048 x 50257 at tau = 2 and 4096 x 32768 loss alone:
-// six and two 697, 80, 49; four and three 745, 93, 49 (the rows in work outgrow L2); eleven and one
-// 681, 100, 67.
+// six and two 696, 78, 47; four and three 732, 88, 45 (the rows in work outgrow L2); eleven and one
+// 702, 102, 65.
 constexpr int kStages = 6, kMaxK = 1024, kMinBlocks = 2;
 
 // The slots of the ring in the order in which a row's chunks take them.  The gradient's pass
@@ -149,7 +149,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 // kMode: 0 the teacher's softmax alone; 1 the label's (temperature 1) beside it; 2 + n the same
 // where tau = 2^n: exp(d) is then exp(d / tau) squared n times, which saves half of the
-// exponentials with two temperatures (2048 x 50257 at tau = 2: 89 -> 80 us).  Each squaring doubles the
+// exponentials with two temperatures (2048 x 50257 at tau = 2: 88 -> 78 us).  Each squaring doubles the
 // exponential's relative error, about 2^-22.
 template <class E, int kMode>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) distill_stream_kernel(DistillParams P) {
