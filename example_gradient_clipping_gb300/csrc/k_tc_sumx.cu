@@ -104,6 +104,7 @@ struct Ctl {
   uint32_t tmem;
   int abort;
   int flags[2];       // [1] go / no-go after the main loops
+  int landed;         // sum mode: examples whose first stage the MMA issuer has seen land
   float red[2][8];    // norm mode: per-warp partials of the last two examples
 };
 
@@ -200,7 +201,10 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, i
 // a box request it at about the same time, and each waited for the first one's miss).
 // The CTAs of the first column tile prefetch their G columns, those of the first row tile
 // their A columns, so every byte is prefetched once.  Warp 3 follows the producers by
-// waiting for the first stage of each example to land.
+// waiting for the first stage of each example to land, and leaves out what has landed already.
+// Nothing waits for warp 3, so the barrier's phases may pass it by (rows off the 128-byte lines, D = 1000,
+// prefetch slowly enough): the MMA issuer's count of landed examples ends its wait then.  (A wait on the
+// barrier alone was for a phase that never came; it ran out and ended the CTA without its outputs.)
 template <bool kTrim>
 __device__ __forceinline__ void prefetcher(const Params& P, const CUtensorMap* mG64, const CUtensorMap* mA64,
                                            const CUtensorMap* mG16, const CUtensorMap* mA16, Ctl* c, int e0,
@@ -226,11 +230,17 @@ __device__ __forceinline__ void prefetcher(const Params& P, const CUtensorMap* m
     __syncwarp();
   };
   for (int e = e0; e < min(e1, e0 + kPrefetch); ++e) fetch(e);
+  volatile int* landed = &c->landed;
   for (int e = e0; e + kPrefetch < e1; ++e) {
-    const int k = (e - e0) * ns;
-    const bool w = ptx::mbar_wait(&c->full[k % STAGES], (k / STAGES) & 1, abort, P.status);
-    if (!__all_sync(0xffffffffu, w)) return;
-    fetch(e + kPrefetch);
+    const int x = e - e0, k = x * ns;
+    const uint64_t t0 = ptx::globaltimer();
+    for (;;) {
+      const bool there = *landed > x || ptx::mbar_try_wait(&c->full[k % STAGES], (k / STAGES) & 1);
+      if (__all_sync(0xffffffffu, there)) break;
+      const bool late = *abort || ptx::globaltimer() - t0 > ptx::kWaitLimitNs;
+      if (__any_sync(0xffffffffu, late)) return;   // (only a hint is lost)
+    }
+    if (x + kPrefetch >= __shfl_sync(0xffffffffu, *landed, 0)) fetch(e + kPrefetch);
   }
 }
 
@@ -256,6 +266,7 @@ __device__ __forceinline__ void mma_issuer(const Params& P, uint8_t* smem, Ctl* 
       const int s = k % STAGES;
       const bool w = ptx::mbar_wait(&c->full[s], (k / STAGES) & 1, abort, P.status);
       if (!__all_sync(0xffffffffu, w)) { live = false; break; }
+      if (u == 0 && (threadIdx.x & 31) == 0) *(volatile int*)&c->landed = x + 1;
       // no tcgen05 fence here: the TMA data is ordered by the mbarrier (both async proxy),
       // and a per-stage fence was measured to stall the MMA pipe
       const uint32_t g = ptx::smem_u32(smem + s * STAGE);
@@ -661,6 +672,7 @@ tc_sumx_kernel(const __grid_constant__ CUtensorMap mapG64, const __grid_constant
     }
     ptx::mbar_init(&c->drain, 1);
     c->abort = 0;
+    c->landed = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tensormap(&mapG64);
     ptx::prefetch_tensormap(&mapA64);
