@@ -216,7 +216,7 @@ def _layer_norm_plain(case, st):
 
 def _logprobs_plain(case, st):
     tau, K = case["tau"], case["K"]
-    z = st["logits"].float()
+    z = st["logits"].to(torch.float32, copy=True)   # (its own: the inputs stay as they are)
     if K:
         v, i = torch.sort(z, dim=-1, descending=True, stable=True)
         top, top_index = v[..., :K] / tau, i[..., :K].to(torch.int32)
