@@ -1,24 +1,14 @@
 // C ABI of the sequence operators (dpclip_seq.h): argument validation and launches.
 #include <algorithm>
 #include <cmath>
-#include <cstdio>
 
+#include "api_check.cuh"
 #include "seq.cuh"
 
+using dph::bad;
+using dph::launched;
+
 namespace {
-
-template <typename... Args>
-dp_status bad(dp_status st, const char* fmt, Args... args) {
-  char buf[400];
-  snprintf(buf, sizeof(buf), fmt, args...);
-  return dph::set_error(st, buf);
-}
-dp_status bad(dp_status st, const char* msg) { return dph::set_error(st, msg); }
-
-dp_status launched(cudaError_t e, const char* where) {
-  if (e != cudaSuccess) cudaGetLastError();   // reported here, and not by the next call that looks
-  return e == cudaSuccess ? DP_OK : bad(DP_ERR_CUDA, "%s launch: %s", where, cudaGetErrorString(e));
-}
 
 bool strides_ok(const dp_strides& s) { return s.b >= 0 && s.t >= 0 && s.h >= 0; }
 // A written tensor's rows must not fall on one another: with the extents above 1 in the order of
@@ -35,8 +25,8 @@ bool writable(const dp_strides& s, int B, int T, int H, int D) {
   }
   return true;
 }
-constexpr int kMaxLen = 1 << 30;   // lengths whose sums stay within 32 bits
-constexpr double kMaxBlocks = 2147483647.0;
+using dph::kMaxBlocks;
+using dph::kMaxLen;
 
 dp_status attn_params(const dp_attn_desc* d, bool grad, dpk::AttnParams* P) {
   if (!d) return bad(DP_ERR_INVALID_ARG, "desc is NULL");

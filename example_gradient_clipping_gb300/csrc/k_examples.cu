@@ -1,0 +1,92 @@
+// Rows of per-example gradients, or of partial sums of them: their squared norms and weighted sums.
+//
+// Both read every row once.  rows_sum_kernel: 32 columns a CTA, 16 warps that each add a consecutive share
+// of the rows in order, eight loads in flight, then the shares in order; so the result has one order.
+#include <algorithm>
+
+#include "seq.cuh"
+
+namespace dpk {
+
+constexpr int kShares = 16;
+
+__global__ void __launch_bounds__(32 * kShares) rows_sum_kernel(const float* __restrict__ rows, int count, size_t n,
+                                                                const float* __restrict__ factors, void* out, int bf16,
+                                                                int accumulate) {
+  pdl_wait();
+  __shared__ float red[kShares][32];
+  const int lane = threadIdx.x % 32, share = threadIdx.x / 32;
+  const size_t col = (size_t)blockIdx.x * 32 + lane;
+  const int i0 = (int)((long long)count * share / kShares), i1 = (int)((long long)count * (share + 1) / kShares);
+  const float* src = rows + (size_t)blockIdx.y * count * n + col;
+  float acc = 0.f;
+  if (col < n) {
+    int i = i0;
+    for (; i + 8 <= i1; i += 8) {
+      float v[8], f[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = src[(size_t)(i + k) * n];
+        f[k] = factors ? factors[i + k] : 1.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc = fmaf(f[k], v[k], acc);
+    }
+    for (; i < i1; ++i) acc = fmaf(factors ? factors[i] : 1.f, src[(size_t)i * n], acc);
+  }
+  red[share][lane] = acc;
+  __syncthreads();
+  pdl_trigger();
+  if (share || col >= n) return;
+#pragma unroll
+  for (int k = 1; k < kShares; ++k) acc += red[k][lane];
+  const size_t at = (size_t)blockIdx.y * n + col;
+  if (bf16) {
+    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(acc);
+  } else {
+    float* o = static_cast<float*>(out) + at;
+    *o = accumulate ? *o + acc : acc;
+  }
+}
+
+__global__ void __launch_bounds__(256) rows_sqnorm_kernel(const float* __restrict__ rows, size_t n, float* __restrict__ out) {
+  pdl_wait();
+  __shared__ float red[8];
+  const float* r = rows + (size_t)blockIdx.x * n;
+  float acc = 0.f;
+  for (size_t i = threadIdx.x; i < n; i += 256) acc = fmaf(r[i], r[i], acc);
+  acc = warp_sum(acc);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = acc;
+  __syncthreads();
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) acc += red[w];
+    out[blockIdx.x] = acc;
+  }
+}
+
+}  // namespace dpk
+
+namespace dph {
+using namespace dpk;
+
+cudaError_t launch_rows_sum(const float* rows, int segments, int count, size_t n, const float* factors, void* out,
+                            int bf16, int accumulate, cudaStream_t s) {
+  // segments beyond a grid's second dimension in several launches
+  for (int g = 0; g < segments; g += 65535) {
+    const int ng = std::min(segments - g, 65535);
+    const size_t off = (size_t)g * n;
+    const cudaError_t e = launch_operator(rows_sum_kernel, dim3((unsigned)((n + 31) / 32), (unsigned)ng),
+                                          dim3(32 * kShares), 0, s, rows + (size_t)g * count * n, count, n, factors,
+                                          static_cast<void*>(static_cast<char*>(out) + off * (bf16 ? 2 : 4)), bf16, accumulate);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_rows_sqnorm(const float* rows, int B, size_t n, float* out, cudaStream_t s) {
+  return launch_operator(rows_sqnorm_kernel, dim3((unsigned)B), dim3(256), 0, s, rows, n, out);
+}
+
+}  // namespace dph

@@ -1,4 +1,5 @@
-// Sequence operators (rotary positions, attention, distillation): parameters and launchers.
+// Sequence operators (rotary positions, attention, distillation, log probabilities, layer norms and
+// embeddings): parameters and launchers.
 #pragma once
 #include "common.cuh"
 #include "dpclip_seq.h"
@@ -135,6 +136,44 @@ struct DistillParams {
   float tau, alpha;
 };
 
+struct LogprobParams {
+  const void *logits, *tokens;
+  float *logprob, *entropy, *stats, *top;   // forward
+  int* top_index;
+  const float *d_logprob, *d_entropy;       // gradient (stats and entropy are read)
+  void* grad;
+  unsigned* status;
+  int B, T, V, K, token_i64;
+  long long ld, ldg;
+  float tau;
+};
+
+struct NormParams {
+  const void *X, *dY, *W, *bias;
+  void *Y, *dX;
+  float *mean, *rstd;      // written by the forward pass (may be null there)
+  float* part;             // gradient: slice s's sums at part + s * k * D (null: not formed)
+  int B, T, D, w_bf16, k;  // k: vectors of D in a row of the parameters' gradient
+  int slices;              // gradient: slices of rows a segment (an example, or the whole batch)
+  int segments;
+  float eps;
+  dp_row_strides x, dy;
+};
+
+struct EmbedParams {
+  const void *tokens, *W, *dY;
+  void *Y, *dW;
+  const float* factors;    // null: 1
+  const int *order, *keys; // the sorted tokens: where each stands in [B, T], and the token (V: no gradient)
+  float* partial;          // [units][2][D], sums of runs that cover a whole unit
+  float* run_sq;           // [slabs][N], squared norms of runs at their first position
+  unsigned* status;
+  int B, T, V, D, N, i64, padding, units, slabs, accumulate;
+  float scale;
+  long long ld;
+  dp_row_strides dy;
+};
+
 }  // namespace dpk
 
 namespace dph {
@@ -171,4 +210,21 @@ cudaError_t launch_attn_tc_grad(const dpk::AttnParams& P, float* ws, cudaStream_
 // delta[b, h, t] = dO . O of each query row.
 cudaError_t launch_attn_delta(const dpk::AttnParams& P, int dtype, float* delta, cudaStream_t s);
 cudaError_t launch_distill(const dpk::DistillParams& P, int dtype, cudaStream_t s);
+cudaError_t launch_logprobs(const dpk::LogprobParams& P, int dtype, cudaStream_t s);
+cudaError_t launch_logprobs_grad(const dpk::LogprobParams& P, int dtype, cudaStream_t s);
+cudaError_t launch_norm_fwd(const dpk::NormParams& P, int dtype, cudaStream_t s);
+// Slices that the rows of a segment are split into (by their shape and type alone).
+int norm_grad_slices(int segments, long long rows, int D, int dtype);
+cudaError_t launch_norm_grad(const dpk::NormParams& P, int dtype, cudaStream_t s);
+// out[g][j] (+)= sum_i factors[i] rows[g * count + i][j], j < n, i in order within shares of the count
+// (factors null: 1); `bf16` out is rounded from the fp32 sum.
+cudaError_t launch_rows_sum(const float* rows, int segments, int count, size_t n, const float* factors, void* out,
+                            int bf16, int accumulate, cudaStream_t s);
+cudaError_t launch_rows_sqnorm(const float* rows, int B, size_t n, float* out, cudaStream_t s);
+cudaError_t launch_embed_lookup(const dpk::EmbedParams& P, int dtype, cudaStream_t s);
+size_t embed_order_ws_bytes(int N, int V);
+cudaError_t launch_embed_order(const dpk::EmbedParams& P, int* order, int* keys, void* ws, cudaStream_t s);
+constexpr int kEmbedUnit = 32, kEmbedSlab = 256;   // sorted rows and columns of a warp's work
+cudaError_t launch_embed_sqnorms(const dpk::EmbedParams& P, int dtype, float* sqnorms, cudaStream_t s);
+cudaError_t launch_embed_grad(const dpk::EmbedParams& P, int dtype, int out_dtype, cudaStream_t s);
 }  // namespace dph

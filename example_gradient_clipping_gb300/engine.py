@@ -20,8 +20,10 @@ Layers: nn.Linear (inputs [B, ..., d]; the middle dimensions are the rows T), nn
 nn.Conv2d and nn.Conv3d (square or cubic kernels, equal stride / padding / dilation in every
 dimension), the conv layers with groups 1 and zero padding.  Conv2d/Conv3d layers whose input
 arrives in PyTorch's channels_last memory format are handed over channels last (no layout
-copy); their output gradients are brought to the same format.  Every trainable parameter of
-the model must belong to such a layer.
+copy); their output gradients are brought to the same format.  dp.Embedding (tokens [B, ...]) is
+clipped by its tokens and output gradient, dp.LayerNorm (inputs [B, ..., D]) by the per-example gradients
+that its backward pass leaves in place of their sum; torch's own two modules are not taken.  A layer is called
+once in a step, and its weight is its own.  Every trainable parameter of the model must belong to such a layer.
 Activations right after them must not be in-place (the backward hook reads the layer's
 output gradient).  PyTorch warns that the hook fires on output gradients when the model
 input needs no gradient; that gradient is the one wanted here.
@@ -31,6 +33,7 @@ from __future__ import annotations
 from typing import List, Optional
 
 from . import DP_BF16, DP_CONV1D, DP_CONV2D, DP_CONV3D, DP_FP32, DP_LINEAR, DP_NCHW, DP_NHWC, DP_NORM_AUTO, layer_desc
+from .layers import Embedding, LayerNorm, embedding_desc, kept_desc
 from .step import ClipStep
 
 
@@ -49,10 +52,19 @@ class PrivacyEngine:
         self.norm_mode, self.keep_grads = norm_mode, keep_grads
         self.layers: List = []
         owned = set()
+        beside = set()   # parameters of embeddings and layer norms, which no other layer may share
         for m in model.modules():
-            if isinstance(m, (nn.Linear,) + convs) and m.weight.requires_grad:
+            if isinstance(m, (nn.Linear, Embedding, LayerNorm) + convs) and m.weight is not None and m.weight.requires_grad:
                 if isinstance(m, convs):
                     self._check_conv(m)
+                if id(m.weight) in owned and (isinstance(m, (Embedding, LayerNorm)) or id(m.weight) in beside):
+                    raise ValueError(f"{m}: shares its weight with another layer, which is not clipped here")
+                if isinstance(m, (Embedding, LayerNorm)):
+                    beside.add(id(m.weight))
+                    if isinstance(m, Embedding):
+                        self.layers.append(m)
+                        owned.add(id(m.weight))
+                        continue
                 if m.bias is not None and not m.bias.requires_grad:
                     raise ValueError(f"{m}: a bias must be trainable with its weight")
                 self.layers.append(m)
@@ -61,14 +73,17 @@ class PrivacyEngine:
                     owned.add(id(m.bias))
         for name, prm in model.named_parameters():
             if prm.requires_grad and id(prm) not in owned:
-                raise ValueError(f"parameter {name}: only nn.Linear and nn.Conv1d/2d/3d layers have per-example "
-                                 "clipping here; freeze it or leave it out of the model")
+                raise ValueError(f"parameter {name}: only nn.Linear, nn.Conv1d/2d/3d, dp.Embedding and dp.LayerNorm "
+                                 "layers have per-example clipping here; freeze it or leave it out of the model")
         if not self.layers:
-            raise ValueError("the model has no trainable nn.Linear or nn.Conv1d/2d/3d layer")
+            raise ValueError("the model has no trainable layer that is clipped here")
         self._acts: List = [None] * len(self.layers)
         self._grads: List = [None] * len(self.layers)
         self._handles = []
         for i, m in enumerate(self.layers):
+            if isinstance(m, LayerNorm):
+                m._sink = self._sink(i)
+                continue
             self._handles.append(m.register_forward_hook(self._fwd_hook(i)))
             self._handles.append(m.register_full_backward_pre_hook(self._bwd_hook(i)))
         self._step: Optional[ClipStep] = None
@@ -92,11 +107,19 @@ class PrivacyEngine:
             self._grads[i] = grad_output[0].detach()
         return hook
 
+    def _sink(self, i):
+        def sink(each):                      # a layer norm's per-example gradients
+            self._acts[i] = each
+        return sink
+
     def detach(self) -> None:
         """Remove the hooks."""
         for h in self._handles:
             h.remove()
         self._handles = []
+        for m in self.layers:
+            if isinstance(m, LayerNorm):
+                m._sink = None
 
     @staticmethod
     def _layout(m, a) -> int:
@@ -119,10 +142,19 @@ class PrivacyEngine:
         return x.contiguous()
 
     def _descs(self, B: int, dtype: int, layouts):
+        import torch
         import torch.nn as nn
         out = []
-        for m, a, lay in zip(self.layers, self._acts, layouts):
+        for m, a, g, lay in zip(self.layers, self._acts, self._grads, layouts):
+            if isinstance(m, Embedding):
+                V, D = m.weight.shape
+                out.append(embedding_desc(DP_BF16 if g.dtype == torch.bfloat16 else DP_FP32, B=B, T=a.numel() // B, V=V,
+                                          D=D, scale=m.scale, padding=m.padding_idx, index_i64=a.dtype == torch.int64))
+                continue
             hb = m.bias is not None
+            if isinstance(m, LayerNorm):
+                out.append(kept_desc(B=B, p=m.weight.numel(), has_bias=hb))
+                continue
             if isinstance(m, nn.Linear):
                 T = a.numel() // (B * m.in_features)
                 out.append(layer_desc(DP_LINEAR, dtype, B=B, p=m.out_features, T=T, d=m.in_features, has_bias=hb))
@@ -143,28 +175,43 @@ class PrivacyEngine:
     def privatise(self, seed: int, stream=None):
         """Replace every layer's .grad by its privatised gradient; returns the flat vector."""
         import torch
-        if any(a is None for a in self._acts) or any(g is None for g in self._grads):
+        if any(a is None or (g is None and not isinstance(m, LayerNorm))
+               for m, a, g in zip(self.layers, self._acts, self._grads)):
             raise RuntimeError("run the forward pass and loss.backward() first")
         B = self._acts[0].shape[0]
-        dt = self._acts[0].dtype
+        if any(a.shape[0] != B for m, a in zip(self.layers, self._acts) if isinstance(m, (Embedding, LayerNorm))):
+            raise ValueError(f"an embedding's tokens or a layer norm's inputs are not of {B} examples")
+        # the type of A and G, which linear and conv layers share
+        dt = next((a.dtype for m, a in zip(self.layers, self._acts) if not isinstance(m, (Embedding, LayerNorm))),
+                  torch.float32)
         if dt not in (torch.bfloat16, torch.float32):
             raise ValueError(f"inputs of dtype {dt}: bf16 or fp32 only")
         dtype = DP_BF16 if dt == torch.bfloat16 else DP_FP32
         layouts = [self._layout(m, a) for m, a in zip(self.layers, self._acts)]
-        key = (B, dtype, tuple(tuple(a.shape) for a in self._acts), tuple(layouts))
+        key = (B, dtype, tuple(tuple(a.shape) for a in self._acts), tuple(layouts),
+               tuple((a.dtype, g.dtype) for m, a, g in zip(self.layers, self._acts, self._grads) if isinstance(m, Embedding)))
         if self._key != key:
             self._step = ClipStep(self._descs(B, dtype, layouts), C=self.C, sigma=self.sigma, per_layer=self.per_layer,
                                   norm_modes=[self.norm_mode] * len(self.layers), device=str(self._acts[0].device),
                                   keep_grads=self.keep_grads)
             self._key = key
         scale = float(B) if self.loss_reduction == "mean" else 1.0
-        inputs = [(self._as_layout(a, lay, dt), self._as_layout(g * scale if scale != 1.0 else g, lay, dt))
-                  for a, g, lay in zip(self._acts, self._grads, layouts)]
+
+        def times(g):
+            return g * scale if scale != 1.0 else g
+        inputs = []
+        for m, a, g, lay in zip(self.layers, self._acts, self._grads, layouts):
+            if isinstance(m, Embedding):
+                inputs.append((a.contiguous(), times(g).contiguous()))
+            elif isinstance(m, LayerNorm):
+                inputs.append((times(a), None))
+            else:
+                inputs.append((self._as_layout(a, lay, dt), self._as_layout(times(g), lay, dt)))
         flat = self._step.run(inputs, seed=seed, stream=stream)
         for l, m in enumerate(self.layers):
             dW, db = self._step.layer_views(l)
             m.weight.grad = dW.view_as(m.weight).to(m.weight.dtype).clone()
-            if m.bias is not None:
+            if getattr(m, "bias", None) is not None:
                 m.bias.grad = db.to(m.bias.dtype).clone()
         self._acts = [None] * len(self.layers)
         self._grads = [None] * len(self.layers)

@@ -8,6 +8,10 @@ and by one multi-block pass after the sums for conv layers (dp_add_noise_blocks)
 layer's noise is drawn at its flat offset, with its own bound when clipping per layer.
 fuse_noise=False runs dp_clipped_sum per layer and dp_add_noise over the vector
 instead; the result is bit-identical.  Torch supplies device memory and the stream only.
+
+Beside the layers of dp_layer_desc a step takes embeddings (embedding_desc: inputs are the tokens and the output
+gradient, which are sorted once for the norms and the sum) and layers whose per-example gradients the
+caller has (kept_desc: a layer norm's, from its backward pass; inputs are the gradients and None).
 """
 from __future__ import annotations
 
@@ -18,11 +22,49 @@ from . import (DP_LINEAR, DP_NORM_AUTO, DP_NORM_INSTANTIATE, LayerDesc, dp_adapt
                dp_clipped_sum, dp_clipped_sum_kept, dp_clipped_sum_kept_noised, dp_clipped_sum_noised,
                dp_clipped_sum_reuse, dp_grads_size, dp_launch_count, dp_layer_sqnorms, dp_layer_sqnorms_keep,
                dp_layout_reused, dp_plan, dp_workspace_size, noise_desc)
+from .layers import (EmbeddingDesc, KeptDesc, dp_embedding_grad, dp_embedding_order, dp_embedding_order_size,
+                     dp_embedding_sqnorms, dp_embedding_workspace, dp_example_sqnorms, dp_example_sum)
 
 # Instantiated layers with at least this many rows per example keep their per-example
 # gradients by default (the clipped sum then reads them once instead of recomputing a
 # contraction over the rows).
 KEEP_MIN_ROWS = 512
+
+
+def _beside(d) -> bool:
+    """Whether d is one of the layers that dp_layer_desc does not describe."""
+    return isinstance(d, (EmbeddingDesc, KeptDesc))
+
+
+def _plan(d, mode):
+    """(chosen mode, T, D) of any layer; the weight's gradient is [p, D]."""
+    if not _beside(d):
+        return dp_plan(d, mode)
+    if isinstance(d, EmbeddingDesc) and not dp_embedding_order_size(d):
+        dp_embedding_order(d, None, None, None)   # raises with what is wrong with it
+    return DP_NORM_INSTANTIATE, d.T if isinstance(d, EmbeddingDesc) else 1, d.D
+
+
+def _workspace_size(d, mode) -> int:
+    if not _beside(d):
+        return dp_workspace_size(d, mode)
+    return dp_embedding_workspace(d) if isinstance(d, EmbeddingDesc) else 0
+
+
+def _beside_sqnorms(d, A, G, order, out, workspace, stream) -> None:
+    if isinstance(d, EmbeddingDesc):
+        dp_embedding_order(d, A, order, workspace, stream=stream)
+        dp_embedding_sqnorms(d, order, G, out, workspace, stream=stream)
+    else:
+        dp_example_sqnorms(A, d.B, d.n, out, stream=stream)
+
+
+def _beside_sum(d, A, G, order, factors, dW, workspace, accumulate, stream) -> None:
+    """The clipped sum to dW (and, right behind it, db); `order` as _beside_sqnorms left it."""
+    if isinstance(d, EmbeddingDesc):
+        dp_embedding_grad(d, order, G, factors, dW, workspace, accumulate=accumulate, stream=stream)
+    else:
+        dp_example_sum(A, d.B, d.n, factors, dW, accumulate=accumulate, stream=stream)
 
 
 class ClipStep:
@@ -51,7 +93,7 @@ class ClipStep:
         self.C = [float(c) for c in (C if isinstance(C, (list, tuple)) else [C] * L)]
         self.sigma = float(sigma)
         self.modes = list(norm_modes) if norm_modes is not None else [DP_NORM_AUTO] * L
-        self.plan = [dp_plan(d, m) for d, m in zip(self.descs, self.modes)]
+        self.plan = [_plan(d, m) for d, m in zip(self.descs, self.modes)]
         self.offsets, o = [], 0
         self.shapes = []
         for d, (_, T, D) in zip(self.descs, self.plan):
@@ -59,7 +101,7 @@ class ClipStep:
             self.shapes.append((d.p, D))
             o += d.p * D + (d.p if d.has_bias else 0)
         self.n_params = o
-        ws = max(dp_workspace_size(d, m) for d, m in zip(self.descs, self.modes))
+        ws = max(_workspace_size(d, m) for d, m in zip(self.descs, self.modes))
         dev = torch.device(device)
         self.workspace = torch.empty(max(ws, 16), dtype=torch.uint8, device=dev)
         self.sqnorms = torch.empty(L, self.B, dtype=torch.float32, device=dev)
@@ -79,15 +121,18 @@ class ClipStep:
         self.kept = []
         for d, (m, T, _) in zip(self.descs, self.plan):
             want = keep_grads is True or (keep_grads == "auto" and T >= KEEP_MIN_ROWS)
-            nbytes = dp_grads_size(d) if (want and m == DP_NORM_INSTANTIATE) else 0
+            nbytes = dp_grads_size(d) if (want and m == DP_NORM_INSTANTIATE and not _beside(d)) else 0
             self.kept.append(torch.empty(nbytes // 4, dtype=torch.float32, device=dev) if nbytes else None)
         # conv layers whose clipped sum reuses the layouts their norm call wrote get a
         # workspace of their own, so the layouts survive the other layers' calls
         self.own_ws = []
         for l, (d, m) in enumerate(zip(self.descs, self.modes)):
-            reuse = self.kept[l] is None and dp_layout_reused(d, m) > 0
+            reuse = not _beside(d) and self.kept[l] is None and dp_layout_reused(d, m) > 0
             self.own_ws.append(torch.empty(max(dp_workspace_size(d, m), 16), dtype=torch.uint8, device=dev)
                                if reuse else None)
+        # the sorted tokens of embeddings, from their norm call to their sum
+        self.order = [torch.empty(dp_embedding_order_size(d), dtype=torch.uint8, device=dev)
+                      if isinstance(d, EmbeddingDesc) else None for d in self.descs]
 
     def layer_views(self, l: int) -> Tuple:
         p, D = self.shapes[l]
@@ -98,7 +143,9 @@ class ClipStep:
 
     def norms(self, inputs, stream=None) -> None:
         for l, (d, (A, G)) in enumerate(zip(self.descs, inputs)):
-            if self.kept[l] is not None:
+            if _beside(d):
+                _beside_sqnorms(d, A, G, self.order[l], self.sqnorms[l], self.workspace, stream)
+            elif self.kept[l] is not None:
                 dp_layer_sqnorms_keep(d, A, G, self.sqnorms[l], self.kept[l], self.workspace, stream=stream)
                 self.chosen[l] = DP_NORM_INSTANTIATE
             else:
@@ -125,7 +172,9 @@ class ClipStep:
         for l, (d, (A, G)) in enumerate(zip(self.descs, inputs)):
             dW, db = self.layer_views(l)
             fac = self.factors[l] if self.per_layer else self.factors[0]
-            if self.kept[l] is not None:
+            if _beside(d):
+                _beside_sum(d, A, G, self.order[l], fac, dW, self.workspace, False, stream)
+            elif self.kept[l] is not None:
                 dp_clipped_sum_kept(d, self.kept[l], fac, dW, db, self.workspace, stream=stream)
             elif self.own_ws[l] is not None:
                 dp_clipped_sum_reuse(d, self.modes[l], A, G, fac, dW, db, self.own_ws[l], stream=stream)
@@ -136,7 +185,8 @@ class ClipStep:
         """sums() and noise() together.  Linear layers' clipped sum calls and every layer's
         sum from kept gradients add their blocks' noise and the 1/B scale in the sum's final
         pass (dp_clipped_sum_noised, dp_clipped_sum_kept_noised); the other conv layers'
-        weight sums end in a column-mapping pass that does not draw noise, so their blocks get
+        weight sums end in a column-mapping pass that does not draw noise, nor do those of embeddings and
+        of gradients that the caller has, so their blocks get
         theirs from one multi-block noise launch after the sums (dp_add_noise_blocks) instead
         of one noise pass per layer."""
         blocks = []
@@ -144,10 +194,12 @@ class ClipStep:
             dW, db = self.layer_views(l)
             fac = self.factors[l] if self.per_layer else self.factors[0]
             C = self.C[l] if self.per_layer else self.C[0]
-            if d.kind != DP_LINEAR and self.kept[l] is None:
+            if _beside(d) or (d.kind != DP_LINEAR and self.kept[l] is None):
                 p, D = self.shapes[l]
                 blocks.append((self.offsets[l], p * D + (p if d.has_bias else 0), C))
-                if self.own_ws[l] is not None:
+                if _beside(d):
+                    _beside_sum(d, A, G, self.order[l], fac, dW, self.workspace, False, stream)
+                elif self.own_ws[l] is not None:
                     dp_clipped_sum_reuse(d, self.modes[l], A, G, fac, dW, db, self.own_ws[l], stream=stream)
                 else:
                     dp_clipped_sum(d, A, G, fac, dW, db, self.workspace, stream=stream)
@@ -157,8 +209,9 @@ class ClipStep:
                 dp_clipped_sum_kept_noised(d, self.kept[l], fac, dW, db, nd, self.workspace, stream=stream)
             else:
                 dp_clipped_sum_noised(d, A, G, fac, dW, db, nd, self.workspace, stream=stream)
-        if blocks:
-            dp_add_noise_blocks(self.grad, blocks, self.sigma, self.B, seed=seed, seed_dev=seed_dev, stream=stream)
+        for k in range(0, len(blocks), 64):
+            dp_add_noise_blocks(self.grad, blocks[k:k + 64], self.sigma, self.B, seed=seed, seed_dev=seed_dev,
+                                stream=stream)
 
     def noise(self, seed: int, stream=None) -> None:
         if not self.per_layer:
@@ -269,18 +322,24 @@ class VirtualStep:
             dm = type(d).from_buffer_copy(d)
             dm.B = B
             descs.append(dm)
-        need = max(dp_workspace_size(d, m) for d, m in zip(descs, b.modes))
+        need = max(_workspace_size(d, m) for d, m in zip(descs, b.modes))
         if need > b.workspace.numel():
             b.workspace = torch.empty(need, dtype=torch.uint8, device=b.grad.device)
         sq = self.sq_flat[:L * B].view(L, B)
         fac = self.fac_flat[:(L if b.per_layer else 1) * B].view(-1, B)
         for l, (d, (A, G)) in enumerate(zip(descs, inputs)):
-            b.chosen[l] = dp_layer_sqnorms(d, A, G, sq[l], b.workspace, mode=b.modes[l], stream=stream)
+            if _beside(d):
+                _beside_sqnorms(d, A, G, b.order[l], sq[l], b.workspace, stream)
+            else:
+                b.chosen[l] = dp_layer_sqnorms(d, A, G, sq[l], b.workspace, mode=b.modes[l], stream=stream)
         dp_clip_factors(sq, B, L, b.per_layer, b.C if b.per_layer else b.C[:1], fac, stream=stream)
         for l, (d, (A, G)) in enumerate(zip(descs, inputs)):
             dW, db = b.layer_views(l)
-            dp_clipped_sum(d, A, G, fac[l] if b.per_layer else fac[0], dW, db, b.workspace, accumulate=True,
-                           stream=stream)
+            f = fac[l] if b.per_layer else fac[0]
+            if _beside(d):
+                _beside_sum(d, A, G, b.order[l], f, dW, b.workspace, True, stream)
+            else:
+                dp_clipped_sum(d, A, G, f, dW, db, b.workspace, accumulate=True, stream=stream)
         self.examples += B
 
     def finish(self, seed: int, stream=None):
@@ -321,6 +380,8 @@ class ClipPipeline:
 
     def __init__(self, descs, shapes, dtype, C, sigma: float, per_layer: bool = False, device: str = "cuda"):
         import torch
+        if any(_beside(d) for d in descs):
+            raise ValueError("a pipeline takes the layers of dp_layer_desc")
         tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
         dev = torch.device(device)
         self.steps = [ClipStep(descs, C=C, sigma=sigma, per_layer=per_layer, device=str(dev)) for _ in range(2)]

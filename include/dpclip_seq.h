@@ -1,9 +1,11 @@
 /*
  * dpclip_seq.h -- the sequence operators of libdpclip: rotary positions, attention with its
- * gradient and the distillation loss with its gradient (sm_103a).
+ * gradient, the distillation loss with its gradient, log probabilities with theirs, and the
+ * embeddings and layer norms that are clipped beside the linear layers (sm_103a).
  *
- * They are the parameter-free operators between the linear layers whose per-example
- * gradients the library clips, and the loss whose gradient is the last layer's G.  The
+ * They are the operators between the linear layers whose per-example
+ * gradients the library clips, and the losses whose gradient is the last layer's G; an embedding
+ * and a layer norm have parameters of their own, with gradients per example.  The
  * conventions of dpclip.h hold: device pointers, caller-owned buffers, no allocation,
  * asynchronous on `stream`, arguments validated on the host before anything is launched, a
  * message in dp_last_error().  Every result is deterministic (the same call on the same inputs
@@ -144,6 +146,114 @@ typedef struct {
 dp_status dp_distill(const dp_distill_desc* desc, const void* logits, const void* indices, const void* teacher,
                      const void* labels, const float* weights, const float* upstream, float* row_loss, float* loss,
                      void* dlogits, cudaStream_t stream);
+
+/* ---- Log probabilities of given tokens -------------------------------------------------
+ * Per row (example i, position t) with logits z [V], temperature tau and the given token y:
+ *   m = max z,   log p_j = (z_j - m) / tau - ls,   ls = log sum_j exp((z_j - m) / tau),
+ *   logprob = log p_y,   entropy = - sum_j p_j log p_j   (p_j = 0 adds nothing),
+ * and the K largest log p_j with their indices, largest first; of equal logits (-0 equals 0) the
+ * lower index comes first.  A token < 0: none is given, logprob 0.  A token >= V sets the device
+ * status DP_ERR_INVALID_ARG, its logprob (and its row's gradient) is NaN.  A NaN or +inf among the
+ * logits, or nothing but -inf, makes the row's values NaN; a NaN ranks above every number.
+ * Gradient of dl logprob + dh entropy:
+ *   dz_j = [ dl (delta_jy - p_j) - dh p_j (log p_j + entropy) ] / tau;
+ * dl counts as 0 where no token is given; a row whose dl and dh are 0 is not read, its gradient
+ * is 0. */
+typedef struct {
+  int dtype;               /* dp_dtype of logits and dlogits */
+  int B, T, V, K;          /* K <= 128 and <= V; 0: no alternatives */
+  int token_i64;           /* 1: tokens are 64-bit integers */
+  long long ld, ld_grad;   /* elements between rows of logits and of dlogits, >= V */
+  float tau;               /* > 0 */
+} dp_logprobs_desc;
+
+/* logprobs, entropy (device fp32 [B, T]) and stats (fp32 [B, T, 2]: m, ls) of logits [B*T rows, V];
+ * tokens device [B, T] (NULL: none is given); top fp32 and top_indices int32 [B, T, K] (K = 0: NULL). */
+dp_status dp_token_logprobs(const dp_logprobs_desc* desc, const void* logits, const void* tokens, float* logprobs,
+                            float* entropy, float* stats, float* top, int* top_indices, cudaStream_t stream);
+
+/* dlogits for the upstream gradients d_logprobs and d_entropy (device fp32 [B, T]; NULL: 0); stats
+ * and entropy as dp_token_logprobs wrote them. */
+dp_status dp_token_logprobs_grad(const dp_logprobs_desc* desc, const void* logits, const void* tokens,
+                                 const float* stats, const float* entropy, const float* d_logprobs,
+                                 const float* d_entropy, void* dlogits, cudaStream_t stream);
+
+/* ---- Layer norm ------------------------------------------------------------------------
+ * Over the D entries of each row x (example i, position t):
+ *   mu = mean x,   rs = 1 / sqrt(mean (x - mu)^2 + eps),   h = (x - mu) rs,   y = w h + b,
+ *   dx = rs (u - mean u - h mean(u h)),  u = w dy,
+ *   dw_i = sum_t dy_t h_t,   db_i = sum_t dy_t   (example i's own),
+ * or both summed over the examples.  W NULL: w = 1; b NULL: 0. */
+typedef struct { long long b, t; } dp_row_strides;   /* element strides of a [B, T, D] tensor, >= 0 */
+
+typedef struct {
+  int dtype;               /* dp_dtype of X, Y, dY and dX */
+  int w_dtype;             /* dp_dtype of W and b, and of their gradient over the batch */
+  int B, T, D;             /* D <= 16384 */
+  int has_bias;            /* gradient: db is formed too */
+  int per_example;         /* gradient: 1 one row an example, 0 summed over the batch */
+  float eps;               /* >= 0 */
+  dp_row_strides x, dy;    /* Y and dX are contiguous */
+} dp_layer_norm_desc;
+
+/* Y [B, T, D], and each row's mu and rs (device fp32 [B, T]; NULL: not written). */
+dp_status dp_layer_norm(const dp_layer_norm_desc* desc, const void* X, const void* W, const void* b, void* Y,
+                        float* mean, float* rstd, cudaStream_t stream);
+
+/* Bytes of device workspace dp_layer_norm_grad needs (0 if the descriptor is invalid). */
+size_t dp_layer_norm_grad_workspace(const dp_layer_norm_desc* desc);
+
+/* dX (NULL: not formed) and grads (NULL: not formed): dw, behind it db with has_bias; device fp32
+ * [B, D or 2 D] with per_example, else [D or 2 D] of type w_dtype.  mean and rstd as dp_layer_norm
+ * wrote them. */
+dp_status dp_layer_norm_grad(const dp_layer_norm_desc* desc, const void* dY, const void* X, const void* W,
+                             const float* mean, const float* rstd, void* dX, void* grads, void* workspace,
+                             size_t ws_bytes, cudaStream_t stream);
+
+/* ---- Per-example gradients that the caller has -----------------------------------------
+ * grads: device fp32 [B, n], one row an example (as dp_layer_norm_grad writes them).
+ *   sqnorms[i] = sum_j grads[i, j]^2,   out[j] (+)= sum_i factors[i] grads[i, j]. */
+dp_status dp_example_sqnorms(const float* grads, int B, size_t n, float* sqnorms, cudaStream_t stream);
+dp_status dp_example_sum(const float* grads, int B, size_t n, const float* factors, float* out, int accumulate,
+                         cudaStream_t stream);
+
+/* ---- Embedding -------------------------------------------------------------------------
+ *   y_it = scale w_{k},  k = tokens[i, t],
+ *   dw_{i,v} = scale sum over the t with tokens[i, t] = v of dy_it   (example i's own),
+ * and from them sqnorms[i] = sum_v |dw_{i,v}|^2 and dw_v = sum_i factors[i] dw_{i,v}.
+ * The rows of the padding token have no gradient (its own row of w is looked up as any other).
+ * A token outside [0, V) sets the device status DP_ERR_INVALID_ARG; its y is NaN and it has no
+ * gradient.  The gradients go by the tokens sorted once (dp_embedding_order): equal tokens stand
+ * together in the order of their positions, so every sum has one order. */
+typedef struct {
+  int dtype;               /* dp_dtype of W and Y, or of dY */
+  int out_dtype;           /* dp_dtype of dW */
+  int B, T, V, D;          /* B T <= 2^30, V <= 2^30 */
+  int index_i64;           /* 1: tokens are 64-bit integers */
+  int padding;             /* the padding token, < 0: none */
+  float scale;             /* finite */
+  long long ld;            /* elements between rows of W, >= D */
+  dp_row_strides dy;       /* Y and dW are contiguous */
+} dp_embedding_desc;
+
+/* Y [B, T, D] of tokens (device [B, T]) and W [V, D]. */
+dp_status dp_embedding(const dp_embedding_desc* desc, const void* tokens, const void* W, void* Y, cudaStream_t stream);
+
+/* Bytes of `order`, and of the workspace of the three calls that take one (0 if the descriptor is
+ * invalid).  Both 16-byte aligned. */
+size_t dp_embedding_order_size(const dp_embedding_desc* desc);
+size_t dp_embedding_workspace(const dp_embedding_desc* desc);
+
+/* Sorts the tokens into `order`, which the next two calls read (B, T, V, padding as here). */
+dp_status dp_embedding_order(const dp_embedding_desc* desc, const void* tokens, void* order, void* workspace,
+                             size_t ws_bytes, cudaStream_t stream);
+/* sqnorms (device fp32 [B]) of the output gradient dY [B, T, D]. */
+dp_status dp_embedding_sqnorms(const dp_embedding_desc* desc, const void* order, const void* dY, float* sqnorms,
+                               void* workspace, size_t ws_bytes, cudaStream_t stream);
+/* dW [V, D] of type out_dtype; factors device fp32 [B] (NULL: 1).  accumulate = 1 adds to dW, which
+ * must be fp32 then. */
+dp_status dp_embedding_grad(const dp_embedding_desc* desc, const void* order, const void* dY, const float* factors,
+                            void* dW, int accumulate, void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
