@@ -108,10 +108,21 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+_current = _device = None   # torch's current stream of a device as a handle, and its current device
+
+
+def _find_current() -> None:
+    global _current, _device
+    import torch
+    torch.cuda.init()
+    _current, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        if _current is None:
+            _find_current()
+        return _current(_device()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None

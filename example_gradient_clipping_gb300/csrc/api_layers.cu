@@ -29,8 +29,7 @@ dp_status logprob_params(const dp_logprobs_desc* d, bool grad, dpk::LogprobParam
   if (d->K && !grad && d->V > 1 << 22) return bad(DP_ERR_UNSUPPORTED, "alternatives of V=%d logits, above 2^22", d->V);
   if (d->ld < d->V || (grad && d->ld_grad < d->V))
     return bad(DP_ERR_INVALID_ARG, "ld=%lld and ld_grad=%lld must be >= V=%d", d->ld, d->ld_grad, d->V);
-  if (!(d->tau > 0.f) || !std::isfinite(d->tau) || !std::isfinite(2.f / d->tau))
-    return bad(DP_ERR_INVALID_ARG, "tau and 1 / tau must be finite and > 0");
+  if (!(d->tau >= 1e-6f && d->tau <= 1e6f)) return bad(DP_ERR_INVALID_ARG, "tau must be from 1e-6 to 1e6");
   if ((double)d->B * d->T * (grad ? ((double)d->V + 16) / 2048 + 1 : 8) > kMaxBlocks)
     return bad(DP_ERR_UNSUPPORTED, "too many rows for one launch");
   *P = {};
@@ -79,7 +78,8 @@ dp_status embed_params(const dp_embedding_desc* d, dpk::EmbedParams* P) {
   P->B = d->B; P->T = d->T; P->V = d->V; P->D = d->D; P->N = d->B * d->T;
   P->i64 = d->index_i64 ? 1 : 0; P->padding = d->padding < 0 ? -1 : d->padding; P->scale = d->scale;
   P->ld = d->ld; P->dy = d->dy;
-  P->units = (P->N + dph::kEmbedUnit - 1) / dph::kEmbedUnit;
+  const int unit = dph::embed_unit(P->N, P->D);
+  P->units = (P->N + unit - 1) / unit;
   P->slabs = (P->D + dph::kEmbedSlab - 1) / dph::kEmbedSlab;
   if (((double)P->units * P->slabs + P->V / 32.0 + 2) / 8 > kMaxBlocks)
     return bad(DP_ERR_UNSUPPORTED, "too many rows for one launch");

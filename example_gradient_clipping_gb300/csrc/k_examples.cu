@@ -21,18 +21,17 @@ __global__ void __launch_bounds__(32 * kShares) rows_sum_kernel(const float* __r
   const float* src = rows + (size_t)blockIdx.y * count * n + col;
   float acc = 0.f;
   if (col < n) {
-    int i = i0;
-    for (; i + 8 <= i1; i += 8) {
+    for (int i = i0; i < i1; i += 8) {
       float v[8], f[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        v[k] = src[(size_t)(i + k) * n];
-        f[k] = factors ? factors[i + k] : 1.f;
+        v[k] = i + k < i1 ? src[(size_t)(i + k) * n] : 0.f;
+        f[k] = factors && i + k < i1 ? factors[i + k] : 1.f;
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc = fmaf(f[k], v[k], acc);
+      for (int k = 0; k < 8; ++k)
+        if (i + k < i1) acc = fmaf(f[k], v[k], acc);
     }
-    for (; i < i1; ++i) acc = fmaf(factors ? factors[i] : 1.f, src[(size_t)i * n], acc);
   }
   red[share][lane] = acc;
   __syncthreads();

@@ -8,25 +8,79 @@
 namespace dpk {
 using namespace lnorm;
 
+// The CTAs go over the rows.  Rows of vectors: each thread copies its own vectors into S slots of shared memory,
+// S - 1 rows ahead, and reads only what it copied (no barrier); others are read when they are due.
+constexpr int fwd_stages(int es, int vec, int G, int C) {
+  const int stage = dph::norm_threads(G) * (C / vec) * 16;
+  return vec * es != 16 ? 0 : 4 * stage <= 48 * 1024 ? 4 : 3;
+}
+constexpr int fwd_ctas(int G, int C) { return G > 32 ? 1024 / G : C > 16 ? 2 : 3; }   // an SM
+
 template <class E, int VEC, int G, int C>
-__global__ void __launch_bounds__(G == 32 ? 256 : G) layer_norm_kernel(NormParams P) {
+__global__ void __launch_bounds__(dph::norm_threads(G), fwd_ctas(G, C)) layer_norm_kernel(NormParams P) {
   pdl_wait();
+  constexpr int NV = C / VEC, S = fwd_stages(sizeof(E), VEC, G, C), threads = dph::norm_threads(G), per = dph::norm_rows(G);
+  using V = Pack<E, VEC>;
+  extern __shared__ uint4 ring[];   // [S][NV][threads]
   __shared__ float red[2][1][32];
   int round = 0;
-  const int lane = G == 32 ? threadIdx.x % 32 : threadIdx.x;
-  const unsigned per = G == 32 ? blockDim.x / 32 : 1, rows = (unsigned)P.B * (unsigned)P.T;
-  const unsigned step = gridDim.x * per;
-  unsigned r = blockIdx.x * per + (G == 32 ? threadIdx.x / 32 : 0);
+  const int lane = threadIdx.x % G;
+  const unsigned rows = (unsigned)P.B * (unsigned)P.T, step = gridDim.x * per;
   const E* X = static_cast<const E*>(P.X);
-  Row<E, VEC, C> x, next;
-  if (r < rows) load_row<E, VEC, G, C>(x, X + row_at(P.x, P.T, r), lane, P.D);
+  auto slot = [&](int stage, int k) { return ring + (stage * NV + k) * threads + threadIdx.x; };
+  auto copy = [&](int stage, unsigned row) {
+    if (row < rows) {
+      const E* p = X + row_at(P.x, P.T, row);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int col = (lane + k * G) * VEC;
+        const bool in = col < P.D;
+        copy16((uint32_t)__cvta_generic_to_shared(slot(stage, k)), in ? p + col : p, in);
+      }
+    }
+    copies_end();
+  };
+  unsigned base = blockIdx.x * per;   // of the CTA's rows: the groups of a warp stay together
+  const unsigned own = threadIdx.x / G;
+  if constexpr (S > 0) {
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) copy(s, base + own + s * step);
+  }
   float w[C], b[C];
-  load_param<VEC, G, C>(w, P.W, P.w_bf16, 1.f, lane, P.D);
-  load_param<VEC, G, C>(b, P.bias, P.w_bf16, 0.f, lane, P.D);
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int col = (lane + k * G) * VEC;
+    float f[VEC] = {}, h[VEC] = {};
+    if (col < P.D) {
+      load_param_at<VEC>(f, P.W, P.w_bf16, 1.f, col);
+      load_param_at<VEC>(h, P.bias, P.w_bf16, 0.f, col);
+    }
+#pragma unroll
+    for (int n = 0; n < VEC; ++n) {
+      w[k * VEC + n] = f[n];
+      b[k * VEC + n] = h[n];
+    }
+  }
   const float inv = 1.f / (float)P.D;
-  for (; r < rows; r += step) {
-    const bool more = r + step > r && r + step < rows;
-    if (more) load_row<E, VEC, G, C>(next, X + row_at(P.x, P.T, r + step), lane, P.D);
+  int stage = 0;
+  for (; base < rows; base += step) {
+    const unsigned r = base + own;
+    const bool there = per == 1 || r < rows;
+    Row<E, VEC, C> x;
+    if constexpr (S > 0) {
+      copies_wait<S ? S - 2 : 0>();
+#pragma unroll
+      for (int k = 0; k < NV; ++k) x.v[k] = *reinterpret_cast<const V*>(slot(stage, k));
+      copy(stage == 0 ? S - 1 : stage - 1, r + (S - 1) * step);   // the slot that the last row left
+      stage = stage + 1 == S ? 0 : stage + 1;
+    } else {
+      const E* p = X + (there ? row_at(P.x, P.T, r) : 0);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int col = (lane + k * G) * VEC;
+        x.v[k] = there && col < P.D ? *reinterpret_cast<const V*>(p + col) : V{};
+      }
+    }
     float s[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c) s[0] += x.get(c);
@@ -40,24 +94,23 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G) layer_norm_kernel(NormParam
     }
     row_sum<G, 1>(s, red, round);
     const float rs = rsqrtf(s[0] * inv + P.eps);
+    if (!there) continue;
     E* y = static_cast<E*>(P.Y) + (size_t)r * P.D;
 #pragma unroll
-    for (int k = 0; k < C / VEC; ++k) {
+    for (int k = 0; k < NV; ++k) {
       const int col = (lane + k * G) * VEC;
       if (col >= P.D) continue;
       float o[VEC];
 #pragma unroll
       for (int n = 0; n < VEC; ++n) o[n] = fmaf((x.v[k].get(n) - mu) * rs, w[k * VEC + n], b[k * VEC + n]);
-      Pack<E, VEC> out;
+      V out;
       out.set(o);
-      *reinterpret_cast<Pack<E, VEC>*>(y + col) = out;
+      *reinterpret_cast<V*>(y + col) = out;
     }
     if (lane == 0 && P.mean) {
       P.mean[r] = mu;
       P.rstd[r] = rs;
     }
-    if (more) x = next;
-    if (!more) break;
   }
   pdl_trigger();
 }
@@ -69,13 +122,15 @@ using namespace dpk;
 
 template <class E, int VEC>
 static cudaError_t run_norm_fwd(const NormParams& P, cudaStream_t s) {
-  return with_norm_shape(P.D, [&](auto g, auto c) {
-    constexpr int G = decltype(g)::value, C = decltype(c)::value;
-    const long long rows = (long long)P.B * P.T;
-    // CTAs that fit on the GPU at once go over the rows (a warp a row: eight rows a CTA)
-    const int per = G == 32 ? 8 : 1;
-    const long long ctas = std::min<long long>((rows + per - 1) / per, 152ll * (G == 32 ? 3 : 2048 / G));
-    return launch_operator(layer_norm_kernel<E, VEC, G, C>, dim3((unsigned)ctas), dim3(G == 32 ? 256 : G), 0, s, P);
+  return with_norm_shape<VEC>(P.D, [&](auto g, auto c) {
+    constexpr int G = decltype(g)::value, C = decltype(c)::value, threads = norm_threads(G), per = norm_rows(G);
+    constexpr int smem = fwd_stages(sizeof(E), VEC, G, C) * (C / VEC) * threads * 16;
+    if (smem > 40 * 1024) {   // (beside the static arrays)
+      const cudaError_t e = allow_smem<layer_norm_kernel<E, VEC, G, C>>(smem);
+      if (e != cudaSuccess) return e;
+    }
+    const long long ctas = std::min<long long>(((long long)P.B * P.T + per - 1) / per, 152ll * fwd_ctas(G, C));
+    return launch_operator(layer_norm_kernel<E, VEC, G, C>, dim3((unsigned)ctas), dim3(threads), smem, s, P);
   });
 }
 

@@ -11,95 +11,168 @@
 namespace dpk {
 using namespace lnorm;
 
+// Rows in flight: with S > 0 each thread copies its own 16-byte vectors of x and dy into S slots of shared memory,
+// S - 1 rows ahead, and reads only what it copied itself (no barrier); with S = 0 (rows that no vector
+// fits, or that are too long for the slots) the next row waits in registers.
+constexpr int ring_stages(int es, int vec, int G, int C) {
+  const int stage = dph::norm_threads(G) * 2 * (C / vec) * 16, fit = 100 * 1024 / stage;   // for two CTAs an SM
+  return vec * es != 16 || 2 * stage > 200 * 1024 ? 0 : fit >= 6 ? 6 : fit >= 2 ? fit : 2;
+}
+constexpr int grad_ctas(int G) { return G > 128 ? (G >= 512 ? 1 : 2) : G > 32 ? 3 : 2; }   // an SM
+
 template <class E, int VEC, int G, int C>
-__global__ void __launch_bounds__(G == 32 ? 256 : G) layer_norm_grad_kernel(NormParams P) {
+__global__ void __launch_bounds__(dph::norm_threads(G), grad_ctas(G)) layer_norm_grad_kernel(NormParams P) {
   pdl_wait();
-  extern __shared__ float sums[];   // G == 32: one warp's columns of dw, then of db
+  constexpr int NV = C / VEC, S = ring_stages(sizeof(E), VEC, G, C), D1 = S ? 1 : NV;
+  using V = Pack<E, VEC>;
+  extern __shared__ uint4 ring[];   // [S][x, dy][NV][threads]; then, G <= 32: every thread's columns of dw and db
   __shared__ float red[2][2][32];
   int round = 0;
-  const int lane = G == 32 ? threadIdx.x % 32 : threadIdx.x;
-  const int warp = G == 32 ? threadIdx.x / 32 : 0, per = G == 32 ? blockDim.x / 32 : 1;
+  const int lane = threadIdx.x % G, threads = blockDim.x;
+  const unsigned per = G > 32 ? 1 : threads / G, own = threadIdx.x / G;
   const unsigned total = (unsigned)P.B * (unsigned)P.T, seg_rows = total / (unsigned)P.segments;
   const unsigned seg = blockIdx.x / (unsigned)P.slices, slice = blockIdx.x - seg * (unsigned)P.slices;
   // this CTA's rows of its segment
-  const unsigned r0 = seg * seg_rows + (unsigned)((unsigned long long)seg_rows * slice / P.slices);
+  unsigned base = seg * seg_rows + (unsigned)((unsigned long long)seg_rows * slice / P.slices);
   const unsigned r1 = seg * seg_rows + (unsigned)((unsigned long long)seg_rows * (slice + 1) / P.slices);
   const E *X = static_cast<const E*>(P.X), *dY = static_cast<const E*>(P.dY);
-  Row<E, VEC, C> x, g, nx, ng;
-  float mu = 0.f, rs = 0.f, nmu = 0.f, nrs = 0.f;
-  auto load = [&](Row<E, VEC, C>& a, Row<E, VEC, C>& b, float& m, float& q, unsigned r) {
-    load_row<E, VEC, G, C>(a, X + row_at(P.x, P.T, r), lane, P.D);
-    load_row<E, VEC, G, C>(b, dY + row_at(P.dy, P.T, r), lane, P.D);
-    m = P.mean[r];
-    q = P.rstd[r];
+  V rx[D1], rg[D1], nx[D1], ng[D1];
+  auto fetch = [&](V (&a)[D1], V (&b)[D1], unsigned row) {   // zeros past the slice
+    const bool there = row < r1;
+    const E *px = X + (there ? row_at(P.x, P.T, row) : 0), *pg = dY + (there ? row_at(P.dy, P.T, row) : 0);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int col = (lane + k * G) * VEC;
+      a[S ? 0 : k] = there && col < P.D ? *reinterpret_cast<const V*>(px + col) : V{};
+      b[S ? 0 : k] = there && col < P.D ? *reinterpret_cast<const V*>(pg + col) : V{};
+    }
   };
-  unsigned r = r0 + warp;
-  if (r < r1) load(x, g, mu, rs, r);
+  auto slot = [&](int stage, int which, int k) { return ring + ((stage * 2 + which) * NV + k) * threads + threadIdx.x; };
+  auto copy = [&](int stage, unsigned row) {
+    if (row < r1 + per) {   // (a group past the slice beside others that are not: zeros)
+      const bool there = row < r1;
+      const E *px = X + (there ? row_at(P.x, P.T, row) : 0), *pg = dY + (there ? row_at(P.dy, P.T, row) : 0);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int col = (lane + k * G) * VEC;
+        const bool in = there && col < P.D;
+        copy16((uint32_t)__cvta_generic_to_shared(slot(stage, 0, k)), in ? px + col : X, in);
+        copy16((uint32_t)__cvta_generic_to_shared(slot(stage, 1, k)), in ? pg + col : dY, in);
+      }
+    }
+    copies_end();
+  };
+  float mu = 0.f, rs = 0.f, nmu = 0.f, nrs = 0.f;
+  if constexpr (S > 0) {
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) copy(s, base + own + s * per);
+  } else {
+    fetch(rx, rg, base + own);
+  }
+  if (base + own < r1) {
+    mu = P.mean[base + own];
+    rs = P.rstd[base + own];
+  }
   float w[C], dw[C], db[C];
-  load_param<VEC, G, C>(w, P.W, P.w_bf16, 1.f, lane, P.D);
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int col = (lane + k * G) * VEC;
+    float f[VEC] = {};
+    if (col < P.D) load_param_at<VEC>(f, P.W, P.w_bf16, 1.f, col);
+#pragma unroll
+    for (int n = 0; n < VEC; ++n) w[k * VEC + n] = f[n];
+  }
 #pragma unroll
   for (int c = 0; c < C; ++c) dw[c] = db[c] = 0.f;
   const float inv = 1.f / (float)P.D;
-  for (; r < r1; r += per) {
-    const bool more = r + per < r1;
-    if (more) load(nx, ng, nmu, nrs, r + per);
+  int stage = 0;
+  for (; base < r1; base += per) {   // (the same for every thread)
+    const unsigned r = base + own;
+    if constexpr (S > 0) {
+      copies_wait<S ? S - 2 : 0>();
+      copy(stage == 0 ? S - 1 : stage - 1, r + (S - 1) * per);   // the slot that the last row left
+    } else if (base + per < r1) {
+      fetch(nx, ng, r + per);
+    }
+    nmu = nrs = 0.f;
+    if (r + per < r1) {
+      nmu = P.mean[r + per];
+      nrs = P.rstd[r + per];
+    }
+    auto vx = [&](int k) { return S ? *reinterpret_cast<const V*>(slot(stage, 0, k)) : rx[S ? 0 : k]; };
+    auto vg = [&](int k) { return S ? *reinterpret_cast<const V*>(slot(stage, 1, k)) : rg[S ? 0 : k]; };
     float s[2] = {0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < C; ++c) {   // past D: w = dy = 0
-      const float d = g.get(c), h = (x.get(c) - mu) * rs, u = w[c] * d;
-      s[0] += u;
-      s[1] = fmaf(u, h, s[1]);
-      dw[c] = fmaf(d, h, dw[c]);
-      db[c] += d;
+    for (int k = 0; k < NV; ++k) {
+      const V x = vx(k), g = vg(k);
+#pragma unroll
+      for (int n = 0; n < VEC; ++n) {   // past D: w = dy = 0
+        const int c = k * VEC + n;
+        const float d = g.get(n), h = (x.get(n) - mu) * rs, u = w[c] * d;
+        s[0] += u;
+        s[1] = fmaf(u, h, s[1]);
+        dw[c] = fmaf(d, h, dw[c]);
+        db[c] += d;
+      }
     }
     if (P.dX) {
       row_sum<G, 2>(s, red, round);
+      if constexpr (S > 0) asm volatile("" ::: "memory");   // the row is read again, and not held over the sums
       const float a = s[0] * inv, b = s[1] * inv;
       E* o = static_cast<E*>(P.dX) + (size_t)r * P.D;
 #pragma unroll
-      for (int k = 0; k < C / VEC; ++k) {
+      for (int k = 0; k < NV; ++k) {
         const int col = (lane + k * G) * VEC;
-        if (col >= P.D) continue;
+        if (col >= P.D || r >= r1) continue;
+        const V x = vx(k), g = vg(k);
         float v[VEC];
 #pragma unroll
         for (int n = 0; n < VEC; ++n) {
-          const float h = (x.v[k].get(n) - mu) * rs;
-          v[n] = (fmaf(w[k * VEC + n], g.v[k].get(n), -a) - h * b) * rs;
+          const float h = (x.get(n) - mu) * rs;
+          v[n] = (fmaf(w[k * VEC + n], g.get(n), -a) - h * b) * rs;
         }
-        Pack<E, VEC> out;
+        V out;
         out.set(v);
-        *reinterpret_cast<Pack<E, VEC>*>(o + col) = out;
+        *reinterpret_cast<V*>(o + col) = out;
       }
     }
-    if (more) {
-      x = nx;
-      g = ng;
-      mu = nmu;
-      rs = nrs;
+    if constexpr (S > 0) {
+      stage = stage + 1 == S ? 0 : stage + 1;
+    } else {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        rx[S ? 0 : k] = nx[S ? 0 : k];
+        rg[S ? 0 : k] = ng[S ? 0 : k];
+      }
     }
+    mu = nmu;
+    rs = nrs;
   }
   pdl_trigger();
   if (!P.part) return;
   float* part = P.part + (size_t)blockIdx.x * P.k * P.D;
-  if constexpr (G == 32) {   // the warps' sums, added in warp order
-    for (int v = 0; v < per; ++v) {
-      if (warp == v) {
+  auto column = [&](int l, int c) { return (l + c / VEC * G) * VEC + c % VEC; };
+  if constexpr (G <= 32) {   // the groups' sums, added in order
+    if constexpr (S > 0) copies_wait<0>();   // (groups without copies)
+    float* sums = reinterpret_cast<float*>(ring);
+    __syncthreads();                          // every warp is done with its slots
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int col = (lane + c / VEC * G) * VEC + c % VEC;
-          if (col < P.D) {
-            sums[col] = v ? sums[col] + dw[c] : dw[c];
-            if (P.k == 2) sums[P.D + col] = v ? sums[P.D + col] + db[c] : db[c];
-          }
-        }
-      }
-      __syncthreads();
+    for (int c = 0; c < C; ++c) {
+      sums[c * threads + threadIdx.x] = dw[c];
+      if (P.k == 2) sums[(C + c) * threads + threadIdx.x] = db[c];
     }
-    for (int i = threadIdx.x; i < P.k * P.D; i += blockDim.x) part[i] = sums[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < P.k * C * G; i += threads) {
+      const int a = i / G, l = i % G, col = column(l, a % C);
+      if (col >= P.D) continue;
+      float t = 0.f;
+      for (unsigned q = 0; q < per; ++q) t += sums[a * threads + q * G + l];
+      part[(a >= C ? P.D : 0) + col] = t;
+    }
   } else {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = (lane + c / VEC * G) * VEC + c % VEC;
+      const int col = column(lane, c);
       if (col < P.D) {
         part[col] = dw[c];
         if (P.k == 2) part[P.D + col] = db[c];
@@ -113,29 +186,31 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G) layer_norm_grad_kernel(Norm
 namespace dph {
 using namespace dpk;
 
-// CTAs that are there at once, about (by what their registers leave).
-static int norm_grad_ctas(int D) {
-  const lnorm::Shape sh = norm_shape(D);
-  return 152 * (sh.G == 32 ? (sh.C <= 16 ? 3 : 2) : std::max(1, 512 / sh.G));
-}
-
-// Enough slices to fill the GPU once; a warp of a slice has four rows or more where the segment does.
-int norm_grad_slices(int segments, long long rows, int D, int) {
-  const int per = norm_shape(D).G == 32 ? 8 : 1;
-  const long long most = std::max<long long>(1, rows / (4 * per));
-  const long long want = (norm_grad_ctas(D) + segments - 1) / segments;
+// Enough slices to fill the GPU once; a group of threads has four rows of a slice or more where the segment has
+// them.  (By width and type alone: the workspace is the same wherever the tensors lie.)
+int norm_grad_slices(int segments, long long rows, int D, int dtype) {
+  const int W = dtype == DP_BF16 ? 8 : 4, G = norm_shape(D, D % W ? 1 : W).G;
+  const long long most = std::max<long long>(1, rows / (4 * norm_rows(G)));
+  const long long want = (152 * grad_ctas(G) + segments - 1) / segments;
   return (int)std::max<long long>(1, std::min(most, want));
 }
 
 template <class E, int VEC>
 static cudaError_t run_norm_grad(const NormParams& P, cudaStream_t s) {
-  return with_norm_shape(P.D, [&](auto g, auto c) {
+  return with_norm_shape<VEC>(P.D, [&](auto g, auto c) {
     constexpr int G = decltype(g)::value, C = decltype(c)::value;
-    const long long rows = (long long)P.B * P.T / P.segments / P.slices;
-    const int warps = (int)std::max<long long>(1, std::min<long long>(8, rows));
-    const size_t smem = G == 32 && P.part ? (size_t)P.k * P.D * 4 : 0;   // at most 8 KB
+    constexpr int S = ring_stages(sizeof(E), VEC, G, C), row_bytes = 2 * C / VEC * 16;   // of a thread
+    const long long rows = ((long long)P.B * P.T / P.segments + P.slices - 1) / P.slices;   // of a slice
+    const int threads = G > 32 ? G : (int)std::min<long long>(256, (rows * G + 31) / 32 * 32);
+    const size_t sums = G <= 32 && P.part ? (size_t)threads * P.k * C * 4 : 0;
+    const size_t smem = std::max((size_t)S * threads * row_bytes, sums);
+    constexpr int most = std::max(S * norm_threads(G) * row_bytes, G <= 32 ? 256 * 2 * C * 4 : 0);
+    if (most > 40 * 1024) {   // (beside the static arrays)
+      const cudaError_t e = allow_smem<layer_norm_grad_kernel<E, VEC, G, C>>(most);
+      if (e != cudaSuccess) return e;
+    }
     return launch_operator(layer_norm_grad_kernel<E, VEC, G, C>, dim3((unsigned)P.segments * (unsigned)P.slices),
-                           dim3(G == 32 ? 32 * warps : G), smem, s, P);
+                           dim3(threads), smem, s, P);
   });
 }
 

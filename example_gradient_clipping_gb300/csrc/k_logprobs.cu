@@ -4,13 +4,14 @@
 //   entropy = ls - sum_j p_j (z_j - m) / tau,
 //   dz_j = [ dl (delta_jy - p_j) - dh p_j (log p_j + entropy) ] / tau
 //
-// Forward: one pass over the row with each thread's running reference and sums (sum of e = 2^x and of e x, x
-// the distance to the reference in log2 units, so that no large logits cancel); the reference moves
-// only when the maximum outgrows it by 2^8.  For the alternatives each group of neighbouring vectors keeps
-// its maximum on chip.  The K-th largest of the 256 threads' maxima is a bound that at least K logits reach, and
-// usually few more: only groups whose maximum reaches it are read again, and what reaches it is ranked by
-// (value, index).  Where more logits reach it than there is room for (many equal ones), the exact K-th
-// largest value is found by bisection, and its ties are taken in the order of their indices.
+// Forward: one pass over the row with each thread's running reference R and sums of e = 2^x and of e x, where
+// x = z log2(e) / tau - R is one rounded multiply-add: R is a number of fp32, so its own rounding moves every
+// x alike, and no large logits cancel.  R moves only when the maximum outgrows it by 2^8.  For the
+// alternatives the vectors that a thread reads together keep their maximum on chip.  The K-th largest of the 256
+// threads' maxima is a bound that at least K logits reach, and usually few more: only groups of vectors
+// whose maximum reaches it are read again, and what reaches it is ranked by (value, index).  Where more logits
+// reach it than there is room for (many equal ones), the exact K-th largest value is found by bisection, and
+// its ties are taken in the order of their indices.
 // A row is one CTA's, or with few rows a cluster's.  Bound by HBM.
 //
 // Gradient: one read and one write of the rows, elementwise from m, ls and the entropy.  Bound by HBM.
@@ -22,9 +23,12 @@
 namespace dpk {
 namespace logprobs {
 
-constexpr int kThreads = 256, kTop = 128, kRoom = 1024;   // most alternatives; candidates that are ranked
+constexpr int kThreads = 256, kTop = 128;   // most alternatives
+constexpr int kRoom = 1024, kList = 512;    // candidates that are ranked, groups that are read again
 constexpr unsigned kAll = 0xffffffffu;
-constexpr float kLowest = -3.402823466e38f, kFloor = -150.f;   // 2^-150 is 0
+constexpr float kFloor = -150.f;   // 2^-150 is 0
+constexpr float kFar = 1e29f;      // logits times log2(e) / tau beyond it take the sums of differences to the maximum
+constexpr int kFly = 4;            // vectors that a thread reads together
 
 __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
   float r;
@@ -44,52 +48,99 @@ template <class E> struct Vec {
   Pack<E, W> p;
   __device__ __forceinline__ float get(int n) const { return p.get(n); }
 };
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {   // two bf16
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The largest entry of N vectors (NaN if there is one).
+template <int N> __device__ __forceinline__ float top_of(const Vec<__nv_bfloat16> (&v)[N]) {
+  uint32_t m = v[0].p.w[0];
+#pragma unroll
+  for (int i = 1; i < 4 * N; ++i) m = max2_nan(m, v[i / 4].p.w[i % 4]);
+  return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+}
+template <int N> __device__ __forceinline__ float top_of(const Vec<float> (&v)[N]) {
+  float m = v[0].p.w[0];
+#pragma unroll
+  for (int i = 1; i < 4 * N; ++i) m = max_nan(m, v[i / 4].p.w[i % 4]);
+  return m;
+}
+// Entries below `low` become it (it: the same value as the vectors hold it).
+__device__ __forceinline__ void raise_to(Vec<__nv_bfloat16>& v, uint32_t low2) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v.p.w[i] = max2_nan(v.p.w[i], low2);
+}
+__device__ __forceinline__ void raise_to(Vec<float>& v, float low) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v.p.w[i] = max_nan(v.p.w[i], low);
+}
+__device__ __forceinline__ uint32_t low_of(float low, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(low, low);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float low_of(float low, float) { return low; }
 
-// The row on the grid of 16-byte vectors: its first entry is entry `mis` of vector 0.
+// The smallest value whose key reaches k; 0 gives a NaN, which no value is below.
+__device__ __forceinline__ float value_of(unsigned k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+
+// The row on the grid of 16-byte vectors: its first entry is entry `mis` of vector 0.  A part of it is the
+// vectors [j0, j1), which the CTA reads in rounds of kFly vectors a thread; a group is what a thread reads in
+// 2^shift consecutive rounds.
 template <class E> struct Grid {
+  static constexpr int W = Vec<E>::W;
   const E* row;
-  int V, mis, nvec;
-  __device__ __forceinline__ Grid(const E* r, int v) : row(r), V(v) {
-    constexpr int W = Vec<E>::W;
+  int V, mis, j0, j1;
+  unsigned inner;   // a vector that starts at an entry below it is whole and in the part
+  __device__ __forceinline__ Grid(const E* r, int v, int rank, int per) : row(r), V(v) {
     mis = (int)(reinterpret_cast<uintptr_t>(r) / sizeof(E)) & (W - 1);
-    nvec = (V + mis + W - 1) / W;
+    const int nvec = (V + mis + W - 1) / W;
+    j0 = (int)min((long long)nvec, (long long)rank * per);
+    j1 = min(nvec, j0 + per);
+    inner = j1 > j0 ? (unsigned)max(0, min(V - W, (j1 - 1) * W - mis) + 1) : 0;
   }
-  // Vector j, entries outside the row as -inf.
+  // Vector j of the part, entries outside the row (and vectors outside the part) as -inf.
   __device__ __forceinline__ Vec<E> load(int j) const {
-    constexpr int W = Vec<E>::W;
     const int e0 = j * W - mis;
     Vec<E> v;
-    if (e0 >= 0 && e0 + W <= V) {
+    if ((unsigned)e0 < inner) {
       v.p = *reinterpret_cast<const Pack<E, W>*>(row + e0);
     } else {
       float f[W];
 #pragma unroll
-      for (int n = 0; n < W; ++n) f[n] = e0 + n >= 0 && e0 + n < V ? to_f(row[e0 + n]) : -INFINITY;
+      for (int n = 0; n < W; ++n) f[n] = j < j1 && e0 + n >= 0 && e0 + n < V ? to_f(row[e0 + n]) : -INFINITY;
       v.p.set(f);
     }
     return v;
   }
+  __device__ __forceinline__ int rounds() const { return (j1 - j0 + kThreads * kFly - 1) / (kThreads * kFly); }
+  __device__ __forceinline__ int groups(int shift) const { return ((rounds() + (1 << shift) - 1) >> shift) * kThreads; }
+  // Vector i (of kFly << shift) of group q; it may lie past the part.
+  __device__ __forceinline__ int vector(int q, int i, int shift) const {
+    return j0 + (((q / kThreads << shift) * kFly + i) * kThreads + q % kThreads);
+  }
 };
 
 using ptx::cluster_sync;
-// A word of another CTA of the cluster, at the place that `p` has here.
-__device__ __forceinline__ float dsmem_ld(const float* p, int rank) {
-  return ptx::ld_cluster_f32(ptx::map_rank(ptx::smem_u32(p), rank));
+// Cluster barrier in two halves, and stores to another CTA of the cluster at the place that `p` has here.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+__device__ __forceinline__ void dsmem_st(float* p, int rank, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ptx::map_rank(ptx::smem_u32(p), rank)), "f"(v) : "memory");
 }
-__device__ __forceinline__ unsigned long long dsmem_ld64(const unsigned long long* p, int rank) {
-  unsigned long long v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(ptx::map_rank(ptx::smem_u32(p), rank)) : "memory");
-  return v;
+__device__ __forceinline__ void dsmem_st(unsigned long long* p, int rank, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(ptx::map_rank(ptx::smem_u32(p), rank)), "l"(v) : "memory");
 }
 
 struct alignas(16) Shared {
   unsigned tmax[kThreads];               // each thread's largest key, 0 without any
   unsigned long long room[kRoom];        // candidates: key, then the index's complement
   unsigned long long best[kTop];         // the part's largest, in order
-  float red[3][8];
-  float m, sum, sumx;
+  unsigned short list[kList];            // groups whose maximum reaches the bound
+  float red[4][8];
+  float peer[8][4];                      // rank 0: every part's maximum and sums
   unsigned bound;
-  int count, wsum[8];
+  int count, groups, wsum[8];
 };
 
 __device__ __forceinline__ int block_sum(int v, Shared& sh) {
@@ -105,9 +156,9 @@ __device__ __forceinline__ int block_sum(int v, Shared& sh) {
 
 // The largest n keys of this part of the row, in order, to sh.best (n at most the part's entries).
 template <class E>
-__device__ void part_top(const Grid<E>& g, int j0, int j1, int shift, const float* gmax, int n, Shared& sh) {
+__device__ void part_top(const Grid<E>& g, int shift, const float* gmax, int n, Shared& sh) {
   constexpr int W = Vec<E>::W;
-  const int tid = threadIdx.x, lane = tid % 32, groups = ((j1 - j0) + (1 << shift) - 1) >> shift;
+  const int tid = threadIdx.x, lane = tid % 32, groups = g.groups(shift), size = kFly << shift;
   // a bound that n keys reach: the n-th largest of the threads' maxima, bit by bit (0 if fewer have one)
   if (tid < 32) {
     unsigned k[kThreads / 32], lo = kAll, hi = 0;
@@ -135,36 +186,56 @@ __device__ void part_top(const Grid<E>& g, int j0, int j1, int shift, const floa
     }
     if (lane == 0) {
       sh.bound = t;
-      sh.count = 0;
+      sh.count = sh.groups = 0;
     }
   }
   __syncthreads();
   unsigned bound = sh.bound;
-  // entries of vector j that pass, to the room; more than it holds are only counted
+  // entries of vector j that reach `least`, to the room; more than it holds are only counted
   auto collect = [&](int j, unsigned least) {
     const Vec<E> v = g.load(j);
+    const float low = value_of(least);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-      const int e = j * W - g.mis + i;
-      const unsigned k = key_of(v.get(i));
-      if (k >= least && e >= 0 && e < g.V) {
+      const float x = v.get(i);
+      if (!(x < low)) {   // (a NaN passes)
+        const int e = j * W - g.mis + i;
+        if (e < 0 || e >= g.V) continue;
         const int at = atomicAdd(&sh.count, 1);
-        if (at < kRoom) sh.room[at] = (unsigned long long)k << 32 | (unsigned)~e;
+        if (at < kRoom) sh.room[at] = (unsigned long long)key_of(x) << 32 | (unsigned)~e;
       }
     }
   };
-  for (int q = tid; q < groups; q += kThreads)
-    if (key_of(gmax[q]) >= bound)
-      for (int j = j0 + (q << shift); j < min(j1, j0 + ((q + 1) << shift)); ++j) collect(j, bound);
+  // the groups first, so that their vectors are then read by all threads at once
+  {
+    const float low = value_of(bound);
+    for (int q = tid; q < groups; q += kThreads)
+      if (!(gmax[q] < low)) {
+        const int at = atomicAdd(&sh.groups, 1);
+        if (at < kList) sh.list[at] = (unsigned short)q;
+      }
+  }
   __syncthreads();
-  int have = sh.count;
+  const int ng = sh.groups;
+  if (ng <= kList) {
+    const int log_size = shift + 2;
+    static_assert(kFly == 4, "log_size");
+    for (int i = tid; i < ng << log_size; i += kThreads) {
+      const int j = g.vector(sh.list[i >> log_size], i & (size - 1), shift);
+      if (j < g.j1) collect(j, bound);
+    }
+  }
+  __syncthreads();
+  int have = ng <= kList ? sh.count : kRoom + 1;
   if (have > kRoom) {
     // how many keys of the part reach `t`
     auto reach = [&](unsigned t) {
       int c = 0;
       for (int q = tid; q < groups; q += kThreads)
         if (key_of(gmax[q]) >= t)
-          for (int j = j0 + (q << shift); j < min(j1, j0 + ((q + 1) << shift)); ++j) {
+          for (int i0 = 0; i0 < size; ++i0) {
+            const int j = g.vector(q, i0, shift);
+            if (j >= g.j1) break;
             const Vec<E> v = g.load(j);
 #pragma unroll
             for (int i = 0; i < W; ++i) {
@@ -190,14 +261,14 @@ __device__ void part_top(const Grid<E>& g, int j0, int j1, int shift, const floa
     if (bound != kAll)
       for (int q = tid; q < groups; q += kThreads)
         if (key_of(gmax[q]) > bound)
-          for (int j = j0 + (q << shift); j < min(j1, j0 + ((q + 1) << shift)); ++j) collect(j, bound + 1);
+          for (int i = 0; i < size && g.vector(q, i, shift) < g.j1; ++i) collect(g.vector(q, i, shift), bound + 1);
     __syncthreads();
     have = sh.count;   // < n
     // its ties, lowest index first
-    for (int base = j0; base < j1 && have < n; base += kThreads) {
+    for (int base = g.j0; base < g.j1 && have < n; base += kThreads) {
       const int j = base + tid;
       unsigned mine = 0;
-      if (j < j1) {
+      if (j < g.j1) {
         const Vec<E> v = g.load(j);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
@@ -228,130 +299,183 @@ __device__ void part_top(const Grid<E>& g, int j0, int j1, int shift, const floa
     __syncthreads();
   }
   // every candidate's place among them
+  if (tid == 0 && (have & 1)) sh.room[have] = 0;   // (room for it: an odd count is below kRoom)
+  __syncthreads();
   for (int c = tid; c < have; c += kThreads) {
     const unsigned long long k = sh.room[c];
     int rank = 0;
-    for (int i = 0; i < have; ++i) rank += sh.room[i] > k;
+#pragma unroll 4
+    for (int i = 0; i < have; i += 2) {
+      const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&sh.room[i]);
+      rank += (o.x > k) + (o.y > k);
+    }
     if (rank < n) sh.best[rank] = k;
   }
   __syncthreads();
 }
 
+// Groups of a part of `per` vectors, at most.
+__host__ __device__ constexpr int max_groups(int per, int shift) {
+  return ((((per + kThreads * kFly - 1) / (kThreads * kFly)) + (1 << shift) - 1) >> shift) * kThreads;
+}
+
+// Sums of the part's e and e x at its maximum m by differences, for logits whose products would not be finite.
+template <class E>
+__device__ void far_sums(const Grid<E>& g, float m, float c2, float* sum, float* sumx) {
+  float s = 0.f, t = 0.f;
+  for (int j = g.j0 + (int)threadIdx.x; j < g.j1; j += kThreads) {
+    const Vec<E> v = g.load(j);
+#pragma unroll
+    for (int n = 0; n < Vec<E>::W; ++n) {
+      const float x = fmaxf((v.get(n) - m) * c2, kFloor), e = ex2(x);
+      s += e;
+      t = fmaf(e, x, t);
+    }
+  }
+  *sum = s;
+  *sumx = t;
+}
+
 template <class E, bool kAlt>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(LogprobParams P, int cluster, int per, int shift) {
+__global__ void __launch_bounds__(kThreads, kAlt ? 6 : 4) token_logprobs_kernel(LogprobParams P, int cluster, int per, int shift) {
   pdl_wait();
+  if (cluster > 1) cluster_arrive();   // that every CTA has begun, before its shared memory is written
   constexpr int W = Vec<E>::W;
   extern __shared__ unsigned char dyn[];
   Shared& sh = *reinterpret_cast<Shared*>(dyn);
   float* gmax = reinterpret_cast<float*>(dyn + sizeof(Shared));
   const int tid = threadIdx.x, lane = tid % 32;
   const unsigned row = blockIdx.x / (unsigned)cluster, rank = blockIdx.x - row * (unsigned)cluster;
-  const Grid<E> g(static_cast<const E*>(P.logits) + (size_t)row * P.ld, P.V);
-  const int j0 = (int)min((long long)g.nvec, (long long)rank * per), j1 = min(g.nvec, j0 + per);
+  const Grid<E> g(static_cast<const E*>(P.logits) + (size_t)row * P.ld, P.V, (int)rank, per);
   const float itau = 1.f / P.tau, c2 = kLog2e * itau, reach = 8.f / c2;
-  float ref = kLowest, top = -INFINITY;
+  // entries below `low` give e = 0 as they do, and a finite x
+  const auto low = low_of(-10.f * kFar / c2, E());
+  float ref = -kFar / c2, R = -kFar, top = -INFINITY;
   uint64_t S = 0, T = 0;   // packed pairs
   const uint64_t cc = pair(c2, c2);
-  constexpr int kFly = 4;
-  for (int base = j0; base < j1; base += kThreads * kFly) {
-    Vec<E> v[kFly];
+  Vec<E> v[kFly], next[kAlt ? 1 : kFly];
+  auto fetch = [&](Vec<E>* d, int j) {
 #pragma unroll
-    for (int f = 0; f < kFly; ++f) {
-      const int j = base + f * kThreads + tid;
-      if (j < j1) v[f] = g.load(j);
+    for (int f = 0; f < kFly; ++f) d[f] = g.load(j + f * kThreads);
+  };
+  const int rounds = g.rounds();
+  if (!kAlt) fetch(v, g.j0 + tid);
+#pragma unroll (kAlt ? 1 : 2)
+  for (int q = 0; q < rounds; ++q) {
+    if (kAlt) fetch(v, g.j0 + q * kThreads * kFly + tid);
+    else if (q + 1 < rounds) fetch(next, g.j0 + (q + 1) * kThreads * kFly + tid);
+    const float m = top_of(v);
+    top = max_nan(top, m);
+    if constexpr (kAlt) {
+      float* at = gmax + (q >> shift) * kThreads + tid;
+      *at = q & ((1 << shift) - 1) ? max_nan(*at, m) : m;
     }
+    if (m > ref + reach) {
+      const float r = m * c2, d = fmaxf(R - r, kFloor), s = ex2(d);
+      const uint64_t ss = pair(s, s), dd = pair(d, d);
+      T = mul2(ss, fma2(S, dd, T));
+      S = mul2(ss, S);
+      ref = m;
+      R = r;
+    }
+    const uint64_t nr = pair(-R, -R);
 #pragma unroll
     for (int f = 0; f < kFly; ++f) {
-      const int j = base + f * kThreads + tid;
-      float m = -INFINITY;
-      if (j < j1) {
-        m = v[f].get(0);
+      raise_to(v[f], low);
 #pragma unroll
-        for (int n = 1; n < W; ++n) m = max_nan(m, v[f].get(n));
-        top = max_nan(top, m);
-        if (m > ref + reach) {
-          const float d = fmaxf((ref - m) * c2, kFloor), s = ex2(d);
-          const uint64_t ss = pair(s, s), dd = pair(d, d);
-          T = mul2(ss, fma2(S, dd, T));
-          S = mul2(ss, S);
-          ref = m;
-        }
-        const uint64_t nr = pair(-ref, -ref);
+      for (int n = 0; n < W; n += 2) {
+        const uint64_t x = fma2(pair(v[f].get(n), v[f].get(n + 1)), cc, nr);
+        const float2 y = unpair(x);
+        const uint64_t e = pair(ex2(y.x), ex2(y.y));
+        S = add2(S, e);
+        T = fma2(e, x, T);
+      }
+    }
+    if constexpr (!kAlt) {
 #pragma unroll
-        for (int n = 0; n < W; n += 2) {
-          const float2 x = unpair(mul2(add2(pair(v[f].get(n), v[f].get(n + 1)), nr), cc));
-          const float a = max_nan(x.x, kFloor), b = max_nan(x.y, kFloor);
-          const uint64_t e = pair(ex2(a), ex2(b));
-          S = add2(S, e);
-          T = fma2(e, pair(a, b), T);
-        }
-      }
-      if constexpr (kAlt) {
-        for (int o = 1; o < 1 << shift && o < 32; o <<= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, o));
-        if (j < j1 && (lane & ((1 << shift) - 1)) == 0) gmax[(j - j0) >> shift] = m;
-      }
+      for (int f = 0; f < kFly; ++f) v[f] = next[f];
     }
   }
-  // the row's (part's) maximum, and the sums at it
-  float m = top;
+  // the row's (part's) maximum and reference
+  float m = top, r = R;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, o));
-  if (lane == 0) sh.red[0][tid / 32] = m;
+  for (int o = 16; o > 0; o >>= 1) {
+    m = max_nan(m, __shfl_xor_sync(kAll, m, o));
+    r = fmaxf(r, __shfl_xor_sync(kAll, r, o));
+  }
+  if (lane == 0) {
+    sh.red[0][tid / 32] = m;
+    sh.red[1][tid / 32] = r;
+  }
   if constexpr (kAlt) {
-    sh.tmax[tid] = j0 + tid < j1 ? key_of(top) : 0;
+    sh.tmax[tid] = g.j0 + tid < g.j1 ? key_of(top) : 0;
     if (tid < kTop) sh.best[tid] = 0;   // below every key, past the part's own
   }
   __syncthreads();
   m = sh.red[0][0];
+  r = sh.red[1][0];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) m = max_nan(m, sh.red[0][w]);
+  for (int w = 1; w < 8; ++w) {
+    m = max_nan(m, sh.red[0][w]);
+    r = fmaxf(r, sh.red[1][w]);
+  }
   {
-    const float d = m == -INFINITY ? 0.f : max_nan((ref - m) * c2, kFloor), s = ex2(d);   // (-inf: the sums are 0)
-    const float2 s2 = unpair(S), t2 = unpair(T);
-    const float sum = s2.x + s2.y, x = s * fmaf(sum, d, t2.x + t2.y);
-    const float a = warp_sum(sum * s), b = warp_sum(x);
+    float sum, x;
+    if (fabsf(m) < INFINITY && !(fabsf(m) * c2 < kFar)) {   // (the same for every thread)
+      far_sums(g, m, c2, &sum, &x);
+    } else {   // moved to x = (z - m) log2(e) / tau
+      const float d = fmaxf(R - r, kFloor) - fmaf(m, c2, -r), s = ex2(d);
+      const float2 s2 = unpair(S), t2 = unpair(T);
+      sum = s2.x + s2.y;
+      x = s * fmaf(sum, d, t2.x + t2.y);
+      sum *= s;
+    }
+    const float a = warp_sum(sum), b = warp_sum(x);
     if (lane == 0) {
-      sh.red[1][tid / 32] = a;
-      sh.red[2][tid / 32] = b;
+      sh.red[2][tid / 32] = a;
+      sh.red[3][tid / 32] = b;
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    float a = 0.f, b = 0.f;
+  float sum = 0.f, sumx = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      a += sh.red[1][w];
-      b += sh.red[2][w];
-    }
-    sh.m = m;
-    sh.sum = a;
-    sh.sumx = b;
+  for (int w = 0; w < 8; ++w) {
+    sum += sh.red[2][w];
+    sumx += sh.red[3][w];
   }
-  __syncthreads();
+  if (m == -INFINITY) sum = sumx = 0.f;   // nothing but masks, or an empty part
   int have = 0;   // alternatives of this part
   if constexpr (kAlt) {
-    const int e0 = max(0, j0 * W - g.mis), e1 = min(P.V, j1 * W - g.mis);
+    const int e0 = max(0, g.j0 * W - g.mis), e1 = min(P.V, g.j1 * W - g.mis);
     have = min(P.K, max(0, e1 - e0));
-    if (have > 0) part_top(g, j0, j1, shift, gmax, have, sh);
+    if (have > 0) part_top(g, shift, gmax, have, sh);
   }
-  __syncthreads();
-  if (cluster > 1) cluster_sync();   // every part's sums and largest keys stand in its shared memory
+  auto* lists = reinterpret_cast<unsigned long long*>(gmax + max_groups(per, shift));   // [cluster][K]
+  if (cluster > 1) {   // to rank 0
+    __syncthreads();
+    cluster_wait();
+    if (tid == 0) {
+      dsmem_st(&sh.peer[rank][0], 0, m);
+      dsmem_st(&sh.peer[rank][1], 0, sum);
+      dsmem_st(&sh.peer[rank][2], 0, sumx);
+    }
+    if (kAlt && tid < P.K) dsmem_st(&lists[rank * P.K + tid], 0, sh.best[tid]);
+    __syncwarp();
+    cluster_sync();
+  }
   if (rank == 0) {
-    float sum = sh.sum, sumx = sh.sumx;
     if (cluster > 1) {
-      float pm[8], ps[8], px[8];
-      for (int r = 0; r < cluster; ++r) {
-        pm[r & 7] = dsmem_ld(&sh.m, r);
-        ps[r & 7] = dsmem_ld(&sh.sum, r);
-        px[r & 7] = dsmem_ld(&sh.sumx, r);
-        m = max_nan(m, pm[r & 7]);
-      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < cluster) m = max_nan(m, sh.peer[r][0]);
       sum = sumx = 0.f;
-      for (int r = 0; r < cluster; ++r) {   // an empty part: its maximum is -inf, its sums 0
-        const float d = max_nan((pm[r & 7] - m) * c2, kFloor), s = ex2(d);
-        sum = fmaf(ps[r & 7], s, sum);
-        sumx += s * fmaf(ps[r & 7], d, px[r & 7]);
-      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < cluster) {   // an empty part: its maximum is -inf, its sums 0
+          const float d = max_nan((sh.peer[r][0] - m) * c2, kFloor), s = ex2(d), q = sh.peer[r][1];
+          sum = fmaf(q, s, sum);
+          sumx += s * fmaf(q, d, sh.peer[r][2]);
+        }
     }
     const float ls = logf(sum), gone = m == -INFINITY ? __int_as_float(0x7fc00000) : 0.f;
     if (tid == 0) {
@@ -370,48 +494,39 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(LogprobParams 
     }
     if constexpr (kAlt) {
       auto put = [&](int at, unsigned long long k) {
-        const unsigned b = (unsigned)(k >> 32);
-        const float z = __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
-        P.top[(size_t)row * P.K + at] = (z - m) * itau - ls + gone;
+        P.top[(size_t)row * P.K + at] = (value_of((unsigned)(k >> 32)) - m) * itau - ls + gone;
         P.top_index[(size_t)row * P.K + at] = (int)~(unsigned)k;
       };
       if (cluster == 1) {
         for (int i = tid; i < P.K; i += kThreads) put(i, sh.best[i]);
       } else {
         // the parts' lists together; a key's place is its own place and, in every other list, how many are above it
-        for (int i = tid; i < cluster * kTop; i += kThreads) {
-          const int r = i / kTop, at = i % kTop;
-          sh.room[i] = at < P.K ? dsmem_ld64(&sh.best[at], r) : 0ull;
-        }
-        __syncthreads();
-        for (int i = tid; i < cluster * kTop; i += kThreads) {
-          const int r = i / kTop, at = i % kTop;
-          const unsigned long long k = sh.room[i];
+        for (int i = tid; i < cluster * P.K; i += kThreads) {
+          const int r = i / P.K;
+          const unsigned long long k = lists[i];
           if (k == 0) continue;
-          int place = at;
-          for (int q = 0; q < cluster; ++q) {
-            if (q == r) continue;
-            int lo = 0, hi = kTop;   // entries above k stand first, zeros last
-            while (lo < hi) {
-              const int mid = (lo + hi) / 2;
-              if (sh.room[q * kTop + mid] > k) lo = mid + 1;
-              else hi = mid;
-            }
-            place += lo;
-          }
+          int above[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) above[q] = 0;
+#pragma unroll
+          for (int step = kTop; step > 0; step >>= 1)   // entries above k stand first, zeros last
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (q < cluster && above[q] + step <= P.K && lists[q * P.K + above[q] + step - 1] > k) above[q] += step;
+          int place = i - r * P.K;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) place += q == r ? 0 : above[q];
           if (place < P.K) put(place, k);
         }
       }
     }
   }
-  __syncthreads();
-  if (cluster > 1) cluster_sync();   // nobody leaves while rank 0 reads its shared memory
   pdl_trigger();
 }
 
-// A CTA takes 1024 vectors of a row.
+// A CTA takes `rounds` times kThreads * kFly vectors of a row, the next round's loads under the current one.
 template <class E, bool kVec>
-__global__ void __launch_bounds__(kThreads) token_logprobs_grad_kernel(LogprobParams P, int chunks) {
+__global__ void __launch_bounds__(kThreads) token_logprobs_grad_kernel(LogprobParams P, int chunks, int rounds) {
   pdl_wait();
   constexpr int W = kVec ? Vec<E>::W : 1, kFly = kVec ? 4 : 8;
   const unsigned row = blockIdx.x / (unsigned)chunks;
@@ -420,50 +535,61 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_grad_kernel(LogprobPa
   E* o = static_cast<E*>(P.grad) + (size_t)row * P.ldg;
   const long long y = P.tokens ? ld_index(P.tokens, P.token_i64, row) : -1;
   const float itau = 1.f / P.tau, c2 = kLog2e * itau;
-  float dl = P.d_logprob && y >= 0 ? P.d_logprob[row] : 0.f;
+  float dl = P.d_logprob ? P.d_logprob[row] : 0.f;
   const float dh = P.d_entropy ? P.d_entropy[row] : 0.f;
+  const float m = P.stats[2 * (size_t)row], ls = P.stats[2 * (size_t)row + 1], ls2 = ls * kLog2e, h = P.entropy[row];
+  if (y < 0) dl = 0.f;
   if (y >= P.V) {
     if (threadIdx.x == 0 && chunk == 0) atomicOr(P.status, kStatusIndex);
     dl = __int_as_float(0x7fc00000);
   }
   const bool zero = dl == 0.f && dh == 0.f;
-  const float m = P.stats[2 * (size_t)row], ls = P.stats[2 * (size_t)row + 1], ls2 = ls * kLog2e;
-  // p_j (a + b x_j), x the distance to m in log2 units; a row of one entry that is all: p = 1
-  const float a = zero ? 0.f : itau * (-dl - dh * (P.entropy[row] - ls)), b = -itau * dh * kLn2, at_y = dl * itau;
+  // p_j (a + b x_j), x the distance to m in log2 units
+  const float a = itau * (-dl - dh * (h - ls)), b = -itau * dh * kLn2, at_y = dl * itau;
   auto grad = [&](float v) {
     const float x = max_nan((v - m) * c2, kFloor);
     return ex2(x - ls2) * fmaf(b, x, a);
   };
   const int mis = kVec ? (int)(reinterpret_cast<uintptr_t>(z) / sizeof(E)) & (W - 1) : 0;
-  const int first = chunk * kThreads * kFly + (int)threadIdx.x;   // vectors
-  Pack<E, W> v[kFly];
+  long long first = (long long)chunk * rounds * kThreads * kFly + (int)threadIdx.x;   // vectors
+  Pack<E, W> v[kFly], next[kFly];
+  auto fetch = [&](Pack<E, W> (&d)[kFly], long long from) {
 #pragma unroll
-  for (int f = 0; f < kFly; ++f) {
-    const long long e = (long long)(first + f * kThreads) * W - mis;
-    if (!zero && e >= 0 && e + W <= P.V) v[f] = *reinterpret_cast<const Pack<E, W>*>(z + e);
-  }
-  pdl_trigger();
-#pragma unroll
-  for (int f = 0; f < kFly; ++f) {
-    const long long e = (long long)(first + f * kThreads) * W - mis;
-    if (e >= 0 && e + W <= P.V) {
-      float d[W];
-#pragma unroll
-      for (int n = 0; n < W; ++n) {
-        d[n] = zero ? 0.f : grad(v[f].get(n));
-        if (e + n == y) d[n] += at_y;
-      }
-      Pack<E, W> out;
-      out.set(d);
-      *reinterpret_cast<Pack<E, W>*>(o + e) = out;
-    } else {
-      for (int n = 0; n < W; ++n)
-        if (e + n >= 0 && e + n < P.V) {
-          float d = zero ? 0.f : grad(to_f(z[e + n]));
-          if (e + n == y) d += at_y;
-          o[e + n] = from_f(d, E());
-        }
+    for (int f = 0; f < kFly; ++f) {
+      const long long e = (from + f * kThreads) * W - mis;
+      if (!zero && e >= 0 && e + W <= P.V) d[f] = *reinterpret_cast<const Pack<E, W>*>(z + e);
     }
+  };
+  fetch(v, first);
+  for (int q = 0; q < rounds; ++q, first += kThreads * kFly) {
+    if (q + 1 < rounds) fetch(next, first + kThreads * kFly);
+    else pdl_trigger();
+#pragma unroll
+    for (int f = 0; f < kFly; ++f) {
+      const long long e = (first + f * kThreads) * W - mis;
+      if (e >= 0 && e + W <= P.V) {
+        float d[W];
+#pragma unroll
+        for (int n = 0; n < W; ++n) d[n] = zero ? 0.f : grad(v[f].get(n));
+        if (y >= e && y < e + W) {
+#pragma unroll
+          for (int n = 0; n < W; ++n)
+            if (e + n == y) d[n] += at_y;
+        }
+        Pack<E, W> out;
+        out.set(d);
+        *reinterpret_cast<Pack<E, W>*>(o + e) = out;
+      } else {
+        for (int n = 0; n < W; ++n)
+          if (e + n >= 0 && e + n < P.V) {
+            float d = zero ? 0.f : grad(to_f(z[e + n]));
+            if (e + n == y) d += at_y;
+            o[e + n] = from_f(d, E());
+          }
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < kFly; ++f) v[f] = next[f];
   }
 }
 
@@ -482,20 +608,14 @@ static cudaError_t run_logprobs(const LogprobParams& P, cudaStream_t s) {
   // a cluster a row while that leaves every CTA two rounds of loads and the GPU is not full
   int cluster = 1;
   while (cluster < 8 && rows * cluster * 2 <= 304 && nvec / (2 * cluster) >= 2 * kThreads) cluster *= 2;
-  // groups of 2^shift vectors, at most 4096 of them a part
-  int shift = 0;
-  long long per = (nvec + cluster - 1) / cluster;
-  while (per >> shift > 4095 && shift < 5) ++shift;
-  per = ((per >> shift) + 1) << shift;
-  const size_t smem = sizeof(Shared) + (kAlt ? (size_t)(per >> shift) * 4 : 0);
+  const int per = (int)((nvec + cluster - 1) / cluster);
+  int shift = 0;   // at most 4096 groups a part: 16 KB
+  while (max_groups(per, shift) > 4096) ++shift;
+  const size_t smem = sizeof(Shared) + (kAlt ? (size_t)max_groups(per, shift) * 4 + (cluster > 1 ? (size_t)cluster * P.K * 8 : 0) : 0);
   auto kernel = token_logprobs_kernel<E, kAlt>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = allow_smem<token_logprobs_kernel<E, kAlt>>(200 * 1024);
-    if (e != cudaSuccess) return e;
-  }
-  if (cluster == 1) return launch_operator(kernel, dim3((unsigned)rows), dim3(kThreads), smem, s, P, 1, (int)per, shift);
+  if (cluster == 1) return launch_operator(kernel, dim3((unsigned)rows), dim3(kThreads), smem, s, P, 1, per, shift);
   return launch_operator_cluster(kernel, cluster, dim3((unsigned)(rows * cluster)), dim3(kThreads), smem, s, P, cluster,
-                                 (int)per, shift);
+                                 per, shift);
 }
 
 cudaError_t launch_logprobs(const LogprobParams& P, int dtype, cudaStream_t s) {
@@ -510,12 +630,16 @@ static cudaError_t run_logprobs_grad(const LogprobParams& P, cudaStream_t s) {
   const auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p) / sizeof(E) % W; };
   const bool vec = at(P.logits) == at(P.grad) && ((P.ld - P.ldg) % W == 0 || (long long)P.B * P.T == 1);
   const long long rows = (long long)P.B * P.T;
-  const long long chunks = vec ? (((long long)P.V + 2 * W - 2) / W + 4 * kThreads - 1) / (4 * kThreads)
-                               : ((long long)P.V + 8 * kThreads - 1) / (8 * kThreads);
+  // rounds a CTA: the row's constants are read once for them, while the CTAs fill the GPU a few times
+  const long long round = vec ? 4 * kThreads * W : 8 * kThreads;
+  const long long all = ((long long)P.V + (vec ? W - 1 : 0) + round - 1) / round;
+  long long rounds = std::max<long long>(1, std::min<long long>(16, all * rows / (152 * 8 * 4)));
+  const long long chunks = (all + rounds - 1) / rounds;
+  rounds = (all + chunks - 1) / chunks;
   if (rows * chunks > 2147483647ll) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)(rows * chunks));
-  return vec ? launch_operator(token_logprobs_grad_kernel<E, true>, grid, dim3(kThreads), 0, s, P, (int)chunks)
-             : launch_operator(token_logprobs_grad_kernel<E, false>, grid, dim3(kThreads), 0, s, P, (int)chunks);
+  return vec ? launch_operator(token_logprobs_grad_kernel<E, true>, grid, dim3(kThreads), 0, s, P, (int)chunks, (int)rounds)
+             : launch_operator(token_logprobs_grad_kernel<E, false>, grid, dim3(kThreads), 0, s, P, (int)chunks, (int)rounds);
 }
 
 cudaError_t launch_logprobs_grad(const LogprobParams& P, int dtype, cudaStream_t s) {

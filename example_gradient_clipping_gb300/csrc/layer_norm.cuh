@@ -7,45 +7,31 @@
 namespace dpk {
 namespace lnorm {
 
-// A row of D entries is held by G threads (a warp of a CTA of several, or a whole CTA), C entries a
-// thread as C / VEC vectors: vector k of a thread is the row's vector lane + k G.
+// A row of D entries is held by G threads (G <= 32: a group of a CTA of 256 threads; else a whole CTA), C entries
+// a thread as C / VEC vectors: vector k of a thread is the row's vector lane + k G.
 template <class E, int VEC, int C> struct Row {
   Pack<E, VEC> v[C / VEC];
   __device__ __forceinline__ float get(int c) const { return v[c / VEC].get(c % VEC); }
 };
 
-template <class E, int VEC, int G, int C>
-__device__ __forceinline__ void load_row(Row<E, VEC, C>& r, const E* p, int lane, int D) {
+// VEC entries of a parameter vector of either type from column col on (null: `none`).
+template <int VEC>
+__device__ __forceinline__ void load_param_at(float (&f)[VEC], const void* p, int bf16, float none, int col) {
+  if (!p) {
 #pragma unroll
-  for (int k = 0; k < C / VEC; ++k) {
-    const int col = (lane + k * G) * VEC;
-    if (col < D) r.v[k] = *reinterpret_cast<const Pack<E, VEC>*>(p + col);
-    else r.v[k] = Pack<E, VEC>{};
-  }
-}
-
-// C entries of a parameter vector of either type in the rows' order (null: `none`), 0 past D.
-template <int VEC, int G, int C>
-__device__ __forceinline__ void load_param(float (&f)[C], const void* p, int bf16, float none, int lane, int D) {
+    for (int n = 0; n < VEC; ++n) f[n] = none;
+  } else if (bf16) {
+    const Pack<__nv_bfloat16, VEC> w = *reinterpret_cast<const Pack<__nv_bfloat16, VEC>*>(
+        static_cast<const __nv_bfloat16*>(p) + col);
 #pragma unroll
-  for (int k = 0; k < C / VEC; ++k) {
-    const int col = (lane + k * G) * VEC;
-    if (col >= D || !p) {
+    for (int n = 0; n < VEC; ++n) f[n] = w.get(n);
+  } else {
+    constexpr int H = VEC > 4 ? 4 : VEC;   // 16 bytes at a time
 #pragma unroll
-      for (int n = 0; n < VEC; ++n) f[k * VEC + n] = col < D ? none : 0.f;
-    } else if (bf16) {
-      const Pack<__nv_bfloat16, VEC> w = *reinterpret_cast<const Pack<__nv_bfloat16, VEC>*>(
-          static_cast<const __nv_bfloat16*>(p) + col);
+    for (int h = 0; h < VEC / H; ++h) {
+      const Pack<float, H> w = *reinterpret_cast<const Pack<float, H>*>(static_cast<const float*>(p) + col + h * H);
 #pragma unroll
-      for (int n = 0; n < VEC; ++n) f[k * VEC + n] = w.get(n);
-    } else {
-      constexpr int H = VEC > 4 ? 4 : VEC;   // 16 bytes at a time
-#pragma unroll
-      for (int h = 0; h < VEC / H; ++h) {
-        const Pack<float, H> w = *reinterpret_cast<const Pack<float, H>*>(static_cast<const float*>(p) + col + h * H);
-#pragma unroll
-        for (int n = 0; n < H; ++n) f[k * VEC + h * H + n] = w.get(n);
-      }
+      for (int n = 0; n < H; ++n) f[h * H + n] = w.get(n);
     }
   }
 }
@@ -56,7 +42,10 @@ __device__ __forceinline__ void load_param(float (&f)[C], const void* p, int bf1
 template <int G, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[N][32], int& round) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) v[n] = warp_sum(v[n]);
+  for (int n = 0; n < N; ++n) {
+#pragma unroll
+    for (int o = (G < 32 ? G : 32) / 2; o > 0; o >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+  }
   if constexpr (G > 32) {
     constexpr int W = G / 32;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -81,37 +70,49 @@ __device__ __forceinline__ size_t row_at(const dp_row_strides& s, int T, unsigne
   return (size_t)b * s.b + (size_t)(r - b * (unsigned)T) * s.t;
 }
 
-// Threads a row and entries a thread (see `plan`).
+// 16 bytes to shared memory, asynchronously (zeros without a source).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Threads a row and entries a thread.
 struct Shape { int G, C; };
 
 }  // namespace lnorm
 }  // namespace dpk
 
 namespace dph {
-// A warp a row up to 1024 entries (32 a thread), else 16 entries a thread and a CTA a row.
-inline dpk::lnorm::Shape norm_shape(int D) {
+// Threads of a CTA, and rows that it holds at once.
+constexpr int norm_threads(int G) { return G > 32 ? G : 256; }
+constexpr int norm_rows(int G) { return G > 32 ? 1 : 256 / G; }
+// Eight entries a thread for short rows, so that their threads have some; up to a warp a row with 32 (bf16
+// vectors) or 16 entries a thread; then a CTA a row.
+inline dpk::lnorm::Shape norm_shape(int D, int vec) {
+  if (D <= 64) return {8, 8};
+  if (D <= 128) return {16, 8};
   if (D <= 256) return {32, 8};
   if (D <= 512) return {32, 16};
-  if (D <= 768) return {32, 24};
-  if (D <= 1024) return {32, 32};
+  if (vec == 8 && D <= 768) return {32, 24};
+  if (vec == 8 && D <= 1024) return {32, 32};
+  if (D <= 1024) return {128, 8};
   if (D <= 2048) return {128, 16};
   if (D <= 4096) return {256, 16};
   if (D <= 8192) return {512, 16};
   return {1024, 16};
 }
-// Calls f<G, C>() for the shape of D.
-template <class F> cudaError_t with_norm_shape(int D, F&& f) {
+// Calls f(G, C), integral constants, for the shape of D.
+template <int VEC, class F> cudaError_t with_norm_shape(int D, F&& f) {
+  const dpk::lnorm::Shape s = norm_shape(D, VEC);
+  auto is = [&](int g, int c) { return s.G == g && s.C == c; };
   using std::integral_constant;
-  const dpk::lnorm::Shape s = norm_shape(D);
-  if (s.G == 32) {
-    if (s.C == 8) return f(integral_constant<int, 32>(), integral_constant<int, 8>());
-    if (s.C == 16) return f(integral_constant<int, 32>(), integral_constant<int, 16>());
-    if (s.C == 24) return f(integral_constant<int, 32>(), integral_constant<int, 24>());
-    return f(integral_constant<int, 32>(), integral_constant<int, 32>());
-  }
-  if (s.G == 128) return f(integral_constant<int, 128>(), integral_constant<int, 16>());
-  if (s.G == 256) return f(integral_constant<int, 256>(), integral_constant<int, 16>());
-  if (s.G == 512) return f(integral_constant<int, 512>(), integral_constant<int, 16>());
+#define NORM_SHAPE(g, c) if (is(g, c)) return f(integral_constant<int, g>(), integral_constant<int, c>());
+  NORM_SHAPE(8, 8) NORM_SHAPE(16, 8) NORM_SHAPE(32, 8) NORM_SHAPE(32, 16)
+  if constexpr (VEC == 8) { NORM_SHAPE(32, 24) NORM_SHAPE(32, 32) }
+  if constexpr (VEC != 8) { NORM_SHAPE(128, 8) }
+  NORM_SHAPE(128, 16) NORM_SHAPE(256, 16) NORM_SHAPE(512, 16)
+#undef NORM_SHAPE
   return f(integral_constant<int, 1024>(), integral_constant<int, 16>());
 }
 // Whether rows of D entries at these strides can be read as 16-byte vectors.

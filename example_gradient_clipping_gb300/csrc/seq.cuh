@@ -224,7 +224,8 @@ cudaError_t launch_rows_sqnorm(const float* rows, int B, size_t n, float* out, c
 cudaError_t launch_embed_lookup(const dpk::EmbedParams& P, int dtype, cudaStream_t s);
 size_t embed_order_ws_bytes(int N, int V);
 cudaError_t launch_embed_order(const dpk::EmbedParams& P, int* order, int* keys, void* ws, cudaStream_t s);
-constexpr int kEmbedUnit = 32, kEmbedSlab = 256;   // sorted rows and columns of a warp's work
+constexpr int kEmbedSlab = 256;   // columns of a warp's work
+int embed_unit(int N, int D);     // and its sorted rows
 cudaError_t launch_embed_sqnorms(const dpk::EmbedParams& P, int dtype, float* sqnorms, cudaStream_t s);
 cudaError_t launch_embed_grad(const dpk::EmbedParams& P, int dtype, int out_dtype, cudaStream_t s);
 }  // namespace dph

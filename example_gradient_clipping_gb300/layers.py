@@ -213,27 +213,34 @@ def _norm_desc(x, weight, bias, eps, dy, mean, rstd, has_bias, per_example):
     return d
 
 
+def _norm(x, weight, bias, eps, stats):
+    if _forward_ad._current_level >= 0:
+        _no_tangents(x, weight, bias)
+    eps, shape = float(eps), x.shape
+    if len(shape) != 3:
+        x = _rows3(x, "x")
+    dev, dtype = x.get_device(), x.dtype
+    key = ("layer_norm", x.shape, x.stride(), dtype, dev, _opt(weight), _opt(bias), eps)
+    d = _get(key) or _keep(key, _norm_desc(x, weight, bias, eps, None, None, None, False, False))
+    device = x.device
+    y = _empty(shape, dtype=dtype, device=device)
+    mean = rstd = None
+    if stats:
+        mean, rstd = _empty(shape[:-1], dtype=_f32, device=device), _empty(shape[:-1], dtype=_f32, device=device)
+    if d.B * d.T:
+        _call(_seq._lib.dp_layer_norm, dev, d, x.data_ptr(), None if weight is None else weight.data_ptr(),
+              None if bias is None else bias.data_ptr(), y.data_ptr(), None if mean is None else mean.data_ptr(),
+              None if rstd is None else rstd.data_ptr())
+    return y, mean, rstd
+
+
 def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, stream=None):
     """(y, mean, rstd): layer norm over the last dimension of x [B, ..., D], with each row's mean and
     1/sqrt(var + eps), fp32 [B, ...].  weight and bias: [D] of one type (bf16 or fp32), or None."""
     if stream is not None:
         with _on(stream, x.device):
-            return layer_norm_forward(x, weight, bias, eps)
-    if _forward_ad._current_level >= 0:
-        _no_tangents(x, weight, bias)
-    eps, shape = float(eps), x.shape
-    if x.dim() != 3:
-        x = _rows3(x, "x")
-    dev = x.get_device()
-    key = ("layer_norm", x.shape, x.stride(), x.dtype, dev, _opt(weight), _opt(bias), eps)
-    d = _get(key) or _keep(key, _norm_desc(x, weight, bias, eps, None, None, None, False, False))
-    device = x.device
-    y = _empty(shape, dtype=x.dtype, device=device)
-    mean, rstd = _empty(shape[:-1], dtype=_f32, device=device), _empty(shape[:-1], dtype=_f32, device=device)
-    if d.B * d.T:
-        _call(_seq._lib.dp_layer_norm, dev, d, x.data_ptr(), None if weight is None else weight.data_ptr(),
-              None if bias is None else bias.data_ptr(), y.data_ptr(), mean.data_ptr(), rstd.data_ptr())
-    return y, mean, rstd
+            return _norm(x, weight, bias, eps, True)
+    return _norm(x, weight, bias, eps, True)
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, per_example: bool = False, dx: bool = True,
@@ -258,11 +265,10 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, per_exampl
     device, D = x.device, d.D
     gx = _empty(shape, dtype=x.dtype, device=device) if dx else None
     grads = None
-    n = 2 * D if bias else D
     if params and per_example:
-        grads = _empty((d.B, n), dtype=_f32, device=device)
+        grads = _empty((d.B, 2 * D if bias else D), dtype=_f32, device=device)
     elif params:
-        grads = _empty(n, dtype=_f32 if weight is None else weight.dtype, device=device)
+        grads = _empty((2 if bias else 1, D), dtype=_f32 if weight is None else weight.dtype, device=device)
     if not d.B * d.T:
         if params:
             grads.zero_()
@@ -276,7 +282,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, per_exampl
         return gx, grads
     if not params:
         return gx, None, None
-    return gx, grads[:D], grads[D:] if bias else None
+    return (gx, *grads.unbind(0)) if bias else (gx, grads[0], None)
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -308,11 +314,15 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stream=None):
 
 
 def _layer_norm(x, weight, bias, eps, sink, stream=None):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
+    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad) or
+                                    (bias is not None and bias.requires_grad)):
         if stream is not None:
             raise ValueError("a differentiable call runs on the current stream")
         return _LayerNorm.apply(x, weight, bias, float(eps), sink)
-    return layer_norm_forward(x, weight, bias, eps, stream)[0]
+    if stream is not None:
+        with _on(stream, x.device):
+            return _norm(x, weight, bias, eps, False)[0]
+    return _norm(x, weight, bias, eps, False)[0]
 
 
 # ---- embedding ------------------------------------------------------------------------

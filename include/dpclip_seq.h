@@ -164,7 +164,7 @@ typedef struct {
   int B, T, V, K;          /* K <= 128 and <= V; 0: no alternatives */
   int token_i64;           /* 1: tokens are 64-bit integers */
   long long ld, ld_grad;   /* elements between rows of logits and of dlogits, >= V */
-  float tau;               /* > 0 */
+  float tau;               /* from 1e-6 to 1e6 */
 } dp_logprobs_desc;
 
 /* logprobs, entropy (device fp32 [B, T]) and stats (fp32 [B, T, 2]: m, ls) of logits [B*T rows, V];
