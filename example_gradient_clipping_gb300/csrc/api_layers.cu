@@ -78,7 +78,7 @@ dp_status embed_params(const dp_embedding_desc* d, dpk::EmbedParams* P) {
   P->B = d->B; P->T = d->T; P->V = d->V; P->D = d->D; P->N = d->B * d->T;
   P->i64 = d->index_i64 ? 1 : 0; P->padding = d->padding < 0 ? -1 : d->padding; P->scale = d->scale;
   P->ld = d->ld; P->dy = d->dy;
-  const int unit = dph::embed_unit(P->N, P->D);
+  const int unit = dph::embed_unit(P->N);
   P->units = (P->N + unit - 1) / unit;
   P->slabs = (P->D + dph::kEmbedSlab - 1) / dph::kEmbedSlab;
   if (((double)P->units * P->slabs + P->V / 32.0 + 2) / 8 > kMaxBlocks)
@@ -91,7 +91,7 @@ size_t embed_keys_at(const dpk::EmbedParams& P) { return up16((size_t)P.N * size
 size_t embed_partial_bytes(const dpk::EmbedParams& P) { return up16((size_t)P.units * 2 * P.D * sizeof(float)); }
 size_t embed_ws(const dpk::EmbedParams& P) {
   return std::max(dph::embed_order_ws_bytes(P.N, P.V),
-                  embed_partial_bytes(P) + up16((size_t)P.slabs * P.N * sizeof(float)));
+                  embed_partial_bytes(P) + up16((size_t)P.N * sizeof(float)));
 }
 dp_status workspace_ok(const void* ws, size_t have, size_t need) {
   if (need && (!ws || have < need))

@@ -239,8 +239,13 @@ __global__ void __launch_bounds__(1024) embed_scan_kernel(const unsigned* __rest
   const unsigned* list = sums ? sums : hist;
   const int len = sums ? (int)blockIdx.x : i0;
   unsigned s = 0;
+  const uint4* four = reinterpret_cast<const uint4*>(list);   // (both lists on 16 bytes)
 #pragma unroll 8
-  for (int k = threadIdx.x; k < len; k += 1024) s += list[k];
+  for (int k = threadIdx.x; k < len / 4; k += 1024) {
+    const uint4 c = four[k];
+    s += c.x + c.y + c.z + c.w;
+  }
+  if ((int)threadIdx.x < len % 4) s += list[len / 4 * 4 + threadIdx.x];
   s = __reduce_add_sync(kAll, s);
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = s;
   __syncthreads();

@@ -4,10 +4,13 @@
 //   sqnorm_i = scale^2 sum_v |sum over example i's r with token_r = v of dy_r|^2
 //
 // A run is a range of equal sorted tokens (norms: of one example); its rows of dy are gathered and added in
-// order, so there are no atomics on data and the result has one order.  A warp takes a unit of U sorted rows
-// and 256 columns: the runs that start there, followed past the unit's end where they go on.  A run that
-// covers a whole unit is too long for that: its units' sums go to partial rows and embed_join_kernel adds
-// them.  The norms and the sums read dy once each; the sum also writes the zero rows of dw.  Bound by HBM.
+// order, so there are no atomics on data and the result has one order.  A warp takes a unit of U sorted rows:
+// the runs that start there, followed past the unit's end where they go on.  It first lists its rows (where
+// each lies, its factor, what ends with it) in shared memory, then streams them, up to 1024 columns a pass:
+// each lane copies its own 16-byte pieces of the next rows into a ring in shared memory and reads only what it
+// copied.  A run that covers a whole unit is too long for one warp: its units' sums go to partial rows and
+// embed_join_kernel adds them.  The norms and the sums read dy once each; the sum also writes the zero rows
+// of dw.  Bound by HBM.
 #include <algorithm>
 
 #include "seq.cuh"
@@ -15,7 +18,7 @@
 namespace dpk {
 namespace embed {
 
-constexpr int SLAB = dph::kEmbedSlab;
+constexpr int SLAB = dph::kEmbedSlab, kTokens = 8;   // tokens of a warp that writes zero rows
 constexpr unsigned kAll = 0xffffffffu;
 
 // A lane's eight columns of a slab that begins at c0: chunks of PV neighbours, 32 PV apart.
@@ -83,26 +86,70 @@ template <bool kNorm> __device__ __forceinline__ bool same_run(const Place& a, c
   return a.key == b.key && (!kNorm || a.ex == b.ex);
 }
 
+// The first sorted place in [lo, hi) that does not stand before (key, ex), by the whole warp, 32 places a step
+// (sums: ex is not looked at).
+template <bool kNorm> __device__ __forceinline__ int lower_bound(const EmbedParams& P, int lo, int hi, int key, int ex) {
+  const int lane = threadIdx.x % 32;
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;   // step >= 1: some of the lanes may be past the end
+    bool before = false;
+    if (at < hi) {
+      const int k = P.keys[at];
+      before = k < key;
+      if (kNorm && k == key) before = (int)((unsigned)P.order[at] / (unsigned)P.T) < ex;
+    }
+    const int n = __popc(__ballot_sync(kAll, before));   // the lanes before it come first
+    if (n == 0) return lo;
+    const int from = lo + (n - 1) * step + 1;
+    hi = min(hi, lo + n * step);
+    lo = from;
+  }
+  return lo;
+}
+
+// A row of a unit's list: where it lies in dY, its factor, and what ends with it: a run (its token; norms: the
+// place where it starts) or this warp's part of one.
+enum { kGoesOn = 0, kRun = 1, kHead = 2, kTail = 3 };
+struct alignas(16) Entry {
+  unsigned long long at;
+  float factor;
+  unsigned end;   // one of the four, and token or place times 4
+};
+
+// Ring of S rows of NS slabs: bytes of a warp.
+constexpr int ring_rows(int es, int NS) { return 6 * 1024 / (NS * SLAB * es) < 3 ? 3 : 6 * 1024 / (NS * SLAB * es); }
+template <class E, int PV, int NS> constexpr int ring_bytes() {
+  return PV * sizeof(E) == 16 ? ring_rows(sizeof(E), NS) * NS * SLAB * (int)sizeof(E) : 0;
+}
+template <class E, int PV, int NS, bool kNorm> constexpr int warp_bytes() {
+  return 64 * (int)sizeof(Entry) + ring_bytes<E, PV, NS>() + (kNorm ? 32 * 33 * 4 : 0);
+}
+
 // Norms (kNorm): each run's squared norm to run_sq at the position of its first row, 0 at every other.
 // Sums: each run's row of dw.
-template <class E, class O, int PV, int U, bool kNorm>
-__global__ void __launch_bounds__(256, 3) embed_runs_kernel(EmbedParams P) {
+template <class E, class O, int PV, int NS, bool kNorm>
+__global__ void __launch_bounds__(256) embed_runs_kernel(EmbedParams P, int U) {
   pdl_wait();
   const int lane = threadIdx.x % 32;
   const long long gw = (long long)blockIdx.x * 8 + threadIdx.x / 32;
-  const long long work = (long long)P.units * P.slabs;
+  const long long work = P.units;
   if (gw >= work) {
-    if constexpr (!kNorm) {   // 32 tokens a warp: those without a row get zeros
-      const long long v0 = (gw - work) * 32;
-      if (v0 >= P.V || P.accumulate) return;
-      const int v = (int)min((long long)P.V, v0 + lane);
-      int lo = 0, hi = P.N;
-      while (lo < hi) {
-        const int mid = (int)(((unsigned)lo + (unsigned)hi) / 2);
-        if (P.keys[mid] < v) lo = mid + 1;
-        else hi = mid;
+    if constexpr (!kNorm) {   // kTokens tokens a warp: those without a row get zeros
+      const long long first = (gw - work) * kTokens;
+      if (first >= P.V || P.accumulate) return;
+      const int v0 = (int)first, v1 = min(P.V, v0 + kTokens), j0 = lower_bound<false>(P, 0, P.N, v0, 0);
+      unsigned there = 0;
+      for (int j = j0, rounds = 0;; j += 32) {
+        const int k = j + lane < P.N ? P.keys[j + lane] : P.V;
+        there |= __reduce_or_sync(kAll, k < v1 ? 1u << (k - v0) : 0);
+        const int last = __shfl_sync(kAll, k, 31);
+        if (last >= v1) break;
+        if (++rounds == 4) {   // a long run: past its end
+          j = lower_bound<false>(P, j + 32, P.N, last + 1, 0) - 32;
+          rounds = 0;
+        }
       }
-      unsigned absent = __ballot_sync(kAll, v < P.V && (lo == P.N || P.keys[lo] != v));
+      unsigned absent = ~there & ((1u << (v1 - v0)) - 1);
       constexpr int W = PV * sizeof(O) > 16 ? 16 / sizeof(O) : PV;
       float none[W];
 #pragma unroll
@@ -110,18 +157,24 @@ __global__ void __launch_bounds__(256, 3) embed_runs_kernel(EmbedParams P) {
       Pack<O, W> zero;
       zero.set(none);
       while (absent) {
-        const int b = __ffs(absent) - 1;
+        const int t = __ffs(absent) - 1;
         absent &= absent - 1;
-        O* dst = static_cast<O*>(P.dW) + (size_t)(v0 + b) * P.D;
+        O* dst = static_cast<O*>(P.dW) + (size_t)(v0 + t) * P.D;
 #pragma unroll 4
         for (int c = lane * W; c < P.D; c += 32 * W) *reinterpret_cast<Pack<O, W>*>(dst + c) = zero;
       }
     }
     return;
   }
-  constexpr unsigned kUnit = U == 32 ? kAll : (1u << U) - 1;
-  const int u = (int)(gw / P.slabs), slab = (int)(gw - (long long)u * P.slabs), c0 = slab * SLAB;
-  const bool holds = U == 32 || lane < U;
+  extern __shared__ uint4 dyn[];
+  unsigned char* mine = reinterpret_cast<unsigned char*>(dyn) + threadIdx.x / 32 * warp_bytes<E, PV, NS, kNorm>();
+  Entry* list = reinterpret_cast<Entry*>(mine);
+  E* ring = reinterpret_cast<E*>(mine + 64 * sizeof(Entry));
+  float* sq = reinterpret_cast<float*>(mine + 64 * sizeof(Entry) + ring_bytes<E, PV, NS>());   // [place][33], norms
+  // ---- the list
+  const unsigned unit_mask = U == 32 ? kAll : (1u << U) - 1;
+  const int u = (int)gw;
+  const bool holds = lane < U;
   const Place own = place(P, holds ? u * U + lane : -1), nxt = place(P, holds ? (u + 1) * U + lane : -1);
   const Place before = place(P, u * U - 1), unit_before = place(P, (u - 1) * U);
   const Place last = {__shfl_sync(kAll, own.key, U - 1), 0, __shfl_sync(kAll, own.ex, U - 1)};
@@ -129,11 +182,11 @@ __global__ void __launch_bounds__(256, 3) embed_runs_kernel(EmbedParams P) {
   Place left = {__shfl_up_sync(kAll, own.key, 1), 0, __shfl_up_sync(kAll, own.ex, 1)};
   if (lane == 0) left = before;
   const int n = __popc(__ballot_sync(kAll, own.key < P.V));
-  const unsigned starts = __ballot_sync(kAll, (u == 0 && lane == 0) || !same_run<kNorm>(own, left)) & kUnit;
+  const unsigned starts = __ballot_sync(kAll, (u == 0 && lane == 0) || !same_run<kNorm>(own, left)) & unit_mask;
   left = {__shfl_up_sync(kAll, nxt.key, 1), 0, __shfl_up_sync(kAll, nxt.ex, 1)};
   if (lane == 0) left = last;
   const int n2 = __popc(__ballot_sync(kAll, nxt.key < P.V));
-  const unsigned starts2 = __ballot_sync(kAll, !same_run<kNorm>(nxt, left)) & kUnit;
+  const unsigned starts2 = __ballot_sync(kAll, !same_run<kNorm>(nxt, left)) & unit_mask;
   const bool full = n == U && !(starts & ~1u);
   const bool goes_on = n == U && n2 > 0 && !(starts2 & 1);          // the last run, into the next unit
   const bool next_full = goes_on && n2 == U && !(starts2 & ~1u);
@@ -143,64 +196,137 @@ __global__ void __launch_bounds__(256, 3) embed_runs_kernel(EmbedParams P) {
   const bool head_own = head > 0 && u > 0 && same_run<kNorm>(unit_before, before);
   const int a = full || head_own ? 0 : head, b = n + (goes_on && !full && !next_full ? head2 : 0);
   const unsigned long long marks = (unsigned long long)starts2 << U | starts;
-  float sq = 0.f;   // of the run that starts at this lane
-  float acc[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-  const E* dY = static_cast<const E*>(P.dY);
-  const float own_f = !kNorm && P.factors && own.key < P.V ? P.factors[own.ex] : 1.f;
-  const float nxt_f = !kNorm && P.factors && nxt.key < P.V ? P.factors[nxt.ex] : 1.f;
-  int run = a;      // the current run's first row here
-  constexpr int kFly = sizeof(E) == 2 && PV > 1 ? 8 : 4;   // rows whose loads are in flight
-  for (int i = a; i < b; i += kFly) {
-    RowLoad<E, PV> row[kFly];
-#pragma unroll
-    for (int f = 0; f < kFly; ++f) {
-      const int at = i + f, pos = __shfl_sync(kAll, at < U ? own.pos : nxt.pos, at & (U - 1));
-      const int ex = __shfl_sync(kAll, at < U ? own.ex : nxt.ex, at & (U - 1));
-      if (at < b) row[f].load(dY + (size_t)ex * P.dy.b + (size_t)(pos - ex * P.T) * P.dy.t, lane, c0, P.D);
+  auto enter = [&](const Place& q, int i) {   // row i of the unit and its successor
+    if (i < a || i >= b) return;
+    Entry e;
+    e.at = (unsigned long long)q.ex * P.dy.b + (unsigned long long)(q.pos - q.ex * P.T) * P.dy.t;
+    e.factor = !kNorm && P.factors ? P.factors[q.ex] : 1.f;
+    e.end = kGoesOn;
+    if (i + 1 == b || (marks >> (i + 1) & 1)) {
+      const int start = 63 - __clzll(marks & (2ull << i) - 1);   // (a head has none)
+      e.end = full || i < head ? kHead : i == U - 1 && next_full ? kTail : kRun | (unsigned)(kNorm ? start : q.key) << 2;
     }
+    list[i - a] = e;
+  };
+  if (holds) {
+    enter(own, lane);
+    enter(nxt, U + lane);
+  }
+  if (kNorm) {
 #pragma unroll
-    for (int f = 0; f < kFly; ++f) {
-      const int at = i + f;
-      const float w = __shfl_sync(kAll, at < U ? own_f : nxt_f, at & (U - 1));
-      if (at >= b) break;
+    for (int i = 0; i < 33; ++i) sq[i * 32 + lane] = 0.f;
+  }
+  __syncwarp();
+  // ---- the rows
+  const int rows = max(0, b - a);
+  const E* dY = static_cast<const E*>(P.dY);
+  for (int c0 = 0; c0 < P.D; c0 += NS * SLAB) {
+    float acc[NS][8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = kNorm ? acc[k] + row[f].get(k) : fmaf(w, row[f].get(k), acc[k]);
-      if (at + 1 < b && !(marks >> (at + 1) & 1)) continue;
-      // the run ends, or what this warp has of it
-      const bool is_head = at < head && !full;
-      if (full || is_head) put_cols<float, PV>(P.partial + (size_t)u * 2 * P.D, acc, lane, c0, P.D);
-      else if (at == U - 1 && next_full) put_cols<float, PV>(P.partial + ((size_t)u * 2 + 1) * P.D, acc, lane, c0, P.D);
-      else if (kNorm) {
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[s][k] = 0.f;
+    auto add = [&](const RowLoad<E, PV> (&row)[NS], const Entry& e) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[s][k] = kNorm ? acc[s][k] + row[s].get(k) : fmaf(e.factor, row[s].get(k), acc[s][k]);
+      if (e.end == kGoesOn) return;
+      const unsigned kind = e.end & 3;
+      if (kind != kRun) {
+        float* dst = P.partial + ((size_t)u * 2 + (kind == kTail)) * P.D;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) put_cols<float, PV>(dst, acc[s], lane, c0 + s * SLAB, P.D);
+      } else if (kNorm) {
         float q = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (col_of<PV>(lane, c0, k) < P.D) q = fmaf(acc[k], acc[k], q);
-        q = warp_sum(q);
-        if (lane == run) sq = q;
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (col_of<PV>(lane, c0 + s * SLAB, k) < P.D) q = fmaf(acc[s][k], acc[s][k], q);
+        sq[(e.end >> 2) * 33 + lane] += q;   // (its own place: the sum over the lanes comes last)
       } else {
-        put_row<O, PV>(P, __shfl_sync(kAll, own.key, run), acc, lane, c0);
+#pragma unroll
+        for (int s = 0; s < NS; ++s) put_row<O, PV>(P, (int)(e.end >> 2), acc[s], lane, c0 + s * SLAB);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-      run = at + 1;
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[s][k] = 0.f;
+    };
+    if constexpr (PV * sizeof(E) == 16) {
+      constexpr int S = ring_rows(sizeof(E), NS), kPieces = 8 / PV;
+      auto piece = [&](int stage, int s, int i) { return ring + ((stage * NS + s) * kPieces + i) * 32 * PV + lane * PV; };
+      auto copy = [&](int stage, int i) {
+        if (i < rows) {
+          const E* row = dY + list[i].at;
+#pragma unroll
+          for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+              const int c = chunk_of<PV>(lane, c0 + s * SLAB, k);
+              if (c < P.D)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(piece(stage, s, k))),
+                             "l"(row + c) : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll
+      for (int i = 0; i < S - 1; ++i) copy(i, i);
+      int stage = 0;
+      for (int i = 0; i < rows; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+        RowLoad<E, PV> row[NS];
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int k = 0; k < kPieces; ++k) row[s].p[k] = *reinterpret_cast<const Pack<E, PV>*>(piece(stage, s, k));
+        copy(stage == 0 ? S - 1 : stage - 1, i + S - 1);   // the slot that the last row left
+        add(row, list[i]);
+        stage = stage + 1 == S ? 0 : stage + 1;
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    } else {
+      constexpr int kFly = 4;   // rows whose loads are in flight
+      for (int i = 0; i < rows; i += kFly) {
+        RowLoad<E, PV> row[kFly][NS];
+#pragma unroll
+        for (int f = 0; f < kFly; ++f)
+          if (i + f < rows) {
+#pragma unroll
+            for (int s = 0; s < NS; ++s) row[f][s].load(dY + list[i + f].at, lane, c0 + s * SLAB, P.D);
+          }
+#pragma unroll
+        for (int f = 0; f < kFly; ++f)
+          if (i + f < rows) add(row[f], list[i + f]);
+      }
     }
   }
   pdl_trigger();
-  if (kNorm && holds && u * U + lane < P.N) P.run_sq[(size_t)slab * P.N + own.pos] = sq;
+  if constexpr (kNorm) {
+    __syncwarp();
+    if (holds && u * U + lane < P.N) {
+      float t = 0.f;
+#pragma unroll 8
+      for (int l = 0; l < 32; ++l) t += sq[lane * 33 + l];
+      P.run_sq[own.pos] = t;
+    }
+  }
 }
 
 // Runs that cover whole units: their partial rows added in order, by a warp, or (many of them) in eight
 // consecutive shares by the warps of the CTA and then in order.
-template <class O, int PV, int U, bool kNorm>
-__global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P) {
+template <class O, int PV, bool kNorm>
+__global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P, int U, int per) {
   pdl_wait();
   __shared__ float share[8][SLAB];
   __shared__ float red[8];
-  __shared__ int many[32], count;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, slab = blockIdx.y, c0 = slab * SLAB;
-  const int u0 = blockIdx.x * 32;
+  __shared__ int many[32], rows[32], count;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int u0 = blockIdx.x * per;   // per units a CTA
+  // sums: a slab a CTA; norms: all of them
+  const int first_slab = kNorm ? 0 : blockIdx.y, slabs = kNorm ? P.slabs : first_slab + 1;
   if (threadIdx.x == 0) count = 0;
   auto covered = [&](int u, Place* first) {   // whether one run covers unit u, and its first place
     *first = place(P, u * U);
@@ -211,46 +337,54 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P) {
   bool begins = false;   // a long run's first rows are in unit u
   Place mine = {P.V, 0, 0};
   int from_tail = 0;
-  if (u < P.units) {
-    if (covered(u, &mine)) {
-      begins = u == 0 || !same_run<kNorm>(place(P, u * U - 1), mine);
-    } else if (u + 1 < P.units && covered(u + 1, &mine)) {
-      begins = same_run<kNorm>(place(P, u * U + U - 1), mine);
+  if (lane < per && u < P.units) {
+    Place next;
+    const Place before = place(P, u * U - 1), end = place(P, u * U + U - 1);
+    const bool own = covered(u, &mine), behind = covered(u + 1, &next);
+    if (own) {
+      begins = u == 0 || !same_run<kNorm>(before, mine);
+    } else if (behind) {
+      begins = same_run<kNorm>(end, next);
       from_tail = 1;
+      mine = next;
     }
   }
   const unsigned todo = __ballot_sync(kAll, begins);
   // the run that begins in unit u0 + b: its partial rows are the first (of the unit's tail or the whole unit)
-  // and those of the L - 1 units behind it
+  // and those of every unit behind it that it reaches
   auto length = [&](int b, const Place& run) {
-    int m = 0;
-    for (;;) {
-      Place f;
-      const int v = u0 + b + 1 + m + lane;
-      const bool c = v < P.units && covered(v, &f) && same_run<kNorm>(f, run);
-      const unsigned mask = __ballot_sync(kAll, c);
-      const int add = mask == kAll ? 32 : __ffs(~mask) - 1;
-      m += add;
-      if (add < 32) break;
+    const int from = u0 + b + 1, v = from + lane;
+    Place f;
+    const unsigned mask = __ballot_sync(kAll, v < P.units && covered(v, &f) && same_run<kNorm>(f, run));
+    if (mask != kAll) {   // it ends in the first unit that it does not cover, or before it
+      const int m = __ffs(~mask) - 1, next = from + m;
+      return 1 + m + (next < P.units && same_run<kNorm>(place(P, next * U), run) ? 1 : 0);
     }
-    const int next = u0 + b + 1 + m;
-    return 1 + m + (next < P.units && same_run<kNorm>(place(P, next * U), run) ? 1 : 0);
+    const int end = lower_bound<kNorm>(P, (from + 32) * U, P.N, kNorm ? run.key : run.key + 1, run.ex + 1);
+    return (end - 1) / U - (u0 + b) + 1;
   };
-  auto add_rows = [&](float (&acc)[8], int b, int tail, int l0, int l1) {
+  auto add_rows = [&](float (&acc)[8], int b, int tail, int l0, int l1, int c0) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-#pragma unroll 4
-    for (int l = l0; l < l1; ++l) {
-      RowLoad<float, PV> row;
-      row.load(P.partial + ((size_t)(u0 + b + l) * 2 + (l == 0 ? tail : 0)) * P.D, lane, c0, P.D);
+    constexpr int kFly = PV > 1 ? 6 : 3;   // rows whose loads are in flight
+    for (int l = l0; l < l1; l += kFly) {
+      RowLoad<float, PV> row[kFly];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] += row.get(k);
+      for (int f = 0; f < kFly; ++f)
+        if (l + f < l1) row[f].load(P.partial + ((size_t)(u0 + b + l + f) * 2 + (l + f == 0 ? tail : 0)) * P.D, lane, c0, P.D);
+#pragma unroll
+      for (int f = 0; f < kFly; ++f)
+        if (l + f < l1) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (col_of<PV>(lane, c0, k) < P.D) acc[k] += row[f].get(k);
+        }
     }
   };
   auto first_position = [&](int b, int tail, const Place& run) {   // of the run
     const int ub = u0 + b;
     if (!tail) return P.order[ub * U];
-    const Place q = place(P, U == 32 || lane < U ? ub * U + lane : -1);
+    const Place q = place(P, lane < U ? ub * U + lane : -1);
     return __shfl_sync(kAll, q.pos, __ffs(__ballot_sync(kAll, same_run<kNorm>(q, run))) - 1);
   };
   __syncthreads();
@@ -261,72 +395,82 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P) {
     const Place run = {__shfl_sync(kAll, mine.key, b), 0, __shfl_sync(kAll, mine.ex, b)};
     const int L = length(b, run);
     if (L > 32) {   // for the whole CTA
-      if (lane == 0) many[atomicAdd(&count, 1)] = b;
+      if (lane == 0) {
+        const int i = atomicAdd(&count, 1);
+        many[i] = b;
+        rows[i] = L;
+      }
       continue;
     }
-    float acc[8];
-    add_rows(acc, b, tail, 0, L);
-    if (kNorm) {
-      float q = 0.f;
+    float q = 0.f;
+    for (int slab = first_slab; slab < slabs; ++slab) {
+      float acc[8];
+      add_rows(acc, b, tail, 0, L, slab * SLAB);
+      if (kNorm) {   // (columns past D are 0)
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (col_of<PV>(lane, c0, k) < P.D) q = fmaf(acc[k], acc[k], q);
+        for (int k = 0; k < 8; ++k) q = fmaf(acc[k], acc[k], q);
+      } else {
+        put_row<O, PV>(P, run.key, acc, lane, slab * SLAB);
+      }
+    }
+    if (kNorm) {
       q = warp_sum(q);
       const int pos = first_position(b, tail, run);
-      if (lane == 0) P.run_sq[(size_t)slab * P.N + pos] = q;
-    } else {
-      put_row<O, PV>(P, run.key, acc, lane, c0);
+      if (lane == 0) P.run_sq[pos] = q;
     }
   }
   __syncthreads();
   for (int i = 0; i < count; ++i) {   // (their order in the list does not matter)
     const int b = many[i], tail = __shfl_sync(kAll, from_tail, b);
     const Place run = {__shfl_sync(kAll, mine.key, b), 0, __shfl_sync(kAll, mine.ex, b)};
-    const int L = length(b, run);
-    float acc[8];
-    add_rows(acc, b, tail, (int)((long long)L * warp / 8), (int)((long long)L * (warp + 1) / 8));
+    const int L = rows[i];
+    float total = 0.f;
+    for (int slab = first_slab; slab < slabs; ++slab) {
+      float acc[8];
+      add_rows(acc, b, tail, (int)((long long)L * warp / 8), (int)((long long)L * (warp + 1) / 8), slab * SLAB);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) share[warp][col_of<PV>(lane, 0, k)] = acc[k];
-    __syncthreads();
-    const int c = c0 + (int)threadIdx.x;
-    float s = 0.f;
-    if (c < P.D) {
+      for (int k = 0; k < 8; ++k) share[warp][col_of<PV>(lane, 0, k)] = acc[k];
+      __syncthreads();
+      const int c = slab * SLAB + (int)threadIdx.x;
+      float s = 0.f;
 #pragma unroll
       for (int w = 0; w < 8; ++w) s += share[w][threadIdx.x];
+      if (kNorm) {
+        total = fmaf(s, s, total);
+      } else if (c < P.D) {
+        O* dst = static_cast<O*>(P.dW) + (size_t)run.key * P.D + c;
+        s *= P.scale;
+        if (P.accumulate) s += to_f(*dst);
+        *dst = from_f(s, O());
+      }
+      __syncthreads();
     }
     if (kNorm) {
-      const float q = warp_sum(s * s);
-      if (lane == 0) red[warp] = q;
+      total = warp_sum(total);
+      if (lane == 0) red[warp] = total;
       const int pos = first_position(b, tail, run);
       __syncthreads();
       if (threadIdx.x == 0) {
         float t = 0.f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) t += red[w];
-        P.run_sq[(size_t)slab * P.N + pos] = t;
+        P.run_sq[pos] = t;
       }
-    } else if (c < P.D) {
-      O* dst = static_cast<O*>(P.dW) + (size_t)run.key * P.D + c;
-      s *= P.scale;
-      if (P.accumulate) s += to_f(*dst);
-      *dst = from_f(s, O());
+      __syncthreads();
     }
-    __syncthreads();
   }
   pdl_trigger();
 }
 
-// sqnorms[i] = scale^2 times the sum of example i's runs, slab by slab.
+// sqnorms[i] = scale^2 times the sum of example i's runs.
 __global__ void __launch_bounds__(1024) embed_sqnorm_kernel(EmbedParams P, float* __restrict__ out) {
   pdl_wait();
   __shared__ float red[32];
   const int i = blockIdx.x;
   float acc = 0.f;
-  for (int s = 0; s < P.slabs; ++s) {
-    const float* q = P.run_sq + (size_t)s * P.N + (size_t)i * P.T;
+  const float* q = P.run_sq + (size_t)i * P.T;
 #pragma unroll 4
-    for (int t = threadIdx.x; t < P.T; t += blockDim.x) acc += q[t];
-  }
+  for (int t = threadIdx.x; t < P.T; t += blockDim.x) acc += q[t];
   acc = warp_sum(acc);
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = acc;
   __syncthreads();
@@ -344,20 +488,25 @@ namespace dph {
 using namespace dpk;
 using namespace dpk::embed;
 
-// Rows of a unit: 32, or 8 where that would leave an SM less than 16 warps, whose rows follow one another.
-int embed_unit(int N, int D) {
-  const long long warps = ((long long)N + 31) / 32 * ((D + kEmbedSlab - 1) / kEmbedSlab);
-  return warps >= 152 * 16 ? 32 : 8;
-}
+// Rows of a unit: 32, or fewer where that would leave an SM less than 16 warps, whose rows follow one another.
+int embed_unit(int N) { return N >= 152 * 16 * 32 ? 32 : N >= 152 * 16 * 16 ? 16 : 8; }
 
-template <class E, class O, int PV, int U, bool kNorm>
+template <class E, class O, int PV, int NS, bool kNorm>
 static cudaError_t run_runs(const EmbedParams& P, cudaStream_t s) {
-  const long long zero = kNorm || P.accumulate ? 0 : ((long long)P.V + 31) / 32;
-  const long long warps = (long long)P.units * P.slabs + zero;
-  cudaError_t e = launch_operator(embed_runs_kernel<E, O, PV, U, kNorm>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, P);
-  if (e == cudaSuccess && P.N >= U)   // shorter: no unit that a run could cover
-    e = launch_operator(embed_join_kernel<O, (PV > 4 ? 4 : PV), U, kNorm>, dim3((unsigned)((P.units + 31) / 32), (unsigned)P.slabs),
-                        dim3(256), 0, s, P);
+  const int U = embed_unit(P.N);
+  constexpr int smem = 8 * warp_bytes<E, PV, NS, kNorm>();
+  if (smem > 40 * 1024) {
+    const cudaError_t e = allow_smem<embed_runs_kernel<E, O, PV, NS, kNorm>>(smem);
+    if (e != cudaSuccess) return e;
+  }
+  const long long zero = kNorm || P.accumulate ? 0 : ((long long)P.V + kTokens - 1) / kTokens;
+  const long long warps = P.units + zero;
+  cudaError_t e = launch_operator(embed_runs_kernel<E, O, PV, NS, kNorm>, dim3((unsigned)((warps + 7) / 8)), dim3(256), smem, s, P, U);
+  if (e == cudaSuccess && P.N >= U) {   // shorter: no unit that a run could cover
+    const int per = (long long)P.units * P.slabs <= 152 * 8 * 8 ? 8 : 32;   // a warp's runs follow one another
+    e = launch_operator(embed_join_kernel<O, (PV > 4 ? 4 : PV), kNorm>,
+                        dim3((unsigned)((P.units + per - 1) / per), kNorm ? 1u : (unsigned)P.slabs), dim3(256), 0, s, P, U, per);
+  }
   return e;
 }
 
@@ -370,10 +519,13 @@ static cudaError_t runs_vec(const EmbedParams& P, cudaStream_t s) {
     return P.D % vec == 0 && on(P.dY, vec * sizeof(E)) && on(P.dW, std::min<size_t>(16, vec * sizeof(O))) &&
            (P.B == 1 || P.dy.b % vec == 0) && (P.T == 1 || P.dy.t % vec == 0);
   };
-  const bool wide = fits(W), two = !wide && fits(2);
-  if (embed_unit(P.N, P.D) == 32)
-    return wide ? run_runs<E, O, W, 32, kNorm>(P, s) : two ? run_runs<E, O, 2, 32, kNorm>(P, s) : run_runs<E, O, 1, 32, kNorm>(P, s);
-  return wide ? run_runs<E, O, W, 8, kNorm>(P, s) : two ? run_runs<E, O, 2, 8, kNorm>(P, s) : run_runs<E, O, 1, 8, kNorm>(P, s);
+  if (!fits(W)) return fits(2) ? run_runs<E, O, 2, 1, kNorm>(P, s) : run_runs<E, O, 1, 1, kNorm>(P, s);
+  switch (P.slabs) {   // columns a pass
+    case 1: return run_runs<E, O, W, 1, kNorm>(P, s);
+    case 2: return run_runs<E, O, W, 2, kNorm>(P, s);
+    case 3: return run_runs<E, O, W, 3, kNorm>(P, s);
+    default: return run_runs<E, O, W, 4, kNorm>(P, s);
+  }
 }
 
 cudaError_t launch_embed_sqnorms(const EmbedParams& P, int dtype, float* sqnorms, cudaStream_t s) {

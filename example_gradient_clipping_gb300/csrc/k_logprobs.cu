@@ -23,8 +23,7 @@
 namespace dpk {
 namespace logprobs {
 
-constexpr int kThreads = 256, kTop = 128;   // most alternatives
-constexpr int kRoom = 1024, kList = 512;    // candidates that are ranked, groups that are read again
+constexpr int kTop = 128;          // most alternatives
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kFloor = -150.f;   // 2^-150 is 0
 constexpr float kFar = 1e29f;      // logits times log2(e) / tau beyond it take the sums of differences to the maximum
@@ -85,9 +84,9 @@ __device__ __forceinline__ float low_of(float low, float) { return low; }
 __device__ __forceinline__ float value_of(unsigned k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
 // The row on the grid of 16-byte vectors: its first entry is entry `mis` of vector 0.  A part of it is the
-// vectors [j0, j1), which the CTA reads in rounds of kFly vectors a thread; a group is what a thread reads in
-// 2^shift consecutive rounds.
-template <class E> struct Grid {
+// vectors [j0, j1), which the CTA (NT threads) reads in rounds of kFly vectors a thread; a group is what a thread
+// reads in 2^shift consecutive rounds.
+template <class E, int NT> struct Grid {
   static constexpr int W = Vec<E>::W;
   const E* row;
   int V, mis, j0, j1;
@@ -113,11 +112,11 @@ template <class E> struct Grid {
     }
     return v;
   }
-  __device__ __forceinline__ int rounds() const { return (j1 - j0 + kThreads * kFly - 1) / (kThreads * kFly); }
-  __device__ __forceinline__ int groups(int shift) const { return ((rounds() + (1 << shift) - 1) >> shift) * kThreads; }
+  __device__ __forceinline__ int rounds() const { return (j1 - j0 + NT * kFly - 1) / (NT * kFly); }
+  __device__ __forceinline__ int groups(int shift) const { return ((rounds() + (1 << shift) - 1) >> shift) * NT; }
   // Vector i (of kFly << shift) of group q; it may lie past the part.
   __device__ __forceinline__ int vector(int q, int i, int shift) const {
-    return j0 + (((q / kThreads << shift) * kFly + i) * kThreads + q % kThreads);
+    return j0 + (((q / NT << shift) * kFly + i) * NT + q % NT);
   }
 };
 
@@ -132,38 +131,39 @@ __device__ __forceinline__ void dsmem_st(unsigned long long* p, int rank, unsign
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(ptx::map_rank(ptx::smem_u32(p), rank)), "l"(v) : "memory");
 }
 
-struct alignas(16) Shared {
-  unsigned tmax[kThreads];               // each thread's largest key, 0 without any
+template <int NT> struct alignas(16) Shared {
+  static constexpr int kWarps = NT / 32, kRoom = 4 * NT, kList = 2 * NT;   // candidates that are ranked, groups read again
+  unsigned tmax[NT];                     // each thread's largest key, 0 without any
   unsigned long long room[kRoom];        // candidates: key, then the index's complement
   unsigned long long best[kTop];         // the part's largest, in order
   unsigned short list[kList];            // groups whose maximum reaches the bound
-  float red[4][8];
+  float red[4][kWarps];
   float peer[8][4];                      // rank 0: every part's maximum and sums
   unsigned bound;
-  int count, groups, wsum[8];
+  int count, groups, wsum[kWarps];
 };
 
-__device__ __forceinline__ int block_sum(int v, Shared& sh) {
+template <int NT> __device__ __forceinline__ int block_sum(int v, Shared<NT>& sh) {
   v = __reduce_add_sync(kAll, v);
   __syncthreads();
   if (threadIdx.x % 32 == 0) sh.wsum[threadIdx.x / 32] = v;
   __syncthreads();
   int s = 0;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) s += sh.wsum[w];
+  for (int w = 0; w < NT / 32; ++w) s += sh.wsum[w];
   return s;
 }
 
 // The largest n keys of this part of the row, in order, to sh.best (n at most the part's entries).
-template <class E>
-__device__ void part_top(const Grid<E>& g, int shift, const float* gmax, int n, Shared& sh) {
-  constexpr int W = Vec<E>::W;
+template <class E, int NT>
+__device__ void part_top(const Grid<E, NT>& g, int shift, const float* gmax, int n, Shared<NT>& sh) {
+  constexpr int W = Vec<E>::W, kRoom = Shared<NT>::kRoom, kList = Shared<NT>::kList, kWarps = NT / 32;
   const int tid = threadIdx.x, lane = tid % 32, groups = g.groups(shift), size = kFly << shift;
   // a bound that n keys reach: the n-th largest of the threads' maxima, bit by bit (0 if fewer have one)
   if (tid < 32) {
-    unsigned k[kThreads / 32], lo = kAll, hi = 0;
+    unsigned k[NT / 32], lo = kAll, hi = 0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
+    for (int i = 0; i < NT / 32; ++i) {
       k[i] = sh.tmax[i * 32 + lane];
       hi = max(hi, k[i]);
       lo = min(lo, k[i]);
@@ -178,7 +178,7 @@ __device__ void part_top(const Grid<E>& g, int shift, const float* gmax, int n, 
         const unsigned trial = t | 1u << b;
         int c = 0;
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) c += k[i] >= trial;
+        for (int i = 0; i < NT / 32; ++i) c += k[i] >= trial;
         c = __reduce_add_sync(kAll, c);
         if (c >= n) t = trial;
         if (c == n) break;
@@ -209,7 +209,7 @@ __device__ void part_top(const Grid<E>& g, int shift, const float* gmax, int n, 
   // the groups first, so that their vectors are then read by all threads at once
   {
     const float low = value_of(bound);
-    for (int q = tid; q < groups; q += kThreads)
+    for (int q = tid; q < groups; q += NT)
       if (!(gmax[q] < low)) {
         const int at = atomicAdd(&sh.groups, 1);
         if (at < kList) sh.list[at] = (unsigned short)q;
@@ -220,7 +220,7 @@ __device__ void part_top(const Grid<E>& g, int shift, const float* gmax, int n, 
   if (ng <= kList) {
     const int log_size = shift + 2;
     static_assert(kFly == 4, "log_size");
-    for (int i = tid; i < ng << log_size; i += kThreads) {
+    for (int i = tid; i < ng << log_size; i += NT) {
       const int j = g.vector(sh.list[i >> log_size], i & (size - 1), shift);
       if (j < g.j1) collect(j, bound);
     }
@@ -231,7 +231,7 @@ __device__ void part_top(const Grid<E>& g, int shift, const float* gmax, int n, 
     // how many keys of the part reach `t`
     auto reach = [&](unsigned t) {
       int c = 0;
-      for (int q = tid; q < groups; q += kThreads)
+      for (int q = tid; q < groups; q += NT)
         if (key_of(gmax[q]) >= t)
           for (int i0 = 0; i0 < size; ++i0) {
             const int j = g.vector(q, i0, shift);
@@ -259,13 +259,13 @@ __device__ void part_top(const Grid<E>& g, int shift, const float* gmax, int n, 
     if (tid == 0) sh.count = 0;
     __syncthreads();
     if (bound != kAll)
-      for (int q = tid; q < groups; q += kThreads)
+      for (int q = tid; q < groups; q += NT)
         if (key_of(gmax[q]) > bound)
           for (int i = 0; i < size && g.vector(q, i, shift) < g.j1; ++i) collect(g.vector(q, i, shift), bound + 1);
     __syncthreads();
     have = sh.count;   // < n
     // its ties, lowest index first
-    for (int base = g.j0; base < g.j1 && have < n; base += kThreads) {
+    for (int base = g.j0; base < g.j1 && have < n; base += NT) {
       const int j = base + tid;
       unsigned mine = 0;
       if (j < g.j1) {
@@ -288,7 +288,7 @@ __device__ void part_top(const Grid<E>& g, int shift, const float* gmax, int n, 
       __syncthreads();
       int at = have + x - c, total = 0;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         if (w < tid / 32) at += sh.wsum[w];
         total += sh.wsum[w];
       }
@@ -301,7 +301,7 @@ __device__ void part_top(const Grid<E>& g, int shift, const float* gmax, int n, 
   // every candidate's place among them
   if (tid == 0 && (have & 1)) sh.room[have] = 0;   // (room for it: an odd count is below kRoom)
   __syncthreads();
-  for (int c = tid; c < have; c += kThreads) {
+  for (int c = tid; c < have; c += NT) {
     const unsigned long long k = sh.room[c];
     int rank = 0;
 #pragma unroll 4
@@ -315,15 +315,15 @@ __device__ void part_top(const Grid<E>& g, int shift, const float* gmax, int n, 
 }
 
 // Groups of a part of `per` vectors, at most.
-__host__ __device__ constexpr int max_groups(int per, int shift) {
-  return ((((per + kThreads * kFly - 1) / (kThreads * kFly)) + (1 << shift) - 1) >> shift) * kThreads;
+template <int NT> __host__ __device__ constexpr int max_groups(int per, int shift) {
+  return ((((per + NT * kFly - 1) / (NT * kFly)) + (1 << shift) - 1) >> shift) * NT;
 }
 
 // Sums of the part's e and e x at its maximum m by differences, for logits whose products would not be finite.
-template <class E>
-__device__ void far_sums(const Grid<E>& g, float m, float c2, float* sum, float* sumx) {
+template <class E, int NT>
+__device__ void far_sums(const Grid<E, NT>& g, float m, float c2, float* sum, float* sumx) {
   float s = 0.f, t = 0.f;
-  for (int j = g.j0 + (int)threadIdx.x; j < g.j1; j += kThreads) {
+  for (int j = g.j0 + (int)threadIdx.x; j < g.j1; j += NT) {
     const Vec<E> v = g.load(j);
 #pragma unroll
     for (int n = 0; n < Vec<E>::W; ++n) {
@@ -336,17 +336,17 @@ __device__ void far_sums(const Grid<E>& g, float m, float c2, float* sum, float*
   *sumx = t;
 }
 
-template <class E, bool kAlt>
-__global__ void __launch_bounds__(kThreads, kAlt ? 6 : 4) token_logprobs_kernel(LogprobParams P, int cluster, int per, int shift) {
+template <class E, bool kAlt, int NT>
+__global__ void __launch_bounds__(NT, (kAlt ? 6 : 4) * 256 / NT) token_logprobs_kernel(LogprobParams P, int cluster, int per, int shift) {
   pdl_wait();
   if (cluster > 1) cluster_arrive();   // that every CTA has begun, before its shared memory is written
-  constexpr int W = Vec<E>::W;
-  extern __shared__ unsigned char dyn[];
-  Shared& sh = *reinterpret_cast<Shared*>(dyn);
-  float* gmax = reinterpret_cast<float*>(dyn + sizeof(Shared));
+  constexpr int W = Vec<E>::W, kWarps = NT / 32;
+  extern __shared__ __align__(16) unsigned char dyn[];
+  Shared<NT>& sh = *reinterpret_cast<Shared<NT>*>(dyn);
+  float* gmax = reinterpret_cast<float*>(dyn + sizeof(Shared<NT>));
   const int tid = threadIdx.x, lane = tid % 32;
   const unsigned row = blockIdx.x / (unsigned)cluster, rank = blockIdx.x - row * (unsigned)cluster;
-  const Grid<E> g(static_cast<const E*>(P.logits) + (size_t)row * P.ld, P.V, (int)rank, per);
+  const Grid<E, NT> g(static_cast<const E*>(P.logits) + (size_t)row * P.ld, P.V, (int)rank, per);
   const float itau = 1.f / P.tau, c2 = kLog2e * itau, reach = 8.f / c2;
   // entries below `low` give e = 0 as they do, and a finite x
   const auto low = low_of(-10.f * kFar / c2, E());
@@ -356,18 +356,18 @@ __global__ void __launch_bounds__(kThreads, kAlt ? 6 : 4) token_logprobs_kernel(
   Vec<E> v[kFly], next[kAlt ? 1 : kFly];
   auto fetch = [&](Vec<E>* d, int j) {
 #pragma unroll
-    for (int f = 0; f < kFly; ++f) d[f] = g.load(j + f * kThreads);
+    for (int f = 0; f < kFly; ++f) d[f] = g.load(j + f * NT);
   };
   const int rounds = g.rounds();
   if (!kAlt) fetch(v, g.j0 + tid);
 #pragma unroll (kAlt ? 1 : 2)
   for (int q = 0; q < rounds; ++q) {
-    if (kAlt) fetch(v, g.j0 + q * kThreads * kFly + tid);
-    else if (q + 1 < rounds) fetch(next, g.j0 + (q + 1) * kThreads * kFly + tid);
+    if (kAlt) fetch(v, g.j0 + q * NT * kFly + tid);
+    else if (q + 1 < rounds) fetch(next, g.j0 + (q + 1) * NT * kFly + tid);
     const float m = top_of(v);
     top = max_nan(top, m);
     if constexpr (kAlt) {
-      float* at = gmax + (q >> shift) * kThreads + tid;
+      float* at = gmax + (q >> shift) * NT + tid;
       *at = q & ((1 << shift) - 1) ? max_nan(*at, m) : m;
     }
     if (m > ref + reach) {
@@ -409,13 +409,13 @@ __global__ void __launch_bounds__(kThreads, kAlt ? 6 : 4) token_logprobs_kernel(
   }
   if constexpr (kAlt) {
     sh.tmax[tid] = g.j0 + tid < g.j1 ? key_of(top) : 0;
-    if (tid < kTop) sh.best[tid] = 0;   // below every key, past the part's own
+    for (int i = tid; i < kTop; i += NT) sh.best[i] = 0;   // below every key, past the part's own
   }
   __syncthreads();
   m = sh.red[0][0];
   r = sh.red[1][0];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) {
+  for (int w = 1; w < kWarps; ++w) {
     m = max_nan(m, sh.red[0][w]);
     r = fmaxf(r, sh.red[1][w]);
   }
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, kAlt ? 6 : 4) token_logprobs_kernel(
   __syncthreads();
   float sum = 0.f, sumx = 0.f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     sum += sh.red[2][w];
     sumx += sh.red[3][w];
   }
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, kAlt ? 6 : 4) token_logprobs_kernel(
     have = min(P.K, max(0, e1 - e0));
     if (have > 0) part_top(g, shift, gmax, have, sh);
   }
-  auto* lists = reinterpret_cast<unsigned long long*>(gmax + max_groups(per, shift));   // [cluster][K]
+  auto* lists = reinterpret_cast<unsigned long long*>(gmax + max_groups<NT>(per, shift));   // [cluster][K]
   if (cluster > 1) {   // to rank 0
     __syncthreads();
     cluster_wait();
@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, kAlt ? 6 : 4) token_logprobs_kernel(
       dsmem_st(&sh.peer[rank][1], 0, sum);
       dsmem_st(&sh.peer[rank][2], 0, sumx);
     }
-    if (kAlt && tid < P.K) dsmem_st(&lists[rank * P.K + tid], 0, sh.best[tid]);
+    if (kAlt)
+      for (int i = tid; i < P.K; i += NT) dsmem_st(&lists[rank * P.K + i], 0, sh.best[i]);
     __syncwarp();
     cluster_sync();
   }
@@ -498,10 +499,10 @@ __global__ void __launch_bounds__(kThreads, kAlt ? 6 : 4) token_logprobs_kernel(
         P.top_index[(size_t)row * P.K + at] = (int)~(unsigned)k;
       };
       if (cluster == 1) {
-        for (int i = tid; i < P.K; i += kThreads) put(i, sh.best[i]);
+        for (int i = tid; i < P.K; i += NT) put(i, sh.best[i]);
       } else {
         // the parts' lists together; a key's place is its own place and, in every other list, how many are above it
-        for (int i = tid; i < cluster * P.K; i += kThreads) {
+        for (int i = tid; i < cluster * P.K; i += NT) {
           const int r = i / P.K;
           const unsigned long long k = lists[i];
           if (k == 0) continue;
@@ -524,13 +525,16 @@ __global__ void __launch_bounds__(kThreads, kAlt ? 6 : 4) token_logprobs_kernel(
   pdl_trigger();
 }
 
-// A CTA takes `rounds` times kThreads * kFly vectors of a row, the next round's loads under the current one.
+// A warp takes `rounds` times 32 kFly vectors of a row, the next round's loads under the current one.
 template <class E, bool kVec>
-__global__ void __launch_bounds__(kThreads) token_logprobs_grad_kernel(LogprobParams P, int chunks, int rounds) {
+__global__ void __launch_bounds__(256, 4) token_logprobs_grad_kernel(LogprobParams P, int chunks, int rounds) {
   pdl_wait();
   constexpr int W = kVec ? Vec<E>::W : 1, kFly = kVec ? 4 : 8;
-  const unsigned row = blockIdx.x / (unsigned)chunks;
-  const int chunk = (int)(blockIdx.x - row * (unsigned)chunks);
+  const int lane = threadIdx.x % 32;
+  const long long unit = (long long)blockIdx.x * 8 + threadIdx.x / 32;
+  const unsigned row = (unsigned)(unit / chunks);
+  const int chunk = (int)(unit - (long long)row * chunks);
+  if (row >= (unsigned)P.B * (unsigned)P.T) return;
   const E* z = static_cast<const E*>(P.logits) + (size_t)row * P.ld;
   E* o = static_cast<E*>(P.grad) + (size_t)row * P.ldg;
   const long long y = P.tokens ? ld_index(P.tokens, P.token_i64, row) : -1;
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_grad_kernel(LogprobPa
   const float m = P.stats[2 * (size_t)row], ls = P.stats[2 * (size_t)row + 1], ls2 = ls * kLog2e, h = P.entropy[row];
   if (y < 0) dl = 0.f;
   if (y >= P.V) {
-    if (threadIdx.x == 0 && chunk == 0) atomicOr(P.status, kStatusIndex);
+    if (lane == 0 && chunk == 0) atomicOr(P.status, kStatusIndex);
     dl = __int_as_float(0x7fc00000);
   }
   const bool zero = dl == 0.f && dh == 0.f;
@@ -551,22 +555,22 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_grad_kernel(LogprobPa
     return ex2(x - ls2) * fmaf(b, x, a);
   };
   const int mis = kVec ? (int)(reinterpret_cast<uintptr_t>(z) / sizeof(E)) & (W - 1) : 0;
-  long long first = (long long)chunk * rounds * kThreads * kFly + (int)threadIdx.x;   // vectors
+  long long first = (long long)chunk * rounds * 32 * kFly + lane;   // vectors
   Pack<E, W> v[kFly], next[kFly];
   auto fetch = [&](Pack<E, W> (&d)[kFly], long long from) {
 #pragma unroll
     for (int f = 0; f < kFly; ++f) {
-      const long long e = (from + f * kThreads) * W - mis;
+      const long long e = (from + f * 32) * W - mis;
       if (!zero && e >= 0 && e + W <= P.V) d[f] = *reinterpret_cast<const Pack<E, W>*>(z + e);
     }
   };
   fetch(v, first);
-  for (int q = 0; q < rounds; ++q, first += kThreads * kFly) {
-    if (q + 1 < rounds) fetch(next, first + kThreads * kFly);
+  for (int q = 0; q < rounds; ++q, first += 32 * kFly) {
+    if (q + 1 < rounds) fetch(next, first + 32 * kFly);
     else pdl_trigger();
 #pragma unroll
     for (int f = 0; f < kFly; ++f) {
-      const long long e = (first + f * kThreads) * W - mis;
+      const long long e = (first + f * 32) * W - mis;
       if (e >= 0 && e + W <= P.V) {
         float d[W];
 #pragma unroll
@@ -600,27 +604,35 @@ namespace dph {
 using namespace dpk;
 using namespace dpk::logprobs;
 
-template <class E, bool kAlt>
+template <class E, bool kAlt, int NT>
 static cudaError_t run_logprobs(const LogprobParams& P, cudaStream_t s) {
   constexpr int W = Vec<E>::W;
   const long long rows = (long long)P.B * P.T;
   const long long nvec = ((long long)P.V + 2 * W - 2) / W;   // at any alignment of the row
   // a cluster a row while that leaves every CTA two rounds of loads and the GPU is not full
   int cluster = 1;
-  while (cluster < 8 && rows * cluster * 2 <= 304 && nvec / (2 * cluster) >= 2 * kThreads) cluster *= 2;
+  while (cluster < 8 && rows * cluster * 2 <= 304 && nvec / (2 * cluster) >= 512) cluster *= 2;
   const int per = (int)((nvec + cluster - 1) / cluster);
   int shift = 0;   // at most 4096 groups a part: 16 KB
-  while (max_groups(per, shift) > 4096) ++shift;
-  const size_t smem = sizeof(Shared) + (kAlt ? (size_t)max_groups(per, shift) * 4 + (cluster > 1 ? (size_t)cluster * P.K * 8 : 0) : 0);
-  auto kernel = token_logprobs_kernel<E, kAlt>;
-  if (cluster == 1) return launch_operator(kernel, dim3((unsigned)rows), dim3(kThreads), smem, s, P, 1, per, shift);
-  return launch_operator_cluster(kernel, cluster, dim3((unsigned)(rows * cluster)), dim3(kThreads), smem, s, P, cluster,
-                                 per, shift);
+  while (max_groups<NT>(per, shift) > 4096) ++shift;
+  const size_t smem = sizeof(Shared<NT>) +
+                      (kAlt ? (size_t)max_groups<NT>(per, shift) * 4 + (cluster > 1 ? (size_t)cluster * P.K * 8 : 0) : 0);
+  auto kernel = token_logprobs_kernel<E, kAlt, NT>;
+  if (cluster == 1) return launch_operator(kernel, dim3((unsigned)rows), dim3(NT), smem, s, P, 1, per, shift);
+  return launch_operator_cluster(kernel, cluster, dim3((unsigned)(rows * cluster)), dim3(NT), smem, s, P, cluster, per,
+                                 shift);
+}
+
+template <class E> static cudaError_t run_logprobs_nt(const LogprobParams& P, cudaStream_t s) {
+  // Short rows on 64 threads: most of 256 would have no vector.  (Their maxima bound the K-th largest while K is
+  // well below 64.)
+  const bool small = P.V <= 512 * Vec<E>::W && P.K <= 32;
+  if (P.K) return small ? run_logprobs<E, true, 64>(P, s) : run_logprobs<E, true, 256>(P, s);
+  return small ? run_logprobs<E, false, 64>(P, s) : run_logprobs<E, false, 256>(P, s);
 }
 
 cudaError_t launch_logprobs(const LogprobParams& P, int dtype, cudaStream_t s) {
-  if (dtype == DP_BF16) return P.K ? run_logprobs<__nv_bfloat16, true>(P, s) : run_logprobs<__nv_bfloat16, false>(P, s);
-  return P.K ? run_logprobs<float, true>(P, s) : run_logprobs<float, false>(P, s);
+  return dtype == DP_BF16 ? run_logprobs_nt<__nv_bfloat16>(P, s) : run_logprobs_nt<float>(P, s);
 }
 
 template <class E>
@@ -630,16 +642,16 @@ static cudaError_t run_logprobs_grad(const LogprobParams& P, cudaStream_t s) {
   const auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p) / sizeof(E) % W; };
   const bool vec = at(P.logits) == at(P.grad) && ((P.ld - P.ldg) % W == 0 || (long long)P.B * P.T == 1);
   const long long rows = (long long)P.B * P.T;
-  // rounds a CTA: the row's constants are read once for them, while the CTAs fill the GPU a few times
-  const long long round = vec ? 4 * kThreads * W : 8 * kThreads;
+  // rounds a warp: the row's constants are read once for them, while the warps fill the GPU a few times
+  const long long round = 32 * (vec ? 4 * W : 8);
   const long long all = ((long long)P.V + (vec ? W - 1 : 0) + round - 1) / round;
-  long long rounds = std::max<long long>(1, std::min<long long>(16, all * rows / (152 * 8 * 4)));
-  const long long chunks = (all + rounds - 1) / rounds;
+  long long rounds = std::max<long long>(1, std::min<long long>(32, all * rows / (152 * 32 * 4)));
+  const long long chunks = (all + rounds - 1) / rounds, ctas = (rows * chunks + 7) / 8;
   rounds = (all + chunks - 1) / chunks;
-  if (rows * chunks > 2147483647ll) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)(rows * chunks));
-  return vec ? launch_operator(token_logprobs_grad_kernel<E, true>, grid, dim3(kThreads), 0, s, P, (int)chunks, (int)rounds)
-             : launch_operator(token_logprobs_grad_kernel<E, false>, grid, dim3(kThreads), 0, s, P, (int)chunks, (int)rounds);
+  if (ctas > 2147483647ll) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)ctas);
+  return vec ? launch_operator(token_logprobs_grad_kernel<E, true>, grid, dim3(256), 0, s, P, (int)chunks, (int)rounds)
+             : launch_operator(token_logprobs_grad_kernel<E, false>, grid, dim3(256), 0, s, P, (int)chunks, (int)rounds);
 }
 
 cudaError_t launch_logprobs_grad(const LogprobParams& P, int dtype, cudaStream_t s) {

@@ -166,7 +166,7 @@ struct EmbedParams {
   const float* factors;    // null: 1
   const int *order, *keys; // the sorted tokens: where each stands in [B, T], and the token (V: no gradient)
   float* partial;          // [units][2][D], sums of runs that cover a whole unit
-  float* run_sq;           // [slabs][N], squared norms of runs at their first position
+  float* run_sq;           // [N], squared norms of runs at their first position
   unsigned* status;
   int B, T, V, D, N, i64, padding, units, slabs, accumulate;
   float scale;
@@ -224,8 +224,8 @@ cudaError_t launch_rows_sqnorm(const float* rows, int B, size_t n, float* out, c
 cudaError_t launch_embed_lookup(const dpk::EmbedParams& P, int dtype, cudaStream_t s);
 size_t embed_order_ws_bytes(int N, int V);
 cudaError_t launch_embed_order(const dpk::EmbedParams& P, int* order, int* keys, void* ws, cudaStream_t s);
-constexpr int kEmbedSlab = 256;   // columns of a warp's work
-int embed_unit(int N, int D);     // and its sorted rows
+constexpr int kEmbedSlab = 256;   // columns of a row's piece
+int embed_unit(int N);            // sorted rows of a warp's work
 cudaError_t launch_embed_sqnorms(const dpk::EmbedParams& P, int dtype, float* sqnorms, cudaStream_t s);
 cudaError_t launch_embed_grad(const dpk::EmbedParams& P, int dtype, int out_dtype, cudaStream_t s);
 }  // namespace dph
