@@ -16,6 +16,7 @@
 //
 // Gradient: one read and one write of the rows, elementwise from m, ls and the entropy.  Bound by HBM.
 #include <algorithm>
+#include <type_traits>
 
 #include "seq.cuh"
 #include "tc_ptx.cuh"
@@ -80,6 +81,9 @@ __device__ __forceinline__ uint32_t low_of(float low, __nv_bfloat16) {
 }
 __device__ __forceinline__ float low_of(float low, float) { return low; }
 
+__device__ __forceinline__ void none(Vec<__nv_bfloat16>& v) { v.p.w[0] = v.p.w[1] = v.p.w[2] = v.p.w[3] = 0xff80ff80u; }
+__device__ __forceinline__ void none(Vec<float>& v) { v.p.w[0] = v.p.w[1] = v.p.w[2] = v.p.w[3] = -INFINITY; }
+
 // The smallest value whose key reaches k; 0 gives a NaN, which no value is below.
 __device__ __forceinline__ float value_of(unsigned k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
@@ -104,11 +108,13 @@ template <class E, int NT> struct Grid {
     Vec<E> v;
     if ((unsigned)e0 < inner) {
       v.p = *reinterpret_cast<const Pack<E, W>*>(row + e0);
-    } else {
+    } else if (j < j1) {
       float f[W];
 #pragma unroll
-      for (int n = 0; n < W; ++n) f[n] = j < j1 && e0 + n >= 0 && e0 + n < V ? to_f(row[e0 + n]) : -INFINITY;
+      for (int n = 0; n < W; ++n) f[n] = e0 + n >= 0 && e0 + n < V ? to_f(row[e0 + n]) : -INFINITY;
       v.p.set(f);
+    } else {
+      none(v);
     }
     return v;
   }
@@ -131,14 +137,17 @@ __device__ __forceinline__ void dsmem_st(unsigned long long* p, int rank, unsign
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(ptx::map_rank(ptx::smem_u32(p), rank)), "l"(v) : "memory");
 }
 
+// A row's (or a part of it) maximum, and the sums of e and e x at it, x = (z - m) log2(e) / tau.
+struct Sums { float m, sum, sumx; };
+
 template <int NT> struct alignas(16) Shared {
   static constexpr int kWarps = NT / 32, kRoom = 4 * NT, kList = 2 * NT;   // candidates that are ranked, groups read again
   unsigned tmax[NT];                     // each thread's largest key, 0 without any
   unsigned long long room[kRoom];        // candidates: key, then the index's complement
   unsigned long long best[kTop];         // the part's largest, in order
   unsigned short list[kList];            // groups whose maximum reaches the bound
-  float red[4][kWarps];
-  float peer[8][4];                      // rank 0: every part's maximum and sums
+  Sums warp[kWarps], whole;
+  Sums peer[8];                          // rank 0: every part's
   unsigned bound;
   int count, groups, wsum[kWarps];
 };
@@ -209,11 +218,18 @@ __device__ void part_top(const Grid<E, NT>& g, int shift, const float* gmax, int
   // the groups first, so that their vectors are then read by all threads at once
   {
     const float low = value_of(bound);
-    for (int q = tid; q < groups; q += NT)
-      if (!(gmax[q] < low)) {
-        const int at = atomicAdd(&sh.groups, 1);
-        if (at < kList) sh.list[at] = (unsigned short)q;
+    for (int q = 4 * tid; q < groups; q += 4 * NT) {   // (a multiple of NT)
+      const float4 t = *reinterpret_cast<const float4*>(gmax + q);
+      const bool in[4] = {!(t.x < low), !(t.y < low), !(t.z < low), !(t.w < low)};
+      if (in[0] | in[1] | in[2] | in[3]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (in[i]) {
+            const int at = atomicAdd(&sh.groups, 1);
+            if (at < kList) sh.list[at] = (unsigned short)(q + i);
+          }
       }
+    }
   }
   __syncthreads();
   const int ng = sh.groups;
@@ -319,7 +335,13 @@ template <int NT> __host__ __device__ constexpr int max_groups(int per, int shif
   return ((((per + NT * kFly - 1) / (NT * kFly)) + (1 << shift) - 1) >> shift) * NT;
 }
 
-// Sums of the part's e and e x at its maximum m by differences, for logits whose products would not be finite.
+// Those of one range at the maximum `m` of several, its sums being at its own.
+__device__ __forceinline__ Sums moved(Sums a, float m, float c2) {
+  const float d = max_nan((a.m - m) * c2, kFloor), s = ex2(d);   // an empty range: -inf, and sums of 0
+  return {m, a.sum * s, s * fmaf(a.sum, d, a.sumx)};
+}
+
+// This thread's part of those sums by differences, for logits whose products would not be finite.
 template <class E, int NT>
 __device__ void far_sums(const Grid<E, NT>& g, float m, float c2, float* sum, float* sumx) {
   float s = 0.f, t = 0.f;
@@ -337,15 +359,16 @@ __device__ void far_sums(const Grid<E, NT>& g, float m, float c2, float* sum, fl
 }
 
 template <class E, bool kAlt, int NT>
-__global__ void __launch_bounds__(NT, (kAlt ? 6 : 4) * 256 / NT) token_logprobs_kernel(LogprobParams P, int cluster, int per, int shift) {
+__global__ void __launch_bounds__(NT, (kAlt ? 6 : 4) * 256 / NT) token_logprobs_kernel(LogprobParams P, int log_cluster, int per, int shift) {
   pdl_wait();
+  const int cluster = 1 << log_cluster;
   if (cluster > 1) cluster_arrive();   // that every CTA has begun, before its shared memory is written
   constexpr int W = Vec<E>::W, kWarps = NT / 32;
   extern __shared__ __align__(16) unsigned char dyn[];
   Shared<NT>& sh = *reinterpret_cast<Shared<NT>*>(dyn);
   float* gmax = reinterpret_cast<float*>(dyn + sizeof(Shared<NT>));
   const int tid = threadIdx.x, lane = tid % 32;
-  const unsigned row = blockIdx.x / (unsigned)cluster, rank = blockIdx.x - row * (unsigned)cluster;
+  const unsigned row = blockIdx.x >> log_cluster, rank = blockIdx.x & (unsigned)(cluster - 1);
   const Grid<E, NT> g(static_cast<const E*>(P.logits) + (size_t)row * P.ld, P.V, (int)rank, per);
   const float itau = 1.f / P.tau, c2 = kLog2e * itau, reach = 8.f / c2;
   // entries below `low` give e = 0 as they do, and a finite x
@@ -354,21 +377,26 @@ __global__ void __launch_bounds__(NT, (kAlt ? 6 : 4) * 256 / NT) token_logprobs_
   uint64_t S = 0, T = 0;   // packed pairs
   const uint64_t cc = pair(c2, c2);
   Vec<E> v[kFly], next[kAlt ? 1 : kFly];
-  auto fetch = [&](Vec<E>* d, int j) {
-#pragma unroll
-    for (int f = 0; f < kFly; ++f) d[f] = g.load(j + f * NT);
-  };
+  // Round q's vectors of this thread.  All of a round's vectors are whole and in the part but for the first
+  // round's and the last's.
   const int rounds = g.rounds();
-  if (!kAlt) fetch(v, g.j0 + tid);
-#pragma unroll (kAlt ? 1 : 2)
-  for (int q = 0; q < rounds; ++q) {
-    if (kAlt) fetch(v, g.j0 + q * NT * kFly + tid);
-    else if (q + 1 < rounds) fetch(next, g.j0 + (q + 1) * NT * kFly + tid);
+  const E* const first = g.row + ((long long)(g.j0 + tid) * W - g.mis);
+  auto fetch = [&](Vec<E>* d, int q) {
+    if (q == 0 || q == rounds - 1) {
+#pragma unroll
+      for (int f = 0; f < kFly; ++f) d[f] = g.load(g.j0 + (q * kFly + f) * NT + tid);
+    } else {
+      const E* p = first + (long long)q * (NT * kFly * W);
+#pragma unroll
+      for (int f = 0; f < kFly; ++f) d[f].p = *reinterpret_cast<const Pack<E, W>*>(p + f * NT * W);
+    }
+  };
+  auto eat = [&](auto last, int q) {
     const float m = top_of(v);
     top = max_nan(top, m);
     if constexpr (kAlt) {
       float* at = gmax + (q >> shift) * NT + tid;
-      *at = q & ((1 << shift) - 1) ? max_nan(*at, m) : m;
+      *at = shift && (q & ((1 << shift) - 1)) ? max_nan(*at, m) : m;
     }
     if (m > ref + reach) {
       const float r = m * c2, d = fmaxf(R - r, kFloor), s = ex2(d);
@@ -381,6 +409,7 @@ __global__ void __launch_bounds__(NT, (kAlt ? 6 : 4) * 256 / NT) token_logprobs_
     const uint64_t nr = pair(-R, -R);
 #pragma unroll
     for (int f = 0; f < kFly; ++f) {
+      if (decltype(last)::value && g.j0 + (q * kFly + f) * NT + (tid & ~31) >= g.j1) break;   // (the whole warp's)
       raise_to(v[f], low);
 #pragma unroll
       for (int n = 0; n < W; n += 2) {
@@ -391,59 +420,77 @@ __global__ void __launch_bounds__(NT, (kAlt ? 6 : 4) * 256 / NT) token_logprobs_
         T = fma2(e, x, T);
       }
     }
-    if constexpr (!kAlt) {
+  };
+  if (rounds > 0) {
+    fetch(v, 0);
+#pragma unroll (kAlt ? 1 : 2)
+    for (int q = 0; q < rounds - 1; ++q) {
+      if constexpr (kAlt) {
+        eat(std::false_type(), q);
+        fetch(v, q + 1);
+      } else {
+        fetch(next, q + 1);
+        eat(std::false_type(), q);
 #pragma unroll
-      for (int f = 0; f < kFly; ++f) v[f] = next[f];
+        for (int f = 0; f < kFly; ++f) v[f] = next[f];
+      }
     }
+    eat(std::true_type(), rounds - 1);
   }
-  // the row's (part's) maximum and reference
+  // the warp's maximum and reference, and its sums at the maximum
   float m = top, r = R;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     m = max_nan(m, __shfl_xor_sync(kAll, m, o));
     r = fmaxf(r, __shfl_xor_sync(kAll, r, o));
   }
-  if (lane == 0) {
-    sh.red[0][tid / 32] = m;
-    sh.red[1][tid / 32] = r;
+  {
+    const float d = fmaxf(R - r, kFloor) - fmaf(m, c2, -r), s = ex2(d);
+    const float2 s2 = unpair(S), t2 = unpair(T);
+    const float sum = s2.x + s2.y, x = s * fmaf(sum, d, t2.x + t2.y);
+    const float a = warp_sum(sum * s), b = warp_sum(x);
+    const bool empty = m < -kFar / c2;   // nothing but masks, or no vector: its sums would be 0 (or are far_sums')
+    if (lane == 0) sh.warp[tid / 32] = {m, empty ? 0.f : a, empty ? 0.f : b};
   }
   if constexpr (kAlt) {
     sh.tmax[tid] = g.j0 + tid < g.j1 ? key_of(top) : 0;
     for (int i = tid; i < kTop; i += NT) sh.best[i] = 0;   // below every key, past the part's own
   }
   __syncthreads();
-  m = sh.red[0][0];
-  r = sh.red[1][0];
+  // the part's, in the first warp (the others need it only behind the barriers of part_top)
+  if (tid < 32) {
+    Sums w = sh.warp[lane < kWarps ? lane : 0];
+    m = w.m;
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) {
-    m = max_nan(m, sh.red[0][w]);
-    r = fmaxf(r, sh.red[1][w]);
-  }
-  {
-    float sum, x;
-    if (fabsf(m) < INFINITY && !(fabsf(m) * c2 < kFar)) {   // (the same for every thread)
-      far_sums(g, m, c2, &sum, &x);
-    } else {   // moved to x = (z - m) log2(e) / tau
-      const float d = fmaxf(R - r, kFloor) - fmaf(m, c2, -r), s = ex2(d);
-      const float2 s2 = unpair(S), t2 = unpair(T);
-      sum = s2.x + s2.y;
-      x = s * fmaf(sum, d, t2.x + t2.y);
-      sum *= s;
+    for (int o = kWarps / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, o));
+    m = __shfl_sync(kAll, m, 0);
+    w = moved(w, m, c2);
+    if (m == -INFINITY) w.sum = w.sumx = 0.f;
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) {
+      w.sum += __shfl_xor_sync(kAll, w.sum, o);
+      w.sumx += __shfl_xor_sync(kAll, w.sumx, o);
     }
-    const float a = warp_sum(sum), b = warp_sum(x);
-    if (lane == 0) {
-      sh.red[2][tid / 32] = a;
-      sh.red[3][tid / 32] = b;
-    }
+    if (lane == 0) sh.whole = w;
   }
   __syncthreads();
-  float sum = 0.f, sumx = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    sum += sh.red[2][w];
-    sumx += sh.red[3][w];
+  if (fabsf(sh.whole.m) < INFINITY && !(fabsf(sh.whole.m) * c2 < kFar)) {   // (the same for every thread)
+    float a, b;
+    far_sums(g, sh.whole.m, c2, &a, &b);
+    a = warp_sum(a);
+    b = warp_sum(b);
+    if (lane == 0) sh.warp[tid / 32] = {sh.whole.m, a, b};
+    __syncthreads();
+    if (tid == 0) {
+      Sums w = sh.warp[0];
+      for (int i = 1; i < kWarps; ++i) {
+        w.sum += sh.warp[i].sum;
+        w.sumx += sh.warp[i].sumx;
+      }
+      sh.whole = w;
+    }
+    __syncthreads();
   }
-  if (m == -INFINITY) sum = sumx = 0.f;   // nothing but masks, or an empty part
   int have = 0;   // alternatives of this part
   if constexpr (kAlt) {
     const int e0 = max(0, g.j0 * W - g.mis), e1 = min(P.V, g.j1 * W - g.mis);
@@ -455,29 +502,31 @@ __global__ void __launch_bounds__(NT, (kAlt ? 6 : 4) * 256 / NT) token_logprobs_
     __syncthreads();
     cluster_wait();
     if (tid == 0) {
-      dsmem_st(&sh.peer[rank][0], 0, m);
-      dsmem_st(&sh.peer[rank][1], 0, sum);
-      dsmem_st(&sh.peer[rank][2], 0, sumx);
+      dsmem_st(&sh.peer[rank].m, 0, sh.whole.m);
+      dsmem_st(&sh.peer[rank].sum, 0, sh.whole.sum);
+      dsmem_st(&sh.peer[rank].sumx, 0, sh.whole.sumx);
     }
     if (kAlt)
       for (int i = tid; i < P.K; i += NT) dsmem_st(&lists[rank * P.K + i], 0, sh.best[i]);
     __syncwarp();
     cluster_sync();
   }
-  if (rank == 0) {
+  if (rank == 0 && (kAlt || tid < 32)) {
+    Sums all = sh.whole;
     if (cluster > 1) {
 #pragma unroll
       for (int r = 0; r < 8; ++r)
-        if (r < cluster) m = max_nan(m, sh.peer[r][0]);
-      sum = sumx = 0.f;
+        if (r < cluster) all.m = max_nan(all.m, sh.peer[r].m);
+      all.sum = all.sumx = 0.f;
 #pragma unroll
       for (int r = 0; r < 8; ++r)
-        if (r < cluster) {   // an empty part: its maximum is -inf, its sums 0
-          const float d = max_nan((sh.peer[r][0] - m) * c2, kFloor), s = ex2(d), q = sh.peer[r][1];
-          sum = fmaf(q, s, sum);
-          sumx += s * fmaf(q, d, sh.peer[r][2]);
+        if (r < cluster) {
+          const Sums p = moved(sh.peer[r], all.m, c2);
+          all.sum += p.sum;
+          all.sumx += p.sumx;
         }
     }
+    const float m = all.m, sum = all.sum, sumx = all.sumx;
     const float ls = logf(sum), gone = m == -INFINITY ? __int_as_float(0x7fc00000) : 0.f;
     if (tid == 0) {
       P.stats[2 * (size_t)row] = m;
@@ -610,17 +659,17 @@ static cudaError_t run_logprobs(const LogprobParams& P, cudaStream_t s) {
   const long long rows = (long long)P.B * P.T;
   const long long nvec = ((long long)P.V + 2 * W - 2) / W;   // at any alignment of the row
   // a cluster a row while that leaves every CTA two rounds of loads and the GPU is not full
-  int cluster = 1;
-  while (cluster < 8 && rows * cluster * 2 <= 304 && nvec / (2 * cluster) >= 512) cluster *= 2;
+  int cluster = 1, log_cluster = 0;
+  for (; cluster < 8 && rows * cluster * 2 <= 304 && nvec / (2 * cluster) >= 512; cluster *= 2) ++log_cluster;
   const int per = (int)((nvec + cluster - 1) / cluster);
   int shift = 0;   // at most 4096 groups a part: 16 KB
   while (max_groups<NT>(per, shift) > 4096) ++shift;
   const size_t smem = sizeof(Shared<NT>) +
                       (kAlt ? (size_t)max_groups<NT>(per, shift) * 4 + (cluster > 1 ? (size_t)cluster * P.K * 8 : 0) : 0);
   auto kernel = token_logprobs_kernel<E, kAlt, NT>;
-  if (cluster == 1) return launch_operator(kernel, dim3((unsigned)rows), dim3(NT), smem, s, P, 1, per, shift);
-  return launch_operator_cluster(kernel, cluster, dim3((unsigned)(rows * cluster)), dim3(NT), smem, s, P, cluster, per,
-                                 shift);
+  if (cluster == 1) return launch_operator(kernel, dim3((unsigned)rows), dim3(NT), smem, s, P, 0, per, shift);
+  return launch_operator_cluster(kernel, cluster, dim3((unsigned)(rows * cluster)), dim3(NT), smem, s, P, log_cluster,
+                                 per, shift);
 }
 
 template <class E> static cudaError_t run_logprobs_nt(const LogprobParams& P, cudaStream_t s) {
