@@ -91,7 +91,7 @@ size_t embed_keys_at(const dpk::EmbedParams& P) { return up16((size_t)P.N * size
 size_t embed_partial_bytes(const dpk::EmbedParams& P) { return up16((size_t)P.units * 2 * P.D * sizeof(float)); }
 size_t embed_ws(const dpk::EmbedParams& P) {
   return std::max(dph::embed_order_ws_bytes(P.N, P.V),
-                  embed_partial_bytes(P) + up16((size_t)P.N * sizeof(float)));
+                  embed_partial_bytes(P) + up16((size_t)P.N * sizeof(float)) + up16((size_t)P.units * sizeof(unsigned)));
 }
 dp_status workspace_ok(const void* ws, size_t have, size_t need) {
   if (need && (!ws || have < need))
@@ -229,6 +229,7 @@ static dp_status embed_sums(const dp_embedding_desc* d, const void* order, const
   P->dY = dY;
   P->partial = static_cast<float*>(ws);
   P->run_sq = reinterpret_cast<float*>(static_cast<char*>(ws) + embed_partial_bytes(*P));
+  P->info = reinterpret_cast<unsigned*>(P->run_sq) + up16((size_t)P->N * sizeof(float)) / sizeof(float);
   return DP_OK;
 }
 

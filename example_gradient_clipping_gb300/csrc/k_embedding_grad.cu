@@ -116,6 +116,11 @@ struct alignas(16) Entry {
   unsigned end;   // one of the four, and token or place times 4
 };
 
+// What embed_join_kernel has to know of a unit: its last run goes on over whole units (its part so far is the
+// unit's second partial row); one run covers it (first partial row); and that run begins here; it begins with the
+// end of a run that covers the unit before it (first partial row).
+enum : unsigned { kTailBegins = 1, kCovered = 2, kBegins = 4, kHeadEnds = 8 };
+
 // Ring of S rows of NS slabs: bytes of a warp.
 constexpr int ring_rows(int es, int NS) { return 6 * 1024 / (NS * SLAB * es) < 3 ? 3 : 6 * 1024 / (NS * SLAB * es); }
 template <class E, int PV, int NS> constexpr int ring_bytes() {
@@ -208,6 +213,8 @@ __global__ void __launch_bounds__(256) embed_runs_kernel(EmbedParams P, int U) {
     }
     list[i - a] = e;
   };
+  if (lane == 0)
+    P.info[u] = full ? kCovered | (starts & 1 ? kBegins : 0u) : (next_full ? kTailBegins : 0u) | (head_own ? kHeadEnds : 0u);
   if (holds) {
     enter(own, lane);
     enter(nxt, U + lane);
@@ -328,37 +335,23 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P, int U, i
   // sums: a slab a CTA; norms: all of them
   const int first_slab = kNorm ? 0 : blockIdx.y, slabs = kNorm ? P.slabs : first_slab + 1;
   if (threadIdx.x == 0) count = 0;
-  auto covered = [&](int u, Place* first) {   // whether one run covers unit u, and its first place
-    *first = place(P, u * U);
-    const Place end = place(P, u * U + U - 1);
-    return (long long)u * U + U <= P.N && first->key < P.V && same_run<kNorm>(*first, end);
-  };
+  // lane l: unit u0 + l, and the run of its last row
   const int u = u0 + lane;
-  bool begins = false;   // a long run's first rows are in unit u
-  Place mine = {P.V, 0, 0};
-  int from_tail = 0;
-  if (lane < per && u < P.units) {
-    Place next;
-    const Place before = place(P, u * U - 1), end = place(P, u * U + U - 1);
-    const bool own = covered(u, &mine), behind = covered(u + 1, &next);
-    if (own) {
-      begins = u == 0 || !same_run<kNorm>(before, mine);
-    } else if (behind) {
-      begins = same_run<kNorm>(end, next);
-      from_tail = 1;
-      mine = next;
-    }
-  }
+  const bool here = lane < per && u < P.units;
+  const unsigned info = here ? P.info[u] : 0;
+  const Place mine = place(P, here ? u * U + U - 1 : -1);
+  const bool begins = info & (kTailBegins | kBegins);
+  const int from_tail = info & kTailBegins;
   const unsigned todo = __ballot_sync(kAll, begins);
   // the run that begins in unit u0 + b: its partial rows are the first (of the unit's tail or the whole unit)
   // and those of every unit behind it that it reaches
   auto length = [&](int b, const Place& run) {
     const int from = u0 + b + 1, v = from + lane;
-    Place f;
-    const unsigned mask = __ballot_sync(kAll, v < P.units && covered(v, &f) && same_run<kNorm>(f, run));
+    const unsigned next = v < P.units ? P.info[v] : 0;
+    const unsigned mask = __ballot_sync(kAll, (next & (kCovered | kBegins)) == kCovered);
     if (mask != kAll) {   // it ends in the first unit that it does not cover, or before it
-      const int m = __ffs(~mask) - 1, next = from + m;
-      return 1 + m + (next < P.units && same_run<kNorm>(place(P, next * U), run) ? 1 : 0);
+      const int m = __ffs(~mask) - 1;
+      return 1 + m + (__shfl_sync(kAll, next, m) & kHeadEnds ? 1 : 0);
     }
     const int end = lower_bound<kNorm>(P, (from + 32) * U, P.N, kNorm ? run.key : run.key + 1, run.ex + 1);
     return (end - 1) / U - (u0 + b) + 1;
@@ -366,7 +359,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P, int U, i
   auto add_rows = [&](float (&acc)[8], int b, int tail, int l0, int l1, int c0) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-    constexpr int kFly = PV > 1 ? 6 : 3;   // rows whose loads are in flight
+    constexpr int kFly = 4;   // rows whose loads are in flight
     for (int l = l0; l < l1; l += kFly) {
       RowLoad<float, PV> row[kFly];
 #pragma unroll
@@ -380,12 +373,6 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P, int U, i
             if (col_of<PV>(lane, c0, k) < P.D) acc[k] += row[f].get(k);
         }
     }
-  };
-  auto first_position = [&](int b, int tail, const Place& run) {   // of the run
-    const int ub = u0 + b;
-    if (!tail) return P.order[ub * U];
-    const Place q = place(P, lane < U ? ub * U + lane : -1);
-    return __shfl_sync(kAll, q.pos, __ffs(__ballot_sync(kAll, same_run<kNorm>(q, run))) - 1);
   };
   __syncthreads();
   int at = 0;
@@ -415,7 +402,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P, int U, i
     }
     if (kNorm) {
       q = warp_sum(q);
-      const int pos = first_position(b, tail, run);
+      const int pos = __shfl_sync(kAll, mine.pos, b);   // a place of the run, whose own value is 0
       if (lane == 0) P.run_sq[pos] = q;
     }
   }
@@ -448,7 +435,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P, int U, i
     if (kNorm) {
       total = warp_sum(total);
       if (lane == 0) red[warp] = total;
-      const int pos = first_position(b, tail, run);
+      const int pos = __shfl_sync(kAll, mine.pos, b);   // a place of the run, whose own value is 0
       __syncthreads();
       if (threadIdx.x == 0) {
         float t = 0.f;

@@ -48,6 +48,34 @@ __global__ void __launch_bounds__(32 * kShares) rows_sum_kernel(const float* __r
   }
 }
 
+// Few rows: a thread a column, all of its loads in flight.
+constexpr int kFew = 8;
+__global__ void __launch_bounds__(256) rows_sum_few_kernel(const float* __restrict__ rows, int count, size_t n,
+                                                           const float* __restrict__ factors, void* out, int bf16,
+                                                           int accumulate) {
+  pdl_wait();
+  const size_t col = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (col >= n) return;
+  const float* src = rows + (size_t)blockIdx.y * count * n + col;
+  float v[kFew], f[kFew], acc = 0.f;
+#pragma unroll
+  for (int k = 0; k < kFew; ++k) {
+    v[k] = k < count ? src[(size_t)k * n] : 0.f;
+    f[k] = factors && k < count ? factors[k] : 1.f;
+  }
+#pragma unroll
+  for (int k = 0; k < kFew; ++k)
+    if (k < count) acc = fmaf(f[k], v[k], acc);
+  pdl_trigger();
+  const size_t at = (size_t)blockIdx.y * n + col;
+  if (bf16) {
+    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(acc);
+  } else {
+    float* o = static_cast<float*>(out) + at;
+    *o = accumulate ? *o + acc : acc;
+  }
+}
+
 __global__ void __launch_bounds__(256) rows_sqnorm_kernel(const float* __restrict__ rows, size_t n, float* __restrict__ out) {
   pdl_wait();
   __shared__ float red[8];
@@ -76,9 +104,13 @@ cudaError_t launch_rows_sum(const float* rows, int segments, int count, size_t n
   for (int g = 0; g < segments; g += 65535) {
     const int ng = std::min(segments - g, 65535);
     const size_t off = (size_t)g * n;
-    const cudaError_t e = launch_operator(rows_sum_kernel, dim3((unsigned)((n + 31) / 32), (unsigned)ng),
-                                          dim3(32 * kShares), 0, s, rows + (size_t)g * count * n, count, n, factors,
-                                          static_cast<void*>(static_cast<char*>(out) + off * (bf16 ? 2 : 4)), bf16, accumulate);
+    const float* from = rows + (size_t)g * count * n;
+    void* to = static_cast<char*>(out) + off * (bf16 ? 2 : 4);
+    const cudaError_t e =
+        count <= kFew ? launch_operator(rows_sum_few_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)ng), dim3(256), 0, s,
+                                        from, count, n, factors, to, bf16, accumulate)
+                      : launch_operator(rows_sum_kernel, dim3((unsigned)((n + 31) / 32), (unsigned)ng), dim3(32 * kShares), 0,
+                                        s, from, count, n, factors, to, bf16, accumulate);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -73,17 +73,23 @@ __global__ void __launch_bounds__(dph::norm_threads(G), grad_ctas(G)) layer_norm
     mu = P.mean[base + own];
     rs = P.rstd[base + own];
   }
-  float w[C], dw[C], db[C];
+  uint64_t w[C / 2], dw[C / 2], db[C / 2];   // packed pairs of entries
+  {
+    float f[C];
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int col = (lane + k * G) * VEC;
-    float f[VEC] = {};
-    if (col < P.D) load_param_at<VEC>(f, P.W, P.w_bf16, 1.f, col);
+    for (int k = 0; k < NV; ++k) {
+      const int col = (lane + k * G) * VEC;
+      float one[VEC] = {};
+      if (col < P.D) load_param_at<VEC>(one, P.W, P.w_bf16, 1.f, col);
 #pragma unroll
-    for (int n = 0; n < VEC; ++n) w[k * VEC + n] = f[n];
+      for (int n = 0; n < VEC; ++n) f[k * VEC + n] = one[n];
+    }
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {
+      w[i] = pair(f[2 * i], f[2 * i + 1]);
+      dw[i] = db[i] = 0;
+    }
   }
-#pragma unroll
-  for (int c = 0; c < C; ++c) dw[c] = db[c] = 0.f;
   const float inv = 1.f / (float)P.D;
   int stage = 0;
   for (; base < r1; base += per) {   // (the same for every thread)
@@ -101,39 +107,61 @@ __global__ void __launch_bounds__(dph::norm_threads(G), grad_ctas(G)) layer_norm
     }
     auto vx = [&](int k) { return S ? *reinterpret_cast<const V*>(slot(stage, 0, k)) : rx[S ? 0 : k]; };
     auto vg = [&](int k) { return S ? *reinterpret_cast<const V*>(slot(stage, 1, k)) : rg[S ? 0 : k]; };
-    float s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const V x = vx(k), g = vg(k);
-#pragma unroll
-      for (int n = 0; n < VEC; ++n) {   // past D: w = dy = 0
-        const int c = k * VEC + n;
-        const float d = g.get(n), h = (x.get(n) - mu) * rs, u = w[c] * d;
-        s[0] += u;
-        s[1] = fmaf(u, h, s[1]);
-        dw[c] = fmaf(d, h, dw[c]);
-        db[c] += d;
+    // entries 2 i and 2 i + 1 of x and dy
+    auto pairs = [&](auto& load, int i) {
+      if constexpr (VEC > 1) {
+        const V v = load(2 * i / VEC);
+        return pair(v.get(2 * i % VEC), v.get(2 * i % VEC + 1));
+      } else {
+        return pair(load(2 * i).get(0), load(2 * i + 1).get(0));
       }
+    };
+    const uint64_t nmu2 = pair(-mu, -mu), rs2 = pair(rs, rs);
+    uint64_t sum = 0, sumh = 0;
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {   // past D: w = dy = 0
+      const uint64_t d = pairs(vg, i), h = mul2(add2(pairs(vx, i), nmu2), rs2), u = mul2(w[i], d);
+      sum = add2(sum, u);
+      sumh = fma2(u, h, sumh);
+      dw[i] = fma2(d, h, dw[i]);
+      db[i] = add2(db[i], d);
     }
     if (P.dX) {
+      const float2 s0 = unpair(sum), s1 = unpair(sumh);
+      float s[2] = {s0.x + s0.y, s1.x + s1.y};
       row_sum<G, 2>(s, red, round);
       if constexpr (S > 0) asm volatile("" ::: "memory");   // the row is read again, and not held over the sums
       const float a = s[0] * inv, b = s[1] * inv;
+      const uint64_t na = pair(-a, -a), nb = pair(-b, -b);
       E* o = static_cast<E*>(P.dX) + (size_t)r * P.D;
+      auto out = [&](int i) {
+        const uint64_t h = mul2(add2(pairs(vx, i), nmu2), rs2);
+        return unpair(mul2(fma2(h, nb, fma2(w[i], pairs(vg, i), na)), rs2));
+      };
+      if constexpr (VEC > 1) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int col = (lane + k * G) * VEC;
-        if (col >= P.D || r >= r1) continue;
-        const V x = vx(k), g = vg(k);
-        float v[VEC];
+        for (int k = 0; k < NV; ++k) {
+          const int col = (lane + k * G) * VEC;
+          if (col >= P.D || r >= r1) continue;
+          float v[VEC];
 #pragma unroll
-        for (int n = 0; n < VEC; ++n) {
-          const float h = (x.get(n) - mu) * rs;
-          v[n] = (fmaf(w[k * VEC + n], g.get(n), -a) - h * b) * rs;
+          for (int n = 0; n < VEC; n += 2) {
+            const float2 f = out((k * VEC + n) / 2);
+            v[n] = f.x;
+            v[n + 1] = f.y;
+          }
+          V q;
+          q.set(v);
+          *reinterpret_cast<V*>(o + col) = q;
         }
-        V out;
-        out.set(v);
-        *reinterpret_cast<V*>(o + col) = out;
+      } else {
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i) {
+          const float2 f = out(i);
+          const int col = lane + 2 * i * G;
+          if (r < r1 && col < P.D) o[col] = from_f(f.x, E());
+          if (r < r1 && col + G < P.D) o[col + G] = from_f(f.y, E());
+        }
       }
     }
     if constexpr (S > 0) {
@@ -152,14 +180,18 @@ __global__ void __launch_bounds__(dph::norm_threads(G), grad_ctas(G)) layer_norm
   if (!P.part) return;
   float* part = P.part + (size_t)blockIdx.x * P.k * P.D;
   auto column = [&](int l, int c) { return (l + c / VEC * G) * VEC + c % VEC; };
+  auto entry = [&](const uint64_t (&a)[C / 2], int c) {
+    const float2 f = unpair(a[c / 2]);
+    return c % 2 ? f.y : f.x;
+  };
   if constexpr (G <= 32) {   // the groups' sums, added in order
     if constexpr (S > 0) copies_wait<0>();   // (groups without copies)
     float* sums = reinterpret_cast<float*>(ring);
     __syncthreads();                          // every warp is done with its slots
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      sums[c * threads + threadIdx.x] = dw[c];
-      if (P.k == 2) sums[(C + c) * threads + threadIdx.x] = db[c];
+      sums[c * threads + threadIdx.x] = entry(dw, c);
+      if (P.k == 2) sums[(C + c) * threads + threadIdx.x] = entry(db, c);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < P.k * C * G; i += threads) {
@@ -174,8 +206,8 @@ __global__ void __launch_bounds__(dph::norm_threads(G), grad_ctas(G)) layer_norm
     for (int c = 0; c < C; ++c) {
       const int col = column(lane, c);
       if (col < P.D) {
-        part[col] = dw[c];
-        if (P.k == 2) part[P.D + col] = db[c];
+        part[col] = entry(dw, c);
+        if (P.k == 2) part[P.D + col] = entry(db, c);
       }
     }
   }

@@ -16,7 +16,6 @@
 //
 // Gradient: one read and one write of the rows, elementwise from m, ls and the entropy.  Bound by HBM.
 #include <algorithm>
-#include <type_traits>
 
 #include "seq.cuh"
 #include "tc_ptx.cuh"
@@ -190,7 +189,7 @@ __device__ void part_top(const Grid<E, NT>& g, int shift, const float* gmax, int
         for (int i = 0; i < NT / 32; ++i) c += k[i] >= trial;
         c = __reduce_add_sync(kAll, c);
         if (c >= n) t = trial;
-        if (c == n) break;
+        if (c >= n && c <= n + min(n / 4, 12) + 2) break;   // near enough
       }
     }
     if (lane == 0) {
@@ -359,7 +358,7 @@ __device__ void far_sums(const Grid<E, NT>& g, float m, float c2, float* sum, fl
 }
 
 template <class E, bool kAlt, int NT>
-__global__ void __launch_bounds__(NT, (kAlt ? 6 : 4) * 256 / NT) token_logprobs_kernel(LogprobParams P, int log_cluster, int per, int shift) {
+__global__ void __launch_bounds__(NT, (kAlt ? 5 : 4) * 256 / NT) token_logprobs_kernel(LogprobParams P, int log_cluster, int per, int shift) {
   pdl_wait();
   const int cluster = 1 << log_cluster;
   if (cluster > 1) cluster_arrive();   // that every CTA has begun, before its shared memory is written
@@ -376,66 +375,81 @@ __global__ void __launch_bounds__(NT, (kAlt ? 6 : 4) * 256 / NT) token_logprobs_
   float ref = -kFar / c2, R = -kFar, top = -INFINITY;
   uint64_t S = 0, T = 0;   // packed pairs
   const uint64_t cc = pair(c2, c2);
-  Vec<E> v[kFly], next[kAlt ? 1 : kFly];
-  // Round q's vectors of this thread.  All of a round's vectors are whole and in the part but for the first
-  // round's and the last's.
+  // Round q's vectors of this thread, kPart at a time: all four with the next round's under way, or (the alternatives'
+  // kernel, whose registers are for more CTAs) two and two, each pair asked for again once it is used.  All of a
+  // round's vectors are whole and in the part but for the first round's and the last's.
+  constexpr int kPart = kAlt ? 2 : kFly;
+  Vec<E> v[2][kPart];
   const int rounds = g.rounds();
   const E* const first = g.row + ((long long)(g.j0 + tid) * W - g.mis);
-  auto fetch = [&](Vec<E>* d, int q) {
-    if (q == 0 || q == rounds - 1) {
+  auto fetch = [&](Vec<E> (&d)[kPart], int q, int f0) {
+    if (q == 0 || q >= rounds - 1) {
 #pragma unroll
-      for (int f = 0; f < kFly; ++f) d[f] = g.load(g.j0 + (q * kFly + f) * NT + tid);
+      for (int f = 0; f < kPart; ++f) d[f] = g.load(g.j0 + (q * kFly + f0 + f) * NT + tid);
     } else {
       const E* p = first + (long long)q * (NT * kFly * W);
 #pragma unroll
-      for (int f = 0; f < kFly; ++f) d[f].p = *reinterpret_cast<const Pack<E, W>*>(p + f * NT * W);
+      for (int f = 0; f < kPart; ++f) d[f].p = *reinterpret_cast<const Pack<E, W>*>(p + (f0 + f) * NT * W);
     }
   };
-  auto eat = [&](auto last, int q) {
-    const float m = top_of(v);
-    top = max_nan(top, m);
-    if constexpr (kAlt) {
-      float* at = gmax + (q >> shift) * NT + tid;
-      *at = shift && (q & ((1 << shift) - 1)) ? max_nan(*at, m) : m;
-    }
+  auto eat = [&](Vec<E> (&d)[kPart], bool last, int q, int f0) {   // returns their maximum
+    const float m = top_of(d);
     if (m > ref + reach) {
-      const float r = m * c2, d = fmaxf(R - r, kFloor), s = ex2(d);
-      const uint64_t ss = pair(s, s), dd = pair(d, d);
-      T = mul2(ss, fma2(S, dd, T));
+      const float r = m * c2, x = fmaxf(R - r, kFloor), s = ex2(x);
+      const uint64_t ss = pair(s, s), xx = pair(x, x);
+      T = mul2(ss, fma2(S, xx, T));
       S = mul2(ss, S);
       ref = m;
       R = r;
     }
     const uint64_t nr = pair(-R, -R);
 #pragma unroll
-    for (int f = 0; f < kFly; ++f) {
-      if (decltype(last)::value && g.j0 + (q * kFly + f) * NT + (tid & ~31) >= g.j1) break;   // (the whole warp's)
-      raise_to(v[f], low);
+    for (int f = 0; f < kPart; ++f) {
+      if (last && g.j0 + (q * kFly + f0 + f) * NT + (tid & ~31) >= g.j1) break;   // (the whole warp's)
+      raise_to(d[f], low);
 #pragma unroll
       for (int n = 0; n < W; n += 2) {
-        const uint64_t x = fma2(pair(v[f].get(n), v[f].get(n + 1)), cc, nr);
+        const uint64_t x = fma2(pair(d[f].get(n), d[f].get(n + 1)), cc, nr);
         const float2 y = unpair(x);
         const uint64_t e = pair(ex2(y.x), ex2(y.y));
         S = add2(S, e);
         T = fma2(e, x, T);
       }
     }
+    return m;
+  };
+  auto group = [&](int q, float m) {   // the round's maximum to its group's
+    top = max_nan(top, m);
+    float* at = gmax + (q >> shift) * NT + tid;
+    *at = shift && (q & ((1 << shift) - 1)) ? max_nan(*at, m) : m;
   };
   if (rounds > 0) {
-    fetch(v, 0);
-#pragma unroll (kAlt ? 1 : 2)
-    for (int q = 0; q < rounds - 1; ++q) {
-      if constexpr (kAlt) {
-        eat(std::false_type(), q);
-        fetch(v, q + 1);
-      } else {
-        fetch(next, q + 1);
-        eat(std::false_type(), q);
-#pragma unroll
-        for (int f = 0; f < kFly; ++f) v[f] = next[f];
+    fetch(v[0], 0, 0);
+    if constexpr (kAlt) {
+      fetch(v[1], 0, 2);
+#pragma unroll 1
+      for (int q = 0; q < rounds - 1; ++q) {
+        const float a = eat(v[0], false, q, 0);
+        fetch(v[0], q + 1, 0);
+        const float b = eat(v[1], false, q, 2);
+        fetch(v[1], q + 1, 2);
+        group(q, max_nan(a, b));
       }
+      const float a = eat(v[0], true, rounds - 1, 0), b = eat(v[1], true, rounds - 1, 2);
+      group(rounds - 1, max_nan(a, b));
+    } else {
+      int q = 0;
+#pragma unroll 1
+      for (; q + 2 < rounds; q += 2) {
+        fetch(v[1], q + 1, 0);
+        top = max_nan(top, eat(v[0], false, q, 0));
+        fetch(v[0], q + 2, 0);
+        top = max_nan(top, eat(v[1], false, q + 1, 0));
+      }
+      if (q + 1 < rounds) fetch(v[1], q + 1, 0);
+      top = max_nan(top, eat(v[0], true, q, 0));
+      if (q + 1 < rounds) top = max_nan(top, eat(v[1], true, q + 1, 0));
     }
-    eat(std::true_type(), rounds - 1);
   }
   // the warp's maximum and reference, and its sums at the maximum
   float m = top, r = R;

@@ -166,7 +166,8 @@ struct EmbedParams {
   const float* factors;    // null: 1
   const int *order, *keys; // the sorted tokens: where each stands in [B, T], and the token (V: no gradient)
   float* partial;          // [units][2][D], sums of runs that cover a whole unit
-  float* run_sq;           // [N], squared norms of runs at their first position
+  float* run_sq;           // [N], squared norms of runs at one of their positions
+  unsigned* info;          // [units]
   unsigned* status;
   int B, T, V, D, N, i64, padding, units, slabs, accumulate;
   float scale;
