@@ -52,6 +52,13 @@ dp_status norm_params(const dp_layer_norm_desc* d, bool grad, dpk::NormParams* P
   *P = {};
   P->B = d->B; P->T = d->T; P->D = d->D; P->w_bf16 = d->w_dtype == DP_BF16; P->k = d->has_bias ? 2 : 1;
   P->eps = d->eps; P->x = d->x; P->dy = d->dy;
+  // rows at one stride (one example: its own; one row an example: theirs)
+  auto flat = [&](dp_row_strides& s) {
+    if (d->T == 1) s.t = s.b;
+    return d->T == 1 || d->B == 1 || s.b == (long long)d->T * s.t ? 0 : d->T;
+  };
+  P->xT = flat(P->x);
+  P->dyT = flat(P->dy);
   P->segments = d->per_example ? d->B : 1;
   P->slices = dph::norm_grad_slices(P->segments, (long long)d->B * d->T / P->segments, d->D, d->dtype);
   return DP_OK;

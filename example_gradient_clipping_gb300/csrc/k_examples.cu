@@ -1,15 +1,16 @@
 // Rows of per-example gradients, or of partial sums of them: their squared norms and weighted sums.
 //
-// Both read every row once.  rows_sum_kernel: 32 columns a CTA, 16 warps that each add a consecutive share
-// of the rows in order, eight loads in flight, then the shares in order; so the result has one order.
+// Both read every row once.  rows_sum_kernel: 32 columns a CTA, 32 or 8 warps that each add a consecutive
+// share of the rows in order, twelve loads in flight, then the shares in order; so the result has one order.
 #include <algorithm>
 
 #include "seq.cuh"
 
 namespace dpk {
 
-constexpr int kShares = 16;
+constexpr int kFly = 12;   // rows in flight
 
+template <int kShares>
 __global__ void __launch_bounds__(32 * kShares) rows_sum_kernel(const float* __restrict__ rows, int count, size_t n,
                                                                 const float* __restrict__ factors, void* out, int bf16,
                                                                 int accumulate) {
@@ -21,15 +22,15 @@ __global__ void __launch_bounds__(32 * kShares) rows_sum_kernel(const float* __r
   const float* src = rows + (size_t)blockIdx.y * count * n + col;
   float acc = 0.f;
   if (col < n) {
-    for (int i = i0; i < i1; i += 8) {
-      float v[8], f[8];
+    for (int i = i0; i < i1; i += kFly) {
+      float v[kFly], f[kFly];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < kFly; ++k) {
         v[k] = i + k < i1 ? src[(size_t)(i + k) * n] : 0.f;
         f[k] = factors && i + k < i1 ? factors[i + k] : 1.f;
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < kFly; ++k)
         if (i + k < i1) acc = fmaf(f[k], v[k], acc);
     }
   }
@@ -106,11 +107,15 @@ cudaError_t launch_rows_sum(const float* rows, int segments, int count, size_t n
     const size_t off = (size_t)g * n;
     const float* from = rows + (size_t)g * count * n;
     void* to = static_cast<char*>(out) + off * (bf16 ? 2 : 4);
-    const cudaError_t e =
-        count <= kFew ? launch_operator(rows_sum_few_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)ng), dim3(256), 0, s,
-                                        from, count, n, factors, to, bf16, accumulate)
-                      : launch_operator(rows_sum_kernel, dim3((unsigned)((n + 31) / 32), (unsigned)ng), dim3(32 * kShares), 0,
-                                        s, from, count, n, factors, to, bf16, accumulate);
+    const dim3 grid((unsigned)((n + 31) / 32), (unsigned)ng);
+    cudaError_t e;
+    if (count <= kFew)
+      e = launch_operator(rows_sum_few_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)ng), dim3(256), 0, s, from, count,
+                          n, factors, to, bf16, accumulate);
+    else if ((unsigned long long)grid.x * grid.y <= 304)   // few columns: shorter shares
+      e = launch_operator(rows_sum_kernel<32>, grid, dim3(1024), 0, s, from, count, n, factors, to, bf16, accumulate);
+    else
+      e = launch_operator(rows_sum_kernel<8>, grid, dim3(256), 0, s, from, count, n, factors, to, bf16, accumulate);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

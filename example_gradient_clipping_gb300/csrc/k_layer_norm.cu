@@ -10,16 +10,17 @@ using namespace lnorm;
 
 // The CTAs go over the rows.  Rows of vectors: each thread copies its own vectors into S slots of shared memory,
 // S - 1 rows ahead, and reads only what it copied (no barrier); others are read when they are due.
+constexpr int fwd_threads(int G) { return G > 32 ? G : 256; }   // of a CTA
 constexpr int fwd_stages(int es, int vec, int G, int C) {
-  const int stage = dph::norm_threads(G) * (C / vec) * 16;
+  const int stage = fwd_threads(G) * (C / vec) * 16;
   return vec * es != 16 ? 0 : 4 * stage <= 48 * 1024 ? 4 : 3;
 }
 constexpr int fwd_ctas(int G, int C) { return G > 32 ? 1024 / G : C > 16 ? 2 : 3; }   // an SM
 
 template <class E, int VEC, int G, int C>
-__global__ void __launch_bounds__(dph::norm_threads(G), fwd_ctas(G, C)) layer_norm_kernel(NormParams P) {
+__global__ void __launch_bounds__(fwd_threads(G), fwd_ctas(G, C)) layer_norm_kernel(NormParams P) {
   pdl_wait();
-  constexpr int NV = C / VEC, S = fwd_stages(sizeof(E), VEC, G, C), threads = dph::norm_threads(G), per = dph::norm_rows(G);
+  constexpr int NV = C / VEC, S = fwd_stages(sizeof(E), VEC, G, C), threads = fwd_threads(G), per = threads / G;
   using V = Pack<E, VEC>;
   extern __shared__ uint4 ring[];   // [S][NV][threads]
   __shared__ float red[2][1][32];
@@ -30,7 +31,7 @@ __global__ void __launch_bounds__(dph::norm_threads(G), fwd_ctas(G, C)) layer_no
   auto slot = [&](int stage, int k) { return ring + (stage * NV + k) * threads + threadIdx.x; };
   auto copy = [&](int stage, unsigned row) {
     if (row < rows) {
-      const E* p = X + row_at(P.x, P.T, row);
+      const E* p = X + row_at(P.x, P.xT, row);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int col = (lane + k * G) * VEC;
@@ -46,19 +47,27 @@ __global__ void __launch_bounds__(dph::norm_threads(G), fwd_ctas(G, C)) layer_no
 #pragma unroll
     for (int s = 0; s < S - 1; ++s) copy(s, base + own + s * step);
   }
-  float w[C], b[C];
+  uint64_t w[C / 2], b[C / 2];   // packed pairs of entries
+  {
+    float f[C], h[C];
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int col = (lane + k * G) * VEC;
-    float f[VEC] = {}, h[VEC] = {};
-    if (col < P.D) {
-      load_param_at<VEC>(f, P.W, P.w_bf16, 1.f, col);
-      load_param_at<VEC>(h, P.bias, P.w_bf16, 0.f, col);
+    for (int k = 0; k < NV; ++k) {
+      const int col = (lane + k * G) * VEC;
+      float one[VEC] = {}, two[VEC] = {};
+      if (col < P.D) {
+        load_param_at<VEC>(one, P.W, P.w_bf16, 1.f, col);
+        load_param_at<VEC>(two, P.bias, P.w_bf16, 0.f, col);
+      }
+#pragma unroll
+      for (int n = 0; n < VEC; ++n) {
+        f[k * VEC + n] = one[n];
+        h[k * VEC + n] = two[n];
+      }
     }
 #pragma unroll
-    for (int n = 0; n < VEC; ++n) {
-      w[k * VEC + n] = f[n];
-      b[k * VEC + n] = h[n];
+    for (int i = 0; i < C / 2; ++i) {
+      w[i] = pair(f[2 * i], f[2 * i + 1]);
+      b[i] = pair(h[2 * i], h[2 * i + 1]);
     }
   }
   const float inv = 1.f / (float)P.D;
@@ -74,38 +83,69 @@ __global__ void __launch_bounds__(dph::norm_threads(G), fwd_ctas(G, C)) layer_no
       copy(stage == 0 ? S - 1 : stage - 1, r + (S - 1) * step);   // the slot that the last row left
       stage = stage + 1 == S ? 0 : stage + 1;
     } else {
-      const E* p = X + (there ? row_at(P.x, P.T, r) : 0);
+      const E* p = X + (there ? row_at(P.x, P.xT, r) : 0);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int col = (lane + k * G) * VEC;
         x.v[k] = there && col < P.D ? *reinterpret_cast<const V*>(p + col) : V{};
       }
     }
-    float s[1] = {0.f};
+    uint64_t d[C / 2], sum = 0;   // x, then x - mu
 #pragma unroll
-    for (int c = 0; c < C; ++c) s[0] += x.get(c);
-    row_sum<G, 1>(s, red, round);
-    const float mu = s[0] * inv;
-    s[0] = 0.f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const float d = (lane + c / VEC * G) * VEC < P.D ? x.get(c) - mu : 0.f;
-      s[0] = fmaf(d, d, s[0]);
+    for (int i = 0; i < C / 2; ++i) {
+      d[i] = pair(x.get(2 * i), x.get(2 * i + 1));
+      sum = add2(sum, d[i]);
     }
-    row_sum<G, 1>(s, red, round);
+    float2 f = unpair(sum);
+    float s[1] = {f.x + f.y};
+    row_sum<G, 1, true>(s, red, round);
+    const float mu = s[0] * inv;
+    const uint64_t nmu = pair(-mu, -mu);
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {
+      d[i] = add2(d[i], nmu);
+      const bool in = (lane + 2 * i / VEC * G) * VEC < P.D;   // (VEC = 1: the pair's second entry is G columns on)
+      if (VEC > 1) {
+        if (in) sum = fma2(d[i], d[i], sum);
+      } else {
+        const float2 e = unpair(d[i]);
+        const uint64_t g = pair(in ? e.x : 0.f, lane + (2 * i + 1) * G < P.D ? e.y : 0.f);
+        sum = fma2(g, g, sum);
+      }
+    }
+    f = unpair(sum);
+    s[0] = f.x + f.y;
+    row_sum<G, 1, true>(s, red, round);
     const float rs = rsqrtf(s[0] * inv + P.eps);
     if (!there) continue;
+    const uint64_t rs2 = pair(rs, rs);
     E* y = static_cast<E*>(P.Y) + (size_t)r * P.D;
+    auto out = [&](int i) { return unpair(fma2(mul2(d[i], rs2), w[i], b[i])); };
+    if constexpr (VEC > 1) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int col = (lane + k * G) * VEC;
-      if (col >= P.D) continue;
-      float o[VEC];
+      for (int k = 0; k < NV; ++k) {
+        const int col = (lane + k * G) * VEC;
+        if (col >= P.D) continue;
+        float o[VEC];
 #pragma unroll
-      for (int n = 0; n < VEC; ++n) o[n] = fmaf((x.v[k].get(n) - mu) * rs, w[k * VEC + n], b[k * VEC + n]);
-      V out;
-      out.set(o);
-      *reinterpret_cast<V*>(y + col) = out;
+        for (int n = 0; n < VEC; n += 2) {
+          const float2 e = out((k * VEC + n) / 2);
+          o[n] = e.x;
+          o[n + 1] = e.y;
+        }
+        V v;
+        v.set(o);
+        *reinterpret_cast<V*>(y + col) = v;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i) {
+        const float2 e = out(i);
+        const int col = lane + 2 * i * G;
+        if (col < P.D) y[col] = from_f(e.x, E());
+        if (col + G < P.D) y[col + G] = from_f(e.y, E());
+      }
     }
     if (lane == 0 && P.mean) {
       P.mean[r] = mu;
@@ -123,7 +163,7 @@ using namespace dpk;
 template <class E, int VEC>
 static cudaError_t run_norm_fwd(const NormParams& P, cudaStream_t s) {
   return with_norm_shape<VEC>(P.D, [&](auto g, auto c) {
-    constexpr int G = decltype(g)::value, C = decltype(c)::value, threads = norm_threads(G), per = norm_rows(G);
+    constexpr int G = decltype(g)::value, C = decltype(c)::value, threads = fwd_threads(G), per = threads / G;
     constexpr int smem = fwd_stages(sizeof(E), VEC, G, C) * (C / VEC) * threads * 16;
     if (smem > 40 * 1024) {   // (beside the static arrays)
       const cudaError_t e = allow_smem<layer_norm_kernel<E, VEC, G, C>>(smem);

@@ -14,22 +14,24 @@ using namespace lnorm;
 // Rows in flight: with S > 0 each thread copies its own 16-byte vectors of x and dy into S slots of shared memory,
 // S - 1 rows ahead, and reads only what it copied itself (no barrier); with S = 0 (rows that no vector
 // fits, or that are too long for the slots) the next row waits in registers.
+constexpr int grad_threads(int G) { return G > 512 ? G : 512; }   // of a CTA, one an SM
 constexpr int ring_stages(int es, int vec, int G, int C) {
-  const int stage = dph::norm_threads(G) * 2 * (C / vec) * 16, fit = 100 * 1024 / stage;   // for two CTAs an SM
-  return vec * es != 16 || 2 * stage > 200 * 1024 ? 0 : fit >= 6 ? 6 : fit >= 2 ? fit : 2;
+  const int stage = grad_threads(G) * 2 * (C / vec) * 16, fit = 200 * 1024 / stage;
+  return vec * es != 16 || fit < 2 ? 0 : fit < 6 ? fit : 6;
 }
-constexpr int grad_ctas(int G) { return G > 128 ? (G >= 512 ? 1 : 2) : G > 32 ? 3 : 2; }   // an SM
 
 template <class E, int VEC, int G, int C>
-__global__ void __launch_bounds__(dph::norm_threads(G), grad_ctas(G)) layer_norm_grad_kernel(NormParams P) {
+__global__ void __launch_bounds__(grad_threads(G)) layer_norm_grad_kernel(NormParams P) {
   pdl_wait();
   constexpr int NV = C / VEC, S = ring_stages(sizeof(E), VEC, G, C), D1 = S ? 1 : NV;
   using V = Pack<E, VEC>;
-  extern __shared__ uint4 ring[];   // [S][x, dy][NV][threads]; then, G <= 32: every thread's columns of dw and db
-  __shared__ float red[2][2][32];
+  extern __shared__ uint4 ring[];   // [S][x, dy][NV][threads]; then every thread's columns of dw and db
+  constexpr bool kAlone = grad_threads(G) == G;
+  __shared__ float reds[kAlone ? 1 : 512 / G][2][2][G > 32 ? 32 : 1];
   int round = 0;
   const int lane = threadIdx.x % G, threads = blockDim.x;
-  const unsigned per = G > 32 ? 1 : threads / G, own = threadIdx.x / G;
+  const unsigned per = threads / G, own = threadIdx.x / G;
+  auto* red = reinterpret_cast<float (*)[2][32]>(reds[kAlone || G <= 32 ? 0 : own]);
   const unsigned total = (unsigned)P.B * (unsigned)P.T, seg_rows = total / (unsigned)P.segments;
   const unsigned seg = blockIdx.x / (unsigned)P.slices, slice = blockIdx.x - seg * (unsigned)P.slices;
   // this CTA's rows of its segment
@@ -39,7 +41,7 @@ __global__ void __launch_bounds__(dph::norm_threads(G), grad_ctas(G)) layer_norm
   V rx[D1], rg[D1], nx[D1], ng[D1];
   auto fetch = [&](V (&a)[D1], V (&b)[D1], unsigned row) {   // zeros past the slice
     const bool there = row < r1;
-    const E *px = X + (there ? row_at(P.x, P.T, row) : 0), *pg = dY + (there ? row_at(P.dy, P.T, row) : 0);
+    const E *px = X + (there ? row_at(P.x, P.xT, row) : 0), *pg = dY + (there ? row_at(P.dy, P.dyT, row) : 0);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int col = (lane + k * G) * VEC;
@@ -51,7 +53,7 @@ __global__ void __launch_bounds__(dph::norm_threads(G), grad_ctas(G)) layer_norm
   auto copy = [&](int stage, unsigned row) {
     if (row < r1 + per) {   // (a group past the slice beside others that are not: zeros)
       const bool there = row < r1;
-      const E *px = X + (there ? row_at(P.x, P.T, row) : 0), *pg = dY + (there ? row_at(P.dy, P.T, row) : 0);
+      const E *px = X + (there ? row_at(P.x, P.xT, row) : 0), *pg = dY + (there ? row_at(P.dy, P.dyT, row) : 0);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int col = (lane + k * G) * VEC;
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(dph::norm_threads(G), grad_ctas(G)) layer_norm
     if (P.dX) {
       const float2 s0 = unpair(sum), s1 = unpair(sumh);
       float s[2] = {s0.x + s0.y, s1.x + s1.y};
-      row_sum<G, 2>(s, red, round);
+      row_sum<G, 2, kAlone>(s, red, round);
       if constexpr (S > 0) asm volatile("" ::: "memory");   // the row is read again, and not held over the sums
       const float a = s[0] * inv, b = s[1] * inv;
       const uint64_t na = pair(-a, -a), nb = pair(-b, -b);
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(dph::norm_threads(G), grad_ctas(G)) layer_norm
     const float2 f = unpair(a[c / 2]);
     return c % 2 ? f.y : f.x;
   };
-  if constexpr (G <= 32) {   // the groups' sums, added in order
+  if constexpr (!kAlone) {   // the groups' sums, added in order
     if constexpr (S > 0) copies_wait<0>();   // (groups without copies)
     float* sums = reinterpret_cast<float*>(ring);
     __syncthreads();                          // every warp is done with its slots
@@ -218,25 +220,34 @@ __global__ void __launch_bounds__(dph::norm_threads(G), grad_ctas(G)) layer_norm
 namespace dph {
 using namespace dpk;
 
-// Enough slices to fill the GPU once; a group of threads has four rows of a slice or more where the segment has
-// them.  (By width and type alone: the workspace is the same wherever the tensors lie.)
+// Slices a segment: what takes the GPU's CTAs, one an SM, the least rounds of a group's rows, each CTA's start and
+// end counted as six rows.  (By width and type alone: the workspace is the same wherever the tensors lie.)
 int norm_grad_slices(int segments, long long rows, int D, int dtype) {
-  const int W = dtype == DP_BF16 ? 8 : 4, G = norm_shape(D, D % W ? 1 : W).G;
-  const long long most = std::max<long long>(1, rows / (4 * norm_rows(G)));
-  const long long want = (152 * grad_ctas(G) + segments - 1) / segments;
-  return (int)std::max<long long>(1, std::min(most, want));
+  const int W = dtype == DP_BF16 ? 8 : 4, G = norm_shape(D, D % W ? 1 : W).G, per = grad_threads(G) / G;
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= 152 && (s == 1 || rows / s >= per); ++s) {
+    const double waves = (double)(((long long)segments * s + 151) / 152);
+    const double cost = waves * ((double)((rows + (long long)s * per - 1) / ((long long)s * per)) + 6);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+    if ((long long)segments * s > 152 * 8) break;
+  }
+  return best;
 }
 
 template <class E, int VEC>
 static cudaError_t run_norm_grad(const NormParams& P, cudaStream_t s) {
   return with_norm_shape<VEC>(P.D, [&](auto g, auto c) {
-    constexpr int G = decltype(g)::value, C = decltype(c)::value;
+    constexpr int G = decltype(g)::value, C = decltype(c)::value, kThreads = grad_threads(G);
     constexpr int S = ring_stages(sizeof(E), VEC, G, C), row_bytes = 2 * C / VEC * 16;   // of a thread
     const long long rows = ((long long)P.B * P.T / P.segments + P.slices - 1) / P.slices;   // of a slice
-    const int threads = G > 32 ? G : (int)std::min<long long>(256, (rows * G + 31) / 32 * 32);
-    const size_t sums = G <= 32 && P.part ? (size_t)threads * P.k * C * 4 : 0;
+    const int threads = (int)std::min<long long>(kThreads, (rows * G + 31) / 32 * 32);
+    const size_t sums = kThreads > G && P.part ? (size_t)threads * P.k * C * 4 : 0;
     const size_t smem = std::max((size_t)S * threads * row_bytes, sums);
-    constexpr int most = std::max(S * norm_threads(G) * row_bytes, G <= 32 ? 256 * 2 * C * 4 : 0);
+    constexpr int most = std::max(S * kThreads * row_bytes, kThreads > G ? kThreads * 2 * C * 4 : 0);
     if (most > 40 * 1024) {   // (beside the static arrays)
       const cudaError_t e = allow_smem<layer_norm_grad_kernel<E, VEC, G, C>>(most);
       if (e != cudaSuccess) return e;

@@ -7,7 +7,7 @@
 namespace dpk {
 namespace lnorm {
 
-// A row of D entries is held by G threads (G <= 32: a group of a CTA of 256 threads; else a whole CTA), C entries
+// A row of D entries is held by a group of G threads of a CTA, C entries
 // a thread as C / VEC vectors: vector k of a thread is the row's vector lane + k G.
 template <class E, int VEC, int C> struct Row {
   Pack<E, VEC> v[C / VEC];
@@ -37,9 +37,9 @@ __device__ __forceinline__ void load_param_at(float (&f)[VEC], const void* p, in
 }
 
 // Sums of N values over the G threads of a row, in every one of them.  G > 32: `red` has room for
-// two rounds of N values a warp; a thread is at most one round ahead of another, so the rounds' buffers
-// alternate.
-template <int G, int N>
+// two rounds of N values a warp of the group; a thread is at most one round ahead of another, so the rounds'
+// buffers alternate.  kAlone: the group is the whole CTA, else it meets at a barrier of its own.
+template <int G, int N, bool kAlone>
 __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[N][32], int& round) {
 #pragma unroll
   for (int n = 0; n < N; ++n) {
@@ -48,12 +48,13 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[N][32], int&
   }
   if constexpr (G > 32) {
     constexpr int W = G / 32;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = threadIdx.x % G / 32, lane = threadIdx.x % 32;
     if (lane == 0) {
 #pragma unroll
       for (int n = 0; n < N; ++n) red[round][n][warp] = v[n];
     }
-    __syncthreads();
+    if constexpr (kAlone) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"((int)threadIdx.x / G + 1), "n"(G) : "memory");
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       float s = lane < W ? red[round][n][lane] : 0.f;
@@ -65,7 +66,9 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[N][32], int&
   }
 }
 
+// Where row r begins; T = 0: all rows at one stride.
 __device__ __forceinline__ size_t row_at(const dp_row_strides& s, int T, unsigned r) {
+  if (T == 0) return (size_t)r * s.t;
   const unsigned b = r / (unsigned)T;
   return (size_t)b * s.b + (size_t)(r - b * (unsigned)T) * s.t;
 }
@@ -84,9 +87,6 @@ struct Shape { int G, C; };
 }  // namespace dpk
 
 namespace dph {
-// Threads of a CTA, and rows that it holds at once.
-constexpr int norm_threads(int G) { return G > 32 ? G : 256; }
-constexpr int norm_rows(int G) { return G > 32 ? 1 : 256 / G; }
 // Eight entries a thread for short rows, so that their threads have some; up to a warp a row with 32 (bf16
 // vectors) or 16 entries a thread; then a CTA a row.
 inline dpk::lnorm::Shape norm_shape(int D, int vec) {

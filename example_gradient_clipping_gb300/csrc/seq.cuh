@@ -154,6 +154,7 @@ struct NormParams {
   float *mean, *rstd;      // written by the forward pass (may be null there)
   float* part;             // gradient: slice s's sums at part + s * k * D (null: not formed)
   int B, T, D, w_bf16, k;  // k: vectors of D in a row of the parameters' gradient
+  int xT, dyT;             // T, or 0 where all rows of x (dy) stand at one stride
   int slices;              // gradient: slices of rows a segment (an example, or the whole batch)
   int segments;
   float eps;
