@@ -3,11 +3,15 @@
 // Lookup: one read of the rows met and one write, bound by HBM.
 //
 // Order: the positions sorted by their tokens, stably (least significant digit first), so that equal tokens
-// stand in the order of their positions and, among them, example by example.  Up to 4096 tokens in one CTA's
-// shared memory; longer lists in tiles of a CTA each: counted, then written to their places.  Bound by latency.
+// stand in the order of their positions and, among them, example by example.  Up to 16384 tokens in one launch: 1024
+// a CTA of a cluster of 1, 8 or 16 that write each digit's keys to one another's shared memory (16384 tokens,
+// V = 50257: 9.9 us, 13.4 in tiles, 26 in one CTA; 4096 tokens a CTA 17.3, for four-byte stores to
+// other SMs are what it then waits for); longer lists in tiles of a CTA each: counted, then written to their
+// places (262144 tokens: 24 us).  Bound by latency.
 #include <algorithm>
 
 #include "seq.cuh"
+#include "tc_ptx.cuh"
 
 namespace dpk {
 namespace embed {
@@ -119,32 +123,35 @@ __device__ __forceinline__ unsigned block_exclusive(unsigned v, unsigned* red) {
 
 constexpr int kDigit = 9;   // bits of the widest digit
 
-// Up to 1024 IT tokens in one CTA, all passes in shared memory.
-template <int IT, int BITS>
-__global__ void __launch_bounds__(1024) embed_sort_small_kernel(EmbedParams P, int passes, int bits, int* order, int* keys) {
+// Up to 1024 tokens a CTA of a cluster of CL, one a thread, all passes in shared memory: a pass counts its digits, tells every
+// CTA how many of each it has, and writes its keys to their places, which may be another CTA's.
+template <int BITS, int CL>
+__global__ void __launch_bounds__(1024) embed_sort_kernel(EmbedParams P, int passes, int bits, int* order, int* keys) {
   pdl_wait();
-  constexpr int kBins = 1 << BITS;
+  if constexpr (CL > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // that all have begun
+  constexpr int kBins = 1 << BITS, M = 1024, IT = 1;
   extern __shared__ unsigned sm[];
   __shared__ unsigned red[32], base[kBins];
-  unsigned *sk = sm, *sv = sm + 1024 * IT;
-  unsigned short* cnt = reinterpret_cast<unsigned short*>(sv + 1024 * IT);   // [32][kBins]
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  unsigned *sk = sm, *sv = sm + M, *totals = sv + M;                            // [CL][kBins]
+  unsigned short* cnt = reinterpret_cast<unsigned short*>(totals + CL * kBins);   // [32][kBins]
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, rank0 = CL > 1 ? (int)blockIdx.x : 0;
+  const int first = rank0 * M, bins = 1 << bits;
   unsigned key[IT], val[IT];
   unsigned short rank[IT];
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int r = (warp * IT + i) * 32 + lane;
+    const int r = first + (warp * IT + i) * 32 + lane;
     // past the end: the largest key of the passes' bits, so the last places stay theirs
     key[i] = r < P.N ? token_key(P, r) : kAll;
     val[i] = (unsigned)r;
   }
   for (int p = 0; p < passes; ++p) {
-    const int shift = p * bits, bins = 1 << bits;
+    const int shift = p * bits;
     for (int b = lane; b < bins; b += 32) cnt[warp * kBins + b] = 0;
     __syncwarp();
     warp_ranks<IT, BITS>(key, rank, cnt + warp * kBins, shift, bits);
     __syncthreads();
-    unsigned total = 0;
+    unsigned total = 0, before = 0;
     if ((int)threadIdx.x < bins) {
 #pragma unroll 8
       for (int w = 0; w < 32; ++w) {
@@ -153,34 +160,64 @@ __global__ void __launch_bounds__(1024) embed_sort_small_kernel(EmbedParams P, i
         total += c;
       }
     }
-    const unsigned first = block_exclusive(total, red);
-    if ((int)threadIdx.x < bins) base[threadIdx.x] = first;
+    if constexpr (CL > 1) {
+      if (p == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      if ((int)threadIdx.x < bins) {
+#pragma unroll
+        for (int c = 0; c < CL; ++c)
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(ptx::map_rank(ptx::smem_u32(totals + rank0 * kBins + threadIdx.x), c)),
+                       "r"(total) : "memory");
+      }
+      __syncwarp();
+      ptx::cluster_sync();
+      total = 0;
+      if ((int)threadIdx.x < bins) {
+#pragma unroll
+        for (int c = 0; c < CL; ++c) {
+          const unsigned t = totals[c * kBins + threadIdx.x];
+          if (c < rank0) before += t;
+          total += t;
+        }
+      }
+    }
+    const unsigned at = block_exclusive(total, red);
+    if ((int)threadIdx.x < bins) base[threadIdx.x] = at + before;
     __syncthreads();
+    const bool last = p == passes - 1;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       const unsigned d = key[i] >> shift & (unsigned)(bins - 1);
       const unsigned to = base[d] + cnt[warp * kBins + d] + rank[i];
-      sk[to] = key[i];
-      sv[to] = val[i];
+      if (last) {
+        if (to < (unsigned)P.N) {
+          order[to] = (int)val[i];
+          keys[to] = (int)key[i];
+        }
+      } else if constexpr (CL > 1) {
+        const unsigned c = to / M, l = to % M;
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(ptx::map_rank(ptx::smem_u32(sk + l), c)), "r"(key[i]) : "memory");
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(ptx::map_rank(ptx::smem_u32(sv + l), c)), "r"(val[i]) : "memory");
+      } else {
+        sk[to] = key[i];
+        sv[to] = val[i];
+      }
     }
-    __syncthreads();
+    if (last) break;
+    if constexpr (CL > 1) {
+      __syncwarp();
+      ptx::cluster_sync();
+    } else {
+      __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int r = (warp * IT + i) * 32 + lane;
-      key[i] = sk[r];
-      val[i] = sv[r];
+      const int l = (warp * IT + i) * 32 + lane;
+      key[i] = sk[l];
+      val[i] = sv[l];
     }
-    // (the next write of sk and sv comes behind the barriers of the scan)
+    // (the next write of sk, sv and totals comes behind the barriers of the next pass, or, totals: of this one)
   }
   pdl_trigger();
-#pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int r = (warp * IT + i) * 32 + lane;
-    if (r < P.N) {
-      order[r] = (int)val[i];
-      keys[r] = (int)key[i];
-    }
-  }
 }
 
 // Longer lists, one digit a pass: tiles of 256 IT keys are counted, the counts summed over (digit, tile), and
@@ -367,7 +404,7 @@ static void digits(int V, int* passes, int* bits) {
   *passes = (b + kDigit - 1) / kDigit;
   *bits = (b + *passes - 1) / *passes;
 }
-constexpr int kSmallSort = 4 * 1024;
+constexpr int kSmallSort = 16 * 1024;
 static int tile_keys(int N) { return N <= 1 << 20 ? 1024 : 4096; }   // few tiles would leave SMs without one
 static int tiles_of(int N) { return (int)(((long long)N + tile_keys(N) - 1) / tile_keys(N)); }
 static size_t up16(size_t n) { return (n + 15) / 16 * 16; }
@@ -379,12 +416,14 @@ size_t embed_order_ws_bytes(int N, int V) {
   return 2 * up16((size_t)N * 4) + 2 * up16(counts * 4) + up16((counts / 1024 + 1) * 4);
 }
 
-template <int IT, int BITS>
+template <int BITS, int CL>
 static cudaError_t run_small_sort(const EmbedParams& P, int passes, int bits, int* order, int* keys, cudaStream_t s) {
-  constexpr int smem = 1024 * IT * 8 + 32 * (1 << BITS) * 2;
-  const cudaError_t e = allow_smem<embed_sort_small_kernel<IT, BITS>>(smem);
+  constexpr int smem = 1024 * 8 + CL * (1 << BITS) * 4 + 32 * (1 << BITS) * 2;
+  cudaError_t e = allow_smem<embed_sort_kernel<BITS, CL>>(smem);
+  if (CL > 8 && e == cudaSuccess) e = allow_clusters<embed_sort_kernel<BITS, CL>>();
   if (e != cudaSuccess) return e;
-  return launch_operator(embed_sort_small_kernel<IT, BITS>, dim3(1), dim3(1024), smem, s, P, passes, bits, order, keys);
+  if (CL == 1) return launch_operator(embed_sort_kernel<BITS, CL>, dim3(1), dim3(1024), smem, s, P, passes, bits, order, keys);
+  return launch_operator_cluster(embed_sort_kernel<BITS, CL>, CL, dim3(CL), dim3(1024), smem, s, P, passes, bits, order, keys);
 }
 
 template <int IT, int BITS>
@@ -421,8 +460,9 @@ static cudaError_t run_tile_sort(const EmbedParams& P, int passes, int bits, int
 
 template <int BITS>
 static cudaError_t run_sort(const EmbedParams& P, int passes, int bits, int* order, int* keys, void* ws, cudaStream_t s) {
-  if (P.N <= 1024) return run_small_sort<1, BITS>(P, passes, bits, order, keys, s);
-  if (P.N <= kSmallSort) return run_small_sort<4, BITS>(P, passes, bits, order, keys, s);
+  if (P.N <= 1024) return run_small_sort<BITS, 1>(P, passes, bits, order, keys, s);
+  if (P.N <= 8 * 1024) return run_small_sort<BITS, 8>(P, passes, bits, order, keys, s);
+  if (P.N <= kSmallSort) return run_small_sort<BITS, 16>(P, passes, bits, order, keys, s);
   return tile_keys(P.N) == 1024 ? run_tile_sort<4, BITS>(P, passes, bits, order, keys, ws, s)
                                 : run_tile_sort<16, BITS>(P, passes, bits, order, keys, ws, s);
 }

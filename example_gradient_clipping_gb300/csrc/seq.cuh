@@ -179,19 +179,26 @@ struct EmbedParams {
 }  // namespace dpk
 
 namespace dph {
-// Lets `Kernel` have `bytes` of dynamic shared memory on the current device, once for each device (the
-// attribute is the device's); a failure is not remembered.
-template <auto Kernel>
-cudaError_t allow_smem(int bytes) {
+// Sets an attribute of `Kernel` on the current device, once for each device (the attribute is the device's); a
+// failure is not remembered.
+template <auto Kernel, cudaFuncAttribute Attribute>
+cudaError_t allow(int value) {
   static std::atomic<bool> set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const bool kept = dev >= 0 && dev < 64;
   if (kept && set[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = cudaFuncSetAttribute(Kernel, Attribute, value);
   if (kept && e == cudaSuccess) set[dev].store(true, std::memory_order_release);
   return e;
+}
+// Lets `Kernel` have `bytes` of dynamic shared memory, or clusters of more than eight CTAs.
+template <auto Kernel> cudaError_t allow_smem(int bytes) {
+  return allow<Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize>(bytes);
+}
+template <auto Kernel> cudaError_t allow_clusters() {
+  return allow<Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed>(1);
 }
 
 cudaError_t launch_rotary_table(const dp_rotary_table_desc& d, float* table, cudaStream_t s);
