@@ -82,6 +82,8 @@ class PrivacyEngine:
         self._handles = []
         for i, m in enumerate(self.layers):
             if isinstance(m, LayerNorm):
+                if m._sink is not None:
+                    raise ValueError(f"{m}: another engine's (its detach() frees it)")
                 m._sink = self._sink(i)
                 continue
             self._handles.append(m.register_forward_hook(self._fwd_hook(i)))

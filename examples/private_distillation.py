@@ -10,7 +10,12 @@ gradients of the linear layers into the privatised gradient (per-example clippin
 1/B).  The operators have no parameters and never mix examples, so clipping the linear layers
 bounds everything that an example contributes.
 
+With --trained the embedding and the layer norms between the linear layers are trained too (dp.Embedding and
+dp.LayerNorm, clipped per example with them), the teacher's alternatives are taken from its logits by
+dp.token_logprobs, and held-out labels are scored at the end.
+
     python examples/private_distillation.py --steps 20
+    python examples/private_distillation.py --steps 20 --trained
 """
 import argparse
 import os
@@ -24,8 +29,14 @@ import example_gradient_clipping_gb300 as dp  # noqa: E402
 
 
 class Block(nn.Module):
-    def __init__(self, width: int, heads: int, kv_heads: int, head: int):
+    """layers: where LayerNorm comes from (None: norms without parameters)."""
+
+    def __init__(self, width: int, heads: int, kv_heads: int, head: int, layers=None):
         super().__init__()
+        if layers is not None:
+            self.norm1, self.norm2 = layers.LayerNorm(width), layers.LayerNorm(width)
+        else:
+            self.norm1 = self.norm2 = self.norm
         self.heads, self.kv_heads, self.head = heads, kv_heads, head
         self.qkv = nn.Linear(width, (heads + 2 * kv_heads) * head)
         self.out = nn.Linear(heads * head, width)
@@ -38,23 +49,24 @@ class Block(nn.Module):
     def forward(self, x, table, lens, ops):
         B, T, _ = x.shape
         # q, k and v are read from the one projection by their strides
-        qkv = self.qkv(self.norm(x)).view(B, T, self.heads + 2 * self.kv_heads, self.head)
+        qkv = self.qkv(self.norm1(x)).view(B, T, self.heads + 2 * self.kv_heads, self.head)
         q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], dim=2)
         q, k = ops.rotary(q, k, table)
         o = ops.attention(q, k, v, causal=True, q_lens=lens, k_lens=lens)
         x = x + self.out(o.reshape(B, T, -1))
-        return x + self.down(nn.functional.gelu(self.up(self.norm(x))))
+        return x + self.down(nn.functional.gelu(self.up(self.norm2(x))))
 
 
 class Student(nn.Module):
-    """ops: where rotary and attention come from (the package)."""
+    """ops: where rotary and attention come from (the package); trained: where a trained Embedding and
+    LayerNorm do (None: a frozen embedding, norms without parameters)."""
 
-    def __init__(self, vocab: int, width=64, heads=4, kv_heads=2, head=16, layers=2, context=512, ops=dp):
+    def __init__(self, vocab: int, width=64, heads=4, kv_heads=2, head=16, layers=2, context=512, ops=dp, trained=None):
         super().__init__()
         self.ops = ops
-        self.embed = nn.Embedding(vocab, width)
-        self.embed.weight.requires_grad_(False)
-        self.blocks = nn.ModuleList([Block(width, heads, kv_heads, head) for _ in range(layers)])
+        self.embed = (trained or nn).Embedding(vocab, width)
+        self.embed.weight.requires_grad_(trained is not None)
+        self.blocks = nn.ModuleList([Block(width, heads, kv_heads, head, trained) for _ in range(layers)])
         self.lm_head = nn.Linear(width, vocab, bias=False)
         self.context, self.rotated = context, head
         self.table = None
@@ -81,6 +93,12 @@ def synthetic_batch(B, T, vocab, K, seed, device="cuda"):
     return tokens, lens, indices.int(), teacher.contiguous(), first, weights
 
 
+def teacher_logits(indices, values, vocab):
+    """A teacher's whole logits: `values` at its top indices, low elsewhere."""
+    out = torch.full((*indices.shape[:2], vocab), -8.0, device=indices.device)
+    return out.scatter_(2, indices.long(), values)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=20)
@@ -90,14 +108,17 @@ def main(argv=None):
     ap.add_argument("--sigma", type=float, default=0.2)
     ap.add_argument("--clip", type=float, default=1.0)
     ap.add_argument("--lr", type=float, default=2.0)
+    ap.add_argument("--trained", action="store_true", help="train the embedding and the layer norms too")
     a = ap.parse_args(argv)
     torch.manual_seed(0)
-    student = Student(a.vocab).to("cuda", torch.bfloat16)
+    student = Student(a.vocab, trained=dp if a.trained else None).to("cuda", torch.bfloat16)
     engine = dp.PrivacyEngine(student, C=a.clip, sigma=a.sigma)
     opt = torch.optim.SGD([p for p in student.parameters() if p.requires_grad], lr=a.lr)
     losses = []
     for step in range(a.steps):
         tokens, lens, indices, teacher, labels, weights = synthetic_batch(a.batch, a.length, a.vocab, 8, seed=step)
+        if a.trained:
+            _, _, teacher, indices = dp.token_logprobs(teacher_logits(indices, teacher, a.vocab), top=8)
         loss, _ = dp.distill_loss(student(tokens, lens), indices, teacher, labels=labels, weights=weights,
                                   temperature=2.0, alpha=0.2)
         loss.sum().backward()          # the sum: every example's G is its own gradient
@@ -105,6 +126,13 @@ def main(argv=None):
         opt.step()
         losses.append((loss.sum() / weights.sum()).item())
         print(f"step {step:3d}  loss per token {losses[-1]:.4f}")
+    if a.trained:
+        tokens, lens, _, _, labels, weights = synthetic_batch(a.batch, a.length, a.vocab, 8, seed=a.steps)
+        with torch.no_grad():
+            logprob, entropy, _, best = dp.token_logprobs(student(tokens, lens), labels, top=1)
+        n = weights.sum()
+        print(f"held out: log probability {(logprob * weights).sum() / n:.4f}, entropy {(entropy * weights).sum() / n:.4f}, "
+              f"first choice {((best[..., 0] == labels) * weights).sum() / n:.4f}")
     if dp.dp_check_status() != dp.DP_OK:
         raise SystemExit("a device-side condition was raised")
     return losses

@@ -10,8 +10,9 @@
  * asynchronous on `stream`, arguments validated on the host before anything is launched, a
  * message in dp_last_error().  Every result is deterministic (the same call on the same inputs
  * gives the same bits), and no example's values enter another's outputs.  (The bits of an
- * example's attention gradient may differ between batch sizes: how many partial sums a key or
- * query tile is split into, each added in order, follows from the whole call's shape.)  Inputs are DP_BF16 or
+ * example's attention gradient, layer norm gradient and embedding norm may differ with the batch that it
+ * stands in: how many partial sums they are split into, each added in order, follows from the whole call's
+ * shape, and for embeddings from its tokens.)  Inputs are DP_BF16 or
  * DP_FP32; sums, maxima and softmax statistics are fp32; an output of type bf16 is rounded
  * once, from fp32.
  *
@@ -212,7 +213,8 @@ dp_status dp_layer_norm_grad(const dp_layer_norm_desc* desc, const void* dY, con
 
 /* ---- Per-example gradients that the caller has -----------------------------------------
  * grads: device fp32 [B, n], one row an example (as dp_layer_norm_grad writes them).
- *   sqnorms[i] = sum_j grads[i, j]^2,   out[j] (+)= sum_i factors[i] grads[i, j]. */
+ *   sqnorms[i] = sum_j grads[i, j]^2,   out[j] (+)= sum_i factors[i] grads[i, j].
+ * A row of a non-finite gradient spoils `out` also with a factor of 0. */
 dp_status dp_example_sqnorms(const float* grads, int B, size_t n, float* sqnorms, cudaStream_t stream);
 dp_status dp_example_sum(const float* grads, int B, size_t n, const float* factors, float* out, int accumulate,
                          cudaStream_t stream);
@@ -223,7 +225,8 @@ dp_status dp_example_sum(const float* grads, int B, size_t n, const float* facto
  * and from them sqnorms[i] = sum_v |dw_{i,v}|^2 and dw_v = sum_i factors[i] dw_{i,v}.
  * The rows of the padding token have no gradient (its own row of w is looked up as any other).
  * A token outside [0, V) sets the device status DP_ERR_INVALID_ARG; its y is NaN and it has no
- * gradient.  The gradients go by the tokens sorted once (dp_embedding_order): equal tokens stand
+ * gradient.  An example whose dY holds inf or NaN spoils dw_v for its tokens v, also with a factor of 0
+ * (0 times it is NaN), as in dp_clipped_sum.  The gradients go by the tokens sorted once (dp_embedding_order): equal tokens stand
  * together in the order of their positions, so every sum has one order. */
 typedef struct {
   int dtype;               /* dp_dtype of W and Y, or of dY */

@@ -216,6 +216,8 @@ def test_engine_takes_the_packages_layers_alone():
     assert len(engine.layers) == 3 and model[1]._sink is not None
     with pytest.raises(RuntimeError, match="backward"):
         engine.privatise(0)
+    with pytest.raises(ValueError, match="another engine"):
+        dp.PrivacyEngine(model)
     engine.detach()
     assert model[1]._sink is None
     dp.PrivacyEngine(nn.Sequential(nn.Linear(4, 4), dp.LayerNorm(4, elementwise_affine=False))).detach()

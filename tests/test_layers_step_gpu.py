@@ -215,3 +215,54 @@ def test_teacher_alternatives_feed_distillation(lib):
     assert (dz.double() - (q.exp() - p.exp())).abs().max() <= 200 * 2.0 ** -24
     same, _ = lib.distill_loss_and_grad(t, at, top)
     assert same.abs().max() <= 7 * 200 * 2.0 ** -24 * 16
+
+
+@pytest.fixture()
+def example(lib):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import private_distillation
+    return private_distillation
+
+
+def test_example_with_trained_layers(lib, example):
+    """The example's student with its embedding and layer norms trained: the privatised gradient is the per-example
+    loop's, and its loop runs."""
+    from test_sequence_example import _Plain
+    torch.backends.cuda.matmul.allow_tf32 = False
+    b, t, v, C = 4, 11, 30, 0.9
+    torch.manual_seed(3)
+    kw = dict(width=32, heads=4, kv_heads=2, head=8, context=32)
+    student = example.Student(v, trained=lib, **kw).cuda()
+    plain = example.Student(v, trained=nn, ops=_Plain, **kw).cuda().double()
+    plain.load_state_dict({k: p.double() for k, p in student.state_dict().items()})
+    tokens, lens, idx, teacher, labels, w = example.synthetic_batch(b, t, v, 6, seed=4)
+    _, _, top, at = lib.token_logprobs(example.teacher_logits(idx, teacher, v), top=6)
+    engine = lib.PrivacyEngine(student, C=C, sigma=0.0)
+    loss, _ = lib.distill_loss(student(tokens, lens), at, top, labels=labels, weights=w, temperature=2.0, alpha=0.3)
+    loss.sum().backward()
+    flat = engine.privatise(seed=0).cpu().numpy()
+    engine.detach()
+    assert len(engine.layers) == 1 + 2 * 6 + 1
+    find = dict(student.named_modules())
+    names = {id(m): n for n, m in find.items()}
+    mirror = [dict(plain.named_modules())[names[id(m)]] for m in engine.layers]
+    want, sizes = 0.0, []
+    for i in range(b):
+        plain.zero_grad()
+        z = plain(tokens[i:i + 1], lens[i:i + 1])[0]
+        logq, logp = torch.log_softmax(z / 2.0, -1), torch.log_softmax(z, -1)
+        p = torch.softmax(top[i].double() / 2.0, -1)
+        kl = (p * (torch.log(p) - torch.gather(logq, 1, at[i].long()))).sum(-1)
+        ((0.7 * 4.0 * kl - 0.3 * logp[torch.arange(t), labels[i]]) * w[i]).sum().backward()
+        parts = [q.grad.flatten() for m in mirror for q in (m.weight, getattr(m, "bias", None)) if q is not None]
+        sizes = [q.numel() for q in parts]
+        g = torch.cat(parts).cpu().numpy()
+        want = want + g * min(1.0, C / np.linalg.norm(g)) / b
+    o = 0
+    for n in sizes:   # fp32 layers and operators through two blocks: about fourteen of 1e-5 follow one another
+        assert rel_rows(flat[o:o + n], want[o:o + n]) <= 2e-4, n
+        o += n
+    losses = example.main(["--steps", "2", "--trained", "--batch", "8", "--length", "16"])
+    assert all(np.isfinite(losses)) and lib.dp_check_status() == lib.DP_OK
