@@ -471,14 +471,20 @@ __global__ void __launch_bounds__(NT, (kAlt ? 5 : 4) * 256 / NT) token_logprobs_
     for (int i = tid; i < kTop; i += NT) sh.best[i] = 0;   // below every key, past the part's own
   }
   __syncthreads();
-  // the part's, in the first warp (the others need it only behind the barriers of part_top)
-  if (tid < 32) {
-    Sums w = sh.warp[lane < kWarps ? lane : 0];
-    m = w.m;
+  m = sh.warp[0].m;
 #pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, o));
-    m = __shfl_sync(kAll, m, 0);
-    w = moved(w, m, c2);
+  for (int w = 1; w < kWarps; ++w) m = max_nan(m, sh.warp[w].m);
+  if (fabsf(m) < INFINITY && !(fabsf(m) * c2 < kFar)) {   // (the same for every thread)
+    float a, b;
+    far_sums(g, m, c2, &a, &b);
+    a = warp_sum(a);
+    b = warp_sum(b);
+    __syncthreads();
+    if (lane == 0) sh.warp[tid / 32] = {m, a, b};
+    __syncthreads();
+  }
+  if (tid < 32) {   // the part's; the other warps see it behind the barriers of part_top
+    Sums w = moved(sh.warp[lane < kWarps ? lane : 0], m, c2);
     if (m == -INFINITY) w.sum = w.sumx = 0.f;
 #pragma unroll
     for (int o = kWarps / 2; o > 0; o >>= 1) {
@@ -486,24 +492,7 @@ __global__ void __launch_bounds__(NT, (kAlt ? 5 : 4) * 256 / NT) token_logprobs_
       w.sumx += __shfl_xor_sync(kAll, w.sumx, o);
     }
     if (lane == 0) sh.whole = w;
-  }
-  __syncthreads();
-  if (fabsf(sh.whole.m) < INFINITY && !(fabsf(sh.whole.m) * c2 < kFar)) {   // (the same for every thread)
-    float a, b;
-    far_sums(g, sh.whole.m, c2, &a, &b);
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if (lane == 0) sh.warp[tid / 32] = {sh.whole.m, a, b};
-    __syncthreads();
-    if (tid == 0) {
-      Sums w = sh.warp[0];
-      for (int i = 1; i < kWarps; ++i) {
-        w.sum += sh.warp[i].sum;
-        w.sumx += sh.warp[i].sumx;
-      }
-      sh.whole = w;
-    }
-    __syncthreads();
+    __syncwarp();
   }
   int have = 0;   // alternatives of this part
   if constexpr (kAlt) {
