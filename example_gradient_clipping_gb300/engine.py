@@ -79,11 +79,13 @@ class PrivacyEngine:
             raise ValueError("the model has no trainable layer that is clipped here")
         self._acts: List = [None] * len(self.layers)
         self._grads: List = [None] * len(self.layers)
+        self._tasks = [-1] * len(self.layers)   # the backward pass that last reached an embedding or a layer norm
         self._handles = []
+        for m in self.layers:
+            if isinstance(m, LayerNorm) and m._sink is not None:
+                raise ValueError(f"{m}: another engine's (its detach() frees it)")
         for i, m in enumerate(self.layers):
             if isinstance(m, LayerNorm):
-                if m._sink is not None:
-                    raise ValueError(f"{m}: another engine's (its detach() frees it)")
                 m._sink = self._sink(i)
                 continue
             self._handles.append(m.register_forward_hook(self._fwd_hook(i)))
@@ -106,13 +108,24 @@ class PrivacyEngine:
 
     def _bwd_hook(self, i):
         def hook(module, grad_output):       # the gradient of the loss w.r.t. the layer output
+            if isinstance(module, Embedding):
+                self._once(i)
             self._grads[i] = grad_output[0].detach()
         return hook
 
     def _sink(self, i):
         def sink(each):                      # a layer norm's per-example gradients
+            self._once(i)
             self._acts[i] = each
         return sink
+
+    def _once(self, i) -> None:
+        """Raises where one backward pass reaches layer i again: the first call's gradient would be lost."""
+        import torch
+        task = torch._C._current_graph_task_id()
+        if task == self._tasks[i]:
+            raise RuntimeError(f"{self.layers[i]}: called more than once in a step, which is not clipped here")
+        self._tasks[i] = task
 
     def detach(self) -> None:
         """Remove the hooks."""

@@ -266,3 +266,32 @@ def test_example_with_trained_layers(lib, example):
         o += n
     losses = example.main(["--steps", "2", "--trained", "--batch", "8", "--length", "16"])
     assert all(np.isfinite(losses)) and lib.dp_check_status() == lib.DP_OK
+
+
+@pytest.mark.parametrize("which", ["embed", "norm1"])
+def test_engine_refuses_a_layer_called_twice(lib, which):
+    model = _Model(lib.Embedding, lib.LayerNorm).cuda()
+    engine = lib.PrivacyEngine(model)
+    tokens = torch.randint(0, V, (B, T), device="cuda")
+
+    def twice():
+        z = model(tokens)
+        again = model.embed(tokens.flip(1)) if which == "embed" else model.norm1(model.embed.weight.detach()[tokens])
+        return z.sum() + again.sum()
+    with pytest.raises(RuntimeError, match="more than once"):
+        twice().backward()
+    for _ in range(2):   # passes that were not privatised do not count
+        model(tokens).sum().backward()
+    engine.privatise(0)
+    with pytest.raises(RuntimeError, match="first"):
+        engine.privatise(0)
+
+
+def test_engine_that_is_refused_leaves_nothing_behind(lib):
+    model = _Model(lib.Embedding, lib.LayerNorm).cuda()
+    model.norm2._sink = lambda each: None   # another engine's
+    with pytest.raises(ValueError, match="another engine"):
+        lib.PrivacyEngine(model)
+    assert model.norm1._sink is None and not model.embed._forward_hooks and not model.up._forward_hooks
+    model.norm2._sink = None
+    lib.PrivacyEngine(model).detach()
