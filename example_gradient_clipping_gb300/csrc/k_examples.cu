@@ -5,6 +5,7 @@
 #include <algorithm>
 
 #include "seq.cuh"
+#include "tc_ptx.cuh"
 
 namespace dpk {
 
@@ -77,12 +78,39 @@ __global__ void __launch_bounds__(256) rows_sum_few_kernel(const float* __restri
   }
 }
 
-__global__ void __launch_bounds__(256) rows_sqnorm_kernel(const float* __restrict__ rows, size_t n, float* __restrict__ out) {
+// A row is one CTA's, or (few long rows) a cluster's: the row on the grid of 16-byte vectors, `per` of them a CTA, four
+// loads in flight a thread, and the CTAs' sums added in order by the first.
+__global__ void __launch_bounds__(256) rows_sqnorm_kernel(const float* __restrict__ rows, size_t n, float* __restrict__ out,
+                                                          int log_cluster, size_t per) {
   pdl_wait();
-  __shared__ float red[8];
-  const float* r = rows + (size_t)blockIdx.x * n;
+  __shared__ float red[8], peer[8];
+  const int cluster = 1 << log_cluster;
+  if (cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // that all have begun
+  const unsigned row = blockIdx.x >> log_cluster, rank = blockIdx.x & (unsigned)(cluster - 1);
+  const float* r = rows + (size_t)row * n;
+  const size_t mis = reinterpret_cast<uintptr_t>(r) / 4 % 4, nvec = (n + mis + 3) / 4;
+  const size_t j0 = min(nvec, rank * per), j1 = min(nvec, j0 + per);
   float acc = 0.f;
-  for (size_t i = threadIdx.x; i < n; i += 256) acc = fmaf(r[i], r[i], acc);
+  for (size_t j = j0 + threadIdx.x; j < j1; j += 4 * 256) {
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const size_t at = j + k * 256;
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (at >= j1) continue;
+      const float* q = r + (long long)(4 * at - mis);   // (of the first vector `mis` entries lie before the row)
+      if (4 * at >= mis && 4 * at + 4 <= n + mis) {
+        v[k] = *reinterpret_cast<const float4*>(q);
+      } else {
+        if (4 * at >= mis) v[k].x = q[0];   // (at < nvec: one entry at least is in the row)
+        if (4 * at + 1 >= mis && 4 * at + 1 < n + mis) v[k].y = q[1];
+        if (4 * at + 2 >= mis && 4 * at + 2 < n + mis) v[k].z = q[2];
+        if (4 * at + 3 >= mis && 4 * at + 3 < n + mis) v[k].w = q[3];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc = fmaf(v[k].x, v[k].x, fmaf(v[k].y, v[k].y, fmaf(v[k].z, v[k].z, fmaf(v[k].w, v[k].w, acc))));
+  }
   acc = warp_sum(acc);
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = acc;
   __syncthreads();
@@ -90,8 +118,19 @@ __global__ void __launch_bounds__(256) rows_sqnorm_kernel(const float* __restric
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int w = 1; w < 8; ++w) acc += red[w];
-    out[blockIdx.x] = acc;
   }
+  if (cluster > 1) {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (threadIdx.x == 0)
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ptx::map_rank(ptx::smem_u32(&peer[rank]), 0)), "f"(acc) : "memory");
+    __syncwarp();
+    ptx::cluster_sync();
+    if (threadIdx.x == 0 && rank == 0) {
+      acc = peer[0];
+      for (int c = 1; c < cluster; ++c) acc += peer[c];
+    }
+  }
+  if (threadIdx.x == 0 && rank == 0) out[row] = acc;
 }
 
 }  // namespace dpk
@@ -122,7 +161,14 @@ cudaError_t launch_rows_sum(const float* rows, int segments, int count, size_t n
 }
 
 cudaError_t launch_rows_sqnorm(const float* rows, int B, size_t n, float* out, cudaStream_t s) {
-  return launch_operator(rows_sqnorm_kernel, dim3((unsigned)B), dim3(256), 0, s, rows, n, out);
+  const size_t nvec = n / 4 + 2;   // at any alignment of the row
+  // Eight CTAs a row of 16384 entries and more while the rows alone leave SMs without one (16 rows of 100001: 3.3 us,
+  // 10.2 on one CTA; of 20000: 2.2, 3.0; 100 of 40000: 3.9, 5.0); up to two rows an SM only long ones, where the
+  // SMs with one row wait for those with two (256 of 200000: 32.6 us, 43; but 300 of 40000: 7.5, 5.5).
+  const bool split = B <= 152 ? nvec >= 4096 : B <= 304 && nvec >= 32768;
+  const size_t per = split ? (nvec + 7) / 8 : nvec;
+  if (!split) return launch_operator(rows_sqnorm_kernel, dim3((unsigned)B), dim3(256), 0, s, rows, n, out, 0, per);
+  return launch_operator_cluster(rows_sqnorm_kernel, 8, dim3((unsigned)B * 8), dim3(256), 0, s, rows, n, out, 3, per);
 }
 
 }  // namespace dph

@@ -122,10 +122,11 @@ __global__ void __launch_bounds__(grad_threads(G)) layer_norm_grad_kernel(NormPa
     uint64_t sum = 0, sumh = 0;
 #pragma unroll
     for (int i = 0; i < C / 2; ++i) {   // past D: w = dy = 0
-      const uint64_t d = pairs(vg, i), h = mul2(add2(pairs(vx, i), nmu2), rs2), u = mul2(w[i], d);
+      // (the sum of u h takes its rs at the end: past D h = -mu rs, which need not be finite)
+      const uint64_t d = pairs(vg, i), xm = add2(pairs(vx, i), nmu2), u = mul2(w[i], d);
       sum = add2(sum, u);
-      sumh = fma2(u, h, sumh);
-      dw[i] = fma2(d, h, dw[i]);
+      sumh = fma2(u, xm, sumh);
+      dw[i] = fma2(d, mul2(xm, rs2), dw[i]);
       db[i] = add2(db[i], d);
     }
     if (P.dX) {
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(grad_threads(G)) layer_norm_grad_kernel(NormPa
       float s[2] = {s0.x + s0.y, s1.x + s1.y};
       row_sum<G, 2, kAlone>(s, red, round);
       if constexpr (S > 0) asm volatile("" ::: "memory");   // the row is read again, and not held over the sums
-      const float a = s[0] * inv, b = s[1] * inv;
+      const float a = s[0] * inv, b = s[1] * inv * rs;
       const uint64_t na = pair(-a, -a), nb = pair(-b, -b);
       E* o = static_cast<E*>(P.dX) + (size_t)r * P.D;
       auto out = [&](int i) {

@@ -96,6 +96,41 @@ def test_layer_norm_without_parameters_large_means_and_eps(lib):
     assert torch.equal(y, torch.zeros_like(y))
 
 
+@pytest.mark.parametrize("dtype,D", [("fp32", 1000), ("fp32", 1001), ("bf16", 1000), ("bf16", 250)])
+def test_layer_norm_gradient_where_mean_times_rstd_overflows(lib, dtype, D):
+    """Constant rows of 2^116 with rstd 2^20: h = 0, so dx = rs (u - mean u) and dw = 0 exactly."""
+    import torch
+    _, w, _, dy = _norm_inputs(2, 3, D, dtype, dtype)
+    x = torch.full((2, 3, D), 2.0 ** 116, device="cuda").to(dy.dtype)
+    mean = torch.full((2, 3), 2.0 ** 116, device="cuda")
+    rstd = torch.full((2, 3), 2.0 ** 20, device="cuda")
+    dx, dw, db = lib.layer_norm_backward(dy, x, w, mean, rstd)
+    u = dy.double() * w.double()
+    want = 2.0 ** 20 * (u - u.mean(-1, keepdim=True))
+    # u and its mean: a product, a sum of D terms in chains of at most 64 with a tree of 10, 1 / D, two roundings
+    # behind it; then the type's own
+    err = 2.0 ** 20 * 80 * 2.0 ** -24 * u.abs().amax() + want.abs() * _r(dtype)
+    assert ((dx.double() - want).abs() <= err).all()
+    assert not dw.any()
+    total = dy.double().sum((0, 1))
+    assert ((db.double() - total).abs() <= 6 * 2.0 ** -24 * dy.double().abs().sum((0, 1)) + total.abs() * _r(dtype)).all()
+
+
+@pytest.mark.parametrize("B,n", [(1, 1), (5, 3), (16, 2002), (3, 40001), (3, 200003), (304, 33000), (305, 33000)])
+def test_example_sqnorms(lib, B, n):
+    """Rows at any alignment, neighbours not read.  Positive terms: each thread's chain of at most n / 256 + 16
+    roundings and the trees behind it bound the relative error."""
+    import torch
+    for off in (4, 5, 7):
+        flat = torch.full((B * n + 16,), float("nan"), device="cuda")
+        rows = flat[off:off + B * n].view(B, n)
+        rows.copy_(torch.randn(B, n, device="cuda"))
+        out = torch.empty(B, device="cuda")
+        lib.dp_example_sqnorms(rows, B, n, out)
+        want = rows.double().square().sum(1)
+        assert ((out.double() - want).abs() <= want * (n / 256 + 48) * 2.0 ** -24).all()
+
+
 def test_layer_norm_shapes_strides_and_bits(lib):
     import torch
     for dtype in ("fp32", "bf16"):
