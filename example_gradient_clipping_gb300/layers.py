@@ -258,7 +258,10 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, per_exampl
     if x.dim() != 3:
         x, dy = _rows3(x, "x"), _rows3(dy, "dy")
     dev = x.get_device()
-    mean, rstd = (m if m.dim() == 2 else m.view(x.shape[:2]) for m in (mean, rstd))
+    if mean.dim() != 2:
+        mean = mean.view(x.shape[:2])
+    if rstd.dim() != 2:
+        rstd = rstd.view(x.shape[:2])
     key = ("layer_norm_backward", x.shape, x.stride(), x.dtype, dev, dy.shape, dy.stride(), dy.dtype, dy.get_device(),
            _opt(weight), _opt(mean), _opt(rstd), bias, per_example)
     d = _get(key) or _keep(key, _norm_desc(x, weight, None, 0.0, dy, mean, rstd, bias, per_example))
@@ -282,7 +285,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, per_exampl
         return gx, grads
     if not params:
         return gx, None, None
-    return (gx, *grads.unbind(0)) if bias else (gx, grads[0], None)
+    return gx, grads[0], grads[1] if bias else None   # (unbind costs the host three microseconds more)
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -390,10 +393,13 @@ def _grad_desc(tokens, dy, V, scale, padding, factors, dtype):
     return dy, _get(key) or _keep(key, _embedding_desc(tokens, None, dy, V, scale, padding, factors, dtype))
 
 
-def _sorted(d, tokens, ws):
-    order = _empty(d.order_bytes, dtype=torch.uint8, device=tokens.device)
-    _call(_seq._lib.dp_embedding_order, tokens.get_device(), d, tokens.data_ptr(), order.data_ptr(), ws.data_ptr(), d.ws_bytes)
-    return order
+def _sorted(d, tokens):
+    """The tokens' order and a workspace as one array (order first), and the addresses of the two."""
+    both = _empty(d.order_bytes + d.ws_bytes, dtype=torch.uint8, device=tokens.device)
+    order = both.data_ptr()
+    ws = order + d.order_bytes   # (a multiple of 16)
+    _call(_seq._lib.dp_embedding_order, tokens.get_device(), d, tokens.data_ptr(), order, ws, d.ws_bytes)
+    return both, order, ws
 
 
 def embedding_backward(tokens, dy, V: int, scale: float = 1.0, padding: Optional[int] = None, factors=None,
@@ -408,10 +414,9 @@ def embedding_backward(tokens, dy, V: int, scale: float = 1.0, padding: Optional
     dw = _empty((d.V, d.D), dtype=dtype, device=tokens.device)
     if not d.B * d.T:
         return dw.zero_()
-    ws = _empty(d.ws_bytes, dtype=torch.uint8, device=tokens.device)
-    order = _sorted(d, tokens, ws)
-    _call(_seq._lib.dp_embedding_grad, tokens.get_device(), d, order.data_ptr(), dy.data_ptr(),
-          None if factors is None else factors.data_ptr(), dw.data_ptr(), 0, ws.data_ptr(), d.ws_bytes)
+    both, order, ws = _sorted(d, tokens)
+    _call(_seq._lib.dp_embedding_grad, tokens.get_device(), d, order, dy.data_ptr(),
+          None if factors is None else factors.data_ptr(), dw.data_ptr(), 0, ws, d.ws_bytes)
     return dw
 
 
@@ -425,10 +430,8 @@ def embedding_sqnorms(tokens, dy, V: int, scale: float = 1.0, padding: Optional[
     sq = _empty(d.B, dtype=_f32, device=tokens.device)
     if not d.B * d.T:
         return sq.zero_()
-    ws = _empty(d.ws_bytes, dtype=torch.uint8, device=tokens.device)
-    order = _sorted(d, tokens, ws)
-    _call(_seq._lib.dp_embedding_sqnorms, tokens.get_device(), d, order.data_ptr(), dy.data_ptr(), sq.data_ptr(),
-          ws.data_ptr(), d.ws_bytes)
+    both, order, ws = _sorted(d, tokens)
+    _call(_seq._lib.dp_embedding_sqnorms, tokens.get_device(), d, order, dy.data_ptr(), sq.data_ptr(), ws, d.ws_bytes)
     return sq
 
 
