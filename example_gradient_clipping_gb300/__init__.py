@@ -298,7 +298,7 @@ from .sequence import (DP_ROTARY_BASE, DP_ROTARY_LINEAR, DP_ROTARY_PARTS, DP_ROT
                        attention_forward, distill_loss, distill_loss_and_grad, dp_attention, dp_attention_grad,
                        dp_attention_grad_workspace, dp_distill, dp_rotary, dp_rotary_table, rotary, rotary_table)
 from .layers import (Embedding, EmbeddingDesc, KeptDesc, LayerNorm, LayerNormDesc, LogprobsDesc,  # noqa: E402,F401
-                     RowStrides, dp_embedding, dp_embedding_grad, dp_embedding_order, dp_embedding_order_size,
+                     RowStrides, dp_embedding, dp_embedding_grad, dp_embedding_order, dp_embedding_order_grad, dp_embedding_order_size,
                      dp_embedding_sqnorms, dp_embedding_workspace, dp_example_sqnorms, dp_example_sum, dp_layer_norm,
                      dp_layer_norm_grad, dp_layer_norm_grad_workspace, dp_token_logprobs, dp_token_logprobs_grad,
                      embedding, embedding_backward, embedding_desc, embedding_sqnorms, kept_desc, layer_norm,

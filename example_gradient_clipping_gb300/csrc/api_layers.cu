@@ -220,7 +220,7 @@ dp_status dp_embedding_order(const dp_embedding_desc* d, const void* tokens, voi
   P.tokens = tokens;
   char* o = static_cast<char*>(order);
   return launched(dph::launch_embed_order(P, reinterpret_cast<int*>(o), reinterpret_cast<int*>(o + embed_keys_at(P)),
-                                          workspace, stream), "dp_embedding_order");
+                                          workspace, 0, stream), "dp_embedding_order");
 }
 
 static dp_status embed_sums(const dp_embedding_desc* d, const void* order, const void* dY, const void* out,
@@ -256,6 +256,24 @@ dp_status dp_embedding_grad(const dp_embedding_desc* d, const void* order, const
   if (accumulate && d->out_dtype != DP_FP32) return bad(DP_ERR_INVALID_ARG, "accumulate needs an fp32 dW");
   P.factors = factors; P.dW = dW; P.accumulate = accumulate ? 1 : 0;
   return launched(dph::launch_embed_grad(P, d->dtype, d->out_dtype, stream), "dp_embedding_grad");
+}
+
+dp_status dp_embedding_order_grad(const dp_embedding_desc* d, const void* tokens, void* order, const void* dY,
+                                  const float* factors, void* dW, int accumulate, void* workspace, size_t ws_bytes,
+                                  cudaStream_t stream) {
+  dpk::EmbedParams P;
+  const dp_status st = embed_sums(d, order, dY, dW, "dW", workspace, ws_bytes, &P);
+  if (st != DP_OK) return st;
+  if (!tokens) return bad(DP_ERR_INVALID_ARG, "tokens must be non-NULL");
+  if (accumulate && d->out_dtype != DP_FP32) return bad(DP_ERR_INVALID_ARG, "accumulate needs an fp32 dW");
+  if (!P.status) return bad(DP_ERR_CUDA, "cannot resolve the device status word");
+  P.tokens = tokens; P.factors = factors; P.dW = dW; P.accumulate = accumulate ? 1 : 0;
+  const size_t all = (size_t)P.V * P.D * (d->out_dtype == DP_BF16 ? 2 : 4);
+  P.cleared = !P.accumulate && dph::embed_order_clears(P.N, all);
+  const size_t bytes = P.cleared ? all : 0;
+  cudaError_t e = dph::launch_embed_order(P, const_cast<int*>(P.order), const_cast<int*>(P.keys), workspace, bytes, stream);
+  if (e == cudaSuccess) e = dph::launch_embed_grad(P, d->dtype, d->out_dtype, stream);
+  return launched(e, "dp_embedding_order_grad");
 }
 
 }  // extern "C"

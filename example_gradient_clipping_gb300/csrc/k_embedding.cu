@@ -123,11 +123,32 @@ __device__ __forceinline__ unsigned block_exclusive(unsigned v, unsigned* red) {
 
 constexpr int kDigit = 9;   // bits of the widest digit
 
+// Zeros over `bytes` bytes (of 2-byte elements at least) by `ctas` CTAs of 1024 threads.
+__device__ __forceinline__ void clear_bytes(void* p, size_t bytes, unsigned cta, unsigned ctas) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), e = a + bytes;
+  const uintptr_t a16 = min((a + 15) & ~(uintptr_t)15, e), e16 = max(e & ~(uintptr_t)15, a16);
+  if (cta == 0 && threadIdx.x < 16) {   // at most seven elements on either side
+    const uintptr_t at = threadIdx.x < 8 ? a + 2 * threadIdx.x : e16 + 2 * (threadIdx.x - 8);
+    if (at < (threadIdx.x < 8 ? a16 : e)) *reinterpret_cast<unsigned short*>(at) = 0;
+  }
+  uint4* v = reinterpret_cast<uint4*>(a16);
+  const size_t n = (e16 - a16) / 16, step = (size_t)ctas * 1024;
+#pragma unroll 4
+  for (size_t i = (size_t)cta * 1024 + threadIdx.x; i < n; i += step) v[i] = make_uint4(0, 0, 0, 0);
+}
+
 // Up to 1024 tokens a CTA of a cluster of CL, one a thread, all passes in shared memory: a pass counts its digits, tells every
-// CTA how many of each it has, and writes its keys to their places, which may be another CTA's.
+// CTA how many of each it has, and writes its keys to their places, which may be another CTA's.  The clusters behind
+// the first clear P.dW meanwhile.
 template <int BITS, int CL>
-__global__ void __launch_bounds__(1024) embed_sort_kernel(EmbedParams P, int passes, int bits, int* order, int* keys) {
+__global__ void __launch_bounds__(1024) embed_sort_kernel(EmbedParams P, int passes, int bits, int* order, int* keys,
+                                                          size_t bytes) {
   pdl_wait();
+  if (blockIdx.x >= CL) {
+    pdl_trigger();
+    clear_bytes(P.dW, bytes, blockIdx.x - CL, gridDim.x - CL);
+    return;
+  }
   if constexpr (CL > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // that all have begun
   constexpr int kBins = 1 << BITS, M = 1024, IT = 1;
   extern __shared__ unsigned sm[];
@@ -417,13 +438,17 @@ size_t embed_order_ws_bytes(int N, int V) {
 }
 
 template <int BITS, int CL>
-static cudaError_t run_small_sort(const EmbedParams& P, int passes, int bits, int* order, int* keys, cudaStream_t s) {
+static cudaError_t run_small_sort(const EmbedParams& P, int passes, int bits, int* order, int* keys, size_t bytes,
+                                  cudaStream_t s) {
   constexpr int smem = 1024 * 8 + CL * (1 << BITS) * 4 + 32 * (1 << BITS) * 2;
   cudaError_t e = allow_smem<embed_sort_kernel<BITS, CL>>(smem);
   if (CL > 8 && e == cudaSuccess) e = allow_clusters<embed_sort_kernel<BITS, CL>>();
   if (e != cudaSuccess) return e;
-  if (CL == 1) return launch_operator(embed_sort_kernel<BITS, CL>, dim3(1), dim3(1024), smem, s, P, passes, bits, order, keys);
-  return launch_operator_cluster(embed_sort_kernel<BITS, CL>, CL, dim3(CL), dim3(1024), smem, s, P, passes, bits, order, keys);
+  // 64 KB a CTA that clears, and two of them an SM
+  const int clear = (int)std::min<size_t>((bytes + 65535) / 65536, 2 * 152);
+  const dim3 grid((unsigned)(CL + (clear + CL - 1) / CL * CL));
+  if (CL == 1) return launch_operator(embed_sort_kernel<BITS, CL>, grid, dim3(1024), smem, s, P, passes, bits, order, keys, bytes);
+  return launch_operator_cluster(embed_sort_kernel<BITS, CL>, CL, grid, dim3(1024), smem, s, P, passes, bits, order, keys, bytes);
 }
 
 template <int IT, int BITS>
@@ -459,18 +484,23 @@ static cudaError_t run_tile_sort(const EmbedParams& P, int passes, int bits, int
 }
 
 template <int BITS>
-static cudaError_t run_sort(const EmbedParams& P, int passes, int bits, int* order, int* keys, void* ws, cudaStream_t s) {
-  if (P.N <= 1024) return run_small_sort<BITS, 1>(P, passes, bits, order, keys, s);
-  if (P.N <= 8 * 1024) return run_small_sort<BITS, 8>(P, passes, bits, order, keys, s);
-  if (P.N <= kSmallSort) return run_small_sort<BITS, 16>(P, passes, bits, order, keys, s);
+static cudaError_t run_sort(const EmbedParams& P, int passes, int bits, int* order, int* keys, void* ws, size_t bytes,
+                            cudaStream_t s) {
+  if (P.N <= 1024) return run_small_sort<BITS, 1>(P, passes, bits, order, keys, bytes, s);
+  if (P.N <= 8 * 1024) return run_small_sort<BITS, 8>(P, passes, bits, order, keys, bytes, s);
+  if (P.N <= kSmallSort) return run_small_sort<BITS, 16>(P, passes, bits, order, keys, bytes, s);
   return tile_keys(P.N) == 1024 ? run_tile_sort<4, BITS>(P, passes, bits, order, keys, ws, s)
                                 : run_tile_sort<16, BITS>(P, passes, bits, order, keys, ws, s);
 }
 
-cudaError_t launch_embed_order(const EmbedParams& P, int* order, int* keys, void* ws, cudaStream_t s) {
+// Beside a sort by one cluster the other SMs have nothing to do: 16384 tokens and 50257 x 768 bf16, sorted and summed,
+// 32.4 us (34.5 where the sum writes the zeros), 8192 and 32000 x 512 fp32 25.5 (28.7).  What takes much longer
+// than the sort is left to the sum, which then reads beside it: 4000 and 128000 x 1024 bf16 52.7 (55.4 cleared).
+bool embed_order_clears(int N, size_t bytes) { return N <= kSmallSort && bytes <= (size_t)128 << 20; }
+cudaError_t launch_embed_order(const EmbedParams& P, int* order, int* keys, void* ws, size_t bytes, cudaStream_t s) {
   int passes, bits;
   digits(P.V, &passes, &bits);
-  return bits <= 8 ? run_sort<8>(P, passes, bits, order, keys, ws, s) : run_sort<9>(P, passes, bits, order, keys, ws, s);
+  return bits <= 8 ? run_sort<8>(P, passes, bits, order, keys, ws, bytes, s) : run_sort<9>(P, passes, bits, order, keys, ws, bytes, s);
 }
 
 }  // namespace dph

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256) embed_runs_kernel(EmbedParams P, int U) {
   if (gw >= work) {
     if constexpr (!kNorm) {   // kTokens tokens a warp: those without a row get zeros
       const long long first = (gw - work) * kTokens;
-      if (first >= P.V || P.accumulate) return;
+      if (first >= P.V || P.accumulate || P.cleared) return;
       const int v0 = (int)first, v1 = min(P.V, v0 + kTokens), j0 = lower_bound<false>(P, 0, P.N, v0, 0);
       unsigned there = 0;
       for (int j = j0, rounds = 0;; j += 32) {
@@ -346,14 +346,20 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P, int U, i
   // the run that begins in unit u0 + b: its partial rows are the first (of the unit's tail or the whole unit)
   // and those of every unit behind it that it reaches
   auto length = [&](int b, const Place& run) {
-    const int from = u0 + b + 1, v = from + lane;
-    const unsigned next = v < P.units ? P.info[v] : 0;
-    const unsigned mask = __ballot_sync(kAll, (next & (kCovered | kBegins)) == kCovered);
-    if (mask != kAll) {   // it ends in the first unit that it does not cover, or before it
-      const int m = __ffs(~mask) - 1;
-      return 1 + m + (__shfl_sync(kAll, next, m) & kHeadEnds ? 1 : 0);
+    constexpr int kAhead = 4;   // 32 units each, all asked for at once
+    const int from = u0 + b + 1;
+    unsigned next[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) next[i] = from + 32 * i + lane < P.units ? P.info[from + 32 * i + lane] : 0;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const unsigned mask = __ballot_sync(kAll, (next[i] & (kCovered | kBegins)) == kCovered);
+      if (mask != kAll) {   // it ends in the first unit that it does not cover, or before it
+        const int m = __ffs(~mask) - 1;
+        return 1 + 32 * i + m + (__shfl_sync(kAll, next[i], m) & kHeadEnds ? 1 : 0);
+      }
     }
-    const int end = lower_bound<kNorm>(P, (from + 32) * U, P.N, kNorm ? run.key : run.key + 1, run.ex + 1);
+    const int end = lower_bound<kNorm>(P, (from + 32 * kAhead) * U, P.N, kNorm ? run.key : run.key + 1, run.ex + 1);
     return (end - 1) / U - (u0 + b) + 1;
   };
   auto add_rows = [&](float (&acc)[8], int b, int tail, int l0, int l1, int c0) {
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P, int U, i
     const int b = __ffs(t) - 1, tail = __shfl_sync(kAll, from_tail, b);
     const Place run = {__shfl_sync(kAll, mine.key, b), 0, __shfl_sync(kAll, mine.ex, b)};
     const int L = length(b, run);
-    if (L > 32) {   // for the whole CTA
+    if (L > per) {   // for the whole CTA: one or two of them begin in its units
       if (lane == 0) {
         const int i = atomicAdd(&count, 1);
         many[i] = b;
@@ -486,7 +492,7 @@ static cudaError_t run_runs(const EmbedParams& P, cudaStream_t s) {
     const cudaError_t e = allow_smem<embed_runs_kernel<E, O, PV, NS, kNorm>>(smem);
     if (e != cudaSuccess) return e;
   }
-  const long long zero = kNorm || P.accumulate ? 0 : ((long long)P.V + kTokens - 1) / kTokens;
+  const long long zero = kNorm || P.accumulate || P.cleared ? 0 : ((long long)P.V + kTokens - 1) / kTokens;
   const long long warps = P.units + zero;
   cudaError_t e = launch_operator(embed_runs_kernel<E, O, PV, NS, kNorm>, dim3((unsigned)((warps + 7) / 8)), dim3(256), smem, s, P, U);
   if (e == cudaSuccess && P.N >= U) {   // shorter: no unit that a run could cover

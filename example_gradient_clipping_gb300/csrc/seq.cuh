@@ -171,6 +171,7 @@ struct EmbedParams {
   unsigned* info;          // [units]
   unsigned* status;
   int B, T, V, D, N, i64, padding, units, slabs, accumulate;
+  int cleared;             // dW is zeros: the rows without a token are not written
   float scale;
   long long ld;
   dp_row_strides dy;
@@ -232,7 +233,9 @@ cudaError_t launch_rows_sum(const float* rows, int segments, int count, size_t n
 cudaError_t launch_rows_sqnorm(const float* rows, int B, size_t n, float* out, cudaStream_t s);
 cudaError_t launch_embed_lookup(const dpk::EmbedParams& P, int dtype, cudaStream_t s);
 size_t embed_order_ws_bytes(int N, int V);
-cudaError_t launch_embed_order(const dpk::EmbedParams& P, int* order, int* keys, void* ws, cudaStream_t s);
+// bytes: of P.dW, cleared beside the sort (0: none); only where embed_order_clears(P.N, bytes).
+bool embed_order_clears(int N, size_t bytes);
+cudaError_t launch_embed_order(const dpk::EmbedParams& P, int* order, int* keys, void* ws, size_t bytes, cudaStream_t s);
 constexpr int kEmbedSlab = 256;   // columns of a row's piece
 int embed_unit(int N);            // sorted rows of a warp's work
 cudaError_t launch_embed_sqnorms(const dpk::EmbedParams& P, int dtype, float* sqnorms, cudaStream_t s);

@@ -95,6 +95,7 @@ def _declare():
         "dp_embedding_order": (i, [P(EmbeddingDesc), v, v, v, sz, v]),
         "dp_embedding_sqnorms": (i, [P(EmbeddingDesc), v, v, v, v, sz, v]),
         "dp_embedding_grad": (i, [P(EmbeddingDesc), v, v, v, v, i, v, sz, v]),
+        "dp_embedding_order_grad": (i, [P(EmbeddingDesc), v, v, v, v, v, i, v, sz, v]),
     }
     for name, (res, args) in sig.items():
         f = getattr(_seq._lib, name)
@@ -173,6 +174,13 @@ def dp_embedding_grad(desc: EmbeddingDesc, order, dY, factors, dW, workspace, ws
                       accumulate: bool = False, stream=None) -> None:
     _check(_seq._lib.dp_embedding_grad(desc, _ptr(order), _ptr(dY), _ptr(factors), _ptr(dW), int(bool(accumulate)),
                                        _ptr(workspace), _bytes(workspace, ws_bytes), _stream(stream)))
+
+
+def dp_embedding_order_grad(desc: EmbeddingDesc, tokens, order, dY, factors, dW, workspace,
+                            ws_bytes: Optional[int] = None, accumulate: bool = False, stream=None) -> None:
+    _check(_seq._lib.dp_embedding_order_grad(desc, _ptr(tokens), _ptr(order), _ptr(dY), _ptr(factors), _ptr(dW),
+                                             int(bool(accumulate)), _ptr(workspace), _bytes(workspace, ws_bytes),
+                                             _stream(stream)))
 
 
 # ---- argument checks ------------------------------------------------------------------
@@ -393,13 +401,11 @@ def _grad_desc(tokens, dy, V, scale, padding, factors, dtype):
     return dy, _get(key) or _keep(key, _embedding_desc(tokens, None, dy, V, scale, padding, factors, dtype))
 
 
-def _sorted(d, tokens):
-    """The tokens' order and a workspace as one array (order first), and the addresses of the two."""
+def _sorting(d, tokens):
+    """Room for the tokens' order and a workspace as one array, and the addresses of the two."""
     both = _empty(d.order_bytes + d.ws_bytes, dtype=torch.uint8, device=tokens.device)
     order = both.data_ptr()
-    ws = order + d.order_bytes   # (a multiple of 16)
-    _call(_seq._lib.dp_embedding_order, tokens.get_device(), d, tokens.data_ptr(), order, ws, d.ws_bytes)
-    return both, order, ws
+    return both, order, order + d.order_bytes   # (a multiple of 16)
 
 
 def embedding_backward(tokens, dy, V: int, scale: float = 1.0, padding: Optional[int] = None, factors=None,
@@ -414,8 +420,8 @@ def embedding_backward(tokens, dy, V: int, scale: float = 1.0, padding: Optional
     dw = _empty((d.V, d.D), dtype=dtype, device=tokens.device)
     if not d.B * d.T:
         return dw.zero_()
-    both, order, ws = _sorted(d, tokens)
-    _call(_seq._lib.dp_embedding_grad, tokens.get_device(), d, order, dy.data_ptr(),
+    both, order, ws = _sorting(d, tokens)
+    _call(_seq._lib.dp_embedding_order_grad, tokens.get_device(), d, tokens.data_ptr(), order, dy.data_ptr(),
           None if factors is None else factors.data_ptr(), dw.data_ptr(), 0, ws, d.ws_bytes)
     return dw
 
@@ -430,7 +436,8 @@ def embedding_sqnorms(tokens, dy, V: int, scale: float = 1.0, padding: Optional[
     sq = _empty(d.B, dtype=_f32, device=tokens.device)
     if not d.B * d.T:
         return sq.zero_()
-    both, order, ws = _sorted(d, tokens)
+    both, order, ws = _sorting(d, tokens)
+    _call(_seq._lib.dp_embedding_order, tokens.get_device(), d, tokens.data_ptr(), order, ws, d.ws_bytes)
     _call(_seq._lib.dp_embedding_sqnorms, tokens.get_device(), d, order, dy.data_ptr(), sq.data_ptr(), ws, d.ws_bytes)
     return sq
 

@@ -257,6 +257,10 @@ dp_status dp_embedding_sqnorms(const dp_embedding_desc* desc, const void* order,
  * must be fp32 then. */
 dp_status dp_embedding_grad(const dp_embedding_desc* desc, const void* order, const void* dY, const float* factors,
                             void* dW, int accumulate, void* workspace, size_t ws_bytes, cudaStream_t stream);
+/* dp_embedding_order and dp_embedding_grad in one call, which can clear dW while it sorts. */
+dp_status dp_embedding_order_grad(const dp_embedding_desc* desc, const void* tokens, void* order, const void* dY,
+                                  const float* factors, void* dW, int accumulate, void* workspace, size_t ws_bytes,
+                                  cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -316,6 +316,42 @@ def test_embedding_strides_accumulate_and_neighbours(lib):
         lib.embedding_backward(t, wide[:, :, ::2], V)
 
 
+@pytest.mark.parametrize("N,V,D", [(1, 1, 1), (7, 50, 3), (1024, 3000, 33), (1500, 700, 128), (9000, 20011, 24), (20000, 4000, 40)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_embedding_sorted_and_summed_in_one_call(lib, N, V, D, dtype):
+    """The bits of the two calls; dW at any alignment, its neighbours left, whatever it held before."""
+    import torch
+    out = lib.DP_BF16 if dtype == "bf16" else lib.DP_FP32
+    d = lib.embedding_desc(lib.DP_FP32, B=1, T=N, V=V, D=D, scale=1.5, padding=V - 1 if V > 1 else None)
+    d.out_dtype = out
+    t = _tokens(1, N, V, N, "skewed").int()
+    dy = torch.randn(1, N, D, device="cuda")
+    f = torch.full((1,), 0.5, device="cuda")
+    order, ws = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in (lib.dp_embedding_order_size(d), lib.dp_embedding_workspace(d)))
+    want = torch.empty(V, D, device="cuda", dtype=_dt(dtype))
+    lib.dp_embedding_order(d, t, order, ws)
+    lib.dp_embedding_grad(d, order, dy, f, want, ws)
+    sorted_ = order.clone()
+    for off in (8, 1, 3, 7):
+        flat = torch.full((V * D + 24,), float("nan"), device="cuda", dtype=_dt(dtype))
+        dw = flat[off:off + V * D].view(V, D)
+        order.zero_()
+        lib.dp_embedding_order_grad(d, t, order, dy, f, dw, ws)
+        if off == 8:
+            assert torch.equal(dw, want)
+        else:   # narrower accesses add in the same order
+            assert torch.allclose(dw.float(), want.float(), rtol=2.0 ** -7 if dtype == "bf16" else 1e-5, atol=1e-5)
+        assert torch.equal(dw == 0, want == 0)
+        assert flat[:off].isnan().all() and flat[off + V * D:].isnan().all()
+        assert torch.equal(order.view(torch.int32)[:N], sorted_.view(torch.int32)[:N])
+    if dtype == "fp32":
+        base = torch.randn(V, D, device="cuda")
+        one, two = base.clone(), base.clone()
+        lib.dp_embedding_order_grad(d, t, order, dy, f, one, ws, accumulate=True)
+        lib.dp_embedding_grad(d, order, dy, f, two, ws, accumulate=True)
+        assert torch.equal(one, two)
+
+
 def test_embedding_autograd(lib):
     import torch
     for dtype in ("bf16", "fp32"):

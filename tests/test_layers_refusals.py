@@ -128,6 +128,23 @@ def test_embedding_pointers_and_workspace(fake):
              "fp32")
 
 
+def test_embedding_order_grad_refuses(fake):
+    dp, d = fake.dp, _embed(fake, T=30000, dy=(30000 * 64, 64))
+    need = dp.dp_embedding_workspace(d)
+    for i in (0, 1, 2, 4):   # tokens, order, dY, dW
+        a = [PTR] * 5
+        a[i] = None
+        _refused(fake, lambda: dp.dp_embedding_order_grad(d, *a, PTR, need, stream=STREAM), INVALID, "non-NULL")
+    a = [PTR] * 5
+    for ws, n, text in ((None, need, "workspace"), (PTR, need - 1, "workspace"), (PTR + 4, need, "aligned")):
+        _refused(fake, lambda: dp.dp_embedding_order_grad(d, *a, ws, n, stream=STREAM), INVALID, text)
+    _refused(fake, lambda: dp.dp_embedding_order_grad(d, PTR, PTR + 8, PTR, PTR, PTR, PTR, need, stream=STREAM), INVALID, "aligned")
+    _refused(fake, lambda: dp.dp_embedding_order_grad(_embed(fake, V=0), *a, PTR, need, stream=STREAM), INVALID, "> 0")
+    half = _embed(fake, out_dtype=0)
+    _refused(fake, lambda: dp.dp_embedding_order_grad(half, *a, PTR, 1 << 40, accumulate=True, stream=STREAM), INVALID, "fp32")
+    assert ctypes.CDLL(dp.LIB_PATH)["dp_embedding_order_grad"](*[None] * 10) == INVALID
+
+
 @pytest.mark.parametrize("kw,status,text", [
     (dict(dtype=3), INVALID, "dtype"), (dict(B=0), INVALID, "> 0"), (dict(V=0), INVALID, "> 0"), (dict(K=-1), INVALID, ">= 0"),
     (dict(K=101), INVALID, "alternatives"), (dict(V=500, ld=500, ld_grad=500, K=129), UNSUPPORTED, "128"),
