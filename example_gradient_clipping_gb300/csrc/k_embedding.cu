@@ -1,13 +1,15 @@
 // Embedding lookup, y_r = scale w[token_r], and the order of its gradients: the tokens sorted.
 //
-// Lookup: one read of the rows met and one write, bound by HBM.
+// Lookup: one read of the rows met and one write, bound by HBM (262144 rows of 1024 bf16, V = 131072: 108 us, of
+// which 80 are the write at the copy rate; 16384 rows of 768, V = 50257: 8.2 us).
 //
 // Order: the positions sorted by their tokens, stably (least significant digit first), so that equal tokens
 // stand in the order of their positions and, among them, example by example.  Up to 16384 tokens in one launch: 1024
 // a CTA of a cluster of 1, 8 or 16 that write each digit's keys to one another's shared memory (16384 tokens,
 // V = 50257: 9.9 us, 13.4 in tiles, 26 in one CTA; 4096 tokens a CTA 17.3, for four-byte stores to
-// other SMs are what it then waits for); longer lists in tiles of a CTA each: counted, then written to their
-// places (262144 tokens: 24 us).  Bound by latency.
+// other SMs are what it then waits for); longer lists in tiles of 1024 keys a CTA: counted, then written to their
+// places (262144 tokens: 21 us, a million 39; tiles of 4096 keys 34 and 58, and 496 against 486 for 16 million).
+// Bound by latency.
 #include <algorithm>
 
 #include "seq.cuh"
@@ -397,8 +399,9 @@ using namespace dpk::embed;
 
 template <class E, int VEC>
 static cudaError_t run_lookup(const EmbedParams& P, cudaStream_t s) {
-  // four rows a warp once that leaves every SM's warps two rounds
-  if (P.N >= 4 * 152 * 32)
+  // four rows a warp once that leaves an SM's warps one round: 16384 rows of 768 bf16 8.2 us (a row a warp 8.9),
+  // 262144 of 64 24 (34); 6000 of 768 4.9 with a row a warp (5.4 with four)
+  if (P.N >= 2 * 152 * 32)
     return launch_operator(embed_lookup_kernel<E, VEC, 4>, dim3((unsigned)((P.N + 31ll) / 32)), dim3(256), 0, s, P);
   return launch_operator(embed_lookup_kernel<E, VEC, 1>, dim3((unsigned)((P.N + 7ll) / 8)), dim3(256), 0, s, P);
 }
@@ -426,8 +429,8 @@ static void digits(int V, int* passes, int* bits) {
   *bits = (b + *passes - 1) / *passes;
 }
 constexpr int kSmallSort = 16 * 1024;
-static int tile_keys(int N) { return N <= 1 << 20 ? 1024 : 4096; }   // few tiles would leave SMs without one
-static int tiles_of(int N) { return (int)(((long long)N + tile_keys(N) - 1) / tile_keys(N)); }
+constexpr int kTileKeys = 1024;
+static int tiles_of(int N) { return (N + kTileKeys - 1) / kTileKeys; }
 static size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 size_t embed_order_ws_bytes(int N, int V) {
   if (N <= kSmallSort) return 0;
@@ -461,12 +464,16 @@ static cudaError_t run_tile_sort(const EmbedParams& P, int passes, int bits, int
   unsigned *offs = hist + hist_words, *sums = offs + hist_words;
   unsigned *k1 = reinterpret_cast<unsigned*>(keys), *v1 = reinterpret_cast<unsigned*>(order);
   const unsigned *kin = nullptr, *vin = nullptr;   // the tokens as they come
-  const bool summed = tiles > 32;                  // fewer: a CTA reads all counts of a digit itself
+  // few tiles: a CTA reads all counts of a digit itself (17000 tokens 12.5 us, 14.4 by the scan; 60000 17.1 by the
+  // scan, 19.1 without)
+  const bool summed = tiles > 32;
   for (int p = 0; p < passes; ++p) {
     const bool to_out = (passes - 1 - p) % 2 == 0;   // the last pass writes `order`
     unsigned *ko = to_out ? k1 : k2, *vo = to_out ? v1 : v2;
     const int n = tiles << bits, blocks = (n + 1023) / 1024;
-    const bool two = blocks > 256;   // a CTA would read 1 MB and more of counts
+    // long lists: sums of 1024 counts first (262144 tokens 21.0 us, 23.2 without; a million 39 and 50; but 40000
+    // tokens 17.2, 15.9 without)
+    const bool two = blocks > 32;
     cudaError_t e = launch_operator(embed_count_kernel<IT, BITS>, dim3(tiles), dim3(256), 0, s, P, kin, p * bits, bits, tiles, hist);
     if (summed) {
       if (e == cudaSuccess && two) e = launch_operator(embed_sums_kernel, dim3(blocks), dim3(1024), 0, s, hist, sums, n);
@@ -489,8 +496,7 @@ static cudaError_t run_sort(const EmbedParams& P, int passes, int bits, int* ord
   if (P.N <= 1024) return run_small_sort<BITS, 1>(P, passes, bits, order, keys, bytes, s);
   if (P.N <= 8 * 1024) return run_small_sort<BITS, 8>(P, passes, bits, order, keys, bytes, s);
   if (P.N <= kSmallSort) return run_small_sort<BITS, 16>(P, passes, bits, order, keys, bytes, s);
-  return tile_keys(P.N) == 1024 ? run_tile_sort<4, BITS>(P, passes, bits, order, keys, ws, s)
-                                : run_tile_sort<16, BITS>(P, passes, bits, order, keys, ws, s);
+  return run_tile_sort<kTileKeys / 256, BITS>(P, passes, bits, order, keys, ws, s);
 }
 
 // Beside a sort by one cluster the other SMs have nothing to do: 16384 tokens and 50257 x 768 bf16, sorted and summed,

@@ -10,7 +10,9 @@
 // each lane copies its own 16-byte pieces of the next rows into a ring in shared memory and reads only what it
 // copied.  A run that covers a whole unit is too long for one warp: its units' sums go to partial rows and
 // embed_join_kernel adds them.  The norms and the sums read dy once each; the sum also writes the zero rows
-// of dw.  Bound by HBM.
+// of dw.  262144 rows of 1024 bf16, V = 131072: norms 110 us (4.9 TB/s; a run ends every few rows, and
+// its squares are summed before the next one is added), sum to fp32 178 us (6.0 TB/s, bound by HBM).
+// 4000 rows of 197 fp32: 8.6 and 7.2 us, three launches' latency.
 #include <algorithm>
 
 #include "seq.cuh"
@@ -387,7 +389,9 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P, int U, i
     const int b = __ffs(t) - 1, tail = __shfl_sync(kAll, from_tail, b);
     const Place run = {__shfl_sync(kAll, mine.key, b), 0, __shfl_sync(kAll, mine.ex, b)};
     const int L = length(b, run);
-    if (L > per) {   // for the whole CTA: one or two of them begin in its units
+    // for the whole CTA: one or two of them begin in its units (4000 rows of 197: 7.3 us, 10.4 where only runs of more
+    // than 32 units do; with 32 units a CTA norms of 262144 rows 110, 118 where those of more than 8 do)
+    if (L > per) {
       if (lane == 0) {
         const int i = atomicAdd(&count, 1);
         many[i] = b;
@@ -481,8 +485,11 @@ namespace dph {
 using namespace dpk;
 using namespace dpk::embed;
 
-// Rows of a unit: 32, or fewer where that would leave an SM less than 16 warps, whose rows follow one another.
-int embed_unit(int N) { return N >= 152 * 16 * 32 ? 32 : N >= 152 * 16 * 16 ? 16 : 8; }
+// Rows of a unit, which follow one another: 32, or fewer where that would leave an SM less than eight warps (of 16
+// rows: six).  Norms and sums of 48000 rows of 768 bf16, V = 50257: 25.3 and 51 us with 32, 28.1 and 50 with 16, 30.8
+// and 54 with 8; 24000 rows 20.8 and 42.8, 18.4 and 40.6, 22.4 and 44.0; 4000 rows 13.6 and 32.6 with 16, 12.6 and
+// 31.7 with 8.  262144 rows of 1024: 110 and 178 with 32, 141 and 242 with 8.
+int embed_unit(int N) { return N >= 152 * 8 * 32 ? 32 : N >= 152 * 6 * 16 ? 16 : 8; }
 
 template <class E, class O, int PV, int NS, bool kNorm>
 static cudaError_t run_runs(const EmbedParams& P, cudaStream_t s) {
@@ -496,7 +503,9 @@ static cudaError_t run_runs(const EmbedParams& P, cudaStream_t s) {
   const long long warps = P.units + zero;
   cudaError_t e = launch_operator(embed_runs_kernel<E, O, PV, NS, kNorm>, dim3((unsigned)((warps + 7) / 8)), dim3(256), smem, s, P, U);
   if (e == cudaSuccess && P.N >= U) {   // shorter: no unit that a run could cover
-    const int per = (long long)P.units * P.slabs <= 152 * 8 * 8 ? 8 : 32;   // a warp's runs follow one another
+    // units a CTA; a warp's runs follow one another (4000 rows of 197 fp32: sum 7.2 us with 8, 10.2 with 32; 262144 of
+    // 1024 bf16: 178 with 32, 184 with 8)
+    const int per = (long long)P.units * P.slabs <= 152 * 8 * 8 ? 8 : 32;
     e = launch_operator(embed_join_kernel<O, (PV > 4 ? 4 : PV), kNorm>,
                         dim3((unsigned)((P.units + per - 1) / per), kNorm ? 1u : (unsigned)P.slabs), dim3(256), 0, s, P, U, per);
   }

@@ -1,7 +1,10 @@
 // Rows of per-example gradients, or of partial sums of them: their squared norms and weighted sums.
 //
 // Both read every row once.  rows_sum_kernel: 32 columns a CTA, 32 or 8 warps that each add a consecutive
-// share of the rows in order, twelve loads in flight, then the shares in order; so the result has one order.
+// share of the rows in order, twelve loads in flight, then the shares in order; so the result has one order.  32 warps
+// take many rows of few columns (700 of 1536: 4.1 us, 5.8 with 8 warps; 152 of 1536 2.5 and 2.15, 500 of 8192 7.3 and
+// 5.7), and up to eight rows are a thread a column (8 of 20000: 1.3, 2.6).  Small ones are bound by latency, large
+// ones by HBM.
 #include <algorithm>
 
 #include "seq.cuh"
@@ -151,7 +154,7 @@ cudaError_t launch_rows_sum(const float* rows, int segments, int count, size_t n
     if (count <= kFew)
       e = launch_operator(rows_sum_few_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)ng), dim3(256), 0, s, from, count,
                           n, factors, to, bf16, accumulate);
-    else if ((unsigned long long)grid.x * grid.y <= 304)   // few columns: shorter shares
+    else if (count > 200 && (unsigned long long)grid.x * grid.y <= 152)   // many rows of few columns: shorter shares
       e = launch_operator(rows_sum_kernel<32>, grid, dim3(1024), 0, s, from, count, n, factors, to, bf16, accumulate);
     else
       e = launch_operator(rows_sum_kernel<8>, grid, dim3(256), 0, s, from, count, n, factors, to, bf16, accumulate);

@@ -2,7 +2,9 @@
 //
 // A row stays in registers between its sums and its result, so it is read once and written once; the
 // variance is the mean of (x - mu)^2 over those registers, a second pass that costs no traffic and
-// does not cancel where mu is large against the spread.  Bound by HBM.
+// does not cancel where mu is large against the spread.  Bound by HBM: 32764 rows of 4096 bf16 94 us (5.7 TB/s),
+// 12608 of 768 8.6 us (4.5), 4000 of 1001 fp32 8.6 us, by scalars; 64 rows of 768 2.4 us, a launch's latency.  One
+// row a CTA instead of CTAs that go over the rows took 116 us for the first.
 #include "layer_norm.cuh"
 
 namespace dpk {
@@ -15,7 +17,9 @@ constexpr int fwd_stages(int es, int vec, int G, int C) {
   const int stage = fwd_threads(G) * (C / vec) * 16;
   return vec * es != 16 ? 0 : 4 * stage <= 48 * 1024 ? 4 : 3;
 }
-constexpr int fwd_ctas(int G, int C) { return G > 32 ? 1024 / G : C > 16 ? 2 : 3; }   // an SM
+// CTAs an SM: what the registers hold (30000 rows of 64 bf16 2.8 us with three, 3.0 with two; 12608 of 768 8.6 with
+// two, 10.4 with three).
+constexpr int fwd_ctas(int G, int C) { return G > 32 ? 1024 / G : C > 16 ? 2 : 3; }
 
 template <class E, int VEC, int G, int C>
 __global__ void __launch_bounds__(fwd_threads(G), fwd_ctas(G, C)) layer_norm_kernel(NormParams P) {

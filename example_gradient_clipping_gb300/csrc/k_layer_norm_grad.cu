@@ -5,7 +5,9 @@
 // One pass: x and dy are read once, dx is written once, and each thread adds its columns of dy h and dy
 // over the rows that it sees in registers.  The rows of a segment (an example, or the whole batch) are
 // split into slices, one CTA each; a slice's sums go to a partial row and rows_sum_kernel adds the
-// slices in order.  Bound by HBM.
+// slices in order.  Bound by HBM and, small batches, by the launches, the CTAs' first loads and the sums behind the
+// last row: 32764 rows of 4096 bf16 150 us (5.4 TB/s; dw alone without dx 90), 12608 of 768 19 us (3.1 TB/s; each
+// further 1000 rows 0.8 us, 5.8 TB/s; dx alone 15.7), 4000 of 1001 fp32 by scalars 15.
 #include "layer_norm.cuh"
 
 namespace dpk {
@@ -222,7 +224,8 @@ namespace dph {
 using namespace dpk;
 
 // Slices a segment: what takes the GPU's CTAs, one an SM, the least rounds of a group's rows, each CTA's start and
-// end counted as six rows.  (By width and type alone: the workspace is the same wherever the tensors lie.)
+// end counted as six rows (64 examples of 197 x 768 each their own gradient: 20.3 us, 24.8 were they counted as none).
+// (By width and type alone: the workspace is the same wherever the tensors lie.)
 int norm_grad_slices(int segments, long long rows, int D, int dtype) {
   const int W = dtype == DP_BF16 ? 8 : 4, G = norm_shape(D, D % W ? 1 : W).G, per = grad_threads(G) / G;
   int best = 1;

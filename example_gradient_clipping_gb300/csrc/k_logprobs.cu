@@ -12,9 +12,14 @@
 // whose maximum reaches it are read again, and what reaches it is ranked by (value, index).  Where more logits
 // reach it than there is room for (many equal ones), the exact K-th largest value is found by bisection, and
 // its ties are taken in the order of their indices.
-// A row is one CTA's, or with few rows a cluster's.  Bound by HBM.
+// A row is one CTA's (64, 128 or 256 threads), or with few rows a cluster's.  4096 rows of 50257 bf16: 66.7 us, 6.2
+// TB/s, bound by HBM; with the 20 largest 80.6 us and the 50 largest 92, where what follows the row's last load (sums,
+// bound, groups read again, ranking: a third of a CTA's time) is only half hidden under the rows beside it.
+// Reading ahead did not help: the next row asked into L2 while this one is ranked 97 -> 99 to 137 us; nor did a
+// cluster of two for every row (68 -> 83), nor collecting by warps instead of by the CTA (97 -> 101).
 //
-// Gradient: one read and one write of the rows, elementwise from m, ls and the entropy.  Bound by HBM.
+// Gradient: one read and one write of the rows, elementwise from m, ls and the entropy.  Bound by HBM: 4096 rows of
+// 50257 bf16 127 us, 6.5 TB/s; 2048 of 131071 164 us.
 #include <algorithm>
 
 #include "seq.cuh"
@@ -189,7 +194,10 @@ __device__ void part_top(const Grid<E, NT>& g, int shift, const float* gmax, int
         for (int i = 0; i < NT / 32; ++i) c += k[i] >= trial;
         c = __reduce_add_sync(kAll, c);
         if (c >= n) t = trial;
-        if (c >= n && c <= n + min(n / 4, 12) + 2) break;   // near enough
+        // near enough: fewer steps for a few candidates more (8 rows' 20: 8.8 us, 9.9 to the last bit; but where n
+        // is near half of the threads each brings many: 4096 rows' 64 with 128 threads 97.5, 99.9)
+        const int more = NT == 256 || 3 * n <= NT ? min(n / 4, 12) + 2 : 1;
+        if (c >= n && c <= n + more) break;
       }
     }
     if (lane == 0) {
@@ -661,9 +669,13 @@ static cudaError_t run_logprobs(const LogprobParams& P, cudaStream_t s) {
   constexpr int W = Vec<E>::W;
   const long long rows = (long long)P.B * P.T;
   const long long nvec = ((long long)P.V + 2 * W - 2) / W;   // at any alignment of the row
-  // a cluster a row while that leaves every CTA two rounds of loads and the GPU is not full
+  // A cluster a row while the GPU is not full and every CTA keeps two rounds of loads, with alternatives, whose
+  // lists are joined at the end, eight (8 rows of 131072: 4.1 and 9.0 us, 8.3 and 13.0 on one CTA each; 150 of 32000,
+  // top 20, not split 7.3, split 8.4); up to four CTAs an SM for long rows (300 of 128000: 15.1, 16.4 not split;
+  // but 150 of 32000 5.7, 4.6 with half the CTAs).
   int cluster = 1, log_cluster = 0;
-  for (; cluster < 8 && rows * cluster * 2 <= 304 && nvec / (2 * cluster) >= 512; cluster *= 2) ++log_cluster;
+  auto least = [&](long long ctas) { return ctas <= 304 ? (P.K ? 2048 : 512) : 4096; };
+  for (; cluster < 8 && rows * cluster * 2 <= 608 && nvec / (2 * cluster) >= least(rows * cluster * 2); cluster *= 2) ++log_cluster;
   const int per = (int)((nvec + cluster - 1) / cluster);
   int shift = 0;   // at most 4096 groups a part: 16 KB
   while (max_groups<NT>(per, shift) > 4096) ++shift;
@@ -676,11 +688,18 @@ static cudaError_t run_logprobs(const LogprobParams& P, cudaStream_t s) {
 }
 
 template <class E> static cudaError_t run_logprobs_nt(const LogprobParams& P, cudaStream_t s) {
-  // Short rows on 64 threads: most of 256 would have no vector.  (Their maxima bound the K-th largest while K is
-  // well below 64.)
-  const bool small = P.V <= 512 * Vec<E>::W && P.K <= 32;
-  if (P.K) return small ? run_logprobs<E, true, 64>(P, s) : run_logprobs<E, true, 256>(P, s);
-  return small ? run_logprobs<E, false, 64>(P, s) : run_logprobs<E, false, 256>(P, s);
+  // Threads a row.  Fewer leave more rows on an SM, so that one row's start, bound and ranking run under the reads of
+  // others: 4096 rows of 8000 bf16 top 20 24.9 us on 64 threads, 25.2 on 128, 39.2 on 256; of 50257 105.7, 80.4,
+  // 90.2.  But their maxima bound the K-th largest loosely where K is not well below their number (50257 top 64:
+  // 99.9 on 128, 102 on 256, top 100 907 and 115) and long rows leave more candidates (131071 top 20: 103 and 97),
+  // and rows that do not fill the GPU want more threads each (300 of 32000 top 20: 9.3 and 8.3).
+  const long long rows = (long long)P.B * P.T, nvec = P.V / Vec<E>::W;
+  const bool many = rows >= 608;
+  if (many && nvec <= 2048 && P.K <= 32)
+    return P.K ? run_logprobs<E, true, 64>(P, s) : run_logprobs<E, false, 64>(P, s);
+  if (many && (P.K == 0 || (P.K <= 64 && nvec <= 8192)))
+    return P.K ? run_logprobs<E, true, 128>(P, s) : run_logprobs<E, false, 128>(P, s);
+  return P.K ? run_logprobs<E, true, 256>(P, s) : run_logprobs<E, false, 256>(P, s);
 }
 
 cudaError_t launch_logprobs(const LogprobParams& P, int dtype, cudaStream_t s) {
@@ -694,7 +713,8 @@ static cudaError_t run_logprobs_grad(const LogprobParams& P, cudaStream_t s) {
   const auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p) / sizeof(E) % W; };
   const bool vec = at(P.logits) == at(P.grad) && ((P.ld - P.ldg) % W == 0 || (long long)P.B * P.T == 1);
   const long long rows = (long long)P.B * P.T;
-  // rounds a warp: the row's constants are read once for them, while the warps fill the GPU a few times
+  // rounds a warp: the row's constants are read once for them, while the warps fill the GPU a few times (4096 x 50257
+  // bf16: 127 us, 166 with one round a warp; few rows are one round)
   const long long round = 32 * (vec ? 4 * W : 8);
   const long long all = ((long long)P.V + (vec ? W - 1 : 0) + round - 1) / round;
   long long rounds = std::max<long long>(1, std::min<long long>(32, all * rows / (152 * 32 * 4)));
