@@ -2,9 +2,10 @@
 //
 // Both read every row once.  rows_sum_kernel: 32 columns a CTA, 32 or 8 warps that each add a consecutive
 // share of the rows in order, twelve loads in flight, then the shares in order; so the result has one order.  32 warps
-// take many rows of few columns (700 of 1536: 4.1 us, 5.8 with 8 warps; 152 of 1536 2.5 and 2.15, 500 of 8192 7.3 and
-// 5.7), and up to eight rows are a thread a column (8 of 20000: 1.3, 2.6).  Small ones are bound by latency, large
-// ones by HBM.
+// take many rows of few columns (the 152 partial rows of a layer norm's gradient of 8192 x 2048 bf16, which then takes
+// 26.7 us in all, 29.0 with 8 warps; 12608 x 768 19.4 and 20.3; but 64 rows of 2002 1.5 us with 8 warps, 2.5 with 32;
+// 64 of 20000 2.8 and 9.7), and up to eight rows are a thread a column (8 of
+// 20000: 1.3, 2.6).  Small ones are bound by latency, large ones by HBM.
 #include <algorithm>
 
 #include "seq.cuh"
@@ -154,7 +155,7 @@ cudaError_t launch_rows_sum(const float* rows, int segments, int count, size_t n
     if (count <= kFew)
       e = launch_operator(rows_sum_few_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)ng), dim3(256), 0, s, from, count,
                           n, factors, to, bf16, accumulate);
-    else if (count > 200 && (unsigned long long)grid.x * grid.y <= 152)   // many rows of few columns: shorter shares
+    else if (count > 64 && (unsigned long long)grid.x * grid.y <= 304)   // many rows of few columns: shorter shares
       e = launch_operator(rows_sum_kernel<32>, grid, dim3(1024), 0, s, from, count, n, factors, to, bf16, accumulate);
     else
       e = launch_operator(rows_sum_kernel<8>, grid, dim3(256), 0, s, from, count, n, factors, to, bf16, accumulate);
