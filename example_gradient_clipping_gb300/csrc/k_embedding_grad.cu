@@ -10,7 +10,7 @@
 // each lane copies its own 16-byte pieces of the next rows into a ring in shared memory and reads only what it
 // copied.  A run that covers a whole unit is too long for one warp: its units' sums go to partial rows and
 // embed_join_kernel adds them.  The norms and the sums read dy once each; the sum also writes the zero rows
-// of dw.  262144 rows of 1024 bf16, V = 131072: norms 110 us (4.9 TB/s; a run ends every few rows, and
+// of dw.  262144 rows of 1024 bf16, V = 131072: norms 106 us (5.1 TB/s; a run ends every few rows, and
 // its squares are summed before the next one is added), sum to fp32 178 us (6.0 TB/s, bound by HBM).
 // 4000 rows of 197 fp32: 8.6 and 7.2 us, three launches' latency.
 #include <algorithm>
@@ -123,8 +123,13 @@ struct alignas(16) Entry {
 // end of a run that covers the unit before it (first partial row).
 enum : unsigned { kTailBegins = 1, kCovered = 2, kBegins = 4, kHeadEnds = 8 };
 
-// Ring of S rows of NS slabs: bytes of a warp.
-constexpr int ring_rows(int es, int NS) { return 6 * 1024 / (NS * SLAB * es) < 3 ? 3 : 6 * 1024 / (NS * SLAB * es); }
+// Ring of S rows of NS slabs: bytes of a warp.  8 KB for rows of three slabs and more (16384 rows of 2048 bf16: norms
+// 31.8 us and sum 66.4, 36.2 and 68.7 with 6 KB; 96000 of 768 43.6 and 63.1, 43.8 and 70.4), 6 KB for shorter ones (65536
+// of 64: sum 33 us, 45 with 9 KB, fewer warps then).
+constexpr int ring_rows(int es, int NS) {
+  const int rows = (NS >= 3 ? 8 : 6) * 1024 / (NS * SLAB * es);
+  return rows < 3 ? 3 : rows;
+}
 template <class E, int PV, int NS> constexpr int ring_bytes() {
   return PV * sizeof(E) == 16 ? ring_rows(sizeof(E), NS) * NS * SLAB * (int)sizeof(E) : 0;
 }
@@ -390,7 +395,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P, int U, i
     const Place run = {__shfl_sync(kAll, mine.key, b), 0, __shfl_sync(kAll, mine.ex, b)};
     const int L = length(b, run);
     // for the whole CTA: one or two of them begin in its units (4000 rows of 197: 7.3 us, 10.4 where only runs of more
-    // than 32 units do; with 32 units a CTA norms of 262144 rows 110, 118 where those of more than 8 do)
+    // than 32 units do; with 32 units a CTA norms of 262144 rows 110 us, 118 where those of more than 8 do)
     if (L > per) {
       if (lane == 0) {
         const int i = atomicAdd(&count, 1);
