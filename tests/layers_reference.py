@@ -78,7 +78,7 @@ def embedding_grad(tokens, dy, V, scale=1.0, padding=None, factors=None, r=0.0):
     return (dw, (count + 4) * U * size + r * dw.abs() + ETA), (sq, esq)
 
 
-def logprobs(logits, tokens, tau=1.0, dl=None, dh=None, r=0.0):
+def logprobs(logits, tokens, tau=1.0, dl=None, dh=None, r=0.0, threads=128):
     """Pairs (logprob, entropy, log p) or with dl and dh (logprob, entropy, log p, dz); tokens [B, T], < 0: none."""
     z = logits.double()
     V = z.shape[-1]
@@ -88,7 +88,7 @@ def logprobs(logits, tokens, tau=1.0, dl=None, dh=None, r=0.0):
     lp = x - ls
     p = torch.exp(lp)
     px = torch.where(p > 0, p * x.abs(), torch.zeros_like(p))
-    chain = (V / 256 + 64) * U   # a thread's additions, and those over threads and parts
+    chain = (V / (2 * threads) + 64) * U   # a thread's additions (two chains), and those over threads and parts
     term = EX2 * p + 4 * U * px  # of each e^x: of 2^x, and of x
     es = term.sum(-1, keepdim=True) + chain
     els = es + 2 * U * ls.abs() + U

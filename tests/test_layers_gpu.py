@@ -421,6 +421,48 @@ def test_token_logprobs(lib, B, T, V, K, dtype, tau):
     assert lib.dp_check_status() == lib.DP_OK
 
 
+@pytest.mark.parametrize("V", [1, 9, 500, 2049, 8195, 16390, 20001])
+@pytest.mark.parametrize("K", [0, 1, 20, 32, 33, 64, 65])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_token_logprobs_of_many_rows(lib, V, K, dtype):
+    """Enough rows that short ones are on 64 threads and ordinary ones on 128; rows on no 16-byte grid, one all
+    masks, one with NaN, one of equal logits."""
+    import torch
+    K, N = min(K, V), 611
+    g = _gen(V + K)
+    z = (torch.randn(1, N, V, generator=g, device="cuda") * 2).to(_dt(dtype))
+    z[0, 7] = -math.inf
+    z[0, 8, V // 2] = math.nan
+    z[0, 9] = 1.5
+    z[0, 10, : V // 2] = torch.finfo(_dt(dtype)).min
+    y = torch.randint(0, V, (1, N), generator=g, device="cuda")
+    y[0, ::5] = -1
+    good = torch.ones(N, dtype=torch.bool, device="cuda")
+    good[7:9] = False
+    lp, h, stats, best, at = lib.token_logprobs_forward(z, y, top=K)
+    vlp, vh, vall = ref.logprobs(z[:, good], y[:, good], threads=64)
+    _within(lp[:, good], vlp, "logprob")
+    _within(h[:, good], vh, "entropy")
+    assert torch.isnan(h[0, 7:9]).all()
+    if K:
+        want = ref.top(z, K)
+        assert torch.equal(at[:, good].long(), want[:, good]) and torch.equal(at[0, 7].long(), want[0, 7])
+        assert int(at[0, 8, 0]) == V // 2
+        _within(best[:, good], (torch.gather(vall[0], 2, want[:, good]), torch.gather(vall[1], 2, want[:, good])), "top")
+    assert lib.dp_check_status() == lib.DP_OK
+
+
+@pytest.mark.parametrize("kind", ["zeros", "two values", "rising", "falling", "few above", "one stretch", "masked", "lowest",
+                                  "all lowest", "strided"])
+@pytest.mark.parametrize("V,K", [(1000, 20), (9000, 32), (9000, 64), (30001, 20), (30001, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_top_alternatives_of_equal_logits_in_many_rows(lib, kind, V, K, dtype):
+    import torch
+    row = _ties(kind, V, dtype)
+    at = lib.token_logprobs(row.expand(1, 610, V).contiguous(), top=K)[3]
+    assert torch.equal(at.long(), ref.top(row[None, None], K).expand(1, 610, K))
+
+
 def _ties(kind, V, dtype):
     """Rows with more equal logits than there are places for."""
     import torch
