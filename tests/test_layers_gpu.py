@@ -96,6 +96,56 @@ def test_layer_norm_without_parameters_large_means_and_eps(lib):
     assert torch.equal(y, torch.zeros_like(y))
 
 
+@pytest.mark.parametrize("B", [1, 8, 9, 64, 65, 700])
+@pytest.mark.parametrize("n", [1, 33, 2002, 20000])
+def test_example_sum(lib, B, n):
+    """Every split of the rows; out (+)= sum_i f_i g_i, of B + 1 terms in one chain at most."""
+    import torch
+    rows, f, base = torch.randn(B, n, device="cuda"), torch.rand(B, device="cuda"), torch.randn(n, device="cuda")
+    for accumulate in (False, True):
+        out = base.clone()
+        lib.dp_example_sum(rows, B, n, f, out, accumulate=accumulate)
+        terms = rows.double() * f.double()[:, None]
+        want = terms.sum(0) + (base.double() if accumulate else 0.0)
+        size = terms.abs().sum(0) + (base.double().abs() if accumulate else 0.0)
+        assert ((out.double() - want).abs() <= (B + 2) * 2.0 ** -24 * size).all()
+
+
+def test_two_host_threads_on_their_streams(lib):
+    import threading
+
+    import torch
+    x, w, b, dy = _norm_inputs(4, 300, 768, "bf16", "bf16")
+    t = _tokens(4, 300, 5000, 1, "skewed").int()
+    z = torch.randn(2, 320, 3000, device="cuda").bfloat16()
+    y = torch.randint(0, 3000, (2, 320), device="cuda", dtype=torch.int32)
+
+    def everything():
+        n, m, r = lib.layer_norm_forward(x, w, b)
+        out = [n, *lib.layer_norm_backward(dy, x, w, m, r), *lib.layer_norm_backward(dy, x, w, m, r, per_example=True)]
+        out += [lib.embedding_backward(t, dy, 5000), lib.embedding_sqnorms(t, dy, 5000)]
+        lp, h, st, best, at = lib.token_logprobs_forward(z, y, top=20)
+        return out + [lp, h, best, at, lib.token_logprobs_backward(z, y, st, h, lp, h)]
+    want = everything()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(k):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for i in range(15):
+                got = everything()
+                s.synchronize()
+                if not all(torch.equal(p, q) for p, q in zip(got, want)):
+                    wrong.append((k, i))
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(3)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong and lib.dp_check_status() == lib.DP_OK
+
+
 @pytest.mark.parametrize("dtype,D", [("fp32", 1000), ("fp32", 1001), ("bf16", 1000), ("bf16", 250)])
 def test_layer_norm_gradient_where_mean_times_rstd_overflows(lib, dtype, D):
     """Constant rows of 2^116 with rstd 2^20: h = 0, so dx = rs (u - mean u) and dw = 0 exactly."""
@@ -244,6 +294,14 @@ def test_embedding(lib, B, T, V, D, dtype, kind):
         assert torch.equal(dw, lib.embedding_backward(tokens, dy, V, scale=scale, padding=padding, factors=factors, dtype=out))
         assert torch.equal(sq, lib.embedding_sqnorms(tokens, dy, V, scale=scale, padding=padding))
     assert lib.dp_check_status() == lib.DP_OK
+
+
+@pytest.mark.parametrize("B,T,V,D", [(3, 20000, 700, 520), (1, 45000, 2, 8), (2, 700, 40, 2104), (40, 1000, 3, 13), (5, 2500, 900, 768)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind", ["even", "skewed"])
+def test_embedding_of_many_rows(lib, B, T, V, D, dtype, kind):
+    """Units of 16 and 32 rows, runs over hundreds of them, rows of more than one pass."""
+    test_embedding(lib, B, T, V, D, dtype, kind)
 
 
 @pytest.mark.parametrize("N", [1, 31, 32, 33, 1024, 1025, 4097, 16384, 16385, 40000, 300000])
