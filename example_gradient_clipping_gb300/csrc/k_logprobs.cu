@@ -85,6 +85,23 @@ __device__ __forceinline__ uint32_t low_of(float low, __nv_bfloat16) {
 }
 __device__ __forceinline__ float low_of(float low, float) { return low; }
 
+// What a group's maximum is kept as, 32 bits: of bf16 the maxima of a round's first two and last two vectors.
+template <class E> struct Tops;
+template <> struct Tops<__nv_bfloat16> {
+  static constexpr int kParts = 2;
+  static __device__ __forceinline__ uint32_t of(float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632); }
+  static __device__ __forceinline__ uint32_t both(uint32_t a, uint32_t b) { return max2_nan(a, b); }
+  static __device__ __forceinline__ float get(uint32_t w, int part) { return __uint_as_float(part ? w & 0xffff0000u : w << 16); }
+  static __device__ __forceinline__ float all(uint32_t w) { return max_nan(get(w, 0), get(w, 1)); }
+};
+template <> struct Tops<float> {
+  static constexpr int kParts = 1;
+  static __device__ __forceinline__ uint32_t of(float a, float b) { return __float_as_uint(max_nan(a, b)); }
+  static __device__ __forceinline__ uint32_t both(uint32_t a, uint32_t b) { return of(__uint_as_float(a), __uint_as_float(b)); }
+  static __device__ __forceinline__ float get(uint32_t w, int) { return __uint_as_float(w); }
+  static __device__ __forceinline__ float all(uint32_t w) { return __uint_as_float(w); }
+};
+
 __device__ __forceinline__ void none(Vec<__nv_bfloat16>& v) { v.p.w[0] = v.p.w[1] = v.p.w[2] = v.p.w[3] = 0xff80ff80u; }
 __device__ __forceinline__ void none(Vec<float>& v) { v.p.w[0] = v.p.w[1] = v.p.w[2] = v.p.w[3] = -INFINITY; }
 
@@ -169,8 +186,9 @@ template <int NT> __device__ __forceinline__ int block_sum(int v, Shared<NT>& sh
 
 // The largest n keys of this part of the row, in order, to sh.best (n at most the part's entries).
 template <class E, int NT>
-__device__ void part_top(const Grid<E, NT>& g, int shift, const float* gmax, int n, Shared<NT>& sh) {
-  constexpr int W = Vec<E>::W, kRoom = Shared<NT>::kRoom, kList = Shared<NT>::kList, kWarps = NT / 32;
+__device__ void part_top(const Grid<E, NT>& g, int shift, const uint32_t* gmax, int n, Shared<NT>& sh) {
+  using Top = Tops<E>;
+  constexpr int W = Vec<E>::W, kParts = Top::kParts, kRoom = Shared<NT>::kRoom, kList = Shared<NT>::kList, kWarps = NT / 32;
   const int tid = threadIdx.x, lane = tid % 32, groups = g.groups(shift), size = kFly << shift;
   // a bound that n keys reach: the n-th largest of the threads' maxima, bit by bit (0 if fewer have one)
   if (tid < 32) {
@@ -226,25 +244,25 @@ __device__ void part_top(const Grid<E, NT>& g, int shift, const float* gmax, int
   {
     const float low = value_of(bound);
     for (int q = 4 * tid; q < groups; q += 4 * NT) {   // (a multiple of NT)
-      const float4 t = *reinterpret_cast<const float4*>(gmax + q);
-      const bool in[4] = {!(t.x < low), !(t.y < low), !(t.z < low), !(t.w < low)};
-      if (in[0] | in[1] | in[2] | in[3]) {
+      const uint4 t = *reinterpret_cast<const uint4*>(gmax + q);
+      const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+      unsigned in = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (in[i]) {
-            const int at = atomicAdd(&sh.groups, 1);
-            if (at < kList) sh.list[at] = (unsigned short)(q + i);
-          }
+      for (int i = 0; i < 4 * kParts; ++i) in |= (unsigned)!(Top::get(w[i / kParts], i % kParts) < low) << i;
+      for (; in; in &= in - 1) {
+        const int at = atomicAdd(&sh.groups, 1);
+        if (at < kList) sh.list[at] = (unsigned short)(q * kParts + __ffs(in) - 1);
       }
     }
   }
   __syncthreads();
   const int ng = sh.groups;
   if (ng <= kList) {
-    const int log_size = shift + 2;
-    static_assert(kFly == 4, "log_size");
-    for (int i = tid; i < ng << log_size; i += NT) {
-      const int j = g.vector(sh.list[i >> log_size], i & (size - 1), shift);
+    static_assert(kFly == 4, "a part of a round is four vectors, or two");
+    constexpr int kLog = kParts == 1 ? 2 : 1;
+    for (int i = tid; i < ng << (shift + kLog); i += NT) {
+      const int e = sh.list[i >> (shift + kLog)], k = i & ((1 << (shift + kLog)) - 1);
+      const int j = g.vector(e / kParts, (k >> kLog) * kFly + (e % kParts << kLog) + (k & ((1 << kLog) - 1)), shift);
       if (j < g.j1) collect(j, bound);
     }
   }
@@ -255,7 +273,7 @@ __device__ void part_top(const Grid<E, NT>& g, int shift, const float* gmax, int
     auto reach = [&](unsigned t) {
       int c = 0;
       for (int q = tid; q < groups; q += NT)
-        if (key_of(gmax[q]) >= t)
+        if (key_of(Top::all(gmax[q])) >= t)
           for (int i0 = 0; i0 < size; ++i0) {
             const int j = g.vector(q, i0, shift);
             if (j >= g.j1) break;
@@ -283,7 +301,7 @@ __device__ void part_top(const Grid<E, NT>& g, int shift, const float* gmax, int
     __syncthreads();
     if (bound != kAll)
       for (int q = tid; q < groups; q += NT)
-        if (key_of(gmax[q]) > bound)
+        if (key_of(Top::all(gmax[q])) > bound)
           for (int i = 0; i < size && g.vector(q, i, shift) < g.j1; ++i) collect(g.vector(q, i, shift), bound + 1);
     __syncthreads();
     have = sh.count;   // < n
@@ -373,7 +391,7 @@ __global__ void __launch_bounds__(NT, (kAlt ? 5 : 4) * 256 / NT) token_logprobs_
   constexpr int W = Vec<E>::W, kWarps = NT / 32;
   extern __shared__ __align__(16) unsigned char dyn[];
   Shared<NT>& sh = *reinterpret_cast<Shared<NT>*>(dyn);
-  float* gmax = reinterpret_cast<float*>(dyn + sizeof(Shared<NT>));
+  uint32_t* gmax = reinterpret_cast<uint32_t*>(dyn + sizeof(Shared<NT>));
   const int tid = threadIdx.x, lane = tid % 32;
   const unsigned row = blockIdx.x >> log_cluster, rank = blockIdx.x & (unsigned)(cluster - 1);
   const Grid<E, NT> g(static_cast<const E*>(P.logits) + (size_t)row * P.ld, P.V, (int)rank, per);
@@ -426,10 +444,11 @@ __global__ void __launch_bounds__(NT, (kAlt ? 5 : 4) * 256 / NT) token_logprobs_
     }
     return m;
   };
-  auto group = [&](int q, float m) {   // the round's maximum to its group's
-    top = max_nan(top, m);
-    float* at = gmax + (q >> shift) * NT + tid;
-    *at = shift && (q & ((1 << shift) - 1)) ? max_nan(*at, m) : m;
+  auto group = [&](int q, float a, float b) {   // the maxima of the round's halves to its group's
+    top = max_nan(top, max_nan(a, b));
+    uint32_t* at = gmax + (q >> shift) * NT + tid;
+    const uint32_t w = Tops<E>::of(a, b);
+    *at = shift && (q & ((1 << shift) - 1)) ? Tops<E>::both(*at, w) : w;
   };
   if (rounds > 0) {
     fetch(v[0], 0, 0);
@@ -441,10 +460,10 @@ __global__ void __launch_bounds__(NT, (kAlt ? 5 : 4) * 256 / NT) token_logprobs_
         fetch(v[0], q + 1, 0);
         const float b = eat(v[1], false, q, 2);
         fetch(v[1], q + 1, 2);
-        group(q, max_nan(a, b));
+        group(q, a, b);
       }
       const float a = eat(v[0], true, rounds - 1, 0), b = eat(v[1], true, rounds - 1, 2);
-      group(rounds - 1, max_nan(a, b));
+      group(rounds - 1, a, b);
     } else {
       int q = 0;
 #pragma unroll 1
