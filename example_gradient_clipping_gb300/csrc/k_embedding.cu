@@ -1,7 +1,8 @@
 // Embedding lookup, y_r = scale w[token_r], and the order of its gradients: the tokens sorted.
 //
-// Lookup: one read of the rows met and one write, bound by HBM (262144 rows of 1024 bf16, V = 131072: 108 us, of
-// which 80 are the write at the copy rate; 16384 rows of 768, V = 50257: 8.2 us).
+// Lookup: one read of the rows met and one write, bound by HBM (262144 rows of 1024 bf16, V = 131072: 103 us, of
+// which 80 are the write at the copy rate, 108 with stores that the caches keep; 16384 rows of 768, V = 50257: 7.4
+// us, 8.2).
 //
 // Order: the positions sorted by their tokens, stably (least significant digit first), so that equal tokens
 // stand in the order of their positions and, among them, example by example.  Up to 16384 tokens in one launch: 1024
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(256) embed_lookup_kernel(EmbedParams P) {
       for (int n = 0; n < VEC; ++n) f[n] = src[i] ? v[i].get(n) * P.scale : __int_as_float(0x7fc00000);
       V o;
       o.set(f);
-      *reinterpret_cast<V*>(y + (size_t)i * P.D + c) = o;
+      st_once(y + (size_t)i * P.D + c, o);
     }
   }
   pdl_trigger();
@@ -136,7 +137,8 @@ __device__ __forceinline__ void clear_bytes(void* p, size_t bytes, unsigned cta,
   uint4* v = reinterpret_cast<uint4*>(a16);
   const size_t n = (e16 - a16) / 16, step = (size_t)ctas * 1024;
 #pragma unroll 4
-  for (size_t i = (size_t)cta * 1024 + threadIdx.x; i < n; i += step) v[i] = make_uint4(0, 0, 0, 0);
+  for (size_t i = (size_t)cta * 1024 + threadIdx.x; i < n; i += step)
+    asm volatile("st.global.cs.v4.u32 [%0], {%1, %1, %1, %1};" ::"l"(v + i), "r"(0) : "memory");
 }
 
 // Up to 1024 tokens a CTA of a cluster of CL, one a thread, all passes in shared memory: a pass counts its digits, tells every
@@ -399,8 +401,8 @@ using namespace dpk::embed;
 
 template <class E, int VEC>
 static cudaError_t run_lookup(const EmbedParams& P, cudaStream_t s) {
-  // four rows a warp once that leaves an SM's warps one round: 16384 rows of 768 bf16 8.2 us (a row a warp 8.9),
-  // 262144 of 64 24 (34); 6000 of 768 4.9 with a row a warp (5.4 with four)
+  // four rows a warp once that leaves an SM's warps one round: 16384 rows of 768 bf16 7.4 us (a row a warp 7.6),
+  // 262144 of 64 23.7 (34.2); 4000 of 768 3.3 with a row a warp (3.7 with four)
   if (P.N >= 2 * 152 * 32)
     return launch_operator(embed_lookup_kernel<E, VEC, 4>, dim3((unsigned)((P.N + 31ll) / 32)), dim3(256), 0, s, P);
   return launch_operator(embed_lookup_kernel<E, VEC, 1>, dim3((unsigned)((P.N + 7ll) / 8)), dim3(256), 0, s, P);
@@ -499,10 +501,11 @@ static cudaError_t run_sort(const EmbedParams& P, int passes, int bits, int* ord
   return run_tile_sort<kTileKeys / 256, BITS>(P, passes, bits, order, keys, ws, s);
 }
 
-// Beside a sort by one cluster the other SMs have nothing to do: 16384 tokens and 50257 x 768 bf16, sorted and summed,
-// 32.4 us (34.5 where the sum writes the zeros), 8192 and 32000 x 512 fp32 25.5 (28.7).  What takes much longer
-// than the sort is left to the sum, which then reads beside it: 4000 and 128000 x 1024 bf16 52.7 (55.4 cleared).
-bool embed_order_clears(int N, size_t bytes) { return N <= kSmallSort && bytes <= (size_t)128 << 20; }
+// Beside a sort by one cluster the other SMs have nothing to do: 8192 tokens and 32000 x 512 fp32, sorted and summed,
+// 25.2 us (28.7 where the sum writes the zeros), 4000 and 50257 x 197 fp32 16.3 (21.6).  What takes longer than the
+// sort is left to the sum, which then reads beside it: 16384 and 50257 x 768 bf16 32.6 (33.6 cleared), 64 and the
+// same 16.9 (18.9), 4000 and 128000 x 1024 bf16 50.3 (55.4).
+bool embed_order_clears(int N, size_t bytes) { return N <= kSmallSort && bytes <= (size_t)64 << 20; }
 cudaError_t launch_embed_order(const EmbedParams& P, int* order, int* keys, void* ws, size_t bytes, cudaStream_t s) {
   int passes, bits;
   digits(P.V, &passes, &bits);

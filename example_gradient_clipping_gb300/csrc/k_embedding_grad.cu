@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(256) embed_runs_kernel(EmbedParams P, int U) {
         absent &= absent - 1;
         O* dst = static_cast<O*>(P.dW) + (size_t)(v0 + t) * P.D;
 #pragma unroll 4
-        for (int c = lane * W; c < P.D; c += 32 * W) *reinterpret_cast<Pack<O, W>*>(dst + c) = zero;
+        for (int c = lane * W; c < P.D; c += 32 * W) st_once(dst + c, zero);
       }
     }
     return;

@@ -177,6 +177,16 @@ struct EmbedParams {
   dp_row_strides dy;
 };
 
+// A store of what this kernel does not read again, which caches need not keep.
+template <class E, int N> __device__ __forceinline__ void st_once(E* p, const Pack<E, N>& v) {
+  if constexpr (sizeof(v) == 16) {
+    const uint4 u = *reinterpret_cast<const uint4*>(&v);
+    asm volatile("st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
+  } else {
+    *reinterpret_cast<Pack<E, N>*>(p) = v;
+  }
+}
+
 }  // namespace dpk
 
 namespace dph {
