@@ -8,17 +8,18 @@
 // x = z log2(e) / tau - R is one rounded multiply-add: R is a number of fp32, so its own rounding moves every
 // x alike, and no large logits cancel.  R moves only when the maximum outgrows it by 2^8.  For the
 // alternatives the vectors that a thread reads together keep their maximum on chip (of bf16 each half's, in one
-// word: half as much is read again, top 50 90 -> 87 us, top 128 128 -> 120; each vector's in two words would take the
-// room of L1: 104).  The K-th largest of the 256
+// word: half as much is read again, top 50 90 -> 87 us, top 128 128 -> 120; each vector's in two words takes room
+// from L1: 104).  The K-th largest of the 256
 // threads' maxima is a bound that at least K logits reach, and usually few more: only groups of vectors
 // whose maximum reaches it are read again, and what reaches it is ranked by (value, index).  Where more logits
 // reach it than there is room for (many equal ones), the exact K-th largest value is found by bisection, and
 // its ties are taken in the order of their indices.
-// A row is one CTA's (64, 128 or 256 threads), or with few rows a cluster's.  4096 rows of 50257 bf16: 60.7 us, 6.8
-// TB/s, bound by HBM; with the 20 largest 76.7 us and the 50 largest 86.5, where what follows the row's last load (sums,
+// A row is one CTA's (64, 128 or 256 threads), or with few rows a cluster's.  4096 rows of 50257 bf16: 65.6 us, 6.3
+// TB/s, bound by HBM; with the 20 largest 79.5 us and the 50 largest 87, where what follows the row's last load (sums,
 // bound, groups read again, ranking: a third of a CTA's time) is only half hidden under the rows beside it.
-// Reading ahead did not help: the next row asked into L2 while this one is ranked 97 -> 99 to 137 us; nor did a
-// cluster of two for every row (68 -> 83), nor collecting by warps instead of by the CTA (97 -> 101).
+// Reading ahead did not help (the next row asked into L2 while this one is ranked: top 50 97 -> 99 to 137 us), nor loads
+// that pass L1 by (65.6, top 20 79.5 -> 82), nor a cluster of two for every row (68 -> 83), nor collecting by warps
+// instead of by the CTA (97 -> 101).
 //
 // Gradient: one read and one write of the rows, elementwise from m, ls and the entropy.  Bound by HBM: 4096 rows of
 // 50257 bf16 127 us, 6.5 TB/s; 2048 of 131071 164 us.
@@ -58,13 +59,6 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {   // two 
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-// 16 bytes, kOnce: not kept in L1.
-template <bool kOnce, class E> __device__ __forceinline__ Pack<E, 16 / sizeof(E)> ld16(const E* p) {
-  if constexpr (!kOnce) return *reinterpret_cast<const Pack<E, 16 / sizeof(E)>*>(p);
-  uint4 u;
-  asm("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
-  return *reinterpret_cast<const Pack<E, 16 / sizeof(E)>*>(&u);
 }
 // The largest entry of N vectors (NaN if there is one).
 template <int N> __device__ __forceinline__ float top_of(const Vec<__nv_bfloat16> (&v)[N]) {
@@ -392,7 +386,7 @@ __device__ void far_sums(const Grid<E, NT>& g, float m, float c2, float* sum, fl
   *sumx = t;
 }
 
-template <class E, bool kAlt, int NT, bool kOnce>
+template <class E, bool kAlt, int NT>
 __global__ void __launch_bounds__(NT, (kAlt ? 5 : 4) * 256 / NT) token_logprobs_kernel(LogprobParams P, int log_cluster, int per, int shift) {
   pdl_wait();
   const int cluster = 1 << log_cluster;
@@ -424,7 +418,7 @@ __global__ void __launch_bounds__(NT, (kAlt ? 5 : 4) * 256 / NT) token_logprobs_
     } else {
       const E* p = first + (long long)q * (NT * kFly * W);
 #pragma unroll
-      for (int f = 0; f < kPart; ++f) d[f].p = ld16<kOnce, E>(p + (f0 + f) * NT * W);
+      for (int f = 0; f < kPart; ++f) d[f].p = *reinterpret_cast<const Pack<E, W>*>(p + (f0 + f) * NT * W);
     }
   };
   auto eat = [&](Vec<E> (&d)[kPart], bool last, int q, int f0) {   // returns their maximum
@@ -692,7 +686,7 @@ namespace dph {
 using namespace dpk;
 using namespace dpk::logprobs;
 
-template <class E, bool kAlt, int NT, bool kOnce>
+template <class E, bool kAlt, int NT>
 static cudaError_t run_logprobs(const LogprobParams& P, cudaStream_t s) {
   constexpr int W = Vec<E>::W;
   const long long rows = (long long)P.B * P.T;
@@ -709,7 +703,7 @@ static cudaError_t run_logprobs(const LogprobParams& P, cudaStream_t s) {
   while (max_groups<NT>(per, shift) > 4096) ++shift;
   const size_t smem = sizeof(Shared<NT>) +
                       (kAlt ? (size_t)max_groups<NT>(per, shift) * 4 + (cluster > 1 ? (size_t)cluster * P.K * 8 : 0) : 0);
-  auto kernel = token_logprobs_kernel<E, kAlt, NT, kOnce>;
+  auto kernel = token_logprobs_kernel<E, kAlt, NT>;
   if (cluster == 1) return launch_operator(kernel, dim3((unsigned)rows), dim3(NT), smem, s, P, 0, per, shift);
   return launch_operator_cluster(kernel, cluster, dim3((unsigned)(rows * cluster)), dim3(NT), smem, s, P, log_cluster,
                                  per, shift);
@@ -722,19 +716,12 @@ template <class E> static cudaError_t run_logprobs_nt(const LogprobParams& P, cu
   // 99.9 on 128, 102 on 256, top 100 907 and 115) and long rows leave more candidates (131071 top 20: 103 and 97),
   // and rows that do not fill the GPU want more threads each (300 of 32000 top 20: 9.3 and 8.3).
   const long long rows = (long long)P.B * P.T, nvec = P.V / Vec<E>::W;
-  // kOnce: loads that L1 does not keep, which leaves it to the loads under way (4096 rows of 50257 bf16 60.7 us, 65.7
-  // kept; top 20 76.7 and 79.2); but what is read again is then further away, which shorter rows (32000 top 20 17.9,
-  // 17.2 kept) and more alternatives (top 128 126, 120 kept) pay for.
   const bool many = rows >= 608;
-  if (P.K == 0) {
-    if (!many) return run_logprobs<E, false, 256, true>(P, s);
-    return nvec <= 2048 ? run_logprobs<E, false, 64, true>(P, s) : run_logprobs<E, false, 128, true>(P, s);
-  }
-  if (many && nvec <= 2048 && P.K <= 32) return run_logprobs<E, true, 64, false>(P, s);
-  const bool once = many && nvec >= 6144 && P.K <= 48;
-  if (many && P.K <= 64 && nvec <= 8192)
-    return once ? run_logprobs<E, true, 128, true>(P, s) : run_logprobs<E, true, 128, false>(P, s);
-  return once ? run_logprobs<E, true, 256, true>(P, s) : run_logprobs<E, true, 256, false>(P, s);
+  if (many && nvec <= 2048 && P.K <= 32)
+    return P.K ? run_logprobs<E, true, 64>(P, s) : run_logprobs<E, false, 64>(P, s);
+  if (many && (P.K == 0 || (P.K <= 64 && nvec <= 8192)))
+    return P.K ? run_logprobs<E, true, 128>(P, s) : run_logprobs<E, false, 128>(P, s);
+  return P.K ? run_logprobs<E, true, 256>(P, s) : run_logprobs<E, false, 256>(P, s);
 }
 
 cudaError_t launch_logprobs(const LogprobParams& P, int dtype, cudaStream_t s) {
