@@ -108,7 +108,8 @@ template <> struct Tops<float> {
 __device__ __forceinline__ void none(Vec<__nv_bfloat16>& v) { v.p.w[0] = v.p.w[1] = v.p.w[2] = v.p.w[3] = 0xff80ff80u; }
 __device__ __forceinline__ void none(Vec<float>& v) { v.p.w[0] = v.p.w[1] = v.p.w[2] = v.p.w[3] = -INFINITY; }
 
-// The smallest value whose key reaches k; 0 gives a NaN, which no value is below.
+// A value that none whose key reaches k is below.  A NaN, below which nothing is, where k is of no number (0, or above
+// +inf's): what must reach such a k is told by its key.
 __device__ __forceinline__ float value_of(unsigned k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
 // The row on the grid of 16-byte vectors: its first entry is entry `mis` of vector 0.  A part of it is the
@@ -235,11 +236,12 @@ __device__ void part_top(const Grid<E, NT>& g, int shift, const uint32_t* gmax, 
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       const float x = v.get(i);
-      if (!(x < low)) {   // (a NaN passes)
+      if (!(x < low)) {   // (few; the exact test is of the key)
         const int e = j * W - g.mis + i;
-        if (e < 0 || e >= g.V) continue;
+        const unsigned key = key_of(x);
+        if (key < least || e < 0 || e >= g.V) continue;
         const int at = atomicAdd(&sh.count, 1);
-        if (at < kRoom) sh.room[at] = (unsigned long long)key_of(x) << 32 | (unsigned)~e;
+        if (at < kRoom) sh.room[at] = (unsigned long long)key << 32 | (unsigned)~e;
       }
     }
   };
@@ -307,7 +309,7 @@ __device__ void part_top(const Grid<E, NT>& g, int shift, const uint32_t* gmax, 
         if (key_of(Top::all(gmax[q])) > bound)
           for (int i = 0; i < size && g.vector(q, i, shift) < g.j1; ++i) collect(g.vector(q, i, shift), bound + 1);
     __syncthreads();
-    have = sh.count;   // < n
+    have = min(sh.count, n);   // (fewer than n exceed the n-th largest)
     // its ties, lowest index first
     for (int base = g.j0; base < g.j1 && have < n; base += NT) {
       const int j = base + tid;
