@@ -133,27 +133,25 @@ class ClipStep:
         # the sorted tokens of embeddings, from their norm call to their sum
         self.order = [torch.empty(dp_embedding_order_size(d), dtype=torch.uint8, device=dev)
                       if isinstance(d, EmbeddingDesc) else None for d in self.descs]
-        # each layer's blocks of the flat gradient, its norms and its factors, made once: a view costs the host
-        # about a microsecond
-        self._views = []
-        for d, o, (p, D) in zip(self.descs, self.offsets, self.shapes):
-            self._views.append((self.grad[o:o + p * D], self.grad[o + p * D:o + p * D + p] if d.has_bias else None))
-        self._sq = [self.sqnorms[l] for l in range(L)]
-        self._fac = [self.factors[l if self.per_layer else 0] for l in range(L)]
 
+    # grad, sqnorms and factors are sliced when they are used: a caller may have put buffers of its own there
     def layer_views(self, l: int) -> Tuple:
-        return self._views[l]
+        p, D = self.shapes[l]
+        o = self.offsets[l]
+        dW = self.grad[o:o + p * D]
+        db = self.grad[o + p * D:o + p * D + p] if self.descs[l].has_bias else None
+        return dW, db
 
     def norms(self, inputs, stream=None) -> None:
         for l, (d, (A, G)) in enumerate(zip(self.descs, inputs)):
             if _beside(d):
-                _beside_sqnorms(d, A, G, self.order[l], self._sq[l], self.workspace, stream)
+                _beside_sqnorms(d, A, G, self.order[l], self.sqnorms[l], self.workspace, stream)
             elif self.kept[l] is not None:
-                dp_layer_sqnorms_keep(d, A, G, self._sq[l], self.kept[l], self.workspace, stream=stream)
+                dp_layer_sqnorms_keep(d, A, G, self.sqnorms[l], self.kept[l], self.workspace, stream=stream)
                 self.chosen[l] = DP_NORM_INSTANTIATE
             else:
                 ws = self.own_ws[l] if self.own_ws[l] is not None else self.workspace
-                self.chosen[l] = dp_layer_sqnorms(d, A, G, self._sq[l], ws, mode=self.modes[l], stream=stream)
+                self.chosen[l] = dp_layer_sqnorms(d, A, G, self.sqnorms[l], ws, mode=self.modes[l], stream=stream)
 
     def adaptive_(self, seed: int = 0, seed_dev=None, stream=None) -> None:
         """The adaptive bound of every layer from the norms just formed, all layers in one
@@ -174,7 +172,7 @@ class ClipStep:
     def sums(self, inputs, stream=None) -> None:
         for l, (d, (A, G)) in enumerate(zip(self.descs, inputs)):
             dW, db = self.layer_views(l)
-            fac = self._fac[l]
+            fac = self.factors[l] if self.per_layer else self.factors[0]
             if _beside(d):
                 _beside_sum(d, A, G, self.order[l], fac, dW, self.workspace, False, stream)
             elif self.kept[l] is not None:
@@ -195,7 +193,7 @@ class ClipStep:
         blocks = []
         for l, (d, (A, G)) in enumerate(zip(self.descs, inputs)):
             dW, db = self.layer_views(l)
-            fac = self._fac[l]
+            fac = self.factors[l] if self.per_layer else self.factors[0]
             C = self.C[l] if self.per_layer else self.C[0]
             if _beside(d) or (d.kind != DP_LINEAR and self.kept[l] is None):
                 p, D = self.shapes[l]
