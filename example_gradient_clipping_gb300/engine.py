@@ -23,7 +23,7 @@ arrives in PyTorch's channels_last memory format are handed over channels last (
 copy); their output gradients are brought to the same format.  dp.Embedding (tokens [B, ...]) is
 clipped by its tokens and output gradient, dp.LayerNorm (inputs [B, ..., D]) by the per-example gradients
 that its backward pass leaves in place of their sum; torch's own two modules are not taken.  A layer is called
-once in a step, and its weight is its own.  Every trainable parameter of the model must belong to such a layer.
+once in a step, and its weight and bias are its own.  Every trainable parameter of the model must belong to such a layer.
 Activations right after them must not be in-place (the backward hook reads the layer's
 output gradient).  PyTorch warns that the hook fires on output gradients when the model
 input needs no gradient; that gradient is the one wanted here.
@@ -52,25 +52,18 @@ class PrivacyEngine:
         self.norm_mode, self.keep_grads = norm_mode, keep_grads
         self.layers: List = []
         owned = set()
-        beside = set()   # parameters of embeddings and layer norms, which no other layer may share
         for m in model.modules():
             if isinstance(m, (nn.Linear, Embedding, LayerNorm) + convs) and m.weight is not None and m.weight.requires_grad:
                 if isinstance(m, convs):
                     self._check_conv(m)
-                if id(m.weight) in owned and (isinstance(m, (Embedding, LayerNorm)) or id(m.weight) in beside):
-                    raise ValueError(f"{m}: shares its weight with another layer, which is not clipped here")
-                if isinstance(m, (Embedding, LayerNorm)):
-                    beside.add(id(m.weight))
-                    if isinstance(m, Embedding):
-                        self.layers.append(m)
-                        owned.add(id(m.weight))
-                        continue
-                if m.bias is not None and not m.bias.requires_grad:
+                bias = getattr(m, "bias", None)
+                if bias is not None and not bias.requires_grad:
                     raise ValueError(f"{m}: a bias must be trainable with its weight")
+                for what, prm in (("weight", m.weight), ("bias", bias)):
+                    if prm is not None and id(prm) in owned:   # its gradient would be the last layer's part alone
+                        raise ValueError(f"{m}: shares its {what} with another layer, which is not clipped here")
+                    owned.add(id(prm))
                 self.layers.append(m)
-                owned.add(id(m.weight))
-                if m.bias is not None:
-                    owned.add(id(m.bias))
         for name, prm in model.named_parameters():
             if prm.requires_grad and id(prm) not in owned:
                 raise ValueError(f"parameter {name}: only nn.Linear, nn.Conv1d/2d/3d, dp.Embedding and dp.LayerNorm "

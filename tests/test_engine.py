@@ -176,3 +176,33 @@ def test_engine_mean_loss_equals_sum_loss(lib, no_tf32):
         outs.append(eng.privatise(seed=5).double().cpu().numpy())
         eng.detach()
     assert _rel(outs[1], outs[0], model) <= 1e-5
+
+
+def _two(a, b, what):
+    setattr(b, what, getattr(a, what))
+    return nn.Sequential(a, b)
+
+
+@pytest.mark.parametrize("kinds,what", [
+    (("norm", "norm"), "bias"), (("norm", "linear"), "bias"), (("linear", "norm"), "bias"), (("linear", "linear"), "bias"),
+    (("conv", "linear"), "bias"), (("norm", "norm"), "weight"), (("linear", "linear"), "weight"), (("conv", "conv"), "weight"),
+    (("embed", "linear"), "weight"), (("linear", "embed"), "weight"), (("embed", "embed"), "weight")])
+def test_engine_refuses_shared_parameters(kinds, what):
+    """A parameter of two layers: its examples' gradients are sums over both, which no layer's clipping sees."""
+    import example_gradient_clipping_gb300 as lib
+    make = {"norm": lambda: lib.LayerNorm(4), "linear": lambda: nn.Linear(4, 4), "conv": lambda: nn.Conv2d(4, 4, 1),
+            "embed": lambda: lib.Embedding(4, 4)}
+    a, b = (make[k]() for k in kinds)
+    with pytest.raises(ValueError, match=f"shares its {what}"):
+        lib.PrivacyEngine(_two(a, b, what))
+    lib.PrivacyEngine(nn.Sequential(*(make[k]() for k in kinds))).detach()
+    # one layer's weight as its own bias
+    both = lib.LayerNorm(4)
+    both.bias = both.weight
+    with pytest.raises(ValueError, match="shares its bias"):
+        lib.PrivacyEngine(nn.Sequential(nn.Linear(4, 4), both))
+    # frozen ones may be shared: they have no gradient
+    a, b = (make[k]() for k in kinds)
+    for m in (a, b):
+        m.requires_grad_(False)
+    lib.PrivacyEngine(nn.Sequential(_two(a, b, what), nn.Linear(4, 4))).detach()
