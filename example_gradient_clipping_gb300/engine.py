@@ -21,8 +21,9 @@ nn.Conv2d and nn.Conv3d (square or cubic kernels, equal stride / padding / dilat
 dimension), the conv layers with groups 1 and zero padding.  Conv2d/Conv3d layers whose input
 arrives in PyTorch's channels_last memory format are handed over channels last (no layout
 copy); their output gradients are brought to the same format.  dp.Embedding (tokens [B, ...]) is
-clipped by its tokens and output gradient, dp.LayerNorm (inputs [B, ..., D]) by the per-example gradients
-that its backward pass leaves in place of their sum; torch's own two modules are not taken.  A layer is called
+clipped by the tokens and the output gradient, dp.LayerNorm (inputs [B, ..., D]) by the per-example gradients,
+that its backward pass leaves in place of its parameters' gradients (their .grad is privatise's alone); torch's
+own two modules are not taken.  A layer is called
 once in a step, and its weight and bias are its own.  Every trainable parameter of the model must belong to such a layer.
 Activations right after them must not be in-place (the backward hook reads the layer's
 output gradient).  PyTorch warns that the hook fires on output gradients when the model
@@ -77,9 +78,14 @@ class PrivacyEngine:
         for m in self.layers:
             if isinstance(m, LayerNorm) and m._sink is not None:
                 raise ValueError(f"{m}: another engine's (its detach() frees it)")
+        self._sinks = []
         for i, m in enumerate(self.layers):
             if isinstance(m, LayerNorm):
                 m._sink = self._sink(i)
+                continue
+            if isinstance(m, Embedding):
+                self._sinks.append(self._sink(i))
+                m._sinks += (self._sinks[-1],)
                 continue
             self._handles.append(m.register_forward_hook(self._fwd_hook(i)))
             self._handles.append(m.register_full_backward_pre_hook(self._bwd_hook(i)))
@@ -101,15 +107,13 @@ class PrivacyEngine:
 
     def _bwd_hook(self, i):
         def hook(module, grad_output):       # the gradient of the loss w.r.t. the layer output
-            if isinstance(module, Embedding):
-                self._once(i)
             self._grads[i] = grad_output[0].detach()
         return hook
 
     def _sink(self, i):
-        def sink(each):                      # a layer norm's per-example gradients
+        def sink(a, g=None):   # a layer norm's per-example gradients; an embedding's tokens and output gradient
             self._once(i)
-            self._acts[i] = each
+            self._acts[i], self._grads[i] = a, g
         return sink
 
     def _once(self, i) -> None:
@@ -128,6 +132,9 @@ class PrivacyEngine:
         for m in self.layers:
             if isinstance(m, LayerNorm):
                 m._sink = None
+            elif isinstance(m, Embedding):
+                m._sinks = tuple(s for s in m._sinks if s not in self._sinks)
+        self._sinks = []
 
     @staticmethod
     def _layout(m, a) -> int:

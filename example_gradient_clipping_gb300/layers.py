@@ -7,8 +7,8 @@
 The three take part in autograd; embedding_backward, layer_norm_forward, layer_norm_backward,
 token_logprobs_forward and token_logprobs_backward are the same computations without it.  dp.Embedding
 and dp.LayerNorm are torch's modules over them, and what PrivacyEngine clips per example:
-an embedding by its tokens and output gradient, a layer norm by the per-example gradients that its
-backward pass leaves.  embedding_desc and kept_desc describe both to ClipStep.
+an embedding by the tokens and the output gradient, a layer norm by the per-example gradients, that its
+backward pass leaves in place of the parameters' gradients.  embedding_desc and kept_desc describe both to ClipStep.
 
 include/dpclip_seq.h states the formulas; the conventions are those of sequence.py (streams, checks, errors).
 """
@@ -444,9 +444,9 @@ def embedding_sqnorms(tokens, dy, V: int, scale: float = 1.0, padding: Optional[
 
 class _Embedding(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, tokens, weight, scale, padding):
+    def forward(ctx, tokens, weight, scale, padding, sinks):
         ctx.save_for_backward(tokens)
-        ctx.opts = (weight.shape[0], scale, padding, weight.dtype)
+        ctx.opts, ctx.sinks = (weight.shape[0], scale, padding, weight.dtype), sinks
         return _lookup(tokens, weight, scale, padding)
 
     @staticmethod
@@ -454,17 +454,25 @@ class _Embedding(torch.autograd.Function):
     def backward(ctx, dy):
         tokens, = ctx.saved_tensors
         V, scale, padding, dtype = ctx.opts
-        return None, embedding_backward(tokens, _rows_contiguous(dy), V, scale, padding, dtype=dtype), None, None
+        if ctx.sinks:   # what the examples' own gradients are formed from, in place of their sum
+            for sink in ctx.sinks:
+                sink(tokens, dy)
+            return None, None, None, None, None
+        return None, embedding_backward(tokens, _rows_contiguous(dy), V, scale, padding, dtype=dtype), None, None, None
 
 
 def embedding(tokens, weight, scale: float = 1.0, padding: Optional[int] = None, stream=None):
     """scale * weight[tokens], [B, ..., D], with the gradient of weight [V, D]; tokens int32 or int64 [B, ...].
     The rows of the padding token have no gradient."""
+    return _embedding(tokens, weight, scale, padding, (), stream)
+
+
+def _embedding(tokens, weight, scale, padding, sinks, stream=None):
     scale, padding = float(scale), None if padding is None else int(padding)
     if torch.is_grad_enabled() and weight.requires_grad:
         if stream is not None:
             raise ValueError("a differentiable call runs on the current stream")
-        return _Embedding.apply(tokens, weight, scale, padding)
+        return _Embedding.apply(tokens, weight, scale, padding, sinks)
     if stream is not None:
         with _on(stream, tokens.device):
             return _lookup(tokens, weight, scale, padding)
@@ -600,6 +608,7 @@ class Embedding(torch.nn.Embedding):
         if self.max_norm is not None or self.scale_grad_by_freq or self.sparse:
             raise ValueError("max_norm, scale_grad_by_freq and sparse gradients are not there")
         self.scale = float(scale)
+        self._sinks = ()   # where a backward pass leaves the tokens and the output gradient (set by PrivacyEngine)
 
     def forward(self, tokens):
-        return embedding(tokens.contiguous(), self.weight, self.scale, self.padding_idx)
+        return _embedding(tokens.contiguous(), self.weight, self.scale, self.padding_idx, self._sinks)

@@ -1,0 +1,148 @@
+"""What PrivacyEngine takes from embeddings and layer norms: of the calls that are differentiated, and of those alone.
+
+On the CPU the two operators are replaced by torch's, so that autograd's side runs without a GPU."""
+import pytest
+import torch
+import torch.nn as nn
+
+from host_library import STREAM, Host
+
+pytestmark = pytest.mark.filterwarnings("ignore:Full backward hook is firing")
+
+B, T, V, D = 4, 6, 11, 8
+
+
+def _on_the_cpu(monkeypatch):
+    import example_gradient_clipping_gb300.layers as layers
+
+    def forward(x, w, b, eps):
+        mean, var = x.mean(-1), x.var(-1, unbiased=False)
+        rstd = 1 / torch.sqrt(var + eps)
+        return nn.functional.layer_norm(x, x.shape[-1:], w, b, eps), mean, rstd
+
+    def backward(dy, x, w, mean, rstd, bias=True, per_example=False, dx=True, params=True):
+        h = (x - mean[..., None]) * rstd[..., None]
+        u = dy * w
+        gx = rstd[..., None] * (u - u.mean(-1, keepdim=True) - h * (u * h).mean(-1, keepdim=True))
+        each = torch.cat([(dy * h).flatten(1, -2).sum(1)] + ([dy.flatten(1, -2).sum(1)] if bias else []), 1)
+        if per_example:
+            return gx, each
+        return gx, each[:, :x.shape[-1]].sum(0), each[:, x.shape[-1]:].sum(0) if bias else None
+
+    def grad(tokens, dy, V, scale=1.0, padding=None, factors=None, dtype=torch.float32, stream=None):
+        w = torch.zeros(V, dy.shape[-1]).index_add_(0, tokens.flatten().long(), scale * dy.flatten(0, -2))
+        if padding is not None:
+            w[padding] = 0
+        return w.to(dtype)
+    monkeypatch.setattr(layers, "_lookup", lambda tokens, w, scale, padding: scale * w.detach()[tokens.long()])
+    monkeypatch.setattr(layers, "embedding_backward", grad)
+    monkeypatch.setattr(layers, "layer_norm_forward", forward)
+    monkeypatch.setattr(layers, "layer_norm_backward", backward)
+    monkeypatch.setattr(layers, "_norm", lambda x, w, b, eps, stats: forward(x, w, b, eps))
+
+
+@pytest.fixture(params=["cpu", pytest.param("cuda", marks=pytest.mark.gpu)])
+def device(request, monkeypatch):
+    if request.param == "cpu":
+        _on_the_cpu(monkeypatch)
+    else:
+        request.getfixturevalue("lib")
+    return request.param
+
+
+class _Model(nn.Module):
+    def __init__(self, device, **kw):
+        super().__init__()
+        import example_gradient_clipping_gb300 as dp
+        torch.manual_seed(0)
+        self.embed, self.norm, self.head = dp.Embedding(V, D, **kw), dp.LayerNorm(D), nn.Linear(D, V)
+        self.to(device)
+
+    def forward(self, tokens):
+        return self.head(self.norm(self.embed(tokens)))
+
+
+def _tokens(device, seed=0, b=B, t=T, dtype=torch.int64):
+    return torch.randint(0, V, (b, t), generator=torch.Generator().manual_seed(seed)).to(device, dtype)
+
+
+def _engine(model, **kw):
+    import example_gradient_clipping_gb300 as dp
+    return dp.PrivacyEngine(model, C=0.1, sigma=0.0, **kw)
+
+
+def _privatised(model, tokens, between=lambda model: None):
+    """The flat gradient on a GPU; on the CPU what the engine would take it from."""
+    engine = _engine(model)
+    loss = model(tokens).square().sum()
+    between(model)
+    loss.backward()
+    if tokens.is_cuda:
+        out = [engine.privatise(0).clone()]
+    else:
+        out = [x.clone() for pair in zip(engine._acts[:2], engine._grads[:2]) for x in pair if x is not None]
+    engine.detach()
+    return out
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("t", [T, T + 3, 1])
+@pytest.mark.parametrize("dtype", [torch.int64, torch.int32])
+def test_a_call_between_forward_and_backward(device, grad, t, dtype):
+    """The embedding called with other tokens (to log something) while a backward pass is still to come."""
+    model, tokens = _Model(device), _tokens(device)
+    want = _privatised(model, tokens)
+
+    def log(model):
+        with torch.set_grad_enabled(grad):
+            model.embed(_tokens(device, 1, t=t, dtype=dtype))
+    got = _privatised(model, tokens, log)
+    assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_parameters_under_an_engine_have_no_gradient_but_the_engines(device):
+    model, tokens = _Model(device), _tokens(device)
+    model(tokens).square().sum().backward()
+    plain = model.embed.weight.grad.clone()
+    model.zero_grad()
+    engine = _engine(model)
+    model(tokens).square().sum().backward()
+    assert all(p.grad is None for p in (model.embed.weight, model.norm.weight, model.norm.bias))
+    engine.detach()
+    model.zero_grad()
+    model(tokens).square().sum().backward()
+    assert torch.equal(model.embed.weight.grad, plain)
+
+
+def test_two_engines_take_the_same_embedding(device):
+    """As they take the same linear layer: each has its own copy, and one's end leaves the other's."""
+    model, tokens = _Model(device), _tokens(device)
+    model.norm.requires_grad_(False)   # (a layer norm is one engine's)
+    first, second = _engine(model), _engine(model)
+    loss = model(tokens).square().sum()
+    loss.backward(retain_graph=True)
+    for e in (first, second):
+        assert torch.equal(e._acts[0], tokens) and e._grads[0].shape == (B, T, D)
+        e._acts, e._grads = [None, None], [None, None]
+    first.detach()
+    assert len(model.embed._sinks) == 1
+    model(tokens).square().sum().backward()
+    assert first._acts[0] is None and second._acts[0] is not None
+    second.detach()
+    assert model.embed._sinks == ()
+
+
+def test_descriptors_of_the_differentiated_call(monkeypatch):
+    """The step's sizes come from the tokens and output gradient that belong together."""
+    host = Host()
+    _on_the_cpu(monkeypatch)
+    model = _Model("cpu", padding_idx=2)
+    engine = _engine(model)
+    loss = model(_tokens("cpu")).sum()
+    with torch.no_grad():
+        model.embed(_tokens("cpu", 1, t=50, dtype=torch.int32))
+    loss.backward()
+    with host.installed():
+        engine.privatise(0, stream=STREAM)
+    d = engine._step.descs[0]
+    assert (d.B, d.T, d.V, d.D, d.index_i64, d.padding) == (B, T, V, D, 1, 2)
