@@ -24,7 +24,8 @@ copy); their output gradients are brought to the same format.  dp.Embedding (tok
 clipped by the tokens and the output gradient, dp.LayerNorm (inputs [B, ..., D]) by the per-example gradients,
 that its backward pass leaves in place of its parameters' gradients (their .grad is privatise's alone); torch's
 own two modules are not taken.  A layer is called
-once in a step, and its weight and bias are its own.  Every trainable parameter of the model must belong to such a layer.
+once in a step, and its weight and bias are its own (of an embedding's or a layer norm's, a use outside the
+layer is an error in the backward pass).  Every trainable parameter of the model must belong to such a layer.
 Activations right after them must not be in-place (the backward hook reads the layer's
 output gradient).  PyTorch warns that the hook fires on output gradients when the model
 input needs no gradient; that gradient is the one wanted here.
@@ -80,6 +81,10 @@ class PrivacyEngine:
                 raise ValueError(f"{m}: another engine's (its detach() frees it)")
         self._sinks = []
         for i, m in enumerate(self.layers):
+            if isinstance(m, (Embedding, LayerNorm)):   # their own backward passes give their parameters no gradient
+                for prm in (m.weight, getattr(m, "bias", None)):
+                    if prm is not None:
+                        self._handles.append(prm.register_hook(self._elsewhere(m)))
             if isinstance(m, LayerNorm):
                 m._sink = self._sink(i)
                 continue
@@ -115,6 +120,13 @@ class PrivacyEngine:
             self._once(i)
             self._acts[i], self._grads[i] = a, g
         return sink
+
+    @staticmethod
+    def _elsewhere(m):
+        def hook(grad):   # None from the layer itself; what reaches it all the same, privatise would write over
+            if grad is not None:
+                raise RuntimeError(f"{m}: a parameter is used beside the layer's own call, which is not clipped here")
+        return hook
 
     def _once(self, i) -> None:
         """Raises where one backward pass reaches layer i again: the first call's gradient would be lost."""

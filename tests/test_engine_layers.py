@@ -146,3 +146,32 @@ def test_descriptors_of_the_differentiated_call(monkeypatch):
         engine.privatise(0, stream=STREAM)
     d = engine._step.descs[0]
     assert (d.B, d.T, d.V, d.D, d.index_i64, d.padding) == (B, T, V, D, 1, 2)
+
+
+@pytest.mark.parametrize("use", ["tied head", "of the tokens' rows", "a penalty", "norm weight", "norm bias"])
+def test_parameters_used_beside_their_layer(device, use):
+    """Gradients that reach a parameter around its layer are in no example's, so that pass is an error."""
+    model, tokens = _Model(device), _tokens(device)
+    engine = _engine(model)
+    x = model.norm(model.embed(tokens))
+    loss = model.head(x).sum()
+    if use == "tied head":
+        loss = loss + nn.functional.linear(x, model.embed.weight).sum()
+    elif use == "of the tokens' rows":
+        loss = loss + model.embed.weight[tokens[0]].sum()
+    elif use == "a penalty":
+        loss = loss + model.embed.weight.square().sum()
+    else:
+        loss = loss + (model.norm.weight if use == "norm weight" else model.norm.bias).sum()
+    with pytest.raises(RuntimeError, match="beside the layer's own call"):
+        loss.backward()
+    model.zero_grad()
+    for _ in range(2):   # the engine's gradients are no such use, whether or not they are cleared between steps
+        model(tokens).sum().backward()
+        if tokens.is_cuda:
+            engine.privatise(0)
+            assert all(p.grad is not None for p in model.parameters())
+    # detached values are numbers like others, and without an engine every use is autograd's
+    (model(tokens).sum() + (model.embed.weight.detach() * 2).sum()).backward()
+    engine.detach()
+    (model(tokens).sum() + model.embed.weight.sum() + model.norm.bias.sum()).backward()
