@@ -74,6 +74,7 @@ class PrivacyEngine:
             raise ValueError("the model has no trainable layer that is clipped here")
         self._acts: List = [None] * len(self.layers)
         self._grads: List = [None] * len(self.layers)
+        self._options: List = [()] * len(self.layers)
         self._tasks = [-1] * len(self.layers)   # the backward pass that last reached an embedding or a layer norm
         self._handles = []
         for m in self.layers:
@@ -116,9 +117,11 @@ class PrivacyEngine:
         return hook
 
     def _sink(self, i):
-        def sink(a, g=None):   # a layer norm's per-example gradients; an embedding's tokens and output gradient
+        # of a layer norm: the per-example gradients; of an embedding: the tokens, the output gradient, and the
+        # scale and padding token that the call had
+        def sink(a, g=None, *options):
             self._once(i)
-            self._acts[i], self._grads[i] = a, g
+            self._acts[i], self._grads[i], self._options[i] = a, g, options
         return sink
 
     @staticmethod
@@ -172,11 +175,12 @@ class PrivacyEngine:
         import torch
         import torch.nn as nn
         out = []
-        for m, a, g, lay in zip(self.layers, self._acts, self._grads, layouts):
+        for m, a, g, more, lay in zip(self.layers, self._acts, self._grads, self._options, layouts):
             if isinstance(m, Embedding):
                 V, D = m.weight.shape
+                scale, padding = more
                 out.append(embedding_desc(DP_BF16 if g.dtype == torch.bfloat16 else DP_FP32, B=B, T=a.numel() // B, V=V,
-                                          D=D, scale=m.scale, padding=m.padding_idx, index_i64=a.dtype == torch.int64))
+                                          D=D, scale=scale, padding=padding, index_i64=a.dtype == torch.int64))
                 continue
             hb = m.bias is not None
             if isinstance(m, LayerNorm):
@@ -215,8 +219,10 @@ class PrivacyEngine:
             raise ValueError(f"inputs of dtype {dt}: bf16 or fp32 only")
         dtype = DP_BF16 if dt == torch.bfloat16 else DP_FP32
         layouts = [self._layout(m, a) for m, a in zip(self.layers, self._acts)]
-        key = (B, dtype, tuple(tuple(a.shape) for a in self._acts), tuple(layouts),
-               tuple((a.dtype, g.dtype) for m, a, g in zip(self.layers, self._acts, self._grads) if isinstance(m, Embedding)))
+        # what the step's descriptors and buffers go by
+        key = (B, dtype, self._acts[0].device, tuple(tuple(a.shape) for a in self._acts), tuple(layouts), tuple(
+            (a.dtype, g.dtype, more) for m, a, g, more in zip(self.layers, self._acts, self._grads, self._options)
+            if isinstance(m, Embedding)))
         if self._key != key:
             self._step = ClipStep(self._descs(B, dtype, layouts), C=self.C, sigma=self.sigma, per_layer=self.per_layer,
                                   norm_modes=[self.norm_mode] * len(self.layers), device=str(self._acts[0].device),

@@ -456,7 +456,7 @@ class _Embedding(torch.autograd.Function):
         V, scale, padding, dtype = ctx.opts
         if ctx.sinks:   # what the examples' own gradients are formed from, in place of their sum
             for sink in ctx.sinks:
-                sink(tokens, dy)
+                sink(tokens, dy, scale, padding)
             return None, None, None, None, None
         return None, embedding_backward(tokens, _rows_contiguous(dy), V, scale, padding, dtype=dtype), None, None, None
 

@@ -175,3 +175,53 @@ def test_parameters_used_beside_their_layer(device, use):
     (model(tokens).sum() + (model.embed.weight.detach() * 2).sum()).backward()
     engine.detach()
     (model(tokens).sum() + model.embed.weight.sum() + model.norm.bias.sum()).backward()
+
+
+@pytest.mark.gpu
+def test_an_embedding_whose_options_change_between_steps(lib):
+    """Scale and padding token are the differentiated call's: each step's gradient is a new engine's."""
+    model, tokens = _Model("cuda"), _tokens("cuda")
+    engine = _engine(model)
+    for scale, padding in ((1.0, None), (3.0, None), (3.0, 2), (0.5, 7), (1.0, None)):
+        model.embed.scale, model.embed.padding_idx = scale, padding
+        loss = model(tokens).square().sum()
+        model.embed.scale = 17.0   # after the forward call
+        loss.backward()
+        got = engine.privatise(0).clone()
+        model.embed.scale = scale
+        assert torch.equal(got, _privatised_beside(engine, model, tokens)), (scale, padding)
+
+
+def _privatised_beside(engine, model, tokens):
+    """A new engine's gradient, with `engine` away meanwhile."""
+    sink, model.norm._sink = model.norm._sink, None
+    sinks, model.embed._sinks = model.embed._sinks, ()
+    try:
+        return _privatised(model, tokens)[0]
+    finally:
+        model.norm._sink, model.embed._sinks = sink, sinks
+
+
+@pytest.mark.parametrize("change", ["scale", "padding", "device"])
+def test_the_step_is_built_anew_for_other_options(monkeypatch, change):
+    host = Host()
+    _on_the_cpu(monkeypatch)
+    model = _Model("cpu", padding_idx=2)
+    engine = _engine(model)
+
+    def step():
+        model(_tokens("cpu")).sum().backward()
+        with host.installed():
+            engine.privatise(0, stream=STREAM)
+        return engine._step
+    first = step()
+    assert step() is first and (first.descs[0].scale, first.descs[0].padding) == (1.0, 2)
+    if change == "scale":
+        model.embed.scale = 0.25
+        assert step().descs[0].scale == 0.25
+    elif change == "padding":
+        model.embed.padding_idx = None
+        assert step().descs[0].padding == -1
+    else:   # (as if the model had moved)
+        engine._key = tuple("cuda:1" if isinstance(k, torch.device) else k for k in engine._key)
+        assert step() is not first
