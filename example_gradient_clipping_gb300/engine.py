@@ -119,8 +119,8 @@ class PrivacyEngine:
     def _sink(self, i):
         # of a layer norm: the per-example gradients; of an embedding: the tokens, the output gradient, and the
         # scale and padding token that the call had
-        def sink(a, g=None, *options):
-            self._once(i)
+        def sink(within, a, g=None, *options):
+            self._once(i, within)
             self._acts[i], self._grads[i], self._options[i] = a, g, options
         return sink
 
@@ -131,10 +131,12 @@ class PrivacyEngine:
                 raise RuntimeError(f"{m}: a parameter is used beside the layer's own call, which is not clipped here")
         return hook
 
-    def _once(self, i) -> None:
-        """Raises where one backward pass reaches layer i again: the first call's gradient would be lost."""
+    def _once(self, i, within: int) -> None:
+        """Raises where one backward pass reaches layer i again: the first call's gradient would be lost.  within:
+        the pass in which the call itself ran, -1 for none (a checkpointed segment is run again in the pass that
+        differentiates it, and differentiated by one of its own)."""
         import torch
-        task = torch._C._current_graph_task_id()
+        task = within if within != -1 else torch._C._current_graph_task_id()
         if task == self._tasks[i]:
             raise RuntimeError(f"{self.layers[i]}: called more than once in a step, which is not clipped here")
         self._tasks[i] = task

@@ -183,6 +183,9 @@ def dp_embedding_order_grad(desc: EmbeddingDesc, tokens, order, dY, factors, dW,
                                              _stream(stream)))
 
 
+_pass = torch._C._current_graph_task_id   # the backward pass that runs, or -1
+
+
 # ---- argument checks ------------------------------------------------------------------
 def _rows3(x, name: str):
     """x [B, ..., D] as [B, T, D]."""
@@ -301,7 +304,7 @@ class _LayerNorm(torch.autograd.Function):
     def forward(ctx, x, weight, bias, eps, sink):
         y, mean, rstd = layer_norm_forward(x, weight, bias, eps)
         ctx.save_for_backward(x, weight, mean, rstd)
-        ctx.has_bias, ctx.sink = bias is not None, sink
+        ctx.has_bias, ctx.sink, ctx.within = bias is not None, sink, _pass()
         return y
 
     @staticmethod
@@ -313,7 +316,7 @@ class _LayerNorm(torch.autograd.Function):
         dy = _rows_contiguous(dy)
         if ctx.sink is not None and params:   # each example's own, in place of their sum
             dx, each = layer_norm_backward(dy, x, weight, mean, rstd, ctx.has_bias, True, want[0])
-            ctx.sink(each)
+            ctx.sink(ctx.within, each)
             return dx, None, None, None, None
         dx, dw, db = layer_norm_backward(dy, x, weight, mean, rstd, ctx.has_bias, False, want[0], params)
         return dx, dw if want[1] else None, db if want[2] else None, None, None
@@ -446,7 +449,7 @@ class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, tokens, weight, scale, padding, sinks):
         ctx.save_for_backward(tokens)
-        ctx.opts, ctx.sinks = (weight.shape[0], scale, padding, weight.dtype), sinks
+        ctx.opts, ctx.sinks, ctx.within = (weight.shape[0], scale, padding, weight.dtype), sinks, _pass()
         return _lookup(tokens, weight, scale, padding)
 
     @staticmethod
@@ -456,7 +459,7 @@ class _Embedding(torch.autograd.Function):
         V, scale, padding, dtype = ctx.opts
         if ctx.sinks:   # what the examples' own gradients are formed from, in place of their sum
             for sink in ctx.sinks:
-                sink(tokens, dy, scale, padding)
+                sink(ctx.within, tokens, dy, scale, padding)
             return None, None, None, None, None
         return None, embedding_backward(tokens, _rows_contiguous(dy), V, scale, padding, dtype=dtype), None, None, None
 

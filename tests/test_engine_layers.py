@@ -225,3 +225,36 @@ def test_the_step_is_built_anew_for_other_options(monkeypatch, change):
     else:   # (as if the model had moved)
         engine._key = tuple("cuda:1" if isinstance(k, torch.device) else k for k in engine._key)
         assert step() is not first
+
+
+@pytest.mark.parametrize("reentrant", [True, False])
+@pytest.mark.parametrize("which", ["embed", "norm"])
+def test_a_layer_in_two_checkpointed_segments(device, which, reentrant):
+    """Segments that a backward pass runs again: a layer of two of them is reached twice by one step."""
+    from torch.utils.checkpoint import checkpoint
+    model, tokens = _Model(device), _tokens(device)
+    want = _privatised(model, tokens)
+    engine = _engine(model)
+    on = torch.ones((), device=device, requires_grad=True)   # what a segment needs to be run again
+    first = lambda on: model.embed(tokens) * on              # noqa: E731
+    second = model.norm
+
+    def segments(again):
+        x = checkpoint(first, on, use_reentrant=reentrant)
+        x = checkpoint(second, x, use_reentrant=reentrant)
+        if again:
+            x = checkpoint((lambda x: x + first(on)) if which == "embed" else second, x, use_reentrant=reentrant)
+        return model.head(x).square().sum()
+    with pytest.raises(RuntimeError, match="more than once"):
+        segments(True).backward()
+    with pytest.raises(RuntimeError, match="more than once"):   # one of them in a segment, the other not
+        y = segments(False)
+        x = model.norm(model.embed(tokens)) if which == "embed" else model.norm(torch.zeros(B, T, D, device=device))
+        (y + x.sum()).backward()
+    for _ in range(2):   # once in each pass, the passes not privatised
+        segments(False).backward()
+    if tokens.is_cuda:
+        assert torch.equal(engine.privatise(0), want[0])
+    else:
+        got = [x for pair in zip(engine._acts[:2], engine._grads[:2]) for x in pair if x is not None]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
