@@ -26,9 +26,7 @@ that its backward pass leaves in place of its parameters' gradients (their .grad
 own two modules are not taken.  A layer is called
 once in a step, and its weight and bias are its own (of an embedding's or a layer norm's, a use outside the
 layer is an error in the backward pass).  Every trainable parameter of the model must belong to such a layer.
-Activations right after them must not be in-place (the backward hook reads the layer's
-output gradient).  PyTorch warns that the hook fires on output gradients when the model
-input needs no gradient; that gradient is the one wanted here.
+A and G are those of the call that the backward pass reaches; calls that none reaches change nothing.
 """
 from __future__ import annotations
 
@@ -75,7 +73,7 @@ class PrivacyEngine:
         self._acts: List = [None] * len(self.layers)
         self._grads: List = [None] * len(self.layers)
         self._options: List = [()] * len(self.layers)
-        self._tasks = [-1] * len(self.layers)   # the backward pass that last reached an embedding or a layer norm
+        self._tasks = [-1] * len(self.layers)   # the backward pass that last reached each
         self._handles = []
         for m in self.layers:
             if isinstance(m, LayerNorm) and m._sink is not None:
@@ -94,7 +92,6 @@ class PrivacyEngine:
                 m._sinks += (self._sinks[-1],)
                 continue
             self._handles.append(m.register_forward_hook(self._fwd_hook(i)))
-            self._handles.append(m.register_full_backward_pre_hook(self._bwd_hook(i)))
         self._step: Optional[ClipStep] = None
         self._key = None
 
@@ -107,13 +104,17 @@ class PrivacyEngine:
             raise ValueError(f"{m}: square or cubic kernels with equal stride/padding/dilation in every dimension only")
 
     def _fwd_hook(self, i):
-        def hook(module, inputs, output):
-            self._acts[i] = inputs[0].detach()
-        return hook
+        import torch
 
-    def _bwd_hook(self, i):
-        def hook(module, grad_output):       # the gradient of the loss w.r.t. the layer output
-            self._grads[i] = grad_output[0].detach()
+        def hook(module, inputs, output):
+            if not output.requires_grad:   # no backward pass reaches this call
+                return
+            a, within = inputs[0].detach(), torch._C._current_graph_task_id()
+
+            def taken(g):                  # the gradient of the loss w.r.t. this call's output
+                self._once(i, within)
+                self._acts[i], self._grads[i] = a, g.detach()
+            output.register_hook(taken)
         return hook
 
     def _sink(self, i):

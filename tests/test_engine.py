@@ -206,3 +206,78 @@ def test_engine_refuses_shared_parameters(kinds, what):
     for m in (a, b):
         m.requires_grad_(False)
     lib.PrivacyEngine(nn.Sequential(_two(a, b, what), nn.Linear(4, 4))).detach()
+
+
+def _taken(engine):
+    return [x.clone() for pair in zip(engine._acts, engine._grads) for x in pair]
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("examples,size", [(6, 6), (2, 6), (9, 10)])
+def test_engine_takes_the_differentiated_call(grad, examples, size):
+    """Forward calls of linear and conv layers that no backward pass reaches, of other sizes too, change nothing."""
+    import example_gradient_clipping_gb300 as lib
+    model = _model()
+    gen = torch.Generator().manual_seed(1)
+    x, other = torch.randn(6, 3, 6, 6, generator=gen), torch.randn(examples, 3, size, size, generator=gen)
+    engine = lib.PrivacyEngine(model)
+    model(x).square().sum().backward()
+    want = _taken(engine)
+    for i in range(len(engine.layers)):
+        engine._acts[i] = engine._grads[i] = None
+    loss = model(x).square().sum()
+    with torch.set_grad_enabled(grad):
+        model[2](model[0](other))
+        model[7](torch.randn(examples, 4, 16, generator=gen))
+    loss.backward()
+    assert all(torch.equal(a, b) for a, b in zip(_taken(engine), want))
+    with torch.no_grad():   # nor do calls behind it
+        model[0](other)
+    assert all(torch.equal(a, b) for a, b in zip(_taken(engine), want))
+    engine.detach()
+
+
+def test_engine_refuses_a_linear_layer_reached_twice():
+    import example_gradient_clipping_gb300 as lib
+    model = nn.Sequential(nn.Linear(4, 4), nn.Tanh(), nn.Linear(4, 4))
+    engine = lib.PrivacyEngine(model)
+    x = torch.randn(3, 4)
+    with pytest.raises(RuntimeError, match="more than once"):
+        model[0](model(x)).sum().backward()
+    for _ in range(2):   # passes that were not privatised do not count
+        model(x).sum().backward()
+    engine.detach()
+
+
+def test_engine_with_activations_in_place():
+    """A and G in front of an in-place activation are those of the layer's own output."""
+    import example_gradient_clipping_gb300 as lib
+    torch.manual_seed(0)
+    linears = nn.Linear(5, 4), nn.Linear(4, 3)
+    x, taken = torch.randn(6, 5), []
+    for inplace in (False, True):
+        model = nn.Sequential(linears[0], nn.ReLU(inplace=inplace), linears[1])
+        engine = lib.PrivacyEngine(model)
+        model(x).square().sum().backward()
+        taken.append(_taken(engine))
+        engine.detach()
+    assert all(torch.equal(a, b) for a, b in zip(*taken))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_engine_with_a_call_between_forward_and_backward(lib, dtype):
+    model = _model(dtype).cuda()
+    gen = torch.Generator().manual_seed(1)
+    x, other = torch.randn(6, 3, 6, 6, generator=gen).to(dtype).cuda(), torch.randn(9, 3, 6, 6, generator=gen).to(dtype).cuda()
+    engine, got = lib.PrivacyEngine(model, C=0.5, sigma=0.3), []
+    for log in (False, True):
+        loss = model(x).float().square().sum()
+        if log:
+            with torch.no_grad():
+                model(other)
+                model(x + 1)
+        loss.backward()
+        got.append(engine.privatise(seed=3).clone())
+    assert torch.equal(*got)
+    engine.detach()
