@@ -185,6 +185,7 @@ dp_status dp_example_sum(const float* grads, int B, size_t n, const float* facto
   if (!grads || !factors || !out) return bad(DP_ERR_INVALID_ARG, "grads, factors and out must be non-NULL");
   if (B <= 0 || n == 0) return bad(DP_ERR_INVALID_ARG, "B=%d and n=%zu must be > 0", B, n);
   if (n > (size_t)1 << 35) return bad(DP_ERR_UNSUPPORTED, "n=%zu is above 2^35", n);
+  if (B > kMaxLen) return bad(DP_ERR_UNSUPPORTED, "B=%d is above 2^30", B);   // (rows are counted in steps of 12)
   return launched(dph::launch_rows_sum(grads, 1, B, n, factors, out, 0, accumulate ? 1 : 0, stream), "dp_example_sum");
 }
 

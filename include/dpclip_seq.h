@@ -214,7 +214,8 @@ dp_status dp_layer_norm_grad(const dp_layer_norm_desc* desc, const void* dY, con
 /* ---- Per-example gradients that the caller has -----------------------------------------
  * grads: device fp32 [B, n], one row an example (as dp_layer_norm_grad writes them).
  *   sqnorms[i] = sum_j grads[i, j]^2,   out[j] (+)= sum_i factors[i] grads[i, j].
- * A row of a non-finite gradient spoils `out` also with a factor of 0. */
+ * A row of a non-finite gradient spoils `out` also with a factor of 0.  Of the sum B <= 2^30 and n <= 2^35,
+ * of the norms n <= 2^36. */
 dp_status dp_example_sqnorms(const float* grads, int B, size_t n, float* sqnorms, cudaStream_t stream);
 dp_status dp_example_sum(const float* grads, int B, size_t n, const float* factors, float* out, int accumulate,
                          cudaStream_t stream);
