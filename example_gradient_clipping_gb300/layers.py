@@ -254,6 +254,14 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, stream=None
     return _norm(x, weight, bias, eps, True)
 
 
+def _statistics(s, shape, x, name):
+    """Each row's statistic, of x's own `shape` but its last dimension (or in one dimension), as [B, T]."""
+    n = x.shape[0] * x.shape[1]
+    if (s.shape != shape[:-1] and s.shape != (n,)) or not s.is_contiguous():
+        raise ValueError(f"{name}: contiguous {list(shape[:-1])}, got {list(s.shape)}")
+    return s.view(x.shape[:2])
+
+
 def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, per_example: bool = False, dx: bool = True,
                         params: bool = True, stream=None):
     """(dx, dw, db) for the gradient dy of layer_norm_forward's y; dw and db of the weight's type, db None
@@ -266,13 +274,16 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, per_exampl
         _no_tangents(dy, x, weight, mean, rstd)
     bias, per_example, dx, params = bool(bias), bool(per_example), bool(dx), bool(params)
     shape = x.shape
-    if x.dim() != 3:
-        x, dy = _rows3(x, "x"), _rows3(dy, "dy")
+    if len(shape) != 3:
+        x = _rows3(x, "x")
+        if dy.shape != shape and dy.shape != x.shape:
+            raise ValueError(f"dy: {list(shape)} as x, got {list(dy.shape)}")
+        dy = _rows3(dy, "dy")
     dev = x.get_device()
     if mean.dim() != 2:
-        mean = mean.view(x.shape[:2])
+        mean = _statistics(mean, shape, x, "mean")
     if rstd.dim() != 2:
-        rstd = rstd.view(x.shape[:2])
+        rstd = _statistics(rstd, shape, x, "rstd")
     key = ("layer_norm_backward", x.shape, x.stride(), x.dtype, dev, dy.shape, dy.stride(), dy.dtype, dy.get_device(),
            _opt(weight), _opt(mean), _opt(rstd), bias, per_example)
     d = _get(key) or _keep(key, _norm_desc(x, weight, None, 0.0, dy, mean, rstd, bias, per_example))
@@ -398,6 +409,8 @@ def _grad_desc(tokens, dy, V, scale, padding, factors, dtype):
         _no_tangents(dy, factors)
     V, scale = int(V), float(scale)
     if dy.dim() == tokens.dim() + 1 and dy.dim() != 3:
+        if dy.shape[:-1] != tokens.shape:
+            raise ValueError(f"dy {list(dy.shape)} does not fit tokens {list(tokens.shape)}")
         dy = _rows3(dy, "dy")
     key = ("embedding_backward", tokens.shape, tokens.stride(), tokens.dtype, tokens.get_device(), dy.shape, dy.stride(),
            dy.dtype, dy.get_device(), V, scale, padding, _opt(factors), dtype)
