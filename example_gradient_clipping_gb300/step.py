@@ -134,7 +134,6 @@ class ClipStep:
         self.order = [torch.empty(dp_embedding_order_size(d), dtype=torch.uint8, device=dev)
                       if isinstance(d, EmbeddingDesc) else None for d in self.descs]
 
-    # grad, sqnorms and factors are sliced when they are used: a caller may have put buffers of its own there
     def layer_views(self, l: int) -> Tuple:
         p, D = self.shapes[l]
         o = self.offsets[l]
@@ -142,16 +141,29 @@ class ClipStep:
         db = self.grad[o + p * D:o + p * D + p] if self.descs[l].has_bias else None
         return dW, db
 
+    # Where layer_views(l), sqnorms[l] and a layer's factors lie, for the C calls: in the buffers that are there when
+    # they are used (a caller may have put its own), and by address, for a view costs the host up to three microseconds.
+    def _blocks(self, l: int, grad: int) -> Tuple:
+        p, D = self.shapes[l]
+        dW = grad + 4 * self.offsets[l]
+        return dW, dW + 4 * p * D if self.descs[l].has_bias else None
+
+    def _layer_factors(self) -> List[int]:
+        at, row = self.factors.data_ptr(), 4 * self.factors.stride(0) if self.per_layer else 0
+        return [at + l * row for l in range(len(self.descs))]
+
     def norms(self, inputs, stream=None) -> None:
+        at, row = self.sqnorms.data_ptr(), 4 * self.sqnorms.stride(0)
         for l, (d, (A, G)) in enumerate(zip(self.descs, inputs)):
+            sq = at + l * row
             if _beside(d):
-                _beside_sqnorms(d, A, G, self.order[l], self.sqnorms[l], self.workspace, stream)
+                _beside_sqnorms(d, A, G, self.order[l], sq, self.workspace, stream)
             elif self.kept[l] is not None:
-                dp_layer_sqnorms_keep(d, A, G, self.sqnorms[l], self.kept[l], self.workspace, stream=stream)
+                dp_layer_sqnorms_keep(d, A, G, sq, self.kept[l], self.workspace, stream=stream)
                 self.chosen[l] = DP_NORM_INSTANTIATE
             else:
                 ws = self.own_ws[l] if self.own_ws[l] is not None else self.workspace
-                self.chosen[l] = dp_layer_sqnorms(d, A, G, self.sqnorms[l], ws, mode=self.modes[l], stream=stream)
+                self.chosen[l] = dp_layer_sqnorms(d, A, G, sq, ws, mode=self.modes[l], stream=stream)
 
     def adaptive_(self, seed: int = 0, seed_dev=None, stream=None) -> None:
         """The adaptive bound of every layer from the norms just formed, all layers in one
@@ -170,9 +182,10 @@ class ClipStep:
                         self.factors, stream=stream)
 
     def sums(self, inputs, stream=None) -> None:
+        grad, factors = self.grad.data_ptr(), self._layer_factors()
         for l, (d, (A, G)) in enumerate(zip(self.descs, inputs)):
-            dW, db = self.layer_views(l)
-            fac = self.factors[l] if self.per_layer else self.factors[0]
+            dW, db = self._blocks(l, grad)
+            fac = factors[l]
             if _beside(d):
                 _beside_sum(d, A, G, self.order[l], fac, dW, self.workspace, False, stream)
             elif self.kept[l] is not None:
@@ -191,9 +204,10 @@ class ClipStep:
         theirs from one multi-block noise launch after the sums (dp_add_noise_blocks) instead
         of one noise pass per layer."""
         blocks = []
+        grad, factors = self.grad.data_ptr(), self._layer_factors()
         for l, (d, (A, G)) in enumerate(zip(self.descs, inputs)):
-            dW, db = self.layer_views(l)
-            fac = self.factors[l] if self.per_layer else self.factors[0]
+            dW, db = self._blocks(l, grad)
+            fac = factors[l]
             C = self.C[l] if self.per_layer else self.C[0]
             if _beside(d) or (d.kind != DP_LINEAR and self.kept[l] is None):
                 p, D = self.shapes[l]
@@ -334,8 +348,9 @@ class VirtualStep:
             else:
                 b.chosen[l] = dp_layer_sqnorms(d, A, G, sq[l], b.workspace, mode=b.modes[l], stream=stream)
         dp_clip_factors(sq, B, L, b.per_layer, b.C if b.per_layer else b.C[:1], fac, stream=stream)
+        grad = b.grad.data_ptr()
         for l, (d, (A, G)) in enumerate(zip(descs, inputs)):
-            dW, db = b.layer_views(l)
+            dW, db = b._blocks(l, grad)
             f = fac[l] if b.per_layer else fac[0]
             if _beside(d):
                 _beside_sum(d, A, G, b.order[l], f, dW, b.workspace, True, stream)

@@ -34,7 +34,7 @@ def test_replaced_buffers_are_the_ones_used(host, monkeypatch, per_layer, fuse):
 
         def call(*a, **kw):
             for what, i in where.items():
-                used[what].append(a[i].data_ptr())
+                used[what].append(a[i] if isinstance(a[i], int) else a[i].data_ptr())
             return real(*a, **kw)
         return call
     for name, where in NAMES.items():
@@ -45,6 +45,11 @@ def test_replaced_buffers_are_the_ones_used(host, monkeypatch, per_layer, fuse):
         x = torch.zeros(4, 3, 8)
         inputs = [(torch.zeros(4, 3, dtype=torch.int32), x), (torch.zeros(4, 16), None), (x, torch.zeros(4, 3, 6))]
         assert step.run(inputs, seed=1, stream=STREAM) is step.grad
+        # all of a layer's, one after another
+        L = [0, 1, 2]
+        assert used["sqnorms"][:3] == [step.sqnorms[l].data_ptr() for l in L]
+        assert used["factors"][1:] == [step.factors[l if per_layer else 0].data_ptr() for l in L]
+        assert used["grad"][:3] == [step.layer_views(l)[0].data_ptr() for l in L]
     for what, at in used.items():
         t = getattr(step, what)
         ends = t.data_ptr(), t.data_ptr() + t.numel() * 4
