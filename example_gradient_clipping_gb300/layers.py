@@ -64,7 +64,7 @@ class KeptDesc(ctypes.Structure):
 
 def embedding_desc(dtype: int, B: int, T: int, V: int, D: int, scale: float = 1.0, padding: Optional[int] = None,
                    index_i64: bool = False) -> EmbeddingDesc:
-    """An embedding for ClipStep: tokens [B, T] (int32, or int64 with index_i64) and the output gradient
+    """An embedding for ClipStep: tokens [B, T] (int32, or torch's int64 with index_i64) and the output gradient
     [B, T, D] of type dtype (DP_BF16 or DP_FP32), contiguous; the weight's gradient is fp32 [V, D]."""
     return EmbeddingDesc(dtype, DP_FP32, B, T, V, D, int(bool(index_i64)), -1 if padding is None else int(padding),
                          float(scale), D, RowStrides(T * D, D))
@@ -76,6 +76,23 @@ def kept_desc(B: int, p: int, D: int = 1, has_bias: bool = False) -> KeptDesc:
     if min(B, p, D) <= 0:
         raise ValueError(f"B={B}, p={p} and D={D} must be > 0")
     return KeptDesc(B, p, D, int(bool(has_bias)))
+
+
+def _inputs_of(d):
+    """(name, type, entries) of each input that a step is given for an EmbeddingDesc or a KeptDesc."""
+    if isinstance(d, KeptDesc):
+        return (("gradients", torch.float32, d.B * d.n),)
+    rows = d.B * d.T
+    own = d.dy.b == d.T * d.D and d.dy.t == d.D   # (other strides are the caller's: only the type is looked at)
+    return (("tokens", torch.int64 if d.index_i64 else torch.int32, rows),
+            ("output gradient", torch.bfloat16 if d.dtype == DP_BF16 else torch.float32, rows * d.D if own else 0))
+
+
+def _check_inputs(wants, inputs) -> None:
+    """Raises where a tensor (addresses are the caller's) is of another type or has not its entries one after another."""
+    for (name, dtype, n), x in zip(wants, inputs):
+        if isinstance(x, torch.Tensor) and (x.dtype != dtype or (n and (x.numel() < n or not x.is_contiguous()))):
+            raise ValueError(f"{name}: contiguous {dtype} of {n} entries, got {x.dtype} {list(x.shape)}, strides {x.stride()}")
 
 
 def _declare():

@@ -22,8 +22,9 @@ from . import (DP_LINEAR, DP_NORM_AUTO, DP_NORM_INSTANTIATE, LayerDesc, dp_adapt
                dp_clipped_sum, dp_clipped_sum_kept, dp_clipped_sum_kept_noised, dp_clipped_sum_noised,
                dp_clipped_sum_reuse, dp_grads_size, dp_launch_count, dp_layer_sqnorms, dp_layer_sqnorms_keep,
                dp_layout_reused, dp_plan, dp_workspace_size, noise_desc)
-from .layers import (EmbeddingDesc, KeptDesc, dp_embedding_grad, dp_embedding_order, dp_embedding_order_size,
-                     dp_embedding_sqnorms, dp_embedding_workspace, dp_example_sqnorms, dp_example_sum)
+from .layers import (EmbeddingDesc, KeptDesc, _check_inputs, _inputs_of, dp_embedding_grad, dp_embedding_order,
+                     dp_embedding_order_size, dp_embedding_sqnorms, dp_embedding_workspace, dp_example_sqnorms,
+                     dp_example_sum)
 
 # Instantiated layers with at least this many rows per example keep their per-example
 # gradients by default (the clipped sum then reads them once instead of recomputing a
@@ -133,6 +134,7 @@ class ClipStep:
         # the sorted tokens of embeddings, from their norm call to their sum
         self.order = [torch.empty(dp_embedding_order_size(d), dtype=torch.uint8, device=dev)
                       if isinstance(d, EmbeddingDesc) else None for d in self.descs]
+        self._wants = [_inputs_of(d) if _beside(d) else () for d in self.descs]
 
     def layer_views(self, l: int) -> Tuple:
         p, D = self.shapes[l]
@@ -157,6 +159,7 @@ class ClipStep:
         for l, (d, (A, G)) in enumerate(zip(self.descs, inputs)):
             sq = at + l * row
             if _beside(d):
+                _check_inputs(self._wants[l], (A, G))
                 _beside_sqnorms(d, A, G, self.order[l], sq, self.workspace, stream)
             elif self.kept[l] is not None:
                 dp_layer_sqnorms_keep(d, A, G, sq, self.kept[l], self.workspace, stream=stream)
@@ -344,6 +347,7 @@ class VirtualStep:
         fac = self.fac_flat[:(L if b.per_layer else 1) * B].view(-1, B)
         for l, (d, (A, G)) in enumerate(zip(descs, inputs)):
             if _beside(d):
+                _check_inputs(_inputs_of(d), (A, G))
                 _beside_sqnorms(d, A, G, b.order[l], sq[l], b.workspace, stream)
             else:
                 b.chosen[l] = dp_layer_sqnorms(d, A, G, sq[l], b.workspace, mode=b.modes[l], stream=stream)
