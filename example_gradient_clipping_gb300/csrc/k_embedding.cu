@@ -9,7 +9,7 @@
 // a CTA of a cluster of 1, 8 or 16 that write each digit's keys to one another's shared memory (16384 tokens,
 // V = 50257: 9.9 us, 13.4 in tiles, 26 in one CTA; 4096 tokens a CTA 17.3, for four-byte stores to
 // other SMs are what it then waits for); longer lists in tiles of 1024 keys a CTA: counted, then written to their
-// places (262144 tokens: 21 us, a million 39; tiles of 4096 keys 34 and 58, and 496 against 486 for 16 million).
+// places (262144 tokens: 24 us, a million 39; tiles of 4096 keys 34 and 58, and 496 against 486 for 16 million).
 // Bound by latency.
 #include <algorithm>
 

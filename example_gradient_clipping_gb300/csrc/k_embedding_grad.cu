@@ -10,9 +10,11 @@
 // each lane copies its own 16-byte pieces of the next rows into a ring in shared memory and reads only what it
 // copied.  A run that covers a whole unit is too long for one warp: its units' sums go to partial rows and
 // embed_join_kernel adds them.  The norms and the sums read dy once each; the sum also writes the zero rows
-// of dw.  262144 rows of 1024 bf16, V = 131072: norms 106 us (5.1 TB/s; a run ends every few rows, and
-// its squares are summed before the next one is added), sum to fp32 178 us (6.0 TB/s, bound by HBM).
-// 4000 rows of 197 fp32: 8.6 and 7.2 us, three launches' latency.
+// of dw.  262144 rows of 1024 bf16, V = 131072: norms 108 us (5.0 TB/s; a run ends every few rows, and
+// its squares are summed before the next one is added), sum to fp32 179 us (6.0 TB/s, bound by HBM); the same of fp32 190
+// and 255 us (5.6 and 6.3 TB/s).  4000 rows of 197 fp32: 8.4 and 7.0 us, three launches' latency.
+// Added in fp32 along a lane's columns, the places of a unit, the units and an example's positions: the norms are off by
+// 1e-7 of their value at that size, 3e-8 where each example's whole gradient is squared and summed pairwise.
 #include <algorithm>
 
 #include "seq.cuh"
@@ -395,7 +397,8 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedParams P, int U, i
     const Place run = {__shfl_sync(kAll, mine.key, b), 0, __shfl_sync(kAll, mine.ex, b)};
     const int L = length(b, run);
     // for the whole CTA: one or two of them begin in its units (4000 rows of 197: 7.3 us, 10.4 where only runs of more
-    // than 32 units do; with 32 units a CTA norms of 262144 rows 110 us, 118 where those of more than 8 do)
+    // than 32 units do; with 32 units a CTA, and rings of 6 KB, norms of 262144 rows 110 us, 118 where those of more than
+    // 8 do)
     if (L > per) {
       if (lane == 0) {
         const int i = atomicAdd(&count, 1);
@@ -493,7 +496,7 @@ using namespace dpk::embed;
 // Rows of a unit, which follow one another: 32, or fewer where that would leave an SM less than eight warps (of 16
 // rows: six).  Norms and sums of 48000 rows of 768 bf16, V = 50257: 25.3 and 51 us with 32, 28.1 and 50 with 16, 30.8
 // and 54 with 8; 24000 rows 20.8 and 42.8, 18.4 and 40.6, 22.4 and 44.0; 4000 rows 13.6 and 32.6 with 16, 12.6 and
-// 31.7 with 8.  262144 rows of 1024: 110 and 178 with 32, 141 and 242 with 8.
+// 31.7 with 8.  262144 rows of 1024 (rings of 6 KB): 110 and 178 with 32, 141 and 242 with 8.
 int embed_unit(int N) { return N >= 152 * 8 * 32 ? 32 : N >= 152 * 6 * 16 ? 16 : 8; }
 
 template <class E, class O, int PV, int NS, bool kNorm>

@@ -3,8 +3,10 @@
 // A row stays in registers between its sums and its result, so it is read once and written once; the
 // variance is the mean of (x - mu)^2 over those registers, a second pass that costs no traffic and
 // does not cancel where mu is large against the spread.  Bound by HBM: 32764 rows of 4096 bf16 94 us (5.7 TB/s),
-// 12608 of 768 8.6 us (4.5), 4000 of 1001 fp32 8.6 us, by scalars; 64 rows of 768 2.4 us, a launch's latency.  One
-// row a CTA instead of CTAs that go over the rows took 116 us for the first.
+// 12608 of 768 9.2 us (4.2), 8192 of 4096 fp32 46 us (5.8), 2048 of 16384 fp32 44 us (6.1); 64 rows of 768 2.4 us, a
+// launch's latency.  One row a CTA instead of CTAs that go over the rows took 116 us for the first.  Rows that no
+// 16-byte vector fits are read by scalars when they are due: 4000 of 1001 fp32 7.2 us (4.5), 8000 of 4097 69 us (3.8);
+// with sixteen entries a thread (more than 1024) that form spills 140 bytes a thread at 64 registers.
 #include "layer_norm.cuh"
 
 namespace dpk {

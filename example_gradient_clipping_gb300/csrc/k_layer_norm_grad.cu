@@ -6,8 +6,12 @@
 // over the rows that it sees in registers.  The rows of a segment (an example, or the whole batch) are
 // split into slices, one CTA each; a slice's sums go to a partial row and rows_sum_kernel adds the
 // slices in order.  Bound by HBM and, small batches, by the launches, the CTAs' first loads and the sums behind the
-// last row: 32764 rows of 4096 bf16 150 us (5.4 TB/s; dw alone without dx 90), 12608 of 768 19 us (3.1 TB/s; each
-// further 1000 rows 0.8 us, 5.8 TB/s; dx alone 15.7), 4000 of 1001 fp32 by scalars 15.
+// last row: 32764 rows of 4096 bf16 147 to 152 us (5.4 TB/s; dw alone without dx 90), 12608 of 768 18 us (3.2 TB/s; each
+// further 1000 rows 0.8 us, 5.8 TB/s; dx alone 14.3), 8192 of 4096 fp32 73 us (5.5 TB/s), 4000 of 1001 fp32 by scalars 13.9
+// (each example's own: 14.9), 8000 of 4097 90 us (4.4 TB/s).
+// Above 8192 columns a row takes 1024 threads of 64 registers, which are too few: fp32 (whose vectors' ring does not fit
+// either) spills 688 bytes a thread and takes 180 us for 2048 rows of 16384 (2.2 TB/s), bf16 48 bytes and 73 us (2.8);
+// rows on no vectors spill 560 to 618.  The 24 entries of 513 to 768 bf16 columns spill 100 bytes, once a row.
 #include "layer_norm.cuh"
 
 namespace dpk {

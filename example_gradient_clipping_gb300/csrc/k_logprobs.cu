@@ -9,20 +9,24 @@
 // x alike, and no large logits cancel.  R moves only when the maximum outgrows it by 2^8.  For the
 // alternatives the vectors that a thread reads together keep their maximum on chip (of bf16 each half's, in one
 // word: half as much is read again, top 50 90 -> 87 us, top 128 128 -> 120; each vector's in two words takes room
-// from L1: 104).  The K-th largest of the 256
+// from L1: 104).  The K-th largest of the
 // threads' maxima is a bound that at least K logits reach, and usually few more: only groups of vectors
 // whose maximum reaches it are read again, and what reaches it is ranked by (value, index).  Where more logits
 // reach it than there is room for (many equal ones), the exact K-th largest value is found by bisection, and
-// its ties are taken in the order of their indices.
+// its ties are taken in the order of their indices.  So the values' places decide what a row costs: 4096 x 50257 bf16 top
+// 50 takes 89 us for independent logits, 85 where likely tokens come first or 2000 neighbours stand out, 106 with a
+// thousand equal largest ones, 172 for sorted rows, whose largest are in a few threads' vectors; top 100 111 us, 523
+// sorted.
 // A row is one CTA's (64, 128 or 256 threads), or with few rows a cluster's.  4096 rows of 50257 bf16: 65.6 us, 6.3
-// TB/s, bound by HBM; with the 20 largest 79.5 us and the 50 largest 87, where what follows the row's last load (sums,
-// bound, groups read again, ranking: a third of a CTA's time) is only half hidden under the rows beside it.
+// TB/s, bound by HBM (fp32 121 us, 6.8 TB/s; top 20 150); with the 20 largest 79.5 us and the 50 largest 87 to 89, where
+// what follows the row's last load (sums, bound, groups read again, ranking: a third of a CTA's time) is only half hidden
+// under the rows beside it.
 // Reading ahead did not help (the next row asked into L2 while this one is ranked: top 50 97 -> 99 to 137 us), nor loads
 // that pass L1 by (65.6, top 20 79.5 -> 82), nor a cluster of two for every row (68 -> 83), nor collecting by warps
 // instead of by the CTA (97 -> 101).
 //
 // Gradient: one read and one write of the rows, elementwise from m, ls and the entropy.  Bound by HBM: 4096 rows of
-// 50257 bf16 127 us, 6.5 TB/s; 2048 of 131071 164 us.
+// 50257 bf16 127 us, 6.5 TB/s; 2048 of 131071 164 us; 2048 of 50257 fp32 125 us, 6.6 TB/s.
 #include <algorithm>
 
 #include "seq.cuh"
