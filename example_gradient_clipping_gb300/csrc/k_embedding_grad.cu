@@ -14,7 +14,7 @@
 // its squares are summed before the next one is added), sum to fp32 179 us (6.0 TB/s, bound by HBM); the same of fp32 190
 // and 255 us (5.6 and 6.3 TB/s).  4000 rows of 197 fp32: 8.4 and 7.0 us, three launches' latency.
 // Added in fp32 along a lane's columns, the places of a unit, the units and an example's positions: the norms are off by
-// 1e-7 of their value at that size, 3e-8 where each example's whole gradient is squared and summed pairwise.
+// 1e-7 to 2e-7 of their value at that size.
 #include <algorithm>
 
 #include "seq.cuh"
