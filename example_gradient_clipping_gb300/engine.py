@@ -107,8 +107,8 @@ class PrivacyEngine:
         import torch
 
         def hook(module, inputs, output):
-            if not output.requires_grad:   # no backward pass reaches this call
-                return
+            if module is not self.layers[i] or not output.requires_grad:
+                return   # (a copy's call, or one that no backward pass reaches)
             a, within = inputs[0].detach(), torch._C._current_graph_task_id()
 
             def taken(g):                  # the gradient of the loss w.r.t. this call's output

@@ -621,12 +621,15 @@ def token_logprobs(logits, tokens=None, top: int = 0, temperature: float = 1.0, 
 class LayerNorm(torch.nn.LayerNorm):
     """torch.nn.LayerNorm over the last dimension, by dp.layer_norm; PrivacyEngine clips its parameters.
     Inputs [B, ..., D], the examples first."""
+    _sink = None   # where a backward pass leaves the per-example gradients (set by PrivacyEngine)
 
     def __init__(self, *args, **kwargs):
         super().__init__(*args, **kwargs)
         if len(self.normalized_shape) != 1:
             raise ValueError(f"normalized_shape {self.normalized_shape}: the last dimension only")
-        self._sink = None   # where a backward pass leaves the per-example gradients (set by PrivacyEngine)
+
+    def __getstate__(self):   # a copy is no engine's
+        return {k: v for k, v in self.__dict__.items() if k != "_sink"}
 
     def forward(self, x):
         return _layer_norm(x, self.weight, self.bias, self.eps, self._sink)
@@ -635,13 +638,16 @@ class LayerNorm(torch.nn.LayerNorm):
 class Embedding(torch.nn.Embedding):
     """torch.nn.Embedding by dp.embedding, times `scale`; PrivacyEngine clips its weight.  Tokens [B, ...],
     the examples first."""
+    _sinks = ()   # where a backward pass leaves the tokens and the output gradient (set by PrivacyEngine)
 
     def __init__(self, *args, scale: float = 1.0, **kwargs):
         super().__init__(*args, **kwargs)
         if self.max_norm is not None or self.scale_grad_by_freq or self.sparse:
             raise ValueError("max_norm, scale_grad_by_freq and sparse gradients are not there")
         self.scale = float(scale)
-        self._sinks = ()   # where a backward pass leaves the tokens and the output gradient (set by PrivacyEngine)
+
+    def __getstate__(self):   # a copy is no engine's
+        return {k: v for k, v in self.__dict__.items() if k != "_sinks"}
 
     def forward(self, tokens):
         return _embedding(tokens.contiguous(), self.weight, self.scale, self.padding_idx, self._sinks)

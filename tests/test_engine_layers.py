@@ -258,3 +258,33 @@ def test_a_layer_in_two_checkpointed_segments(device, which, reentrant):
     else:
         got = [x for pair in zip(engine._acts[:2], engine._grads[:2]) for x in pair if x is not None]
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "layers"])
+def test_a_copy_of_a_model_under_an_engine(device, how):
+    """A copy trains as a model without an engine, and its passes are none of the engine's."""
+    import copy
+    import pickle
+    model, tokens = _Model(device), _tokens(device)
+    plain = copy.deepcopy(model)
+    want = _privatised(model, tokens)
+    engine = _engine(model)
+    if how == "deepcopy":
+        other = copy.deepcopy(model)
+    else:   # (a linear layer's hook cannot be pickled)
+        other = copy.deepcopy(plain)
+        other.embed, other.norm = pickle.loads(pickle.dumps(model.embed)), copy.deepcopy(model.norm)
+    loss = model(tokens).square().sum()
+    for m in (plain, other):
+        m(_tokens(device, 1)).square().sum().backward()
+    for (name, p), q in zip(plain.named_parameters(), other.parameters()):
+        assert q.grad is not None and torch.equal(p.grad, q.grad), name
+    assert all(x is None for x in engine._acts + engine._grads)
+    loss.backward()
+    other(_tokens(device, 2)).sum().backward()
+    if tokens.is_cuda:
+        assert torch.equal(engine.privatise(0), want[0])
+    else:
+        got = [x for pair in zip(engine._acts[:2], engine._grads[:2]) for x in pair if x is not None]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    _engine(other).detach()   # and may have an engine of its own
